@@ -13,6 +13,14 @@ import ctypes
 import os
 from typing import Optional, Sequence, Tuple
 
+from . import outcomes
+from .outcomes import (Distill, Outcomes, Scores, TN_OUTCOMES_MAX_IDS, TN_OUTCOMES_MAX_TOP,  # noqa: F401
+                       TN_TYPE_BF16, TN_TYPE_C64, TN_TYPE_F16, TN_TYPE_F32, tn_outcomes_check,
+                       tn_outcomes_create, tn_outcomes_destroy, tn_outcomes_distill,
+                       tn_outcomes_distill_grad, tn_outcomes_distill_step, tn_outcomes_last_error,
+                       tn_outcomes_score, tn_outcomes_score_grad, tn_outcomes_set_workspace,
+                       tn_outcomes_workspace_bytes, tn_rows, tn_teacher)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtn_gb300.so")
 
@@ -108,6 +116,7 @@ SIGNATURES = {
     "tn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "tn_last_error": (ctypes.c_char_p, [_P]),
 }
+SIGNATURES.update(outcomes.SIGNATURES)
 
 
 def lib() -> ctypes.CDLL:

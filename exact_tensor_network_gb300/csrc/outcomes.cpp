@@ -1,0 +1,333 @@
+// C ABI of the operators on outcome distributions (include/tn_outcomes.h):
+// argument checks, workspace layout and launches.  Kernels are in
+// k_outcomes*.cu.  Nothing here allocates after tn_outcomes_create, and
+// nothing throws.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+
+#include "outcomes.h"
+
+namespace {
+
+using tn::Outcomes;
+
+thread_local char g_error[256] = {0};
+
+tn_status fail(char (&buf)[256], tn_status st, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    return st;
+}
+
+tn_status cuda_fail(Outcomes &o, cudaError_t e, const char *what) {
+    return fail(o.error, TN_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
+
+// Most segments that calls of up to max_rows rows can use at once, and most
+// rows that are split.
+void workspace_slots(const Outcomes &o, uint64_t *tickets, uint64_t *slots) {
+    *tickets = *slots = 0;
+    // the number of segments a row falls to its lowest value once the rows
+    // alone fill the GPU
+    const int64_t last = o.max_rows < 4 * 152 ? o.max_rows : 4 * 152;
+    for (int64_t r = 1; r <= last; ++r) {
+        const tn::OutSplit s = tn::out_split(o.type, o.cols, r);
+        if (s.segs > 1) {
+            *tickets = r;
+            if ((uint64_t)(r * s.segs) > *slots) *slots = r * s.segs;
+        }
+    }
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, o.max_rows);
+    if (s.segs > 1) {
+        *tickets = o.max_rows;
+        if ((uint64_t)(o.max_rows * s.segs) > *slots) *slots = o.max_rows * s.segs;
+    }
+}
+
+uint64_t align(uint64_t x) { return (x + 255) / 256 * 256; }
+
+// Checks of the rows and the arguments that every call shares.
+tn_status common(Outcomes &o, const tn_rows *r) {
+    if (!r || (r->rows > 0 && !r->data)) return fail(o.error, TN_EINVAL, "rows and their data are required");
+    if (r->rows < 0 || r->rows > o.max_rows)
+        return fail(o.error, TN_EINVAL, "%lld rows: the handle was made for at most %lld",
+                    (long long)r->rows, (long long)o.max_rows);
+    if (reinterpret_cast<uintptr_t>(r->data) % tn::out_entry_bytes(o.type))
+        return fail(o.error, TN_EINVAL, "rows are not aligned to their entry type");
+    if (r->row_stride < 0 || r->col_stride < 0 || (r->col_stride == 0 && o.cols > 1))
+        return fail(o.error, TN_EINVAL, "row_stride must be >= 0 and col_stride >= 1");
+    if (r->mask && (r->mask_row_stride < 0 || r->mask_col_stride < 0))
+        return fail(o.error, TN_EINVAL, "mask strides must be >= 0");
+    if (!o.ws) return fail(o.error, TN_ENOMEM, "no workspace bound (tn_outcomes_set_workspace)");
+    return TN_OK;
+}
+
+tn_status check_teacher(Outcomes &o, const tn_rows *r, const tn_teacher *t) {
+    if (!t || (r->rows > 0 && (!t->ids || !t->logits)))
+        return fail(o.error, TN_EINVAL, "the teacher's ids and logits are required");
+    if (t->count < 1 || t->count > TN_OUTCOMES_MAX_IDS)
+        return fail(o.error, TN_EINVAL, "teacher count %d outside 1 .. %d", (int)t->count,
+                    (int)TN_OUTCOMES_MAX_IDS);
+    if (t->type != TN_TYPE_F32 && t->type != TN_TYPE_BF16 && t->type != TN_TYPE_F16)
+        return fail(o.error, TN_EINVAL, "the teacher's logits must be f32, bf16 or f16");
+    if (!(t->scale > 0.f) || std::isinf(t->scale))
+        return fail(o.error, TN_EINVAL, "the teacher's scale must be finite and > 0");
+    return TN_OK;
+}
+
+tn_status check_grad(Outcomes &o, const tn_rows *r, const void *grad, int64_t rs, int64_t cs) {
+    if (r->rows > 0 && !grad) return fail(o.error, TN_EINVAL, "grad is required");
+    if (reinterpret_cast<uintptr_t>(grad) % tn::out_entry_bytes(o.type))
+        return fail(o.error, TN_EINVAL, "grad is not aligned to its entry type");
+    if (rs < 0 || cs < 0 || (cs == 0 && o.cols > 1) || (rs == 0 && r->rows > 1))
+        return fail(o.error, TN_EINVAL, "grad strides must be >= 1");
+    return TN_OK;
+}
+
+tn::OutRows rows_of(const Outcomes &o, const tn_rows *r, const tn::OutSplit &s) {
+    tn::OutRows a = {};
+    a.data = static_cast<const char *>(r->data);
+    a.rows = r->rows;
+    a.cols = o.cols;
+    a.row_stride = r->row_stride;
+    a.col_stride = o.cols == 1 ? 1 : r->col_stride;
+    a.mask = r->mask;
+    a.mask_row_stride = r->mask_row_stride;
+    a.mask_col_stride = r->mask_col_stride;
+    a.scale = o.scale;
+    a.c2 = o.type == TN_TYPE_C64 ? o.scale : static_cast<float>(o.scale * 1.4426950408889634);
+    a.seg_vecs = s.seg_vecs;
+    a.segs = s.segs;
+    a.status = reinterpret_cast<tn::DevStatus *>(o.ws);
+    return a;
+}
+
+tn::OutTeacher teacher_of(const tn_teacher *t) {
+    return tn::OutTeacher{t->ids, t->logits, t->type, t->count, t->scale};
+}
+
+tn_status forward(Outcomes &o, tn::OutForward &a, const tn::OutSplit &s, cudaStream_t stream) {
+    const int64_t E = tn::kOutVecBytes / tn::out_entry_bytes(o.type);
+    const int64_t k = a.n_top;
+    if (k > 0) {
+        const int64_t nv = s.seg_vecs;
+        int64_t words = nv <= tn::kOutKeys ? nv : (nv + 31) / 32;
+        const int64_t entries = (k < nv ? k : nv) * E;
+        if (words < entries) words = entries;
+        if (s.segs > 1 && words < 8 * k) words = 8 * k;
+        a.key_words = static_cast<int32_t>(words);
+        // vector maxima of k chunks; or the joiner's octets of k lists
+        int64_t sub = nv > tn::kOutKeys ? 32 * k : 0;
+        if (s.segs > 1 && sub < k * ((k + 7) / 8)) sub = k * ((k + 7) / 8);
+        a.sub_words = static_cast<int32_t>(sub);
+    }
+    a.tickets = reinterpret_cast<uint32_t *>(o.ws + o.ticket_off);
+    a.partials = reinterpret_cast<tn::OutPartial *>(o.ws + o.partial_off);
+    a.lists = reinterpret_cast<uint2 *>(o.ws + o.list_off);
+    const cudaError_t e = tn::launch_outcomes_forward(o.type, a, s.warp_rows, stream);
+    return e == cudaSuccess ? TN_OK : cuda_fail(o, e, "launching the forward pass");
+}
+
+tn_status gradient(Outcomes &o, const tn::OutGrad &a, const tn::OutSplit &s, cudaStream_t stream) {
+    const cudaError_t e = tn::launch_outcomes_grad(o.type, a, s.warp_rows, stream);
+    return e == cudaSuccess ? TN_OK : cuda_fail(o, e, "launching the gradient");
+}
+
+}  // namespace
+
+extern "C" {
+
+tn_status tn_outcomes_create(int32_t type, int64_t cols, int64_t max_rows, int32_t max_top, float scale,
+                             tn_outcomes_t **out) {
+    if (!out) return fail(g_error, TN_EINVAL, "out is NULL");
+    *out = nullptr;
+    if (type < TN_TYPE_C64 || type > TN_TYPE_F16) return fail(g_error, TN_EINVAL, "unknown entry type %d", (int)type);
+    if (cols < 1 || max_rows < 1) return fail(g_error, TN_EINVAL, "cols and max_rows must be >= 1");
+    if (max_top < 0 || max_top > TN_OUTCOMES_MAX_TOP)
+        return fail(g_error, TN_EINVAL, "max_top %d outside 0 .. %d", (int)max_top, (int)TN_OUTCOMES_MAX_TOP);
+    if (!(scale > 0.f) || std::isinf(scale)) return fail(g_error, TN_EINVAL, "scale must be finite and > 0");
+    if (cols > (int64_t)1 << 40) return fail(g_error, TN_EOVERFLOW, "more than 2^40 entries a row");
+    int64_t items;
+    if (!mul_ok(max_rows, tn::out_split(type, cols, max_rows).segs, &items) || items > 0x7fffffff)
+        return fail(g_error, TN_EOVERFLOW, "more than 2^31 - 1 row segments");
+    tn_outcomes_s *h = new (std::nothrow) tn_outcomes_s;
+    if (!h) return fail(g_error, TN_ENOMEM, "host allocation failed");
+    Outcomes &o = h->o;
+    o.type = type;
+    o.cols = cols;
+    o.max_rows = max_rows;
+    o.max_top = max_top;
+    o.scale = scale;
+    uint64_t slots;
+    workspace_slots(o, &o.ticket_count, &slots);
+    o.ticket_off = 256;
+    o.partial_off = align(o.ticket_off + o.ticket_count * sizeof(uint32_t));
+    o.list_off = align(o.partial_off + slots * sizeof(tn::OutPartial));
+    o.ws_bytes = align(o.list_off + slots * max_top * sizeof(uint2));
+    g_error[0] = 0;
+    *out = h;
+    return TN_OK;
+}
+
+void tn_outcomes_destroy(tn_outcomes_t *h) { delete h; }
+
+tn_status tn_outcomes_workspace_bytes(const tn_outcomes_t *h, uint64_t *bytes) {
+    if (!h || !bytes) return TN_EINVAL;
+    *bytes = h->o.ws_bytes;
+    return TN_OK;
+}
+
+tn_status tn_outcomes_set_workspace(tn_outcomes_t *h, void *dev_ptr, uint64_t bytes) {
+    if (!h) return TN_EINVAL;
+    Outcomes &o = h->o;
+    if (!dev_ptr || reinterpret_cast<uintptr_t>(dev_ptr) % 256)
+        return fail(o.error, TN_EINVAL, "workspace must be a non-NULL 256-byte aligned device pointer");
+    if (bytes < o.ws_bytes)
+        return fail(o.error, TN_ENOMEM, "workspace of %llu bytes is smaller than the %llu bytes needed",
+                    (unsigned long long)bytes, (unsigned long long)o.ws_bytes);
+    o.ws = nullptr;
+    // status word and tickets; the rest is written before it is read
+    cudaError_t e = cudaMemset(dev_ptr, 0, o.partial_off);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return cuda_fail(o, e, "clearing the workspace");
+    o.ws = static_cast<char *>(dev_ptr);
+    return TN_OK;
+}
+
+tn_status tn_outcomes_score(tn_outcomes_t *h, const tn_rows *rows, const int64_t *given, int32_t n_given,
+                            float *logp, float *logz, float *entropy, int32_t n_top, int64_t *top_ids,
+                            float *top_logp, tn_stream_t stream) {
+    if (!h) return TN_EINVAL;
+    Outcomes &o = h->o;
+    tn_status st = common(o, rows);
+    if (st != TN_OK) return st;
+    if (n_given < 0 || n_given > TN_OUTCOMES_MAX_IDS)
+        return fail(o.error, TN_EINVAL, "n_given %d outside 0 .. %d", (int)n_given, (int)TN_OUTCOMES_MAX_IDS);
+    if (n_top < 0 || n_top > o.max_top)
+        return fail(o.error, TN_EINVAL, "n_top %d outside 0 .. %d", (int)n_top, (int)o.max_top);
+    if (rows->rows == 0) return TN_OK;
+    if (!logz || !entropy || (n_given > 0 && (!given || !logp)) || (n_top > 0 && (!top_ids || !top_logp)))
+        return fail(o.error, TN_EINVAL, "an output or the given outcomes are missing");
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows);
+    tn::OutForward a = {};
+    a.r = rows_of(o, rows, s);
+    a.given = given;
+    a.n_given = n_given;
+    a.logp = logp;
+    a.logz = logz;
+    a.entropy = entropy;
+    a.n_top = n_top;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    return forward(o, a, s, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tn_status tn_outcomes_score_grad(tn_outcomes_t *h, const tn_rows *rows, const int64_t *given, int32_t n_given,
+                                 const float *logz, const float *entropy, const float *g_logp,
+                                 const float *g_entropy, void *grad, int64_t grad_row_stride,
+                                 int64_t grad_col_stride, tn_stream_t stream) {
+    if (!h) return TN_EINVAL;
+    Outcomes &o = h->o;
+    tn_status st = common(o, rows);
+    if (st == TN_OK) st = check_grad(o, rows, grad, grad_row_stride, grad_col_stride);
+    if (st != TN_OK) return st;
+    if (n_given < 0 || n_given > TN_OUTCOMES_MAX_IDS)
+        return fail(o.error, TN_EINVAL, "n_given %d outside 0 .. %d", (int)n_given, (int)TN_OUTCOMES_MAX_IDS);
+    if (rows->rows == 0) return TN_OK;
+    if (!logz || (n_given > 0 && (!given || !g_logp)) || (g_entropy && !entropy))
+        return fail(o.error, TN_EINVAL, "logz, the given outcomes with g_logp, or entropy are missing");
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows);
+    tn::OutGrad a = {};
+    a.r = rows_of(o, rows, s);
+    a.logz = logz;
+    a.given = given;
+    a.n_given = n_given;
+    a.entropy = entropy;
+    a.g_logp = g_logp;
+    a.g_entropy = g_entropy;
+    a.grad = static_cast<char *>(grad);
+    a.grad_row_stride = grad_row_stride;
+    a.grad_col_stride = o.cols == 1 ? 1 : grad_col_stride;
+    return gradient(o, a, s, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tn_status tn_outcomes_distill(tn_outcomes_t *h, const tn_rows *rows, const tn_teacher *teacher, float *loss,
+                              float *logz, tn_stream_t stream) {
+    if (!h) return TN_EINVAL;
+    Outcomes &o = h->o;
+    tn_status st = common(o, rows);
+    if (st == TN_OK) st = check_teacher(o, rows, teacher);
+    if (st != TN_OK) return st;
+    if (rows->rows == 0) return TN_OK;
+    if (!loss || !logz) return fail(o.error, TN_EINVAL, "loss and logz are required");
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows);
+    tn::OutForward a = {};
+    a.r = rows_of(o, rows, s);
+    a.logz = logz;
+    a.loss = loss;
+    a.teacher = teacher_of(teacher);
+    return forward(o, a, s, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tn_status tn_outcomes_distill_grad(tn_outcomes_t *h, const tn_rows *rows, const tn_teacher *teacher,
+                                   const float *logz, const float *g_loss, void *grad,
+                                   int64_t grad_row_stride, int64_t grad_col_stride, tn_stream_t stream) {
+    if (!h) return TN_EINVAL;
+    Outcomes &o = h->o;
+    tn_status st = common(o, rows);
+    if (st == TN_OK) st = check_teacher(o, rows, teacher);
+    if (st == TN_OK) st = check_grad(o, rows, grad, grad_row_stride, grad_col_stride);
+    if (st != TN_OK) return st;
+    if (rows->rows == 0) return TN_OK;
+    if (!logz || !g_loss) return fail(o.error, TN_EINVAL, "logz and g_loss are required");
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows);
+    tn::OutGrad a = {};
+    a.r = rows_of(o, rows, s);
+    a.logz = logz;
+    a.g_loss = g_loss;
+    a.teacher = teacher_of(teacher);
+    a.grad = static_cast<char *>(grad);
+    a.grad_row_stride = grad_row_stride;
+    a.grad_col_stride = o.cols == 1 ? 1 : grad_col_stride;
+    return gradient(o, a, s, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tn_status tn_outcomes_distill_step(tn_outcomes_t *h, const tn_rows *rows, const tn_teacher *teacher,
+                                   const float *g_loss, float *loss, float *logz, void *grad,
+                                   int64_t grad_row_stride, int64_t grad_col_stride, tn_stream_t stream) {
+    if (!h) return TN_EINVAL;
+    if (rows && rows->rows > 0 && !g_loss) return fail(h->o.error, TN_EINVAL, "g_loss is required");
+    if (rows) {
+        const tn_status st = check_grad(h->o, rows, grad, grad_row_stride, grad_col_stride);
+        if (st != TN_OK) return st;
+    }
+    const tn_status st = tn_outcomes_distill(h, rows, teacher, loss, logz, stream);
+    if (st != TN_OK) return st;
+    return tn_outcomes_distill_grad(h, rows, teacher, logz, g_loss, grad, grad_row_stride,
+                                    grad_col_stride, stream);
+}
+
+tn_status tn_outcomes_check(tn_outcomes_t *h) {
+    if (!h) return TN_EINVAL;
+    Outcomes &o = h->o;
+    if (!o.ws) return TN_OK;
+    tn::DevStatus d{0, 0};
+    cudaError_t e = cudaMemcpy(&d, o.ws, sizeof(d), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(o, e, "reading the status word");
+    if (d.code == tn::ERR_NONE) return TN_OK;
+    e = cudaMemset(o.ws, 0, sizeof(d));
+    if (e != cudaSuccess) return cuda_fail(o, e, "clearing the status word");
+    return fail(o.error, TN_EDEVICE, "an outcome's id is outside [-1, cols) in row %d", (int)d.where);
+}
+
+const char *tn_outcomes_last_error(const tn_outcomes_t *h) { return h ? h->o.error : g_error; }
+
+}  // extern "C"

@@ -1,0 +1,393 @@
+// Device helpers of the operators on outcome distributions: reading rows
+// (types, strides, masks), groups of threads that share a row, teachers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "outcomes.h"
+
+namespace tn {
+
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// larger of two, NaN if either is (a row with a NaN has no distribution: it
+// must not be lost in a maximum)
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// ---- entries ----------------------------------------------------------------
+//
+// An entry is worked on as its order value v, by which alternatives are
+// ranked: the logit itself, or w = re^2 + im^2 of an amplitude with every
+// operation rounded (no fused multiply-add, so that equal amplitudes tie in
+// any other implementation of the definition too).  kAbsent marks an absent
+// entry.
+
+template <int TYPE>
+struct Entry;
+
+template <>
+struct Entry<TN_TYPE_F32> {
+    using T = float;
+    static constexpr int E = 4;
+    static constexpr bool kReal = true;
+    static __device__ __forceinline__ float value(T x) { return x; }
+    static __device__ __forceinline__ void values(const uint4 &r, float (&v)[E]) {
+        v[0] = __uint_as_float(r.x);
+        v[1] = __uint_as_float(r.y);
+        v[2] = __uint_as_float(r.z);
+        v[3] = __uint_as_float(r.w);
+    }
+};
+
+template <>
+struct Entry<TN_TYPE_BF16> {
+    using T = __nv_bfloat16;
+    static constexpr int E = 8;
+    static constexpr bool kReal = true;
+    static __device__ __forceinline__ float value(T x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ void values(const uint4 &r, float (&v)[E]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+template <>
+struct Entry<TN_TYPE_F16> {
+    using T = __half;
+    static constexpr int E = 8;
+    static constexpr bool kReal = true;
+    static __device__ __forceinline__ float value(T x) { return __half2float(x); }
+    static __device__ __forceinline__ void values(const uint4 &r, float (&v)[E]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+};
+
+template <>
+struct Entry<TN_TYPE_C64> {
+    using T = float2;
+    static constexpr int E = 2;
+    static constexpr bool kReal = false;
+    static __device__ __forceinline__ float value(T a) {
+        return __fadd_rn(__fmul_rn(a.x, a.x), __fmul_rn(a.y, a.y));
+    }
+    static __device__ __forceinline__ void values(const uint4 &r, float (&v)[E]) {
+        v[0] = value(make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
+        v[1] = value(make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
+    }
+};
+
+template <int TYPE>
+__device__ __forceinline__ constexpr float absent() {
+    return Entry<TYPE>::kReal ? -__builtin_huge_valf() : 0.f;
+}
+
+// Order value as an unsigned integer of the same order (-0 and +0 equal); 0
+// for absent entries.
+template <int TYPE>
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);
+    const uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+    return v == absent<TYPE>() ? 0u : k;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+
+// ---- one row ----------------------------------------------------------------
+//
+// Vectors are 16-byte pieces of the row that start at 16-byte boundaries:
+// vector j holds entries j E - head .. j E - head + E - 1, of which those in
+// [0, cols) exist.  Only vectors that lie inside the row are read as such;
+// the others (and every vector of a strided row, where head is 0) entry by
+// entry.
+
+template <int TYPE>
+struct Row {
+    using En = Entry<TYPE>;
+    const typename En::T *p;
+    const uint8_t *m;
+    int64_t cols, cs, mcs;
+    int head;
+
+    __device__ __forceinline__ Row(const OutRows &a, int64_t row)
+        : p(reinterpret_cast<const typename En::T *>(a.data) + row * a.row_stride),
+          m(a.mask ? a.mask + row * a.mask_row_stride : nullptr),
+          cols(a.cols), cs(a.col_stride), mcs(a.mask_col_stride), head(0) {
+        if (cs == 1)
+            head = static_cast<int>((reinterpret_cast<uintptr_t>(p) % kOutVecBytes) / sizeof(typename En::T));
+    }
+    __device__ __forceinline__ bool inside(int64_t e0) const {
+        return cs == 1 && e0 >= 0 && e0 + En::E <= cols;
+    }
+    __device__ __forceinline__ uint4 raw(int64_t e0) const {
+        return __ldg(reinterpret_cast<const uint4 *>(p + e0));
+    }
+    __device__ __forceinline__ bool keep(int64_t e) const { return !m || m[e * mcs] != 0; }
+    __device__ __forceinline__ float value(int64_t e) const {
+        return keep(e) ? En::value(p[e * cs]) : absent<TYPE>();
+    }
+    // bit i: entry e0 + i of a vector inside the row is kept
+    __device__ __forceinline__ uint32_t keep_bits(int64_t e0) const {
+        constexpr int E = En::E;
+        uint32_t bits = 0;
+        if constexpr (E >= 4) {
+            if (mcs == 1) {
+                // mask bytes lie at any offset from the data's vectors: one
+                // aligned word, or two and a shift where both are inside
+                using W = typename std::conditional<E == 8, uint64_t, uint32_t>::type;
+                const uint8_t *q = m + e0;
+                const int off = static_cast<int>(reinterpret_cast<uintptr_t>(q) % E);
+                const uint8_t *b = q - off;
+                W w;
+                bool have = false;
+                if (off == 0) {
+                    w = *reinterpret_cast<const W *>(b);
+                    have = true;
+                } else if (b >= m && b + 2 * E <= m + cols) {
+                    const W lo = reinterpret_cast<const W *>(b)[0];
+                    const W hi = reinterpret_cast<const W *>(b)[1];
+                    w = (lo >> (8 * off)) | (hi << (8 * (E - off)));
+                    have = true;
+                }
+                if (have) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        if ((w >> (8 * i)) & 0xff) bits |= 1u << i;
+                    return bits;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (m[(e0 + i) * mcs]) bits |= 1u << i;
+        return bits;
+    }
+    // the order values of vector j
+    __device__ __forceinline__ void vector(int64_t j, float (&v)[En::E]) const {
+        const int64_t e0 = j * En::E - head;
+        if (inside(e0)) {
+            En::values(raw(e0), v);
+            if (m) {
+                const uint32_t bits = keep_bits(e0);
+#pragma unroll
+                for (int i = 0; i < En::E; ++i)
+                    if (!(bits >> i & 1)) v[i] = absent<TYPE>();
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < En::E; ++i) {
+                const int64_t e = e0 + i;
+                v[i] = e >= 0 && e < cols ? value(e) : absent<TYPE>();
+            }
+        }
+    }
+};
+
+// ---- groups -----------------------------------------------------------------
+//
+// G threads that share a row: a warp or the whole CTA.  Sums and scans of a
+// CTA go through `red`, two halves used in turn so that each needs one barrier.
+
+template <int G>
+struct Group {
+    static constexpr int kWarps = G / 32;
+    int t, lane, warp;   // thread in the group, lane, warp in the group
+    uint32_t *red;       // 2 * 2 * kWarps words (unused by a warp)
+    int half;
+
+    __device__ __forceinline__ explicit Group(uint32_t *r)
+        : t(threadIdx.x % G), lane(threadIdx.x % 32), warp(threadIdx.x % G / 32), red(r), half(0) {}
+    __device__ __forceinline__ void sync() const {
+        if constexpr (G == 32) __syncwarp();
+        else __syncthreads();
+    }
+    __device__ __forceinline__ uint32_t *slot() {
+        half ^= 1;
+        return red + half * 2 * kWarps;
+    }
+    __device__ __forceinline__ uint32_t sum(uint32_t x) {
+        x = __reduce_add_sync(0xffffffffu, x);
+        if constexpr (G > 32) {
+            uint32_t *s = slot();
+            if (lane == 0) s[warp] = x;
+            __syncthreads();
+            x = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) x += s[w];
+        }
+        return x;
+    }
+    __device__ __forceinline__ uint32_t max(uint32_t x) {
+        x = __reduce_max_sync(0xffffffffu, x);
+        if constexpr (G > 32) {
+            uint32_t *s = slot();
+            if (lane == 0) s[warp] = x;
+            __syncthreads();
+            x = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) x = ::max(x, s[w]);
+        }
+        return x;
+    }
+    // NaN if any is
+    __device__ __forceinline__ float max(float x) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+        if constexpr (G > 32) {
+            uint32_t *s = slot();
+            if (lane == 0) s[warp] = __float_as_uint(x);
+            __syncthreads();
+            x = __uint_as_float(s[0]);
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) x = max_nan(x, __uint_as_float(s[w]));
+        }
+        return x;
+    }
+    // two sums, added in a fixed order
+    __device__ __forceinline__ void sum2(float &x, float &y) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        if constexpr (G > 32) {
+            uint32_t *s = slot();
+            if (lane == 0) {
+                s[2 * warp] = __float_as_uint(x);
+                s[2 * warp + 1] = __float_as_uint(y);
+            }
+            __syncthreads();
+            x = y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                x += __uint_as_float(s[2 * w]);
+                y += __uint_as_float(s[2 * w + 1]);
+            }
+        }
+    }
+    __device__ __forceinline__ float sum(float x) {
+        float y = 0.f;
+        sum2(x, y);
+        return x;
+    }
+    // exclusive prefix sums of two counters over the group's threads
+    __device__ __forceinline__ void scan2(uint32_t &x, uint32_t &y) {
+        const uint32_t x0 = x, y0 = y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) {
+                x += a;
+                y += b;
+            }
+        }
+        if constexpr (G > 32) {
+            uint32_t *s = slot();
+            if (lane == 31) {
+                s[2 * warp] = x;
+                s[2 * warp + 1] = y;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                if (w < warp) {
+                    x += s[2 * w];
+                    y += s[2 * w + 1];
+                }
+        }
+        x -= x0;
+        y -= y0;
+    }
+};
+
+// ---- ids and teachers -------------------------------------------------------
+
+__device__ __forceinline__ void flag_bad_id(const OutRows &a, int64_t row) {
+    if (atomicCAS(&a.status->code, ERR_NONE, ERR_DESC) == ERR_NONE)
+        a.status->where = static_cast<int32_t>(row);
+}
+
+// A row's teacher over the group: this thread's outcomes t, t + G, ...; id -1
+// where left out.  q = exp(logit - max) / total.
+template <int G>
+struct Teacher {
+    static constexpr int kPer = TN_OUTCOMES_MAX_IDS / G;
+    int64_t id[kPer];
+    float q[kPer], logq[kPer];
+    float used;    // 1 if anything is left, else 0
+    bool bad;      // an id out of range (this thread's)
+
+    template <int TYPE>
+    __device__ __forceinline__ void load(Group<G> &g, const OutTeacher &a, const OutRows &rows,
+                                         const Row<TYPE> &r, int64_t row) {
+        bad = false;
+        float top = -__builtin_huge_valf();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int j = g.t + i * G;
+            id[i] = -1;
+            q[i] = -__builtin_huge_valf();
+            if (j < a.count) {
+                const int64_t at = row * a.count + j;
+                const int64_t x = a.ids[at];
+                if (x < -1 || x >= r.cols) {
+                    bad = true;
+                    flag_bad_id(rows, row);
+                } else if (x >= 0 && r.keep(x)) {
+                    float l;
+                    if (a.type == TN_TYPE_F32) l = static_cast<const float *>(a.logits)[at];
+                    else if (a.type == TN_TYPE_BF16)
+                        l = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[at]);
+                    else l = __half2float(static_cast<const __half *>(a.logits)[at]);
+                    l *= a.scale;
+                    if (l != -__builtin_huge_valf()) {
+                        id[i] = x;
+                        q[i] = l;
+                    }
+                }
+            }
+            top = max_nan(top, q[i]);
+        }
+        top = g.max(top);
+        float total = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) total += id[i] >= 0 ? expf(q[i] - top) : 0.f;
+        total = g.sum(total);
+        const float logt = logf(total);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            logq[i] = id[i] >= 0 ? (q[i] - top) - logt : 0.f;
+            q[i] = id[i] >= 0 ? expf(q[i] - top) / total : 0.f;
+        }
+        used = top == -__builtin_huge_valf() ? 0.f : 1.f;
+    }
+};
+
+}  // namespace tn

@@ -1,0 +1,116 @@
+// Operators on outcome distributions: the handle, the kernels' arguments and
+// their launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/tn_outcomes.h"
+#include "kernels.h"
+
+namespace tn {
+
+constexpr int kOutVecBytes = 16;        // entries are read 16 bytes at a time
+constexpr int kOutThreads = 256;        // CTA of the kernels below
+// Rows of at most this many 16-byte vectors (4 KiB) belong to one warp each:
+// a CTA would have no second vector for its threads.
+constexpr int kOutWarpVecs = 256;
+// Maxima kept per segment for the alternatives: one per vector, or one per 32
+// vectors in segments of more vectors than this.
+constexpr int kOutKeys = 1024;
+constexpr int64_t kOutSegVecs = 32 * (int64_t)kOutKeys;   // longest segment (512 KiB)
+
+inline int out_entry_bytes(int32_t type) { return type == TN_TYPE_C64 ? 8 : type == TN_TYPE_F32 ? 4 : 2; }
+
+// How a batch of rows is cut: `segs` segments of `seg_vecs` vectors a row.
+struct OutSplit {
+    int64_t vecs;       // vectors of the longest row (its first may be partial)
+    int64_t seg_vecs;
+    int64_t segs;
+    bool warp_rows;     // one warp per row (segs is 1)
+};
+
+struct OutRows {
+    const char *data;
+    int64_t rows, cols, row_stride, col_stride;
+    const uint8_t *mask;
+    int64_t mask_row_stride, mask_col_stride;
+    // log p = scale z - log Z.  c2: weights as powers of two, 2^(c2 z) with
+    // c2 = scale log2(e), or (amplitudes) 2^(c2 log2 w) with c2 = scale
+    float scale, c2;
+    int64_t seg_vecs;
+    int64_t segs;
+    DevStatus *status;
+};
+
+struct OutTeacher {
+    const int64_t *ids;
+    const void *logits;
+    int32_t type, count;
+    float scale;
+};
+
+// Partial result of a segment: its reference entry and sums (see Sums in
+// k_outcomes.cu).
+struct OutPartial {
+    float z0, s, t;
+    int32_t pad;
+};
+
+struct OutForward {
+    OutRows r;
+    // scores
+    const int64_t *given;
+    float *logp, *logz, *entropy;
+    int64_t *top_ids;
+    float *top_logp;
+    int32_t n_given, n_top;
+    // distillation (count 0: scores)
+    OutTeacher teacher;
+    float *loss;
+    // split rows: a ticket per row (zero between calls), a partial and n_top
+    // (key, index) pairs per segment
+    uint32_t *tickets;
+    OutPartial *partials;
+    uint2 *lists;
+    int32_t key_words;  // shared-memory words per group: vector or chunk maxima
+    int32_t sub_words;  // and vector maxima of selected chunks
+};
+
+struct OutGrad {
+    OutRows r;
+    const float *logz;
+    // scores: ids = given outcomes, g = g_logp
+    const int64_t *given;
+    const float *entropy, *g_logp, *g_entropy;
+    int32_t n_given;
+    // distillation (count 0: scores)
+    OutTeacher teacher;
+    const float *g_loss;
+    char *grad;
+    int64_t grad_row_stride, grad_col_stride;
+};
+
+struct Outcomes {
+    int32_t type = 0;
+    int64_t cols = 0, max_rows = 0;
+    int32_t max_top = 0;
+    float scale = 1.f;
+    uint64_t ws_bytes = 0;
+    uint64_t ticket_off = 0, ticket_count = 0, partial_off = 0, list_off = 0;
+    char *ws = nullptr;
+    char error[256] = {0};
+};
+
+OutSplit out_split(int32_t type, int64_t cols, int64_t rows);
+cudaError_t launch_outcomes_forward(int32_t type, const OutForward &a, bool warp_rows,
+                                    cudaStream_t stream);
+cudaError_t launch_outcomes_grad(int32_t type, const OutGrad &a, bool warp_rows,
+                                 cudaStream_t stream);
+
+}  // namespace tn
+
+struct tn_outcomes_s {
+    tn::Outcomes o;
+};

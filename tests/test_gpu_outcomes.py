@@ -1,0 +1,569 @@
+"""Outcome operators against their definitions in 64 bits.
+
+Tolerances (derived, u = 2^-24 the fp32 rounding):
+* log Z: every exponential carries the exponential unit's error (2 ulp = 4 u),
+  its argument's roundings (3 u |d|, whose weighted mean is at most the
+  entropy plus the reference's lag of 8 powers of two), sums of at most a few
+  hundred sequential terms of random-signed roundings (8 u), and the final sum
+  rounds |scale z| and |log Z|.  In all below 16 u (1 + M + H), M = max |scale z|.
+* log p adds one rounding of each; entropy the same error once more (ln s - t / s).
+* gradients: p inherits log p's absolute error as a relative one; the result
+  is rounded to the rows' type once.
+Ids have to be equal."""
+import numpy as np
+import pytest
+
+import exact_tensor_network_gb300 as tn
+from outcome_reference import INF, Row
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+OUT_EPS = {"f32": 2 * U, "bf16": 2.0 ** -8, "f16": 2.0 ** -11, "c64": 8 * U}
+# smallest steps of the types: results below underflow
+OUT_MIN = {"f32": 1e-44, "bf16": 1e-40, "f16": 2.0 ** -24, "c64": 1e-44}
+TYPES = ["c64", "f32", "bf16", "f16"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def torch_type(t):
+    import torch
+    return {"c64": torch.complex64, "f32": torch.float32, "bf16": torch.bfloat16,
+            "f16": torch.float16}[t]
+
+
+def make_rows(rng, R, V, t, spread=3.0):
+    import torch
+    if t == "c64":
+        a = (rng.standard_normal((R, V)) + 1j * rng.standard_normal((R, V))) / np.sqrt(2.0 * V)
+        return torch.from_numpy(a.astype(np.complex64))
+    z = torch.from_numpy((spread * rng.standard_normal((R, V))).astype(np.float32))
+    return z.to(torch_type(t))
+
+
+def to_np(x):
+    import torch
+    if x.dtype in (torch.bfloat16, torch.float16):
+        x = x.float()
+    return x.cpu().numpy()
+
+
+def close(got, ref, tol, what):
+    got, ref = np.asarray(got, dtype=ref.dtype), np.asarray(ref)
+    tol = np.broadcast_to(tol, ref.shape)
+    nan = np.isnan(ref)
+    assert (np.isnan(got) == nan).all(), f"{what}: NaN in other places"
+    inf = np.isinf(ref) if not np.iscomplexobj(ref) else np.zeros(ref.shape, bool)
+    assert (got[inf] == ref[inf]).all(), f"{what}: infinities differ"
+    ok = ~(nan | inf)
+    err = np.abs(got[ok] - ref[ok])
+    worst = (err - tol[ok]).max() if err.size else -1.0
+    assert worst <= 0, (f"{what}: error {err[np.argmax(err - tol[ok])]:.3e} above its bound "
+                        f"{tol[ok][np.argmax(err - tol[ok])]:.3e}")
+
+
+def tol_logz(r):
+    return 16 * U * (1 + r.mag + abs(r.entropy if np.isfinite(r.entropy) else 0.0))
+
+
+def run_all(rows, t, given, top, teacher, mask=None, scale=1.0, grad_out=None, max_rows=None,
+            teacher_scale=1.0, teacher_type="f32", rng=None):
+    """Every call on these rows (a CPU tensor or a CUDA view) against the
+    definitions."""
+    import torch
+    rng = rng or np.random.default_rng(1)
+    d_rows = rows if rows.is_cuda else rows.cuda()
+    R, V = d_rows.shape
+    d_mask = None if mask is None else (mask if mask.is_cuda else mask.cuda())
+    op = tn.Outcomes(V, torch_type(t), max_rows=max_rows or R, top=top, scale=scale)
+    h_rows = to_np(d_rows)
+    h_mask = None if mask is None else np.broadcast_to(to_np(d_mask), (R, V))
+    ref = [Row(h_rows[i], None if h_mask is None else h_mask[i], scale) for i in range(R)]
+    d_given = None if given is None else torch.from_numpy(given).cuda()
+    s = op.score(d_rows, d_given, mask=d_mask)
+    torch.cuda.synchronize()
+    op.check()
+    tz = np.array([tol_logz(r) for r in ref])
+    close(to_np(s.logz), np.array([r.logz for r in ref]), tz, "log Z")
+    close(to_np(s.entropy), np.array([r.entropy for r in ref]), 2 * tz, "entropy")
+    if given is not None:
+        want = np.stack([r.logp(given[i].reshape(-1)) for i, r in enumerate(ref)])
+        close(to_np(s.logp).reshape(R, -1), want, 2 * tz[:, None], "log p")
+    if top:
+        want = [r.top(top) for r in ref]
+        assert (to_np(s.top_ids) == np.stack([w[0] for w in want])).all(), "alternatives differ"
+        close(to_np(s.top_logp), np.stack([w[1] for w in want]), 2 * tz[:, None], "alternatives' log p")
+
+    def close_grad(got, pairs, what):
+        want = np.stack([p[0] for p in pairs])
+        scale_ = np.stack([p[1] for p in pairs])
+        size = np.abs(np.where(np.isnan(want), 0, want))
+        # log p's error, p's own units, and the rounding to the type
+        tol = (4 * tz[:, None] + 16 * U) * scale_ + OUT_EPS[t] * size + OUT_MIN[t]
+        close(to_np(got), want, tol, what)
+
+    if given is not None:
+        n = given.reshape(R, -1).shape[1]
+        g = rng.standard_normal((R, n)).astype(np.float32)
+        h = rng.standard_normal(R).astype(np.float32)
+        d_g = torch.from_numpy(g).reshape(given.shape).cuda()
+        d_h = torch.from_numpy(h).cuda()
+        got = op.score_grad(d_rows, d_given, s.logz, s.entropy, d_g, d_h, mask=d_mask, out=grad_out)
+        close_grad(got, [r.score_grad(given[i].reshape(-1), g[i], h[i]) for i, r in enumerate(ref)],
+                   "score gradient")
+        got = op.score_grad(d_rows, d_given, s.logz, s.entropy, d_g, mask=d_mask, out=grad_out)
+        close_grad(got, [r.score_grad(given[i].reshape(-1), g[i]) for i, r in enumerate(ref)],
+                   "score gradient without entropy")
+    if teacher is not None:
+        ids, logits = teacher
+        lt = torch.from_numpy(logits).to(torch_type(teacher_type))
+        lref = to_np(lt).astype(np.float64) * np.float64(np.float32(teacher_scale))
+        d_ids, d_l = torch.from_numpy(ids).cuda(), lt.cuda()
+        w = rng.standard_normal(R).astype(np.float32)
+        d_w = torch.from_numpy(w).cuda()
+        r1 = op.distill(d_rows, d_ids, d_l, mask=d_mask, teacher_scale=teacher_scale)
+        r2 = op.distill_step(d_rows, d_ids, d_l, d_w, mask=d_mask, teacher_scale=teacher_scale,
+                             out=grad_out)
+        close_grad(r2.grad, [r.distill_grad(ids[i], lref[i], w[i]) for i, r in enumerate(ref)],
+                   "distill step gradient")
+        g2 = op.distill_grad(d_rows, d_ids, d_l, r1.logz, d_w, mask=d_mask,
+                             teacher_scale=teacher_scale, out=grad_out)
+        close_grad(g2, [r.distill_grad(ids[i], lref[i], w[i]) for i, r in enumerate(ref)],
+                   "distill gradient")
+        want = np.array([r.distill(ids[i], lref[i]) for i, r in enumerate(ref)])
+        fin = np.where(np.isfinite(lref), np.abs(lref), 0.0)
+        tl = 2 * tz + 16 * U * (1 + fin.max(axis=1))
+        for what, r in (("distill", r1), ("distill step", r2)):
+            close(to_np(r.loss), want, tl, what + " loss")
+            close(to_np(r.logz), np.array([x.logz for x in ref]), tz, what + " log Z")
+        torch.cuda.synchronize()
+        op.check()
+    return op
+
+
+def rand_ids(rng, R, n, V):
+    ids = rng.integers(0, V, size=(R, n))
+    ids[rng.random((R, n)) < 0.1] = -1
+    return ids.astype(np.int64)
+
+
+def rand_teacher(rng, R, K, V):
+    t = (2.0 * rng.standard_normal((R, K))).astype(np.float32)
+    t[rng.random((R, K)) < 0.05] = -INF
+    return rand_ids(rng, R, K, V), t
+
+
+SHAPES = [(1, 1), (5, 1), (3, 2), (7, 7), (2, 31), (33, 64), (9, 255), (4, 1000), (3, 2049), (2, 4099),
+          (5, 8192), (1, 50001), (3, 50000), (1, 300007)]
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0]}x{s[1]}")
+def test_matches_definition(shape, t):
+    R, V = shape
+    rng = np.random.default_rng(R * 1000003 + V)
+    run_all(make_rows(rng, R, V, t), t, rand_ids(rng, R, 3, V), 5, rand_teacher(rng, R, 9, V), rng=rng)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("scale", [0.125, 0.7, 2.5])
+@pytest.mark.parametrize("shape", [(6, 333), (2, 20011)], ids=lambda s: f"{s[0]}x{s[1]}")
+def test_temperatures(shape, scale, t):
+    R, V = shape
+    rng = np.random.default_rng(V)
+    run_all(make_rows(rng, R, V, t), t, rand_ids(rng, R, 2, V), 4, rand_teacher(rng, R, 20, V),
+            scale=scale, teacher_scale=scale, teacher_type="bf16" if t == "bf16" else "f16", rng=rng)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("shape", [(12, 77), (10, 1601), (9, 9001), (3, 65537)],
+                         ids=lambda s: f"{s[0]}x{s[1]}")
+@pytest.mark.parametrize("kind", ["random", "prefix", "one_row", "one_column"])
+def test_masks(shape, kind, t):
+    """Masked rows, an empty one among them; NaN, infinities and the type's
+    lowest value lie in masked places."""
+    import torch
+    R, V = shape
+    rng = np.random.default_rng(V + len(kind))
+    rows = make_rows(rng, R, V, t)
+    if kind == "random":
+        keep = rng.random((R, V)) < rng.random((R, 1))
+        keep[R // 2] = False
+    elif kind == "prefix":
+        keep = np.arange(V)[None, :] < rng.integers(0, V + 1, size=(R, 1))
+        keep[0] = False
+        keep[1] = np.arange(V) < 1
+    elif kind == "one_row":
+        keep = rng.random((1, V)) < 0.5
+    else:
+        keep = rng.random((R, 1)) < 0.5
+        keep[0], keep[1] = True, False
+    mask = torch.from_numpy(keep)
+    out = ~np.broadcast_to(keep, (R, V))
+    junk = rng.integers(0, 4, size=(R, V))
+    for v, x in enumerate([float("nan"), INF, -INF, float(torch.finfo(torch_type(t)).min)]):
+        rows[torch.from_numpy(out & (junk == v))] = x
+    run_all(rows, t, rand_ids(rng, R, 4, V), 7, rand_teacher(rng, R, 30, V), mask=mask, rng=rng)
+
+
+def _views(t, kind):
+    """(rows, mask, grad out) views of one layout, 5 x 3001."""
+    import torch
+    rng = np.random.default_rng(11)
+    R, V = 5, 3001
+    data = make_rows(rng, R, V, t).cuda()
+    keep = torch.from_numpy(rng.random((R, V)) < 0.7).cuda()
+
+    def place(x):
+        if kind == "padded":
+            buf = torch.zeros((R, V + 13), dtype=x.dtype, device="cuda")
+            v = buf[:, 5:5 + V]
+        elif kind == "every_second":
+            v = torch.zeros((R, 2 * V), dtype=x.dtype, device="cuda")[:, ::2]
+        elif kind == "transposed":
+            v = torch.zeros((V, R), dtype=x.dtype, device="cuda").t()
+        else:   # rows far apart, first one odd
+            buf = torch.zeros((R * 2, V + 1), dtype=x.dtype, device="cuda")
+            v = buf[1::2, 1:]
+        v.copy_(x)
+        return v
+    return place(data), place(keep), place(torch.zeros_like(data)), rng
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("kind", ["padded", "every_second", "transposed", "far"])
+@pytest.mark.parametrize("masked", [False, True])
+def test_strides(kind, masked, t):
+    rows, keep, out, rng = _views(t, kind)
+    R, V = rows.shape
+    run_all(rows, t, rand_ids(rng, R, 3, V), 6, rand_teacher(rng, R, 11, V),
+            mask=keep if masked else None, grad_out=out, rng=rng)
+    # the same with a contiguous gradient, whose alignment differs
+    run_all(rows, t, rand_ids(rng, R, 3, V), 6, rand_teacher(rng, R, 11, V),
+            mask=keep if masked else None, rng=rng)
+
+
+def test_repeated_row_view():
+    """Row stride 0 (an expanded row)."""
+    rng = np.random.default_rng(5)
+    row = make_rows(rng, 1, 777, "f32").cuda()
+    run_all(row.expand(6, 777), "f32", rand_ids(rng, 6, 2, 777), 3, rand_teacher(rng, 6, 4, 777), rng=rng)
+
+
+@pytest.mark.parametrize("k", [1, 2, 33, 128])
+@pytest.mark.parametrize("order", ["ascending", "descending", "equal", "two_values", "few", "zeros",
+                                   "block"])
+@pytest.mark.parametrize("shape", [(3, 100), (3, 1700), (2, 30000), (4, 262144), (1, 1500001)],
+                         ids=lambda s: f"{s[0]}x{s[1]}")
+def test_alternatives_of_hard_rows(shape, order, k):
+    """Sorted rows, ties everywhere (lowest index first), fewer present
+    entries than alternatives, signed zeros, all the best side by side."""
+    import torch
+    R, V = shape
+    rng = np.random.default_rng(k)
+    z = np.zeros((R, V), np.float32)
+    if order == "ascending":
+        z[:] = np.arange(V) * (30.0 / V)
+    elif order == "descending":
+        z[:] = -np.arange(V) * (30.0 / V)
+    elif order == "equal":
+        z[:] = 1.5
+    elif order == "two_values":
+        z[:] = rng.integers(0, 2, size=(R, V))
+    elif order == "few":
+        z[:] = -INF
+        for r in range(R):
+            z[r, rng.integers(0, V, size=5)] = rng.standard_normal(5)
+    elif order == "zeros":
+        z[:] = np.where(rng.random((R, V)) < 0.5, 0.0, -0.0)
+    else:
+        z[:] = rng.standard_normal((R, V))
+        z[:, V // 3:V // 3 + 200] += 20.0
+    for t in ("f32", "bf16"):
+        run_all(torch.from_numpy(z).to(torch_type(t)), t, None, k, None)
+
+
+@pytest.mark.parametrize("t", ["bf16", "c64"])
+def test_many_rows_of_one_cta_each(t):
+    """Rows that fill the GPU alone: one segment per row, maxima of 32
+    vectors."""
+    V = {"bf16": 20001, "c64": 2501}[t]
+    rng = np.random.default_rng(3)
+    run_all(make_rows(rng, 640, V, t), t, rand_ids(rng, 640, 1, V), 20, None, rng=rng)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("V", [50, 40000])
+def test_rows_without_distribution(V, t):
+    """NaN and +inf in present places, -inf everywhere, the lowest value
+    everywhere; neighbours are untouched."""
+    import torch
+    rng = np.random.default_rng(9)
+    rows = make_rows(rng, 6, V, t)
+    rows[1, V // 2] = float("nan")
+    rows[3, V - 1] = INF
+    rows[4] = -INF if t != "c64" else 0.0
+    if t != "c64":
+        rows[5] = -INF
+        rows[5, 7] = 2.0        # one outcome left: probability one
+    run_all(rows, t, rand_ids(rng, 6, 4, V), 5, rand_teacher(rng, 6, 6, V), rng=rng)
+    if t in ("f32", "bf16"):
+        low = torch.full((2, V), float(torch.finfo(torch_type(t)).min), dtype=torch_type(t)).cuda()
+        s = tn.Outcomes(V, torch_type(t), max_rows=2, top=3).score(low)
+        assert (to_np(s.top_ids) == [0, 1, 2]).all()
+        np.testing.assert_allclose(to_np(s.entropy), np.log(V), rtol=1e-5)
+        np.testing.assert_allclose(to_np(s.logz), float(torch.finfo(torch_type(t)).min), rtol=1e-6)
+
+
+def test_absent_teacher_outcomes():
+    """A teacher's outcome with an unmasked -inf logit: infinite loss; the
+    same outcome masked: left out of the teacher."""
+    import torch
+    rng = np.random.default_rng(2)
+    rows = make_rows(rng, 3, 100, "f32")
+    rows[:, 10] = -INF
+    ids = np.array([[10, 20], [20, 30], [10, -1]], np.int64)
+    t = np.zeros((3, 2), np.float32)
+    run_all(rows, "f32", None, 0, (ids, t))
+    keep = torch.ones((3, 100), dtype=torch.bool)
+    keep[:, 10] = False
+    run_all(rows, "f32", None, 0, (ids, t), mask=keep)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("V", [40, 30011])
+def test_repeated_ids_add_up(V, t):
+    rng = np.random.default_rng(21)
+    R = 4
+    ids = rng.integers(0, 6, size=(R, 256)).astype(np.int64)
+    given = rng.integers(0, 5, size=(R, 256)).astype(np.int64)
+    run_all(make_rows(rng, R, V, t), t, given, 0,
+            (ids, rng.standard_normal((R, 256)).astype(np.float32)), rng=rng)
+
+
+@pytest.mark.parametrize("V", [60, 70001])
+def test_given_shapes_and_none(V):
+    """[R] ids, all -1, and no given at all."""
+    rng = np.random.default_rng(4)
+    rows = make_rows(rng, 3, V, "bf16")
+    run_all(rows, "bf16", rng.integers(0, V, size=3).astype(np.int64), 0, None, rng=rng)
+    run_all(rows, "bf16", np.full((3, 2), -1, np.int64), 1, None, rng=rng)
+    run_all(rows, "bf16", None, 2, (np.full((3, 2), -1, np.int64), np.zeros((3, 2), np.float32)), rng=rng)
+
+
+@pytest.mark.parametrize("V", [50, 30000])
+def test_ids_out_of_range_are_reported(V):
+    """Ids outside [-1, cols) read nothing: NaN in their places and a device
+    status, which the next check finds cleared."""
+    import torch
+    rng = np.random.default_rng(6)
+    rows = make_rows(rng, 3, V, "f32").cuda()
+    op = tn.Outcomes(V, torch.float32, max_rows=3)
+    given = torch.tensor([[0, V], [1, -1], [-2, 3]]).cuda()
+    s = op.score(rows, given)
+    torch.cuda.synchronize()
+    with pytest.raises(tn.TNError) as e:
+        op.check()
+    assert e.value.status == tn.TN_EDEVICE
+    op.check()
+    lp = to_np(s.logp)
+    assert np.isnan(lp[0, 1]) and np.isnan(lp[2, 0]) and np.isfinite(lp[[0, 1, 1, 2], [0, 0, 1, 1]]).all()
+    g = op.score_grad(rows, given, s.logz, s.entropy, torch.ones_like(s.logp))
+    with pytest.raises(tn.TNError):
+        op.check()
+    assert np.isfinite(to_np(g)).all()
+    r = op.distill(rows, given, torch.zeros_like(s.logp))
+    with pytest.raises(tn.TNError):
+        op.check()
+    loss = to_np(r.loss)
+    assert np.isnan(loss[[0, 2]]).all() and np.isfinite(loss[1])
+
+
+@pytest.mark.parametrize("t", ["f32", "c64"])
+def test_gradients_against_differences(t):
+    """Central differences of the 64-bit scores and loss along single
+    entries, at steps whose truncation (h^2) and cancellation (2^-53 / h) are
+    both below 1e-8."""
+    import torch
+    rng = np.random.default_rng(8)
+    V, c = 23, 0.8
+    rows = make_rows(rng, 1, V, t)
+    h_row = to_np(rows)[0]
+    given = np.array([[3, 3, 11]], np.int64)
+    g, he = np.array([0.3, -1.1, 0.7]), 0.4
+    ids, tl = np.array([[2, 5, 5, 19]], np.int64), np.array([[0.5, -1.0, 0.1, 2.0]], np.float32)
+
+    def score(row):
+        r = Row64(row, c)
+        return float(g @ r.logp(given[0]) + he * r.entropy)
+
+    def loss(row):
+        return Row64(row, c).distill(ids[0], tl[0].astype(np.float64))
+
+    op = tn.Outcomes(V, torch_type(t), scale=c)
+    d = rows.cuda()
+    s = op.score(d, torch.from_numpy(given).cuda())
+    gs = to_np(op.score_grad(d, torch.from_numpy(given).cuda(), s.logz, s.entropy,
+                             torch.from_numpy(g[None].astype(np.float32)).cuda(),
+                             torch.tensor([he], dtype=torch.float32).cuda()))[0]
+    gd = to_np(op.distill_step(d, torch.from_numpy(ids).cuda(), torch.from_numpy(tl).cuda(),
+                               torch.ones(1).cuda()).grad)[0]
+    base = h_row.astype(np.complex128 if t == "c64" else np.float64)
+    eps = 1e-4 * (np.abs(base).mean() if t == "c64" else 1.0)
+    for got, fn in ((gs, score), (gd, loss)):
+        scale = np.abs(got).max()
+        for v in range(V):
+            for unit, part in ((1.0, np.real), (1j, np.imag)) if t == "c64" else ((1.0, np.real),):
+                up, dn = base.copy(), base.copy()
+                up[v] += eps * unit
+                dn[v] -= eps * unit
+                want = (fn(up) - fn(dn)) / (2 * eps)
+                assert abs(part(got[v]) - want) <= 2e-5 * scale, (v, unit)
+
+
+class Row64(Row):
+    """The definition without the 32-bit order value, for differences."""
+
+    def __init__(self, row, scale):
+        super().__init__(row, None, scale)
+        if np.iscomplexobj(row):
+            self.x = scale * np.log(row.real ** 2 + row.imag ** 2)
+            m = self.x.max()
+            self.logz = m + np.log(np.exp(self.x - m).sum())
+            lp = self.x - self.logz
+            self.entropy = -(np.exp(lp) * lp).sum()
+
+
+@pytest.mark.parametrize("shape", [(3, 1000), (2, 200001)], ids=lambda s: f"{s[0]}x{s[1]}")
+def test_results_do_not_vary(shape):
+    """Bitwise equal from run to run, and on a handle made for more rows."""
+    import torch
+    R, V = shape
+    rng = np.random.default_rng(12)
+    rows = make_rows(rng, R, V, "bf16").cuda()
+    given = torch.from_numpy(rand_ids(rng, R, 3, V)).cuda()
+    ids, t = rand_teacher(rng, R, 12, V)
+    ids, t, w = torch.from_numpy(ids).cuda(), torch.from_numpy(t).cuda(), torch.ones(R).cuda()
+    runs = []
+    for max_rows in (R, R, 50):
+        op = tn.Outcomes(V, torch.bfloat16, max_rows=max_rows, top=9)
+        for _ in range(3):
+            s = op.score(rows, given)
+            d = op.distill_step(rows, ids, t, w)
+            runs.append([to_np(x) for x in (*s, *d)])
+    for r in runs[1:]:
+        for a, b in zip(runs[0], r):
+            assert a.tobytes() == b.tobytes()
+
+
+def test_own_stream_and_graph():
+    """On a side stream, and captured into a CUDA graph and replayed on new
+    contents."""
+    import torch
+    rng = np.random.default_rng(13)
+    V, R = 100003, 2
+    a, b = make_rows(rng, R, V, "f32").cuda(), make_rows(rng, R, V, "f32").cuda()
+    op = tn.Outcomes(V, torch.float32, max_rows=R, top=4)
+    want = [to_np(x) for r in (a, b) for x in op.score(r)[:2] + op.score(r)[3:]]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    s = op.score(a, stream=side)
+    side.synchronize()
+    for x, y in zip((s.logz, s.entropy, s.top_ids, s.top_logp), want[:4]):
+        assert (to_np(x) == y).all()
+    buf, out = a.clone(), op.score(a)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.score(buf, out=out)
+    for rows, w in ((b, want[4:]), (a, want[:4])):
+        buf.copy_(rows)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip((out.logz, out.entropy, out.top_ids, out.top_logp), w):
+            assert (to_np(x) == y).all()
+
+
+def test_no_rows():
+    import torch
+    op = tn.Outcomes(100, torch.float32, max_rows=4, top=3)
+    s = op.score(torch.empty((0, 100), device="cuda"))
+    assert s.logz.shape == (0,) and s.top_ids.shape == (0, 3)
+    e = torch.empty((0, 2), dtype=torch.int64, device="cuda")
+    d = op.distill_step(torch.empty((0, 100), device="cuda"), e, torch.empty((0, 2), device="cuda"),
+                        torch.empty(0, device="cuda"))
+    assert d.grad.shape == (0, 100)
+
+
+def test_offsets_past_32_bits():
+    """Rows whose last entries lie past 2^32 bytes and 2^31 entries."""
+    import torch
+    V, R = 3000001, 720                     # 2.16e9 entries of bf16: 4.3 GB
+    rows = torch.zeros((R, V), dtype=torch.bfloat16, device="cuda")
+    rows[R - 1, V - 2] = 9.0
+    rows[R - 1, V - 1] = 8.0
+    rows[0, 5] = 7.0
+    op = tn.Outcomes(V, torch.bfloat16, max_rows=R, top=2)
+    given = torch.full((R, 1), V - 2, dtype=torch.int64, device="cuda")
+    s = op.score(rows, given)
+    assert to_np(s.top_ids[R - 1]).tolist() == [V - 2, V - 1]
+    assert to_np(s.top_ids[0]).tolist() == [5, 0]
+    lz = np.log(V - 2 + np.exp(9.0) + np.exp(8.0))
+    np.testing.assert_allclose(float(s.logz[R - 1]), lz, rtol=1e-6)
+    np.testing.assert_allclose(float(s.logp[R - 1, 0]), 9.0 - lz, rtol=1e-5)
+    g = op.score_grad(rows, given, s.logz, s.entropy, torch.ones((R, 1), device="cuda"))
+    np.testing.assert_allclose(float(g[R - 1, V - 2]), 1 - np.exp(9.0 - lz), rtol=2.0 ** -8)
+    np.testing.assert_allclose(float(g[R - 1, V - 1]), -np.exp(8.0 - lz), rtol=2.0 ** -8)
+    np.testing.assert_allclose(float(g[R - 1, 0]), -np.exp(-lz), rtol=2.0 ** -8)
+
+
+def test_refusals():
+    import torch
+    op = tn.Outcomes(64, torch.float32, max_rows=2, top=3)
+    ok = torch.zeros((2, 64), device="cuda")
+    ids, t, w = torch.zeros((2, 4), dtype=torch.int64).cuda(), torch.zeros((2, 4)).cuda(), torch.ones(2).cuda()
+    bad_calls = [
+        lambda: op.score(ok.double()),
+        lambda: op.score(ok.cpu()),
+        lambda: op.score(ok[:, :63]),
+        lambda: op.score(ok[None]),
+        lambda: op.score(ok, ids.int()),
+        lambda: op.score(ok, ids.cpu()),
+        lambda: op.score(ok, ids[:1]),
+        lambda: op.score(ok, ids.t().contiguous().t()),
+        lambda: op.score(ok, mask=ok),
+        lambda: op.score(ok, mask=torch.ones((2, 64), dtype=torch.bool)),
+        lambda: op.score_grad(ok, ids, w, w, t[:, :2].contiguous()),
+        lambda: op.score_grad(ok, ids, w.double(), w, t),
+        lambda: op.score_grad(ok, ids, w, w, t, w[:1]),
+        lambda: op.score_grad(ok, ids, w, w, t, out=ok[:1]),
+        lambda: op.distill(ok, ids, t.double()),
+        lambda: op.distill(ok, ids, t[:, :3].contiguous()),
+        lambda: op.distill_step(ok, ids, t, w.cpu()),
+        lambda: tn.Outcomes(64, torch.complex64, max_rows=2).score(torch.zeros((2, 64), dtype=torch.complex64).cuda().conj()),
+        lambda: tn.Outcomes(64, torch.float64),
+    ]
+    for f in bad_calls:
+        with pytest.raises((ValueError, RuntimeError)):
+            f()
+    # refused by the library
+    for f in (lambda: op.score(torch.zeros((3, 64), device="cuda")),            # more rows than made for
+              lambda: op.score(ok, torch.zeros((2, 257), dtype=torch.int64).cuda()),
+              lambda: op.distill(ok, ids, t, teacher_scale=0.0),
+              lambda: op.distill(ok, ids, t, teacher_scale=INF),
+              lambda: op.score(torch.zeros((2, 1), device="cuda").expand(2, 64))):
+        with pytest.raises(tn.TNError) as e:
+            f()
+        assert e.value.status == tn.TN_EINVAL
+    with pytest.raises(tn.TNError) as e:
+        tn.tn_outcomes_score(tn.Outcomes(64, torch.float32).handle,
+                             tn.tn_rows(ok.data_ptr(), 1, 64, 1, None, 0, 0), None, 0, None,
+                             w.data_ptr(), w.data_ptr(), 0, None, None)
+    assert e.value.status == tn.TN_ENOMEM
+    torch.cuda.synchronize()
+    op.check()
