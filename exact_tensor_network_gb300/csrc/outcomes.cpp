@@ -11,6 +11,35 @@
 
 #include "outcomes.h"
 
+namespace tn {
+
+OutSplit out_split(int32_t type, int64_t cols, int64_t rows) {
+    const int64_t E = kOutVecBytes / out_entry_bytes(type);
+    OutSplit s;
+    s.vecs = (cols + E - 1 + E - 1) / E;   // the first vector may hold one entry only
+    s.warp_rows = s.vecs <= kOutWarpVecs;
+    s.segs = 1;
+    s.seg_vecs = s.vecs;
+    s.flat = false;
+    if (s.warp_rows) return s;
+    // a CTA of less than two vectors a thread gains nothing
+    const int64_t target = kOutTarget;
+    int64_t want = rows >= target ? 1 : (target + rows - 1) / rows;
+    const int64_t most = (s.vecs + 2 * kOutThreads - 1) / (2 * kOutThreads);
+    if (want > most) want = most;
+    const int64_t least = (s.vecs + kOutSegVecs - 1) / kOutSegVecs;
+    if (want < least) want = least;
+    int64_t sv = (s.vecs + want - 1) / want;
+    if (want > 1) sv = (sv + kOutThreads - 1) / kOutThreads * kOutThreads;
+    if (sv > kOutSegVecs) sv = kOutSegVecs;
+    s.seg_vecs = sv;
+    s.segs = (s.vecs + sv - 1) / sv;
+    s.flat = s.segs > 1 && s.vecs <= kOutSegVecs;
+    return s;
+}
+
+}  // namespace tn
+
 namespace {
 
 using tn::Outcomes;
@@ -31,25 +60,32 @@ tn_status cuda_fail(Outcomes &o, cudaError_t e, const char *what) {
 
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
 
-// Most segments that calls of up to max_rows rows can use at once, and most
-// rows that are split.
-void workspace_slots(const Outcomes &o, uint64_t *tickets, uint64_t *slots) {
-    *tickets = *slots = 0;
+// What calls of up to max_rows rows need at most: rows that are split, their
+// segments, and bytes for the segments' lists or chunk maxima.
+struct Need {
+    uint64_t tickets = 0, slots = 0, list_bytes = 0;
+};
+
+void add_need(const Outcomes &o, int64_t rows, Need *n) {
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows);
+    if (s.segs == 1) return;
+    const uint64_t slots = (uint64_t)rows * s.segs;
+    const uint64_t bytes = o.max_top == 0 ? 0
+                           : s.flat       ? (uint64_t)rows * (tn::kOutKeys + 1) * sizeof(uint32_t)
+                                          : slots * o.max_top * sizeof(uint64_t);
+    if ((uint64_t)rows > n->tickets) n->tickets = rows;
+    if (slots > n->slots) n->slots = slots;
+    if (bytes > n->list_bytes) n->list_bytes = bytes;
+}
+
+Need workspace_need(const Outcomes &o) {
+    Need n;
     // the number of segments a row falls to its lowest value once the rows
     // alone fill the GPU
-    const int64_t last = o.max_rows < 4 * 152 ? o.max_rows : 4 * 152;
-    for (int64_t r = 1; r <= last; ++r) {
-        const tn::OutSplit s = tn::out_split(o.type, o.cols, r);
-        if (s.segs > 1) {
-            *tickets = r;
-            if ((uint64_t)(r * s.segs) > *slots) *slots = r * s.segs;
-        }
-    }
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, o.max_rows);
-    if (s.segs > 1) {
-        *tickets = o.max_rows;
-        if ((uint64_t)(o.max_rows * s.segs) > *slots) *slots = o.max_rows * s.segs;
-    }
+    const int64_t last = o.max_rows < tn::kOutTarget ? o.max_rows : tn::kOutTarget;
+    for (int64_t r = 1; r <= last; ++r) add_need(o, r, &n);
+    add_need(o, o.max_rows, &n);
+    return n;
 }
 
 uint64_t align(uint64_t x) { return (x + 255) / 256 * 256; }
@@ -104,6 +140,9 @@ tn::OutRows rows_of(const Outcomes &o, const tn_rows *r, const tn::OutSplit &s) 
     a.mask_col_stride = r->mask_col_stride;
     a.scale = o.scale;
     a.c2 = o.type == TN_TYPE_C64 ? o.scale : static_cast<float>(o.scale * 1.4426950408889634);
+    int x;
+    std::frexp(a.c2, &x);                       // c2 <= 2^x
+    a.floor = -std::ldexp(1.f, x > 0 ? 126 - x : 126);   // a bf16 number as well
     a.seg_vecs = s.seg_vecs;
     a.segs = s.segs;
     a.status = reinterpret_cast<tn::DevStatus *>(o.ws);
@@ -114,30 +153,59 @@ tn::OutTeacher teacher_of(const tn_teacher *t) {
     return tn::OutTeacher{t->ids, t->logits, t->type, t->count, t->scale};
 }
 
+// The kernel of the rows' type.
+template <class Args, class C64, class F32, class BF16, class F16>
+cudaError_t by_type(int32_t type, C64 c64, F32 f32, BF16 bf16, F16 f16, const Args &a, bool warp_rows,
+                    cudaStream_t stream) {
+    switch (type) {
+        case TN_TYPE_C64: return c64(a, warp_rows, stream);
+        case TN_TYPE_F32: return f32(a, warp_rows, stream);
+        case TN_TYPE_BF16: return bf16(a, warp_rows, stream);
+        default: return f16(a, warp_rows, stream);
+    }
+}
+
 tn_status forward(Outcomes &o, tn::OutForward &a, const tn::OutSplit &s, cudaStream_t stream) {
     const int64_t E = tn::kOutVecBytes / tn::out_entry_bytes(o.type);
     const int64_t k = a.n_top;
     if (k > 0) {
-        const int64_t nv = s.seg_vecs;
-        int64_t words = nv <= tn::kOutKeys ? nv : (nv + 31) / 32;
-        const int64_t entries = (k < nv ? k : nv) * E;
-        if (words < entries) words = entries;
-        if (s.segs > 1 && words < 8 * k) words = 8 * k;
-        a.key_words = static_cast<int32_t>(words);
-        // vector maxima of k chunks; or the joiner's octets of k lists
-        int64_t sub = nv > tn::kOutKeys ? 32 * k : 0;
+        // maxima of as many vectors as leave four times as many of them as
+        // alternatives, so that the cut is well inside; at most kOutKeys
+        const int64_t nv = s.flat ? s.vecs : s.seg_vecs;
+        int log = s.warp_rows ? 0 : tn::kOutChunkLog;
+        while (log > 0 && nv >> log < 4 * k && nv <= (int64_t)tn::kOutKeys << (log - 1)) --log;
+        a.chunk_log = log;
+        int64_t words = (nv >> log) + 1;
+        if (s.segs > 1 && words < s.segs) words = s.segs < tn::kOutKeys ? s.segs : tn::kOutKeys;
+        words = (words + 3) / 4 * 4;
+        // room for the entries of k vectors or of k octets of list entries;
+        // as words, for the maxima of k chunks' vectors and of k lists' octets
+        int64_t cand = 8 * k, sub = k << log;
         if (s.segs > 1 && sub < k * ((k + 7) / 8)) sub = k * ((k + 7) / 8);
-        a.sub_words = static_cast<int32_t>(sub);
+        if (cand < sub / 2 + 1) cand = sub / 2 + 1;
+        if (!s.warp_rows && cand < 128) cand = 128;
+        cand = (cand + 1) / 2 * 2;
+        a.key_words = static_cast<int32_t>(words);
+        a.cand_len = static_cast<int32_t>(cand);
+        const int64_t kk = (k + 3) / 4 * 4, pp = (tn::out_most((int)k) + 3) / 4 * 4;
+        a.group_bytes = static_cast<int32_t>(words * 4 + cand * 8 + kk * 8 + pp * 8 + 16);
     }
     a.tickets = reinterpret_cast<uint32_t *>(o.ws + o.ticket_off);
     a.partials = reinterpret_cast<tn::OutPartial *>(o.ws + o.partial_off);
-    a.lists = reinterpret_cast<uint2 *>(o.ws + o.list_off);
-    const cudaError_t e = tn::launch_outcomes_forward(o.type, a, s.warp_rows, stream);
+    a.flat = s.flat;
+    a.row_chunks = static_cast<int32_t>(s.flat ? (s.vecs >> a.chunk_log) + 1 : 0);
+    if (s.flat) a.maxima = reinterpret_cast<uint32_t *>(o.ws + o.list_off);
+    else a.lists = reinterpret_cast<uint64_t *>(o.ws + o.list_off);
+    const cudaError_t e = by_type(o.type, tn::outcomes_forward_of<TN_TYPE_C64>, tn::outcomes_forward_of<TN_TYPE_F32>,
+                                  tn::outcomes_forward_of<TN_TYPE_BF16>, tn::outcomes_forward_of<TN_TYPE_F16>, a,
+                                  s.warp_rows, stream);
     return e == cudaSuccess ? TN_OK : cuda_fail(o, e, "launching the forward pass");
 }
 
 tn_status gradient(Outcomes &o, const tn::OutGrad &a, const tn::OutSplit &s, cudaStream_t stream) {
-    const cudaError_t e = tn::launch_outcomes_grad(o.type, a, s.warp_rows, stream);
+    const cudaError_t e = by_type(o.type, tn::outcomes_grad_of<TN_TYPE_C64>, tn::outcomes_grad_of<TN_TYPE_F32>,
+                                  tn::outcomes_grad_of<TN_TYPE_BF16>, tn::outcomes_grad_of<TN_TYPE_F16>, a,
+                                  s.warp_rows, stream);
     return e == cudaSuccess ? TN_OK : cuda_fail(o, e, "launching the gradient");
 }
 
@@ -153,7 +221,8 @@ tn_status tn_outcomes_create(int32_t type, int64_t cols, int64_t max_rows, int32
     if (cols < 1 || max_rows < 1) return fail(g_error, TN_EINVAL, "cols and max_rows must be >= 1");
     if (max_top < 0 || max_top > TN_OUTCOMES_MAX_TOP)
         return fail(g_error, TN_EINVAL, "max_top %d outside 0 .. %d", (int)max_top, (int)TN_OUTCOMES_MAX_TOP);
-    if (!(scale > 0.f) || std::isinf(scale)) return fail(g_error, TN_EINVAL, "scale must be finite and > 0");
+    if (!(scale >= 0x1p-40f && scale <= 0x1p40f))
+        return fail(g_error, TN_EINVAL, "scale must lie in 2^-40 .. 2^40");
     if (cols > (int64_t)1 << 40) return fail(g_error, TN_EOVERFLOW, "more than 2^40 entries a row");
     int64_t items;
     if (!mul_ok(max_rows, tn::out_split(type, cols, max_rows).segs, &items) || items > 0x7fffffff)
@@ -166,12 +235,11 @@ tn_status tn_outcomes_create(int32_t type, int64_t cols, int64_t max_rows, int32
     o.max_rows = max_rows;
     o.max_top = max_top;
     o.scale = scale;
-    uint64_t slots;
-    workspace_slots(o, &o.ticket_count, &slots);
+    const Need n = workspace_need(o);
     o.ticket_off = 256;
-    o.partial_off = align(o.ticket_off + o.ticket_count * sizeof(uint32_t));
-    o.list_off = align(o.partial_off + slots * sizeof(tn::OutPartial));
-    o.ws_bytes = align(o.list_off + slots * max_top * sizeof(uint2));
+    o.partial_off = align(o.ticket_off + n.tickets * sizeof(uint32_t));
+    o.list_off = align(o.partial_off + n.slots * sizeof(tn::OutPartial));
+    o.ws_bytes = align(o.list_off + n.list_bytes);
     g_error[0] = 0;
     *out = h;
     return TN_OK;

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "outcomes.h"
 
@@ -13,15 +15,40 @@ namespace tn {
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Results below 2^-126 are flushed to 0: next to sums that hold a term of
+// about 1 they are nothing, and keeping them costs three more instructions.
 __device__ __forceinline__ float ex2(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float lg2(float x) {
     float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+          "l"(reinterpret_cast<uint64_t &>(c)));
+    return reinterpret_cast<float2 &>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return reinterpret_cast<float2 &>(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return reinterpret_cast<float2 &>(d);
 }
 // larger of two, NaN if either is (a row with a NaN has no distribution: it
 // must not be lost in a maximum)
@@ -29,6 +56,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // ---- entries ----------------------------------------------------------------
@@ -39,6 +72,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // any other implementation of the definition too).  kAbsent marks an absent
 // entry.
 
+// Mask bytes: 0x80 in every nonzero byte; those bits spread over the bytes
+// that a selector names; one of two by such a mask.
+__device__ __forceinline__ uint32_t nonzero_bytes(uint32_t x) {
+    return (((x & 0x7f7f7f7fu) + 0x7f7f7f7fu) | x) & 0x80808080u;
+}
+__device__ __forceinline__ uint32_t spread(uint32_t k, uint32_t selector) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(d) : "r"(k), "r"(selector));
+    return d;
+}
+__device__ __forceinline__ uint32_t pick(uint32_t a, uint32_t mask, uint32_t b) {
+    return (a & mask) | (b & ~mask);
+}
+__device__ __forceinline__ void blank16(uint4 &r, uint64_t keep, uint32_t absent) {
+    const uint32_t a = nonzero_bytes(static_cast<uint32_t>(keep));
+    const uint32_t b = nonzero_bytes(static_cast<uint32_t>(keep >> 32));
+    r.x = pick(r.x, spread(a, 0x9988), absent);
+    r.y = pick(r.y, spread(a, 0xbbaa), absent);
+    r.z = pick(r.z, spread(b, 0x9988), absent);
+    r.w = pick(r.w, spread(b, 0xbbaa), absent);
+}
+
+// absent_vector: 16 bytes of absent entries; blank: make the entries absent
+// whose mask byte is 0.
 template <int TYPE>
 struct Entry;
 
@@ -53,6 +110,16 @@ struct Entry<TN_TYPE_F32> {
         v[1] = __uint_as_float(r.y);
         v[2] = __uint_as_float(r.z);
         v[3] = __uint_as_float(r.w);
+    }
+    static __device__ __forceinline__ uint4 absent_vector() {
+        return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+    }
+    static __device__ __forceinline__ void blank(uint4 &r, uint32_t keep) {
+        const uint32_t k = nonzero_bytes(keep);
+        r.x = pick(r.x, spread(k, 0x8888), 0xff800000u);
+        r.y = pick(r.y, spread(k, 0x9999), 0xff800000u);
+        r.z = pick(r.z, spread(k, 0xaaaa), 0xff800000u);
+        r.w = pick(r.w, spread(k, 0xbbbb), 0xff800000u);
     }
 };
 
@@ -70,6 +137,10 @@ struct Entry<TN_TYPE_BF16> {
             v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    static __device__ __forceinline__ uint4 absent_vector() {
+        return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+    }
+    static __device__ __forceinline__ void blank(uint4 &r, uint64_t keep) { blank16(r, keep, 0xff80ff80u); }
 };
 
 template <>
@@ -87,6 +158,10 @@ struct Entry<TN_TYPE_F16> {
             v[2 * i + 1] = f.y;
         }
     }
+    static __device__ __forceinline__ uint4 absent_vector() {
+        return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u);
+    }
+    static __device__ __forceinline__ void blank(uint4 &r, uint64_t keep) { blank16(r, keep, 0xfc00fc00u); }
 };
 
 template <>
@@ -100,6 +175,11 @@ struct Entry<TN_TYPE_C64> {
     static __device__ __forceinline__ void values(const uint4 &r, float (&v)[E]) {
         v[0] = value(make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
         v[1] = value(make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
+    }
+    static __device__ __forceinline__ uint4 absent_vector() { return make_uint4(0, 0, 0, 0); }
+    static __device__ __forceinline__ void blank(uint4 &r, uint32_t keep) {
+        if (!(keep & 0xff)) r.x = r.y = 0;
+        if (!(keep & 0xff00)) r.z = r.w = 0;
     }
 };
 
@@ -149,66 +229,83 @@ struct Row {
     __device__ __forceinline__ uint4 raw(int64_t e0) const {
         return __ldg(reinterpret_cast<const uint4 *>(p + e0));
     }
-    __device__ __forceinline__ bool keep(int64_t e) const { return !m || m[e * mcs] != 0; }
+    __device__ __forceinline__ bool kept(int64_t e) const { return !m || m[e * mcs] != 0; }
     __device__ __forceinline__ float value(int64_t e) const {
-        return keep(e) ? En::value(p[e * cs]) : absent<TYPE>();
+        return kept(e) ? En::value(p[e * cs]) : absent<TYPE>();
     }
-    // bit i: entry e0 + i of a vector inside the row is kept
-    __device__ __forceinline__ uint32_t keep_bits(int64_t e0) const {
+    // The mask bytes of the vector at e0, which lies inside the row, entry i in
+    // byte i.  They lie at any offset from the data's vectors: one aligned
+    // word, or two and a shift where both are inside the mask's row.
+    using Keep = typename std::conditional<En::E == 8, uint64_t, uint32_t>::type;
+    __device__ __forceinline__ Keep keep(int64_t e0) const {
         constexpr int E = En::E;
-        uint32_t bits = 0;
         if constexpr (E >= 4) {
             if (mcs == 1) {
-                // mask bytes lie at any offset from the data's vectors: one
-                // aligned word, or two and a shift where both are inside
-                using W = typename std::conditional<E == 8, uint64_t, uint32_t>::type;
                 const uint8_t *q = m + e0;
                 const int off = static_cast<int>(reinterpret_cast<uintptr_t>(q) % E);
                 const uint8_t *b = q - off;
-                W w;
-                bool have = false;
-                if (off == 0) {
-                    w = *reinterpret_cast<const W *>(b);
-                    have = true;
-                } else if (b >= m && b + 2 * E <= m + cols) {
-                    const W lo = reinterpret_cast<const W *>(b)[0];
-                    const W hi = reinterpret_cast<const W *>(b)[1];
-                    w = (lo >> (8 * off)) | (hi << (8 * (E - off)));
-                    have = true;
-                }
-                if (have) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i)
-                        if ((w >> (8 * i)) & 0xff) bits |= 1u << i;
-                    return bits;
+                if (off == 0) return __ldg(reinterpret_cast<const Keep *>(b));
+                if (b >= m && b + 2 * E <= m + cols) {
+                    const Keep lo = __ldg(reinterpret_cast<const Keep *>(b));
+                    const Keep hi = __ldg(reinterpret_cast<const Keep *>(b) + 1);
+                    return (lo >> (8 * off)) | (hi << (8 * (E - off)));
                 }
             }
         }
+        Keep w = 0;
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (m[(e0 + i) * mcs]) bits |= 1u << i;
-        return bits;
+        for (int i = 0; i < E; ++i) w |= static_cast<Keep>(m[(e0 + i) * mcs]) << (8 * i);
+        return w;
     }
-    // the order values of vector j
-    __device__ __forceinline__ void vector(int64_t j, float (&v)[En::E]) const {
-        const int64_t e0 = j * En::E - head;
-        if (inside(e0)) {
-            En::values(raw(e0), v);
-            if (m) {
-                const uint32_t bits = keep_bits(e0);
-#pragma unroll
-                for (int i = 0; i < En::E; ++i)
-                    if (!(bits >> i & 1)) v[i] = absent<TYPE>();
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < En::E; ++i) {
-                const int64_t e = e0 + i;
-                v[i] = e >= 0 && e < cols ? value(e) : absent<TYPE>();
-            }
-        }
+    // vectors [lo, hi) lie inside the row
+    __device__ __forceinline__ void inside_range(int64_t &lo, int64_t &hi) const {
+        lo = cs == 1 ? (head + En::E - 1) / En::E : 0;
+        hi = cs == 1 ? (head + cols) / En::E : 0;
+    }
+    __device__ __forceinline__ const uint4 *vectors() const {
+        return reinterpret_cast<const uint4 *>(p - head);
     }
 };
+
+// Out of line, for what is not in a kernel's steady loop (inlined, these
+// would be most of its code, and that code's instruction-cache misses most of
+// a short row's time).
+template <int E>
+struct Values {
+    float v[E];
+};
+
+template <int TYPE>
+__device__ __noinline__ typename Row<TYPE>::Keep row_keep(const Row<TYPE> r, int64_t e0) {
+    return r.keep(e0);
+}
+
+// order value of entry e
+template <int TYPE>
+__device__ __noinline__ float row_value(const Row<TYPE> r, int64_t e) {
+    return r.value(e);
+}
+
+// order values of vector j, absent outside the row
+template <int TYPE>
+__device__ __noinline__ Values<Entry<TYPE>::E> row_vector(const Row<TYPE> r, int64_t j) {
+    using En = Entry<TYPE>;
+    Values<En::E> o;
+    const int64_t e0 = j * En::E - r.head;
+    if (r.inside(e0)) {
+        uint4 q = r.raw(e0);
+        if (r.m) En::blank(q, row_keep<TYPE>(r, e0));
+        En::values(q, o.v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < En::E; ++i) {
+            const int64_t e = e0 + i;
+            o.v[i] = absent<TYPE>();
+            if (e >= 0 && e < r.cols) o.v[i] = r.value(e);
+        }
+    }
+    return o;
+}
 
 // ---- groups -----------------------------------------------------------------
 //
@@ -349,7 +446,7 @@ struct Teacher {
                                          const Row<TYPE> &r, int64_t row) {
         bad = false;
         float top = -__builtin_huge_valf();
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kPer; ++i) {
             const int j = g.t + i * G;
             id[i] = -1;
@@ -360,7 +457,7 @@ struct Teacher {
                 if (x < -1 || x >= r.cols) {
                     bad = true;
                     flag_bad_id(rows, row);
-                } else if (x >= 0 && r.keep(x)) {
+                } else if (x >= 0 && r.kept(x)) {
                     float l;
                     if (a.type == TN_TYPE_F32) l = static_cast<const float *>(a.logits)[at];
                     else if (a.type == TN_TYPE_BF16)
@@ -377,14 +474,18 @@ struct Teacher {
         }
         top = g.max(top);
         float total = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) total += id[i] >= 0 ? expf(q[i] - top) : 0.f;
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i) {
+            logq[i] = q[i] - top;
+            q[i] = id[i] >= 0 ? expf(logq[i]) : 0.f;
+            total += q[i];
+        }
         total = g.sum(total);
         const float logt = logf(total);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kPer; ++i) {
-            logq[i] = id[i] >= 0 ? (q[i] - top) - logt : 0.f;
-            q[i] = id[i] >= 0 ? expf(q[i] - top) / total : 0.f;
+            logq[i] = id[i] >= 0 ? logq[i] - logt : 0.f;
+            q[i] = id[i] >= 0 ? q[i] / total : 0.f;
         }
         used = top == -__builtin_huge_valf() ? 0.f : 1.f;
     }

@@ -12,14 +12,22 @@
 namespace tn {
 
 constexpr int kOutVecBytes = 16;        // entries are read 16 bytes at a time
-constexpr int kOutThreads = 256;        // CTA of the kernels below
+constexpr int kOutThreads = 128;        // CTA of the kernels below
+constexpr int kOutCtas = 8;             // that many on an SM (64 registers a thread)
 // Rows of at most this many 16-byte vectors (4 KiB) belong to one warp each:
 // a CTA would have no second vector for its threads.
 constexpr int kOutWarpVecs = 256;
-// Maxima kept per segment for the alternatives: one per vector, or one per 32
-// vectors in segments of more vectors than this.
+// Maxima kept for the alternatives, one per 1, 2, 4, .. or 2^kOutChunkLog
+// vectors (what a warp reads in one step).
 constexpr int kOutKeys = 1024;
-constexpr int64_t kOutSegVecs = 32 * (int64_t)kOutKeys;   // longest segment (512 KiB)
+constexpr int kOutChunkLog = 7;
+constexpr int64_t kOutSegVecs = (int64_t)kOutKeys << 5;   // longest segment (512 KiB)
+
+constexpr int64_t kOutTarget = kOutCtas * 152;   // CTAs that fill the GPU
+
+// A first cut for k alternatives keeps up to this many chunks: a bisection
+// that may stop anywhere between k and here takes a few steps less.
+__host__ __device__ inline int out_most(int k) { return k + k / 4 + 2; }
 
 inline int out_entry_bytes(int32_t type) { return type == TN_TYPE_C64 ? 8 : type == TN_TYPE_F32 ? 4 : 2; }
 
@@ -29,6 +37,7 @@ struct OutSplit {
     int64_t seg_vecs;
     int64_t segs;
     bool warp_rows;     // one warp per row (segs is 1)
+    bool flat;          // split, but short enough for one CTA to hold all chunk maxima
 };
 
 struct OutRows {
@@ -39,6 +48,7 @@ struct OutRows {
     // log p = scale z - log Z.  c2: weights as powers of two, 2^(c2 z) with
     // c2 = scale log2(e), or (amplitudes) 2^(c2 log2 w) with c2 = scale
     float scale, c2;
+    float floor;        // stands for absent logits in the sums, about -2^126 / c2
     int64_t seg_vecs;
     int64_t segs;
     DevStatus *status;
@@ -70,12 +80,15 @@ struct OutForward {
     OutTeacher teacher;
     float *loss;
     // split rows: a ticket per row (zero between calls), a partial and n_top
-    // (key, index) pairs per segment
+    // candidates per segment; flat ones row_chunks maxima a row instead
     uint32_t *tickets;
     OutPartial *partials;
-    uint2 *lists;
-    int32_t key_words;  // shared-memory words per group: vector or chunk maxima
-    int32_t sub_words;  // and vector maxima of selected chunks
+    uint64_t *lists;
+    uint32_t *maxima;
+    int32_t flat, row_chunks;
+    int32_t chunk_log;  // maxima are those of 2^chunk_log vectors
+    // shared memory of a group for the alternatives (see Scratch)
+    int32_t key_words, cand_len, group_bytes;
 };
 
 struct OutGrad {
@@ -98,16 +111,17 @@ struct Outcomes {
     int32_t max_top = 0;
     float scale = 1.f;
     uint64_t ws_bytes = 0;
-    uint64_t ticket_off = 0, ticket_count = 0, partial_off = 0, list_off = 0;
+    uint64_t ticket_off = 0, partial_off = 0, list_off = 0;
     char *ws = nullptr;
     char error[256] = {0};
 };
 
 OutSplit out_split(int32_t type, int64_t cols, int64_t rows);
-cudaError_t launch_outcomes_forward(int32_t type, const OutForward &a, bool warp_rows,
-                                    cudaStream_t stream);
-cudaError_t launch_outcomes_grad(int32_t type, const OutGrad &a, bool warp_rows,
-                                 cudaStream_t stream);
+// Launchers, instantiated by k_outcomes_<type>.cu.
+template <int TYPE>
+cudaError_t outcomes_forward_of(const OutForward &a, bool warp_rows, cudaStream_t stream);
+template <int TYPE>
+cudaError_t outcomes_grad_of(const OutGrad &a, bool warp_rows, cudaStream_t stream);
 
 }  // namespace tn
 

@@ -1,5 +1,6 @@
 // Gradients of the scores and of the loss against a teacher: one pass over
-// the rows, from the saved log Z.
+// the rows, from the saved log Z.  Included by the translation unit of each
+// entry type.
 //
 // Both have the form
 //     dL/dz_v = mult (p_v (alpha + beta (log p_v + H)) + sum_j add_j [id_j = v])
@@ -8,13 +9,15 @@
 // nothing left), beta = 0, add = - q.  A CTA writes the dense part of its
 // segment and then, after a barrier, overwrites the few entries with ids: the
 // first of equal ids adds up all of them in order, so no atomics are needed.
+#pragma once
+
 #include "outcomes.cuh"
 
 namespace tn {
 
 namespace {
 
-constexpr int kU = 4;               // vectors in flight per thread
+constexpr int kGradU = 4;           // vectors in flight per thread
 
 struct RowGrad {
     float mult, alpha, beta, logz, entropy;
@@ -27,14 +30,14 @@ struct RowGrad {
 template <int TYPE>
 __device__ __forceinline__ float entry_grad(const RowGrad &c, float v, float add) {
     if constexpr (Entry<TYPE>::kReal) {
-        const float lp = fmaf(v, c.scale, -c.logz);
+        const float lp = __fadd_rn(__fmul_rn(v, c.scale), -c.logz);
         const float p = ex2(lp * kLog2E);
         return c.mult * fmaf(p, fmaf(c.beta, lp + c.entropy, c.alpha), add);
     } else {
         // 2 / w dL/dz, with p / w taken together
         float lp = 0.f, pw = c.inv_z;
         if (c.beta != 0.f || c.inv_z == 0.f) {
-            lp = fmaf(c.scale, logf(v), -c.logz);
+            lp = __fadd_rn(__fmul_rn(c.scale, logf(v)), -c.logz);
             if (c.inv_z == 0.f) pw = ex2(lp * kLog2E) / v;
         }
         const float dense = pw * fmaf(c.beta, lp + c.entropy, c.alpha);
@@ -152,12 +155,11 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
     const bool wide = os == 1 && r.cs == 1 &&
                       (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(r.p)) % kOutVecBytes == 0;
 
-    for (int b = 0; b < nv; b += kU * G) {
-        uint4 raw[kU];
-        uint32_t bits[kU];
-        bool in[kU];
+    for (int b = 0; b < nv; b += kGradU * G) {
+        uint4 raw[kGradU];
+        bool in[kGradU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
+        for (int u = 0; u < kGradU; ++u) {
             const int j = b + u * G + g.t;
             const int64_t e0 = (v0 + j) * E - r.head;
             in[u] = wide && j < nv && r.inside(e0);
@@ -165,33 +167,22 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
         }
         if constexpr (MASK) {
 #pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (in[u]) bits[u] = r.keep_bits((v0 + b + u * G + g.t) * E - r.head);
+            for (int u = 0; u < kGradU; ++u)
+                if (in[u]) En::blank(raw[u], r.keep((v0 + b + u * G + g.t) * E - r.head));
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
+        for (int u = 0; u < kGradU; ++u) {
             const int j = b + u * G + g.t;
             const int64_t e0 = (v0 + j) * E - r.head;
             if (in[u]) {
                 float v[E];
                 En::values(raw[u], v);
-                if constexpr (MASK) {
-#pragma unroll
-                    for (int i = 0; i < E; ++i)
-                        if (!(bits[u] >> i & 1)) v[i] = absent<TYPE>();
-                }
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
                     const float x = entry_grad<TYPE>(c, v[i], 0.f);
                     v[i] = v[i] == absent<TYPE>() ? 0.f : x;
                 }
-                uint4 o = pack<TYPE>(v, raw[u]);
-                if constexpr (TYPE == TN_TYPE_C64) {
-                    // a masked amplitude may be NaN: its zero is not a product
-                    if (v[0] == 0.f) o.x = o.y = 0;
-                    if (v[1] == 0.f) o.z = o.w = 0;
-                }
-                *reinterpret_cast<uint4 *>(out + e0) = o;
+                *reinterpret_cast<uint4 *>(out + e0) = pack<TYPE>(v, raw[u]);
             } else if (j < nv) {
 #pragma unroll 1
                 for (int i = 0; i < E; ++i) {
@@ -226,7 +217,7 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
 }
 
 template <int TYPE, int G, bool MASK>
-cudaError_t launch(const OutGrad &a, cudaStream_t stream) {
+cudaError_t launch_grad(const OutGrad &a, cudaStream_t stream) {
     const int64_t items = a.r.rows * a.r.segs;
     const int groups = kOutThreads / G;
     const int n = a.teacher.count ? a.teacher.count : a.n_given;
@@ -235,23 +226,14 @@ cudaError_t launch(const OutGrad &a, cudaStream_t stream) {
                       dim3(kOutThreads), smem, stream, a);
 }
 
-template <int TYPE>
-cudaError_t launch_type(const OutGrad &a, bool warp_rows, cudaStream_t stream) {
-    if (warp_rows)
-        return a.r.mask ? launch<TYPE, 32, true>(a, stream) : launch<TYPE, 32, false>(a, stream);
-    return a.r.mask ? launch<TYPE, kOutThreads, true>(a, stream)
-                    : launch<TYPE, kOutThreads, false>(a, stream);
-}
-
 }  // namespace
 
-cudaError_t launch_outcomes_grad(int32_t type, const OutGrad &a, bool warp_rows, cudaStream_t stream) {
-    switch (type) {
-        case TN_TYPE_C64: return launch_type<TN_TYPE_C64>(a, warp_rows, stream);
-        case TN_TYPE_F32: return launch_type<TN_TYPE_F32>(a, warp_rows, stream);
-        case TN_TYPE_BF16: return launch_type<TN_TYPE_BF16>(a, warp_rows, stream);
-        default: return launch_type<TN_TYPE_F16>(a, warp_rows, stream);
-    }
+template <int TYPE>
+cudaError_t outcomes_grad_of(const OutGrad &a, bool warp_rows, cudaStream_t stream) {
+    if (warp_rows)
+        return a.r.mask ? launch_grad<TYPE, 32, true>(a, stream) : launch_grad<TYPE, 32, false>(a, stream);
+    return a.r.mask ? launch_grad<TYPE, kOutThreads, true>(a, stream)
+                    : launch_grad<TYPE, kOutThreads, false>(a, stream);
 }
 
 }  // namespace tn

@@ -181,6 +181,11 @@ class Outcomes:
         self.cols, self.dtype, self.max_rows = int(cols), dtype, int(max_rows)
         self.top, self.scale = int(top), float(scale)
         self._ws = None
+        # the small calls cost what their host side costs: what does not
+        # change from call to call is looked up once
+        self._torch, self._L = torch, _lib()
+        self._r, self._t = tn_rows(), tn_teacher()
+        self._rp, self._tp = ctypes.byref(self._r), ctypes.byref(self._t)
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -205,74 +210,82 @@ class Outcomes:
     # -- arguments --
 
     def _rows(self, rows, mask):
-        import torch
+        """Check the rows and the mask into self._r; (rows, device, R)."""
         if rows.dim() == 1:
             rows = rows.unsqueeze(0)
-        if rows.dim() != 2 or rows.shape[1] != self.cols:
-            raise ValueError(f"rows must be [R, {self.cols}], not {tuple(rows.shape)}")
-        if rows.dtype != self.dtype or not rows.is_cuda:
+        shape = rows.shape
+        if len(shape) != 2 or shape[1] != self.cols:
+            raise ValueError(f"rows must be [R, {self.cols}], not {tuple(shape)}")
+        if rows.dtype is not self.dtype or not rows.is_cuda:
             raise ValueError(f"rows must be {self.dtype} CUDA tensors")
         if rows.is_conj() or rows.is_neg():
             raise ValueError("rows are a lazily conjugated or negated view: resolve it first")
-        R = rows.shape[0]
-        rs, cs = rows.stride()
+        R, device, s = shape[0], rows.device, self._r
+        s.data, s.rows = rows.data_ptr(), R
+        s.row_stride, s.col_stride = rows.stride()
         if mask is None:
-            s = tn_rows(rows.data_ptr(), R, rs, cs, None, 0, 0)
+            s.mask = None
         else:
-            if mask.dtype not in (torch.bool, torch.uint8) or mask.device != rows.device:
+            torch = self._torch
+            if mask.dtype not in (torch.bool, torch.uint8) or mask.device != device:
                 raise ValueError("mask must be a bool or uint8 tensor on the rows' device")
             mask = mask.expand(R, self.cols)
-            s = tn_rows(rows.data_ptr(), R, rs, cs, mask.data_ptr(), *mask.stride())
+            s.mask = mask.data_ptr()
+            s.mask_row_stride, s.mask_col_stride = mask.stride()
         if self._ws is None:
-            self.bind_workspace(rows.device)
-        return rows, mask, s, R
+            self.bind_workspace(device)
+        return rows, device, R
 
     def _on(self, device, stream, inputs):
-        """(stream handle, context to allocate outputs in)."""
-        import contextlib
-        import torch
+        """(stream handle, torch stream to allocate outputs on or None)."""
+        torch = self._torch
         if stream is None:
-            return torch.cuda.current_stream(device).cuda_stream, contextlib.nullcontext()
+            return torch._C._cuda_getCurrentRawStream(device.index), None
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         for t in inputs:
             if t is not None:
                 t.record_stream(stream)
-        return stream.cuda_stream, torch.cuda.stream(stream)
+        return stream.cuda_stream, stream
 
-    @staticmethod
-    def _vec(t, R, name, rows, dtype=None):
-        import torch
-        if (t.dtype != (dtype or torch.float32) or t.device != rows.device or t.numel() != R
-                or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype or torch.float32} tensor of {R} entries "
-                             "on the rows' device")
-        return t
+    def _alloc(self, stream, fn):
+        if stream is None:
+            return fn()
+        with self._torch.cuda.stream(stream):
+            return fn()
 
-    @staticmethod
-    def _ids(ids, R, name, rows):
-        import torch
-        if ids.dtype != torch.int64 or ids.device != rows.device or not ids.is_contiguous():
+    def _vec(self, t, n, name, device, dtype=None):
+        dtype = dtype or self._torch.float32
+        if t.dtype is not dtype or t.device != device or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} entries on the rows' device")
+        return t.data_ptr()
+
+    def _ids(self, ids, R, name, device):
+        if ids.dtype is not self._torch.int64 or ids.device != device or not ids.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int64 tensor on the rows' device")
-        if ids.dim() == 0 or ids.dim() > 2 or ids.shape[0] != R:
-            raise ValueError(f"{name} must be [{R}] or [{R}, n], not {tuple(ids.shape)}")
-        return ids.shape[1] if ids.dim() == 2 else 1
+        shape = ids.shape
+        if not 1 <= len(shape) <= 2 or shape[0] != R:
+            raise ValueError(f"{name} must be [{R}] or [{R}, n], not {tuple(shape)}")
+        return shape[1] if len(shape) == 2 else 1
 
-    def _teacher(self, ids, logits, R, rows, scale):
-        n = self._ids(ids, R, "ids", rows)
+    def _teacher(self, ids, logits, R, device, scale):
+        """Check the teacher into self._t."""
+        n = self._ids(ids, R, "ids", device)
         t = _types().get(logits.dtype, TN_TYPE_C64)
-        if (t == TN_TYPE_C64 or logits.shape != ids.shape or logits.device != rows.device
+        if (t == TN_TYPE_C64 or logits.shape != ids.shape or logits.device != device
                 or not logits.is_contiguous()):
             raise ValueError("the teacher's logits must be a contiguous float32, bfloat16 or float16 "
                              "tensor of the ids' shape on the rows' device")
-        return tn_teacher(ids.data_ptr(), logits.data_ptr(), t, n, scale)
+        s = self._t
+        s.ids, s.logits, s.type, s.count, s.scale = ids.data_ptr(), logits.data_ptr(), t, n, scale
 
-    def _grad(self, rows, R, out):
-        import torch
+    def _grad(self, rows, R, out, device):
         if out is None:
-            return torch.empty((R, self.cols), dtype=self.dtype, device=rows.device)
-        if out.shape != rows.shape or out.dtype != self.dtype or out.device != rows.device:
+            return self._torch.empty((R, self.cols), dtype=self.dtype, device=device)
+        if out.shape != rows.shape or out.dtype is not self.dtype or out.device != device:
             raise ValueError("out must have the rows' shape, type and device")
+        if out.is_conj() or out.is_neg():
+            raise ValueError("out is a lazily conjugated or negated view")
         return out
 
     # -- calls --
@@ -281,101 +294,94 @@ class Outcomes:
         """Log Z, entropy, log probabilities of the ``given`` outcomes ([R] or
         [R, n] int64, -1 = none) and the ``top`` most likely outcomes of every
         row.  ``out``: an earlier result of the same shapes, overwritten."""
-        import torch
-        rows, mask, s, R = self._rows(rows, mask)
-        n, k, dev, f32 = 0, self.top, rows.device, torch.float32
+        rows, dev, R = self._rows(rows, mask)
+        n, k = 0, self.top
         if given is not None:
-            n = self._ids(given, R, "given", rows)
-        sp, ctx = self._on(dev, stream, (rows, mask, given) if stream is not None else ())
+            n = self._ids(given, R, "given", dev)
+        sp, on = self._on(dev, stream, (rows, mask, given) if stream is not None else ())
         if out is None:
-            with ctx:
-                out = Scores(torch.empty(R, dtype=f32, device=dev), torch.empty(R, dtype=f32, device=dev),
-                             None if given is None else torch.empty(given.shape, dtype=f32, device=dev),
-                             torch.empty((R, k), dtype=torch.int64, device=dev) if k else None,
-                             torch.empty((R, k), dtype=f32, device=dev) if k else None)
-        else:
-            self._vec(out.logz, R, "out.logz", rows)
-            self._vec(out.entropy, R, "out.entropy", rows)
-            if given is not None:
-                self._vec(out.logp, R * n, "out.logp", rows)
-            if k:
-                self._vec(out.top_ids, R * k, "out.top_ids", rows, torch.int64)
-                self._vec(out.top_logp, R * k, "out.top_logp", rows)
-        tn_outcomes_score(self.handle, s, given.data_ptr() if n else None, n,
-                          out.logp.data_ptr() if n else None, out.logz.data_ptr(),
-                          out.entropy.data_ptr(), k, out.top_ids.data_ptr() if k else None,
-                          out.top_logp.data_ptr() if k else None, sp)
+            out = self._alloc(on, lambda: self._new_scores(R, k, given, dev))
+        logz, entropy = self._vec(out.logz, R, "out.logz", dev), self._vec(out.entropy, R, "out.entropy", dev)
+        logp = self._vec(out.logp, R * n, "out.logp", dev) if n else None
+        ids = lp = None
+        if k:
+            ids = self._vec(out.top_ids, R * k, "out.top_ids", dev, self._torch.int64)
+            lp = self._vec(out.top_logp, R * k, "out.top_logp", dev)
+        _check(self._L.tn_outcomes_score(self.handle, self._rp, given.data_ptr() if n else None, n, logp,
+                                         logz, entropy, k, ids, lp, sp), self.handle)
         return out
+
+    def _new_scores(self, R, k, given, dev):
+        empty, f32 = self._torch.empty, self._torch.float32
+        return Scores(empty(R, dtype=f32, device=dev), empty(R, dtype=f32, device=dev),
+                      None if given is None else empty(given.shape, dtype=f32, device=dev),
+                      empty((R, k), dtype=self._torch.int64, device=dev) if k else None,
+                      empty((R, k), dtype=f32, device=dev) if k else None)
 
     def score_grad(self, rows, given, logz, entropy, g_logp, g_entropy=None, mask=None, out=None,
                    stream=None):
         """Gradient of the rows from those of ``score``'s logp (``g_logp``, the
         shape of ``given``) and entropy (``g_entropy``, [R] or None).  For
         amplitudes dL/dRe + i dL/dIm, torch's convention."""
-        rows, mask, s, R = self._rows(rows, mask)
-        n = 0
+        rows, dev, R = self._rows(rows, mask)
+        n, ids, gl, h, e = 0, None, None, None, None
         if given is not None:
-            n = self._ids(given, R, "given", rows)
-            self._vec(g_logp, R * n, "g_logp", rows)
-        self._vec(logz, R, "logz", rows)
+            n = self._ids(given, R, "given", dev)
+            gl = self._vec(g_logp, R * n, "g_logp", dev)
+            ids = given.data_ptr()
+        z = self._vec(logz, R, "logz", dev)
         if g_entropy is not None:
-            self._vec(g_entropy, R, "g_entropy", rows)
-            self._vec(entropy, R, "entropy", rows)
-        sp, ctx = self._on(rows.device, stream, (rows, mask, given, logz, entropy, g_logp, g_entropy)
-                           if stream is not None else ())
-        with ctx:
-            g = self._grad(rows, R, out)
-        tn_outcomes_score_grad(self.handle, s, given.data_ptr() if n else None, n, logz.data_ptr(),
-                               entropy.data_ptr() if g_entropy is not None else None,
-                               g_logp.data_ptr() if n else None,
-                               g_entropy.data_ptr() if g_entropy is not None else None,
-                               g.data_ptr(), g.stride(0), g.stride(1), sp)
+            h = self._vec(g_entropy, R, "g_entropy", dev)
+            e = self._vec(entropy, R, "entropy", dev)
+        sp, on = self._on(dev, stream, (rows, mask, given, logz, entropy, g_logp, g_entropy)
+                          if stream is not None else ())
+        g = self._alloc(on, lambda: self._grad(rows, R, out, dev))
+        rs, cs = g.stride()
+        _check(self._L.tn_outcomes_score_grad(self.handle, self._rp, ids, n, z, e, gl, h, g.data_ptr(), rs,
+                                              cs, sp), self.handle)
         return g
+
+    def _new_loss(self, R, dev):
+        empty, f32 = self._torch.empty, self._torch.float32
+        return empty(R, dtype=f32, device=dev), empty(R, dtype=f32, device=dev)
 
     def distill(self, rows, ids, logits, mask=None, teacher_scale: float = 1.0, stream=None) -> Distill:
         """Distance (KL) of every row from the teacher that gives its outcomes
         ``ids`` ([R, K] int64, -1 = none) the logits ``logits``."""
-        import torch
-        rows, mask, s, R = self._rows(rows, mask)
-        t = self._teacher(ids, logits, R, rows, teacher_scale)
-        sp, ctx = self._on(rows.device, stream, (rows, mask, ids, logits) if stream is not None else ())
-        with ctx:
-            loss = torch.empty(R, dtype=torch.float32, device=rows.device)
-            logz = torch.empty(R, dtype=torch.float32, device=rows.device)
-        tn_outcomes_distill(self.handle, s, t, loss.data_ptr(), logz.data_ptr(), sp)
+        rows, dev, R = self._rows(rows, mask)
+        self._teacher(ids, logits, R, dev, teacher_scale)
+        sp, on = self._on(dev, stream, (rows, mask, ids, logits) if stream is not None else ())
+        loss, logz = self._alloc(on, lambda: self._new_loss(R, dev))
+        _check(self._L.tn_outcomes_distill(self.handle, self._rp, self._tp, loss.data_ptr(), logz.data_ptr(),
+                                           sp), self.handle)
         return Distill(loss, logz)
 
     def distill_grad(self, rows, ids, logits, logz, g_loss, mask=None, teacher_scale: float = 1.0,
                      out=None, stream=None):
         """Gradient of the rows from that of ``distill``'s loss ([R])."""
-        rows, mask, s, R = self._rows(rows, mask)
-        t = self._teacher(ids, logits, R, rows, teacher_scale)
-        self._vec(logz, R, "logz", rows)
-        self._vec(g_loss, R, "g_loss", rows)
-        sp, ctx = self._on(rows.device, stream, (rows, mask, ids, logits, logz, g_loss)
-                           if stream is not None else ())
-        with ctx:
-            g = self._grad(rows, R, out)
-        tn_outcomes_distill_grad(self.handle, s, t, logz.data_ptr(), g_loss.data_ptr(), g.data_ptr(),
-                                 g.stride(0), g.stride(1), sp)
+        rows, dev, R = self._rows(rows, mask)
+        self._teacher(ids, logits, R, dev, teacher_scale)
+        z, w = self._vec(logz, R, "logz", dev), self._vec(g_loss, R, "g_loss", dev)
+        sp, on = self._on(dev, stream, (rows, mask, ids, logits, logz, g_loss) if stream is not None else ())
+        g = self._alloc(on, lambda: self._grad(rows, R, out, dev))
+        rs, cs = g.stride()
+        _check(self._L.tn_outcomes_distill_grad(self.handle, self._rp, self._tp, z, w, g.data_ptr(), rs, cs,
+                                                sp), self.handle)
         return g
 
     def distill_step(self, rows, ids, logits, g_loss, mask=None, teacher_scale: float = 1.0, out=None,
                      stream=None) -> Distill:
         """Loss and gradient together, for a loss gradient ``g_loss`` ([R])
         that is known beforehand (1 / R for a mean over the rows)."""
-        import torch
-        rows, mask, s, R = self._rows(rows, mask)
-        t = self._teacher(ids, logits, R, rows, teacher_scale)
-        self._vec(g_loss, R, "g_loss", rows)
-        sp, ctx = self._on(rows.device, stream, (rows, mask, ids, logits, g_loss)
-                           if stream is not None else ())
-        with ctx:
-            loss = torch.empty(R, dtype=torch.float32, device=rows.device)
-            logz = torch.empty(R, dtype=torch.float32, device=rows.device)
-            g = self._grad(rows, R, out)
-        tn_outcomes_distill_step(self.handle, s, t, g_loss.data_ptr(), loss.data_ptr(), logz.data_ptr(),
-                                 g.data_ptr(), g.stride(0), g.stride(1), sp)
+        rows, dev, R = self._rows(rows, mask)
+        self._teacher(ids, logits, R, dev, teacher_scale)
+        w = self._vec(g_loss, R, "g_loss", dev)
+        sp, on = self._on(dev, stream, (rows, mask, ids, logits, g_loss) if stream is not None else ())
+        loss, logz = self._alloc(on, lambda: self._new_loss(R, dev))
+        g = self._alloc(on, lambda: self._grad(rows, R, out, dev))
+        rs, cs = g.stride()
+        _check(self._L.tn_outcomes_distill_step(self.handle, self._rp, self._tp, w, loss.data_ptr(),
+                                                logz.data_ptr(), g.data_ptr(), rs, cs, sp), self.handle)
         return Distill(loss, logz, g)
 
     def check(self) -> None:

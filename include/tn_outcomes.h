@@ -87,7 +87,7 @@ typedef struct tn_outcomes_s tn_outcomes_t;
 /*
  * Make a handle for rows of `cols` entries of `type`, at most `max_rows` rows
  * and `max_top` alternatives (0 .. TN_OUTCOMES_MAX_TOP) per call, at inverse
- * temperature `scale` (finite, > 0).  Host only.  Errors: TN_EINVAL (a value
+ * temperature `scale` (2^-40 .. 2^40).  Host only.  Errors: TN_EINVAL (a value
  * outside its range; see tn_outcomes_last_error(NULL)), TN_EOVERFLOW.
  */
 TN_API tn_status tn_outcomes_create(int32_t type, int64_t cols, int64_t max_rows, int32_t max_top,
