@@ -169,14 +169,17 @@ tn_status forward(Outcomes &o, tn::OutForward &a, const tn::OutSplit &s, cudaStr
     const int64_t E = tn::kOutVecBytes / tn::out_entry_bytes(o.type);
     const int64_t k = a.n_top;
     if (k > 0) {
-        // maxima of as many vectors as leave four times as many of them as
-        // alternatives, so that the cut is well inside; at most kOutKeys
+        // Chunks are as large as leaves four times as many of them as
+        // alternatives (a cut well inside) and at most 1024 vectors to read
+        // again, but no more of them than kOutKeys.
         const int64_t nv = s.flat ? s.vecs : s.seg_vecs;
         int log = s.warp_rows ? 0 : tn::kOutChunkLog;
-        while (log > 0 && nv >> log < 4 * k && nv <= (int64_t)tn::kOutKeys << (log - 1)) --log;
+        while (log > 0 && (nv >> log < 4 * k || (int64_t)tn::out_most((int)k) << log > 1024) &&
+               nv <= (int64_t)tn::kOutKeys << (log - 1))
+            --log;
         a.chunk_log = log;
         int64_t words = (nv >> log) + 1;
-        if (s.segs > 1 && words < s.segs) words = s.segs < tn::kOutKeys ? s.segs : tn::kOutKeys;
+        if (s.segs > 1 && words < s.segs && s.segs <= 2 * tn::kOutKeys) words = s.segs;
         words = (words + 3) / 4 * 4;
         // room for the entries of k vectors or of k octets of list entries;
         // as words, for the maxima of k chunks' vectors and of k lists' octets

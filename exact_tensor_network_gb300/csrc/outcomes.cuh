@@ -27,6 +27,18 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 16 bytes from global to shared memory, asynchronously
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // two fp32 operations in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     uint64_t d;
@@ -237,6 +249,14 @@ struct Row {
     // byte i.  They lie at any offset from the data's vectors: one aligned
     // word, or two and a shift where both are inside the mask's row.
     using Keep = typename std::conditional<En::E == 8, uint64_t, uint32_t>::type;
+    // whether every vector's mask bytes are one aligned word
+    __device__ __forceinline__ bool mask_words() const {
+        return mcs == 1 && (reinterpret_cast<uintptr_t>(m) - head) % En::E == 0;
+    }
+    __device__ __forceinline__ Keep keep_word(int64_t e0) const {
+        if constexpr (En::E == 2) return __ldg(reinterpret_cast<const uint16_t *>(m + e0));
+        else return __ldg(reinterpret_cast<const Keep *>(m + e0));
+    }
     __device__ __forceinline__ Keep keep(int64_t e0) const {
         constexpr int E = En::E;
         if constexpr (E >= 4) {

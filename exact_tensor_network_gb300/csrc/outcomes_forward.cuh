@@ -31,7 +31,7 @@ namespace tn {
 
 namespace {
 
-constexpr int kU = 4;               // vectors in flight per thread
+constexpr int kU = 4;               // vectors of a thread's step
 constexpr float kLag = 8.f;         // of the reference, in powers of two
 constexpr float kFar = 4.253529586511730e37f;   // 2^125
 constexpr float kTiny = 7.888609052210118e-31f; // 2^-100
@@ -253,15 +253,18 @@ __device__ __noinline__ Cut warp_select(const uint32_t *keys, int n, int k, int 
     const int lane = threadIdx.x % 32;
     const uint4 *k4 = reinterpret_cast<const uint4 *>(keys);
     const int n4 = (n + 3) / 4;
-    uint32_t mx = 0, nz = 0;
+    uint32_t mx = 0, nz = 0, mn = 0xffffffffu;     // mn: smallest but 0
 #pragma unroll 1
     for (int i = lane; i < n4; i += 32) {
         const uint4 q = k4[i];
         mx = max(max(mx, q.x), max(max(q.y, q.z), q.w));
+        mn = min(min(mn, q.x - 1), min(min(q.y - 1, q.z - 1), q.w - 1));
         nz += (q.x != 0) + (q.y != 0) + (q.z != 0) + (q.w != 0);
     }
     // each lane has a key of at least the smallest of the lanes' largest
-    const uint32_t low = __reduce_min_sync(0xffffffffu, mx);
+    uint32_t low = __reduce_min_sync(0xffffffffu, mx);
+    mn = __reduce_min_sync(0xffffffffu, mn);
+    if (k > 32 || low == 0) low = mn + 1;
     mx = __reduce_max_sync(0xffffffffu, mx);
     nz = __reduce_add_sync(0xffffffffu, nz);
     const Cut c = bisect([=](uint32_t mid) {
@@ -272,7 +275,7 @@ __device__ __noinline__ Cut warp_select(const uint32_t *keys, int n, int k, int 
             m += (q.x >= mid) + (q.y >= mid) + (q.z >= mid) + (q.w >= mid);
         }
         return __reduce_add_sync(0xffffffffu, m);
-    }, k <= 32 && low ? low : 1u, mx, nz, k, most);
+    }, low, mx, nz, k, most);
     uint32_t at = 0, tied = 0;
     const uint32_t before = (1u << lane) - 1;
 #pragma unroll 1
@@ -421,7 +424,7 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 // The k best entries of `nv` vectors from v0 on into sm.best, as candidates
 // with indices (vector - v0) E + entry, from the maxima in sm.keys, each that
 // of 2^log vectors.  Returns their number.
-template <int TYPE, int G>
+template <int TYPE, bool MASK, int G>
 __device__ __noinline__ int best_entries(Group<G> g, const Scratch sm, const Row<TYPE> r, int64_t v0,
                                          int nv, int k, int log, int cand_len) {
     using En = Entry<TYPE>;
@@ -434,32 +437,40 @@ __device__ __noinline__ int best_entries(Group<G> g, const Scratch sm, const Row
     const float bar = fmaxf(key_value(least), En::kReal ? -3.402823466e38f : 1.401298464e-45f);
     uint32_t *list = reinterpret_cast<uint32_t *>(sm.cand + cand_len / 2);   // cand_len positions
     const int work = nc << log;
+    const bool words = MASK && r.mask_words();
 #pragma unroll 1
     for (int b = g.t; b < work; b += kU * G) {
         int j[kU];
         uint4 q[kU];
-        bool in[kU];
+        uint32_t odd = 0;       // vectors to be read entry by entry
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int i = b + u * G;
             j[u] = i < work ? ((int)sm.pos[i >> log] << log) + (i & low) : nv;
             const int64_t e0 = (v0 + j[u]) * E - r.head;
-            in[u] = j[u] < nv && r.inside(e0) && !r.m;
+            const bool in = j[u] < nv && r.inside(e0) && (!MASK || words);
             q[u] = En::absent_vector();
-            if (in[u]) q[u] = r.raw(e0);
+            if (in) q[u] = r.raw(e0);
+            if (MASK && in) En::blank(q[u], r.keep_word(e0));
+            if (!in && j[u] < nv) odd |= 1u << u;
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            float lm = vector_max<TYPE>(q[u]);
-            if (!in[u] && j[u] < nv) {
-                const auto x = row_vector<TYPE>(r, v0 + j[u]);
-                lm = absent<TYPE>();
-#pragma unroll
-                for (int e = 0; e < E; ++e) lm = fmaxf(lm, x.v[e]);
-            }
-            if (lm >= bar) {
+        for (int u = 0; u < kU; ++u)
+            if (vector_max<TYPE>(q[u]) >= bar) {
                 const uint32_t at = atomicAdd(sm.n + 3, 1u);
                 if (at < (uint32_t)cand_len) list[at] = j[u];
+            }
+#pragma unroll 1
+        for (; odd; odd &= odd - 1) {
+            const int i = b + (__ffs(odd) - 1) * G;
+            const int jj = ((int)sm.pos[i >> log] << log) + (i & low);
+            const auto x = row_vector<TYPE>(r, v0 + jj);
+            float lm = absent<TYPE>();
+#pragma unroll
+            for (int e = 0; e < E; ++e) lm = fmaxf(lm, x.v[e]);
+            if (lm >= bar) {
+                const uint32_t at = atomicAdd(sm.n + 3, 1u);
+                if (at < (uint32_t)cand_len) list[at] = jj;
             }
         }
     }
@@ -544,10 +555,12 @@ __device__ __noinline__ int join_lists(Group<G> g, const Scratch sm, const OutFo
         g.sync();
     }
 #pragma unroll 1
-    for (int i = g.t; i < nc * 32; i += G)
-        for (int e = i & 31; e < k; e += 32) {
-            const uint32_t at = sm.pos[i >> 5] * k + e, key = key_at(at);
-            if (key >= least) sm.offer(key, at, a.cand_len);
+    for (int i = g.t; i < nc * 4; i += G)      // sorted: few go past their first entries
+#pragma unroll 1
+        for (int e = i & 3; e < k; e += 4) {
+            const uint32_t at = sm.pos[i >> 2] * k + e, key = key_at(at);
+            if (key < least) break;
+            sm.offer(key, at, a.cand_len);
         }
     g.sync();
     int n = (int)sm.n[0];
@@ -678,83 +691,96 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     const int hi = max(lo, (int)max((int64_t)0, min((int64_t)nv, in1 - v0)));
     const uint4 *vecs = r.vectors() + v0;
 
-    // a warp's step is kU * 32 consecutive vectors, a chunk of them at most
-    const int first = g.warp * (kU * 32) + g.lane;
+    // A warp takes kU * 32 consecutive vectors a step (a chunk of them at most).
+    constexpr int kStep = kU * 32;
+    const bool words = MASK && r.mask_words();
+    using Keep = typename Row<TYPE>::Keep;
     Stream<TYPE, ENT, UNIT> st;
-    for (int b = 0; b < nv; b += kU * G) {
-        uint4 raw[kU];
-        const int j0 = b + first;
-        uint32_t later = 0;         // vectors that the straight way cannot do
-        if (b >= lo && b + kU * G <= hi) {
+
+    // the largest of each of the step's kU rows of 32 vectors, into the maxima
+    const auto put_maxima = [&](int b, float (&lm)[kU]) {
+        if (G > 32 && log >= 5) {
+            const int rows = (1 << log) >> 5;     // of 32 vectors in a chunk: 1, 2 or 4
 #pragma unroll
-            for (int u = 0; u < kU; ++u) raw[u] = __ldg(vecs + j0 + u * 32);
-            if constexpr (MASK) {
-                typename Row<TYPE>::Keep keep[kU];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) keep[u] = r.keep((v0 + j0 + u * 32) * E - r.head);
-#pragma unroll
-                for (int u = 0; u < kU; ++u) En::blank(raw[u], keep[u]);
+            for (int u = 0; u < kU; ++u) {
+                if (u & (rows - 1)) lm[u] = fmaxf(lm[u], lm[u - 1]);
+                if (((u + 1) & (rows - 1)) == 0) {
+                    const uint32_t x = __reduce_max_sync(0xffffffffu, order_key<TYPE>(lm[u]));
+                    const int at = (b + u * 32) >> log;
+                    if (g.lane == 0 && at << log < nv) sm.keys[at] = x;
+                }
             }
         } else {
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                const int j = j0 + u * 32;
+                const int j = b + u * 32 + g.lane;
+                uint32_t x = order_key<TYPE>(lm[u]);
+#pragma unroll 1
+                for (int o = 1; o < 1 << log; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+                if ((g.lane & ((1 << log) - 1)) == 0 && j < nv) sm.keys[j >> log] = x;
+            }
+        }
+    };
+    // a whole step inside the row
+    const auto whole = [&](int b) { return b >= lo && b + kStep <= hi; };
+#pragma unroll 1
+    for (int b = g.warp * kStep; b < nv; b += kU * G) {
+        float lm[kU];
+        uint32_t later = 0;         // vectors that the straight way cannot do
+        uint4 raw[kU];
+        if (whole(b)) {
+            if (MASK) {
+                Keep keep[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int64_t e0 = (v0 + b + u * 32 + g.lane) * E - r.head;
+                    keep[u] = words ? r.keep_word(e0) : row_keep<TYPE>(r, e0);
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    raw[u] = __ldg(vecs + b + u * 32 + g.lane);
+                    En::blank(raw[u], keep[u]);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    raw[u] = __ldg(vecs + b + u * 32 + g.lane);
+            }
+        } else {
+            // the row's first or last vectors, or a strided row
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int j = b + u * 32 + g.lane;
                 raw[u] = En::absent_vector();
-                if (j >= lo && j < hi) {
+                if (j >= lo && j < hi && (!MASK || words)) {
                     raw[u] = __ldg(vecs + j);
-                    if constexpr (MASK) En::blank(raw[u], row_keep<TYPE>(r, (v0 + j) * E - r.head));
+                    if (MASK) En::blank(raw[u], r.keep_word((v0 + j) * E - r.head));
                 } else if (j < nv) {
                     later |= 1u << u;
                 }
             }
         }
-        uint32_t key[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             float v[E];
-            const float lm = decode<TYPE>(raw[u], v, a.r.floor);
-            if (!st.add(v, lm, a.r.c2)) later |= 1u << u;
-            key[u] = __float_as_uint(lm);
+            lm[u] = decode<TYPE>(raw[u], v, a.r.floor);
+            if (!st.add(v, lm[u], a.r.c2)) later |= 1u << u;
         }
-        if (ENT && k > 0) {
-            const int c0 = j0 - g.lane;      // the warp's first vector
-            if (G > 32 && log >= 5) {
-                const int rows = (1 << (log & 7)) >> 5;     // of 32 vectors in a chunk: 1, 2 or 4
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    if (u & (rows - 1)) key[u] = __float_as_uint(fmaxf(__uint_as_float(key[u]), __uint_as_float(key[u - 1])));
-                    if (((u + 1) & (rows - 1)) == 0) {
-                        const uint32_t x = __reduce_max_sync(0xffffffffu, order_key<TYPE>(__uint_as_float(key[u])));
-                        const int at = (c0 + u * 32) >> log;
-                        if (g.lane == 0 && at << log < nv) sm.keys[at] = x;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int j = j0 + u * 32;
-                    uint32_t x = order_key<TYPE>(__uint_as_float(key[u]));
-#pragma unroll 1
-                    for (int o = 1; o < 1 << log; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-                    if ((g.lane & ((1 << log) - 1)) == 0 && j < nv) sm.keys[j >> log] = x;
-                }
-            }
-        }
-        // a row's first and last vector, strided rows, logits far out
+        if (ENT && k > 0) put_maxima(b, lm);
         if (__any_sync(0xffffffffu, later)) {
             __syncwarp();
 #pragma unroll 1
             while (later) {
                 const int u = __ffs(later) - 1;
                 later &= later - 1;
-                const int j = j0 + u * 32;
+                const int j = b + u * 32 + g.lane;
                 const auto x = row_vector<TYPE>(r, v0 + j);
                 float v[E];
 #pragma unroll
                 for (int i = 0; i < E; ++i) v[i] = x.v[i];
-                const float lm = largest<TYPE>(v, a.r.floor);
-                if (!st.add(v, lm, a.r.c2)) st.far(x.v, lm, a.r.c2);
-                if (k > 0) atomicMax(sm.keys + (j >> log), order_key<TYPE>(lm));
+                const float m = largest<TYPE>(v, a.r.floor);
+                if (!st.add(v, m, a.r.c2)) st.far(x.v, m, a.r.c2);
+                if (ENT && k > 0) atomicMax(sm.keys + (j >> log), order_key<TYPE>(m));
             }
             __syncwarp();
         }
@@ -772,7 +798,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         // leave the segment's part in the workspace; the last one joins
         const int64_t slot0 = row * a.r.segs;
         if (k > 0 && lists) {
-            if (valid) found = best_entries<TYPE>(g, sm, r, v0, nv, k, log, a.cand_len);
+            if (valid) found = best_entries<TYPE, MASK>(g, sm, r, v0, nv, k, log, a.cand_len);
             for (int i = g.t; i < k; i += G) a.lists[(slot0 + seg) * k + i] = i < found ? sm.best[i] : 0;
         } else if (k > 0) {
             uint32_t *to = a.maxima + row * a.row_chunks + (v0 >> log);
@@ -846,7 +872,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         }
     } else if (valid) {
         if (lists) found = join_lists(g, sm, a, row);
-        else found = best_entries<TYPE>(g, sm, r, 0, (int)all, k, log, a.cand_len);
+        else found = best_entries<TYPE, MASK>(g, sm, r, 0, (int)all, k, log, a.cand_len);
         for (int i = g.t; i < found; i += G) {
             const uint64_t x = sm.best[i];
             const uint32_t at = 0xffffffffu - (uint32_t)x;

@@ -299,16 +299,30 @@ class Outcomes:
         if given is not None:
             n = self._ids(given, R, "given", dev)
         sp, on = self._on(dev, stream, (rows, mask, given) if stream is not None else ())
+        logp = ids = lp = None
         if out is None:
-            out = self._alloc(on, lambda: self._new_scores(R, k, given, dev))
-        logz, entropy = self._vec(out.logz, R, "out.logz", dev), self._vec(out.entropy, R, "out.entropy", dev)
-        logp = self._vec(out.logp, R * n, "out.logp", dev) if n else None
-        ids = lp = None
-        if k:
-            ids = self._vec(out.top_ids, R * k, "out.top_ids", dev, self._torch.int64)
-            lp = self._vec(out.top_logp, R * k, "out.top_logp", dev)
-        _check(self._L.tn_outcomes_score(self.handle, self._rp, given.data_ptr() if n else None, n, logp,
-                                         logz, entropy, k, ids, lp, sp), self.handle)
+            if on is None:
+                out = self._new_scores(R, k, given, dev)
+            else:
+                with self._torch.cuda.stream(on):
+                    out = self._new_scores(R, k, given, dev)
+            logz, entropy = out[0].data_ptr(), out[1].data_ptr()
+            if n:
+                logp = out[2].data_ptr()
+            if k:
+                ids, lp = out[3].data_ptr(), out[4].data_ptr()
+        else:
+            logz = self._vec(out.logz, R, "out.logz", dev)
+            entropy = self._vec(out.entropy, R, "out.entropy", dev)
+            if n:
+                logp = self._vec(out.logp, R * n, "out.logp", dev)
+            if k:
+                ids = self._vec(out.top_ids, R * k, "out.top_ids", dev, self._torch.int64)
+                lp = self._vec(out.top_logp, R * k, "out.top_logp", dev)
+        st = self._L.tn_outcomes_score(self.handle, self._rp, given.data_ptr() if n else None, n, logp,
+                                       logz, entropy, k, ids, lp, sp)
+        if st:
+            _check(st, self.handle)
         return out
 
     def _new_scores(self, R, k, given, dev):
