@@ -1,10 +1,10 @@
 // The outcome operators' kernels for f32 logits.
-#include "outcomes_forward.cuh"
-#include "outcomes_grad.cuh"
+#include "outcomes_step.cuh"
 
 namespace tn {
 
 template cudaError_t outcomes_forward_of<TN_TYPE_F32>(const OutForward &, bool, cudaStream_t);
 template cudaError_t outcomes_grad_of<TN_TYPE_F32>(const OutGrad &, bool, cudaStream_t);
+template cudaError_t outcomes_step_of<TN_TYPE_F32>(const OutStep &, bool, cudaStream_t);
 
 }  // namespace tn

@@ -46,6 +46,8 @@ using tn::Outcomes;
 
 thread_local char g_error[256] = {0};
 
+constexpr int64_t kStepBatch = 48 << 20;   // bytes of rows between a forward pass and its gradient
+
 tn_status fail(char (&buf)[256], tn_status st, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -210,6 +212,46 @@ tn_status gradient(Outcomes &o, const tn::OutGrad &a, const tn::OutSplit &s, cud
                                   tn::outcomes_grad_of<TN_TYPE_BF16>, tn::outcomes_grad_of<TN_TYPE_F16>, a,
                                   s.warp_rows, stream);
     return e == cudaSuccess ? TN_OK : cuda_fail(o, e, "launching the gradient");
+}
+
+// CTAs of a cluster that hold a row in shared memory; segs 0: too long.
+tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows) {
+    tn::OutSplit s = tn::out_split(type, cols, rows);
+    if (s.warp_rows) return s;
+    const int64_t bytes = s.vecs * tn::kOutVecBytes;
+    int64_t c = 1;
+    while (c < tn::kStepCluster && bytes > c * tn::kStepSlice) c *= 2;
+    // few rows: more CTAs a row, of two vectors a thread at least
+    while (c < tn::kStepCluster && rows * c < 2 * 152 && s.vecs >= 4 * c * tn::kStepThreads) c *= 2;
+    s.flat = false;
+    s.segs = c;
+    s.seg_vecs = (s.vecs + c - 1) / c;
+    if (s.seg_vecs * tn::kOutVecBytes > tn::kStepSliceMost) s.segs = 0;
+    return s;
+}
+
+// Rows that no cluster holds: the forward pass and the gradient, some rows at
+// a time, so that the second finds them in the L2 cache.
+tn_status step_in_two(tn_outcomes_t *h, const tn_rows *rows, const tn_teacher *teacher, const float *g_loss,
+                      float *loss, float *logz, void *grad, int64_t rs, int64_t cs, tn_stream_t stream) {
+    const int64_t size = tn::out_entry_bytes(h->o.type), row_bytes = h->o.cols * size;
+    const int64_t batch = row_bytes >= kStepBatch ? 1 : kStepBatch / row_bytes;
+    for (int64_t i = 0; i < rows->rows; i += batch) {
+        tn_rows r = *rows;
+        tn_teacher t = *teacher;
+        r.rows = rows->rows - i < batch ? rows->rows - i : batch;
+        r.data = static_cast<const char *>(rows->data) + i * rows->row_stride * size;
+        if (rows->mask) r.mask = rows->mask + i * rows->mask_row_stride;
+        t.ids = teacher->ids + i * teacher->count;
+        t.logits = static_cast<const char *>(teacher->logits) +
+                   i * teacher->count * tn::out_entry_bytes(teacher->type);
+        tn_status st = tn_outcomes_distill(h, &r, &t, loss + i, logz + i, stream);
+        if (st == TN_OK)
+            st = tn_outcomes_distill_grad(h, &r, &t, logz + i, g_loss + i,
+                                          static_cast<char *>(grad) + i * rs * size, rs, cs, stream);
+        if (st != TN_OK) return st;
+    }
+    return TN_OK;
 }
 
 }  // namespace
@@ -380,10 +422,28 @@ tn_status tn_outcomes_distill_step(tn_outcomes_t *h, const tn_rows *rows, const 
         const tn_status st = check_grad(h->o, rows, grad, grad_row_stride, grad_col_stride);
         if (st != TN_OK) return st;
     }
-    const tn_status st = tn_outcomes_distill(h, rows, teacher, loss, logz, stream);
+    Outcomes &o = h->o;
+    tn_status st = common(o, rows);
+    if (st == TN_OK) st = check_teacher(o, rows, teacher);
     if (st != TN_OK) return st;
-    return tn_outcomes_distill_grad(h, rows, teacher, logz, g_loss, grad, grad_row_stride,
-                                    grad_col_stride, stream);
+    if (rows->rows == 0) return TN_OK;
+    if (!loss || !logz) return fail(o.error, TN_EINVAL, "loss and logz are required");
+    const tn::OutSplit s = step_split(o.type, o.cols, rows->rows);
+    if (s.segs == 0) return step_in_two(h, rows, teacher, g_loss, loss, logz, grad, grad_row_stride,
+                                        grad_col_stride, stream);
+    tn::OutStep a = {};
+    a.r = rows_of(o, rows, s);
+    a.teacher = teacher_of(teacher);
+    a.g_loss = g_loss;
+    a.loss = loss;
+    a.logz = logz;
+    a.grad = static_cast<char *>(grad);
+    a.grad_row_stride = grad_row_stride;
+    a.grad_col_stride = o.cols == 1 ? 1 : grad_col_stride;
+    const cudaError_t e = by_type(o.type, tn::outcomes_step_of<TN_TYPE_C64>, tn::outcomes_step_of<TN_TYPE_F32>,
+                                  tn::outcomes_step_of<TN_TYPE_BF16>, tn::outcomes_step_of<TN_TYPE_F16>, a,
+                                  s.warp_rows, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TN_OK : cuda_fail(o, e, "launching the training step");
 }
 
 tn_status tn_outcomes_check(tn_outcomes_t *h) {

@@ -451,63 +451,66 @@ __device__ __forceinline__ void flag_bad_id(const OutRows &a, int64_t row) {
         a.status->where = static_cast<int32_t>(row);
 }
 
-// A row's teacher over the group: this thread's outcomes t, t + G, ...; id -1
-// where left out.  q = exp(logit - max) / total.
-template <int G>
+// A row's teacher in shared memory: ids (-1 where left out), probabilities,
+// their logarithms and, where the loss is wanted, the row's order values
+// there.  The group reads it (its loads in flight together) with read(); after
+// a barrier one warp normalises it.
 struct Teacher {
-    static constexpr int kPer = TN_OUTCOMES_MAX_IDS / G;
-    int64_t id[kPer];
-    float q[kPer], logq[kPer];
+    int64_t id[TN_OUTCOMES_MAX_IDS];
+    float q[TN_OUTCOMES_MAX_IDS], logq[TN_OUTCOMES_MAX_IDS], value[TN_OUTCOMES_MAX_IDS];
     float used;    // 1 if anything is left, else 0
-    bool bad;      // an id out of range (this thread's)
 
-    template <int TYPE>
-    __device__ __forceinline__ void load(Group<G> &g, const OutTeacher &a, const OutRows &rows,
-                                         const Row<TYPE> &r, int64_t row) {
-        bad = false;
-        float top = -__builtin_huge_valf();
-#pragma unroll 1
+    template <int TYPE, int G>
+    __device__ __forceinline__ void read(const Group<G> &g, const OutTeacher &a, const OutRows &rows,
+                                         const Row<TYPE> &r, int64_t row, bool values) {
+        constexpr int kPer = TN_OUTCOMES_MAX_IDS / G;
+#pragma unroll (kPer < 4 ? kPer : 4)
         for (int i = 0; i < kPer; ++i) {
             const int j = g.t + i * G;
-            id[i] = -1;
-            q[i] = -__builtin_huge_valf();
-            if (j < a.count) {
-                const int64_t at = row * a.count + j;
-                const int64_t x = a.ids[at];
-                if (x < -1 || x >= r.cols) {
-                    bad = true;
-                    flag_bad_id(rows, row);
-                } else if (x >= 0 && r.kept(x)) {
-                    float l;
-                    if (a.type == TN_TYPE_F32) l = static_cast<const float *>(a.logits)[at];
-                    else if (a.type == TN_TYPE_BF16)
-                        l = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[at]);
-                    else l = __half2float(static_cast<const __half *>(a.logits)[at]);
-                    l *= a.scale;
-                    if (l != -__builtin_huge_valf()) {
-                        id[i] = x;
-                        q[i] = l;
-                    }
-                }
-            }
-            top = max_nan(top, q[i]);
+            if (j >= a.count) break;
+            const int64_t at = row * a.count + j;
+            const int64_t x = a.ids[at];
+            float l;
+            if (a.type == TN_TYPE_F32) l = static_cast<const float *>(a.logits)[at];
+            else if (a.type == TN_TYPE_BF16) l = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[at]);
+            else l = __half2float(static_cast<const __half *>(a.logits)[at]);
+            l *= a.scale;
+            const bool in = x >= 0 && x < r.cols;
+            float v = absent<TYPE>();
+            if (in && values) v = Entry<TYPE>::value(r.p[x * r.cs]);
+            const bool kept = in && r.kept(x) && l != -__builtin_huge_valf();
+            if (!in && x != -1) flag_bad_id(rows, row);
+            // -2: an id out of range
+            id[j] = kept ? x : (!in && x != -1 ? -2 : -1);
+            logq[j] = kept ? l : -__builtin_huge_valf();
+            value[j] = v;
         }
-        top = g.max(top);
-        float total = 0.f;
+    }
+    // one warp
+    __device__ __forceinline__ void normalise(int count) {
+        const int lane = threadIdx.x % 32;
+        float top = -__builtin_huge_valf(), total = 0.f;
 #pragma unroll 1
-        for (int i = 0; i < kPer; ++i) {
-            logq[i] = q[i] - top;
-            q[i] = id[i] >= 0 ? expf(logq[i]) : 0.f;
-            total += q[i];
+        for (int j = lane; j < count; j += 32) top = max_nan(top, logq[j]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll 1
+        for (int j = lane; j < count; j += 32) {
+            const float l = logq[j] - top, e = id[j] >= 0 ? expf(l) : 0.f;
+            logq[j] = l;
+            q[j] = e;
+            total += e;
         }
-        total = g.sum(total);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         const float logt = logf(total);
 #pragma unroll 1
-        for (int i = 0; i < kPer; ++i) {
-            logq[i] = id[i] >= 0 ? logq[i] - logt : 0.f;
-            q[i] = id[i] >= 0 ? q[i] / total : 0.f;
+        for (int j = lane; j < count; j += 32) {
+            logq[j] -= logt;
+            q[j] = id[j] >= 0 ? q[j] / total : 0.f;
         }
-        used = top == -__builtin_huge_valf() ? 0.f : 1.f;
+        if (lane == 0) used = top == -__builtin_huge_valf() ? 0.f : 1.f;
+        __syncwarp();
     }
 };
 

@@ -105,6 +105,22 @@ struct OutGrad {
     int64_t grad_row_stride, grad_col_stride;
 };
 
+// Loss and gradient in one kernel: r.segs CTAs of a cluster hold a row,
+// r.seg_vecs vectors each.
+struct OutStep {
+    OutRows r;
+    OutTeacher teacher;
+    const float *g_loss;
+    float *loss, *logz;
+    char *grad;
+    int64_t grad_row_stride, grad_col_stride;
+};
+
+constexpr int kStepThreads = 256;
+constexpr int64_t kStepSlice = 68 * 1024;      // three CTAs on an SM
+constexpr int64_t kStepSliceMost = 216 * 1024; // one
+constexpr int kStepCluster = 8;
+
 struct Outcomes {
     int32_t type = 0;
     int64_t cols = 0, max_rows = 0;
@@ -122,6 +138,8 @@ template <int TYPE>
 cudaError_t outcomes_forward_of(const OutForward &a, bool warp_rows, cudaStream_t stream);
 template <int TYPE>
 cudaError_t outcomes_grad_of(const OutGrad &a, bool warp_rows, cudaStream_t stream);
+template <int TYPE>
+cudaError_t outcomes_step_of(const OutStep &a, bool warp_rows, cudaStream_t stream);
 
 }  // namespace tn
 

@@ -600,9 +600,30 @@ __device__ __forceinline__ float log_prob(const OutRows &r, float v, float logz)
     return __fadd_rn(__fmul_rn(r.scale, Entry<TYPE>::kReal ? v : logf(v)), -logz);
 }
 
+// The loss of a row by one warp.
+template <int TYPE>
+__device__ __forceinline__ float teacher_loss(int count, const OutRows &r, const Teacher &te, float logz) {
+    constexpr float kInf = __builtin_huge_valf();
+    float loss = 0.f, bad = 0.f;
+#pragma unroll 1
+    for (int j = threadIdx.x % 32; j < count; j += 32) {
+        if (te.id[j] == -2) bad = __int_as_float(0x7fffffff);
+        if (te.id[j] >= 0 && te.q[j] != 0.f) {
+            const float v = te.value[j];
+            const float lp = v == absent<TYPE>() ? -kInf : log_prob<TYPE>(r, v, logz);
+            loss += te.q[j] * (te.logq[j] - lp);
+        }
+    }
+    if (logz == -kInf) loss = 0.f;
+    loss += bad;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+    return loss;
+}
+
 template <int TYPE, bool ENT, int G>
 __device__ __forceinline__ void finish_row(Group<G> &g, const OutForward &a, const Row<TYPE> &r,
-                                           int64_t row, float logz, float entropy) {
+                                           Teacher *te, int64_t row, float logz, float entropy) {
     constexpr float kInf = __builtin_huge_valf();
     if (g.t == 0) a.logz[row] = logz;
     if constexpr (ENT) {
@@ -623,20 +644,11 @@ __device__ __forceinline__ void finish_row(Group<G> &g, const OutForward &a, con
             a.logp[row * a.n_given + j] = lp;
         }
     } else {
-        Teacher<G> te;
-        te.load(g, a.teacher, a.r, r, row);
-        float loss = 0.f;
-#pragma unroll 1
-        for (int i = 0; i < Teacher<G>::kPer; ++i)
-            if (te.id[i] >= 0 && te.q[i] != 0.f) {
-                const float v = row_value<TYPE>(r, te.id[i]);
-                const float lp = v == absent<TYPE>() ? -kInf : log_prob<TYPE>(a.r, v, logz);
-                loss += te.q[i] * (te.logq[i] - lp);
-            }
-        if (logz == -kInf) loss = 0.f;
-        if (te.bad) loss = __int_as_float(0x7fffffff);
-        loss = g.sum(loss);
-        if (g.t == 0) a.loss[row] = loss;
+        if (g.warp == 0) {
+            te->normalise(a.teacher.count);
+            const float loss = teacher_loss<TYPE>(a.teacher.count, a.r, *te, logz);
+            if (g.t == 0) a.loss[row] = loss;
+        }
     }
 }
 
@@ -668,11 +680,13 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint32_t red[4 * kOutThreads / 32];
     __shared__ bool last;
+    __shared__ Teacher teachers[ENT ? 1 : kGroups];
+    Teacher *te = teachers + (ENT ? 0 : threadIdx.x / G);
     pdl_trigger();
     Group<G> g(red);
-    const int64_t item = (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
-    const int64_t row = G == 32 ? item : item / a.r.segs;
-    const int64_t seg = G == 32 ? 0 : item - row * a.r.segs;
+    const uint32_t item = blockIdx.x * kGroups + threadIdx.x / G, segs = (uint32_t)a.r.segs;
+    const int64_t row = G == 32 ? item : item / segs;
+    const int64_t seg = G == 32 ? 0 : item % segs;
     const Scratch sm(smem + (size_t)(threadIdx.x / G) * a.group_bytes, a);
     pdl_wait();
     if (G == 32 && row >= a.r.rows) return;
@@ -696,6 +710,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     const bool words = MASK && r.mask_words();
     using Keep = typename Row<TYPE>::Keep;
     Stream<TYPE, ENT, UNIT> st;
+    if (!ENT) te->read(g, a.teacher, a.r, r, row, true);
 
     // the largest of each of the step's kU rows of 32 vectors, into the maxima
     const auto put_maxima = [&](int b, float (&lm)[kU]) {
@@ -819,12 +834,11 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         if (!last) return;
         __threadfence();
         if (g.t == 0) a.tickets[row] = 0;    // ready for the next call
-        const int segs = static_cast<int>(a.r.segs);
         if (k > 0 && !lists)
             for (int i = g.t; i < (int)((all + (1 << log) - 1) >> log); i += G)
                 sm.keys[i] = __ldcg(a.maxima + row * a.row_chunks + i);
         sum = Sums<TYPE>();
-        for (int i = g.t; i < segs; i += G) {
+        for (int i = g.t; i < (int)segs; i += G) {
             const float4 f = __ldcg(reinterpret_cast<const float4 *>(a.partials + slot0 + i));
             Sums<TYPE> o;
             o.z0 = f.x;
@@ -841,7 +855,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         valid = sum.s < kInf;
     }
     normaliser<TYPE>(a.r, sum, logz, entropy);
-    finish_row<TYPE, ENT>(g, a, r, row, logz, entropy);
+    finish_row<TYPE, ENT>(g, a, r, te, row, logz, entropy);
     if constexpr (!ENT) return;
     if (k == 0) return;
     int64_t *ids = a.top_ids + row * k;

@@ -17,13 +17,20 @@ namespace tn {
 
 namespace {
 
-constexpr int kGradU = 4;           // vectors in flight per thread
+constexpr int kGradU = 4;           // vectors of a thread's step
 
 struct RowGrad {
     float mult, alpha, beta, logz, entropy;
     float inv_z;      // amplitudes at scale 1: p = w inv_z (0: not used)
     float scale;
+    bool plain;       // log Z is a number: no entry needs a second look
 };
+
+template <int TYPE>
+__device__ __forceinline__ void finish_row_grad(RowGrad &c) {
+    c.plain = fabsf(c.logz) < __builtin_huge_valf();
+    c.inv_z = !Entry<TYPE>::kReal && c.scale == 1.f && fabsf(c.logz) < 80.f ? expf(-c.logz) : 0.f;
+}
 
 // What multiplies the entry (an amplitude) or is the gradient itself (a real
 // logit).  v: order value of a present entry.
@@ -82,23 +89,183 @@ __device__ __forceinline__ uint4 pack(const float (&g)[Entry<TYPE>::E], const ui
     return o;
 }
 
+// The dense part of a vector of a row with a plain log Z (absent entries, at
+// -inf or 0, come out as 0: their p is 0 and its factor finite).
+template <int TYPE, bool BETA>
+__device__ __forceinline__ uint4 dense_grad(const RowGrad &c, const uint4 &raw) {
+    constexpr int E = Entry<TYPE>::E;
+    float v[E];
+    Entry<TYPE>::values(raw, v);
+    if constexpr (Entry<TYPE>::kReal) {
+        const float2 scale = make_float2(c.scale, c.scale), lz = make_float2(-c.logz, -c.logz);
+        const float2 l2 = make_float2(kLog2E, kLog2E);
+        const float ma = c.mult * c.alpha;
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            float2 lp = add2(mul2(make_float2(v[i], v[i + 1]), scale), lz);
+            if constexpr (BETA) lp = make_float2(fmaxf(lp.x, -1e30f), fmaxf(lp.y, -1e30f));
+            const float2 d = mul2(lp, l2);
+            const float2 p = make_float2(ex2(d.x), ex2(d.y));
+            float2 o;
+            if constexpr (BETA) {
+                const float2 h = make_float2(c.entropy, c.entropy), b = make_float2(c.beta, c.beta);
+                const float2 f = fma2(b, add2(lp, h), make_float2(c.alpha, c.alpha));
+                o = mul2(mul2(p, f), make_float2(c.mult, c.mult));
+            } else {
+                o = mul2(p, make_float2(ma, ma));
+            }
+            v[i] = o.x;
+            v[i + 1] = o.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = v[i] == 0.f ? 0.f : entry_grad<TYPE>(c, v[i], 0.f);
+    }
+    return pack<TYPE>(v, raw);
+}
+
+// Where a row's gradient goes.
+template <int TYPE>
+struct Out {
+    using T = typename Entry<TYPE>::T;
+    T *p;
+    int64_t cs;
+    bool wide;     // vectors of the row are vectors of the gradient
+
+    __device__ __forceinline__ Out(char *grad, int64_t row_stride, int64_t col_stride, const Row<TYPE> &r,
+                                   int64_t row)
+        : p(reinterpret_cast<T *>(grad) + row * row_stride), cs(col_stride) {
+        wide = cs == 1 && (reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(r.p)) % kOutVecBytes == 0;
+    }
+    __device__ __forceinline__ void put(int64_t e0, const uint4 &o) const {
+        if (wide) {
+            *reinterpret_cast<uint4 *>(p + e0) = o;
+        } else {
+            union {
+                uint4 q;
+                T t[Entry<TYPE>::E];
+            } u;
+            u.q = o;
+#pragma unroll
+            for (int i = 0; i < Entry<TYPE>::E; ++i) p[(e0 + i) * cs] = u.t[i];
+        }
+    }
+};
+
+// Vector j entry by entry, with everything looked at.
+template <int TYPE>
+__device__ __noinline__ void grad_vector(const Row<TYPE> r, const RowGrad c, const Out<TYPE> out, int64_t j) {
+    constexpr int E = Entry<TYPE>::E;
+    const int64_t e0 = j * E - r.head;
+#pragma unroll 1
+    for (int64_t e = e0 < 0 ? 0 : e0; e < e0 + E && e < r.cols; ++e) {
+        const float v = r.value(e);
+        typename Entry<TYPE>::T o = to_entry<TYPE>(0.f, typename Entry<TYPE>::T());
+        if (v != absent<TYPE>()) o = to_entry<TYPE>(entry_grad<TYPE>(c, v, 0.f), r.p[e * r.cs]);
+        out.p[e * out.cs] = o;
+    }
+}
+
+// The entries with ids among entries [lo, hi), after the dense part; entries
+// [held_lo, held_hi) of the row are at held[entry - lo], masked ones absent.
+template <int TYPE, int G>
+__device__ __forceinline__ void grad_ids(const Group<G> &g, const Row<TYPE> &r, const RowGrad &c,
+                                         const Out<TYPE> &out, const int64_t *ids, const float *adds, float sign,
+                                         int n, int64_t lo, int64_t hi,
+                                         const typename Entry<TYPE>::T *held = nullptr, int64_t held_lo = 0,
+                                         int64_t held_hi = 0) {
+#pragma unroll 1
+    for (int j = g.t; j < n; j += G) {
+        const int64_t id = ids[j];
+        if (id < 0 || id < lo || id >= hi) continue;
+        float add = 0.f;
+        bool first = true;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i)
+            if (ids[i] == id) {
+                first = first && i >= j;
+                add += adds[i];
+            }
+        if (!first) continue;
+        typename Entry<TYPE>::T x;
+        float v;
+        if (held && id >= held_lo && id < held_hi) {
+            x = held[id - lo];
+            v = Entry<TYPE>::value(x);
+        } else {
+            x = r.p[id * r.cs];
+            v = row_value<TYPE>(r, id);
+        }
+        if (v != absent<TYPE>()) out.p[id * out.cs] = to_entry<TYPE>(entry_grad<TYPE>(c, v, sign * add), x);
+    }
+}
+
+template <int TYPE, int G, bool MASK, bool BETA>
+__device__ __forceinline__ void grad_dense(const Group<G> &g, const Row<TYPE> &r, const RowGrad &c,
+                                           const Out<TYPE> &out, int64_t v0, int nv) {
+    using En = Entry<TYPE>;
+    constexpr int E = En::E;
+    int64_t in0, in1;
+    r.inside_range(in0, in1);
+    const int lo = (int)max((int64_t)0, min((int64_t)nv, in0 - v0));
+    const int hi = c.plain ? max(lo, (int)max((int64_t)0, min((int64_t)nv, in1 - v0))) : lo;
+    const uint4 *vecs = r.vectors() + v0;
+    const bool words = !MASK || r.mask_words();
+    const int64_t first = v0 * E - r.head;
+#pragma unroll 1
+    for (int b = 0; b < nv; b += kGradU * G) {
+        uint4 raw[kGradU];
+        if (words && out.wide && b >= lo && b + kGradU * G <= hi) {
+#pragma unroll
+            for (int u = 0; u < kGradU; ++u) raw[u] = __ldg(vecs + b + u * G + g.t);
+            if (MASK) {
+                typename Row<TYPE>::Keep keep[kGradU];
+#pragma unroll
+                for (int u = 0; u < kGradU; ++u) keep[u] = r.keep_word(first + (int64_t)(b + u * G + g.t) * E);
+#pragma unroll
+                for (int u = 0; u < kGradU; ++u) En::blank(raw[u], keep[u]);
+            }
+            uint4 *to = reinterpret_cast<uint4 *>(out.p + first) + b + g.t;
+#pragma unroll
+            for (int u = 0; u < kGradU; ++u) to[u * G] = dense_grad<TYPE, BETA>(c, raw[u]);
+            continue;
+        }
+        uint32_t odd = 0;
+#pragma unroll
+        for (int u = 0; u < kGradU; ++u) {
+            const int j = b + u * G + g.t;
+            if (j >= lo && j < hi && words) {
+                raw[u] = __ldg(vecs + j);
+                if (MASK) En::blank(raw[u], r.keep_word(first + (int64_t)j * E));
+            } else if (j < nv) {
+                odd |= 1u << u;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kGradU; ++u) {
+            const int j = b + u * G + g.t;
+            if (j >= lo && j < hi && words) out.put(first + (int64_t)j * E, dense_grad<TYPE, BETA>(c, raw[u]));
+        }
+#pragma unroll 1
+        for (; odd; odd &= odd - 1) grad_vector<TYPE>(r, c, out, v0 + b + (__ffs(odd) - 1) * G + g.t);
+    }
+}
+
 template <int TYPE, int G, bool MASK>
 __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_constant__ OutGrad a) {
-    using En = Entry<TYPE>;
-    using T = typename En::T;
-    constexpr int E = En::E;
+    constexpr int E = Entry<TYPE>::E;
     constexpr int kGroups = kOutThreads / G;
-    constexpr float kInf = __builtin_huge_valf();
     extern __shared__ int64_t lists[];
     __shared__ uint32_t red[4 * kOutThreads / 32];
     pdl_trigger();
     Group<G> g(red);
-    const int64_t item = (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
-    const int64_t row = G == 32 ? item : item / a.r.segs;
-    const int64_t seg = G == 32 ? 0 : item - row * a.r.segs;
+    const uint32_t item = blockIdx.x * kGroups + threadIdx.x / G, segs = (uint32_t)a.r.segs;
+    const int64_t row = G == 32 ? item : item / segs;
+    const int64_t seg = G == 32 ? 0 : item % segs;
     const int n = a.teacher.count ? a.teacher.count : a.n_given;
-    int64_t *ids = lists + (size_t)(threadIdx.x / G) * n;
-    float *adds = reinterpret_cast<float *>(lists + (size_t)kGroups * n) + (size_t)(threadIdx.x / G) * n;
+    Teacher &te = reinterpret_cast<Teacher *>(lists)[threadIdx.x / G];
+    int64_t *ids = te.id;
+    float *adds = te.q;
     pdl_wait();
     if (G == 32 && row >= a.r.rows) return;
 
@@ -114,27 +281,22 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
     c.beta = 0.f;
     c.entropy = 0.f;
     if (a.teacher.count) {
-        Teacher<G> te;
-        te.load(g, a.teacher, a.r, r, row);
-#pragma unroll
-        for (int i = 0; i < Teacher<G>::kPer; ++i) {
-            const int j = g.t + i * G;
-            if (j < n) {
-                ids[j] = te.id[i];
-                adds[j] = -te.q[i];
-            }
-        }
+        te.read(g, a.teacher, a.r, r, row, false);
+        g.sync();
+        if (g.warp == 0) te.normalise(n);
+        g.sync();
         c.alpha = te.used;
         c.mult = a.g_loss[row] * a.r.scale;
     } else {
         float total = 0.f;
+#pragma unroll 1
         for (int j = g.t; j < n; j += G) {
             int64_t id = a.given[row * n + j];
             if (id < -1 || id >= r.cols) {
                 flag_bad_id(a.r, row);
                 id = -1;
             }
-            if (id >= 0 && r.value(id) == absent<TYPE>()) id = -1;
+            if (id >= 0 && row_value<TYPE>(r, id) == absent<TYPE>()) id = -1;
             const float x = id >= 0 ? a.g_logp[row * n + j] : 0.f;
             ids[j] = id;
             adds[j] = x;
@@ -147,73 +309,13 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
         }
         c.mult = a.r.scale;
     }
-    c.inv_z = !En::kReal && a.r.scale == 1.f && c.logz > -80.f && c.logz < 80.f ? expf(-c.logz) : 0.f;
-
-    T *out = reinterpret_cast<T *>(a.grad) + row * a.grad_row_stride;
-    const int64_t os = a.grad_col_stride;
-    // vectors of the gradient are aligned where the row's are, or never
-    const bool wide = os == 1 && r.cs == 1 &&
-                      (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(r.p)) % kOutVecBytes == 0;
-
-    for (int b = 0; b < nv; b += kGradU * G) {
-        uint4 raw[kGradU];
-        bool in[kGradU];
-#pragma unroll
-        for (int u = 0; u < kGradU; ++u) {
-            const int j = b + u * G + g.t;
-            const int64_t e0 = (v0 + j) * E - r.head;
-            in[u] = wide && j < nv && r.inside(e0);
-            if (in[u]) raw[u] = r.raw(e0);
-        }
-        if constexpr (MASK) {
-#pragma unroll
-            for (int u = 0; u < kGradU; ++u)
-                if (in[u]) En::blank(raw[u], r.keep((v0 + b + u * G + g.t) * E - r.head));
-        }
-#pragma unroll
-        for (int u = 0; u < kGradU; ++u) {
-            const int j = b + u * G + g.t;
-            const int64_t e0 = (v0 + j) * E - r.head;
-            if (in[u]) {
-                float v[E];
-                En::values(raw[u], v);
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float x = entry_grad<TYPE>(c, v[i], 0.f);
-                    v[i] = v[i] == absent<TYPE>() ? 0.f : x;
-                }
-                *reinterpret_cast<uint4 *>(out + e0) = pack<TYPE>(v, raw[u]);
-            } else if (j < nv) {
-#pragma unroll 1
-                for (int i = 0; i < E; ++i) {
-                    const int64_t e = e0 + i;
-                    if (e < 0 || e >= r.cols) continue;
-                    const float v = r.value(e);
-                    T o = to_entry<TYPE>(0.f, T());
-                    if (v != absent<TYPE>()) o = to_entry<TYPE>(entry_grad<TYPE>(c, v, 0.f), r.p[e * r.cs]);
-                    out[e * os] = o;
-                }
-            }
-        }
-    }
+    finish_row_grad<TYPE>(c);
+    const Out<TYPE> out(a.grad, a.grad_row_stride, a.grad_col_stride, r, row);
+    if (c.beta != 0.f) grad_dense<TYPE, G, MASK, true>(g, r, c, out, v0, nv);
+    else grad_dense<TYPE, G, MASK, false>(g, r, c, out, v0, nv);
     if (n == 0) return;
     g.sync();
-    const int64_t e_lo = v0 * E - r.head, e_hi = v1 * E - r.head;
-    for (int j = g.t; j < n; j += G) {
-        const int64_t id = ids[j];
-        if (id < 0 || id < e_lo || id >= e_hi) continue;
-        float add = 0.f;
-        bool first = true;
-        for (int i = 0; i < n; ++i)
-            if (ids[i] == id) {
-                first = first && i >= j;
-                add += adds[i];
-            }
-        if (!first) continue;
-        const float v = r.value(id);
-        if (v != absent<TYPE>())
-            out[id * os] = to_entry<TYPE>(entry_grad<TYPE>(c, v, add), r.p[id * r.cs]);
-    }
+    grad_ids<TYPE>(g, r, c, out, ids, adds, a.teacher.count ? -1.f : 1.f, n, v0 * E - r.head, v1 * E - r.head);
 }
 
 template <int TYPE, int G, bool MASK>
@@ -221,7 +323,7 @@ cudaError_t launch_grad(const OutGrad &a, cudaStream_t stream) {
     const int64_t items = a.r.rows * a.r.segs;
     const int groups = kOutThreads / G;
     const int n = a.teacher.count ? a.teacher.count : a.n_given;
-    const size_t smem = (size_t)groups * n * (sizeof(int64_t) + sizeof(float));
+    const size_t smem = n ? groups * sizeof(Teacher) : 0;
     return launch_pdl(outcomes_grad<TYPE, G, MASK>, dim3((unsigned)((items + groups - 1) / groups)),
                       dim3(kOutThreads), smem, stream, a);
 }
