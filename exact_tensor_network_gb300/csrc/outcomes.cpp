@@ -13,10 +13,10 @@
 
 namespace tn {
 
-OutSplit out_split(int32_t type, int64_t cols, int64_t rows) {
+OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned) {
     const int64_t E = kOutVecBytes / out_entry_bytes(type);
     OutSplit s;
-    s.vecs = (cols + E - 1 + E - 1) / E;   // the first vector may hold one entry only
+    s.vecs = (cols + E - 1 + (aligned ? 0 : E - 1)) / E;   // its first may hold one entry only
     s.warp_rows = s.vecs <= kOutWarpVecs;
     s.segs = 1;
     s.seg_vecs = s.vecs;
@@ -68,8 +68,8 @@ struct Need {
     uint64_t tickets = 0, slots = 0, list_bytes = 0;
 };
 
-void add_need(const Outcomes &o, int64_t rows, Need *n) {
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows);
+void add_need(const Outcomes &o, int64_t rows, bool aligned, Need *n) {
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows, aligned);
     if (s.segs == 1) return;
     const uint64_t slots = (uint64_t)rows * s.segs;
     const uint64_t bytes = o.max_top == 0 ? 0
@@ -85,12 +85,23 @@ Need workspace_need(const Outcomes &o) {
     // the number of segments a row falls to its lowest value once the rows
     // alone fill the GPU
     const int64_t last = o.max_rows < tn::kOutTarget ? o.max_rows : tn::kOutTarget;
-    for (int64_t r = 1; r <= last; ++r) add_need(o, r, &n);
-    add_need(o, o.max_rows, &n);
+    for (int aligned = 0; aligned < 2; ++aligned) {
+        for (int64_t r = 1; r <= last; ++r) add_need(o, r, aligned, &n);
+        add_need(o, o.max_rows, aligned, &n);
+    }
     return n;
 }
 
 uint64_t align(uint64_t x) { return (x + 255) / 256 * 256; }
+
+// Whether every row starts at a 16-byte boundary (strided rows have no
+// vectors that could be cut short).
+bool aligned(const Outcomes &o, const tn_rows *r) {
+    const int64_t size = tn::out_entry_bytes(o.type);
+    if (r->col_stride != 1 && o.cols > 1) return true;
+    return reinterpret_cast<uintptr_t>(r->data) % tn::kOutVecBytes == 0 &&
+           (r->rows == 1 || r->row_stride * size % tn::kOutVecBytes == 0);
+}
 
 // Checks of the rows and the arguments that every call shares.
 tn_status common(Outcomes &o, const tn_rows *r) {
@@ -215,18 +226,18 @@ tn_status gradient(Outcomes &o, const tn::OutGrad &a, const tn::OutSplit &s, cud
 }
 
 // CTAs of a cluster that hold a row in shared memory; segs 0: too long.
-tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows) {
-    tn::OutSplit s = tn::out_split(type, cols, rows);
+tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int32_t count) {
+    tn::OutSplit s = tn::out_split(type, cols, rows, aligned);
     if (s.warp_rows) return s;
-    const int64_t bytes = s.vecs * tn::kOutVecBytes;
-    int64_t c = 1;
-    while (c < tn::kStepCluster && bytes > c * tn::kStepSlice) c *= 2;
+    const int64_t bytes = s.vecs * tn::kOutVecBytes, teachers = 2 * tn::teacher_bytes(count);
+    int64_t c = (bytes + tn::kStepSlice - teachers - 1) / (tn::kStepSlice - teachers);
+    if (c > tn::kStepCluster) c = tn::kStepCluster;
     // few rows: more CTAs a row, of two vectors a thread at least
-    while (c < tn::kStepCluster && rows * c < 2 * 152 && s.vecs >= 4 * c * tn::kStepThreads) c *= 2;
+    while (c < tn::kStepCluster && rows * c < 2 * 152 && s.vecs >= 2 * (c + 1) * tn::kStepThreads) ++c;
     s.flat = false;
     s.segs = c;
     s.seg_vecs = (s.vecs + c - 1) / c;
-    if (s.seg_vecs * tn::kOutVecBytes > tn::kStepSliceMost) s.segs = 0;
+    if (s.seg_vecs * tn::kOutVecBytes + teachers > tn::kStepSliceMost) s.segs = 0;
     return s;
 }
 
@@ -270,7 +281,7 @@ tn_status tn_outcomes_create(int32_t type, int64_t cols, int64_t max_rows, int32
         return fail(g_error, TN_EINVAL, "scale must lie in 2^-40 .. 2^40");
     if (cols > (int64_t)1 << 40) return fail(g_error, TN_EOVERFLOW, "more than 2^40 entries a row");
     int64_t items;
-    if (!mul_ok(max_rows, tn::out_split(type, cols, max_rows).segs, &items) || items > 0x7fffffff)
+    if (!mul_ok(max_rows, tn::out_split(type, cols, max_rows, false).segs, &items) || items > 0x7fffffff)
         return fail(g_error, TN_EOVERFLOW, "more than 2^31 - 1 row segments");
     tn_outcomes_s *h = new (std::nothrow) tn_outcomes_s;
     if (!h) return fail(g_error, TN_ENOMEM, "host allocation failed");
@@ -329,7 +340,7 @@ tn_status tn_outcomes_score(tn_outcomes_t *h, const tn_rows *rows, const int64_t
     if (rows->rows == 0) return TN_OK;
     if (!logz || !entropy || (n_given > 0 && (!given || !logp)) || (n_top > 0 && (!top_ids || !top_logp)))
         return fail(o.error, TN_EINVAL, "an output or the given outcomes are missing");
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows);
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows));
     tn::OutForward a = {};
     a.r = rows_of(o, rows, s);
     a.given = given;
@@ -357,7 +368,7 @@ tn_status tn_outcomes_score_grad(tn_outcomes_t *h, const tn_rows *rows, const in
     if (rows->rows == 0) return TN_OK;
     if (!logz || (n_given > 0 && (!given || !g_logp)) || (g_entropy && !entropy))
         return fail(o.error, TN_EINVAL, "logz, the given outcomes with g_logp, or entropy are missing");
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows);
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows));
     tn::OutGrad a = {};
     a.r = rows_of(o, rows, s);
     a.logz = logz;
@@ -381,7 +392,7 @@ tn_status tn_outcomes_distill(tn_outcomes_t *h, const tn_rows *rows, const tn_te
     if (st != TN_OK) return st;
     if (rows->rows == 0) return TN_OK;
     if (!loss || !logz) return fail(o.error, TN_EINVAL, "loss and logz are required");
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows);
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows));
     tn::OutForward a = {};
     a.r = rows_of(o, rows, s);
     a.logz = logz;
@@ -401,7 +412,7 @@ tn_status tn_outcomes_distill_grad(tn_outcomes_t *h, const tn_rows *rows, const 
     if (st != TN_OK) return st;
     if (rows->rows == 0) return TN_OK;
     if (!logz || !g_loss) return fail(o.error, TN_EINVAL, "logz and g_loss are required");
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows);
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows));
     tn::OutGrad a = {};
     a.r = rows_of(o, rows, s);
     a.logz = logz;
@@ -428,7 +439,7 @@ tn_status tn_outcomes_distill_step(tn_outcomes_t *h, const tn_rows *rows, const 
     if (st != TN_OK) return st;
     if (rows->rows == 0) return TN_OK;
     if (!loss || !logz) return fail(o.error, TN_EINVAL, "loss and logz are required");
-    const tn::OutSplit s = step_split(o.type, o.cols, rows->rows);
+    const tn::OutSplit s = step_split(o.type, o.cols, rows->rows, aligned(o, rows), teacher->count);
     if (s.segs == 0) return step_in_two(h, rows, teacher, g_loss, loss, logz, grad, grad_row_stride,
                                         grad_col_stride, stream);
     tn::OutStep a = {};

@@ -453,13 +453,55 @@ __device__ __forceinline__ void flag_bad_id(const OutRows &a, int64_t row) {
 
 // A row's teacher in shared memory: ids (-1 where left out), probabilities,
 // their logarithms and, where the loss is wanted, the row's order values
-// there.  The group reads it (its loads in flight together) with read(); after
-// a barrier one warp normalises it.
+// there, in teacher_bytes(count) at `base`.  The group reads it (its loads in
+// flight together) with read(); after a barrier one warp normalises it.
 struct Teacher {
-    int64_t id[TN_OUTCOMES_MAX_IDS];
-    float q[TN_OUTCOMES_MAX_IDS], logq[TN_OUTCOMES_MAX_IDS], value[TN_OUTCOMES_MAX_IDS];
-    float used;    // 1 if anything is left, else 0
+    int64_t *id;
+    float *q, *logq, *value;
+    float *used;   // 1 if anything is left, else 0
 
+    __device__ __forceinline__ Teacher(void *base, int count)
+        : id(static_cast<int64_t *>(base)), q(reinterpret_cast<float *>(id + count)), logq(q + count),
+          value(logq + count), used(value + count) {}
+
+    // one of the row's outcomes, between its loads and its place: item() loads
+    // it, look() what the row holds there, settle() waits for that
+    template <int TYPE>
+    struct Item {
+        int64_t x;
+        float l;
+        typename Entry<TYPE>::T v;
+        uint8_t keep;
+    };
+    template <int TYPE>
+    static __device__ __forceinline__ Item<TYPE> item(const OutTeacher &a, int64_t row, int j) {
+        const int64_t at = row * a.count + j;
+        Item<TYPE> t;
+        t.x = a.ids[at];
+        if (a.type == TN_TYPE_F32) t.l = static_cast<const float *>(a.logits)[at];
+        else if (a.type == TN_TYPE_BF16) t.l = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[at]);
+        else t.l = __half2float(static_cast<const __half *>(a.logits)[at]);
+        return t;
+    }
+    template <int TYPE>
+    static __device__ __forceinline__ void look(Item<TYPE> &t, const Row<TYPE> &r, bool values) {
+        const bool in = t.x >= 0 && t.x < r.cols;
+        t.v = typename Entry<TYPE>::T();
+        if (in && values) t.v = r.p[t.x * r.cs];
+        t.keep = 1;
+        if (in && r.m) t.keep = r.m[t.x * r.mcs];
+    }
+    template <int TYPE>
+    __device__ __forceinline__ void settle(int j, const Item<TYPE> &t, const OutTeacher &a, const OutRows &rows,
+                                           const Row<TYPE> &r, int64_t row) {
+        const bool in = t.x >= 0 && t.x < r.cols, wrong = !in && t.x != -1;
+        const float l = t.l * a.scale;
+        const bool used_ = in && t.keep && l != -__builtin_huge_valf();
+        if (wrong) flag_bad_id(rows, row);
+        id[j] = used_ ? t.x : wrong ? -2 : -1;       // -2: an id out of range
+        logq[j] = used_ ? l : -__builtin_huge_valf();
+        value[j] = Entry<TYPE>::value(t.v);
+    }
     template <int TYPE, int G>
     __device__ __forceinline__ void read(const Group<G> &g, const OutTeacher &a, const OutRows &rows,
                                          const Row<TYPE> &r, int64_t row, bool values) {
@@ -468,22 +510,9 @@ struct Teacher {
         for (int i = 0; i < kPer; ++i) {
             const int j = g.t + i * G;
             if (j >= a.count) break;
-            const int64_t at = row * a.count + j;
-            const int64_t x = a.ids[at];
-            float l;
-            if (a.type == TN_TYPE_F32) l = static_cast<const float *>(a.logits)[at];
-            else if (a.type == TN_TYPE_BF16) l = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[at]);
-            else l = __half2float(static_cast<const __half *>(a.logits)[at]);
-            l *= a.scale;
-            const bool in = x >= 0 && x < r.cols;
-            float v = absent<TYPE>();
-            if (in && values) v = Entry<TYPE>::value(r.p[x * r.cs]);
-            const bool kept = in && r.kept(x) && l != -__builtin_huge_valf();
-            if (!in && x != -1) flag_bad_id(rows, row);
-            // -2: an id out of range
-            id[j] = kept ? x : (!in && x != -1 ? -2 : -1);
-            logq[j] = kept ? l : -__builtin_huge_valf();
-            value[j] = v;
+            Item<TYPE> t = item<TYPE>(a, row, j);
+            look<TYPE>(t, r, values);
+            settle<TYPE>(j, t, a, rows, r, row);
         }
     }
     // one warp
@@ -509,7 +538,7 @@ struct Teacher {
             logq[j] -= logt;
             q[j] = id[j] >= 0 ? q[j] / total : 0.f;
         }
-        if (lane == 0) used = top == -__builtin_huge_valf() ? 0.f : 1.f;
+        if (lane == 0) *used = top == -__builtin_huge_valf() ? 0.f : 1.f;
         __syncwarp();
     }
 };

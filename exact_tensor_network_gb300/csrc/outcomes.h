@@ -33,7 +33,7 @@ inline int out_entry_bytes(int32_t type) { return type == TN_TYPE_C64 ? 8 : type
 
 // How a batch of rows is cut: `segs` segments of `seg_vecs` vectors a row.
 struct OutSplit {
-    int64_t vecs;       // vectors of the longest row (its first may be partial)
+    int64_t vecs;       // vectors of the longest row
     int64_t seg_vecs;
     int64_t segs;
     bool warp_rows;     // one warp per row (segs is 1)
@@ -117,9 +117,16 @@ struct OutStep {
 };
 
 constexpr int kStepThreads = 256;
-constexpr int64_t kStepSlice = 68 * 1024;      // three CTAs on an SM
-constexpr int64_t kStepSliceMost = 216 * 1024; // one
+constexpr int kStepCtas = 3;                   // on an SM
+// Shared memory of a CTA for its slice and two teachers: three CTAs on an SM,
+// and one.
+constexpr int64_t kStepSlice = 73 * 1024;
+constexpr int64_t kStepSliceMost = 222 * 1024;
 constexpr int kStepCluster = 8;
+
+// Shared memory of a row's teacher (see Teacher): id, q, log q and value of
+// each outcome, and a flag.
+__host__ __device__ inline int teacher_bytes(int count) { return (count * 20 + 16 + 15) / 16 * 16; }
 
 struct Outcomes {
     int32_t type = 0;
@@ -132,7 +139,8 @@ struct Outcomes {
     char error[256] = {0};
 };
 
-OutSplit out_split(int32_t type, int64_t cols, int64_t rows);
+// aligned: every row starts at a 16-byte boundary.
+OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned);
 // Launchers, instantiated by k_outcomes_<type>.cu.
 template <int TYPE>
 cudaError_t outcomes_forward_of(const OutForward &a, bool warp_rows, cudaStream_t stream);

@@ -63,6 +63,22 @@ struct Sums {
     }
 };
 
+// largest order value of a vector's 16 bytes
+template <int TYPE>
+__device__ __forceinline__ float vector_max(const uint4 &q) {
+    if constexpr (TYPE == TN_TYPE_BF16) {
+        const uint32_t m = max_bf16x2(max_bf16x2(q.x, q.y), max_bf16x2(q.z, q.w));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    } else {
+        float v[Entry<TYPE>::E];
+        Entry<TYPE>::values(q, v);
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < Entry<TYPE>::E; ++i) m = max_nan(m, v[i]);
+        return m;
+    }
+}
+
 // A thread's sums while it streams, in two halves for the packed arithmetic.
 //
 // Real logits: d = c2 v - ref with ref = c2 z0 rounded, one fused operation;
@@ -141,6 +157,58 @@ struct Stream {
             }
         }
         return true;
+    }
+    // Add a step of vectors without a look at each one's maximum (sums alone,
+    // no entropy).  The reference comes from the first step; later ones may
+    // exceed it by far before a sum overflows, and the sums are as good either
+    // way.  False: nothing was added, take the vectors one by one.
+    __device__ __forceinline__ bool add_step(const uint4 (&raw)[kU], float c2) {
+        static_assert(!ENT, "the entropy's sum needs a near reference");
+        constexpr float kBig = 1.2379400392853803e27f;    // 2^90
+        constexpr float kInf = __builtin_huge_valf();
+        if (En::kReal ? ref == -kInf : z0 == 0.f) {
+            if (s.x != 0.f || s.y != 0.f) return false;   // (far out)
+            float lm = vector_max<TYPE>(raw[0]);
+#pragma unroll
+            for (int u = 1; u < kU; ++u) lm = max_nan(lm, vector_max<TYPE>(raw[u]));
+            if (lm == absent<TYPE>()) return true;
+            if constexpr (En::kReal) {
+                const float r = lm * c2;
+                if (!(fabsf(r) <= kFar)) return false;
+                ref = r;
+                z0 = lm;
+            } else {
+                if (!(lm < kInf)) return false;
+                z0 = lm < kTiny ? kTiny : lm;
+                inv = __fdiv_rn(1.f, z0);
+            }
+        }
+        const float2 before = s;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            float v[E];
+            En::values(raw[u], v);
+            if constexpr (En::kReal) {
+                const float2 cc = make_float2(c2, c2), rr = make_float2(-ref, -ref);
+#pragma unroll
+                for (int i = 0; i < E; i += 2) {
+                    const float2 d = fma2(make_float2(v[i], v[i + 1]), cc, rr);
+                    s = add2(s, make_float2(ex2(d.x), ex2(d.y)));
+                }
+            } else {
+                float e[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const float q = v[i] * inv;
+                    e[i] = fmaf(fmaf(-q, z0, v[i]), inv, q);
+                    if (!UNIT) e[i] = ex2(c2 * lg2(e[i]));
+                }
+                s = add2(s, make_float2(e[0], e[1]));
+            }
+        }
+        if (s.x + s.y < kBig) return true;
+        s = before;
+        return false;
     }
     // the same for logits far out: v as they are
     __device__ __forceinline__ void far(const float (&v)[E], float lm, float c2) {
@@ -405,22 +473,6 @@ __device__ __forceinline__ int rank_candidates(Group<G> &g, const Scratch &sm, i
     return (int)found;
 }
 
-// largest order value of a vector's 16 bytes
-template <int TYPE>
-__device__ __forceinline__ float vector_max(const uint4 &q) {
-    if constexpr (TYPE == TN_TYPE_BF16) {
-        const uint32_t m = max_bf16x2(max_bf16x2(q.x, q.y), max_bf16x2(q.z, q.w));
-        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-    } else {
-        float v[Entry<TYPE>::E];
-        Entry<TYPE>::values(q, v);
-        float m = v[0];
-#pragma unroll
-        for (int i = 1; i < Entry<TYPE>::E; ++i) m = fmaxf(m, v[i]);
-        return m;
-    }
-}
-
 // The k best entries of `nv` vectors from v0 on into sm.best, as candidates
 // with indices (vector - v0) E + entry, from the maxima in sm.keys, each that
 // of 2^log vectors.  Returns their number.
@@ -623,7 +675,7 @@ __device__ __forceinline__ float teacher_loss(int count, const OutRows &r, const
 
 template <int TYPE, bool ENT, int G>
 __device__ __forceinline__ void finish_row(Group<G> &g, const OutForward &a, const Row<TYPE> &r,
-                                           Teacher *te, int64_t row, float logz, float entropy) {
+                                           Teacher &te, int64_t row, float logz, float entropy) {
     constexpr float kInf = __builtin_huge_valf();
     if (g.t == 0) a.logz[row] = logz;
     if constexpr (ENT) {
@@ -645,8 +697,8 @@ __device__ __forceinline__ void finish_row(Group<G> &g, const OutForward &a, con
         }
     } else {
         if (g.warp == 0) {
-            te->normalise(a.teacher.count);
-            const float loss = teacher_loss<TYPE>(a.teacher.count, a.r, *te, logz);
+            te.normalise(a.teacher.count);
+            const float loss = teacher_loss<TYPE>(a.teacher.count, a.r, te, logz);
             if (g.t == 0) a.loss[row] = loss;
         }
     }
@@ -680,8 +732,9 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint32_t red[4 * kOutThreads / 32];
     __shared__ bool last;
-    __shared__ Teacher teachers[ENT ? 1 : kGroups];
-    Teacher *te = teachers + (ENT ? 0 : threadIdx.x / G);
+    constexpr int kTeacher = ENT ? 16 : TN_OUTCOMES_MAX_IDS * 20 + 16;
+    __shared__ __align__(16) unsigned char teachers[kGroups * kTeacher];
+    Teacher te(teachers + threadIdx.x / G * kTeacher, ENT ? 0 : a.teacher.count);
     pdl_trigger();
     Group<G> g(red);
     const uint32_t item = blockIdx.x * kGroups + threadIdx.x / G, segs = (uint32_t)a.r.segs;
@@ -710,7 +763,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     const bool words = MASK && r.mask_words();
     using Keep = typename Row<TYPE>::Keep;
     Stream<TYPE, ENT, UNIT> st;
-    if (!ENT) te->read(g, a.teacher, a.r, r, row, true);
+    if (!ENT) te.read(g, a.teacher, a.r, r, row, true);
 
     // the largest of each of the step's kU rows of 32 vectors, into the maxima
     const auto put_maxima = [&](int b, float (&lm)[kU]) {
@@ -740,7 +793,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     const auto whole = [&](int b) { return b >= lo && b + kStep <= hi; };
 #pragma unroll 1
     for (int b = g.warp * kStep; b < nv; b += kU * G) {
-        float lm[kU];
+        [[maybe_unused]] float lm[kU];
         uint32_t later = 0;         // vectors that the straight way cannot do
         uint4 raw[kU];
         if (whole(b)) {
@@ -775,11 +828,19 @@ outcomes_forward(const __grid_constant__ OutForward a) {
                 }
             }
         }
+        if constexpr (!ENT) {
+            if (!st.add_step(raw, a.r.c2)) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            float v[E];
-            lm[u] = decode<TYPE>(raw[u], v, a.r.floor);
-            if (!st.add(v, lm[u], a.r.c2)) later |= 1u << u;
+                for (int u = 0; u < kU; ++u)
+                    if (b + u * 32 + g.lane < nv) later |= 1u << u;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                float v[E];
+                lm[u] = decode<TYPE>(raw[u], v, a.r.floor);
+                if (!st.add(v, lm[u], a.r.c2)) later |= 1u << u;
+            }
         }
         if (ENT && k > 0) put_maxima(b, lm);
         if (__any_sync(0xffffffffu, later)) {

@@ -255,7 +255,7 @@ template <int TYPE, int G, bool MASK>
 __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_constant__ OutGrad a) {
     constexpr int E = Entry<TYPE>::E;
     constexpr int kGroups = kOutThreads / G;
-    extern __shared__ int64_t lists[];
+    extern __shared__ __align__(16) unsigned char lists[];
     __shared__ uint32_t red[4 * kOutThreads / 32];
     pdl_trigger();
     Group<G> g(red);
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
     const int64_t row = G == 32 ? item : item / segs;
     const int64_t seg = G == 32 ? 0 : item % segs;
     const int n = a.teacher.count ? a.teacher.count : a.n_given;
-    Teacher &te = reinterpret_cast<Teacher *>(lists)[threadIdx.x / G];
+    Teacher te(lists + threadIdx.x / G * teacher_bytes(n), n);
     int64_t *ids = te.id;
     float *adds = te.q;
     pdl_wait();
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
         g.sync();
         if (g.warp == 0) te.normalise(n);
         g.sync();
-        c.alpha = te.used;
+        c.alpha = *te.used;
         c.mult = a.g_loss[row] * a.r.scale;
     } else {
         float total = 0.f;
@@ -323,7 +323,7 @@ cudaError_t launch_grad(const OutGrad &a, cudaStream_t stream) {
     const int64_t items = a.r.rows * a.r.segs;
     const int groups = kOutThreads / G;
     const int n = a.teacher.count ? a.teacher.count : a.n_given;
-    const size_t smem = n ? groups * sizeof(Teacher) : 0;
+    const size_t smem = n ? groups * teacher_bytes(n) : 0;
     return launch_pdl(outcomes_grad<TYPE, G, MASK>, dim3((unsigned)((items + groups - 1) / groups)),
                       dim3(kOutThreads), smem, stream, a);
 }

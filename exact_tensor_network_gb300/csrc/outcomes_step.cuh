@@ -2,13 +2,13 @@
 // memory between the sums and the gradient, so that it is read once and its
 // gradient written once.  Included by the translation unit of each entry type.
 //
-// A cluster of up to eight CTAs holds a row (kStepSlice bytes a CTA, so that
-// three CTAs are on an SM and one's loads run beside another's stores; more
-// for longer rows, more CTAs for few rows).  Every thread copies its own
-// vectors to shared memory ahead of the sums (cp.async, no barrier), the CTAs
-// exchange their sums through distributed shared memory, and every thread
-// reads its own vectors back for the gradient.  Rows of one warp are held by
-// one warp each.
+// A cluster of up to eight CTAs holds a row and goes from row to row.  Every
+// thread copies its own vectors to shared memory (cp.async, no barrier for the
+// data), sums them, and after the CTAs have exchanged their sums through
+// distributed shared memory reads them back for the gradient; as soon as it
+// has used a vector it copies the next row's in its place.  So the loads of
+// the next row run beside the stores of this one, and three CTAs an SM cover
+// each other's barriers.  Rows of one warp are held by one warp each.
 #pragma once
 
 #include "outcomes_forward.cuh"
@@ -18,7 +18,17 @@ namespace tn {
 
 namespace {
 
-constexpr int kStepAhead = 4;      // steps of kU vectors in flight per thread
+// At most n of this thread's last copy groups still in flight.
+__device__ __forceinline__ void copy_wait_all_but(int n) {
+    switch (n) {
+        case 0: copy_wait<0>(); break;
+        case 1: copy_wait<1>(); break;
+        case 2: copy_wait<2>(); break;
+        case 3: copy_wait<3>(); break;
+        case 4: copy_wait<4>(); break;
+        default: copy_wait<5>(); break;
+    }
+}
 
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -26,15 +36,11 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 cluster_load(const float4 *p, int rank) {
+// v to where p is in the shared memory of CTA `rank` of the cluster
+__device__ __forceinline__ void cluster_store(const float2 *p, int rank, float2 v) {
     uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p)), far;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(far)
-                 : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(far), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // The dense part of a vector where the row's sums are at hand.
@@ -43,7 +49,7 @@ struct Dense {
     float2 z0, c2, ls, ma;
     __device__ __forceinline__ Dense(const RowGrad &c, float z, float s, float c2_)
         : z0(make_float2(-z, -z)), c2(make_float2(c2_, c2_)) {
-        const float l = -log2f(s), m = c.mult * c.alpha;
+        const float l = -kLog2E * logf(s), m = c.mult * c.alpha;     // (as log Z has it)
         ls = make_float2(l, l);
         ma = make_float2(m, m);
     }
@@ -66,75 +72,66 @@ struct Dense {
     }
 };
 
+// A CTA's part of a row.  Vectors [lo, hi) of its nv go through shared memory;
+// the row's first and last (all of a strided row's, or of one whose mask bytes
+// are not words) do not.
+template <int TYPE, bool MASK, int G>
+struct Slice {
+    Row<TYPE> r;
+    int nv, lo, hi, steps;
+    int64_t v0, first;       // first vector, first entry
+    const uint4 *vecs;
+
+    __device__ __forceinline__ Slice(const OutRows &a, int64_t row, int rank) : r(a, row) {
+        constexpr int E = Entry<TYPE>::E;
+        // (a row that fits a cluster has fewer than 2^31 entries)
+        const int slice = (int)a.seg_vecs, at = rank * slice, end = r.head + (int)r.cols;
+        v0 = at;
+        first = (int64_t)at * E - r.head;
+        nv = max(0, min((end + E - 1) / E - at, slice));
+        lo = r.cs == 1 && rank == 0 && r.head > 0 ? min(1, nv) : 0;
+        hi = r.cs == 1 && (!MASK || r.mask_words()) ? max(lo, min(nv, end / E - at)) : lo;
+        steps = (nv + kU * G - 1) / (kU * G);
+        vecs = r.vectors() + v0;
+    }
+    __device__ __forceinline__ bool whole(int b, int n) const { return b >= lo && b + n <= hi; }
+};
+
+// One step (kU vectors a thread, from vector b on) of a row into hold.
+template <int TYPE, bool MASK, int G>
+__device__ __forceinline__ void copy_step(const Slice<TYPE, MASK, G> &s, uint4 *hold, int b, int t) {
+    if (s.whole(b, kU * G)) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) copy16(hold + b + u * G + t, s.vecs + b + u * G + t);
+    } else if (b < s.nv) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int j = b + u * G + t;
+            if (j >= s.lo && j < s.hi) copy16(hold + j, s.vecs + j);
+        }
+    }
+    copy_commit();
+}
+
+// The sums of a slice, whose copies are the last groups (one a step).
 template <int TYPE, int G, bool MASK, bool UNIT>
-__global__ void __launch_bounds__(G == 32 ? kOutThreads : G, G == 32 ? 6 : 3)
-outcomes_step(const __grid_constant__ OutStep a) {
+__device__ __forceinline__ Sums<TYPE> sum_slice(const Slice<TYPE, MASK, G> &s, uint4 *hold, int t,
+                                                const OutRows &a) {
     using En = Entry<TYPE>;
     constexpr int E = En::E;
-    constexpr int kGroups = G == 32 ? kOutThreads / 32 : 1;
-    constexpr float kInf = __builtin_huge_valf();
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ uint32_t red[4 * G / 32];
-    __shared__ float4 part;
-    __shared__ Teacher teachers[kGroups];
-    pdl_trigger();
-    Group<G> g(red);
-    const int group = threadIdx.x / G;
-    const uint32_t item = blockIdx.x * kGroups + group, ranks = G == 32 ? 1 : (uint32_t)a.r.segs;
-    const int64_t row = G == 32 ? item : item / ranks;
-    const int rank = G == 32 ? 0 : item % ranks;
-    const int n = a.teacher.count;
-    Teacher &te = teachers[group];
-    uint4 *hold = reinterpret_cast<uint4 *>(smem) + group * a.r.seg_vecs + g.t;
-    pdl_wait();
-    if (G == 32 && row >= a.r.rows) return;
-
-    const Row<TYPE> r(a.r, row);
-    const int64_t v0 = rank * a.r.seg_vecs;
-    const int64_t all = (r.head + r.cols + E - 1) / E;
-    const int64_t v1 = min(all, v0 + a.r.seg_vecs);
-    const int nv = static_cast<int>(max((int64_t)0, v1 - v0));
-    const bool words = !MASK || r.mask_words();
-    int64_t in0, in1;
-    r.inside_range(in0, in1);
-    // vectors [lo, hi) go through shared memory; the row's first and last
-    // (all of a strided row's, or of one whose mask bytes are not words) do not
-    const int lo = (int)max((int64_t)0, min((int64_t)nv, in0 - v0));
-    const int hi = words ? max(lo, (int)max((int64_t)0, min((int64_t)nv, in1 - v0))) : lo;
-    const uint4 *vecs = r.vectors() + v0 + g.t;
-    const int64_t first = v0 * E - r.head;
-
-    const auto whole = [&](int b) { return b >= lo && b + kU * G <= hi; };
-    const auto copy_step = [&](int b) {
-        if (whole(b)) {
-#pragma unroll
-            for (int u = 0; u < kU; ++u) copy16(hold + b + u * G, vecs + b + u * G);
-        } else if (b < nv) {
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int j = b + u * G + g.t;
-                if (j >= lo && j < hi) copy16(hold + b + u * G, vecs + b + u * G);
-            }
-        }
-        copy_commit();
-    };
-#pragma unroll 1
-    for (int i = 0; i < kStepAhead; ++i) copy_step(i * kU * G);
     typename Row<TYPE>::Keep next_keep[kU];
     const auto load_keep = [&](int b) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int j = b + u * G + g.t;
-            if (j >= lo && j < hi) next_keep[u] = r.keep_word(first + (int64_t)j * E);
+            const int j = b + u * G + t;
+            if (j >= s.lo && j < s.hi) next_keep[u] = s.r.keep_word(s.first + (int64_t)j * E);
         }
     };
     if (MASK) load_keep(0);
-
-    te.read(g, a.teacher, a.r, r, row, rank == 0);
-
     Stream<TYPE, false, UNIT> st;
 #pragma unroll 1
-    for (int b = 0; b < nv; b += kU * G) {
+    for (int i = 0; i < s.steps; ++i) {
+        const int b = i * kU * G;
         uint32_t later = 0;
         typename Row<TYPE>::Keep keep[kU];
         if (MASK) {
@@ -142,147 +139,342 @@ outcomes_step(const __grid_constant__ OutStep a) {
             for (int u = 0; u < kU; ++u) keep[u] = next_keep[u];
             load_keep(b + kU * G);
         }
-        copy_wait<kStepAhead - 1>();
-        const bool full = whole(b);
+        copy_wait_all_but(s.steps - 1 - i);
+        uint4 raw[kU];
+        if (s.whole(b, kU * G)) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int j = b + u * G + g.t;
-            const bool in = full || (j >= lo && j < hi);
-            uint4 raw = En::absent_vector();
-            if (in) {
-                raw = hold[b + u * G];
+            for (int u = 0; u < kU; ++u) {
+                raw[u] = hold[b + u * G + t];
                 if (MASK) {
-                    En::blank(raw, keep[u]);
-                    hold[b + u * G] = raw;
+                    En::blank(raw[u], keep[u]);
+                    hold[b + u * G + t] = raw[u];
                 }
-            } else if (j < nv) {
-                later |= 1u << u;
             }
-            float v[E];
-            const float lm = decode<TYPE>(raw, v, a.r.floor);
-            if (!st.add(v, lm, a.r.c2)) later |= 1u << u;
+        } else {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int j = b + u * G + t;
+                raw[u] = En::absent_vector();
+                if (j >= s.lo && j < s.hi) {
+                    raw[u] = hold[j];
+                    if (MASK) {
+                        En::blank(raw[u], keep[u]);
+                        hold[j] = raw[u];
+                    }
+                } else if (j < s.nv) {
+                    later |= 1u << u;
+                }
+            }
+        }
+        if (!st.add_step(raw, a.c2)) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (b + u * G + t < s.nv) later |= 1u << u;
         }
 #pragma unroll 1
         for (; later; later &= later - 1) {
-            const auto x = row_vector<TYPE>(r, v0 + b + (__ffs(later) - 1) * G + g.t);
+            const auto x = row_vector<TYPE>(s.r, s.v0 + b + (__ffs(later) - 1) * G + t);
             float v[E];
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = x.v[i];
-            const float m = largest<TYPE>(v, a.r.floor);
-            if (!st.add(v, m, a.r.c2)) st.far(x.v, m, a.r.c2);
+            for (int e = 0; e < E; ++e) v[e] = x.v[e];
+            const float m = largest<TYPE>(v, a.floor);
+            if (!st.add(v, m, a.c2)) st.far(x.v, m, a.c2);
         }
-        copy_step(b + kStepAhead * kU * G);
     }
-    Sums<TYPE> sum = st.done(a.r.c2);
-    combine(g, sum, a.r.c2);
-    if (G == 32) g.sync();
-    if (G > 32 && ranks > 1) {
-        if (g.t == 0) part = make_float4(sum.z0, sum.s, 0.f, 0.f);
-        cluster_arrive();
-        if (g.warp == 0) te.normalise(n);
-        cluster_wait();
-        // the cluster's sums, one a lane
-        sum = Sums<TYPE>();
-        if (g.lane < (int)ranks) {
-            const float4 f = cluster_load(&part, g.lane);
-            sum.z0 = f.x;
-            sum.s = f.y;
-        }
-        float m = sum.z0;
-#pragma unroll
-        for (int o = 4; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (sum.z0 != m) sum.move_to(m, a.r.c2);
-#pragma unroll
-        for (int o = 4; o; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
-        sum.z0 = __shfl_sync(0xffffffffu, m, 0);      // lanes from 8 on saw nothing
-        sum.s = __shfl_sync(0xffffffffu, sum.s, 0);
-        cluster_arrive();      // (waited for at the end: the others may still read)
-    } else if (g.warp == 0) {
-        te.normalise(n);
-    }
-    g.sync();
-    float logz, entropy;
-    normaliser<TYPE>(a.r, sum, logz, entropy);
+    return st.done(a.c2);
+}
 
+// The dense gradient of one step of a slice.
+template <int TYPE, int G, bool MASK>
+__device__ __forceinline__ void grad_step(const Slice<TYPE, MASK, G> &s, const uint4 *hold, int b, int t,
+                                          const RowGrad &c, const Dense<TYPE> &dense, const Out<TYPE> &out) {
+    constexpr int E = Entry<TYPE>::E;
+    if (c.plain && out.wide && s.whole(b, kU * G)) {
+        uint4 *to = reinterpret_cast<uint4 *>(out.p + s.first) + b + t;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) to[u * G] = dense.grad(c, hold[b + u * G + t]);
+        return;
+    }
+    uint32_t odd = 0;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const int j = b + u * G + t;
+        if (c.plain && j >= s.lo && j < s.hi) out.put(s.first + (int64_t)j * E, dense.grad(c, hold[j]));
+        else if (j < s.nv) odd |= 1u << u;
+    }
+#pragma unroll 1
+    for (; odd; odd &= odd - 1) grad_vector<TYPE>(s.r, c, out, s.v0 + b + (__ffs(odd) - 1) * G + t);
+}
+
+template <int TYPE>
+__device__ __forceinline__ RowGrad step_grad(const OutStep &a, float g_loss, float logz, float used) {
     RowGrad c;
     c.scale = a.r.scale;
     c.logz = logz;
     c.beta = c.entropy = 0.f;
-    c.alpha = te.used;
-    c.mult = a.g_loss[row] * a.r.scale;
+    c.alpha = used;
+    c.mult = g_loss * a.r.scale;
     finish_row_grad<TYPE>(c);
-    const Out<TYPE> out(a.grad, a.grad_row_stride, a.grad_col_stride, r, row);
-    // p = 2^(c2 (z - z0) - log2 s): 1 exactly for a row's only entry
-    Dense<TYPE> dense(c, sum.z0, sum.s, a.r.c2);
-#pragma unroll 1
-    for (int b = 0; b < nv; b += kU * G) {
-        if (c.plain && out.wide && whole(b)) {
-            uint4 *to = reinterpret_cast<uint4 *>(out.p + first) + b + g.t;
-#pragma unroll
-            for (int u = 0; u < kU; ++u) to[u * G] = dense.grad(c, hold[b + u * G]);
-            continue;
-        }
-        uint32_t odd = 0;
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int j = b + u * G + g.t;
-            if (c.plain && j >= lo && j < hi) out.put(first + (int64_t)j * E, dense.grad(c, hold[b + u * G]));
-            else if (j < nv) odd |= 1u << u;
-        }
-#pragma unroll 1
-        for (; odd; odd &= odd - 1) grad_vector<TYPE>(r, c, out, v0 + b + (__ffs(odd) - 1) * G + g.t);
-    }
-    g.sync();
-    const typename En::T *held = reinterpret_cast<const typename En::T *>(hold - g.t);
-    grad_ids<TYPE>(g, r, c, out, te.id, te.q, -1.f, n, first, v1 * E - r.head, held, first + (int64_t)lo * E,
-                   first + (int64_t)hi * E);
-    if (rank == 0 && g.warp == 0) {
-        const float loss = teacher_loss<TYPE>(n, a.r, te, logz);
-        if (g.t == 0) {
-            a.loss[row] = loss;
-            a.logz[row] = logz;
-        }
-    }
-    if (G > 32 && ranks > 1) cluster_wait();
+    return c;
 }
 
-template <int TYPE, int G, bool MASK, bool UNIT>
-cudaError_t launch_step(const OutStep &a, cudaStream_t stream) {
-    auto *kernel = outcomes_step<TYPE, G, MASK, UNIT>;
-    const int threads = G == 32 ? kOutThreads : G, groups = threads / G;
-    const size_t smem = (size_t)groups * a.r.seg_vecs * kOutVecBytes;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// Rows of one warp.
+template <int TYPE, bool MASK, bool UNIT>
+__global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __grid_constant__ OutStep a) {
+    using En = Entry<TYPE>;
+    constexpr int E = En::E;
+    constexpr int kGroups = kOutThreads / 32;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ __align__(16) unsigned char teachers[kGroups * (TN_OUTCOMES_MAX_IDS * 20 + 16)];
+    pdl_trigger();
+    Group<32> g(nullptr);
+    const int group = threadIdx.x / 32;
+    const int64_t row = (int64_t)blockIdx.x * kGroups + group;
+    Teacher te(teachers + group * (TN_OUTCOMES_MAX_IDS * 20 + 16), a.teacher.count);
+    uint4 *hold = reinterpret_cast<uint4 *>(smem) + group * a.r.seg_vecs;
+    const int n = a.teacher.count;
+    pdl_wait();
+    if (row >= a.r.rows) return;
+    const Slice<TYPE, MASK, 32> s(a.r, row, 0);
+#pragma unroll 1
+    for (int i = 0; i < s.steps; ++i) copy_step<TYPE, MASK, 32>(s, hold, i * kU * 32, g.t);
+    te.read(g, a.teacher, a.r, s.r, row, true);
+    Sums<TYPE> sum = sum_slice<TYPE, 32, MASK, UNIT>(s, hold, g.t, a.r);
+    combine(g, sum, a.r.c2);
+    g.sync();
+    te.normalise(n);
+    float logz, entropy;
+    normaliser<TYPE>(a.r, sum, logz, entropy);
+    const RowGrad c = step_grad<TYPE>(a, a.g_loss[row], logz, *te.used);
+    const Dense<TYPE> dense(c, sum.z0, sum.s, a.r.c2);
+    const Out<TYPE> out(a.grad, a.grad_row_stride, a.grad_col_stride, s.r, row);
+#pragma unroll 1
+    for (int i = 0; i < s.steps; ++i) grad_step<TYPE, 32, MASK>(s, hold, i * kU * 32, g.t, c, dense, out);
+    g.sync();
+    grad_ids<TYPE>(g, s.r, c, out, te.id, te.q, -1.f, n, s.first, s.first + (int64_t)s.nv * E,
+                   reinterpret_cast<const typename En::T *>(hold), s.first + (int64_t)s.lo * E,
+                   s.first + (int64_t)s.hi * E);
+    const float loss = teacher_loss<TYPE>(n, a.r, te, logz);
+    if (g.t == 0) {
+        a.loss[row] = loss;
+        a.logz[row] = logz;
+    }
+}
+
+// Longer rows: a.r.segs CTAs of a cluster a row.  Two barriers a row:
+// the cluster's, at which every warp's sums have reached every CTA, and one
+// between reading the entries at the teacher's outcomes and the copies that
+// take their place.  What follows from a row but has no hurry (the entries at
+// the teacher's outcomes, which others' dense stores must precede) waits for
+// the next row's barrier; the next row's teacher is fetched one row ahead.
+template <int TYPE, bool MASK, bool UNIT>
+__global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const __grid_constant__ OutStep a) {
+    using En = Entry<TYPE>;
+    using T = typename En::T;
+    constexpr int E = En::E, G = kStepThreads, kWarps = G / 32;
+    static_assert(G >= TN_OUTCOMES_MAX_IDS, "one of the teacher's outcomes a thread");
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float2 part[2][kWarps * kStepCluster];
+    pdl_trigger();
+    const int t = threadIdx.x, lane = t % 32, warp = t / 32;
+    const uint32_t ranks = (uint32_t)a.r.segs, clusters = gridDim.x / ranks;
+    const int rank = blockIdx.x % ranks, n = a.teacher.count;
+    int64_t row = blockIdx.x / ranks;
+    uint4 *hold = reinterpret_cast<uint4 *>(smem);
+    unsigned char *te_base = smem + a.r.seg_vecs * kOutVecBytes;
+    // the cluster's CTAs have all started before any writes to another's memory
+    if (ranks > 1) cluster_arrive();
+    pdl_wait();
+
+    Slice<TYPE, MASK, G> s(a.r, row, rank);
+#pragma unroll 1
+    for (int i = 0; i < s.steps; ++i) copy_step<TYPE, MASK, G>(s, hold, i * kU * G, t);
+    {
+        Teacher te(te_base, n);
+        if (t < n) {
+            Teacher::Item<TYPE> it = Teacher::item<TYPE>(a.teacher, row, t);
+            Teacher::look<TYPE>(it, s.r, rank == 0);
+            te.settle<TYPE>(t, it, a.teacher, a.r, s.r, row);
+        }
+        __syncthreads();
+        if (warp == 0) te.normalise(n);
+    }
+    if (ranks > 1) cluster_wait();
+    int turn = 0;
+    T fix = T();                 // the entry of this thread's outcome in the
+    T *fix_at = nullptr;         // last row, if it is this CTA's
+#pragma unroll 1
+    while (true) {
+        const int64_t next_row = row + clusters;
+        const bool more = next_row < a.r.rows;
+        const Slice<TYPE, MASK, G> next(a.r, more ? next_row : row, rank);
+        Teacher::Item<TYPE> it;
+        if (more && t < n) it = Teacher::item<TYPE>(a.teacher, next_row, t);
+        const float g_loss = a.g_loss[row];
+
+        Sums<TYPE> sum = sum_slice<TYPE, G, MASK, UNIT>(s, hold, t, a.r);
+        float m = sum.z0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (sum.z0 != m) sum.move_to(m, a.r.c2);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
+        if (more && t < n) Teacher::look<TYPE>(it, next.r, rank == 0);
+        // part alternates: a slot is written again only after the barrier
+        // that follows its reading
+        float2 *mine = part[turn] + rank * kWarps + warp;
+        if (ranks == 1) {
+            if (lane == 0) *mine = make_float2(sum.z0, sum.s);
+            __syncthreads();
+        } else {
+            if (lane < (int)ranks) cluster_store(mine, lane, make_float2(sum.z0, sum.s));
+            cluster_arrive();
+            cluster_wait();
+        }
+        if (fix_at) *fix_at = fix;
+        fix_at = nullptr;
+        const int np = (int)ranks * kWarps;
+        sum = Sums<TYPE>();
+#pragma unroll 1
+        for (int i = lane; i < np; i += 32) {
+            const float2 f = part[turn][i];
+            Sums<TYPE> o;
+            o.z0 = f.x;
+            o.s = f.y;
+            m = max_nan(sum.z0, o.z0);
+            if (sum.z0 != m) sum.move_to(m, a.r.c2);
+            if (o.z0 != m) o.move_to(m, a.r.c2);
+            sum.s += o.s;
+        }
+        m = sum.z0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (sum.z0 != m) sum.move_to(m, a.r.c2);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
+        float logz, entropy;
+        normaliser<TYPE>(a.r, sum, logz, entropy);
+
+        Teacher te(te_base + turn * teacher_bytes(n), n);
+        const RowGrad c = step_grad<TYPE>(a, g_loss, logz, *te.used);
+        const Dense<TYPE> dense(c, sum.z0, sum.s, a.r.c2);
+        const Out<TYPE> out(a.grad, a.grad_row_stride, a.grad_col_stride, s.r, row);
+        const int64_t id = t < n ? te.id[t] : -1;
+        const bool here = id >= 0 && id >= s.first && id < s.first + (int64_t)s.nv * E;
+        T x = T();
+        float v = absent<TYPE>();
+        if (here) {
+            const int j = (int)((id - s.first) / E);
+            if (j >= s.lo && j < s.hi) {
+                x = reinterpret_cast<const T *>(hold)[id - s.first];
+                v = En::value(x);
+            } else {
+                x = s.r.p[id * s.r.cs];
+                v = row_value<TYPE>(s.r, id);
+            }
+        }
+        if (more && t < n) {
+            Teacher(te_base + (turn ^ 1) * teacher_bytes(n), n)
+                .settle<TYPE>(t, it, a.teacher, a.r, next.r, next_row);
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = 0; i < s.steps; ++i) {
+            grad_step<TYPE, G, MASK>(s, hold, i * kU * G, t, c, dense, out);
+        }
+        if (more)
+#pragma unroll 1
+            for (int i = 0; i < next.steps; ++i) copy_step<TYPE, MASK, G>(next, hold, i * kU * G, t);
+        if (here && v != absent<TYPE>()) {
+            float add = 0.f;
+            bool is_first = true;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i)
+                if (te.id[i] == id) {
+                    is_first = is_first && i >= t;
+                    add += te.q[i];
+                }
+            if (is_first) {
+                fix = to_entry<TYPE>(entry_grad<TYPE>(c, v, -add), x);
+                fix_at = out.p + id * out.cs;
+            }
+        }
+        // (small jobs, each on its own warp: the slowest warp of a cluster is
+        // what its barrier waits for)
+        if (warp == kWarps - 1 && rank == 0) {
+            const float loss = teacher_loss<TYPE>(n, a.r, te, logz);
+            if (lane == 0) {
+                a.loss[row] = loss;
+                a.logz[row] = logz;
+            }
+        }
+        if (warp == kWarps - 2 && more) Teacher(te_base + (turn ^ 1) * teacher_bytes(n), n).normalise(n);
+        if (!more) break;
+        row = next_row;
+        s = next;
+        turn ^= 1;
+    }
+    __syncthreads();
+    if (fix_at) *fix_at = fix;
+}
+
+template <int TYPE, bool MASK, bool UNIT>
+cudaError_t launch_step(const OutStep &a, bool warp_rows, cudaStream_t stream) {
+    size_t row_bytes = (size_t)a.r.seg_vecs * kOutVecBytes;
+    if (warp_rows) {
+        const int groups = kOutThreads / 32;
+        return launch_pdl(outcomes_step_warps<TYPE, MASK, UNIT>, dim3((unsigned)((a.r.rows + groups - 1) / groups)),
+                          dim3(kOutThreads), groups * row_bytes, stream, a);
+    }
+    auto *kernel = outcomes_step<TYPE, MASK, UNIT>;
+    row_bytes += 2 * teacher_bytes(a.teacher.count);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)row_bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.r.rows * a.r.segs + groups - 1) / groups));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(kStepThreads);
+    cfg.dynamicSmemBytes = row_bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)a.r.segs;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.r.segs;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.r.segs > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
-template <int TYPE, int G>
-cudaError_t step_mask(const OutStep &a, cudaStream_t stream) {
-    if constexpr (TYPE == TN_TYPE_C64) {
-        if (a.r.scale == 1.f)
-            return a.r.mask ? launch_step<TYPE, G, true, true>(a, stream) : launch_step<TYPE, G, false, true>(a, stream);
+    // as many clusters as run at once: each goes through its share of the rows
+    int64_t clusters = a.r.rows;
+    if (clusters * a.r.segs > 152) {
+        thread_local struct {
+            size_t bytes = 0;
+            int64_t segs = 0;
+            int most = 0;
+        } known;      // the query costs as much as the launch
+        if (known.bytes != row_bytes || known.segs != a.r.segs) {
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3((unsigned)a.r.segs);
+            e = cudaOccupancyMaxActiveClusters(&known.most, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+            known.bytes = row_bytes;
+            known.segs = a.r.segs;
+        }
+        if (known.most > 0 && clusters > known.most) clusters = known.most;
     }
-    return a.r.mask ? launch_step<TYPE, G, true, false>(a, stream) : launch_step<TYPE, G, false, false>(a, stream);
+    cfg.gridDim = dim3((unsigned)(clusters * a.r.segs));
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
 
 template <int TYPE>
 cudaError_t outcomes_step_of(const OutStep &a, bool warp_rows, cudaStream_t stream) {
-    return warp_rows ? step_mask<TYPE, 32>(a, stream) : step_mask<TYPE, kStepThreads>(a, stream);
+    if constexpr (TYPE == TN_TYPE_C64) {
+        if (a.r.scale == 1.f)
+            return a.r.mask ? launch_step<TYPE, true, true>(a, warp_rows, stream)
+                            : launch_step<TYPE, false, true>(a, warp_rows, stream);
+    }
+    return a.r.mask ? launch_step<TYPE, true, false>(a, warp_rows, stream)
+                    : launch_step<TYPE, false, false>(a, warp_rows, stream);
 }
 
 }  // namespace tn
