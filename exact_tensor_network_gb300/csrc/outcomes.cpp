@@ -20,11 +20,10 @@ OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned) {
     s.warp_rows = s.vecs <= kOutWarpVecs;
     s.segs = 1;
     s.seg_vecs = s.vecs;
-    s.flat = false;
     if (s.warp_rows) return s;
     // a CTA of less than two vectors a thread gains nothing
     const int64_t target = kOutTarget;
-    int64_t want = rows >= target ? 1 : (target + rows - 1) / rows;
+    int64_t want = rows >= target ? 1 : target / rows;      // one wave of CTAs
     const int64_t most = (s.vecs + 2 * kOutThreads - 1) / (2 * kOutThreads);
     if (want > most) want = most;
     const int64_t least = (s.vecs + kOutSegVecs - 1) / kOutSegVecs;
@@ -34,7 +33,6 @@ OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned) {
     if (sv > kOutSegVecs) sv = kOutSegVecs;
     s.seg_vecs = sv;
     s.segs = (s.vecs + sv - 1) / sv;
-    s.flat = s.segs > 1 && s.vecs <= kOutSegVecs;
     return s;
 }
 
@@ -62,22 +60,42 @@ tn_status cuda_fail(Outcomes &o, cudaError_t e, const char *what) {
 
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
 
-// What calls of up to max_rows rows need at most: rows that are split, their
-// segments, and bytes for the segments' lists or chunk maxima.
+// How the maxima of k alternatives lie.  Chunks are as large as leaves four
+// times as many of them as alternatives (a cut well inside) and at most 1024
+// vectors to read again, but no more of them in a segment than kOutKeys.
+struct Chunks {
+    int log;
+    int64_t seg_chunks;     // of a segment
+    bool tree;
+};
+
+Chunks chunks_of(const tn::OutSplit &s, int64_t k) {
+    Chunks c;
+    c.log = s.warp_rows ? 0 : tn::kOutChunkLog;
+    while (c.log > 0 && (s.vecs >> c.log < 4 * k || (int64_t)tn::out_most((int)k) << c.log > 1024) &&
+           s.seg_vecs <= (int64_t)tn::kOutKeys << (c.log - 1))
+        --c.log;
+    c.seg_chunks = (s.seg_vecs + (1 << c.log) - 1) >> c.log;
+    c.tree = c.seg_chunks * s.segs > tn::kOutTree;
+    return c;
+}
+
+// What calls of up to max_rows rows need at most: segments, and maxima.
 struct Need {
-    uint64_t tickets = 0, slots = 0, list_bytes = 0;
+    uint64_t slots = 0, maxima = 0, supers = 0;
 };
 
 void add_need(const Outcomes &o, int64_t rows, bool aligned, Need *n) {
     const tn::OutSplit s = tn::out_split(o.type, o.cols, rows, aligned);
-    if (s.segs == 1) return;
+    if (s.warp_rows || (s.segs == 1 && o.max_top == 0)) return;
     const uint64_t slots = (uint64_t)rows * s.segs;
-    const uint64_t bytes = o.max_top == 0 ? 0
-                           : s.flat       ? (uint64_t)rows * (tn::kOutKeys + 1) * sizeof(uint32_t)
-                                          : slots * o.max_top * sizeof(uint64_t);
-    if ((uint64_t)rows > n->tickets) n->tickets = rows;
     if (slots > n->slots) n->slots = slots;
-    if (bytes > n->list_bytes) n->list_bytes = bytes;
+    // fewer alternatives have larger chunks
+    for (int k = 1; k <= o.max_top; k *= 2) {
+        const Chunks c = chunks_of(s, k * 2 > o.max_top ? o.max_top : k);
+        if (slots * c.seg_chunks > n->maxima) n->maxima = slots * c.seg_chunks;
+        if (c.tree && slots * 33 > n->supers) n->supers = slots * 33;
+    }
 }
 
 Need workspace_need(const Outcomes &o) {
@@ -179,39 +197,30 @@ cudaError_t by_type(int32_t type, C64 c64, F32 f32, BF16 bf16, F16 f16, const Ar
 }
 
 tn_status forward(Outcomes &o, tn::OutForward &a, const tn::OutSplit &s, cudaStream_t stream) {
-    const int64_t E = tn::kOutVecBytes / tn::out_entry_bytes(o.type);
     const int64_t k = a.n_top;
+    a.finish = !s.warp_rows && (s.segs > 1 || k > 0);
     if (k > 0) {
-        // Chunks are as large as leaves four times as many of them as
-        // alternatives (a cut well inside) and at most 1024 vectors to read
-        // again, but no more of them than kOutKeys.
-        const int64_t nv = s.flat ? s.vecs : s.seg_vecs;
-        int log = s.warp_rows ? 0 : tn::kOutChunkLog;
-        while (log > 0 && (nv >> log < 4 * k || (int64_t)tn::out_most((int)k) << log > 1024) &&
-               nv <= (int64_t)tn::kOutKeys << (log - 1))
-            --log;
-        a.chunk_log = log;
-        int64_t words = (nv >> log) + 1;
-        if (s.segs > 1 && words < s.segs && s.segs <= 2 * tn::kOutKeys) words = s.segs;
+        const Chunks c = chunks_of(s, k);
+        a.chunk_log = c.log;
+        a.seg_chunks = static_cast<int32_t>(c.seg_chunks);
+        a.tree = c.tree;
+        int64_t words = c.seg_chunks * s.segs;
+        if (c.tree) words = s.segs <= tn::kOutTree ? s.segs : 4;
         words = (words + 3) / 4 * 4;
-        // room for the entries of k vectors or of k octets of list entries;
-        // as words, for the maxima of k chunks' vectors and of k lists' octets
-        int64_t cand = 8 * k, sub = k << log;
-        if (s.segs > 1 && sub < k * ((k + 7) / 8)) sub = k * ((k + 7) / 8);
-        if (cand < sub / 2 + 1) cand = sub / 2 + 1;
-        if (!s.warp_rows && cand < 128) cand = 128;
+        // room for the entries of k vectors; as words, for the maxima of k
+        // chunks' vectors and the 256 bins of the cut
+        int64_t cand = 8 * k;
+        if (cand < (k << c.log) / 2) cand = (k << c.log) / 2;
+        if (cand < 128) cand = 128;
         cand = (cand + 1) / 2 * 2;
         a.key_words = static_cast<int32_t>(words);
         a.cand_len = static_cast<int32_t>(cand);
         const int64_t kk = (k + 3) / 4 * 4, pp = (tn::out_most((int)k) + 3) / 4 * 4;
         a.group_bytes = static_cast<int32_t>(words * 4 + cand * 8 + kk * 8 + pp * 8 + 16);
     }
-    a.tickets = reinterpret_cast<uint32_t *>(o.ws + o.ticket_off);
     a.partials = reinterpret_cast<tn::OutPartial *>(o.ws + o.partial_off);
-    a.flat = s.flat;
-    a.row_chunks = static_cast<int32_t>(s.flat ? (s.vecs >> a.chunk_log) + 1 : 0);
-    if (s.flat) a.maxima = reinterpret_cast<uint32_t *>(o.ws + o.list_off);
-    else a.lists = reinterpret_cast<uint64_t *>(o.ws + o.list_off);
+    a.maxima = reinterpret_cast<uint32_t *>(o.ws + o.maxima_off);
+    a.supers = reinterpret_cast<uint32_t *>(o.ws + o.super_off);
     const cudaError_t e = by_type(o.type, tn::outcomes_forward_of<TN_TYPE_C64>, tn::outcomes_forward_of<TN_TYPE_F32>,
                                   tn::outcomes_forward_of<TN_TYPE_BF16>, tn::outcomes_forward_of<TN_TYPE_F16>, a,
                                   s.warp_rows, stream);
@@ -234,7 +243,6 @@ tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, 
     if (c > tn::kStepCluster) c = tn::kStepCluster;
     // few rows: more CTAs a row, of two vectors a thread at least
     while (c < tn::kStepCluster && rows * c < 2 * 152 && s.vecs >= 2 * (c + 1) * tn::kStepThreads) ++c;
-    s.flat = false;
     s.segs = c;
     s.seg_vecs = (s.vecs + c - 1) / c;
     if (s.seg_vecs * tn::kOutVecBytes + teachers > tn::kStepSliceMost) s.segs = 0;
@@ -292,10 +300,10 @@ tn_status tn_outcomes_create(int32_t type, int64_t cols, int64_t max_rows, int32
     o.max_top = max_top;
     o.scale = scale;
     const Need n = workspace_need(o);
-    o.ticket_off = 256;
-    o.partial_off = align(o.ticket_off + n.tickets * sizeof(uint32_t));
-    o.list_off = align(o.partial_off + n.slots * sizeof(tn::OutPartial));
-    o.ws_bytes = align(o.list_off + n.list_bytes);
+    o.partial_off = 256;
+    o.maxima_off = align(o.partial_off + n.slots * sizeof(tn::OutPartial));
+    o.super_off = align(o.maxima_off + n.maxima * sizeof(uint32_t));
+    o.ws_bytes = align(o.super_off + n.supers * sizeof(uint32_t));
     g_error[0] = 0;
     *out = h;
     return TN_OK;
@@ -318,7 +326,7 @@ tn_status tn_outcomes_set_workspace(tn_outcomes_t *h, void *dev_ptr, uint64_t by
         return fail(o.error, TN_ENOMEM, "workspace of %llu bytes is smaller than the %llu bytes needed",
                     (unsigned long long)bytes, (unsigned long long)o.ws_bytes);
     o.ws = nullptr;
-    // status word and tickets; the rest is written before it is read
+    // the status word; the rest is written before it is read
     cudaError_t e = cudaMemset(dev_ptr, 0, o.partial_off);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(o, e, "clearing the workspace");

@@ -505,7 +505,7 @@ struct Teacher {
     template <int TYPE, int G>
     __device__ __forceinline__ void read(const Group<G> &g, const OutTeacher &a, const OutRows &rows,
                                          const Row<TYPE> &r, int64_t row, bool values) {
-        constexpr int kPer = TN_OUTCOMES_MAX_IDS / G;
+        constexpr int kPer = G < TN_OUTCOMES_MAX_IDS ? TN_OUTCOMES_MAX_IDS / G : 1;
 #pragma unroll (kPer < 4 ? kPer : 4)
         for (int i = 0; i < kPer; ++i) {
             const int j = g.t + i * G;

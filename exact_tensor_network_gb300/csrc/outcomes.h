@@ -21,13 +21,14 @@ constexpr int kOutWarpVecs = 256;
 // vectors (what a warp reads in one step).
 constexpr int kOutKeys = 1024;
 constexpr int kOutChunkLog = 7;
+constexpr int kOutTree = 2048;          // maxima of a row that one CTA looks at; more form a tree
 constexpr int64_t kOutSegVecs = (int64_t)kOutKeys << 5;   // longest segment (512 KiB)
 
 constexpr int64_t kOutTarget = kOutCtas * 152;   // CTAs that fill the GPU
 
 // A first cut for k alternatives keeps up to this many chunks: a bisection
 // that may stop anywhere between k and here takes a few steps less.
-__host__ __device__ inline int out_most(int k) { return k + k / 4 + 2; }
+__host__ __device__ inline int out_most(int k) { return k + k / 8 + 2; }
 
 inline int out_entry_bytes(int32_t type) { return type == TN_TYPE_C64 ? 8 : type == TN_TYPE_F32 ? 4 : 2; }
 
@@ -37,7 +38,6 @@ struct OutSplit {
     int64_t seg_vecs;
     int64_t segs;
     bool warp_rows;     // one warp per row (segs is 1)
-    bool flat;          // split, but short enough for one CTA to hold all chunk maxima
 };
 
 struct OutRows {
@@ -79,15 +79,15 @@ struct OutForward {
     // distillation (count 0: scores)
     OutTeacher teacher;
     float *loss;
-    // split rows: a ticket per row (zero between calls), a partial and n_top
-    // candidates per segment; flat ones row_chunks maxima a row instead
-    uint32_t *tickets;
+    // A second kernel finishes the rows (segments, or alternatives of rows of a
+    // CTA): partials [rows][segs] and, for alternatives, maxima
+    // [rows][segs][seg_chunks] of chunks of 2^chunk_log vectors; with `tree`
+    // also supers [rows][segs][33], the maximum of a segment and those of its
+    // groups of 32 chunks.
     OutPartial *partials;
-    uint64_t *lists;
-    uint32_t *maxima;
-    int32_t flat, row_chunks;
-    int32_t chunk_log;  // maxima are those of 2^chunk_log vectors
-    // shared memory of a group for the alternatives (see Scratch)
+    uint32_t *maxima, *supers;
+    int32_t finish, tree, seg_chunks, chunk_log;
+    // shared memory of a row for the alternatives (see Scratch)
     int32_t key_words, cand_len, group_bytes;
 };
 
@@ -134,7 +134,7 @@ struct Outcomes {
     int32_t max_top = 0;
     float scale = 1.f;
     uint64_t ws_bytes = 0;
-    uint64_t ticket_off = 0, partial_off = 0, list_off = 0;
+    uint64_t partial_off = 0, maxima_off = 0, super_off = 0;
     char *ws = nullptr;
     char error[256] = {0};
 };

@@ -10,19 +10,22 @@
 // near the maximum will do, and a rescale on every new maximum would be a
 // divergent branch in most steps.
 //
-// Alternatives cost the pass one maximum per vector of 16 bytes, kept in
-// shared memory (per 32 vectors in segments of more than 16 KiB).  Ordered by
-// (value, lowest index first), the k best entries lie in the k best groups of
-// any division into contiguous index ranges ordered by (largest entry, lowest
-// range first): k groups that come before a group each hold an entry that
-// comes before all of that group's.  So the k best chunks, then the k best of
-// their vectors, then the k best of those vectors' entries are selected, and
-// only those chunks are read again (from L2).
+// Alternatives cost the pass one maximum per chunk of vectors (a vector is 16
+// bytes, a chunk what a warp reads in one step, or less of it for many
+// alternatives).  Ordered by (value, lowest index first), the k best entries
+// lie in the k best groups of any division into contiguous index ranges
+// ordered by (largest entry, lowest range first): k groups that come before a
+// group each hold an entry that comes before all of that group's.  So the k
+// best chunks are found, and only those are read again.  In segments of a long
+// row the maxima form a tree (of 32 chunks, of a segment), and the search goes
+// down it.
 //
-// A row of more than kOutSegVecs vectors, or one of a few rows, is cut into
-// segments of one CTA each; the last CTA of a row to finish (a ticket)
-// combines the segments' sums in segment order and selects among their lists
-// in the same way.
+// Rows of up to 4 KiB are a warp's.  Longer ones are one CTA's, or cut into
+// segments of one CTA each where there are few; a second, dependent kernel
+// then joins the segments in order and searches for the alternatives.  It is a
+// kernel of its own because the search is a few thousand instructions that
+// only the first of a row's warps would run: beside the streaming loop they
+// cost that loop its registers and its instruction cache.
 #pragma once
 
 #include "outcomes.cuh"
@@ -315,47 +318,92 @@ __device__ __forceinline__ Cut bisect(CountFrom count_from, uint32_t lo, uint32_
     return c;
 }
 
-// One warp: positions of the keys before a cut, of n keys in shared memory
-// (readable and zero up to a multiple of four), in ascending order.
-__device__ __noinline__ Cut warp_select(const uint32_t *keys, int n, int k, int most, uint32_t *out) {
-    const int lane = threadIdx.x % 32;
-    const uint4 *k4 = reinterpret_cast<const uint4 *>(keys);
-    const int n4 = (n + 3) / 4;
-    uint32_t mx = 0, nz = 0, mn = 0xffffffffu;     // mn: smallest but 0
-#pragma unroll 1
-    for (int i = lane; i < n4; i += 32) {
-        const uint4 q = k4[i];
-        mx = max(max(mx, q.x), max(max(q.y, q.z), q.w));
-        mn = min(min(mn, q.x - 1), min(min(q.y - 1, q.z - 1), q.w - 1));
-        nz += (q.x != 0) + (q.y != 0) + (q.z != 0) + (q.w != 0);
+// Positions of the keys before a cut, of n <= PER G keys in shared memory, in
+// ascending order.  Every thread keeps PER consecutive keys in registers; a
+// histogram of 256 bins over the range in question finds the bin with the k-th
+// key, which is the cut unless too many keys share it: then it is the next
+// range (a factor of 256 smaller each time; one or two are the rule).
+template <int PER, int G>
+__device__ __noinline__ Cut cut_keys(Group<G> g, const uint32_t *keys, int n, int k, int most, uint32_t *out,
+                                     uint32_t *bins) {
+    uint32_t key[PER];
+    const int i0 = g.t * PER;
+    uint32_t mx = 0, nz = 0, mn = 0xffffffffu;     // mn: smallest but 0, less 1
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        key[i] = i0 + i < n ? keys[i0 + i] : 0u;
+        mx = max(mx, key[i]);
+        mn = min(mn, key[i] - 1);
+        nz += key[i] != 0;
     }
-    // each lane has a key of at least the smallest of the lanes' largest
-    uint32_t low = __reduce_min_sync(0xffffffffu, mx);
-    mn = __reduce_min_sync(0xffffffffu, mn);
-    if (k > 32 || low == 0) low = mn + 1;
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    nz = __reduce_add_sync(0xffffffffu, nz);
-    const Cut c = bisect([=](uint32_t mid) {
-        uint32_t m = 0;
-    #pragma unroll 1
-    for (int i = lane; i < n4; i += 32) {
-            const uint4 q = k4[i];
-            m += (q.x >= mid) + (q.y >= mid) + (q.z >= mid) + (q.w >= mid);
+    mx = g.max(mx);
+    uint32_t lo = ~g.max(~mn) + 1, hi = mx, above = 0;
+    nz = g.sum(nz);
+    Cut c = {1u, 0xffffffffu, nz};
+    while (nz > (uint32_t)k) {
+        const int shift = max(0, 24 - __clz((hi - lo) | 1));
+        for (int i = g.t; i < 256; i += G) bins[i] = 0;
+        g.sync();
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (key[i] >= lo && key[i] <= hi) atomicAdd(bins + ((key[i] - lo) >> shift), 1u);
+        g.sync();
+        // every warp on its own: lane l has the bins 255 - 8 l .. 248 - 8 l
+        const uint4 b0 = reinterpret_cast<const uint4 *>(bins)[63 - 2 * g.lane];
+        const uint4 b1 = reinterpret_cast<const uint4 *>(bins)[62 - 2 * g.lane];
+        const uint32_t bin[8] = {b0.w, b0.z, b0.y, b0.x, b1.w, b1.z, b1.y, b1.x};
+        uint32_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine += bin[i];
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (g.lane >= o) upto += x;
         }
-        return __reduce_add_sync(0xffffffffu, m);
-    }, low, mx, nz, k, most);
-    uint32_t at = 0, tied = 0;
-    const uint32_t before = (1u << lane) - 1;
-#pragma unroll 1
-    for (int b = 0; b < n && at < c.count; b += 32) {
-        const uint32_t x = b + lane < n ? keys[b + lane] : 0u;
-        const uint32_t te = __ballot_sync(0xffffffffu, x == c.thr);
-        const bool take = x > c.thr || (x == c.thr && tied + __popc(te & before) < c.ties);
-        const uint32_t ms = __ballot_sync(0xffffffffu, take);
-        if (take) out[at + __popc(ms & before)] = b + lane;
-        at += __popc(ms);
-        tied += __popc(te);
+        const int src = __ffs(__ballot_sync(0xffffffffu, above + upto >= (uint32_t)k)) - 1;
+        uint32_t before = above + upto - mine, at = 0;
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (at == (uint32_t)i && before + bin[i] < (uint32_t)k) {
+                before += bin[i];
+                ++at;
+            }
+        uint32_t in = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) in = at == (uint32_t)i ? bin[i] : in;
+        at += 8 * g.lane;
+        before = __shfl_sync(0xffffffffu, before, src);
+        in = __shfl_sync(0xffffffffu, in, src);
+        at = 255 - __shfl_sync(0xffffffffu, at, src);
+        c.thr = lo + (at << shift);
+        if (before + in <= (uint32_t)most) {
+            c.count = before + in;
+            break;
+        }
+        if (shift == 0) {
+            c.ties = k - before;
+            c.count = k;
+            break;
+        }
+        g.sync();      // (all have read the bins)
+        above = before;
+        lo = c.thr;
+        hi = lo + min(hi - lo, (1u << shift) - 1);
     }
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        gt += key[i] > c.thr;
+        eq += key[i] == c.thr;
+    }
+    uint32_t pg = gt, pe = eq;
+    g.scan2(pg, pe);
+    uint32_t at = pg + min(pe, c.ties);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (key[i] > c.thr || (key[i] == c.thr && pe++ < c.ties)) out[at++] = i0 + i;
+    g.sync();
     return c;
 }
 
@@ -411,237 +459,6 @@ __device__ __forceinline__ int rank_of(const uint64_t *c, int n, uint64_t x) {
 #pragma unroll 4
     for (int j = 0; j < n; ++j) r += c[j] > x;
     return r;
-}
-
-// Shared memory of a group (all offsets multiples of 16 bytes).
-struct Scratch {
-    uint32_t *keys;       // maxima of vectors or of chunks
-    uint64_t *cand;       // candidates
-    uint64_t *best;       // the k best, in order
-    uint32_t *pos, *pos2; // out_most(k) positions each
-    uint32_t *n;          // number of candidates, of positions, threshold, number of vectors
-    __device__ __forceinline__ Scratch(unsigned char *base, const OutForward &a) {
-        const int kk = (a.n_top + 3) / 4 * 4, pp = (out_most(a.n_top) + 3) / 4 * 4;
-        keys = reinterpret_cast<uint32_t *>(base);
-        cand = reinterpret_cast<uint64_t *>(keys + a.key_words);
-        best = cand + a.cand_len;
-        pos = reinterpret_cast<uint32_t *>(best + kk);
-        pos2 = pos + pp;
-        n = pos2 + pp;
-    }
-    // First k (up to `most`) of keys[0 .. n) by the group's first warp, into
-    // pos; returns their number, `least` a lower bound of the k best entries.
-    template <int G>
-    __device__ __forceinline__ int cut(Group<G> &g, int nk, int k, int most, uint32_t &least) const {
-        if (g.t < 32) {
-            if (g.t < 4 && nk + g.t < (nk + 3) / 4 * 4) keys[nk + g.t] = 0;
-            __syncwarp();
-            const Cut c = warp_select(keys, nk, k, most, pos);
-            if (g.t == 0) {
-                n[0] = n[3] = 0;
-                n[1] = c.count;
-                n[2] = c.thr;
-            }
-        }
-        g.sync();
-        least = n[2];
-        return (int)n[1];
-    }
-    __device__ __forceinline__ void offer(uint32_t key, uint32_t index, int cand_len) const {
-        const uint32_t at = atomicAdd(n, 1u);
-        if (at < (uint32_t)cand_len) cand[at] = candidate(key, index);
-    }
-};
-
-// The k best of the candidates (0: none), in order, into sm.best.  Returns
-// their number.
-template <int G>
-__device__ __forceinline__ int rank_candidates(Group<G> &g, const Scratch &sm, int n, int k) {
-    uint32_t found = 0;
-#pragma unroll 1
-    for (int i = g.t; i < n; i += G) {
-        const uint64_t x = sm.cand[i];
-        if (x == 0) continue;
-        const int r = rank_of(sm.cand, n, x);
-        if (r < k) {
-            sm.best[r] = x;
-            ++found;
-        }
-    }
-    found = g.sum(found);
-    g.sync();
-    return (int)found;
-}
-
-// The k best entries of `nv` vectors from v0 on into sm.best, as candidates
-// with indices (vector - v0) E + entry, from the maxima in sm.keys, each that
-// of 2^log vectors.  Returns their number.
-template <int TYPE, bool MASK, int G>
-__device__ __noinline__ int best_entries(Group<G> g, const Scratch sm, const Row<TYPE> r, int64_t v0,
-                                         int nv, int k, int log, int cand_len) {
-    using En = Entry<TYPE>;
-    constexpr int E = En::E;
-    const int nk = (nv + (1 << log) - 1) >> log, low = (1 << log) - 1;
-    uint32_t least;
-    int nc = sm.cut(g, nk, k, log ? out_most(k) : k, least);
-    // vectors with an entry of at least `bar` (the lowest present value at the
-    // lowest), then those entries
-    const float bar = fmaxf(key_value(least), En::kReal ? -3.402823466e38f : 1.401298464e-45f);
-    uint32_t *list = reinterpret_cast<uint32_t *>(sm.cand + cand_len / 2);   // cand_len positions
-    const int work = nc << log;
-    const bool words = MASK && r.mask_words();
-#pragma unroll 1
-    for (int b = g.t; b < work; b += kU * G) {
-        int j[kU];
-        uint4 q[kU];
-        uint32_t odd = 0;       // vectors to be read entry by entry
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = b + u * G;
-            j[u] = i < work ? ((int)sm.pos[i >> log] << log) + (i & low) : nv;
-            const int64_t e0 = (v0 + j[u]) * E - r.head;
-            const bool in = j[u] < nv && r.inside(e0) && (!MASK || words);
-            q[u] = En::absent_vector();
-            if (in) q[u] = r.raw(e0);
-            if (MASK && in) En::blank(q[u], r.keep_word(e0));
-            if (!in && j[u] < nv) odd |= 1u << u;
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-            if (vector_max<TYPE>(q[u]) >= bar) {
-                const uint32_t at = atomicAdd(sm.n + 3, 1u);
-                if (at < (uint32_t)cand_len) list[at] = j[u];
-            }
-#pragma unroll 1
-        for (; odd; odd &= odd - 1) {
-            const int i = b + (__ffs(odd) - 1) * G;
-            const int jj = ((int)sm.pos[i >> log] << log) + (i & low);
-            const auto x = row_vector<TYPE>(r, v0 + jj);
-            float lm = absent<TYPE>();
-#pragma unroll
-            for (int e = 0; e < E; ++e) lm = fmaxf(lm, x.v[e]);
-            if (lm >= bar) {
-                const uint32_t at = atomicAdd(sm.n + 3, 1u);
-                if (at < (uint32_t)cand_len) list[at] = jj;
-            }
-        }
-    }
-    g.sync();
-    int nl = (int)sm.n[3];
-    if (nl <= cand_len) {
-#pragma unroll 1
-        for (int i = g.t; i < nl * E; i += G) {
-            const int jj = (int)list[i / E], e = i % E;
-            const int64_t at = (v0 + jj) * E - r.head + e;
-            const float v = at >= 0 && at < r.cols ? row_value<TYPE>(r, at) : absent<TYPE>();
-            if (v >= bar) sm.offer(order_key<TYPE>(v), jj * E + e, cand_len / 2);
-        }
-        g.sync();
-    }
-    int n = (int)sm.n[0];
-    if (nl > cand_len || n > cand_len / 2) {
-        // Too many entries at the cut (long runs of equal or of sorted
-        // entries): exactly k chunks, then the k best of their vectors, whose
-        // entries fit (log > 0 here: the entries of k vectors always do).
-        g.sync();
-        nc = sm.cut(g, nk, k, k, least);
-        uint32_t *sub = reinterpret_cast<uint32_t *>(sm.cand);
-#pragma unroll 1
-        for (int i = g.t; i < nc << log; i += G) {
-            const int j = ((int)sm.pos[i >> log] << log) + (i & low);
-            uint32_t key = 0;
-            if (j < nv) {
-                const auto x = row_vector<TYPE>(r, v0 + j);
-                float lm = absent<TYPE>();
-#pragma unroll
-                for (int e = 0; e < E; ++e) lm = fmaxf(lm, x.v[e]);
-                key = order_key<TYPE>(lm);
-            }
-            sub[i] = key;
-        }
-        g.sync();
-        const int nsel = select(g, [=](int i) { return sub[i]; }, nc << log, k, sm.pos2);
-#pragma unroll 1
-        for (int i = g.t; i < nsel; i += G) {
-            const uint32_t x = sm.pos2[i];
-            sm.pos2[i] = (sm.pos[x >> log] << log) + (x & low);
-        }
-        g.sync();
-#pragma unroll 1
-        for (int i = g.t; i < nsel * E; i += G) {
-            const int j = (int)sm.pos2[i / E], e = i % E;
-            const int64_t at = (v0 + j) * E - r.head + e;
-            const float v = at >= 0 && at < r.cols ? row_value<TYPE>(r, at) : absent<TYPE>();
-            const uint32_t key = order_key<TYPE>(v);
-            sm.cand[i] = key ? candidate(key, j * E + e) : 0;
-        }
-        g.sync();
-        n = nsel * E;
-    }
-    // (ends with a barrier: the caller's g may use any slot again)
-    return rank_candidates(g, sm, n, k);
-}
-
-// The k best of a split row among its segments' sorted lists, as candidates
-// with positions in the row's lists.
-template <int G>
-__device__ __noinline__ int join_lists(Group<G> g, const Scratch sm, const OutForward &a, int64_t row) {
-    const int k = a.n_top, segs = (int)a.r.segs;
-    const uint64_t *lists = a.lists + row * a.r.segs * k;
-    const auto key_at = [=](uint32_t i) { return (uint32_t)(__ldcg(lists + i) >> 32); };
-    int nc;
-    uint32_t least;
-    if (segs <= a.key_words) {
-#pragma unroll 1
-        for (int i = g.t; i < segs; i += G) sm.keys[i] = key_at(i * k);
-        g.sync();
-        nc = sm.cut(g, segs, k, k, least);
-    } else {
-        nc = select(g, [=](int i) { return key_at((uint32_t)i * k); }, segs, k, sm.pos);
-        uint32_t inv = 0;
-#pragma unroll 1
-        for (int i = g.t; i < nc; i += G) inv = max(inv, ~key_at(sm.pos[i] * k));
-        inv = g.max(inv);
-        least = nc ? ~inv : 1u;
-        if (g.t == 0) sm.n[0] = 0;
-        g.sync();
-    }
-#pragma unroll 1
-    for (int i = g.t; i < nc * 4; i += G)      // sorted: few go past their first entries
-#pragma unroll 1
-        for (int e = i & 3; e < k; e += 4) {
-            const uint32_t at = sm.pos[i >> 2] * k + e, key = key_at(at);
-            if (key < least) break;
-            sm.offer(key, at, a.cand_len);
-        }
-    g.sync();
-    int n = (int)sm.n[0];
-    if (n > a.cand_len) {
-        // the first of eight consecutive keys of a list is their largest
-        uint32_t *sub = reinterpret_cast<uint32_t *>(sm.cand);
-        const int oct = (k + 7) / 8;
-        g.sync();
-#pragma unroll 1
-        for (int i = g.t; i < nc * oct; i += G) sub[i] = key_at(sm.pos[i / oct] * k + i % oct * 8);
-        g.sync();
-        const int no = select(g, [=](int i) { return sub[i]; }, nc * oct, k, sm.pos2);
-#pragma unroll 1
-        for (int i = g.t; i < no; i += G) {
-            const uint32_t x = sm.pos2[i];
-            sm.pos2[i] = sm.pos[x / oct] * k + x % oct * 8;
-        }
-        g.sync();
-#pragma unroll 1
-        for (int i = g.t; i < no * 8; i += G) {
-            const uint32_t first = sm.pos2[i / 8], at = first + i % 8;
-            // the last octet of a list may be short
-            const uint32_t key = at / k == first / k ? key_at(at) : 0u;
-            sm.cand[i] = key ? candidate(key, at) : 0;
-        }
-        g.sync();
-        n = no * 8;
-    }
-    return rank_candidates(g, sm, n, k);
 }
 
 // ---- the end of a row -------------------------------------------------------
@@ -720,7 +537,206 @@ __device__ __forceinline__ void normaliser(const OutRows &r, const Sums<TYPE> &a
     }
 }
 
-// ---- the kernel -------------------------------------------------------------
+// Shared memory of a group (all offsets multiples of 16 bytes).
+struct Scratch {
+    uint32_t *keys;       // maxima (key_words)
+    uint64_t *cand;       // candidates (cand_len)
+    uint64_t *best;       // the k best, in order
+    uint32_t *pos, *pos2; // out_most(k) chunks each
+    uint32_t *n;          // counters
+    __device__ __forceinline__ Scratch(unsigned char *base, const OutForward &a) {
+        const int kk = (a.n_top + 3) / 4 * 4, pp = (out_most(a.n_top) + 3) / 4 * 4;
+        keys = reinterpret_cast<uint32_t *>(base);
+        cand = reinterpret_cast<uint64_t *>(keys + a.key_words);
+        best = cand + a.cand_len;
+        pos = reinterpret_cast<uint32_t *>(best + kk);
+        pos2 = pos + pp;
+        n = pos2 + pp;
+    }
+    // First k (up to `most`) of keys[0 .. nk) into pos; returns their number,
+    // `least` a lower bound of the k best entries.
+    template <int G>
+    __device__ __forceinline__ int cut(Group<G> &g, int nk, int k, int most, uint32_t &least) const {
+        uint32_t *bins = reinterpret_cast<uint32_t *>(cand);
+        if (G > 32 && nk <= 256) {      // few enough for one warp, without barriers
+            if (g.t < 32) {
+                const Cut c = cut_keys<8>(Group<32>(nullptr), keys, nk, k, most, pos, bins);
+                if (g.t == 0) {
+                    n[1] = c.count;
+                    n[2] = c.thr;
+                }
+            }
+            g.sync();
+            least = n[2];
+            return (int)n[1];
+        }
+        const Cut c = cut_keys<G == 32 ? kOutWarpVecs / 32 : kOutTree / G>(g, keys, nk, k, most, pos, bins);
+        least = c.thr;
+        return (int)c.count;
+    }
+    __device__ __forceinline__ void offer(uint32_t key, uint32_t index, int len) const {
+        const uint32_t at = atomicAdd(n, 1u);
+        if (at < (uint32_t)len) cand[at] = candidate(key, index);
+    }
+};
+
+// The k best of the candidates (0: none), in order, into sm.best.  Returns
+// their number.
+template <int G>
+__device__ __forceinline__ int rank_candidates(Group<G> &g, const Scratch &sm, int n, int k) {
+    uint32_t found = 0;
+#pragma unroll 1
+    for (int i = g.t; i < n; i += G) {
+        const uint64_t x = sm.cand[i];
+        if (x == 0) continue;
+        const int r = rank_of(sm.cand, n, x);
+        if (r < k) {
+            sm.best[r] = x;
+            ++found;
+        }
+    }
+    found = g.sum(found);
+    g.sync();
+    return (int)found;
+}
+
+// largest order value of vector j
+template <int TYPE>
+__device__ __forceinline__ float row_vector_max(const Row<TYPE> &r, int64_t j) {
+    const auto x = row_vector<TYPE>(r, j);
+    float lm = absent<TYPE>();
+#pragma unroll
+    for (int e = 0; e < Entry<TYPE>::E; ++e) lm = fmaxf(lm, x.v[e]);
+    return lm;
+}
+
+// The k best entries of a row into sm.best, from the nc chunks of 2^log
+// vectors in sm.pos (ascending; `least` a lower bound of the k best), as
+// candidates whose index is ((place in sm.pos << log) + vector) E + entry.
+// Returns their number, or -1: too many entries at the bound.
+template <int TYPE, bool MASK, int G>
+__device__ __forceinline__ int best_of_chunks(Group<G> &g, const Scratch &sm, const Row<TYPE> &r, int nc,
+                                              uint32_t least, int k, int log, int cand_len) {
+    using En = Entry<TYPE>;
+    constexpr int E = En::E;
+    constexpr int kAgain = G == 32 ? 2 : 8;     // vectors in flight per thread
+    const int low = (1 << log) - 1, work = nc << log;
+    const int64_t all = (r.head + r.cols + E - 1) / E;
+    // vectors with an entry of at least `bar` (the lowest present value at the
+    // lowest), then those entries
+    const float bar = fmaxf(key_value(least), En::kReal ? -3.402823466e38f : 1.401298464e-45f);
+    uint32_t *list = reinterpret_cast<uint32_t *>(sm.cand + cand_len / 2);   // cand_len places
+    const bool words = !MASK || r.mask_words();
+    if (g.t == 0) sm.n[0] = sm.n[3] = 0;
+    g.sync();
+    const auto keep_vector = [&](int i) {
+        const uint32_t at = atomicAdd(sm.n + 3, 1u);
+        if (at < (uint32_t)cand_len) list[at] = i;
+    };
+#pragma unroll 1
+    for (int b = g.t; b - g.t < work; b += kAgain * G) {
+        uint4 q[kAgain];
+        uint32_t odd = 0;       // vectors to be read entry by entry
+#pragma unroll
+        for (int u = 0; u < kAgain; ++u) {
+            const int i = b + u * G;
+            q[u] = En::absent_vector();
+            if (i >= work) continue;
+            const int64_t j = ((int64_t)sm.pos[i >> log] << log) + (i & low);
+            if (j >= all) continue;
+            const int64_t e0 = j * E - r.head;
+            if (words && r.inside(e0)) {
+                q[u] = r.raw(e0);
+                if (MASK) En::blank(q[u], r.keep_word(e0));
+            } else {
+                odd |= 1u << u;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAgain; ++u) {
+            if (b - g.t + u * G >= work) break;
+            if (vector_max<TYPE>(q[u]) >= bar) keep_vector(b + u * G);
+        }
+#pragma unroll 1
+        for (; odd; odd &= odd - 1) {
+            const int i = b + (__ffs(odd) - 1) * G;
+            if (row_vector_max<TYPE>(r, ((int64_t)sm.pos[i >> log] << log) + (i & low)) >= bar) keep_vector(i);
+        }
+    }
+    g.sync();
+    const int nl = (int)sm.n[3];
+    if (nl > cand_len) return -1;
+#pragma unroll 1
+    for (int i = g.t; i < nl * E; i += G) {
+        const int x = (int)list[i / E], e = i % E;
+        const int64_t at = (((int64_t)sm.pos[x >> log] << log) + (x & low)) * E - r.head + e;
+        const float v = at >= 0 && at < r.cols ? row_value<TYPE>(r, at) : absent<TYPE>();
+        if (v >= bar) sm.offer(order_key<TYPE>(v), x * E + e, cand_len / 2);
+    }
+    g.sync();
+    const int n = (int)sm.n[0];
+    if (n > cand_len / 2) return -1;
+    return rank_candidates(g, sm, n, k);
+}
+
+// The same from exactly the k best chunks, whatever lies at the bound (long
+// runs of equal or of sorted entries): the k best of their vectors, then of
+// those vectors' entries.
+template <int TYPE, int G>
+__device__ __noinline__ int best_of_exact_chunks(Group<G> g, const Scratch sm, const Row<TYPE> r, int nc, int k,
+                                                 int log) {
+    using En = Entry<TYPE>;
+    constexpr int E = En::E;
+    const int low = (1 << log) - 1;
+    const int64_t all = (r.head + r.cols + E - 1) / E;
+    uint32_t *sub = reinterpret_cast<uint32_t *>(sm.cand);
+    g.sync();
+#pragma unroll 1
+    for (int i = g.t; i < nc << log; i += G) {
+        const int64_t j = ((int64_t)sm.pos[i >> log] << log) + (i & low);
+        sub[i] = j < all ? order_key<TYPE>(row_vector_max<TYPE>(r, j)) : 0u;
+    }
+    g.sync();
+    const int nv = select(g, [=](int i) { return sub[i]; }, nc << log, k, sm.pos2);
+#pragma unroll 1
+    for (int i = g.t; i < nv * E; i += G) {
+        const int x = (int)sm.pos2[i / E], e = i % E;
+        const int64_t at = (((int64_t)sm.pos[x >> log] << log) + (x & low)) * E - r.head + e;
+        const float v = at >= 0 && at < r.cols ? row_value<TYPE>(r, at) : absent<TYPE>();
+        const uint32_t key = order_key<TYPE>(v);
+        sm.cand[i] = key ? candidate(key, x * E + e) : 0;
+    }
+    g.sync();
+    return rank_candidates(g, sm, nv * E, k);
+}
+
+// The k best entries of a row whose nk chunk maxima are in sm.keys.
+template <int TYPE, bool MASK, int G>
+__device__ __forceinline__ int best_entries(Group<G> &g, const Scratch &sm, const Row<TYPE> &r, int nk, int k,
+                                            int log, int cand_len) {
+    uint32_t least;
+    const int nc = sm.cut(g, nk, k, log ? out_most(k) : k, least);
+    int found = best_of_chunks<TYPE, MASK>(g, sm, r, nc, least, k, log, cand_len);
+    if (found < 0) {
+        g.sync();
+        const int exact = sm.cut(g, nk, k, k, least);
+        found = best_of_exact_chunks<TYPE>(g, sm, r, exact, k, log);
+    }
+    return found;
+}
+
+// Alternative i of the row, from sm.best.
+template <int TYPE>
+__device__ __forceinline__ void put_alternative(const OutForward &a, const Row<TYPE> &r, const Scratch &sm, int i,
+                                                int log, float logz, int64_t *ids, float *lps) {
+    constexpr int E = Entry<TYPE>::E;
+    const uint64_t c = sm.best[i];
+    const uint32_t x = 0xffffffffu - (uint32_t)c, j = x / E;
+    ids[i] = (((int64_t)sm.pos[j >> log] << log) + (j & ((1 << log) - 1))) * E + x % E - r.head;
+    lps[i] = log_prob<TYPE>(a.r, key_value((uint32_t)(c >> 32)), logz);
+}
+
+// ---- the kernels ------------------------------------------------------------
 
 template <int TYPE, int G, bool MASK, bool ENT, bool UNIT>
 __global__ void __launch_bounds__(kOutThreads, G == 32 ? 6 : kOutCtas)
@@ -731,7 +747,6 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     constexpr float kInf = __builtin_huge_valf();
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint32_t red[4 * kOutThreads / 32];
-    __shared__ bool last;
     constexpr int kTeacher = ENT ? 16 : TN_OUTCOMES_MAX_IDS * 20 + 16;
     __shared__ __align__(16) unsigned char teachers[kGroups * kTeacher];
     Teacher te(teachers + threadIdx.x / G * kTeacher, ENT ? 0 : a.teacher.count);
@@ -740,7 +755,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     const uint32_t item = blockIdx.x * kGroups + threadIdx.x / G, segs = (uint32_t)a.r.segs;
     const int64_t row = G == 32 ? item : item / segs;
     const int64_t seg = G == 32 ? 0 : item % segs;
-    const Scratch sm(smem + (size_t)(threadIdx.x / G) * a.group_bytes, a);
+    const Scratch sm(smem + (G == 32 ? (size_t)(threadIdx.x / G) * a.group_bytes : 0), a);
     pdl_wait();
     if (G == 32 && row >= a.r.rows) return;
 
@@ -864,143 +879,282 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     Sums<TYPE> sum = st.done(a.r.c2);
     combine(g, sum, a.r.c2);     // its barriers also publish the maxima
     g.sync();
-    bool valid = sum.s < kInf;
-
-    float logz, entropy;
-    int found = 0;
-    bool lists = false;
-    if (G > 32 && a.r.segs > 1) {
-        lists = !a.flat;
-        // leave the segment's part in the workspace; the last one joins
-        const int64_t slot0 = row * a.r.segs;
-        if (k > 0 && lists) {
-            if (valid) found = best_entries<TYPE, MASK>(g, sm, r, v0, nv, k, log, a.cand_len);
-            for (int i = g.t; i < k; i += G) a.lists[(slot0 + seg) * k + i] = i < found ? sm.best[i] : 0;
-        } else if (k > 0) {
-            uint32_t *to = a.maxima + row * a.row_chunks + (v0 >> log);
-            for (int i = g.t; i < (nv + (1 << log) - 1) >> log; i += G) to[i] = sm.keys[i];
-        }
+    if (G > 32 && a.finish) {
+        // leave the segment's part for the second kernel
         if (g.t == 0) {
             OutPartial p;
             p.z0 = sum.z0;
             p.s = sum.s;
             p.t = sum.t;
             p.pad = 0;
-            a.partials[slot0 + seg] = p;
+            a.partials[row * segs + seg] = p;
         }
-        __threadfence();
-        __syncthreads();
-        if (g.t == 0) last = atomicAdd(a.tickets + row, 1u) == (uint32_t)a.r.segs - 1;
-        __syncthreads();
-        if (!last) return;
-        __threadfence();
-        if (g.t == 0) a.tickets[row] = 0;    // ready for the next call
-        if (k > 0 && !lists)
-            for (int i = g.t; i < (int)((all + (1 << log) - 1) >> log); i += G)
-                sm.keys[i] = __ldcg(a.maxima + row * a.row_chunks + i);
-        sum = Sums<TYPE>();
-        for (int i = g.t; i < (int)segs; i += G) {
-            const float4 f = __ldcg(reinterpret_cast<const float4 *>(a.partials + slot0 + i));
-            Sums<TYPE> o;
-            o.z0 = f.x;
-            o.s = f.y;
-            o.t = f.z;
-            const float z = max_nan(sum.z0, o.z0);
-            if (sum.z0 != z) sum.move_to(z, a.r.c2);
-            if (o.z0 != z) o.move_to(z, a.r.c2);
-            sum.s += o.s;
-            sum.t += o.t;
+        if (ENT && k > 0) {
+            const int nc = (nv + (1 << log) - 1) >> log;
+            uint32_t *to = a.maxima + (row * segs + seg) * a.seg_chunks;
+            for (int i = g.t; i < a.seg_chunks; i += G) to[i] = i < nc ? sm.keys[i] : 0u;
+            if (a.tree) {
+                // the maxima of 32 chunks, and of the segment
+                uint32_t *up = a.supers + (row * segs + seg) * 33;
+                uint32_t top = 0;
+                for (int i = g.warp; i < 32; i += Group<G>::kWarps) {
+                    const int at = i * 32 + g.lane;
+                    const uint32_t x = __reduce_max_sync(0xffffffffu, at < nc ? sm.keys[at] : 0u);
+                    if (g.lane == 0) up[1 + i] = x;
+                    top = max(top, x);
+                }
+                top = g.max(top);
+                if (g.t == 0) up[0] = top;
+            }
         }
-        combine(g, sum, a.r.c2);
-        g.sync();
-        valid = sum.s < kInf;
+        return;
     }
+    float logz, entropy;
     normaliser<TYPE>(a.r, sum, logz, entropy);
     finish_row<TYPE, ENT>(g, a, r, te, row, logz, entropy);
-    if constexpr (!ENT) return;
-    if (k == 0) return;
-    int64_t *ids = a.top_ids + row * k;
-    float *lps = a.top_logp + row * k;
-    found = 0;
-    if (G == 32 && nv <= 32) {
-        // one vector a lane: take the largest k times
-        const auto x = row_vector<TYPE>(r, g.lane);
-        uint32_t key[E];
+    if constexpr (ENT && G == 32) {
+        if (k == 0) return;
+        const bool valid = sum.s < kInf;
+        int64_t *ids = a.top_ids + row * k;
+        float *lps = a.top_logp + row * k;
+        int found = 0;
+        if (nv <= 32) {
+            // one vector a lane: take the largest k times
+            const auto x = row_vector<TYPE>(r, g.lane);
+            uint32_t key[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) key[i] = valid ? order_key<TYPE>(x.v[i]) : 0u;
-        for (; found < k; ++found) {
-            uint32_t m = key[0];
+            for (int i = 0; i < E; ++i) key[i] = valid ? order_key<TYPE>(x.v[i]) : 0u;
+            for (; found < k; ++found) {
+                uint32_t m = key[0];
 #pragma unroll
-            for (int i = 1; i < E; ++i) m = max(m, key[i]);
-            const uint32_t mx = __reduce_max_sync(0xffffffffu, m);
-            if (mx == 0) break;
-            const int src = __ffs(__ballot_sync(0xffffffffu, m == mx)) - 1;
-            if (g.lane == src) {
-                int at = E;
+                for (int i = 1; i < E; ++i) m = max(m, key[i]);
+                const uint32_t mx = __reduce_max_sync(0xffffffffu, m);
+                if (mx == 0) break;
+                const int src = __ffs(__ballot_sync(0xffffffffu, m == mx)) - 1;
+                if (g.lane == src) {
+                    int at = E;
 #pragma unroll
-                for (int i = E - 1; i >= 0; --i) at = key[i] == mx ? i : at;
+                    for (int i = E - 1; i >= 0; --i) at = key[i] == mx ? i : at;
 #pragma unroll
-                for (int i = 0; i < E; ++i) key[i] = i == at ? 0u : key[i];
-                ids[found] = g.lane * E + at - r.head;
-                lps[found] = log_prob<TYPE>(a.r, key_value(mx), logz);
+                    for (int i = 0; i < E; ++i) key[i] = i == at ? 0u : key[i];
+                    ids[found] = g.lane * E + at - r.head;
+                    lps[found] = log_prob<TYPE>(a.r, key_value(mx), logz);
+                }
             }
+        } else if (valid) {
+            found = best_entries<TYPE, MASK>(g, sm, r, nv, k, 0, a.cand_len);
+            for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, 0, logz, ids, lps);
         }
-    } else if (valid) {
-        if (lists) found = join_lists(g, sm, a, row);
-        else found = best_entries<TYPE, MASK>(g, sm, r, 0, (int)all, k, log, a.cand_len);
-        for (int i = g.t; i < found; i += G) {
-            const uint64_t x = sm.best[i];
-            const uint32_t at = 0xffffffffu - (uint32_t)x;
-            int64_t id = at;
-            if (lists) {     // a position in the row's lists
-                const uint32_t local = 0xffffffffu - (uint32_t)__ldcg(a.lists + row * a.r.segs * k + at);
-                id = (int64_t)(at / (uint32_t)k) * a.r.seg_vecs * E + local;
-            }
-            ids[i] = id - r.head;
-            lps[i] = log_prob<TYPE>(a.r, key_value((uint32_t)(x >> 32)), logz);
+        for (int i = found + g.t; i < k; i += G) {
+            ids[i] = -1;
+            lps[i] = valid ? -kInf : logz;
         }
-    }
-    for (int i = found + g.t; i < k; i += G) {
-        ids[i] = -1;
-        lps[i] = valid ? -kInf : logz;
     }
 }
 
-template <int TYPE, int G, bool MASK, bool ENT, bool UNIT>
-cudaError_t launch_forward(const OutForward &a, cudaStream_t stream) {
-    const int64_t items = a.r.rows * a.r.segs;
-    const int groups = kOutThreads / G;
-    const size_t smem = (size_t)groups * a.group_bytes;
-    auto *kernel = outcomes_forward<TYPE, G, MASK, ENT, UNIT>;
+// The chunks to read again of a row with a tree of maxima: the first k
+// segments (or a few more), their groups of 32 chunks with a maximum of at
+// least the cut's, those groups' chunks likewise; into sm.pos in ascending
+// order.  Returns their number, or -1: more than there is room for.
+template <int G>
+__device__ __noinline__ int chunks_of_tree(Group<G> g, const Scratch sm, const OutForward &a, int64_t row,
+                                           uint32_t &least) {
+    const int k = a.n_top, segs = (int)a.r.segs, room = out_most(k), len = 2 * a.cand_len;
+    const uint32_t *supers = a.supers + row * segs * 33;
+    const uint32_t *maxima = a.maxima + row * segs * a.seg_chunks;
+    int nc;
+    if (segs <= a.key_words) {
+#pragma unroll 4
+        for (int i = g.t; i < segs; i += G) sm.keys[i] = __ldcg(supers + (int64_t)i * 33);
+        g.sync();
+        nc = sm.cut(g, segs, k, room, least);
+    } else {
+        nc = select(g, [=](int i) { return __ldcg(supers + (int64_t)i * 33); }, segs, k, sm.pos);
+        uint32_t inv = 0;
+#pragma unroll 1
+        for (int i = g.t; i < nc; i += G) inv = max(inv, ~__ldcg(supers + (int64_t)sm.pos[i] * 33));
+        inv = g.max(inv);
+        least = nc ? ~inv : 1u;
+    }
+    // groups of 32 chunks, as (place in sm.pos) 32 + group
+    uint32_t *list = reinterpret_cast<uint32_t *>(sm.cand);
+    g.sync();
+    if (g.t == 0) sm.n[0] = sm.n[3] = 0;
+    g.sync();
+#pragma unroll 4
+    for (int i = g.t; i < nc * 32; i += G)
+        if (__ldcg(supers + (int64_t)sm.pos[i >> 5] * 33 + 1 + (i & 31)) >= least) {
+            const uint32_t at = atomicAdd(sm.n + 3, 1u);
+            if (at < (uint32_t)len) list[at] = i;
+        }
+    g.sync();
+    const int ng = (int)sm.n[3];
+    if (ng > len) return -1;
+#pragma unroll 4
+    for (int i = g.t; i < ng * 32; i += G) {
+        const uint32_t x = list[i >> 5], c = (x & 31) * 32 + (i & 31);
+        const uint32_t at = sm.pos[x >> 5] * a.seg_chunks + c;
+        if (c < (uint32_t)a.seg_chunks && __ldcg(maxima + at) >= least) {
+            const uint32_t w = atomicAdd(sm.n, 1u);
+            if (w < (uint32_t)room) sm.pos2[w] = at;
+        }
+    }
+    g.sync();
+    const int n = (int)sm.n[0];
+    if (n > room) return -1;
+#pragma unroll 1
+    for (int i = g.t; i < n; i += G) {
+        const uint32_t x = sm.pos2[i];
+        int at = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) at += sm.pos2[j] < x;
+        sm.pos[at] = x;
+    }
+    g.sync();
+    return n;
+}
+
+// Exactly the k best chunks of such a row.
+template <int G>
+__device__ __noinline__ int exact_chunks_of_tree(Group<G> g, const Scratch sm, const OutForward &a, int64_t row) {
+    const int k = a.n_top, segs = (int)a.r.segs, chunks = a.seg_chunks;
+    const uint32_t *supers = a.supers + row * segs * 33;
+    const uint32_t *maxima = a.maxima + row * segs * chunks;
+    const uint32_t *pos = sm.pos;
+    g.sync();
+    const int ns = select(g, [=](int i) { return __ldcg(supers + (int64_t)i * 33); }, segs, k, sm.pos);
+    const int nc = select(g, [=](int i) { return __ldcg(maxima + (int64_t)pos[i / chunks] * chunks + i % chunks); },
+                          ns * chunks, k, sm.pos2);
+#pragma unroll 1
+    for (int i = g.t; i < nc; i += G) {
+        const int x = (int)sm.pos2[i];
+        sm.pos2[i] = pos[x / chunks] * chunks + x % chunks;
+    }
+    g.sync();
+#pragma unroll 1
+    for (int i = g.t; i < nc; i += G) sm.pos[i] = sm.pos2[i];
+    g.sync();
+    return nc;
+}
+
+// What follows the streaming kernel for rows in segments or with
+// alternatives: one CTA a row joins the segments' sums in order and searches.
+template <int TYPE, int G, bool MASK, bool ENT>
+__global__ void __launch_bounds__(G, G == 128 ? 6 : 1) outcomes_finish(const __grid_constant__ OutForward a) {
+    using En = Entry<TYPE>;
+    constexpr int E = En::E;
+    constexpr float kInf = __builtin_huge_valf();
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ uint32_t red[4 * G / 32];
+    constexpr int kTeacher = ENT ? 16 : TN_OUTCOMES_MAX_IDS * 20 + 16;
+    __shared__ __align__(16) unsigned char teacher[kTeacher];
+    Teacher te(teacher, ENT ? 0 : a.teacher.count);
+    pdl_trigger();
+    Group<G> g(red);
+    const int64_t row = blockIdx.x;
+    const int segs = (int)a.r.segs, k = ENT ? a.n_top : 0, log = a.chunk_log;
+    const Scratch sm(smem, a);
+    const Row<TYPE> r(a.r, row);
+    pdl_wait();
+    // (the workspace is read past the L1 cache: this grid may have started while
+    // the previous call's was still filling it)
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (g.t < segs) f = __ldcg(reinterpret_cast<const float4 *>(a.partials + row * segs + g.t));
+    const int nk = segs * a.seg_chunks;
+    if (ENT && k > 0 && !a.tree) {
+#pragma unroll 4
+        for (int i = g.t; i < nk; i += G) sm.keys[i] = __ldcg(a.maxima + row * nk + i);
+    }
+    if (!ENT) te.read(g, a.teacher, a.r, r, row, true);
+    Sums<TYPE> sum;
+#pragma unroll 1
+    for (int i = g.t; i < segs; i += G) {
+        Sums<TYPE> o;
+        o.z0 = f.x;
+        o.s = f.y;
+        o.t = f.z;
+        const float z = max_nan(sum.z0, o.z0);
+        if (sum.z0 != z) sum.move_to(z, a.r.c2);
+        if (o.z0 != z) o.move_to(z, a.r.c2);
+        sum.s += o.s;
+        sum.t += o.t;
+        if (i + G < segs) f = __ldcg(reinterpret_cast<const float4 *>(a.partials + row * segs + i + G));
+    }
+    combine(g, sum, a.r.c2);
+    g.sync();
+    const bool valid = sum.s < kInf;
+    float logz, entropy;
+    normaliser<TYPE>(a.r, sum, logz, entropy);
+    finish_row<TYPE, ENT>(g, a, r, te, row, logz, entropy);
+    if constexpr (ENT) {
+        if (k == 0) return;
+        int64_t *ids = a.top_ids + row * k;
+        float *lps = a.top_logp + row * k;
+        int found = 0;
+        if (valid && !a.tree) {
+            found = best_entries<TYPE, MASK>(g, sm, r, nk, k, log, a.cand_len);
+        } else if (valid) {
+            uint32_t least;
+            const int nc = chunks_of_tree(g, sm, a, row, least);
+            found = nc < 0 ? -1 : best_of_chunks<TYPE, MASK>(g, sm, r, nc, least, k, log, a.cand_len);
+            if (found < 0) {
+                const int exact = exact_chunks_of_tree(g, sm, a, row);
+                found = best_of_exact_chunks<TYPE>(g, sm, r, exact, k, log);
+            }
+        }
+        for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, log, logz, ids, lps);
+        for (int i = found + g.t; i < k; i += G) {
+            ids[i] = -1;
+            lps[i] = valid ? -kInf : logz;
+        }
+    }
+}
+
+template <class Kernel>
+cudaError_t launch_rows(Kernel *kernel, int64_t ctas, int threads, size_t smem, const OutForward &a,
+                        cudaStream_t stream) {
     if (smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kernel, dim3((unsigned)((items + groups - 1) / groups)), dim3(kOutThreads), smem,
-                      stream, a);
+    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(threads), smem, stream, a);
 }
 
-template <int TYPE, int G, bool ENT, bool UNIT>
-cudaError_t forward_mask(const OutForward &a, cudaStream_t stream) {
-    return a.r.mask ? launch_forward<TYPE, G, true, ENT, UNIT>(a, stream)
-                    : launch_forward<TYPE, G, false, ENT, UNIT>(a, stream);
-}
-
-template <int TYPE, int G>
-cudaError_t forward_ent(const OutForward &a, cudaStream_t stream) {
-    const bool ent = a.teacher.count == 0;
-    if constexpr (TYPE == TN_TYPE_C64) {
-        if (a.r.scale == 1.f)
-            return ent ? forward_mask<TYPE, G, true, true>(a, stream) : forward_mask<TYPE, G, false, true>(a, stream);
+template <int TYPE, bool MASK, bool ENT, bool UNIT>
+cudaError_t launch_forward(const OutForward &a, bool warp_rows, cudaStream_t stream) {
+    if (warp_rows) {
+        const int groups = kOutThreads / 32;
+        return launch_rows(outcomes_forward<TYPE, 32, MASK, ENT, UNIT>, (a.r.rows + groups - 1) / groups, kOutThreads,
+                           (size_t)groups * a.group_bytes, a, stream);
     }
-    return ent ? forward_mask<TYPE, G, true, false>(a, stream) : forward_mask<TYPE, G, false, false>(a, stream);
+    const size_t keys = ENT && a.n_top > 0 ? (size_t)(a.seg_chunks + 3) / 4 * 16 : 0;
+    cudaError_t e = launch_rows(outcomes_forward<TYPE, kOutThreads, MASK, ENT, UNIT>, a.r.rows * a.r.segs, kOutThreads,
+                                keys, a, stream);
+    if (e != cudaSuccess || !a.finish) return e;
+    // few rows: as many threads as help one
+    if (a.r.rows >= kOutTarget / 4)
+        return launch_rows(outcomes_finish<TYPE, 128, MASK, ENT>, a.r.rows, 128, a.group_bytes, a, stream);
+    return launch_rows(outcomes_finish<TYPE, 512, MASK, ENT>, a.r.rows, 512, a.group_bytes, a, stream);
+}
+
+template <int TYPE, bool ENT, bool UNIT>
+cudaError_t forward_mask(const OutForward &a, bool warp_rows, cudaStream_t stream) {
+    return a.r.mask ? launch_forward<TYPE, true, ENT, UNIT>(a, warp_rows, stream)
+                    : launch_forward<TYPE, false, ENT, UNIT>(a, warp_rows, stream);
 }
 
 }  // namespace
 
 template <int TYPE>
 cudaError_t outcomes_forward_of(const OutForward &a, bool warp_rows, cudaStream_t stream) {
-    return warp_rows ? forward_ent<TYPE, 32>(a, stream) : forward_ent<TYPE, kOutThreads>(a, stream);
+    const bool ent = a.teacher.count == 0;
+    if constexpr (TYPE == TN_TYPE_C64) {
+        if (a.r.scale == 1.f)
+            return ent ? forward_mask<TYPE, true, true>(a, warp_rows, stream)
+                       : forward_mask<TYPE, false, true>(a, warp_rows, stream);
+    }
+    return ent ? forward_mask<TYPE, true, false>(a, warp_rows, stream)
+               : forward_mask<TYPE, false, false>(a, warp_rows, stream);
 }
 
 }  // namespace tn
