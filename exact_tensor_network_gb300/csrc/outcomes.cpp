@@ -62,17 +62,19 @@ bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow
 
 // How the maxima of k alternatives lie.  Chunks are as large as leaves four
 // times as many of them as alternatives (a cut well inside) and at most 1024
-// vectors to read again, but no more of them in a segment than kOutKeys.
+// vectors to read again (4096 for the larger groups that few rows have), but
+// no more of them in a segment than kOutKeys.
 struct Chunks {
     int log;
     int64_t seg_chunks;     // of a segment
     bool tree;
 };
 
-Chunks chunks_of(const tn::OutSplit &s, int64_t k) {
+Chunks chunks_of(const tn::OutSplit &s, int64_t rows, int64_t k) {
     Chunks c;
+    const int64_t again = rows >= tn::kOutTarget / 4 ? 1024 : 4096;
     c.log = s.warp_rows ? 0 : tn::kOutChunkLog;
-    while (c.log > 0 && (s.vecs >> c.log < 4 * k || (int64_t)tn::out_most((int)k) << c.log > 1024) &&
+    while (c.log > 0 && (s.vecs >> c.log < 4 * k || (int64_t)tn::out_most((int)k) << c.log > again) &&
            s.seg_vecs <= (int64_t)tn::kOutKeys << (c.log - 1))
         --c.log;
     c.seg_chunks = (s.seg_vecs + (1 << c.log) - 1) >> c.log;
@@ -92,7 +94,7 @@ void add_need(const Outcomes &o, int64_t rows, bool aligned, Need *n) {
     if (slots > n->slots) n->slots = slots;
     // fewer alternatives have larger chunks
     for (int k = 1; k <= o.max_top; k *= 2) {
-        const Chunks c = chunks_of(s, k * 2 > o.max_top ? o.max_top : k);
+        const Chunks c = chunks_of(s, rows, k * 2 > o.max_top ? o.max_top : k);
         if (slots * c.seg_chunks > n->maxima) n->maxima = slots * c.seg_chunks;
         if (c.tree && slots * 33 > n->supers) n->supers = slots * 33;
     }
@@ -200,7 +202,7 @@ tn_status forward(Outcomes &o, tn::OutForward &a, const tn::OutSplit &s, cudaStr
     const int64_t k = a.n_top;
     a.finish = !s.warp_rows && (s.segs > 1 || k > 0);
     if (k > 0) {
-        const Chunks c = chunks_of(s, k);
+        const Chunks c = chunks_of(s, a.r.rows, k);
         a.chunk_log = c.log;
         a.seg_chunks = static_cast<int32_t>(c.seg_chunks);
         a.tree = c.tree;

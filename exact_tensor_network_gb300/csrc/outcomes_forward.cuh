@@ -233,7 +233,15 @@ struct Stream {
         a.z0 = z0;
         a.s = s.x + s.y;
         a.t = t.x + t.y;
-        if (En::kReal && ref != -__builtin_huge_valf()) a.move_by(-fmaf(z0, c2, -ref));
+        if (En::kReal && ref != -__builtin_huge_valf()) {
+            const float left = fmaf(z0, c2, -ref), one = ex2(left);
+            if (a.s == one && a.t == one * left) {   // of one entry: exactly 1 and 0
+                a.s = 1.f;
+                a.t = 0.f;
+            } else {
+                a.move_by(-left);
+            }
+        }
         return a;
     }
 };
@@ -738,8 +746,9 @@ __device__ __forceinline__ void put_alternative(const OutForward &a, const Row<T
 
 // ---- the kernels ------------------------------------------------------------
 
-template <int TYPE, int G, bool MASK, bool ENT, bool UNIT>
-__global__ void __launch_bounds__(kOutThreads, G == 32 ? 6 : kOutCtas)
+// SHORT: rows of one vector a lane, whose alternatives need no search.
+template <int TYPE, int G, bool SHORT, bool MASK, bool ENT, bool UNIT>
+__global__ void __launch_bounds__(kOutThreads, G == 32 && !SHORT ? 6 : kOutCtas)
 outcomes_forward(const __grid_constant__ OutForward a) {
     using En = Entry<TYPE>;
     constexpr int E = En::E;
@@ -780,27 +789,32 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     Stream<TYPE, ENT, UNIT> st;
     if (!ENT) te.read(g, a.teacher, a.r, r, row, true);
 
-    // the largest of each of the step's kU rows of 32 vectors, into the maxima
+    // The largest entries of the step's chunks, as they are; keys are made of
+    // them once the row is read (a warp's rows: at once).
     const auto put_maxima = [&](int b, float (&lm)[kU]) {
-        if (G > 32 && log >= 5) {
-            const int rows = (1 << log) >> 5;     // of 32 vectors in a chunk: 1, 2 or 4
+        float *maxima = reinterpret_cast<float *>(sm.keys);
+        if (G > 32 && log == kOutChunkLog) {
+            const float x = warp_max(fmaxf(fmaxf(lm[0], lm[1]), fmaxf(lm[2], lm[3])));
+            if (g.lane == 0) maxima[b >> kOutChunkLog] = x;
+        } else if (G > 32 && log >= 5) {
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                if (u & (rows - 1)) lm[u] = fmaxf(lm[u], lm[u - 1]);
-                if (((u + 1) & (rows - 1)) == 0) {
-                    const uint32_t x = __reduce_max_sync(0xffffffffu, order_key<TYPE>(lm[u]));
-                    const int at = (b + u * 32) >> log;
-                    if (g.lane == 0 && at << log < nv) sm.keys[at] = x;
-                }
+                if (log == 6 && (u & 1) == 0) continue;
+                const float x = warp_max(log == 6 ? fmaxf(lm[u], lm[u - (u & 1)]) : lm[u]);
+                const int at = (b + u * 32) >> log;
+                if (g.lane == 0 && at << log < nv) maxima[at] = x;
             }
         } else {
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
                 const int j = b + u * 32 + g.lane;
-                uint32_t x = order_key<TYPE>(lm[u]);
+                float x = lm[u];
 #pragma unroll 1
-                for (int o = 1; o < 1 << log; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-                if ((g.lane & ((1 << log) - 1)) == 0 && j < nv) sm.keys[j >> log] = x;
+                for (int o = 1; o < 1 << log; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                if ((g.lane & ((1 << log) - 1)) == 0 && j < nv) {
+                    if (G == 32) sm.keys[j] = order_key<TYPE>(x);
+                    else maxima[j >> log] = x;
+                }
             }
         }
     };
@@ -851,15 +865,13 @@ outcomes_forward(const __grid_constant__ OutForward a) {
             }
         } else {
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
+            for (int u = 0; u < (SHORT ? 1 : kU); ++u) {
                 float v[E];
                 lm[u] = decode<TYPE>(raw[u], v, a.r.floor);
                 if (!st.add(v, lm[u], a.r.c2)) later |= 1u << u;
             }
         }
-        if (ENT && k > 0) put_maxima(b, lm);
         if (__any_sync(0xffffffffu, later)) {
-            __syncwarp();
 #pragma unroll 1
             while (later) {
                 const int u = __ffs(later) - 1;
@@ -871,10 +883,14 @@ outcomes_forward(const __grid_constant__ OutForward a) {
                 for (int i = 0; i < E; ++i) v[i] = x.v[i];
                 const float m = largest<TYPE>(v, a.r.floor);
                 if (!st.add(v, m, a.r.c2)) st.far(x.v, m, a.r.c2);
-                if (ENT && k > 0) atomicMax(sm.keys + (j >> log), order_key<TYPE>(m));
+                if constexpr (ENT) {
+#pragma unroll
+                    for (int i = 0; i < kU; ++i) lm[i] = i == u ? fmaxf(lm[i], m) : lm[i];
+                }
             }
             __syncwarp();
         }
+        if (ENT && !SHORT && k > 0) put_maxima(b, lm);
     }
     Sums<TYPE> sum = st.done(a.r.c2);
     combine(g, sum, a.r.c2);     // its barriers also publish the maxima
@@ -892,8 +908,13 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         if (ENT && k > 0) {
             const int nc = (nv + (1 << log) - 1) >> log;
             uint32_t *to = a.maxima + (row * segs + seg) * a.seg_chunks;
-            for (int i = g.t; i < a.seg_chunks; i += G) to[i] = i < nc ? sm.keys[i] : 0u;
+            for (int i = g.t; i < a.seg_chunks; i += G) {
+                const uint32_t x = i < nc ? order_key<TYPE>(__uint_as_float(sm.keys[i])) : 0u;
+                to[i] = x;
+                sm.keys[i] = x;
+            }
             if (a.tree) {
+                g.sync();
                 // the maxima of 32 chunks, and of the segment
                 uint32_t *up = a.supers + (row * segs + seg) * 33;
                 uint32_t top = 0;
@@ -918,7 +939,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         int64_t *ids = a.top_ids + row * k;
         float *lps = a.top_logp + row * k;
         int found = 0;
-        if (nv <= 32) {
+        if constexpr (SHORT) {
             // one vector a lane: take the largest k times
             const auto x = row_vector<TYPE>(r, g.lane);
             uint32_t key[E];
@@ -942,6 +963,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
                 }
             }
         } else if (valid) {
+            g.sync();
             found = best_entries<TYPE, MASK>(g, sm, r, nv, k, 0, a.cand_len);
             for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, 0, logz, ids, lps);
         }
@@ -1038,24 +1060,31 @@ __device__ __noinline__ int exact_chunks_of_tree(Group<G> g, const Scratch sm, c
 }
 
 // What follows the streaming kernel for rows in segments or with
-// alternatives: one CTA a row joins the segments' sums in order and searches.
+// alternatives: a group a row joins the segments' sums in order and searches.
+// It waits for memory and for itself most of the time (about ten dependent
+// steps), so many rows are better served by a warp each, all at once, than by
+// a CTA each in turn.
+template <int G>
+constexpr int finish_threads() { return G == 32 ? 128 : G; }
 template <int TYPE, int G, bool MASK, bool ENT>
-__global__ void __launch_bounds__(G, G == 128 ? 6 : 1) outcomes_finish(const __grid_constant__ OutForward a) {
+__global__ void __launch_bounds__(finish_threads<G>(), G == 512 ? 1 : 6) outcomes_finish(const __grid_constant__ OutForward a) {
     using En = Entry<TYPE>;
     constexpr int E = En::E;
     constexpr float kInf = __builtin_huge_valf();
     extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int kGroups = finish_threads<G>() / G;
     __shared__ uint32_t red[4 * G / 32];
     constexpr int kTeacher = ENT ? 16 : TN_OUTCOMES_MAX_IDS * 20 + 16;
-    __shared__ __align__(16) unsigned char teacher[kTeacher];
-    Teacher te(teacher, ENT ? 0 : a.teacher.count);
+    __shared__ __align__(16) unsigned char teacher[kGroups * kTeacher];
+    Teacher te(teacher + threadIdx.x / G * kTeacher, ENT ? 0 : a.teacher.count);
     pdl_trigger();
     Group<G> g(red);
-    const int64_t row = blockIdx.x;
+    const int64_t row = blockIdx.x * kGroups + threadIdx.x / G;
     const int segs = (int)a.r.segs, k = ENT ? a.n_top : 0, log = a.chunk_log;
-    const Scratch sm(smem, a);
-    const Row<TYPE> r(a.r, row);
+    const Scratch sm(smem + threadIdx.x / G * a.group_bytes, a);
     pdl_wait();
+    if (G == 32 && row >= a.r.rows) return;
+    const Row<TYPE> r(a.r, row);
     // (the workspace is read past the L1 cache: this grid may have started while
     // the previous call's was still filling it)
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1124,14 +1153,23 @@ template <int TYPE, bool MASK, bool ENT, bool UNIT>
 cudaError_t launch_forward(const OutForward &a, bool warp_rows, cudaStream_t stream) {
     if (warp_rows) {
         const int groups = kOutThreads / 32;
-        return launch_rows(outcomes_forward<TYPE, 32, MASK, ENT, UNIT>, (a.r.rows + groups - 1) / groups, kOutThreads,
+        const int64_t ctas = (a.r.rows + groups - 1) / groups;
+        if (ENT && a.r.seg_vecs <= 32)
+            return launch_rows(outcomes_forward<TYPE, 32, ENT, MASK, ENT, UNIT>, ctas, kOutThreads, 0, a, stream);
+        return launch_rows(outcomes_forward<TYPE, 32, false, MASK, ENT, UNIT>, ctas, kOutThreads,
                            (size_t)groups * a.group_bytes, a, stream);
     }
     const size_t keys = ENT && a.n_top > 0 ? (size_t)(a.seg_chunks + 3) / 4 * 16 : 0;
-    cudaError_t e = launch_rows(outcomes_forward<TYPE, kOutThreads, MASK, ENT, UNIT>, a.r.rows * a.r.segs, kOutThreads,
+    cudaError_t e = launch_rows(outcomes_forward<TYPE, kOutThreads, false, MASK, ENT, UNIT>, a.r.rows * a.r.segs, kOutThreads,
                                 keys, a, stream);
     if (e != cudaSuccess || !a.finish) return e;
-    // few rows: as many threads as help one
+    // many rows: a warp each, if their maxima fit its registers; few: as many
+    // threads as help one
+    if constexpr (ENT) {
+        if (a.r.rows >= kOutTarget / 4 && a.r.segs * a.seg_chunks <= kOutWarpVecs)
+            return launch_rows(outcomes_finish<TYPE, 32, MASK, ENT>, (a.r.rows + 3) / 4, 128, (size_t)4 * a.group_bytes,
+                               a, stream);
+    }
     if (a.r.rows >= kOutTarget / 4)
         return launch_rows(outcomes_finish<TYPE, 128, MASK, ENT>, a.r.rows, 128, a.group_bytes, a, stream);
     return launch_rows(outcomes_finish<TYPE, 512, MASK, ENT>, a.r.rows, 512, a.group_bytes, a, stream);

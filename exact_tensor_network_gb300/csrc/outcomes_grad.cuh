@@ -37,9 +37,13 @@ __device__ __forceinline__ void finish_row_grad(RowGrad &c) {
 template <int TYPE>
 __device__ __forceinline__ float entry_grad(const RowGrad &c, float v, float add) {
     if constexpr (Entry<TYPE>::kReal) {
-        const float lp = __fadd_rn(__fmul_rn(v, c.scale), -c.logz);
-        const float p = ex2(lp * kLog2E);
-        return c.mult * fmaf(p, fmaf(c.beta, lp + c.entropy, c.alpha), add);
+        const float lp = max_nan(__fadd_rn(__fmul_rn(v, c.scale), -c.logz), -1e30f);
+        const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
+        if (lp < -80.f) {       // p may underflow where p f does not
+            const float q = ex2(lp * (0.5f * kLog2E));
+            return c.mult * fmaf(q, q * f, add);
+        }
+        return c.mult * fmaf(ex2(lp * kLog2E), f, add);
     } else {
         // 2 / w dL/dz, with p / w taken together
         float lp = 0.f, pw = c.inv_z;
@@ -47,8 +51,11 @@ __device__ __forceinline__ float entry_grad(const RowGrad &c, float v, float add
             lp = __fadd_rn(__fmul_rn(c.scale, logf(v)), -c.logz);
             if (c.inv_z == 0.f) pw = ex2(lp * kLog2E) / v;
         }
-        const float dense = pw * fmaf(c.beta, lp + c.entropy, c.alpha);
-        return 2.f * c.mult * (add == 0.f ? dense : dense + add / v);
+        const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
+        if (add == 0.f) return 2.f * c.mult * (pw * f);
+        // over one denominator: nothing is left where p f = -add (p = 1)
+        if (c.beta == 0.f && c.inv_z != 0.f) lp = __fadd_rn(__fmul_rn(c.scale, logf(v)), -c.logz);
+        return 2.f * c.mult * (fmaf(ex2(lp * kLog2E), f, add) / v);
     }
 }
 
@@ -98,7 +105,12 @@ __device__ __forceinline__ uint4 dense_grad(const RowGrad &c, const uint4 &raw) 
     Entry<TYPE>::values(raw, v);
     if constexpr (Entry<TYPE>::kReal) {
         const float2 scale = make_float2(c.scale, c.scale), lz = make_float2(-c.logz, -c.logz);
-        const float2 l2 = make_float2(kLog2E, kLog2E);
+        // bf16 reaches below the least p that ex2 gives: p is the square of
+        // ex2(d / 2) there, multiplied in turn.  (f16 does not reach that far;
+        // f32 rows keep the better p, and p < 2^-126 counts as 0.)
+        constexpr bool kSquare = TYPE == TN_TYPE_BF16;
+        constexpr float kL2 = kSquare ? 0.5f * kLog2E : kLog2E;
+        const float2 l2 = make_float2(kL2, kL2);
         const float ma = c.mult * c.alpha;
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
@@ -114,6 +126,7 @@ __device__ __forceinline__ uint4 dense_grad(const RowGrad &c, const uint4 &raw) 
             } else {
                 o = mul2(p, make_float2(ma, ma));
             }
+            if constexpr (kSquare) o = mul2(o, p);
             v[i] = o.x;
             v[i + 1] = o.y;
         }

@@ -298,6 +298,87 @@ def test_many_rows_of_one_cta_each(t):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+@pytest.mark.parametrize("V", [1, 60, 5000, 200000])
+def test_only_entry_is_certain(V, scale, t):
+    """One entry present: log p and entropy are exactly 0, and so are the
+    gradients, whatever the entry's value."""
+    import torch
+    rng = np.random.default_rng(V)
+    R = 40
+    at = rng.integers(0, V, size=(R, 1))
+    z = np.zeros((R, V), np.complex64) if t == "c64" else np.full((R, V), -INF, np.float32)
+    np.put_along_axis(z, at, (rng.standard_normal((R, 1)) * 5 + 0.1).astype(z.dtype), axis=1)
+    rows = torch.from_numpy(z).to(torch_type(t)).cuda()
+    ids = torch.from_numpy(at).cuda()
+    op = tn.Outcomes(V, torch_type(t), max_rows=R, top=2, scale=scale)
+    s = op.score(rows, ids)
+    g = op.score_grad(rows, ids, s.logz, s.entropy, torch.ones((R, 1), device="cuda"),
+                      torch.ones(R, device="cuda"))
+    d = op.distill_step(rows, ids, torch.ones((R, 1), device="cuda"), torch.ones(R, device="cuda"))
+    op.check()
+    for x in (s.entropy, s.logp, s.top_logp[:, 0], g, d.loss, d.grad):
+        assert (x == 0).all()
+    assert (s.top_ids[:, :1] == ids).all() and (s.top_ids[:, 1] == -1).all()
+
+
+@pytest.mark.parametrize("k", [3, 100])
+@pytest.mark.parametrize("order", ["random", "equal", "few", "masked", "block"])
+@pytest.mark.parametrize("t", ["c64", "bf16"])
+def test_alternatives_of_very_long_rows(t, order, k):
+    """Rows whose pieces' maxima form a tree: every outcome as likely as the
+    next, a handful of outcomes, the best ones side by side."""
+    import torch
+    R, V = 2, 2500003
+    rng = np.random.default_rng(k)
+    rows, mask = make_rows(rng, R, V, t), None
+    if order == "equal":
+        rows[:] = 0.25
+    elif order == "few":
+        keep = torch.zeros((R, V), dtype=torch.bool)
+        for r in range(R):
+            keep[r, torch.from_numpy(rng.integers(0, V, size=50))] = True
+        rows[~keep] = 0.0 if t == "c64" else -INF
+    elif order == "masked":
+        mask = torch.from_numpy(rng.random((1, V)) < 0.3)
+    elif order == "block":
+        rows[:, V // 2:V // 2 + 300] *= 64.0
+    run_all(rows, t, rand_ids(rng, R, 2, V), k, None, mask=mask, rng=rng)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("t,R,V", [("bf16", 2500, 2601), ("c64", 1300, 1031), ("f32", 700, 5003)])
+def test_many_rows(t, R, V, masked):
+    """More rows than the GPU holds groups, odd lengths, a mask of its own
+    for every row (an empty one among them)."""
+    import torch
+    rng = np.random.default_rng(V)
+    keep = None
+    if masked:
+        keep = rng.random((R, V)) < rng.random((R, 1))
+        keep[R // 3] = False
+        keep = torch.from_numpy(keep)
+    run_all(make_rows(rng, R, V, t), t, rand_ids(rng, R, 1, V), 3 if masked else 40,
+            rand_teacher(rng, R, 17, V), mask=keep, rng=rng)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("t,R,V", [("bf16", 30, 70001), ("f32", 21, 90001), ("c64", 9, 150001),
+                                   ("f16", 3, 900001), ("f32", 2, 800003)])
+def test_distillation_of_long_rows(t, R, V, masked):
+    """Rows that several CTAs hold between them, and rows too long for that."""
+    import torch
+    rng = np.random.default_rng(V)
+    keep = None
+    if masked:
+        keep = rng.random((R, V)) < 0.5
+        keep[1] = False
+        keep[0, :V - 9] = False
+        keep = torch.from_numpy(keep)
+    run_all(make_rows(rng, R, V, t), t, None, 0, rand_teacher(rng, R, 200, V), mask=keep, rng=rng)
+
+
+@pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("V", [50, 40000])
 def test_rows_without_distribution(V, t):
     """NaN and +inf in present places, -inf everywhere, the lowest value
