@@ -13,11 +13,11 @@
 
 namespace tn {
 
-OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned) {
+OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int64_t warp_vecs) {
     const int64_t E = kOutVecBytes / out_entry_bytes(type);
     OutSplit s;
     s.vecs = (cols + E - 1 + (aligned ? 0 : E - 1)) / E;   // its first may hold one entry only
-    s.warp_rows = s.vecs <= kOutWarpVecs;
+    s.warp_rows = s.vecs <= warp_vecs;
     s.segs = 1;
     s.seg_vecs = s.vecs;
     if (s.warp_rows) return s;
@@ -58,6 +58,21 @@ tn_status cuda_fail(Outcomes &o, cudaError_t e, const char *what) {
     return fail(o.error, TN_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Rows of how many vectors are one warp's.  Short ones always are: a CTA would
+// have less than two vectors a thread.  Longer ones cost fewer instructions as
+// a warp's (what a row costs besides its vectors is paid once, not once for
+// each of four or eight warps), if there are rows enough for all warps.
+// Measured, CTA against warp a row: scores of 20000 rows of 6 KB 44 against
+// 28 us, of 10 KB 58 against 41, of 10000 rows of 16 KB 35 against 32, but of
+// 1300 rows 6.2 against 7.6; gradients of 20000 rows of 6 KB 65 against 45 us, of
+// 10 KB 85 against 70, but of 10000 rows of 16 KB 56 against 59 and of 2500
+// rows 10.9 against 15.5; training steps of 20000 rows of 4 KB 173 against 41 us,
+// of 8 KB 181 against 64, of 10000 rows of 16 KB 101 against 73, but of 100
+// rows of 16 KB 5.5 against 7.7 and of 10000 rows of 32 KB 132 against 218.
+int64_t warp_vecs(int64_t rows) { return rows > 2 * tn::kOutTarget ? 1024 : tn::kOutWarpVecs; }
+int64_t grad_warp_vecs(int64_t rows) { return rows > 4 * tn::kOutTarget ? 640 : tn::kOutWarpVecs; }
+int64_t step_warp_vecs(int64_t rows) { return rows > tn::kStepCtas * 152 ? 1024 : tn::kOutWarpVecs; }
+
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
 
 // How the maxima of k alternatives lie.  Chunks are as large as leaves four
@@ -88,7 +103,7 @@ struct Need {
 };
 
 void add_need(const Outcomes &o, int64_t rows, bool aligned, Need *n) {
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows, aligned);
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows, aligned, tn::kOutWarpVecs);
     if (s.warp_rows || (s.segs == 1 && o.max_top == 0)) return;
     const uint64_t slots = (uint64_t)rows * s.segs;
     if (slots > n->slots) n->slots = slots;
@@ -237,16 +252,18 @@ tn_status gradient(Outcomes &o, const tn::OutGrad &a, const tn::OutSplit &s, cud
 }
 
 // CTAs of a cluster that hold a row in shared memory; segs 0: too long.
-tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int32_t count) {
-    tn::OutSplit s = tn::out_split(type, cols, rows, aligned);
+tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int32_t count, int32_t *two) {
+    tn::OutSplit s = tn::out_split(type, cols, rows, aligned, step_warp_vecs(rows));
+    *two = 0;
     if (s.warp_rows) return s;
-    const int64_t bytes = s.vecs * tn::kOutVecBytes, teachers = 2 * tn::teacher_bytes(count);
+    const int64_t bytes = s.vecs * tn::kOutVecBytes, teachers = tn::step_lists(count);
     int64_t c = (bytes + tn::kStepSlice - teachers - 1) / (tn::kStepSlice - teachers);
     if (c > tn::kStepCluster) c = tn::kStepCluster;
     // few rows: more CTAs a row, of two vectors a thread at least
     while (c < tn::kStepCluster && rows * c < 2 * 152 && s.vecs >= 2 * (c + 1) * tn::kStepThreads) ++c;
     s.segs = c;
     s.seg_vecs = (s.vecs + c - 1) / c;
+    *two = 2 * s.seg_vecs * tn::kOutVecBytes + teachers <= tn::kStepSlice;
     if (s.seg_vecs * tn::kOutVecBytes + teachers > tn::kStepSliceMost) s.segs = 0;
     return s;
 }
@@ -291,7 +308,7 @@ tn_status tn_outcomes_create(int32_t type, int64_t cols, int64_t max_rows, int32
         return fail(g_error, TN_EINVAL, "scale must lie in 2^-40 .. 2^40");
     if (cols > (int64_t)1 << 40) return fail(g_error, TN_EOVERFLOW, "more than 2^40 entries a row");
     int64_t items;
-    if (!mul_ok(max_rows, tn::out_split(type, cols, max_rows, false).segs, &items) || items > 0x7fffffff)
+    if (!mul_ok(max_rows, tn::out_split(type, cols, max_rows, false, tn::kOutWarpVecs).segs, &items) || items > 0x7fffffff)
         return fail(g_error, TN_EOVERFLOW, "more than 2^31 - 1 row segments");
     tn_outcomes_s *h = new (std::nothrow) tn_outcomes_s;
     if (!h) return fail(g_error, TN_ENOMEM, "host allocation failed");
@@ -350,7 +367,8 @@ tn_status tn_outcomes_score(tn_outcomes_t *h, const tn_rows *rows, const int64_t
     if (rows->rows == 0) return TN_OK;
     if (!logz || !entropy || (n_given > 0 && (!given || !logp)) || (n_top > 0 && (!top_ids || !top_logp)))
         return fail(o.error, TN_EINVAL, "an output or the given outcomes are missing");
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows));
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows),
+                                         n_top > 0 ? tn::kOutWarpVecs : warp_vecs(rows->rows));
     tn::OutForward a = {};
     a.r = rows_of(o, rows, s);
     a.given = given;
@@ -378,7 +396,8 @@ tn_status tn_outcomes_score_grad(tn_outcomes_t *h, const tn_rows *rows, const in
     if (rows->rows == 0) return TN_OK;
     if (!logz || (n_given > 0 && (!given || !g_logp)) || (g_entropy && !entropy))
         return fail(o.error, TN_EINVAL, "logz, the given outcomes with g_logp, or entropy are missing");
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows));
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows),
+                                         grad_warp_vecs(rows->rows));
     tn::OutGrad a = {};
     a.r = rows_of(o, rows, s);
     a.logz = logz;
@@ -402,7 +421,8 @@ tn_status tn_outcomes_distill(tn_outcomes_t *h, const tn_rows *rows, const tn_te
     if (st != TN_OK) return st;
     if (rows->rows == 0) return TN_OK;
     if (!loss || !logz) return fail(o.error, TN_EINVAL, "loss and logz are required");
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows));
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows),
+                                         warp_vecs(rows->rows));
     tn::OutForward a = {};
     a.r = rows_of(o, rows, s);
     a.logz = logz;
@@ -422,7 +442,8 @@ tn_status tn_outcomes_distill_grad(tn_outcomes_t *h, const tn_rows *rows, const 
     if (st != TN_OK) return st;
     if (rows->rows == 0) return TN_OK;
     if (!logz || !g_loss) return fail(o.error, TN_EINVAL, "logz and g_loss are required");
-    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows));
+    const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows),
+                                         grad_warp_vecs(rows->rows));
     tn::OutGrad a = {};
     a.r = rows_of(o, rows, s);
     a.logz = logz;
@@ -449,11 +470,13 @@ tn_status tn_outcomes_distill_step(tn_outcomes_t *h, const tn_rows *rows, const 
     if (st != TN_OK) return st;
     if (rows->rows == 0) return TN_OK;
     if (!loss || !logz) return fail(o.error, TN_EINVAL, "loss and logz are required");
-    const tn::OutSplit s = step_split(o.type, o.cols, rows->rows, aligned(o, rows), teacher->count);
+    int32_t two;
+    const tn::OutSplit s = step_split(o.type, o.cols, rows->rows, aligned(o, rows), teacher->count, &two);
     if (s.segs == 0) return step_in_two(h, rows, teacher, g_loss, loss, logz, grad, grad_row_stride,
                                         grad_col_stride, stream);
     tn::OutStep a = {};
     a.r = rows_of(o, rows, s);
+    a.two = two;
     a.teacher = teacher_of(teacher);
     a.g_loss = g_loss;
     a.loss = loss;

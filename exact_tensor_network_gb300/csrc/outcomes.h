@@ -114,6 +114,7 @@ struct OutStep {
     float *loss, *logz;
     char *grad;
     int64_t grad_row_stride, grad_col_stride;
+    int32_t two;             // shared memory for two slices: the next row's is on its way
 };
 
 constexpr int kStepThreads = 256;
@@ -128,6 +129,21 @@ constexpr int kStepCluster = 8;
 // each outcome, and a flag.
 __host__ __device__ inline int teacher_bytes(int count) { return (count * 20 + 16 + 15) / 16 * 16; }
 
+// What finds repeated ids (see Repeats): two tables, of four places an id or
+// more, and a mark for each.
+__host__ __device__ inline int repeat_slots(int count) {
+    int s = 32;
+    while (s < 4 * count) s *= 2;
+    return s;
+}
+__host__ __device__ inline int repeat_marks(int count) { return (count + 15) / 16 * 16; }
+__host__ __device__ inline int repeat_bytes(int count) { return 2 * repeat_slots(count) + repeat_marks(count); }
+// Shared memory of a training step's CTA besides its slices: two rows'
+// teachers and marks, one pair of tables.
+__host__ __device__ inline int step_lists(int count) {
+    return 2 * (teacher_bytes(count) + repeat_marks(count)) + 2 * repeat_slots(count);
+}
+
 struct Outcomes {
     int32_t type = 0;
     int64_t cols = 0, max_rows = 0;
@@ -140,7 +156,7 @@ struct Outcomes {
 };
 
 // aligned: every row starts at a 16-byte boundary.
-OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned);
+OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int64_t warp_vecs);
 // Launchers, instantiated by k_outcomes_<type>.cu.
 template <int TYPE>
 cudaError_t outcomes_forward_of(const OutForward &a, bool warp_rows, cudaStream_t stream);

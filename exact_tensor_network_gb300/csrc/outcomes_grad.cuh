@@ -179,27 +179,98 @@ __device__ __noinline__ void grad_vector(const Row<TYPE> r, const RowGrad c, con
     }
 }
 
+// Ids that stand in a list more than once, without comparing all with all:
+// every id leaves its place in two tables, at two hashes of it; one that finds
+// another place there with its own id, or its own place in neither, is marked
+// (with whom it found).  A mark may be wrong, the absence of one is not: equal
+// ids meet at the same places, and whoever of them a table kept is found by
+// the others.  put() for all, a barrier, look() for all, a barrier.
+struct Repeats {
+    uint8_t *a, *b, *mark;
+    int slots;
+
+    __device__ __forceinline__ Repeats(void *tables, void *marks, int n)
+        : a(static_cast<uint8_t *>(tables)), b(a + repeat_slots(n)), mark(static_cast<uint8_t *>(marks)),
+          slots(repeat_slots(n)) {}
+    __device__ __forceinline__ uint32_t second(int64_t id) const {
+        return ((uint32_t)id * 2654435769u) >> (__clz(slots) + 1);     // Fibonacci hashing
+    }
+    __device__ __forceinline__ void put(int j, int64_t id) const {
+        mark[j] = 0;
+        a[(uint32_t)id & (slots - 1)] = (uint8_t)j;
+        b[second(id)] = (uint8_t)j;
+    }
+    __device__ __forceinline__ void look(const int64_t *ids, int j, int64_t id) const {
+        const int x = a[(uint32_t)id & (slots - 1)], y = b[second(id)];
+        const bool ex = ids[x] == id, ey = ids[y] == id;
+        if (ex && x != j) mark[x] = mark[j] = 1;
+        if (ey && y != j) mark[y] = mark[j] = 1;
+        if (!ex && !ey) mark[j] = 1;
+    }
+};
+
+// What the outcomes equal to ids[j] add up to, in order, for a warp's j's;
+// false where ids[j] is not the first of them.  The warp looks through the
+// list once for each marked one.
+__device__ __forceinline__ bool sum_of_equal(const int64_t *ids, const float *adds, int n, int j, int64_t id,
+                                             bool marked, float &sum) {
+    const int lane = threadIdx.x % 32;
+    bool first = true;
+#pragma unroll 1
+    for (uint32_t m = __ballot_sync(0xffffffffu, marked); m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        const int64_t x = __shfl_sync(0xffffffffu, id, src);
+        const int at = __shfl_sync(0xffffffffu, j, src);
+        float total = 0.f;
+        bool lead = true;
+#pragma unroll 1
+        for (int i = 0; i < n; i += 32) {
+            uint32_t e = __ballot_sync(0xffffffffu, i + lane < n && ids[i + lane] == x);
+            if (e && i + __ffs(e) - 1 < at) {
+                lead = false;
+                break;
+            }
+#pragma unroll 1
+            for (; e; e &= e - 1) total += adds[i + __ffs(e) - 1];
+        }
+        if (lane == src) {
+            sum = total;
+            first = lead;
+        }
+    }
+    return first;
+}
+
 // The entries with ids among entries [lo, hi), after the dense part; entries
 // [held_lo, held_hi) of the row are at held[entry - lo], masked ones absent.
+// scratch: the tables and marks of n ids.
 template <int TYPE, int G>
 __device__ __forceinline__ void grad_ids(const Group<G> &g, const Row<TYPE> &r, const RowGrad &c,
                                          const Out<TYPE> &out, const int64_t *ids, const float *adds, float sign,
-                                         int n, int64_t lo, int64_t hi,
+                                         int n, int64_t lo, int64_t hi, unsigned char *scratch,
                                          const typename Entry<TYPE>::T *held = nullptr, int64_t held_lo = 0,
                                          int64_t held_hi = 0) {
+    const Repeats rp(scratch + repeat_marks(n), scratch, n);
+    const auto mine = [&](int j) { return j < n && ids[j] >= 0 && ids[j] >= lo && ids[j] < hi; };
+    if (n > 1) {
+        g.sync();
 #pragma unroll 1
-    for (int j = g.t; j < n; j += G) {
-        const int64_t id = ids[j];
-        if (id < 0 || id < lo || id >= hi) continue;
-        float add = 0.f;
-        bool first = true;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i)
-            if (ids[i] == id) {
-                first = first && i >= j;
-                add += adds[i];
-            }
-        if (!first) continue;
+        for (int j = g.t; j < n; j += G)
+            if (mine(j)) rp.put(j, ids[j]);
+        g.sync();
+#pragma unroll 1
+        for (int j = g.t; j < n; j += G)
+            if (mine(j)) rp.look(ids, j, ids[j]);
+        g.sync();
+    }
+#pragma unroll 1
+    for (int j0 = 0; j0 < n; j0 += G) {
+        const int j = j0 + g.t;
+        const bool in = mine(j);
+        const int64_t id = in ? ids[j] : -1;
+        float add = in ? adds[j] : 0.f;
+        const bool first = n == 1 || sum_of_equal(ids, adds, n, j, id, in && rp.mark[j], add);
+        if (!in || !first) continue;
         typename Entry<TYPE>::T x;
         float v;
         if (held && id >= held_lo && id < held_hi) {
@@ -328,7 +399,8 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
     else grad_dense<TYPE, G, MASK, false>(g, r, c, out, v0, nv);
     if (n == 0) return;
     g.sync();
-    grad_ids<TYPE>(g, r, c, out, ids, adds, a.teacher.count ? -1.f : 1.f, n, v0 * E - r.head, v1 * E - r.head);
+    grad_ids<TYPE>(g, r, c, out, ids, adds, a.teacher.count ? -1.f : 1.f, n, v0 * E - r.head, v1 * E - r.head,
+                   lists + kGroups * teacher_bytes(n) + threadIdx.x / G * repeat_bytes(n));
 }
 
 template <int TYPE, int G, bool MASK>
@@ -336,7 +408,7 @@ cudaError_t launch_grad(const OutGrad &a, cudaStream_t stream) {
     const int64_t items = a.r.rows * a.r.segs;
     const int groups = kOutThreads / G;
     const int n = a.teacher.count ? a.teacher.count : a.n_given;
-    const size_t smem = n ? groups * teacher_bytes(n) : 0;
+    const size_t smem = n ? groups * (teacher_bytes(n) + repeat_bytes(n)) : 0;
     return launch_pdl(outcomes_grad<TYPE, G, MASK>, dim3((unsigned)((items + groups - 1) / groups)),
                       dim3(kOutThreads), smem, stream, a);
 }

@@ -26,7 +26,9 @@ __device__ __forceinline__ void copy_wait_all_but(int n) {
         case 2: copy_wait<2>(); break;
         case 3: copy_wait<3>(); break;
         case 4: copy_wait<4>(); break;
-        default: copy_wait<5>(); break;
+        case 5: copy_wait<5>(); break;
+        case 6: copy_wait<6>(); break;
+        default: copy_wait<7>(); break;
     }
 }
 
@@ -113,10 +115,11 @@ __device__ __forceinline__ void copy_step(const Slice<TYPE, MASK, G> &s, uint4 *
     copy_commit();
 }
 
-// The sums of a slice, whose copies are the last groups (one a step).
+// The sums of a slice, whose copies are the last groups (one a step) but
+// `behind`.
 template <int TYPE, int G, bool MASK, bool UNIT>
 __device__ __forceinline__ Sums<TYPE> sum_slice(const Slice<TYPE, MASK, G> &s, uint4 *hold, int t,
-                                                const OutRows &a) {
+                                                const OutRows &a, int behind) {
     using En = Entry<TYPE>;
     constexpr int E = En::E;
     typename Row<TYPE>::Keep next_keep[kU];
@@ -139,7 +142,7 @@ __device__ __forceinline__ Sums<TYPE> sum_slice(const Slice<TYPE, MASK, G> &s, u
             for (int u = 0; u < kU; ++u) keep[u] = next_keep[u];
             load_keep(b + kU * G);
         }
-        copy_wait_all_but(s.steps - 1 - i);
+        copy_wait_all_but(s.steps - 1 - i + behind);
         uint4 raw[kU];
         if (s.whole(b, kU * G)) {
 #pragma unroll
@@ -225,21 +228,21 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
     constexpr int E = En::E;
     constexpr int kGroups = kOutThreads / 32;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ __align__(16) unsigned char teachers[kGroups * (TN_OUTCOMES_MAX_IDS * 20 + 16)];
     pdl_trigger();
     Group<32> g(nullptr);
     const int group = threadIdx.x / 32;
     const int64_t row = (int64_t)blockIdx.x * kGroups + group;
-    Teacher te(teachers + group * (TN_OUTCOMES_MAX_IDS * 20 + 16), a.teacher.count);
-    uint4 *hold = reinterpret_cast<uint4 *>(smem) + group * a.r.seg_vecs;
     const int n = a.teacher.count;
+    uint4 *hold = reinterpret_cast<uint4 *>(smem) + group * a.r.seg_vecs;
+    unsigned char *lists = smem + kGroups * a.r.seg_vecs * kOutVecBytes + group * (teacher_bytes(n) + repeat_bytes(n));
+    Teacher te(lists, n);
     pdl_wait();
     if (row >= a.r.rows) return;
     const Slice<TYPE, MASK, 32> s(a.r, row, 0);
 #pragma unroll 1
     for (int i = 0; i < s.steps; ++i) copy_step<TYPE, MASK, 32>(s, hold, i * kU * 32, g.t);
     te.read(g, a.teacher, a.r, s.r, row, true);
-    Sums<TYPE> sum = sum_slice<TYPE, 32, MASK, UNIT>(s, hold, g.t, a.r);
+    Sums<TYPE> sum = sum_slice<TYPE, 32, MASK, UNIT>(s, hold, g.t, a.r, 0);
     combine(g, sum, a.r.c2);
     g.sync();
     te.normalise(n);
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
     for (int i = 0; i < s.steps; ++i) grad_step<TYPE, 32, MASK>(s, hold, i * kU * 32, g.t, c, dense, out);
     g.sync();
     grad_ids<TYPE>(g, s.r, c, out, te.id, te.q, -1.f, n, s.first, s.first + (int64_t)s.nv * E,
-                   reinterpret_cast<const typename En::T *>(hold), s.first + (int64_t)s.lo * E,
+                   lists + teacher_bytes(n), reinterpret_cast<const typename En::T *>(hold), s.first + (int64_t)s.lo * E,
                    s.first + (int64_t)s.hi * E);
     const float loss = teacher_loss<TYPE>(n, a.r, te, logz);
     if (g.t == 0) {
@@ -267,7 +270,9 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
 // take their place.  What follows from a row but has no hurry (the entries at
 // the teacher's outcomes, which others' dense stores must precede) waits for
 // the next row's barrier; the next row's teacher is fetched one row ahead.
-template <int TYPE, bool MASK, bool UNIT>
+// TWO: shared memory for two slices, so that the next row's copies start with
+// this row's sums instead of with its stores.
+template <int TYPE, bool TWO, bool MASK, bool UNIT>
 __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const __grid_constant__ OutStep a) {
     using En = Entry<TYPE>;
     using T = typename En::T;
@@ -280,24 +285,33 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
     const uint32_t ranks = (uint32_t)a.r.segs, clusters = gridDim.x / ranks;
     const int rank = blockIdx.x % ranks, n = a.teacher.count;
     int64_t row = blockIdx.x / ranks;
-    uint4 *hold = reinterpret_cast<uint4 *>(smem);
-    unsigned char *te_base = smem + a.r.seg_vecs * kOutVecBytes;
+    uint4 *hold0 = reinterpret_cast<uint4 *>(smem);
+    unsigned char *te_base = smem + (TWO ? 2 : 1) * a.r.seg_vecs * kOutVecBytes;
+    const auto repeats = [&](int i) {     // of the even and of the odd rows
+        unsigned char *p = te_base + 2 * teacher_bytes(n);
+        return Repeats(p + 2 * repeat_marks(n), p + i * repeat_marks(n), n);
+    };
+    const auto copy_row = [&](const Slice<TYPE, MASK, G> &x, uint4 *to) {
+#pragma unroll 1
+        for (int i = 0; i < x.steps; ++i) copy_step<TYPE, MASK, G>(x, to, i * kU * G, t);
+    };
     // the cluster's CTAs have all started before any writes to another's memory
     if (ranks > 1) cluster_arrive();
     pdl_wait();
 
     Slice<TYPE, MASK, G> s(a.r, row, rank);
-#pragma unroll 1
-    for (int i = 0; i < s.steps; ++i) copy_step<TYPE, MASK, G>(s, hold, i * kU * G, t);
+    copy_row(s, hold0);
     {
         Teacher te(te_base, n);
         if (t < n) {
             Teacher::Item<TYPE> it = Teacher::item<TYPE>(a.teacher, row, t);
             Teacher::look<TYPE>(it, s.r, rank == 0);
             te.settle<TYPE>(t, it, a.teacher, a.r, s.r, row);
+            if (te.id[t] >= 0) repeats(0).put(t, te.id[t]);
         }
         __syncthreads();
-        if (warp == 0) te.normalise(n);
+        if (t < n && te.id[t] >= 0) repeats(0).look(te.id, t, te.id[t]);
+        if (warp == kWarps - 2) te.normalise(n);
     }
     if (ranks > 1) cluster_wait();
     int turn = 0;
@@ -312,10 +326,11 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
         if (more && t < n) it = Teacher::item<TYPE>(a.teacher, next_row, t);
         const float g_loss = a.g_loss[row];
 
-        Sums<TYPE> sum = sum_slice<TYPE, G, MASK, UNIT>(s, hold, t, a.r);
-        float m = sum.z0;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (more && TWO)
+            copy_row(next, hold0 + (turn ^ 1) * a.r.seg_vecs);
+        uint4 *hold = hold0 + (TWO ? turn * a.r.seg_vecs : 0);
+        Sums<TYPE> sum = sum_slice<TYPE, G, MASK, UNIT>(s, hold, t, a.r, more && TWO ? next.steps : 0);
+        float m = warp_max_nan(sum.z0);
         if (sum.z0 != m) sum.move_to(m, a.r.c2);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
@@ -346,9 +361,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
             if (o.z0 != m) o.move_to(m, a.r.c2);
             sum.s += o.s;
         }
-        m = sum.z0;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = warp_max_nan(sum.z0);
         if (sum.z0 != m) sum.move_to(m, a.r.c2);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
@@ -376,25 +389,22 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
         if (more && t < n) {
             Teacher(te_base + (turn ^ 1) * teacher_bytes(n), n)
                 .settle<TYPE>(t, it, a.teacher, a.r, next.r, next_row);
+            if (it.x >= 0) repeats(turn ^ 1).put(t, it.x);
         }
         __syncthreads();
+        if (more && t < n && it.x >= 0)
+            repeats(turn ^ 1).look(Teacher(te_base + (turn ^ 1) * teacher_bytes(n), n).id, t, it.x);
 #pragma unroll 1
         for (int i = 0; i < s.steps; ++i) {
             grad_step<TYPE, G, MASK>(s, hold, i * kU * G, t, c, dense, out);
         }
-        if (more)
-#pragma unroll 1
-            for (int i = 0; i < next.steps; ++i) copy_step<TYPE, MASK, G>(next, hold, i * kU * G, t);
+        if (more && !TWO) copy_row(next, hold0);
+        // (a warp's vote: every lane takes part)
+        float add = here ? te.q[t] : 0.f;
+        const bool lead =
+            warp * 32 >= n || sum_of_equal(te.id, te.q, n, t, id, here && repeats(turn).mark[t], add);
         if (here && v != absent<TYPE>()) {
-            float add = 0.f;
-            bool is_first = true;
-#pragma unroll 4
-            for (int i = 0; i < n; ++i)
-                if (te.id[i] == id) {
-                    is_first = is_first && i >= t;
-                    add += te.q[i];
-                }
-            if (is_first) {
+            if (lead) {
                 fix = to_entry<TYPE>(entry_grad<TYPE>(c, v, -add), x);
                 fix_at = out.p + id * out.cs;
             }
@@ -418,16 +428,10 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
     if (fix_at) *fix_at = fix;
 }
 
-template <int TYPE, bool MASK, bool UNIT>
-cudaError_t launch_step(const OutStep &a, bool warp_rows, cudaStream_t stream) {
-    size_t row_bytes = (size_t)a.r.seg_vecs * kOutVecBytes;
-    if (warp_rows) {
-        const int groups = kOutThreads / 32;
-        return launch_pdl(outcomes_step_warps<TYPE, MASK, UNIT>, dim3((unsigned)((a.r.rows + groups - 1) / groups)),
-                          dim3(kOutThreads), groups * row_bytes, stream, a);
-    }
-    auto *kernel = outcomes_step<TYPE, MASK, UNIT>;
-    row_bytes += 2 * teacher_bytes(a.teacher.count);
+template <int TYPE, bool TWO, bool MASK, bool UNIT>
+cudaError_t launch_clusters(const OutStep &a, cudaStream_t stream) {
+    auto *kernel = outcomes_step<TYPE, TWO, MASK, UNIT>;
+    const size_t row_bytes = (size_t)a.r.seg_vecs * kOutVecBytes * (TWO ? 2 : 1) + step_lists(a.teacher.count);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)row_bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -462,6 +466,23 @@ cudaError_t launch_step(const OutStep &a, bool warp_rows, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)(clusters * a.r.segs));
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int TYPE, bool MASK, bool UNIT>
+cudaError_t launch_step(const OutStep &a, bool warp_rows, cudaStream_t stream) {
+    size_t row_bytes = (size_t)a.r.seg_vecs * kOutVecBytes;
+    if (warp_rows) {
+        const int groups = kOutThreads / 32;
+        auto *kernel = outcomes_step_warps<TYPE, MASK, UNIT>;
+        row_bytes += teacher_bytes(a.teacher.count) + repeat_bytes(a.teacher.count);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)(groups * row_bytes));
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3((unsigned)((a.r.rows + groups - 1) / groups)),
+                          dim3(kOutThreads), groups * row_bytes, stream, a);
+    }
+    return a.two ? launch_clusters<TYPE, true, MASK, UNIT>(a, stream)
+                 : launch_clusters<TYPE, false, MASK, UNIT>(a, stream);
 }
 
 }  // namespace

@@ -363,6 +363,22 @@ def test_many_rows(t, R, V, masked):
 
 
 @pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("t,R,V", [("f16", 4900, 2203), ("c64", 4900, 601), ("f32", 470, 4001)])
+def test_warps_hold_longer_rows(t, R, V, masked):
+    """Rows enough that a warp each is faster than a CTA each; many of the
+    teacher's outcomes are repeated."""
+    import torch
+    rng = np.random.default_rng(V)
+    keep = torch.from_numpy(rng.random((R, V)) < 0.5) if masked else None
+    ids, logits = rand_teacher(rng, R, 90, V)
+    ids[:, ::2] %= 300
+    ids[:, 1::7] = ids[:, :1]
+    given = rand_ids(rng, R, 40, V)
+    given[:, 1::2] = given[:, ::2]
+    run_all(make_rows(rng, R, V, t), t, given, 0, (ids, logits), mask=keep, rng=rng)
+
+
+@pytest.mark.parametrize("masked", [False, True])
 @pytest.mark.parametrize("t,R,V", [("bf16", 30, 70001), ("f32", 21, 90001), ("c64", 9, 150001),
                                    ("f16", 3, 900001), ("f32", 2, 800003)])
 def test_distillation_of_long_rows(t, R, V, masked):
