@@ -101,8 +101,7 @@ TN_API tn_status tn_outcomes_workspace_bytes(const tn_outcomes_t *h, uint64_t *b
 
 /* Bind device memory (256-byte aligned, at least that large, owned by the
  * caller and left alone by everyone else while bound).  Clears its status word
- * and counters (synchronous).  Errors: TN_EINVAL, TN_ENOMEM (too small),
- * TN_ECUDA. */
+ * (synchronous).  Errors: TN_EINVAL, TN_ENOMEM (too small), TN_ECUDA. */
 TN_API tn_status tn_outcomes_set_workspace(tn_outcomes_t *h, void *dev_ptr, uint64_t bytes);
 
 /*
@@ -114,7 +113,8 @@ TN_API tn_status tn_outcomes_set_workspace(tn_outcomes_t *h, void *dev_ptr, uint
  *   top_ids    [rows, n_top]   the n_top <= max_top most likely outcomes
  *   top_logp   [rows, n_top]   and their log probabilities, in descending order
  * All contiguous; given, logp (with n_given = 0) and top_ids, top_logp (with
- * n_top = 0) may be NULL.  The rows are read once, whatever is asked.
+ * n_top = 0) may be NULL.  The rows are read once, but for the few pieces of them
+ * that hold the alternatives.
  * Errors of this and the calls below: TN_EINVAL (arguments), TN_ENOMEM (no
  * workspace), TN_ECUDA (launch).
  */
