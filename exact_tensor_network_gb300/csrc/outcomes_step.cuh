@@ -428,12 +428,31 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
     if (fix_at) *fix_at = fix;
 }
 
+// Lets the kernel use shared memory up to what any step needs (one value for
+// all calls: it is the kernel's, not the launch's), unless that was done on
+// this device.
+template <class Kernel>
+cudaError_t allow_memory(Kernel *kernel, int done, int *device) {
+    cudaError_t e = cudaGetDevice(device);
+    if (e != cudaSuccess || *device == done) return e;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStepSliceMost);
+}
+
 template <int TYPE, bool TWO, bool MASK, bool UNIT>
 cudaError_t launch_clusters(const OutStep &a, cudaStream_t stream) {
     auto *kernel = outcomes_step<TYPE, TWO, MASK, UNIT>;
     const size_t row_bytes = (size_t)a.r.seg_vecs * kOutVecBytes * (TWO ? 2 : 1) + step_lists(a.teacher.count);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)row_bytes);
+    thread_local struct {      // what costs as much as the launch to set or ask
+        int device = -1;
+        size_t bytes = 0;
+        int64_t segs = 0;
+        int most = 0;
+    } known;
+    int device;
+    cudaError_t e = allow_memory(kernel, known.device, &device);
     if (e != cudaSuccess) return e;
+    if (known.device != device) known.bytes = 0;
+    known.device = device;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kStepThreads);
     cfg.dynamicSmemBytes = row_bytes;
@@ -448,11 +467,6 @@ cudaError_t launch_clusters(const OutStep &a, cudaStream_t stream) {
     // as many clusters as run at once: each goes through its share of the rows
     int64_t clusters = a.r.rows;
     if (clusters * a.r.segs > 152) {
-        thread_local struct {
-            size_t bytes = 0;
-            int64_t segs = 0;
-            int most = 0;
-        } known;      // the query costs as much as the launch
         if (known.bytes != row_bytes || known.segs != a.r.segs) {
             cfg.numAttrs = 1;
             cfg.gridDim = dim3((unsigned)a.r.segs);
@@ -475,9 +489,12 @@ cudaError_t launch_step(const OutStep &a, bool warp_rows, cudaStream_t stream) {
         const int groups = kOutThreads / 32;
         auto *kernel = outcomes_step_warps<TYPE, MASK, UNIT>;
         row_bytes += teacher_bytes(a.teacher.count) + repeat_bytes(a.teacher.count);
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)(groups * row_bytes));
-        if (e != cudaSuccess) return e;
+        thread_local int ready = -1;
+        const cudaError_t e = allow_memory(kernel, ready, &ready);
+        if (e != cudaSuccess) {
+            ready = -1;
+            return e;
+        }
         return launch_pdl(kernel, dim3((unsigned)((a.r.rows + groups - 1) / groups)),
                           dim3(kOutThreads), groups * row_bytes, stream, a);
     }

@@ -184,6 +184,7 @@ class Outcomes:
         # the small calls cost what their host side costs: what does not
         # change from call to call is looked up once
         self._torch, self._L = torch, _lib()
+        self._empty, self._f32, self._teacher_types = torch.empty, torch.float32, _types()
         self._r, self._t = tn_rows(), tn_teacher()
         self._rp, self._tp = ctypes.byref(self._r), ctypes.byref(self._t)
 
@@ -248,14 +249,8 @@ class Outcomes:
                 t.record_stream(stream)
         return stream.cuda_stream, stream
 
-    def _alloc(self, stream, fn):
-        if stream is None:
-            return fn()
-        with self._torch.cuda.stream(stream):
-            return fn()
-
     def _vec(self, t, n, name, device, dtype=None):
-        dtype = dtype or self._torch.float32
+        dtype = dtype or self._f32
         if t.dtype is not dtype or t.device != device or t.numel() != n or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} entries on the rows' device")
         return t.data_ptr()
@@ -271,7 +266,7 @@ class Outcomes:
     def _teacher(self, ids, logits, R, device, scale):
         """Check the teacher into self._t."""
         n = self._ids(ids, R, "ids", device)
-        t = _types().get(logits.dtype, TN_TYPE_C64)
+        t = self._teacher_types.get(logits.dtype, TN_TYPE_C64)
         if (t == TN_TYPE_C64 or logits.shape != ids.shape or logits.device != device
                 or not logits.is_contiguous()):
             raise ValueError("the teacher's logits must be a contiguous float32, bfloat16 or float16 "
@@ -279,9 +274,12 @@ class Outcomes:
         s = self._t
         s.ids, s.logits, s.type, s.count, s.scale = ids.data_ptr(), logits.data_ptr(), t, n, scale
 
-    def _grad(self, rows, R, out, device):
+    def _grad(self, rows, R, out, device, stream):
         if out is None:
-            return self._torch.empty((R, self.cols), dtype=self.dtype, device=device)
+            if stream is None:
+                return self._empty((R, self.cols), dtype=self.dtype, device=device)
+            with self._torch.cuda.stream(stream):
+                return self._empty((R, self.cols), dtype=self.dtype, device=device)
         if out.shape != rows.shape or out.dtype is not self.dtype or out.device != device:
             raise ValueError("out must have the rows' shape, type and device")
         if out.is_conj() or out.is_neg():
@@ -326,7 +324,7 @@ class Outcomes:
         return out
 
     def _new_scores(self, R, k, given, dev):
-        empty, f32 = self._torch.empty, self._torch.float32
+        empty, f32 = self._empty, self._f32
         return Scores(empty(R, dtype=f32, device=dev), empty(R, dtype=f32, device=dev),
                       None if given is None else empty(given.shape, dtype=f32, device=dev),
                       empty((R, k), dtype=self._torch.int64, device=dev) if k else None,
@@ -349,14 +347,19 @@ class Outcomes:
             e = self._vec(entropy, R, "entropy", dev)
         sp, on = self._on(dev, stream, (rows, mask, given, logz, entropy, g_logp, g_entropy)
                           if stream is not None else ())
-        g = self._alloc(on, lambda: self._grad(rows, R, out, dev))
+        g = self._grad(rows, R, out, dev, on)
         rs, cs = g.stride()
-        _check(self._L.tn_outcomes_score_grad(self.handle, self._rp, ids, n, z, e, gl, h, g.data_ptr(), rs,
-                                              cs, sp), self.handle)
+        st = self._L.tn_outcomes_score_grad(self.handle, self._rp, ids, n, z, e, gl, h, g.data_ptr(), rs,
+                                            cs, sp)
+        if st:
+            _check(st, self.handle)
         return g
 
-    def _new_loss(self, R, dev):
-        empty, f32 = self._torch.empty, self._torch.float32
+    def _new_loss(self, R, dev, stream):
+        if stream is not None:
+            with self._torch.cuda.stream(stream):
+                return self._new_loss(R, dev, None)
+        empty, f32 = self._empty, self._f32
         return empty(R, dtype=f32, device=dev), empty(R, dtype=f32, device=dev)
 
     def distill(self, rows, ids, logits, mask=None, teacher_scale: float = 1.0, stream=None) -> Distill:
@@ -365,9 +368,10 @@ class Outcomes:
         rows, dev, R = self._rows(rows, mask)
         self._teacher(ids, logits, R, dev, teacher_scale)
         sp, on = self._on(dev, stream, (rows, mask, ids, logits) if stream is not None else ())
-        loss, logz = self._alloc(on, lambda: self._new_loss(R, dev))
-        _check(self._L.tn_outcomes_distill(self.handle, self._rp, self._tp, loss.data_ptr(), logz.data_ptr(),
-                                           sp), self.handle)
+        loss, logz = self._new_loss(R, dev, on)
+        st = self._L.tn_outcomes_distill(self.handle, self._rp, self._tp, loss.data_ptr(), logz.data_ptr(), sp)
+        if st:
+            _check(st, self.handle)
         return Distill(loss, logz)
 
     def distill_grad(self, rows, ids, logits, logz, g_loss, mask=None, teacher_scale: float = 1.0,
@@ -377,10 +381,11 @@ class Outcomes:
         self._teacher(ids, logits, R, dev, teacher_scale)
         z, w = self._vec(logz, R, "logz", dev), self._vec(g_loss, R, "g_loss", dev)
         sp, on = self._on(dev, stream, (rows, mask, ids, logits, logz, g_loss) if stream is not None else ())
-        g = self._alloc(on, lambda: self._grad(rows, R, out, dev))
+        g = self._grad(rows, R, out, dev, on)
         rs, cs = g.stride()
-        _check(self._L.tn_outcomes_distill_grad(self.handle, self._rp, self._tp, z, w, g.data_ptr(), rs, cs,
-                                                sp), self.handle)
+        st = self._L.tn_outcomes_distill_grad(self.handle, self._rp, self._tp, z, w, g.data_ptr(), rs, cs, sp)
+        if st:
+            _check(st, self.handle)
         return g
 
     def distill_step(self, rows, ids, logits, g_loss, mask=None, teacher_scale: float = 1.0, out=None,
@@ -391,11 +396,13 @@ class Outcomes:
         self._teacher(ids, logits, R, dev, teacher_scale)
         w = self._vec(g_loss, R, "g_loss", dev)
         sp, on = self._on(dev, stream, (rows, mask, ids, logits, g_loss) if stream is not None else ())
-        loss, logz = self._alloc(on, lambda: self._new_loss(R, dev))
-        g = self._alloc(on, lambda: self._grad(rows, R, out, dev))
+        loss, logz = self._new_loss(R, dev, on)
+        g = self._grad(rows, R, out, dev, on)
         rs, cs = g.stride()
-        _check(self._L.tn_outcomes_distill_step(self.handle, self._rp, self._tp, w, loss.data_ptr(),
-                                                logz.data_ptr(), g.data_ptr(), rs, cs, sp), self.handle)
+        st = self._L.tn_outcomes_distill_step(self.handle, self._rp, self._tp, w, loss.data_ptr(),
+                                              logz.data_ptr(), g.data_ptr(), rs, cs, sp)
+        if st:
+            _check(st, self.handle)
         return Distill(loss, logz, g)
 
     def check(self) -> None:
