@@ -71,7 +71,7 @@ tn_status cuda_fail(Outcomes &o, cudaError_t e, const char *what) {
 // rows of 16 KB 5.5 against 7.7 and of 10000 rows of 32 KB 132 against 218.
 int64_t warp_vecs(int64_t rows) { return rows > 2 * tn::kOutTarget ? 1024 : tn::kOutWarpVecs; }
 int64_t grad_warp_vecs(int64_t rows) { return rows > 4 * tn::kOutTarget ? 640 : tn::kOutWarpVecs; }
-int64_t step_warp_vecs(int64_t rows) { return rows > tn::kStepCtas * 152 ? 1024 : tn::kOutWarpVecs; }
+int64_t step_warp_vecs(int64_t rows) { return rows > 3 * 152 ? 1024 : tn::kOutWarpVecs; }
 
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
 
@@ -252,9 +252,8 @@ tn_status gradient(Outcomes &o, const tn::OutGrad &a, const tn::OutSplit &s, cud
 }
 
 // CTAs of a cluster that hold a row in shared memory; segs 0: too long.
-tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int32_t count, int32_t *two) {
+tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int32_t count, tn::OutStep *a) {
     tn::OutSplit s = tn::out_split(type, cols, rows, aligned, step_warp_vecs(rows));
-    *two = 0;
     if (s.warp_rows) return s;
     const int64_t bytes = s.vecs * tn::kOutVecBytes, teachers = tn::step_lists(count);
     int64_t c = (bytes + tn::kStepSlice - teachers - 1) / (tn::kStepSlice - teachers);
@@ -263,8 +262,15 @@ tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, 
     while (c < tn::kStepCluster && rows * c < 2 * 152 && s.vecs >= 2 * (c + 1) * tn::kStepThreads) ++c;
     s.segs = c;
     s.seg_vecs = (s.vecs + c - 1) / c;
-    *two = 2 * s.seg_vecs * tn::kOutVecBytes + teachers <= tn::kStepSlice;
-    if (s.seg_vecs * tn::kOutVecBytes + teachers > tn::kStepSliceMost) s.segs = 0;
+    const int64_t slice = s.seg_vecs * tn::kOutVecBytes;
+    // Twice the threads where a CTA waits for others that hold as much: half
+    // the work between two barriers (500x32003 f32 by two CTAs 36 against 39 us,
+    // 1000x50000 f32 by three 95 against 105).  Otherwise what a row costs a
+    // warp besides its vectors counts for more (4096x32000 bf16 by one 99
+    // against 96, 2048x50001 bf16 by two 105 against 95, 2000x16384 amplitudes
+    // by two 125 against 118).  And where the teacher's outcomes need them.
+    a->wide = count > tn::kStepThreads || (slice > (32 << 10) && c >= (type == TN_TYPE_F32 ? 2 : 3));
+    if (slice + teachers > tn::kStepSliceMost) s.segs = 0;
     return s;
 }
 
@@ -470,13 +476,11 @@ tn_status tn_outcomes_distill_step(tn_outcomes_t *h, const tn_rows *rows, const 
     if (st != TN_OK) return st;
     if (rows->rows == 0) return TN_OK;
     if (!loss || !logz) return fail(o.error, TN_EINVAL, "loss and logz are required");
-    int32_t two;
-    const tn::OutSplit s = step_split(o.type, o.cols, rows->rows, aligned(o, rows), teacher->count, &two);
+    tn::OutStep a = {};
+    const tn::OutSplit s = step_split(o.type, o.cols, rows->rows, aligned(o, rows), teacher->count, &a);
     if (s.segs == 0) return step_in_two(h, rows, teacher, g_loss, loss, logz, grad, grad_row_stride,
                                         grad_col_stride, stream);
-    tn::OutStep a = {};
     a.r = rows_of(o, rows, s);
-    a.two = two;
     a.teacher = teacher_of(teacher);
     a.g_loss = g_loss;
     a.loss = loss;

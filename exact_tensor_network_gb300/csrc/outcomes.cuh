@@ -505,7 +505,7 @@ struct Teacher {
     }
     template <int TYPE>
     __device__ __forceinline__ void settle(int j, const Item<TYPE> &t, const OutTeacher &a, const OutRows &rows,
-                                           const Row<TYPE> &r, int64_t row) {
+                                           const Row<TYPE> &r, int64_t row) const {
         const bool in = t.x >= 0 && t.x < r.cols, wrong = !in && t.x != -1;
         const float l = t.l * a.scale;
         const bool used_ = in && t.keep && l != -__builtin_huge_valf();
@@ -528,7 +528,7 @@ struct Teacher {
         }
     }
     // one warp
-    __device__ __forceinline__ void normalise(int count) {
+    __device__ __forceinline__ void normalise(int count) const {
         const int lane = threadIdx.x % 32;
         float top = -__builtin_huge_valf(), total = 0.f;
 #pragma unroll 1

@@ -114,13 +114,11 @@ struct OutStep {
     float *loss, *logz;
     char *grad;
     int64_t grad_row_stride, grad_col_stride;
-    int32_t two;             // shared memory for two slices: the next row's is on its way
+    bool wide;     // CTAs of twice kStepThreads
 };
 
-constexpr int kStepThreads = 256;
-constexpr int kStepCtas = 3;                   // on an SM
-// Shared memory of a CTA for its slice and two teachers: three CTAs on an SM,
-// and one.
+constexpr int kStepThreads = 128;              // or twice that
+// Shared memory of a CTA for its slice and teachers: three CTAs on an SM, and one.
 constexpr int64_t kStepSlice = 73 * 1024;
 constexpr int64_t kStepSliceMost = 222 * 1024;
 constexpr int kStepCluster = 8;

@@ -115,11 +115,10 @@ __device__ __forceinline__ void copy_step(const Slice<TYPE, MASK, G> &s, uint4 *
     copy_commit();
 }
 
-// The sums of a slice, whose copies are the last groups (one a step) but
-// `behind`.
+// The sums of a slice, whose copies are the last groups (one a step).
 template <int TYPE, int G, bool MASK, bool UNIT>
 __device__ __forceinline__ Sums<TYPE> sum_slice(const Slice<TYPE, MASK, G> &s, uint4 *hold, int t,
-                                                const OutRows &a, int behind) {
+                                                const OutRows &a) {
     using En = Entry<TYPE>;
     constexpr int E = En::E;
     typename Row<TYPE>::Keep next_keep[kU];
@@ -142,7 +141,7 @@ __device__ __forceinline__ Sums<TYPE> sum_slice(const Slice<TYPE, MASK, G> &s, u
             for (int u = 0; u < kU; ++u) keep[u] = next_keep[u];
             load_keep(b + kU * G);
         }
-        copy_wait_all_but(s.steps - 1 - i + behind);
+        copy_wait_all_but(s.steps - 1 - i);
         uint4 raw[kU];
         if (s.whole(b, kU * G)) {
 #pragma unroll
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
 #pragma unroll 1
     for (int i = 0; i < s.steps; ++i) copy_step<TYPE, MASK, 32>(s, hold, i * kU * 32, g.t);
     te.read(g, a.teacher, a.r, s.r, row, true);
-    Sums<TYPE> sum = sum_slice<TYPE, 32, MASK, UNIT>(s, hold, g.t, a.r, 0);
+    Sums<TYPE> sum = sum_slice<TYPE, 32, MASK, UNIT>(s, hold, g.t, a.r);
     combine(g, sum, a.r.c2);
     g.sync();
     te.normalise(n);
@@ -270,14 +269,12 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
 // take their place.  What follows from a row but has no hurry (the entries at
 // the teacher's outcomes, which others' dense stores must precede) waits for
 // the next row's barrier; the next row's teacher is fetched one row ahead.
-// TWO: shared memory for two slices, so that the next row's copies start with
-// this row's sums instead of with its stores.
-template <int TYPE, bool TWO, bool MASK, bool UNIT>
-__global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const __grid_constant__ OutStep a) {
+// G threads, one for each of the teacher's outcomes at least.
+template <int TYPE, int G, bool MASK, bool UNIT>
+__global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ OutStep a) {
     using En = Entry<TYPE>;
     using T = typename En::T;
-    constexpr int E = En::E, G = kStepThreads, kWarps = G / 32;
-    static_assert(G >= TN_OUTCOMES_MAX_IDS, "one of the teacher's outcomes a thread");
+    constexpr int E = En::E, kWarps = G / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float2 part[2][kWarps * kStepCluster];
     pdl_trigger();
@@ -285,22 +282,22 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
     const uint32_t ranks = (uint32_t)a.r.segs, clusters = gridDim.x / ranks;
     const int rank = blockIdx.x % ranks, n = a.teacher.count;
     int64_t row = blockIdx.x / ranks;
-    uint4 *hold0 = reinterpret_cast<uint4 *>(smem);
-    unsigned char *te_base = smem + (TWO ? 2 : 1) * a.r.seg_vecs * kOutVecBytes;
+    uint4 *hold = reinterpret_cast<uint4 *>(smem);
+    unsigned char *te_base = smem + a.r.seg_vecs * kOutVecBytes;
     const auto repeats = [&](int i) {     // of the even and of the odd rows
         unsigned char *p = te_base + 2 * teacher_bytes(n);
         return Repeats(p + 2 * repeat_marks(n), p + i * repeat_marks(n), n);
     };
-    const auto copy_row = [&](const Slice<TYPE, MASK, G> &x, uint4 *to) {
+    const auto copy_row = [&](const Slice<TYPE, MASK, G> &x) {
 #pragma unroll 1
-        for (int i = 0; i < x.steps; ++i) copy_step<TYPE, MASK, G>(x, to, i * kU * G, t);
+        for (int i = 0; i < x.steps; ++i) copy_step<TYPE, MASK, G>(x, hold, i * kU * G, t);
     };
     // the cluster's CTAs have all started before any writes to another's memory
     if (ranks > 1) cluster_arrive();
     pdl_wait();
 
     Slice<TYPE, MASK, G> s(a.r, row, rank);
-    copy_row(s, hold0);
+    copy_row(s);
     {
         Teacher te(te_base, n);
         if (t < n) {
@@ -326,10 +323,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
         if (more && t < n) it = Teacher::item<TYPE>(a.teacher, next_row, t);
         const float g_loss = a.g_loss[row];
 
-        if (more && TWO)
-            copy_row(next, hold0 + (turn ^ 1) * a.r.seg_vecs);
-        uint4 *hold = hold0 + (TWO ? turn * a.r.seg_vecs : 0);
-        Sums<TYPE> sum = sum_slice<TYPE, G, MASK, UNIT>(s, hold, t, a.r, more && TWO ? next.steps : 0);
+        Sums<TYPE> sum = sum_slice<TYPE, G, MASK, UNIT>(s, hold, t, a.r);
         float m = warp_max_nan(sum.z0);
         if (sum.z0 != m) sum.move_to(m, a.r.c2);
 #pragma unroll
@@ -386,25 +380,21 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
                 v = row_value<TYPE>(s.r, id);
             }
         }
-        if (more && t < n) {
-            Teacher(te_base + (turn ^ 1) * teacher_bytes(n), n)
-                .settle<TYPE>(t, it, a.teacher, a.r, next.r, next_row);
-            if (it.x >= 0) repeats(turn ^ 1).put(t, it.x);
-        }
+        const Teacher then(te_base + (turn ^ 1) * teacher_bytes(n), n);
+        const bool given = more && t < n && it.x >= 0;
+        if (more && t < n) then.settle<TYPE>(t, it, a.teacher, a.r, next.r, next_row);
+        if (given) repeats(turn ^ 1).put(t, it.x);
         __syncthreads();
-        if (more && t < n && it.x >= 0)
-            repeats(turn ^ 1).look(Teacher(te_base + (turn ^ 1) * teacher_bytes(n), n).id, t, it.x);
+        if (given) repeats(turn ^ 1).look(then.id, t, it.x);
 #pragma unroll 1
         for (int i = 0; i < s.steps; ++i) {
             grad_step<TYPE, G, MASK>(s, hold, i * kU * G, t, c, dense, out);
         }
-        if (more && !TWO) copy_row(next, hold0);
-        // (a warp's vote: every lane takes part)
-        float add = here ? te.q[t] : 0.f;
-        const bool lead =
-            warp * 32 >= n || sum_of_equal(te.id, te.q, n, t, id, here && repeats(turn).mark[t], add);
-        if (here && v != absent<TYPE>()) {
-            if (lead) {
+        if (more) copy_row(next);
+        if (warp * 32 < n) {       // (a warp's votes: every lane takes part)
+            float add = here ? te.q[t] : 0.f;
+            const bool lead = sum_of_equal(te.id, te.q, n, t, id, here && repeats(turn).mark[t], add);
+            if (lead && v != absent<TYPE>()) {
                 fix = to_entry<TYPE>(entry_grad<TYPE>(c, v, -add), x);
                 fix_at = out.p + id * out.cs;
             }
@@ -418,7 +408,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) outcomes_step(const _
                 a.logz[row] = logz;
             }
         }
-        if (warp == kWarps - 2 && more) Teacher(te_base + (turn ^ 1) * teacher_bytes(n), n).normalise(n);
+        if (warp == kWarps - 2 && more) then.normalise(n);
         if (!more) break;
         row = next_row;
         s = next;
@@ -438,10 +428,10 @@ cudaError_t allow_memory(Kernel *kernel, int done, int *device) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStepSliceMost);
 }
 
-template <int TYPE, bool TWO, bool MASK, bool UNIT>
+template <int TYPE, int G, bool MASK, bool UNIT>
 cudaError_t launch_clusters(const OutStep &a, cudaStream_t stream) {
-    auto *kernel = outcomes_step<TYPE, TWO, MASK, UNIT>;
-    const size_t row_bytes = (size_t)a.r.seg_vecs * kOutVecBytes * (TWO ? 2 : 1) + step_lists(a.teacher.count);
+    auto *kernel = outcomes_step<TYPE, G, MASK, UNIT>;
+    const size_t row_bytes = (size_t)a.r.seg_vecs * kOutVecBytes + step_lists(a.teacher.count);
     thread_local struct {      // what costs as much as the launch to set or ask
         int device = -1;
         size_t bytes = 0;
@@ -454,7 +444,7 @@ cudaError_t launch_clusters(const OutStep &a, cudaStream_t stream) {
     if (known.device != device) known.bytes = 0;
     known.device = device;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kStepThreads);
+    cfg.blockDim = dim3(G);
     cfg.dynamicSmemBytes = row_bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -498,8 +488,8 @@ cudaError_t launch_step(const OutStep &a, bool warp_rows, cudaStream_t stream) {
         return launch_pdl(kernel, dim3((unsigned)((a.r.rows + groups - 1) / groups)),
                           dim3(kOutThreads), groups * row_bytes, stream, a);
     }
-    return a.two ? launch_clusters<TYPE, true, MASK, UNIT>(a, stream)
-                 : launch_clusters<TYPE, false, MASK, UNIT>(a, stream);
+    return a.wide ? launch_clusters<TYPE, 2 * kStepThreads, MASK, UNIT>(a, stream)
+                  : launch_clusters<TYPE, kStepThreads, MASK, UNIT>(a, stream);
 }
 
 }  // namespace
