@@ -222,7 +222,7 @@ tn_status forward(Outcomes &o, tn::OutForward &a, const tn::OutSplit &s, cudaStr
         a.seg_chunks = static_cast<int32_t>(c.seg_chunks);
         a.tree = c.tree;
         int64_t words = c.seg_chunks * s.segs;
-        if (c.tree) words = s.segs <= tn::kOutTree ? s.segs : 4;
+        if (c.tree) words = tn::kOutTree;
         words = (words + 3) / 4 * 4;
         // room for the entries of k vectors; as words, for the maxima of k
         // chunks' vectors and the 256 bins of the cut
@@ -232,8 +232,9 @@ tn_status forward(Outcomes &o, tn::OutForward &a, const tn::OutSplit &s, cudaStr
         cand = (cand + 1) / 2 * 2;
         a.key_words = static_cast<int32_t>(words);
         a.cand_len = static_cast<int32_t>(cand);
-        const int64_t kk = (k + 3) / 4 * 4, pp = (tn::out_most((int)k) + 3) / 4 * 4;
-        a.group_bytes = static_cast<int32_t>(words * 4 + cand * 8 + kk * 8 + pp * 8 + 16);
+        const int64_t kk = (k + 3) / 4 * 4, pp = ((c.tree ? tn::out_room((int)k) : tn::out_most((int)k)) + 3) / 4 * 4;
+        a.group_bytes = static_cast<int32_t>(words * 4 + cand * 8 + kk * 8 + pp * 8 + 16 +
+                                             (c.tree ? 2 * tn::kOutList * 4 : 0));
     }
     a.partials = reinterpret_cast<tn::OutPartial *>(o.ws + o.partial_off);
     a.maxima = reinterpret_cast<uint32_t *>(o.ws + o.maxima_off);

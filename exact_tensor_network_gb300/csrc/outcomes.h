@@ -30,6 +30,11 @@ constexpr int64_t kOutTarget = kOutCtas * 152;   // CTAs that fill the GPU
 // that may stop anywhere between k and here takes a few steps less.
 __host__ __device__ inline int out_most(int k) { return k + k / 8 + 2; }
 
+// Chunks to look at again of a row with a tree; segments and groups of chunks
+// on the way to them.
+constexpr int kOutList = 1024;
+__host__ __device__ inline int out_room(int k) { return 2 * k + 32; }
+
 inline int out_entry_bytes(int32_t type) { return type == TN_TYPE_C64 ? 8 : type == TN_TYPE_F32 ? 4 : 2; }
 
 // How a batch of rows is cut: `segs` segments of `seg_vecs` vectors a row.

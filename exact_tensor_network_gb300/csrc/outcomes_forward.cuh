@@ -550,16 +550,18 @@ struct Scratch {
     uint32_t *keys;       // maxima (key_words)
     uint64_t *cand;       // candidates (cand_len)
     uint64_t *best;       // the k best, in order
-    uint32_t *pos, *pos2; // out_most(k) chunks each
+    uint32_t *pos, *pos2; // chunks: out_most(k) each, of a tree out_room(k)
     uint32_t *n;          // counters
+    uint32_t *lists;      // of a tree: segments and groups of chunks
     __device__ __forceinline__ Scratch(unsigned char *base, const OutForward &a) {
-        const int kk = (a.n_top + 3) / 4 * 4, pp = (out_most(a.n_top) + 3) / 4 * 4;
+        const int kk = (a.n_top + 3) / 4 * 4, pp = ((a.tree ? out_room(a.n_top) : out_most(a.n_top)) + 3) / 4 * 4;
         keys = reinterpret_cast<uint32_t *>(base);
         cand = reinterpret_cast<uint64_t *>(keys + a.key_words);
         best = cand + a.cand_len;
         pos = reinterpret_cast<uint32_t *>(best + kk);
         pos2 = pos + pp;
         n = pos2 + pp;
+        lists = n + 4;
     }
     // First k (up to `most`) of keys[0 .. nk) into pos; returns their number,
     // `least` a lower bound of the k best entries.
@@ -974,55 +976,80 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     }
 }
 
-// The chunks to read again of a row with a tree of maxima: the first k
-// segments (or a few more), their groups of 32 chunks with a maximum of at
-// least the cut's, those groups' chunks likewise; into sm.pos in ascending
-// order.  Returns their number, or -1: more than there is room for.
+// The maxima of a row with a tree: of segment i, of group i % 32 of 32 chunks
+// of the segment list[i / 32], or of chunk i % 32 of the group list[i / 32]
+// (as segment 32 + group), 0 for none.
+struct Tree {
+    const uint32_t *supers, *maxima;
+    int chunks;             // of a segment
+    const uint32_t *list;
+    __device__ __forceinline__ int chunk(int i) const {
+        const uint32_t x = list[i >> 5], c = (x & 31) * 32 + (i & 31);
+        return c < (uint32_t)chunks ? (int)((x >> 5) * chunks + c) : -1;
+    }
+    __device__ __forceinline__ uint32_t at(int level, int i) const {
+        if (level == 0) return __ldcg(supers + (int64_t)i * 33);
+        if (level == 1) return __ldcg(supers + (int64_t)list[i >> 5] * 33 + 1 + (i & 31));
+        const int c = chunk(i);
+        return c < 0 ? 0u : __ldcg(maxima + c);
+    }
+};
+
+// A lower bound of the k best entries from n maxima of a level, taken together
+// as many in a row as leaves kOutTree of them; 1 if they are not enough.
+template <int G>
+__device__ __noinline__ uint32_t tree_bound(Group<G> g, const Scratch sm, const Tree tree, int level, int n, int k) {
+    const int per = (n + kOutTree - 1) / kOutTree, nk = (n + per - 1) / per;
+#pragma unroll 1
+    for (int i = g.t; i < nk; i += G) {
+        uint32_t x = 0;
+#pragma unroll 4
+        for (int j = i * per; j < min(n, (i + 1) * per); ++j) x = max(x, tree.at(level, j));
+        sm.keys[i] = x;
+    }
+    g.sync();
+    uint32_t least;
+    sm.cut(g, nk, k, out_most(k), least);
+    g.sync();
+    return least;
+}
+
+// The chunks to read again of a row with a tree of maxima, into sm.pos in
+// ascending order: the segments with a maximum of at least a bound, their
+// groups of 32 chunks, those groups' chunks.  The bound is a cut of the first
+// level that has four times as many maxima as there are alternatives (about
+// 1.15 k chunks lie above it then, unless entries are equal or sorted).  Returns
+// their number, or -1: more than there is room for.
 template <int G>
 __device__ __noinline__ int chunks_of_tree(Group<G> g, const Scratch sm, const OutForward &a, int64_t row,
                                            uint32_t &least) {
-    const int k = a.n_top, segs = (int)a.r.segs, room = out_most(k), len = 2 * a.cand_len;
-    const uint32_t *supers = a.supers + row * segs * 33;
-    const uint32_t *maxima = a.maxima + row * segs * a.seg_chunks;
-    int nc;
-    if (segs <= a.key_words) {
-#pragma unroll 4
-        for (int i = g.t; i < segs; i += G) sm.keys[i] = __ldcg(supers + (int64_t)i * 33);
+    const int k = a.n_top, segs = (int)a.r.segs, room = out_room(k);
+    uint32_t *groups = sm.lists + kOutList;
+    Tree tree = {a.supers + row * segs * 33, a.maxima + row * segs * a.seg_chunks, a.seg_chunks, sm.lists};
+    // the n maxima of a level that reach the bound
+    const auto gather = [&](int level, int n, uint32_t *out, int len) {
+        if (g.t == 0) sm.n[0] = 0;
         g.sync();
-        nc = sm.cut(g, segs, k, room, least);
-    } else {
-        nc = select(g, [=](int i) { return __ldcg(supers + (int64_t)i * 33); }, segs, k, sm.pos);
-        uint32_t inv = 0;
-#pragma unroll 1
-        for (int i = g.t; i < nc; i += G) inv = max(inv, ~__ldcg(supers + (int64_t)sm.pos[i] * 33));
-        inv = g.max(inv);
-        least = nc ? ~inv : 1u;
-    }
-    // groups of 32 chunks, as (place in sm.pos) 32 + group
-    uint32_t *list = reinterpret_cast<uint32_t *>(sm.cand);
-    g.sync();
-    if (g.t == 0) sm.n[0] = sm.n[3] = 0;
-    g.sync();
 #pragma unroll 4
-    for (int i = g.t; i < nc * 32; i += G)
-        if (__ldcg(supers + (int64_t)sm.pos[i >> 5] * 33 + 1 + (i & 31)) >= least) {
-            const uint32_t at = atomicAdd(sm.n + 3, 1u);
-            if (at < (uint32_t)len) list[at] = i;
-        }
-    g.sync();
-    const int ng = (int)sm.n[3];
-    if (ng > len) return -1;
-#pragma unroll 4
-    for (int i = g.t; i < ng * 32; i += G) {
-        const uint32_t x = list[i >> 5], c = (x & 31) * 32 + (i & 31);
-        const uint32_t at = sm.pos[x >> 5] * a.seg_chunks + c;
-        if (c < (uint32_t)a.seg_chunks && __ldcg(maxima + at) >= least) {
-            const uint32_t w = atomicAdd(sm.n, 1u);
-            if (w < (uint32_t)room) sm.pos2[w] = at;
-        }
-    }
-    g.sync();
-    const int n = (int)sm.n[0];
+        for (int i = g.t; i < n; i += G)
+            if (tree.at(level, i) >= least) {
+                const uint32_t at = atomicAdd(sm.n, 1u);
+                if (at < (uint32_t)len)
+                    out[at] = level == 0 ? i : level == 1 ? tree.list[i >> 5] * 32 + (i & 31) : tree.chunk(i);
+            }
+        g.sync();
+        return (int)min(sm.n[0], 0x7fffffffu);
+    };
+    least = 1;
+    if (segs >= 4 * k) least = tree_bound(g, sm, tree, 0, segs, k);
+    const int ns = gather(0, segs, sm.lists, kOutList);
+    if (ns > kOutList) return -1;
+    if (least == 1 && ns * ((a.seg_chunks + 31) / 32) >= 4 * k) least = tree_bound(g, sm, tree, 1, ns * 32, k);
+    const int ng = gather(1, ns * 32, groups, kOutList);
+    if (ng > kOutList) return -1;
+    tree.list = groups;
+    if (least == 1) least = tree_bound(g, sm, tree, 2, ng * 32, k);
+    const int n = gather(2, ng * 32, sm.pos2, room);
     if (n > room) return -1;
 #pragma unroll 1
     for (int i = g.t; i < n; i += G) {

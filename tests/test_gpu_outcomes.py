@@ -346,6 +346,28 @@ def test_alternatives_of_very_long_rows(t, order, k):
     run_all(rows, t, rand_ids(rng, R, 2, V), k, None, mask=mask, rng=rng)
 
 
+@pytest.mark.parametrize("k", [1, 60, 128])
+@pytest.mark.parametrize("t,R,V", [("f32", 40, 300007), ("bf16", 64, 400001), ("c64", 3, 3000001),
+                                   ("f32", 700, 40001)])
+@pytest.mark.parametrize("part", ["all", "start", "place"])
+def test_alternatives_of_a_part(t, R, V, k, part):
+    """Long rows in few and in many segments, with entries everywhere, at the
+    start only, or at one place only."""
+    import torch
+    rng = np.random.default_rng(V + k)
+    if R * V > 2e7 and part != "all":
+        R //= 10
+    mask = None
+    if part != "all":
+        keep = np.zeros((1, V), bool)
+        if part == "start":
+            keep[0, :V // 20] = True
+        else:
+            keep[0, V // 2:V // 2 + 900] = True
+        mask = torch.from_numpy(keep)
+    run_all(make_rows(rng, R, V, t), t, None, k, None, mask=mask, rng=rng)
+
+
 @pytest.mark.parametrize("masked", [False, True])
 @pytest.mark.parametrize("t,R,V", [("bf16", 2500, 2601), ("c64", 1300, 1031), ("f32", 700, 5003)])
 def test_many_rows(t, R, V, masked):
