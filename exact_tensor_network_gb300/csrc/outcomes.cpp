@@ -21,9 +21,13 @@ OutSplit out_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int64
     s.segs = 1;
     s.seg_vecs = s.vecs;
     if (s.warp_rows) return s;
-    // a CTA of less than two vectors a thread gains nothing
+    // One wave of CTAs where whole segments fill five sixths of it, else up to two
+    // (64x131072 bf16 one 8.0 us, half of one 10.1, two 8.2, four 10.1; 700x50001
+    // bf16 one, 58 % full, 22.7, two 16.7; 1024x50001 amplitudes one, 84 % full, 67,
+    // two 71).  A CTA of less than two vectors a thread gains nothing.
     const int64_t target = kOutTarget;
-    int64_t want = rows >= target ? 1 : target / rows;      // one wave of CTAs
+    int64_t want = rows >= target ? 1 : target / rows;
+    if (rows < target && rows * want * 6 < target * 5) want = 2 * target / rows;
     const int64_t most = (s.vecs + 2 * kOutThreads - 1) / (2 * kOutThreads);
     if (want > most) want = most;
     const int64_t least = (s.vecs + kOutSegVecs - 1) / kOutSegVecs;
@@ -43,8 +47,6 @@ namespace {
 using tn::Outcomes;
 
 thread_local char g_error[256] = {0};
-
-constexpr int64_t kStepBatch = 48 << 20;   // bytes of rows between a forward pass and its gradient
 
 tn_status fail(char (&buf)[256], tn_status st, const char *fmt, ...) {
     va_list ap;
@@ -75,10 +77,13 @@ int64_t step_warp_vecs(int64_t rows) { return rows > 3 * 152 ? 1024 : tn::kOutWa
 
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
 
-// How the maxima of k alternatives lie.  Chunks are as large as leaves four
-// times as many of them as alternatives (a cut well inside) and at most 1024
-// vectors to read again (4096 for the larger groups that few rows have), but
-// no more of them in a segment than kOutKeys.
+// How the maxima of k alternatives lie.  Chunks are as large as leaves twice as
+// many of them as alternatives (a cut well inside) and at most 1024 vectors to
+// read again (4096 for the larger groups that few rows have), but no more of
+// them in a segment than kOutKeys.  Measured, chunks of 64, 32, 16, 8, 4 vectors:
+// 2048x50001 bf16 with 20 alternatives 73, 65, 86, 84, 84 us, with 128 (a tenth
+// of a row's vectors read again at 4) 3285, 253, 125, 113, 109; 300x65536 f32
+// with 64 28.5, 27.7, 31.6, 30.3, 46.2.
 struct Chunks {
     int log;
     int64_t seg_chunks;     // of a segment
@@ -89,7 +94,7 @@ Chunks chunks_of(const tn::OutSplit &s, int64_t rows, int64_t k) {
     Chunks c;
     const int64_t again = rows >= tn::kOutTarget / 4 ? 1024 : 4096;
     c.log = s.warp_rows ? 0 : tn::kOutChunkLog;
-    while (c.log > 0 && (s.vecs >> c.log < 4 * k || (int64_t)tn::out_most((int)k) << c.log > again) &&
+    while (c.log > 0 && (s.vecs >> c.log < 2 * k || (int64_t)tn::out_most((int)k) << c.log > again) &&
            s.seg_vecs <= (int64_t)tn::kOutKeys << (c.log - 1))
         --c.log;
     c.seg_chunks = (s.seg_vecs + (1 << c.log) - 1) >> c.log;
@@ -252,51 +257,38 @@ tn_status gradient(Outcomes &o, const tn::OutGrad &a, const tn::OutSplit &s, cud
     return e == cudaSuccess ? TN_OK : cuda_fail(o, e, "launching the gradient");
 }
 
-// CTAs of a cluster that hold a row in shared memory; segs 0: too long.
+// CTAs of a cluster that hold a row in shared memory: a power of two, as others
+// pack badly (2048x100001 bf16 by three 265 us, by four 205; 300x100001 f32 by six
+// 69, by eight 62).  segs 0: better by a forward pass and a gradient, which read
+// the row twice.  That is so
+//  - for slices that leave one or two CTAs an SM: 200x800003 bf16 167 against
+//    227 us, 500x100001 amplitudes 204 against 336, 300x200001 f32 130 against 142;
+//  - for many rows by eight that could almost be by four: 2048x160001 bf16 318
+//    against 375 (but 500x250001 135 against 127);
+//  - for many rows of amplitudes by four or more: 500x25001 62 against 73, 500x60001
+//    127 against 142 (by two 2000x16384 135 against 120).
 tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, int32_t count, tn::OutStep *a) {
     tn::OutSplit s = tn::out_split(type, cols, rows, aligned, step_warp_vecs(rows));
     if (s.warp_rows) return s;
     const int64_t bytes = s.vecs * tn::kOutVecBytes, teachers = tn::step_lists(count);
     int64_t c = (bytes + tn::kStepSlice - teachers - 1) / (tn::kStepSlice - teachers);
-    if (c > tn::kStepCluster) c = tn::kStepCluster;
     // few rows: more CTAs a row, of two vectors a thread at least
     while (c < tn::kStepCluster && rows * c < 2 * 152 && s.vecs >= 2 * (c + 1) * tn::kStepThreads) ++c;
+    c = c <= 2 ? c : c <= 4 ? 4 : tn::kStepCluster;
     s.segs = c;
     s.seg_vecs = (s.vecs + c - 1) / c;
     const int64_t slice = s.seg_vecs * tn::kOutVecBytes;
     // Twice the threads where a CTA waits for others that hold as much: half
     // the work between two barriers (500x32003 f32 by two CTAs 36 against 39 us,
-    // 1000x50000 f32 by three 95 against 105).  Otherwise what a row costs a
+    // 1000x50000 f32 by four 95 against 105).  Otherwise what a row costs a
     // warp besides its vectors counts for more (4096x32000 bf16 by one 99
     // against 96, 2048x50001 bf16 by two 105 against 95, 2000x16384 amplitudes
     // by two 125 against 118).  And where the teacher's outcomes need them.
     a->wide = count > tn::kStepThreads || (slice > (32 << 10) && c >= (type == TN_TYPE_F32 ? 2 : 3));
-    if (slice + teachers > tn::kStepSliceMost) s.segs = 0;
+    const bool many = rows * c > 3 * 152;
+    if (slice + teachers > tn::kStepSlice) s.segs = 0;
+    if (many && (type == TN_TYPE_C64 ? c >= 4 : type != TN_TYPE_F32 && c == 8 && slice < (48 << 10))) s.segs = 0;
     return s;
-}
-
-// Rows that no cluster holds: the forward pass and the gradient, some rows at
-// a time, so that the second finds them in the L2 cache.
-tn_status step_in_two(tn_outcomes_t *h, const tn_rows *rows, const tn_teacher *teacher, const float *g_loss,
-                      float *loss, float *logz, void *grad, int64_t rs, int64_t cs, tn_stream_t stream) {
-    const int64_t size = tn::out_entry_bytes(h->o.type), row_bytes = h->o.cols * size;
-    const int64_t batch = row_bytes >= kStepBatch ? 1 : kStepBatch / row_bytes;
-    for (int64_t i = 0; i < rows->rows; i += batch) {
-        tn_rows r = *rows;
-        tn_teacher t = *teacher;
-        r.rows = rows->rows - i < batch ? rows->rows - i : batch;
-        r.data = static_cast<const char *>(rows->data) + i * rows->row_stride * size;
-        if (rows->mask) r.mask = rows->mask + i * rows->mask_row_stride;
-        t.ids = teacher->ids + i * teacher->count;
-        t.logits = static_cast<const char *>(teacher->logits) +
-                   i * teacher->count * tn::out_entry_bytes(teacher->type);
-        tn_status st = tn_outcomes_distill(h, &r, &t, loss + i, logz + i, stream);
-        if (st == TN_OK)
-            st = tn_outcomes_distill_grad(h, &r, &t, logz + i, g_loss + i,
-                                          static_cast<char *>(grad) + i * rs * size, rs, cs, stream);
-        if (st != TN_OK) return st;
-    }
-    return TN_OK;
 }
 
 }  // namespace
@@ -479,8 +471,12 @@ tn_status tn_outcomes_distill_step(tn_outcomes_t *h, const tn_rows *rows, const 
     if (!loss || !logz) return fail(o.error, TN_EINVAL, "loss and logz are required");
     tn::OutStep a = {};
     const tn::OutSplit s = step_split(o.type, o.cols, rows->rows, aligned(o, rows), teacher->count, &a);
-    if (s.segs == 0) return step_in_two(h, rows, teacher, g_loss, loss, logz, grad, grad_row_stride,
-                                        grad_col_stride, stream);
+    if (s.segs == 0) {      // rows that no cluster holds: two passes
+        st = tn_outcomes_distill(h, rows, teacher, loss, logz, stream);
+        if (st != TN_OK) return st;
+        return tn_outcomes_distill_grad(h, rows, teacher, logz, g_loss, grad, grad_row_stride, grad_col_stride,
+                                        stream);
+    }
     a.r = rows_of(o, rows, s);
     a.teacher = teacher_of(teacher);
     a.g_loss = g_loss;

@@ -123,9 +123,10 @@ struct OutStep {
 };
 
 constexpr int kStepThreads = 128;              // or twice that
-// Shared memory of a CTA for its slice and teachers: three CTAs on an SM, and one.
+// Shared memory of a CTA for its slice and teachers: three CTAs on an SM.
 constexpr int64_t kStepSlice = 73 * 1024;
-constexpr int64_t kStepSliceMost = 222 * 1024;
+// The most that any step's CTA asks for (four warps' rows and teachers).
+constexpr int64_t kStepMemory = 4 * (16 * 1024 + 8 * 1024);
 constexpr int kStepCluster = 8;
 
 // Shared memory of a row's teacher (see Teacher): id, q, log q and value of

@@ -1190,14 +1190,17 @@ cudaError_t launch_forward(const OutForward &a, bool warp_rows, cudaStream_t str
     cudaError_t e = launch_rows(outcomes_forward<TYPE, kOutThreads, false, MASK, ENT, UNIT>, a.r.rows * a.r.segs, kOutThreads,
                                 keys, a, stream);
     if (e != cudaSuccess || !a.finish) return e;
-    // many rows: a warp each, if their maxima fit its registers; few: as many
-    // threads as help one
+    // Many rows: a warp each, if their maxima fit its registers; few: as many
+    // threads as help one.  A warp, 128 and 512 threads: 2048x50001 bf16 with one
+    // alternative 54, 60, 118 us; 1000x50001 with 20 47, 43, 71; 200x50001 with one
+    // 15.8, 13.9, 18.3; 64x131072 with 20 38, 17.7, 13.3; 300x65536 f32 with 64
+    // 28.5, 28.9, 28.3, masked 128 and 512 threads 39.4, 37.4.
     if constexpr (ENT) {
-        if (a.r.rows >= kOutTarget / 4 && a.r.segs * a.seg_chunks <= kOutWarpVecs)
+        if (a.r.rows >= kOutTarget && a.r.segs * a.seg_chunks <= kOutWarpVecs)
             return launch_rows(outcomes_finish<TYPE, 32, MASK, ENT>, (a.r.rows + 3) / 4, 128, (size_t)4 * a.group_bytes,
                                a, stream);
     }
-    if (a.r.rows >= kOutTarget / 4)
+    if (a.r.rows > (a.n_top < 32 ? 152 : 2 * 152))
         return launch_rows(outcomes_finish<TYPE, 128, MASK, ENT>, a.r.rows, 128, a.group_bytes, a, stream);
     return launch_rows(outcomes_finish<TYPE, 512, MASK, ENT>, a.r.rows, 512, a.group_bytes, a, stream);
 }

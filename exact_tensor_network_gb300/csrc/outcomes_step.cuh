@@ -425,7 +425,7 @@ template <class Kernel>
 cudaError_t allow_memory(Kernel *kernel, int done, int *device) {
     cudaError_t e = cudaGetDevice(device);
     if (e != cudaSuccess || *device == done) return e;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStepSliceMost);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStepMemory);
 }
 
 template <int TYPE, int G, bool MASK, bool UNIT>
