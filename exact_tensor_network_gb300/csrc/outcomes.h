@@ -13,7 +13,7 @@ namespace tn {
 
 constexpr int kOutVecBytes = 16;        // entries are read 16 bytes at a time
 constexpr int kOutThreads = 128;        // CTA of the kernels below
-constexpr int kOutCtas = 8;             // that many on an SM (64 registers a thread)
+constexpr int kOutCtas = 8;             // that many on an SM (64 registers a thread; 6, 10 and 12 were slower)
 // Rows of at most this many 16-byte vectors (4 KiB) belong to one warp each:
 // a CTA would have no second vector for its threads.
 constexpr int kOutWarpVecs = 256;

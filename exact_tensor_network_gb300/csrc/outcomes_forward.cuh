@@ -20,12 +20,22 @@
 // row the maxima form a tree (of 32 chunks, of a segment), and the search goes
 // down it.
 //
-// Rows of up to 4 KiB are a warp's.  Longer ones are one CTA's, or cut into
-// segments of one CTA each where there are few; a second, dependent kernel
-// then joins the segments in order and searches for the alternatives.  It is a
-// kernel of its own because the search is a few thousand instructions that
-// only the first of a row's warps would run: beside the streaming loop they
-// cost that loop its registers and its instruction cache.
+// Rows of up to 4 KiB (where there are many, 16 KiB) are a warp's.  Longer ones
+// are one CTA's, or cut into segments of one CTA each where there are few; a
+// second, dependent kernel then joins the segments in order and searches for
+// the alternatives.  It is a kernel of its own because the search is a few
+// thousand instructions that only the first of a row's warps would run: beside
+// the streaming loop they cost that loop its registers and its instruction
+// cache.
+//
+// What bounds it.  32-bit entries: memory (2^26 amplitudes 83 us, 6.4 TB/s;
+// 2048x50001 f32 67 us, 6.1 TB/s).  16-bit ones: twice the entries a byte, so
+// issue slots as well (2048x50001 bf16 42 us, 4.9 TB/s at 57 % of the issue
+// slots; without the entropy, for the loss, 39 us).  Alternatives: their
+// maxima, and the search, which is latency, about ten dependent steps (the
+// same with one alternative 54 us, with 20 65; 1x32768 with 5 8.7 us, without
+// 4.5).  Short rows: what a row costs besides its entries (20000 rows of 64
+// amplitudes 10 us, with 4 alternatives 16).
 #pragma once
 
 #include "outcomes.cuh"

