@@ -65,12 +65,14 @@ tn_status cuda_fail(Outcomes &o, cudaError_t e, const char *what) {
 // a warp's (what a row costs besides its vectors is paid once, not once for
 // each of four or eight warps), if there are rows enough for all warps.
 // Measured, CTA against warp a row: scores of 20000 rows of 6 KB 44 against
-// 28 us, of 10 KB 58 against 41, of 10000 rows of 16 KB 35 against 32, but of
-// 1300 rows 6.2 against 7.6; gradients of 20000 rows of 6 KB 65 against 45 us, of
+// 28 us (with five alternatives 92 against 61), of 10 KB 58 against 41, of 10000
+// rows of 16 KB 35 against 32 (66 against 53), but of 1300 rows 6.2 against 7.6 (15.5
+// against 15.6), of 10000 rows of 24 KB 45 against 44; gradients of 20000 rows of 6 KB 65 against 45 us, of
 // 10 KB 85 against 70, but of 10000 rows of 16 KB 56 against 59 and of 2500
 // rows 10.9 against 15.5; training steps of 20000 rows of 4 KB 173 against 41 us,
 // of 8 KB 181 against 64, of 10000 rows of 16 KB 101 against 73, but of 100
 // rows of 16 KB 5.5 against 7.7 and of 10000 rows of 32 KB 132 against 218.
+// None of these is below the limit that the workspace is made for.
 int64_t warp_vecs(int64_t rows) { return rows > 2 * tn::kOutTarget ? 1024 : tn::kOutWarpVecs; }
 int64_t grad_warp_vecs(int64_t rows) { return rows > 4 * tn::kOutTarget ? 640 : tn::kOutWarpVecs; }
 int64_t step_warp_vecs(int64_t rows) { return rows > 3 * 152 ? 1024 : tn::kOutWarpVecs; }
@@ -93,7 +95,14 @@ struct Chunks {
 Chunks chunks_of(const tn::OutSplit &s, int64_t rows, int64_t k) {
     Chunks c;
     const int64_t again = rows >= tn::kOutTarget / 4 ? 1024 : 4096;
-    c.log = s.warp_rows ? 0 : tn::kOutChunkLog;
+    if (s.warp_rows) {      // what a warp has registers for
+        c.log = 0;
+        while (s.vecs >> c.log > tn::kOutWarpVecs) ++c.log;
+        c.seg_chunks = (s.vecs + (1 << c.log) - 1) >> c.log;
+        c.tree = false;
+        return c;
+    }
+    c.log = tn::kOutChunkLog;
     while (c.log > 0 && (s.vecs >> c.log < 2 * k || (int64_t)tn::out_most((int)k) << c.log > again) &&
            s.seg_vecs <= (int64_t)tn::kOutKeys << (c.log - 1))
         --c.log;
@@ -367,7 +376,7 @@ tn_status tn_outcomes_score(tn_outcomes_t *h, const tn_rows *rows, const int64_t
     if (!logz || !entropy || (n_given > 0 && (!given || !logp)) || (n_top > 0 && (!top_ids || !top_logp)))
         return fail(o.error, TN_EINVAL, "an output or the given outcomes are missing");
     const tn::OutSplit s = tn::out_split(o.type, o.cols, rows->rows, aligned(o, rows),
-                                         n_top > 0 ? tn::kOutWarpVecs : warp_vecs(rows->rows));
+                                         warp_vecs(rows->rows));
     tn::OutForward a = {};
     a.r = rows_of(o, rows, s);
     a.given = given;

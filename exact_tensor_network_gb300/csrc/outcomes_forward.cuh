@@ -786,7 +786,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
     const int64_t v1 = min(all, v0 + a.r.seg_vecs);
     const int nv = static_cast<int>(max((int64_t)0, v1 - v0));   // may be 0 in a row's last segment
     const int k = ENT ? a.n_top : 0;
-    const int log = G > 32 ? a.chunk_log : 0;   // one maximum per 2^log vectors
+    const int log = a.chunk_log;                // one maximum per 2^log vectors
     // vectors [lo, hi) of the segment lie inside the row
     int64_t in0, in1;
     r.inside_range(in0, in1);
@@ -824,7 +824,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
 #pragma unroll 1
                 for (int o = 1; o < 1 << log; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
                 if ((g.lane & ((1 << log) - 1)) == 0 && j < nv) {
-                    if (G == 32) sm.keys[j] = order_key<TYPE>(x);
+                    if (G == 32) sm.keys[j >> log] = order_key<TYPE>(x);
                     else maxima[j >> log] = x;
                 }
             }
@@ -976,8 +976,8 @@ outcomes_forward(const __grid_constant__ OutForward a) {
             }
         } else if (valid) {
             g.sync();
-            found = best_entries<TYPE, MASK>(g, sm, r, nv, k, 0, a.cand_len);
-            for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, 0, logz, ids, lps);
+            found = best_entries<TYPE, MASK>(g, sm, r, (nv + (1 << log) - 1) >> log, k, log, a.cand_len);
+            for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, log, logz, ids, lps);
         }
         for (int i = found + g.t; i < k; i += G) {
             ids[i] = -1;

@@ -384,6 +384,25 @@ def test_many_rows(t, R, V, masked):
             rand_teacher(rng, R, 17, V), mask=keep, rng=rng)
 
 
+@pytest.mark.parametrize("k", [1, 50, 128])
+@pytest.mark.parametrize("t,R,V", [("f16", 2500, 5003), ("c64", 2500, 901), ("f32", 2500, 4090)])
+def test_alternatives_in_a_warp(t, R, V, k):
+    """Rows enough for a warp each, whose maxima lie over two or four
+    vectors; among them equal, sorted, masked and empty ones."""
+    import torch
+    rng = np.random.default_rng(V + k)
+    rows = make_rows(rng, R, V, t)
+    rows[1] = 0.5
+    rows[2, 7:] = 0.0 if t == "c64" else -INF
+    if t != "c64":
+        rows[3] = torch.sort(rows[3].float()).values.to(rows.dtype)
+        rows[4] = torch.sort(rows[4].float(), descending=True).values.to(rows.dtype)
+    keep = rng.random((R, V)) < 0.9
+    keep[5] = False
+    keep[6, 30:] = False
+    run_all(rows, t, None, k, None, mask=torch.from_numpy(keep), rng=rng)
+
+
 @pytest.mark.parametrize("masked", [False, True])
 @pytest.mark.parametrize("t,R,V", [("f16", 4900, 2203), ("c64", 4900, 601), ("f32", 470, 4001)])
 def test_warps_hold_longer_rows(t, R, V, masked):
