@@ -126,7 +126,7 @@ constexpr int kStepThreads = 128;              // or twice that
 // Shared memory of a CTA for its slice and teachers: three CTAs on an SM.
 constexpr int64_t kStepSlice = 73 * 1024;
 // The most that any step's CTA asks for (four warps' rows and teachers).
-constexpr int64_t kStepMemory = 4 * (16 * 1024 + 8 * 1024);
+constexpr int64_t kStepMemory = 4 * (16 * 1024 + 9 * 1024);
 constexpr int kStepCluster = 8;
 
 // Shared memory of a row's teacher (see Teacher): id, q, log q and value of
@@ -142,6 +142,8 @@ __host__ __device__ inline int repeat_slots(int count) {
 }
 __host__ __device__ inline int repeat_marks(int count) { return (count + 15) / 16 * 16; }
 __host__ __device__ inline int repeat_bytes(int count) { return 2 * repeat_slots(count) + repeat_marks(count); }
+// and of rows of one warp, a sum for each id
+__host__ __device__ inline int repeat_sums(int count) { return (count * 4 + 15) / 16 * 16; }
 // Shared memory of a training step's CTA besides its slices: two rows'
 // teachers and marks, one pair of tables.
 __host__ __device__ inline int step_lists(int count) {

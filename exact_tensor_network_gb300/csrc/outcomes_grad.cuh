@@ -245,6 +245,66 @@ __device__ __forceinline__ bool sum_of_equal(const int64_t *ids, const float *ad
     return first;
 }
 
+// The same for a whole list at once, by a warp and whatever it costs with few
+// repeats: sum[j] for each id, the same for equal ones.  The list is taken 32
+// at a time; the first lane of equal ids adds up theirs in order, finds their
+// place in a table (2 n places or more, by linear probing: the index, plus one,
+// of the first with that id) and adds to what came before.  Lists of up to 32
+// need no table.
+__device__ __noinline__ void sums_of_equal(const int64_t *ids, const float *adds, int n, float *sum, uint32_t *table,
+                                           uint8_t *first) {
+    const int lane = threadIdx.x % 32;
+    int slots = 64;
+    while (slots < 2 * n) slots *= 2;
+    if (n > 32) {
+#pragma unroll 1
+        for (int i = lane; i < slots / 4; i += 32) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int j = i0 + lane;
+        const int64_t id = j < n ? ids[j] : -1;
+        const uint32_t peers = __match_any_sync(0xffffffffu, (unsigned long long)id);
+        const int lead = __ffs(peers) - 1;
+        float total = 0.f;
+        int at = j;
+        if (lane == lead && id >= 0) {
+#pragma unroll 1
+            for (uint32_t m = peers; m; m &= m - 1) total += adds[i0 + __ffs(m) - 1];
+            if (n > 32) {
+                uint32_t place = ((uint32_t)id * 2654435769u) >> (__clz(slots) + 1);
+#pragma unroll 1
+                while (true) {       // (at most n places are ever taken)
+                    const uint32_t old = atomicCAS(table + place, 0u, (uint32_t)j + 1);
+                    if (old == 0) break;
+                    if (ids[old - 1] == id) {
+                        at = (int)old - 1;
+                        break;
+                    }
+                    place = (place + 1) & (slots - 1);
+                }
+                if (at != j) total += sum[at];
+                sum[at] = total;
+            }
+        }
+        if (n > 32) {
+            at = __shfl_sync(0xffffffffu, at, lead);
+            if (id >= 0) first[j] = (uint8_t)at;
+        } else {
+            total = __shfl_sync(0xffffffffu, total, lead);
+            if (id >= 0) sum[j] = total;
+        }
+        __syncwarp();
+    }
+    if (n > 32) {
+#pragma unroll 1
+        for (int j = lane; j < n; j += 32)
+            if (ids[j] >= 0 && first[j] != j) sum[j] = sum[first[j]];
+        __syncwarp();
+    }
+}
+
 // The entries with ids among entries [lo, hi), after the dense part; entries
 // [held_lo, held_hi) of the row are at held[entry - lo], masked ones absent.
 // scratch: the tables and marks of n ids.
@@ -256,7 +316,9 @@ __device__ __forceinline__ void grad_ids(const Group<G> &g, const Row<TYPE> &r, 
                                          int64_t held_hi = 0) {
     const Repeats rp(scratch + repeat_marks(n), scratch, n);
     const auto mine = [&](int j) { return j < n && ids[j] >= 0 && ids[j] >= lo && ids[j] < hi; };
-    if (n > 1) {
+    const float *sums = nullptr;       // where all are added up
+    const bool marks = n > (G == 32 ? 32 : 1);
+    if (marks) {
         g.sync();
 #pragma unroll 1
         for (int j = g.t; j < n; j += G)
@@ -267,13 +329,31 @@ __device__ __forceinline__ void grad_ids(const Group<G> &g, const Row<TYPE> &r, 
             if (mine(j)) rp.look(ids, j, ids[j]);
         g.sync();
     }
+    if constexpr (G == 32) {
+        // One marked id costs about a sixteenth of all added up: 20000 rows of 1000
+        // entries with 64 ids (a few of them repeated) take 53 us by the marks and
+        // 72 all added up, with 256 (57 marked) 466 and 231; 60375 of 32 entries
+        // with 64 305 and 100.
+        int marked = 0;
+        if (marks) {
+#pragma unroll 1
+            for (int j0 = 0; j0 < n; j0 += 32)
+                marked += __popc(__ballot_sync(0xffffffffu, mine(j0 + g.t) && rp.mark[j0 + g.t]));
+        }
+        if (n > 1 && (!marks || marked > 16)) {
+            float *to = reinterpret_cast<float *>(scratch + repeat_bytes(n));
+            g.sync();
+            sums_of_equal(ids, adds, n, to, reinterpret_cast<uint32_t *>(scratch + repeat_marks(n)), scratch);
+            sums = to;
+        }
+    }
 #pragma unroll 1
     for (int j0 = 0; j0 < n; j0 += G) {
         const int j = j0 + g.t;
         const bool in = mine(j);
         const int64_t id = in ? ids[j] : -1;
-        float add = in ? adds[j] : 0.f;
-        const bool first = n == 1 || sum_of_equal(ids, adds, n, j, id, in && rp.mark[j], add);
+        float add = in ? (sums ? sums[j] : adds[j]) : 0.f;
+        const bool first = sums || n == 1 || sum_of_equal(ids, adds, n, j, id, in && rp.mark[j], add);
         if (!in || !first) continue;
         typename Entry<TYPE>::T x;
         float v;
@@ -404,7 +484,7 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
     if (n == 0) return;
     g.sync();
     grad_ids<TYPE>(g, r, c, out, ids, adds, a.teacher.count ? -1.f : 1.f, n, v0 * E - r.head, v1 * E - r.head,
-                   lists + kGroups * teacher_bytes(n) + threadIdx.x / G * repeat_bytes(n));
+                   lists + kGroups * teacher_bytes(n) + threadIdx.x / G * (repeat_bytes(n) + repeat_sums(n)));
 }
 
 template <int TYPE, int G, bool MASK>
@@ -412,7 +492,7 @@ cudaError_t launch_grad(const OutGrad &a, cudaStream_t stream) {
     const int64_t items = a.r.rows * a.r.segs;
     const int groups = kOutThreads / G;
     const int n = a.teacher.count ? a.teacher.count : a.n_given;
-    const size_t smem = n ? groups * (teacher_bytes(n) + repeat_bytes(n)) : 0;
+    const size_t smem = n ? groups * (teacher_bytes(n) + repeat_bytes(n) + repeat_sums(n)) : 0;
     return launch_pdl(outcomes_grad<TYPE, G, MASK>, dim3((unsigned)((items + groups - 1) / groups)),
                       dim3(kOutThreads), smem, stream, a);
 }

@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
     const int64_t row = (int64_t)blockIdx.x * kGroups + group;
     const int n = a.teacher.count;
     uint4 *hold = reinterpret_cast<uint4 *>(smem) + group * a.r.seg_vecs;
-    unsigned char *lists = smem + kGroups * a.r.seg_vecs * kOutVecBytes + group * (teacher_bytes(n) + repeat_bytes(n));
+    unsigned char *lists = smem + kGroups * a.r.seg_vecs * kOutVecBytes +
+                           group * (teacher_bytes(n) + repeat_bytes(n) + repeat_sums(n));
     Teacher te(lists, n);
     pdl_wait();
     if (row >= a.r.rows) return;
@@ -488,7 +489,7 @@ cudaError_t launch_step(const OutStep &a, bool warp_rows, cudaStream_t stream) {
     if (warp_rows) {
         const int groups = kOutThreads / 32;
         auto *kernel = outcomes_step_warps<TYPE, MASK, UNIT>;
-        row_bytes += teacher_bytes(a.teacher.count) + repeat_bytes(a.teacher.count);
+        row_bytes += teacher_bytes(a.teacher.count) + repeat_bytes(a.teacher.count) + repeat_sums(a.teacher.count);
         thread_local int ready = -1;
         const cudaError_t e = allow_memory(kernel, ready, &ready);
         if (e != cudaSuccess) {
