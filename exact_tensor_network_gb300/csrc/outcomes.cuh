@@ -231,6 +231,11 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // [0, cols) exist.  Only vectors that lie inside the row are read as such;
 // the others (and every vector of a strided row, where head is 0) entry by
 // entry.
+//
+// Vectors and masks are read past the L1 cache, which they would only pass
+// through: a grid starts before the one that writes its rows has ended, so it
+// may not take them for constant (1 to 3 % on 16-bit rows, whose search reads
+// some vectors twice).
 
 template <int TYPE>
 struct Row {
@@ -251,7 +256,7 @@ struct Row {
         return cs == 1 && e0 >= 0 && e0 + En::E <= cols;
     }
     __device__ __forceinline__ uint4 raw(int64_t e0) const {
-        return __ldg(reinterpret_cast<const uint4 *>(p + e0));
+        return __ldcg(reinterpret_cast<const uint4 *>(p + e0));
     }
     __device__ __forceinline__ bool kept(int64_t e) const { return !m || m[e * mcs] != 0; }
     __device__ __forceinline__ float value(int64_t e) const {
@@ -266,8 +271,8 @@ struct Row {
         return mcs == 1 && (reinterpret_cast<uintptr_t>(m) - head) % En::E == 0;
     }
     __device__ __forceinline__ Keep keep_word(int64_t e0) const {
-        if constexpr (En::E == 2) return __ldg(reinterpret_cast<const uint16_t *>(m + e0));
-        else return __ldg(reinterpret_cast<const Keep *>(m + e0));
+        if constexpr (En::E == 2) return __ldcg(reinterpret_cast<const uint16_t *>(m + e0));
+        else return __ldcg(reinterpret_cast<const Keep *>(m + e0));
     }
     __device__ __forceinline__ Keep keep(int64_t e0) const {
         constexpr int E = En::E;
@@ -276,10 +281,10 @@ struct Row {
                 const uint8_t *q = m + e0;
                 const int off = static_cast<int>(reinterpret_cast<uintptr_t>(q) % E);
                 const uint8_t *b = q - off;
-                if (off == 0) return __ldg(reinterpret_cast<const Keep *>(b));
+                if (off == 0) return __ldcg(reinterpret_cast<const Keep *>(b));
                 if (b >= m && b + 2 * E <= m + cols) {
-                    const Keep lo = __ldg(reinterpret_cast<const Keep *>(b));
-                    const Keep hi = __ldg(reinterpret_cast<const Keep *>(b) + 1);
+                    const Keep lo = __ldcg(reinterpret_cast<const Keep *>(b));
+                    const Keep hi = __ldcg(reinterpret_cast<const Keep *>(b) + 1);
                     return (lo >> (8 * off)) | (hi << (8 * (E - off)));
                 }
             }

@@ -847,13 +847,13 @@ outcomes_forward(const __grid_constant__ OutForward a) {
                 }
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    raw[u] = __ldg(vecs + b + u * 32 + g.lane);
+                    raw[u] = __ldcg(vecs + b + u * 32 + g.lane);
                     En::blank(raw[u], keep[u]);
                 }
             } else {
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    raw[u] = __ldg(vecs + b + u * 32 + g.lane);
+                    raw[u] = __ldcg(vecs + b + u * 32 + g.lane);
             }
         } else {
             // the row's first or last vectors, or a strided row
@@ -862,7 +862,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
                 const int j = b + u * 32 + g.lane;
                 raw[u] = En::absent_vector();
                 if (j >= lo && j < hi && (!MASK || words)) {
-                    raw[u] = __ldg(vecs + j);
+                    raw[u] = __ldcg(vecs + j);
                     if (MASK) En::blank(raw[u], r.keep_word((v0 + j) * E - r.head));
                 } else if (j < nv) {
                     later |= 1u << u;

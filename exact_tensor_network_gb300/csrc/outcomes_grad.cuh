@@ -385,7 +385,7 @@ __device__ __forceinline__ void grad_dense(const Group<G> &g, const Row<TYPE> &r
         uint4 raw[kGradU];
         if (words && out.wide && b >= lo && b + kGradU * G <= hi) {
 #pragma unroll
-            for (int u = 0; u < kGradU; ++u) raw[u] = __ldg(vecs + b + u * G + g.t);
+            for (int u = 0; u < kGradU; ++u) raw[u] = __ldcg(vecs + b + u * G + g.t);
             if (MASK) {
                 typename Row<TYPE>::Keep keep[kGradU];
 #pragma unroll
@@ -403,7 +403,7 @@ __device__ __forceinline__ void grad_dense(const Group<G> &g, const Row<TYPE> &r
         for (int u = 0; u < kGradU; ++u) {
             const int j = b + u * G + g.t;
             if (j >= lo && j < hi && words) {
-                raw[u] = __ldg(vecs + j);
+                raw[u] = __ldcg(vecs + j);
                 if (MASK) En::blank(raw[u], r.keep_word(first + (int64_t)j * E));
             } else if (j < nv) {
                 odd |= 1u << u;
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
 
     RowGrad c;
     c.scale = a.r.scale;
-    c.logz = a.logz[row];
+    c.logz = __ldcg(a.logz + row);
     c.beta = 0.f;
     c.entropy = 0.f;
     if (a.teacher.count) {
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
         c.alpha = -g.sum(total);
         if (a.g_entropy) {
             c.beta = -a.g_entropy[row];
-            c.entropy = a.entropy[row];
+            c.entropy = __ldcg(a.entropy + row);
         }
         c.mult = a.r.scale;
     }
