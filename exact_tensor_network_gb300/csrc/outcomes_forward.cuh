@@ -30,11 +30,11 @@
 //
 // What bounds it.  32-bit entries: memory (2^26 amplitudes 83 us, 6.4 TB/s;
 // 2048x50001 f32 67 us, 6.1 TB/s).  16-bit ones: twice the entries a byte, so
-// issue slots as well (2048x50001 bf16 42 us, 4.9 TB/s at 57 % of the issue
+// issue slots as well (2048x50001 bf16 42 us, 4.8 TB/s at 57 % of the issue
 // slots; without the entropy, for the loss, 39 us).  Alternatives: their
 // maxima, and the search, which is latency, about ten dependent steps (the
-// same with one alternative 54 us, with 20 65; 1x32768 with 5 8.7 us, without
-// 4.5).  Short rows: what a row costs besides its entries (20000 rows of 64
+// same with one alternative 56 us, with 20 67; 1x32768 with 5 8.9 us, without
+// 4.6).  Short rows: what a row costs besides its entries (20000 rows of 64
 // amplitudes 10 us, with 4 alternatives 16).
 #pragma once
 

@@ -168,7 +168,7 @@ class Outcomes:
     Calls are asynchronous on ``stream`` (default: torch's current stream).
     On another stream the caller orders it after the inputs' producers, as for
     any other launch; outputs made by the call belong to that stream, and the
-    inputs are recorded on it.
+    inputs, ``out`` and the workspace are recorded on it.
     """
 
     def __init__(self, cols: int, dtype=None, max_rows: int = 1, top: int = 0, scale: float = 1.0):
@@ -180,7 +180,7 @@ class Outcomes:
         self.handle = tn_outcomes_create(_types()[dtype], int(cols), int(max_rows), int(top), float(scale))
         self.cols, self.dtype, self.max_rows = int(cols), dtype, int(max_rows)
         self.top, self.scale = int(top), float(scale)
-        self._ws = None
+        self._ws, self._ws_streams = None, set()
         # the small calls cost what their host side costs: what does not
         # change from call to call is looked up once
         self._torch, self._L = torch, _lib()
@@ -205,7 +205,7 @@ class Outcomes:
         nbytes = self.workspace_bytes
         ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         tn_outcomes_set_workspace(self.handle, (ws.data_ptr() + 255) // 256 * 256, nbytes)
-        self._ws = ws
+        self._ws, self._ws_streams = ws, set()
         return ws
 
     # -- arguments --
@@ -241,13 +241,23 @@ class Outcomes:
         """(stream handle, torch stream to allocate outputs on or None)."""
         torch = self._torch
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(device.index), None
+            raw = torch._C._cuda_getCurrentRawStream(device.index)
+            if raw not in self._ws_streams:
+                self._use_workspace(torch.cuda.current_stream(device))
+            return raw, None
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         for t in inputs:
             if t is not None:
                 t.record_stream(stream)
+        if stream.cuda_stream not in self._ws_streams:
+            self._use_workspace(stream)
         return stream.cuda_stream, stream
+
+    def _use_workspace(self, stream):
+        # freed with the handle, it must outlive the work on every stream
+        self._ws.record_stream(stream)
+        self._ws_streams.add(stream.cuda_stream)
 
     def _vec(self, t, n, name, device, dtype=None):
         dtype = dtype or self._f32
@@ -296,7 +306,7 @@ class Outcomes:
         n, k = 0, self.top
         if given is not None:
             n = self._ids(given, R, "given", dev)
-        sp, on = self._on(dev, stream, (rows, mask, given) if stream is not None else ())
+        sp, on = self._on(dev, stream, (rows, mask, given, *(out or ())) if stream is not None else ())
         logp = ids = lp = None
         if out is None:
             if on is None:
@@ -345,7 +355,7 @@ class Outcomes:
         if g_entropy is not None:
             h = self._vec(g_entropy, R, "g_entropy", dev)
             e = self._vec(entropy, R, "entropy", dev)
-        sp, on = self._on(dev, stream, (rows, mask, given, logz, entropy, g_logp, g_entropy)
+        sp, on = self._on(dev, stream, (rows, mask, given, logz, entropy, g_logp, g_entropy, out)
                           if stream is not None else ())
         g = self._grad(rows, R, out, dev, on)
         rs, cs = g.stride()
@@ -380,7 +390,8 @@ class Outcomes:
         rows, dev, R = self._rows(rows, mask)
         self._teacher(ids, logits, R, dev, teacher_scale)
         z, w = self._vec(logz, R, "logz", dev), self._vec(g_loss, R, "g_loss", dev)
-        sp, on = self._on(dev, stream, (rows, mask, ids, logits, logz, g_loss) if stream is not None else ())
+        sp, on = self._on(dev, stream, (rows, mask, ids, logits, logz, g_loss, out)
+                          if stream is not None else ())
         g = self._grad(rows, R, out, dev, on)
         rs, cs = g.stride()
         st = self._L.tn_outcomes_distill_grad(self.handle, self._rp, self._tp, z, w, g.data_ptr(), rs, cs, sp)
@@ -395,7 +406,8 @@ class Outcomes:
         rows, dev, R = self._rows(rows, mask)
         self._teacher(ids, logits, R, dev, teacher_scale)
         w = self._vec(g_loss, R, "g_loss", dev)
-        sp, on = self._on(dev, stream, (rows, mask, ids, logits, g_loss) if stream is not None else ())
+        sp, on = self._on(dev, stream, (rows, mask, ids, logits, g_loss, out)
+                          if stream is not None else ())
         loss, logz = self._new_loss(R, dev, on)
         g = self._grad(rows, R, out, dev, on)
         rs, cs = g.stride()

@@ -705,3 +705,28 @@ def test_refusals():
     assert e.value.status == tn.TN_ENOMEM
     torch.cuda.synchronize()
     op.check()
+
+
+def test_handle_may_go_before_its_work():
+    """A handle and its inputs dropped while a side stream still works with
+    them; what is allocated next does not land in their memory."""
+    import torch
+    rng = np.random.default_rng(17)
+    rows = make_rows(rng, 64, 200003, "f32").cuda()
+    want = tn.Outcomes(200003, torch.float32, max_rows=64, top=20).score(rows)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        op = tn.Outcomes(200003, torch.float32, max_rows=64, top=20)
+        op.score(rows)
+        nbytes = op.workspace_bytes
+        side.wait_stream(torch.cuda.current_stream())
+        got = [op.score(rows, stream=side) for _ in range(5)]
+        del op
+        junk = [torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        side.synchronize()
+        torch.cuda.synchronize()
+        del junk
+        for s in got:
+            for x, y in zip(s[:2] + s[3:], want[:2] + want[3:]):
+                assert (x == y).all()
