@@ -82,10 +82,13 @@ bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow
 // How the maxima of k alternatives lie.  Chunks are as large as leaves twice as
 // many of them as alternatives (a cut well inside) and at most 1024 vectors to
 // read again (4096 for the larger groups that few rows have), but no more of
-// them in a segment than kOutKeys.  Measured, chunks of 64, 32, 16, 8, 4 vectors:
-// 2048x50001 bf16 with 20 alternatives 73, 65, 86, 84, 84 us, with 128 (a tenth
-// of a row's vectors read again at 4) 3285, 253, 125, 113, 109; 300x65536 f32
-// with 64 28.5, 27.7, 31.6, 30.3, 46.2.
+// them in a segment than kOutKeys.  32 vectors, a warp's load, are the last that
+// one reduction finds the largest of; they stay for up to three tenths of a row
+// to read again.  Measured, chunks of 64, 32, 16, 8, 4 vectors: 2048x50001 bf16
+// with 20 alternatives 73, 65, 86, 84, 84 us, with 128 (three quarters of a row's
+// vectors read again at 32) 3285, 253, 125, 113, 109; 300x65536 f32 with 64 28.5,
+// 27.7, 31.6, 30.3, 46.2; 32, 16, 8 vectors: 400x65536 f32 with 64 35, 38, 51,
+// 2000x30001 with 64 (31 % of a row at 32) 100, 97, 92.
 struct Chunks {
     int log;
     int64_t seg_chunks;     // of a segment
@@ -103,9 +106,11 @@ Chunks chunks_of(const tn::OutSplit &s, int64_t rows, int64_t k) {
         return c;
     }
     c.log = tn::kOutChunkLog;
-    while (c.log > 0 && (s.vecs >> c.log < 2 * k || (int64_t)tn::out_most((int)k) << c.log > again) &&
-           s.seg_vecs <= (int64_t)tn::kOutKeys << (c.log - 1))
+    while (c.log > 0 && s.seg_vecs <= (int64_t)tn::kOutKeys << (c.log - 1)) {
+        const int64_t most = (int64_t)tn::out_most((int)k) << c.log;
+        if (s.vecs >> c.log >= 2 * k && (most <= again || (c.log == 5 && most * 10 <= s.vecs * 3))) break;
         --c.log;
+    }
     c.seg_chunks = (s.seg_vecs + (1 << c.log) - 1) >> c.log;
     c.tree = c.seg_chunks * s.segs > tn::kOutTree;
     return c;

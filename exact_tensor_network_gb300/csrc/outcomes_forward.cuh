@@ -1103,8 +1103,8 @@ __device__ __noinline__ int exact_chunks_of_tree(Group<G> g, const Scratch sm, c
 // a CTA each in turn.
 template <int G>
 constexpr int finish_threads() { return G == 32 ? 128 : G; }
-template <int TYPE, int G, bool MASK, bool ENT>
-__global__ void __launch_bounds__(finish_threads<G>(), G == 512 ? 1 : 6) outcomes_finish(const __grid_constant__ OutForward a) {
+template <int TYPE, int G, int CTAS, bool MASK, bool ENT>
+__global__ void __launch_bounds__(finish_threads<G>(), CTAS) outcomes_finish(const __grid_constant__ OutForward a) {
     using En = Entry<TYPE>;
     constexpr int E = En::E;
     constexpr float kInf = __builtin_huge_valf();
@@ -1201,18 +1201,22 @@ cudaError_t launch_forward(const OutForward &a, bool warp_rows, cudaStream_t str
                                 keys, a, stream);
     if (e != cudaSuccess || !a.finish) return e;
     // Many rows: a warp each, if their maxima fit its registers; few: as many
-    // threads as help one.  A warp, 128 and 512 threads: 2048x50001 bf16 with one
-    // alternative 54, 60, 118 us; 1000x50001 with 20 47, 43, 71; 200x50001 with one
-    // 15.8, 13.9, 18.3; 64x131072 with 20 38, 17.7, 13.3; 300x65536 f32 with 64
-    // 28.5, 28.9, 28.3, masked 128 and 512 threads 39.4, 37.4.
+    // threads as help one, with all their registers where a row has an SM, or two
+    // such CTAs an SM where the search is long.  A warp, 128 threads, 512: 2048x50001
+    // bf16 with one alternative 54, 60, 118 us; 1000x50001 with 20 47, 43, 71;
+    // 64x131072 with 20 38, 17.7, 13.3.  128, twice 512, 512 threads: 300x65536 f32
+    // with 64 alternatives 29.1, 24.2, 28.3 (masked 39.4, 31.2, 37.4), with 20 22.7,
+    // 20.4, with 5 18.6, 19.5; 64x131072 bf16 with 20 17.7, 14.6, 13.3.
     if constexpr (ENT) {
         if (a.r.rows >= kOutTarget && a.r.segs * a.seg_chunks <= kOutWarpVecs)
-            return launch_rows(outcomes_finish<TYPE, 32, MASK, ENT>, (a.r.rows + 3) / 4, 128, (size_t)4 * a.group_bytes,
+            return launch_rows(outcomes_finish<TYPE, 32, 6, MASK, ENT>, (a.r.rows + 3) / 4, 128, (size_t)4 * a.group_bytes,
                                a, stream);
+        if (a.r.rows > 152 && a.r.rows <= 2 * 152 && a.n_top >= 16)
+            return launch_rows(outcomes_finish<TYPE, 512, 2, MASK, ENT>, a.r.rows, 512, a.group_bytes, a, stream);
     }
-    if (a.r.rows > (a.n_top < 32 ? 152 : 2 * 152))
-        return launch_rows(outcomes_finish<TYPE, 128, MASK, ENT>, a.r.rows, 128, a.group_bytes, a, stream);
-    return launch_rows(outcomes_finish<TYPE, 512, MASK, ENT>, a.r.rows, 512, a.group_bytes, a, stream);
+    if (a.r.rows > 152)
+        return launch_rows(outcomes_finish<TYPE, 128, 6, MASK, ENT>, a.r.rows, 128, a.group_bytes, a, stream);
+    return launch_rows(outcomes_finish<TYPE, 512, 1, MASK, ENT>, a.r.rows, 512, a.group_bytes, a, stream);
 }
 
 template <int TYPE, bool ENT, bool UNIT>
