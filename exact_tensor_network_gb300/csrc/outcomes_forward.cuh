@@ -1048,7 +1048,9 @@ __device__ __noinline__ int chunks_of_tree(Group<G> g, const Scratch sm, const O
                     out[at] = level == 0 ? i : level == 1 ? tree.list[i >> 5] * 32 + (i & 31) : tree.chunk(i);
             }
         g.sync();
-        return (int)min(sm.n[0], 0x7fffffffu);
+        const int found = (int)min(sm.n[0], 0x7fffffffu);
+        g.sync();      // (all have read it: the next level starts by clearing it)
+        return found;
     };
     least = 1;
     if (segs >= 4 * k) least = tree_bound(g, sm, tree, 0, segs, k);

@@ -346,6 +346,24 @@ def test_alternatives_of_very_long_rows(t, order, k):
     run_all(rows, t, rand_ids(rng, R, 2, V), k, None, mask=mask, rng=rng)
 
 
+@pytest.mark.parametrize("t,V,k", [("bf16", 30000001, 3), ("c64", 8000001, 20), ("f32", 16000000, 100)])
+def test_search_of_very_long_rows_does_not_vary(t, V, k):
+    """Rows with four segments an alternative or more: the search goes down
+    its three levels one right after the other.  Every warp has to see every
+    level's count before the next level clears it, in each of many calls."""
+    import torch
+    rows = torch.randn((1, V), generator=torch.Generator().manual_seed(V), dtype=torch.float32)
+    if t == "c64":
+        rows = torch.complex(rows, rows.flip(1)) * V ** -0.5
+    rows = rows.to(torch_type(t)).cuda()
+    op = tn.Outcomes(V, torch_type(t), top=k)
+    got = [op.score(rows) for _ in range(100)]
+    ids, lp = Row(to_np(rows)[0], None, 1.0).top(k)
+    for s in got:
+        assert (to_np(s.top_ids)[0] == ids).all()
+        assert (s.top_logp == got[0].top_logp).all() and (s.logz == got[0].logz).all()
+
+
 @pytest.mark.parametrize("k", [1, 60, 128])
 @pytest.mark.parametrize("t,R,V", [("f32", 40, 300007), ("bf16", 64, 400001), ("c64", 3, 3000001),
                                    ("f32", 700, 40001)])
