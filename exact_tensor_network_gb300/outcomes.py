@@ -163,7 +163,10 @@ class Outcomes:
 
     Rows are CUDA tensors ``[R, cols]`` of any strides (innermost 1 is the
     fast layout) or ``[cols]`` (one row).  ``mask`` is a bool or uint8 tensor
-    that broadcasts to the rows (0 = absent).  Ids are int64.
+    that broadcasts to the rows (0 = absent).  Ids are int64.  All tensors of
+    a call, its stream and the workspace are on the current device; the first
+    call binds a workspace there unless ``bind_workspace`` did, and waits for
+    the device once (so bind it before a call is captured into a graph).
 
     Calls are asynchronous on ``stream`` (default: torch's current stream).
     On another stream the caller orders it after the inputs' producers, as for
@@ -181,9 +184,11 @@ class Outcomes:
         self.cols, self.dtype, self.max_rows = int(cols), dtype, int(max_rows)
         self.top, self.scale = int(top), float(scale)
         self._ws, self._ws_streams = None, set()
+        self._index = None          # of the workspace's device
         # the small calls cost what their host side costs: what does not
         # change from call to call is looked up once
         self._torch, self._L = torch, _lib()
+        self._current_device = torch._C._cuda_getDevice
         self._empty, self._f32, self._teacher_types = torch.empty, torch.float32, _types()
         self._r, self._t = tn_rows(), tn_teacher()
         self._rp, self._tp = ctypes.byref(self._r), ctypes.byref(self._t)
@@ -200,12 +205,15 @@ class Outcomes:
     workspace_bytes = property(lambda self: tn_outcomes_workspace_bytes(self.handle))
 
     def bind_workspace(self, device=None):
-        """Allocate the workspace with torch on ``device`` and bind it."""
+        """Allocate the workspace with torch on ``device`` (default: the
+        current one) and bind it.  Waits for the device."""
         import torch
         nbytes = self.workspace_bytes
-        ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
-        tn_outcomes_set_workspace(self.handle, (ws.data_ptr() + 255) // 256 * 256, nbytes)
-        self._ws, self._ws_streams = ws, set()
+        device = torch.device("cuda" if device is None else device)
+        with torch.cuda.device(device):     # the library clears it on the current device
+            ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+            tn_outcomes_set_workspace(self.handle, (ws.data_ptr() + 255) // 256 * 256, nbytes)
+        self._ws, self._ws_streams, self._index = ws, set(), ws.device.index
         return ws
 
     # -- arguments --
@@ -222,6 +230,14 @@ class Outcomes:
         if rows.is_conj() or rows.is_neg():
             raise ValueError("rows are a lazily conjugated or negated view: resolve it first")
         R, device, s = shape[0], rows.device, self._r
+        # kernels go to the current device, with the workspace's addresses
+        index = device.index
+        if index != self._current_device():
+            raise ValueError(f"rows are on {device}, which is not the current device")
+        if self._ws is None:
+            self.bind_workspace(device)
+        elif index != self._index:
+            raise ValueError(f"rows are on {device}, the workspace is on cuda:{self._index}")
         s.data, s.rows = rows.data_ptr(), R
         s.row_stride, s.col_stride = rows.stride()
         if mask is None:
@@ -233,8 +249,6 @@ class Outcomes:
             mask = mask.expand(R, self.cols)
             s.mask = mask.data_ptr()
             s.mask_row_stride, s.mask_col_stride = mask.stride()
-        if self._ws is None:
-            self.bind_workspace(device)
         return rows, device, R
 
     def _on(self, device, stream, inputs):
@@ -247,6 +261,8 @@ class Outcomes:
             return raw, None
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
+        elif getattr(stream, "device", device) != device:
+            raise ValueError(f"the stream is on {stream.device}, the rows on {device}")
         for t in inputs:
             if t is not None:
                 t.record_stream(stream)

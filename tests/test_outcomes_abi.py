@@ -95,3 +95,68 @@ def test_reference_closed_forms():
     r = Row(z, None, 1.0)
     assert abs(r.distill([0, 1, 2], z.astype(np.float64))) < 1e-12
     assert np.abs(r.distill_grad([0, 1, 2], z.astype(np.float64), 1.0)[0]).max() < 1e-12
+
+
+class _Tensor:
+    """What a call looks at before it launches anything, on any device."""
+
+    def __init__(self, device, shape=(2, 16)):
+        import torch
+        self.device, self.shape, self.dtype, self.is_cuda = torch.device(device), shape, torch.float32, True
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return (self.shape[1], 1)
+
+    def data_ptr(self):
+        return 4096
+
+    def is_conj(self):
+        return False
+
+    is_neg = is_conj
+
+
+class _NoLaunch:
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was reached")
+
+
+@pytest.mark.parametrize("bound, current, rows", [
+    (0, 0, 1),      # rows of another device than the workspace, and not current
+    (0, 1, 1),      # current, but the workspace is elsewhere
+    (0, 1, 0),      # with the workspace, but not current
+    (None, 0, 1),   # not current, nothing bound yet
+])
+def test_rows_of_another_device_are_refused(bound, current, rows, monkeypatch):
+    """On the host, before anything is bound or launched: a kernel would run on
+    the current device with another one's addresses."""
+    import torch
+    op = tn.Outcomes(16, torch.float32, max_rows=2)
+    monkeypatch.setattr(op, "_L", _NoLaunch())
+    monkeypatch.setattr(op, "_current_device", lambda: current, raising=False)
+    monkeypatch.setattr(op, "bind_workspace", lambda device=None: pytest.fail("workspace bound"))
+    if bound is not None:
+        op._ws, op._index = object(), bound
+    x = _Tensor(f"cuda:{rows}")
+    for call in (lambda: op.score(x), lambda: op.score_grad(x, None, None, None, None),
+                 lambda: op.distill(x, None, None), lambda: op.distill_grad(x, None, None, None, None),
+                 lambda: op.distill_step(x, None, None, None)):
+        with pytest.raises(ValueError, match="device|workspace"):
+            call()
+
+
+def test_stream_of_another_device_is_refused(monkeypatch):
+    import torch
+    op = tn.Outcomes(16, torch.float32, max_rows=2)
+    monkeypatch.setattr(op, "_L", _NoLaunch())
+    monkeypatch.setattr(op, "_current_device", lambda: 0, raising=False)
+    op._ws, op._index = object(), 0
+
+    class Stream:
+        cuda_stream, device = 1, torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="stream"):
+        op.score(_Tensor("cuda:0"), stream=Stream())
