@@ -100,7 +100,7 @@ Chunks chunks_of(const tn::OutSplit &s, int64_t rows, int64_t k) {
     const int64_t again = rows >= tn::kOutTarget / 4 ? 1024 : 4096;
     if (s.warp_rows) {      // what a warp has registers for
         c.log = 0;
-        while (s.vecs >> c.log > tn::kOutWarpVecs) ++c.log;
+        while ((s.vecs + (1 << c.log) - 1) >> c.log > tn::kOutWarpVecs) ++c.log;
         c.seg_chunks = (s.vecs + (1 << c.log) - 1) >> c.log;
         c.tree = false;
         return c;

@@ -421,6 +421,21 @@ def test_alternatives_in_a_warp(t, R, V, k):
     run_all(rows, t, None, k, None, mask=torch.from_numpy(keep), rng=rng)
 
 
+@pytest.mark.parametrize("t,V", [(t, V) for t, at in (("bf16", 4097), ("f16", 4097), ("f32", 2049), ("c64", 1025))
+                                 for V in (at - 7, at - 3, at - 1, at, at + 1, at + 7)])
+def test_best_entry_ends_a_warps_row(t, V):
+    """Rows of one warp each around the length at which their maxima double in
+    size (512 vectors, with and without room for a misaligned start): every
+    maximum counts, the one of the row's last vector too."""
+    import torch
+    R = 2500
+    rng = np.random.default_rng(V)
+    rows = make_rows(rng, R, V, t)
+    rows[::2, V - 1] = 40.0
+    rows[::3, V - 2] = 30.0
+    run_all(rows, t, None, 3, None, rng=rng)
+
+
 @pytest.mark.parametrize("masked", [False, True])
 @pytest.mark.parametrize("t,R,V", [("f16", 4900, 2203), ("c64", 4900, 601), ("f32", 470, 4001)])
 def test_warps_hold_longer_rows(t, R, V, masked):
