@@ -108,7 +108,7 @@ __device__ __forceinline__ uint4 dense_grad(const RowGrad &c, const uint4 &raw) 
     float v[E];
     Entry<TYPE>::values(raw, v);
     if constexpr (Entry<TYPE>::kReal) {
-        const float2 scale = make_float2(c.scale, c.scale), lz = make_float2(-c.logz, -c.logz);
+        const float2 lz = make_float2(-c.logz, -c.logz);
         // bf16 reaches below the least p that ex2 gives: p is the square of
         // ex2(d / 2) there, multiplied in turn.  (f16 does not reach that far;
         // f32 rows keep the better p, and p < 2^-126 counts as 0.)
@@ -118,7 +118,10 @@ __device__ __forceinline__ uint4 dense_grad(const RowGrad &c, const uint4 &raw) 
         const float ma = c.mult * c.alpha;
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
-            float2 lp = add2(mul2(make_float2(v[i], v[i + 1]), scale), lz);
+            // (scalar products: they are rounded as log Z's is.  A packed product and a
+            // packed sum become one fused operation, whose lp is the product's
+            // rounding where both are large: p = inf for logits of 1e10.)
+            float2 lp = add2(make_float2(__fmul_rn(v[i], c.scale), __fmul_rn(v[i + 1], c.scale)), lz);
             if constexpr (BETA) lp = make_float2(fmaxf(lp.x, -1e30f), fmaxf(lp.y, -1e30f));
             const float2 d = mul2(lp, l2);
             const float2 p = make_float2(ex2(d.x), ex2(d.y));

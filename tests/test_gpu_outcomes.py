@@ -555,6 +555,39 @@ def test_ids_out_of_range_are_reported(V):
     assert np.isnan(loss[[0, 2]]).all() and np.isfinite(loss[1])
 
 
+@pytest.mark.parametrize("z", [1e10, -1e10, -1e30])
+@pytest.mark.parametrize("scale", [0.7, 1.0, 1.25])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [75, 4001, 50001])
+def test_gradients_of_large_logits(V, t, scale, z):
+    """log p = scale z - log Z with the product rounded, in every entry: where
+    log Z is the rounded product itself, p is 1 and not e to the power of that
+    rounding (512 at 1e10).  Rows without weight have no gradient."""
+    import torch
+    R = 2
+    rng = np.random.default_rng(V)
+    rows = torch.full((R, V), z).to(torch_type(t)).cuda()
+    c = np.float32(scale)
+    logz = rows[:, 0].float() * float(c)
+    given = torch.from_numpy(rand_ids(rng, R, 2, V)).cuda()
+    given[0, 0] = 3
+    g = torch.tensor([[0.75, 0.5], [0.0, 0.0]], device="cuda")
+    h = torch.tensor([0.5, 0.0], device="cuda")
+    op = tn.Outcomes(V, torch_type(t), max_rows=R, scale=scale)
+    zero = torch.zeros(R, device="cuda")
+    total = (g * (given >= 0)).sum(dim=1, keepdim=True)
+    at = torch.zeros((R, V), device="cuda").scatter_add_(1, given.clamp(min=0), g * (given >= 0))
+    for he in (None, h):        # with log p = 0 and an entropy given as 0 it adds nothing
+        got = op.score_grad(rows, given, logz, zero, g, he).float()
+        close(to_np(got), to_np(float(c) * (at - total)), np.full((R, V), 8 * U + OUT_EPS[t]), "score gradient")
+    w = torch.tensor([0.25, 0.0], device="cuda")
+    ids = given[:, :1].contiguous()
+    ids[ids < 0] = 0
+    got = op.distill_grad(rows, ids, torch.zeros((R, 1), device="cuda"), logz, w).float()
+    want = torch.full((R, V), float(c), device="cuda").scatter_add_(1, ids, torch.full((R, 1), -float(c), device="cuda"))
+    close(to_np(got), to_np(want * w[:, None]), np.full((R, V), 8 * U + OUT_EPS[t]), "distill gradient")
+
+
 @pytest.mark.parametrize("t", ["f32", "c64"])
 def test_gradients_against_differences(t):
     """Central differences of the 64-bit scores and loss along single
