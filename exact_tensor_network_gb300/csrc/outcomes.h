@@ -53,7 +53,9 @@ struct OutRows {
     // log p = scale z - log Z.  c2: weights as powers of two, 2^(c2 z) with
     // c2 = scale log2(e), or (amplitudes) 2^(c2 log2 w) with c2 = scale
     float scale, c2;
-    float floor;        // stands for absent logits in the sums, about -2^126 / c2
+    // stands for absent logits in the sums, about -2^126 / max(c2, 1).  Present ones
+    // may lie below it where c2 < 1 (the types end near -2^128).
+    float floor;
     int64_t seg_vecs;
     int64_t segs;
     DevStatus *status;

@@ -98,8 +98,9 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 // done() takes the rounding of ref out again.  Absent entries become `floor`,
 // about -2^126 / c2, so that they add 0 to both sums instead of 0 times -inf.
 // Logits beyond 2^125 / c2 either way (masks written as the type's lowest
-// value) would overflow there: ref = -inf then sends every vector through
-// far(), which works with differences of logits.
+// value) would overflow there, and those below half of `floor` would not be
+// told from absent ones: ref = -inf then sends every vector through far(),
+// which works with differences of logits.
 //
 // Amplitudes: the quotient w / z0 as q = w (1 / z0) with one Newton correction
 // q + (w - q z0) / z0 (Markstein 1990), which makes z0 / z0 exactly 1.  z0 is
@@ -124,14 +125,18 @@ struct Stream {
         s.x = any ? f * s.x : 0.f;
         s.y = any ? f * s.y : 0.f;
     }
+    // Whether a logit can be the reference of the straight way.
+    static __device__ __forceinline__ bool near(float lm, float r, float floor) {
+        return fabsf(r) <= kFar && lm >= 0.5f * floor;
+    }
     // Add a vector: v its order values, for real logits not below `floor`, lm
     // their largest before that.  False if it is one for far().
-    __device__ __forceinline__ bool add(const float (&v)[E], float lm, float c2) {
+    __device__ __forceinline__ bool add(const float (&v)[E], float lm, float c2, float floor) {
         if constexpr (En::kReal) {
             if (!(fmaf(lm, c2, -ref) <= kLag)) {
                 if (lm == absent<TYPE>()) return true;
                 const float r = lm * c2;
-                if (fabsf(r) > kFar || (ref == -__builtin_huge_valf() && s.x != 0.f && z0 > 0.f)) return false;
+                if (!near(lm, r, floor) || (ref == -__builtin_huge_valf() && s.x != 0.f && z0 > 0.f)) return false;
                 move_by(ref - r);
                 ref = r;
                 z0 = lm;
@@ -175,7 +180,7 @@ struct Stream {
     // no entropy).  The reference comes from the first step; later ones may
     // exceed it by far before a sum overflows, and the sums are as good either
     // way.  False: nothing was added, take the vectors one by one.
-    __device__ __forceinline__ bool add_step(const uint4 (&raw)[kU], float c2) {
+    __device__ __forceinline__ bool add_step(const uint4 (&raw)[kU], float c2, float floor) {
         static_assert(!ENT, "the entropy's sum needs a near reference");
         constexpr float kBig = 1.2379400392853803e27f;    // 2^90
         constexpr float kInf = __builtin_huge_valf();
@@ -187,7 +192,7 @@ struct Stream {
             if (lm == absent<TYPE>()) return true;
             if constexpr (En::kReal) {
                 const float r = lm * c2;
-                if (!(fabsf(r) <= kFar)) return false;
+                if (!near(lm, r, floor)) return false;
                 ref = r;
                 z0 = lm;
             } else {
@@ -870,7 +875,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
             }
         }
         if constexpr (!ENT) {
-            if (!st.add_step(raw, a.r.c2)) {
+            if (!st.add_step(raw, a.r.c2, a.r.floor)) {
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
                     if (b + u * 32 + g.lane < nv) later |= 1u << u;
@@ -880,7 +885,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
             for (int u = 0; u < (SHORT ? 1 : kU); ++u) {
                 float v[E];
                 lm[u] = decode<TYPE>(raw[u], v, a.r.floor);
-                if (!st.add(v, lm[u], a.r.c2)) later |= 1u << u;
+                if (!st.add(v, lm[u], a.r.c2, a.r.floor)) later |= 1u << u;
             }
         }
         if (__any_sync(0xffffffffu, later)) {
@@ -894,7 +899,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) v[i] = x.v[i];
                 const float m = largest<TYPE>(v, a.r.floor);
-                if (!st.add(v, m, a.r.c2)) st.far(x.v, m, a.r.c2);
+                if (!st.add(v, m, a.r.c2, a.r.floor)) st.far(x.v, m, a.r.c2);
                 if constexpr (ENT) {
 #pragma unroll
                     for (int i = 0; i < kU; ++i) lm[i] = i == u ? fmaxf(lm[i], m) : lm[i];

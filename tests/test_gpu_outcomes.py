@@ -491,6 +491,86 @@ def test_rows_without_distribution(V, t):
         np.testing.assert_allclose(to_np(s.logz), float(torch.finfo(torch_type(t)).min), rtol=1e-6)
 
 
+def _check_filled_rows(t, fill, scale, V, layout):
+    """Rows whose unwanted entries hold a large negative logit instead of
+    -inf.  Beside ordinary logits its weight is 0, so that everything but the
+    fill's own log p is as for -inf, within the bounds of those rows (M is of
+    the ordinary logits).  A row of nothing else is uniform."""
+    import torch
+    rng = np.random.default_rng(V)
+    R, K = 5, 6
+    rows = make_rows(rng, R, V, t)
+    out = rng.random((R, V)) < 0.5
+    out[0, :V // 2] = True                  # whole vectors before any ordinary logit
+    out[1, V // 2:] = True                  # and after
+    out[2, :V - 1] = True
+    out[2, V - 1] = False
+    out[3] = True
+    rows[torch.from_numpy(out)] = fill
+    clean = to_np(rows).copy()
+    clean[out] = -INF
+    buf = torch.zeros((R, 2 * V + 16), dtype=rows.dtype, device="cuda")
+    d = {"aligned": buf[:, :V], "misaligned": buf[:, 1:V + 1], "strided": buf[:, ::2][:, :V]}[layout]
+    if layout == "aligned":
+        d = torch.empty((R, (V + 7) // 8 * 8), dtype=rows.dtype, device="cuda")[:, :V]
+    d.copy_(rows)
+    ids = np.stack([rng.choice(np.flatnonzero(~out[i]), K) if i != 3 else rng.integers(0, V, K) for i in range(R)])
+    logits = rng.standard_normal((R, K)).astype(np.float32)
+    w = rng.standard_normal(R).astype(np.float32)
+    d_ids, d_l, d_w = torch.from_numpy(ids).cuda(), torch.from_numpy(logits).cuda(), torch.from_numpy(w).cuda()
+    op = tn.Outcomes(V, torch_type(t), max_rows=R, top=3, scale=scale)
+    s = op.score(d, d_ids)
+    ref = [Row(clean[i], None, scale) for i in range(R)]
+    tz = np.array([tol_logz(r) for r in ref])
+    some = [0, 1, 2, 4]
+    close(to_np(s.logz)[some], np.array([ref[i].logz for i in some]), tz[some], "log Z")
+    close(to_np(s.entropy)[some], np.array([ref[i].entropy for i in some]), 2 * tz[some], "entropy")
+    close(to_np(s.logp)[some], np.stack([ref[i].logp(ids[i]) for i in some]), 2 * tz[some][:, None], "log p")
+    for i in some:
+        n = min(3, int((~out[i]).sum()))
+        assert (to_np(s.top_ids)[i][:n] == ref[i].top(3)[0][:n]).all()
+    np.testing.assert_allclose(to_np(s.logz)[3], float(d[3, 0]) * scale, rtol=1e-6)
+    np.testing.assert_allclose(to_np(s.entropy)[3], np.log(V), rtol=1e-5)
+    assert to_np(s.top_ids)[3].tolist() == [0, 1, 2]
+    g = w[:, None] * logits
+    got = to_np(op.score_grad(d, d_ids, s.logz, s.entropy, torch.from_numpy(g).cuda()))
+    loss = op.distill(d, d_ids, d_l)
+    step = op.distill_step(d, d_ids, d_l, d_w)
+    dg = to_np(op.distill_grad(d, d_ids, d_l, loss.logz, d_w))
+    for what, x in (("distill", loss), ("distill step", step)):
+        close(to_np(x.logz)[some], np.array([ref[i].logz for i in some]), tz[some], what + " log Z")
+        want = np.array([ref[i].distill(ids[i], logits[i].astype(np.float64)) for i in some])
+        close(to_np(x.loss)[some], want, 2 * tz[some] + 64 * U, what + " loss")
+    for i in some:
+        for what, x, (want, mag) in (
+                ("score", got, ref[i].score_grad(ids[i], g[i])),
+                ("step", to_np(step.grad), ref[i].distill_grad(ids[i], logits[i].astype(np.float64), w[i])),
+                ("distill", dg, ref[i].distill_grad(ids[i], logits[i].astype(np.float64), w[i]))):
+            tol = (4 * tz[i] + 16 * U) * mag + OUT_EPS[t] * np.abs(want) + OUT_MIN[t]
+            close(x[i], want, tol, what + " gradient")
+    # the uniform row: p = 1 / V from the sums (log Z itself rounds to the fill's)
+    uniform = Row(np.zeros(V, np.float32), None, scale)
+    want, mag = uniform.distill_grad(ids[3], logits[3].astype(np.float64), w[3])
+    if V * d.element_size() < 60000:            # the row is held on chip
+        dense = np.setdiff1d(np.arange(V), np.concatenate([ids[3], [*range(8), *range(V - 8, V)]]))
+        if layout != "strided":
+            close(to_np(step.grad)[3][dense], want[dense],
+                  (1e-5 * mag + OUT_EPS[t] * np.abs(want) + OUT_MIN[t])[dense], "uniform row's gradient")
+    assert np.isfinite(to_np(step.grad)[3]).all() and np.isfinite(got[3]).all()
+
+
+@pytest.mark.parametrize("layout", ["aligned", "misaligned", "strided"])
+@pytest.mark.parametrize("V", [75, 4001, 50001])
+@pytest.mark.parametrize("scale", [2.0 ** -40, 0.01, 0.05, 0.08, 0.3, 1.0])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_lowest_values_at_high_temperature(t, scale, V, layout):
+    """The type's lowest value, and one between it and -2^126: c z may be small
+    there although z is not."""
+    import torch
+    _check_filled_rows(t, float(torch.finfo(torch_type(t)).min), scale, V, layout)
+    _check_filled_rows(t, -1.2e38, scale, V, layout)
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
