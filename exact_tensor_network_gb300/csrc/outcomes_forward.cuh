@@ -98,9 +98,12 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 // done() takes the rounding of ref out again.  Absent entries become `floor`,
 // about -2^126 / c2, so that they add 0 to both sums instead of 0 times -inf.
 // Logits beyond 2^125 / c2 either way (masks written as the type's lowest
-// value) would overflow there, and those below half of `floor` would not be
-// told from absent ones: ref = -inf then sends every vector through far(),
-// which works with differences of logits.
+// value) would overflow there, those below half of `floor` would not be told
+// from absent ones, and the rounding of a ref beyond 2^30 (2^6 and more: masks
+// written as -1e10) would itself be too large an exponent: ref = -inf then
+// sends every vector through far(), which works with differences of logits.
+// Different logits that far out differ by 2^6 powers of two at least, so the
+// sums of smaller ones are dropped on the way back.
 //
 // Amplitudes: the quotient w / z0 as q = w (1 / z0) with one Newton correction
 // q + (w - q z0) / z0 (Markstein 1990), which makes z0 / z0 exactly 1.  z0 is
@@ -125,9 +128,10 @@ struct Stream {
         s.x = any ? f * s.x : 0.f;
         s.y = any ? f * s.y : 0.f;
     }
-    // Whether a logit can be the reference of the straight way.
-    static __device__ __forceinline__ bool near(float lm, float r, float floor) {
-        return fabsf(r) <= kFar && lm >= 0.5f * floor;
+    // Whether a logit, of the rounded product r, can be the reference of the
+    // straight way.  False for NaN and infinities.
+    static __device__ __forceinline__ bool near(float lm, float r, float c2, float floor) {
+        return fabsf(r) <= kFar && lm >= 0.5f * floor && fabsf(fmaf(lm, c2, -r)) <= 32.f;
     }
     // Add a vector: v its order values, for real logits not below `floor`, lm
     // their largest before that.  False if it is one for far().
@@ -136,7 +140,8 @@ struct Stream {
             if (!(fmaf(lm, c2, -ref) <= kLag)) {
                 if (lm == absent<TYPE>()) return true;
                 const float r = lm * c2;
-                if (!near(lm, r, floor) || (ref == -__builtin_huge_valf() && s.x != 0.f && z0 > 0.f)) return false;
+                if (!near(lm, r, c2, floor) || (ref == -__builtin_huge_valf() && s.x != 0.f && !(lm > z0)))
+                    return false;
                 move_by(ref - r);
                 ref = r;
                 z0 = lm;
@@ -192,7 +197,7 @@ struct Stream {
             if (lm == absent<TYPE>()) return true;
             if constexpr (En::kReal) {
                 const float r = lm * c2;
-                if (!near(lm, r, floor)) return false;
+                if (!near(lm, r, c2, floor)) return false;
                 ref = r;
                 z0 = lm;
             } else {

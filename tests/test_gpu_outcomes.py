@@ -571,6 +571,56 @@ def test_lowest_values_at_high_temperature(t, scale, V, layout):
     _check_filled_rows(t, -1.2e38, scale, V, layout)
 
 
+@pytest.mark.parametrize("layout", ["aligned", "misaligned", "strided"])
+@pytest.mark.parametrize("V", [75, 4001, 50001])
+@pytest.mark.parametrize("scale", [0.08, 0.7, 1.0, 1.25])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_large_fills(t, scale, V, layout):
+    """What masks are written as, from 1e9 to 1e37: scale log2(e) z rounds by
+    2^6 and more from 2^30 on."""
+    for fill in (-1e9, -2e9, -1e10, -1e12, -1e20, -1e30, -1e37):
+        _check_filled_rows(t, fill, scale, V, layout)
+
+
+@pytest.mark.parametrize("V", [75, 4001, 50001])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_large_logits(t, V):
+    """Logits whose differences are lost beside them, and all of whose
+    neighbours are below e^-44 (2^-64): the largest alone is left, wherever it
+    stands and whichever ones come before it.  Large scales of ordinary ones
+    are the same case."""
+    import torch
+    rng = np.random.default_rng(V)
+    R = 12
+    for unit, scale in ((1e9, 2.0), (3e9, 1.0), (1e10, 1.0), (1e20, 0.7), (1e30, 1.25), (3.0, 2.0 ** 30),
+                        (3.0, 2.0 ** 40)):
+        z = rng.standard_normal((R, V)) * unit
+        z[3] = -np.abs(z[3])
+        z[4] = np.sort(z[4])
+        z[5] = -np.sort(z[5])
+        z[6] = -1e9 * (1 + rng.random(V))           # on both sides of 2^30
+        z[7] = 1e9 * (1 + rng.random(V))
+        rows = torch.from_numpy(z.astype(np.float32)).to(torch_type(t))
+        h = to_np(rows).astype(np.float64)
+        best = h.max(axis=1)
+        many = (h == best[:, None]).sum(axis=1)
+        d = rows.cuda()
+        ids = torch.from_numpy(h.argmax(axis=1)[:, None]).cuda()
+        op = tn.Outcomes(V, torch_type(t), max_rows=R, top=2, scale=scale)
+        s = op.score(d, ids)
+        x = op.distill(d, ids, torch.zeros((R, 1), device="cuda"))
+        step = op.distill_step(d, ids, torch.zeros((R, 1), device="cuda"), torch.ones(R, device="cuda"))
+        assert (s.top_ids[:, :1] == ids).all()
+        for lz in (s.logz, x.logz, step.logz):
+            np.testing.assert_allclose(to_np(lz), best * scale, rtol=4 * U, atol=np.log(V))
+        np.testing.assert_allclose(to_np(s.entropy), np.log(many), rtol=1e-5, atol=1e-6)
+        got = to_np(step.grad)
+        assert np.isfinite(got).all()
+        assert (got[h < best[:, None]] == 0).all(), (unit, scale)
+        one = many == 1
+        assert (got[one, h.argmax(axis=1)[one]] == 0).all()
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
