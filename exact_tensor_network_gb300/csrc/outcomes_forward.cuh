@@ -52,11 +52,12 @@ constexpr float kTiny = 7.888609052210118e-31f; // 2^-100
 // ---- running sums -----------------------------------------------------------
 
 // Distance of order value v from reference z in powers of two (amplitudes:
-// of the weights' quotient, so that the reference itself is at 0 exactly).
+// of the weights' quotient, so that the reference itself is at 0 exactly; z is
+// the larger there, and the logarithm of a quotient near 1 may be above 0).
 template <int TYPE>
 __device__ __forceinline__ float distance(float v, float z, float c2) {
     if constexpr (Entry<TYPE>::kReal) return (v - z) * c2;
-    else return c2 * lg2(__fdiv_rn(v, z));
+    else return min_nan(c2 * lg2(__fdiv_rn(v, z)), 0.f);
 }
 
 // z0: reference, an order value that was seen (absent until then).
@@ -107,7 +108,10 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 //
 // Amplitudes: the quotient w / z0 as q = w (1 / z0) with one Newton correction
 // q + (w - q z0) / z0 (Markstein 1990), which makes z0 / z0 exactly 1.  z0 is
-// at least 2^-100, for a finite reciprocal.
+// at least 2^-100, for a finite reciprocal.  It moves where a weight's power is
+// 2^8 above it, at a quotient of 2^(8 / scale) (256 at most), and from scale
+// 2^12 on at each larger weight: the logarithm's error (2^-22) would be most of
+// the distance.
 template <int TYPE, bool ENT, bool UNIT>
 struct Stream {
     using En = Entry<TYPE>;
@@ -135,12 +139,13 @@ struct Stream {
     }
     // Add a vector: v its order values, for real logits not below `floor`, lm
     // their largest before that.  False if it is one for far().
-    __device__ __forceinline__ bool add(const float (&v)[E], float lm, float c2, float floor) {
+    __device__ __forceinline__ bool add(const float (&v)[E], float lm, const OutRows &a) {
+        const float c2 = a.c2;
         if constexpr (En::kReal) {
             if (!(fmaf(lm, c2, -ref) <= kLag)) {
                 if (lm == absent<TYPE>()) return true;
                 const float r = lm * c2;
-                if (!near(lm, r, c2, floor) || (ref == -__builtin_huge_valf() && s.x != 0.f && !(lm > z0)))
+                if (!near(lm, r, c2, a.floor) || (ref == -__builtin_huge_valf() && s.x != 0.f && !(lm > z0)))
                     return false;
                 move_by(ref - r);
                 ref = r;
@@ -155,12 +160,14 @@ struct Stream {
                 if constexpr (ENT) t = fma2(e, d, t);
             }
         } else {
-            if (!(lm * inv <= 256.f)) {
+            if (UNIT ? !(lm * inv <= 256.f) : !(lm * inv < a.lag)) {
                 if (lm == 0.f) return true;
-                const float z = lm < kTiny ? kTiny : lm;
-                move_by(z0 == 0.f ? 0.f : distance<TYPE>(z0, z, c2));
-                z0 = z;
-                inv = __fdiv_rn(1.f, z);
+                if (UNIT || !(lm <= z0)) {
+                    const float z = lm < kTiny ? kTiny : lm;
+                    move_by(z0 == 0.f ? 0.f : distance<TYPE>(z0, z, c2));
+                    z0 = z;
+                    inv = __fdiv_rn(1.f, z);
+                }
             }
 #pragma unroll
             for (int i = 0; i < E; ++i) {
@@ -169,7 +176,7 @@ struct Stream {
                 float d = 0.f, e = q;
                 // at scale 1 the weight may be below what lg2 takes, not 0
                 if (ENT || !UNIT) d = max_nan(UNIT ? lg2(q) : c2 * lg2(q), UNIT ? -200.f : -1e30f);
-                if (!UNIT) e = ex2(d);
+                if (!UNIT) e = ex2(d = min_nan(d, a.most));
                 if (i & 1) {
                     s.y += e;
                     if constexpr (ENT) t.y = fmaf(e, d, t.y);
@@ -185,7 +192,8 @@ struct Stream {
     // no entropy).  The reference comes from the first step; later ones may
     // exceed it by far before a sum overflows, and the sums are as good either
     // way.  False: nothing was added, take the vectors one by one.
-    __device__ __forceinline__ bool add_step(const uint4 (&raw)[kU], float c2, float floor) {
+    __device__ __forceinline__ bool add_step(const uint4 (&raw)[kU], const OutRows &a) {
+        const float c2 = a.c2;
         static_assert(!ENT, "the entropy's sum needs a near reference");
         constexpr float kBig = 1.2379400392853803e27f;    // 2^90
         constexpr float kInf = __builtin_huge_valf();
@@ -197,7 +205,7 @@ struct Stream {
             if (lm == absent<TYPE>()) return true;
             if constexpr (En::kReal) {
                 const float r = lm * c2;
-                if (!near(lm, r, c2, floor)) return false;
+                if (!near(lm, r, c2, a.floor)) return false;
                 ref = r;
                 z0 = lm;
             } else {
@@ -205,6 +213,12 @@ struct Stream {
                 z0 = lm < kTiny ? kTiny : lm;
                 inv = __fdiv_rn(1.f, z0);
             }
+        }
+        if (!En::kReal && !UNIT && a.lag == 1.f) {      // every larger weight moves it
+            float lm = vector_max<TYPE>(raw[0]);
+#pragma unroll
+            for (int u = 1; u < kU; ++u) lm = max_nan(lm, vector_max<TYPE>(raw[u]));
+            if (!(lm <= z0)) return false;
         }
         const float2 before = s;
 #pragma unroll
@@ -880,7 +894,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
             }
         }
         if constexpr (!ENT) {
-            if (!st.add_step(raw, a.r.c2, a.r.floor)) {
+            if (!st.add_step(raw, a.r)) {
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
                     if (b + u * 32 + g.lane < nv) later |= 1u << u;
@@ -890,7 +904,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
             for (int u = 0; u < (SHORT ? 1 : kU); ++u) {
                 float v[E];
                 lm[u] = decode<TYPE>(raw[u], v, a.r.floor);
-                if (!st.add(v, lm[u], a.r.c2, a.r.floor)) later |= 1u << u;
+                if (!st.add(v, lm[u], a.r)) later |= 1u << u;
             }
         }
         if (__any_sync(0xffffffffu, later)) {
@@ -904,7 +918,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) v[i] = x.v[i];
                 const float m = largest<TYPE>(v, a.r.floor);
-                if (!st.add(v, m, a.r.c2, a.r.floor)) st.far(x.v, m, a.r.c2);
+                if (!st.add(v, m, a.r)) st.far(x.v, m, a.r.c2);
                 if constexpr (ENT) {
 #pragma unroll
                     for (int i = 0; i < kU; ++i) lm[i] = i == u ? fmaxf(lm[i], m) : lm[i];

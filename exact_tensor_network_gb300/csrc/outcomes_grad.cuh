@@ -36,6 +36,12 @@ __device__ __forceinline__ void finish_row_grad(RowGrad &c) {
     c.inv_z = !Entry<TYPE>::kReal && c.scale == 1.f && fabsf(c.logz) < 80.f ? expf(-c.logz) : 0.f;
 }
 
+// log p of a weight; the roundings of scale ln w and log Z may leave it above 0,
+// and far above where scale is large
+__device__ __forceinline__ float amplitude_log_prob(const RowGrad &c, float w) {
+    return min_nan(__fadd_rn(__fmul_rn(c.scale, logf(w)), -c.logz), 0.f);
+}
+
 // What multiplies the entry (an amplitude) or is the gradient itself (a real
 // logit).  v: order value of a present entry.
 template <int TYPE>
@@ -52,13 +58,13 @@ __device__ __forceinline__ float entry_grad(const RowGrad &c, float v, float add
         // 2 / w dL/dz, with p / w taken together
         float lp = 0.f, pw = c.inv_z;
         if (c.beta != 0.f || c.inv_z == 0.f) {
-            lp = __fadd_rn(__fmul_rn(c.scale, logf(v)), -c.logz);
+            lp = amplitude_log_prob(c, v);
             if (c.inv_z == 0.f) pw = ex2(lp * kLog2E) / v;
         }
         const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
         if (add == 0.f) return 2.f * c.mult * (pw * f);
         // over one denominator: nothing is left where p f = -add (p = 1)
-        if (c.beta == 0.f && c.inv_z != 0.f) lp = __fadd_rn(__fmul_rn(c.scale, logf(v)), -c.logz);
+        if (c.beta == 0.f && c.inv_z != 0.f) lp = amplitude_log_prob(c, v);
         return 2.f * c.mult * (fmaf(ex2(lp * kLog2E), f, add) / v);
     }
 }

@@ -178,7 +178,7 @@ __device__ __forceinline__ Sums<TYPE> sum_slice(const Slice<TYPE, MASK, G> &s, u
                 }
             }
         }
-        if (!st.add_step(raw, a.c2, a.floor)) {
+        if (!st.add_step(raw, a)) {
 #pragma unroll
             for (int u = 0; u < kU; ++u)
                 if (b + u * G + t < s.nv) later |= 1u << u;
@@ -190,7 +190,7 @@ __device__ __forceinline__ Sums<TYPE> sum_slice(const Slice<TYPE, MASK, G> &s, u
 #pragma unroll
             for (int e = 0; e < E; ++e) v[e] = x.v[e];
             const float m = largest<TYPE>(v, a.floor);
-            if (!st.add(v, m, a.c2, a.floor)) st.far(x.v, m, a.c2);
+            if (!st.add(v, m, a)) st.far(x.v, m, a.c2);
         }
     }
     return st.done(a.c2);

@@ -621,6 +621,103 @@ def test_large_logits(t, V):
         assert (got[one, h.argmax(axis=1)[one]] == 0).all()
 
 
+def _check_amplitudes(rows, scale, rng, grad_floor):
+    """Every call on complex64 rows against the definitions, at any scale.
+
+    The bounds are those of the module for log Z (the rounding of scale ln w,
+    and so M, is most of it at large scales).  A gradient's p has log p's error
+    as an exponent, its factor log p + H has that error once more, and p below
+    2^-126 may count as 0 where ``grad_floor``."""
+    import torch
+    R, V = rows.shape
+    K = 6
+    d = rows.cuda()
+    h_rows = to_np(rows)
+    ids = rand_ids(rng, R, K, V)
+    with np.errstate(under="ignore"):
+        ids[:, 0] = (h_rows.real ** 2 + h_rows.imag ** 2).argmax(axis=1)
+    logits = rng.standard_normal((R, K)).astype(np.float32)
+    g = rng.standard_normal((R, K)).astype(np.float32)
+    h, w = rng.standard_normal(R).astype(np.float32), rng.standard_normal(R).astype(np.float32)
+    dev = [torch.from_numpy(x).cuda() for x in (ids, logits, g, h, w)]
+    op = tn.Outcomes(V, torch.complex64, max_rows=R, top=4, scale=scale)
+    s = op.score(d, dev[0])
+    gs = to_np(op.score_grad(d, dev[0], s.logz, s.entropy, dev[2], dev[3]))
+    loss = op.distill(d, dev[0], dev[1])
+    gd = to_np(op.distill_grad(d, dev[0], dev[1], loss.logz, dev[4]))
+    step = op.distill_step(d, dev[0], dev[1], dev[4])
+    torch.cuda.synchronize()
+    op.check()
+    for i in range(R):
+        r = Row(h_rows[i], None, scale)
+        tz = tol_logz(r)
+        top = r.top(4)
+        assert (to_np(s.top_ids)[i] == top[0]).all(), "alternatives differ"
+        one = np.ones(1)
+        for what, got, want, tol in (
+                ("log Z", s.logz[i:i + 1], np.array([r.logz]), tz * one),
+                ("distill log Z", loss.logz[i:i + 1], np.array([r.logz]), tz * one),
+                ("step log Z", step.logz[i:i + 1], np.array([r.logz]), tz * one),
+                ("entropy", s.entropy[i:i + 1], np.array([r.entropy]), 2 * tz * one),
+                ("log p", s.logp[i], r.logp(ids[i]), 2 * tz * np.ones(K)),
+                ("alternatives", s.top_logp[i], top[1], 2 * tz * np.ones(4)),
+                ("loss", loss.loss[i:i + 1], np.array([r.distill(ids[i], logits[i].astype(np.float64))]),
+                 (2 * tz + 64 * U) * one),
+                ("step loss", step.loss[i:i + 1], np.array([r.distill(ids[i], logits[i].astype(np.float64))]),
+                 (2 * tz + 64 * U) * one)):
+            close(to_np(got), want, tol, what)
+        lp = np.where(r.present, r.x - r.logz, 0.0)
+        p = np.where(r.present, np.exp(lp), 0.0)
+        wt = np.where(r.present, np.abs(h_rows[i].astype(np.complex128)), 1.0)
+        with np.errstate(over="ignore", invalid="ignore"):
+            rel = np.expm1(4 * tz) + 16 * U
+            low = scale * 2.0 ** -126 * (np.abs(g[i]).sum() + abs(h[i]) * 128 + abs(w[i])) if grad_floor else 0.0
+            for what, got, (want, mag), he in (
+                    ("score gradient", gs[i], r.score_grad(ids[i], g[i], h[i]), abs(h[i])),
+                    ("distill gradient", gd[i], r.distill_grad(ids[i], logits[i].astype(np.float64), w[i]), 0.0),
+                    ("step gradient", step.grad[i].cpu().numpy(),
+                     r.distill_grad(ids[i], logits[i].astype(np.float64), w[i]), 0.0)):
+                assert np.isfinite(got).all(), what
+                tol = rel * mag + 2 / wt * (scale * he * 2 * tz * p * (1 + rel) + low) + OUT_MIN["c64"]
+                tol += OUT_EPS["c64"] * np.abs(want)
+                close(got, want, np.where(np.isnan(tol), INF, tol), f"{what} of row {i}")
+
+
+@pytest.mark.parametrize("R,V", [(9, 64), (9, 1500), (9, 9001), (3, 32768), (2, 400001), (470, 701), (2500, 65)],
+                         ids=lambda v: str(v))
+@pytest.mark.parametrize("scale", [6.0, 16.0, 20.0, 32.0, 64.0, 1000.0, 5000.0, 2.0 ** 20, 2.0 ** 40])
+def test_amplitudes_at_low_temperature(scale, R, V):
+    """A quotient of two weights that is small has a power that is not: random
+    rows, sorted ones (a new largest weight in every vector), equal ones, and
+    ones that differ by their last bits."""
+    import torch
+    rng = np.random.default_rng(V)
+    rows = make_rows(rng, R, V, "c64")
+    order = (rows.real.square() + rows.imag.square()).argsort(dim=1)
+    rows[1] = rows[1, order[1]]
+    rows[2 % R] = rows[2 % R, order[2 % R].flip(0)]
+    if R > 3:
+        rows[3] = 0.125
+    if R > 4:
+        rows[4] = 0.25 * (1 + 2.0 ** -23 * torch.from_numpy(rng.integers(0, 4, size=V).astype(np.float32)))
+    _check_amplitudes(rows[:9], scale, rng, grad_floor=True)
+    if R > 9:       # the kernels that many rows take
+        ids = torch.from_numpy(rand_ids(rng, R, 6, V)).cuda()
+        d, few = rows.cuda(), rows[:9].cuda()
+        one = torch.ones((R, 6), device="cuda")
+        ids[:9] = (few.real.square() + few.imag.square()).argmax(dim=1)[:, None]
+        many = tn.Outcomes(V, torch.complex64, max_rows=R, top=4, scale=scale)
+        less = tn.Outcomes(V, torch.complex64, max_rows=9, top=4, scale=scale)
+        a, b = many.score(d, ids), less.score(few, ids[:9])
+        assert (a.top_ids[:9] == b.top_ids).all() and torch.isfinite(a.logz).all()
+        torch.testing.assert_close(a.logz[:9], b.logz, rtol=4 * U, atol=1e-5)
+        torch.testing.assert_close(a.entropy[:9], b.entropy, rtol=1e-4, atol=1e-5)
+        a = many.distill_step(d, ids, one, one[:, 0].contiguous())
+        b = less.distill_step(few, ids[:9], one[:9], one[:9, 0].contiguous())
+        torch.testing.assert_close(a.logz[:9], b.logz, rtol=4 * U, atol=1e-5)
+        assert torch.isfinite(a.loss).all() and torch.isfinite(torch.view_as_real(a.grad)).all()
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
