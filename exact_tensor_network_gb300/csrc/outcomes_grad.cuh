@@ -42,53 +42,55 @@ __device__ __forceinline__ float amplitude_log_prob(const RowGrad &c, float w) {
     return min_nan(__fadd_rn(__fmul_rn(c.scale, logf(w)), -c.logz), 0.f);
 }
 
-// What multiplies the entry (an amplitude) or is the gradient itself (a real
-// logit).  v: order value of a present entry.
-template <int TYPE>
-__device__ __forceinline__ float entry_grad(const RowGrad &c, float v, float add) {
-    if constexpr (Entry<TYPE>::kReal) {
-        const float lp = max_nan(__fadd_rn(__fmul_rn(v, c.scale), -c.logz), -1e30f);
-        const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
-        if (lp < -80.f) {       // p may underflow where p f does not
-            const float q = ex2(lp * (0.5f * kLog2E));
-            return c.mult * fmaf(q, q * f, add);
-        }
-        return c.mult * fmaf(ex2(lp * kLog2E), f, add);
-    } else {
-        // 2 / w dL/dz, with p / w taken together
-        float lp = 0.f, pw = c.inv_z;
-        if (c.beta != 0.f || c.inv_z == 0.f) {
-            lp = amplitude_log_prob(c, v);
-            if (c.inv_z == 0.f) pw = ex2(lp * kLog2E) / v;
-        }
-        const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
-        if (add == 0.f) return 2.f * c.mult * (pw * f);
-        // over one denominator: nothing is left where p f = -add (p = 1)
-        if (c.beta == 0.f && c.inv_z != 0.f) lp = amplitude_log_prob(c, v);
-        return 2.f * c.mult * (fmaf(ex2(lp * kLog2E), f, add) / v);
+// Gradient of a real logit v that is present.
+__device__ __forceinline__ float logit_grad(const RowGrad &c, float v, float add) {
+    const float lp = max_nan(__fadd_rn(__fmul_rn(v, c.scale), -c.logz), -1e30f);
+    const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
+    if (lp < -80.f) {       // p may underflow where p f does not
+        const float q = ex2(lp * (0.5f * kLog2E));
+        return c.mult * fmaf(q, q * f, add);
     }
+    return c.mult * fmaf(ex2(lp * kLog2E), f, add);
 }
 
-template <int TYPE>
-__device__ __forceinline__ typename Entry<TYPE>::T to_entry(float g, typename Entry<TYPE>::T x) {
-    if constexpr (TYPE == TN_TYPE_F32) return g;
-    else if constexpr (TYPE == TN_TYPE_BF16) return __float2bfloat16_rn(g);
-    else if constexpr (TYPE == TN_TYPE_F16) return __float2half_rn(g);
-    else return make_float2(g * x.x, g * x.y);
+// Gradient at an amplitude a of weight w that is present: 2 a / w dL/dz.  The
+// quotients by w meet a first: 1 / w itself, and more so with what else there is
+// to multiply, may be beyond fp32 where the gradient, of the size of 1 / |a|, is
+// not.
+__device__ __forceinline__ float2 amplitude_grad(const RowGrad &c, float w, float2 a, float add) {
+    float lp = 0.f, pw = c.inv_z;        // p / w taken together
+    if (c.beta != 0.f || c.inv_z == 0.f) {
+        lp = amplitude_log_prob(c, w);
+        if (c.inv_z == 0.f) pw = ex2(lp * kLog2E) / w;
+    }
+    const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
+    if (add == 0.f) {
+        const float m = 2.f * c.mult * f;
+        return make_float2(pw * a.x * m, pw * a.y * m);
+    }
+    // over one denominator: nothing is left where p f = -add (p = 1)
+    if (c.beta == 0.f && c.inv_z != 0.f) lp = amplitude_log_prob(c, w);
+    const float m = 2.f * c.mult * fmaf(ex2(lp * kLog2E), f, add);
+    return make_float2(a.x / w * m, a.y / w * m);
 }
 
-// g[i] of the vector's entries as 16 bytes of the rows' type
+// The same for entry x of order value v, rounded to the rows' type.
 template <int TYPE>
-__device__ __forceinline__ uint4 pack(const float (&g)[Entry<TYPE>::E], const uint4 &raw) {
+__device__ __forceinline__ typename Entry<TYPE>::T entry_grad(const RowGrad &c, float v,
+                                                              typename Entry<TYPE>::T x, float add) {
+    if constexpr (TYPE == TN_TYPE_F32) return logit_grad(c, v, add);
+    else if constexpr (TYPE == TN_TYPE_BF16) return __float2bfloat16_rn(logit_grad(c, v, add));
+    else if constexpr (TYPE == TN_TYPE_F16) return __float2half_rn(logit_grad(c, v, add));
+    else return amplitude_grad(c, v, x, add);
+}
+
+// g[i] of the vector's real entries as 16 bytes of the rows' type
+template <int TYPE>
+__device__ __forceinline__ uint4 pack(const float (&g)[Entry<TYPE>::E]) {
     uint4 o;
     if constexpr (TYPE == TN_TYPE_F32) {
         o = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]),
                        __float_as_uint(g[3]));
-    } else if constexpr (TYPE == TN_TYPE_C64) {
-        o = make_uint4(__float_as_uint(g[0] * __uint_as_float(raw.x)),
-                       __float_as_uint(g[0] * __uint_as_float(raw.y)),
-                       __float_as_uint(g[1] * __uint_as_float(raw.z)),
-                       __float_as_uint(g[1] * __uint_as_float(raw.w)));
     } else {
         uint32_t w[4];
 #pragma unroll
@@ -143,11 +145,16 @@ __device__ __forceinline__ uint4 dense_grad(const RowGrad &c, const uint4 &raw) 
             v[i] = o.x;
             v[i + 1] = o.y;
         }
+        return pack<TYPE>(v);
     } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = v[i] == 0.f ? 0.f : entry_grad<TYPE>(c, v[i], 0.f);
+        const float2 a = make_float2(__uint_as_float(raw.x), __uint_as_float(raw.y));
+        const float2 b = make_float2(__uint_as_float(raw.z), __uint_as_float(raw.w));
+        const float2 none = make_float2(0.f, 0.f);
+        const float2 ga = v[0] == 0.f ? none : amplitude_grad(c, v[0], a, 0.f);
+        const float2 gb = v[1] == 0.f ? none : amplitude_grad(c, v[1], b, 0.f);
+        return make_uint4(__float_as_uint(ga.x), __float_as_uint(ga.y), __float_as_uint(gb.x),
+                          __float_as_uint(gb.y));
     }
-    return pack<TYPE>(v, raw);
 }
 
 // Where a row's gradient goes.
@@ -186,8 +193,8 @@ __device__ __noinline__ void grad_vector(const Row<TYPE> r, const RowGrad c, con
 #pragma unroll 1
     for (int64_t e = e0 < 0 ? 0 : e0; e < e0 + E && e < r.cols; ++e) {
         const float v = r.value(e);
-        typename Entry<TYPE>::T o = to_entry<TYPE>(0.f, typename Entry<TYPE>::T());
-        if (v != absent<TYPE>()) o = to_entry<TYPE>(entry_grad<TYPE>(c, v, 0.f), r.p[e * r.cs]);
+        typename Entry<TYPE>::T o = typename Entry<TYPE>::T();
+        if (v != absent<TYPE>()) o = entry_grad<TYPE>(c, v, r.p[e * r.cs], 0.f);
         out.p[e * out.cs] = o;
     }
 }
@@ -373,7 +380,7 @@ __device__ __forceinline__ void grad_ids(const Group<G> &g, const Row<TYPE> &r, 
             x = r.p[id * r.cs];
             v = row_value<TYPE>(r, id);
         }
-        if (v != absent<TYPE>()) out.p[id * out.cs] = to_entry<TYPE>(entry_grad<TYPE>(c, v, sign * add), x);
+        if (v != absent<TYPE>()) out.p[id * out.cs] = entry_grad<TYPE>(c, v, x, sign * add);
     }
 }
 

@@ -77,7 +77,7 @@ struct Dense {
                 v[i] = o.x;
                 v[i + 1] = o.y;
             }
-            return pack<TYPE>(v, raw);
+            return pack<TYPE>(v);
         } else {
             return dense_grad<TYPE, false>(c, raw);
         }
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ Ou
             float add = here ? te.q[t] : 0.f;
             const bool lead = sum_of_equal(te.id, te.q, n, t, id, here && repeats(turn).mark[t], add);
             if (lead && v != absent<TYPE>()) {
-                fix = to_entry<TYPE>(entry_grad<TYPE>(c, v, -add), x);
+                fix = entry_grad<TYPE>(c, v, x, -add);
                 fix_at = out.p + id * out.cs;
             }
         }

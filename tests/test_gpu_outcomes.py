@@ -718,6 +718,40 @@ def test_amplitudes_at_low_temperature(scale, R, V):
         assert torch.isfinite(a.loss).all() and torch.isfinite(torch.view_as_real(a.grad)).all()
 
 
+@pytest.mark.parametrize("V", [64, 1500, 40001])
+@pytest.mark.parametrize("scale", [0.7, 1.0])
+def test_gradients_of_tiny_amplitudes(scale, V):
+    """The gradient at an amplitude of 2^-60 is 2^60 and more, and its weight's
+    reciprocal times a loss scale of 2^16 beyond fp32."""
+    import torch
+    rng = np.random.default_rng(V)
+    R, K = 4, 5
+    a = rng.standard_normal((R, V)) + 1j * rng.standard_normal((R, V))
+    a *= 2.0 ** -60 / np.abs(a).max(axis=1, keepdims=True)
+    a[np.abs(a) < 2.0 ** -62.9] = 0
+    a[1, 0] = 1.0
+    rows = torch.from_numpy(a.astype(np.complex64))
+    h_rows = to_np(rows)
+    ids = np.stack([rng.choice(np.flatnonzero(h_rows[i]), K) for i in range(R)])
+    g = (2.0 ** 16 * rng.standard_normal((R, K))).astype(np.float32)
+    w = (2.0 ** 16 * rng.standard_normal(R)).astype(np.float32)
+    logits = rng.standard_normal((R, K)).astype(np.float32)
+    d = rows.cuda()
+    d_ids, d_g, d_w, d_l = (torch.from_numpy(x).cuda() for x in (ids, g, w, logits))
+    op = tn.Outcomes(V, torch.complex64, max_rows=R, scale=scale)
+    s = op.score(d, d_ids)
+    got = {"score": op.score_grad(d, d_ids, s.logz, s.entropy, d_g),
+           "distill": op.distill_grad(d, d_ids, d_l, s.logz, d_w),
+           "step": op.distill_step(d, d_ids, d_l, d_w).grad}
+    for i in range(R):
+        r = Row(h_rows[i], None, scale)
+        loss = r.distill_grad(ids[i], logits[i].astype(np.float64), w[i])
+        for what, (want, mag) in (("score", r.score_grad(ids[i], g[i])), ("distill", loss), ("step", loss)):
+            tol = (4 * tol_logz(r) + 16 * U) * mag + OUT_EPS["c64"] * np.abs(want) + OUT_MIN["c64"]
+            assert np.isfinite(to_np(got[what])[i]).all(), what
+            close(to_np(got[what])[i], want, tol, what + " gradient")
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
