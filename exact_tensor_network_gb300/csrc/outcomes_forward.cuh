@@ -108,10 +108,12 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 //
 // Amplitudes: the quotient w / z0 as q = w (1 / z0) with one Newton correction
 // q + (w - q z0) / z0 (Markstein 1990), which makes z0 / z0 exactly 1.  z0 is
-// at least 2^-100, for a finite reciprocal.  It moves where a weight's power is
-// 2^8 above it, at a quotient of 2^(8 / scale) (256 at most), and from scale
-// 2^12 on at each larger weight: the logarithm's error (2^-22) would be most of
-// the distance.
+// at least 2^-100, for a finite reciprocal and a correction that is not lost.
+// Where all weights are smaller and the scale is above 2, powers of quotients by
+// that could vanish: inv = infinity then sends every vector through far(), which
+// divides.  z0 moves where a weight's power is 2^8 above its own, at a quotient
+// of 2^(8 / scale) (256 at most), and from scale 2^12 on at each larger weight:
+// the logarithm's error (2^-22) would be most of the distance.
 template <int TYPE, bool ENT, bool UNIT>
 struct Stream {
     using En = Entry<TYPE>;
@@ -137,6 +139,8 @@ struct Stream {
     static __device__ __forceinline__ bool near(float lm, float r, float c2, float floor) {
         return fabsf(r) <= kFar && lm >= 0.5f * floor && fabsf(fmaf(lm, c2, -r)) <= 32.f;
     }
+    // Whether a row's largest weight is one for far().
+    static __device__ __forceinline__ bool tiny(float lm, float c2) { return lm < kTiny && c2 > 2.f; }
     // Add a vector: v its order values, for real logits not below `floor`, lm
     // their largest before that.  False if it is one for far().
     __device__ __forceinline__ bool add(const float (&v)[E], float lm, const OutRows &a) {
@@ -162,6 +166,7 @@ struct Stream {
         } else {
             if (UNIT ? !(lm * inv <= 256.f) : !(lm * inv < a.lag)) {
                 if (lm == 0.f) return true;
+                if (!UNIT && tiny(lm, c2) && inv == __builtin_huge_valf()) return false;
                 if (UNIT || !(lm <= z0)) {
                     const float z = lm < kTiny ? kTiny : lm;
                     move_by(z0 == 0.f ? 0.f : distance<TYPE>(z0, z, c2));
@@ -197,8 +202,8 @@ struct Stream {
         static_assert(!ENT, "the entropy's sum needs a near reference");
         constexpr float kBig = 1.2379400392853803e27f;    // 2^90
         constexpr float kInf = __builtin_huge_valf();
-        if (En::kReal ? ref == -kInf : z0 == 0.f) {
-            if (s.x != 0.f || s.y != 0.f) return false;   // (far out)
+        if (En::kReal ? ref == -kInf : inv == kInf) {
+            if (s.x != 0.f || s.y != 0.f) return false;   // (far out, or tiny)
             float lm = vector_max<TYPE>(raw[0]);
 #pragma unroll
             for (int u = 1; u < kU; ++u) lm = max_nan(lm, vector_max<TYPE>(raw[u]));
@@ -209,7 +214,7 @@ struct Stream {
                 ref = r;
                 z0 = lm;
             } else {
-                if (!(lm < kInf)) return false;
+                if (!(lm < kInf) || (!UNIT && tiny(lm, c2))) return false;
                 z0 = lm < kTiny ? kTiny : lm;
                 inv = __fdiv_rn(1.f, z0);
             }
@@ -247,16 +252,16 @@ struct Stream {
         s = before;
         return false;
     }
-    // the same for logits far out: v as they are
+    // the same for logits far out and tiny weights: v as they are
     __device__ __forceinline__ void far(const float (&v)[E], float lm, float c2) {
         if (!(lm <= z0)) {
-            move_by((z0 - lm) * c2);
+            move_by(z0 == absent<TYPE>() ? 0.f : distance<TYPE>(z0, lm, c2));
             z0 = lm;
         }
         ref = -__builtin_huge_valf();
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const float d = (v[i] - z0) * c2;
+            const float d = distance<TYPE>(v[i], z0, c2);
             const float e = ex2(d);
             s.x += e;
             if (ENT && e != 0.f) t.x = fmaf(e, d, t.x);

@@ -752,6 +752,24 @@ def test_gradients_of_tiny_amplitudes(scale, V):
             close(to_np(got[what])[i], want, tol, what + " gradient")
 
 
+@pytest.mark.parametrize("V", [64, 1500, 9001, 400001])
+@pytest.mark.parametrize("scale", [0.7, 1.0, 2.5, 6.0, 16.0, 2.0 ** 20])
+@pytest.mark.parametrize("largest", [-90, -101, -115, -125])
+def test_tiny_amplitudes(largest, scale, V):
+    """Rows whose largest weight is 2^largest (a hundred qubits and more), at
+    scales whose powers of such weights are below fp32's range; one of them
+    ends, one begins with an ordinary weight."""
+    import torch
+    rng = np.random.default_rng(V)
+    a = rng.standard_normal((5, V)) + 1j * rng.standard_normal((5, V))
+    a *= 2.0 ** (largest / 2) / np.abs(a).max(axis=1, keepdims=True)
+    small = np.abs(a) < 2.0 ** -62.9          # weights are normal numbers, or 0
+    a[small] = 0
+    a[1, V - 1] = 0.25
+    a[2, 0] = 0.25
+    _check_amplitudes(torch.from_numpy(a.astype(np.complex64)), scale, rng, grad_floor=True)
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
