@@ -56,22 +56,27 @@ __device__ __forceinline__ float logit_grad(const RowGrad &c, float v, float add
 // Gradient at an amplitude a of weight w that is present: 2 a / w dL/dz.  The
 // quotients by w meet a first: 1 / w itself, and more so with what else there is
 // to multiply, may be beyond fp32 where the gradient, of the size of 1 / |a|, is
-// not.
-__device__ __forceinline__ float2 amplitude_grad(const RowGrad &c, float w, float2 a, float add) {
-    float lp = 0.f, pw = c.inv_z;        // p / w taken together
+// not.  p is the square of q, whose factors are multiplied in turn, as p may be
+// below 2^-126 where p / |a| is not.
+__device__ __forceinline__ float2 amplitude_grad(const RowGrad &c, float w, float2 a) {
+    float lp = 0.f, q = 1.f, t = c.inv_z;
     if (c.beta != 0.f || c.inv_z == 0.f) {
         lp = amplitude_log_prob(c, w);
-        if (c.inv_z == 0.f) pw = ex2(lp * kLog2E) / w;
+        if (c.inv_z == 0.f) {
+            q = ex2(lp * (0.5f * kLog2E));
+            t = q / w;
+        }
     }
-    const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
-    if (add == 0.f) {
-        const float m = 2.f * c.mult * f;
-        return make_float2(pw * a.x * m, pw * a.y * m);
-    }
-    // over one denominator: nothing is left where p f = -add (p = 1)
-    if (c.beta == 0.f && c.inv_z != 0.f) lp = amplitude_log_prob(c, w);
-    const float m = 2.f * c.mult * fmaf(ex2(lp * kLog2E), f, add);
-    return make_float2(a.x / w * m, a.y / w * m);
+    const float n = 2.f * c.mult * fmaf(c.beta, lp + c.entropy, c.alpha) * q;
+    return make_float2(t * a.x * n, t * a.y * n);
+}
+// and with what is added there: over one denominator, so that nothing is left
+// where p f = -add (p = 1)
+__device__ __forceinline__ float2 amplitude_grad(const RowGrad &c, float w, float2 a, float add) {
+    if (add == 0.f) return amplitude_grad(c, w, a);
+    const float lp = amplitude_log_prob(c, w), q = ex2(lp * (0.5f * kLog2E)), t = 1.f / w;
+    const float n = 2.f * c.mult * fmaf(q, q * fmaf(c.beta, lp + c.entropy, c.alpha), add);
+    return make_float2(t * a.x * n, t * a.y * n);
 }
 
 // The same for entry x of order value v, rounded to the rows' type.
@@ -150,8 +155,8 @@ __device__ __forceinline__ uint4 dense_grad(const RowGrad &c, const uint4 &raw) 
         const float2 a = make_float2(__uint_as_float(raw.x), __uint_as_float(raw.y));
         const float2 b = make_float2(__uint_as_float(raw.z), __uint_as_float(raw.w));
         const float2 none = make_float2(0.f, 0.f);
-        const float2 ga = v[0] == 0.f ? none : amplitude_grad(c, v[0], a, 0.f);
-        const float2 gb = v[1] == 0.f ? none : amplitude_grad(c, v[1], b, 0.f);
+        const float2 ga = v[0] == 0.f ? none : amplitude_grad(c, v[0], a);
+        const float2 gb = v[1] == 0.f ? none : amplitude_grad(c, v[1], b);
         return make_uint4(__float_as_uint(ga.x), __float_as_uint(ga.y), __float_as_uint(gb.x),
                           __float_as_uint(gb.y));
     }

@@ -770,6 +770,17 @@ def test_tiny_amplitudes(largest, scale, V):
     _check_amplitudes(torch.from_numpy(a.astype(np.complex64)), scale, rng, grad_floor=True)
 
 
+@pytest.mark.parametrize("R,V", [(9, 64), (9, 1500), (4, 40001), (1, 400001)], ids=lambda v: str(v))
+@pytest.mark.parametrize("scale", [1.0, 2.0, 4.0, 8.0])
+def test_gradients_of_unlikely_amplitudes(scale, R, V):
+    """Probabilities below 2^-126 whose gradient, p / |a|, is a normal number."""
+    import torch
+    rng = np.random.default_rng(V)
+    a = rng.standard_normal((R, V)) + 1j * rng.standard_normal((R, V))
+    a *= 2.0 ** rng.uniform(-35.0, 0.0, size=(R, V))
+    _check_amplitudes(torch.from_numpy(a.astype(np.complex64)), scale, rng, grad_floor=False)
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
