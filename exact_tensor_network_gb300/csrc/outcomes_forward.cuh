@@ -51,13 +51,22 @@ constexpr float kTiny = 7.888609052210118e-31f; // 2^-100
 
 // ---- running sums -----------------------------------------------------------
 
+// The same for a weight below 2^-100 z.
+__device__ __noinline__ float wide_distance(float v, float z, float c2) {
+    return v == 0.f ? -__builtin_huge_valf()
+                    : c2 * (lg2(__fdiv_rn(v * 0x1p100f, z * 0x1p-100f)) - 200.f);
+}
+
 // Distance of order value v from reference z in powers of two (amplitudes:
 // of the weights' quotient, so that the reference itself is at 0 exactly; z is
-// the larger there, and the logarithm of a quotient near 1 may be above 0).
+// the larger there, and the logarithm of a quotient near 1 may be above 0.  A
+// quotient below fp32's range counts where the scale is small).
 template <int TYPE>
 __device__ __forceinline__ float distance(float v, float z, float c2) {
     if constexpr (Entry<TYPE>::kReal) return (v - z) * c2;
-    else return min_nan(c2 * lg2(__fdiv_rn(v, z)), 0.f);
+    const float q = __fdiv_rn(v, z);
+    if (q < 0x1p-100f && c2 < 1.f) return wide_distance(v, z, c2);
+    return min_nan(c2 * lg2(q), 0.f);
 }
 
 // z0: reference, an order value that was seen (absent until then).
@@ -113,7 +122,9 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 // that could vanish: inv = infinity then sends every vector through far(), which
 // divides.  z0 moves where a weight's power is 2^8 above its own, at a quotient
 // of 2^(8 / scale) (256 at most), and from scale 2^12 on at each larger weight:
-// the logarithm's error (2^-22) would be most of the distance.
+// the logarithm's error (2^-22) would be most of the distance.  Up to scale 1/4,
+// where a weight far below another counts beside it, z0 is 1 at most, so that no
+// quotient is below its weight, and powers (2^32 at most) need no nearer one.
 template <int TYPE, bool ENT, bool UNIT>
 struct Stream {
     using En = Entry<TYPE>;
@@ -138,6 +149,11 @@ struct Stream {
     // straight way.  False for NaN and infinities.
     static __device__ __forceinline__ bool near(float lm, float r, float c2, float floor) {
         return fabsf(r) <= kFar && lm >= 0.5f * floor && fabsf(fmaf(lm, c2, -r)) <= 32.f;
+    }
+    // The reference for a largest weight.
+    static __device__ __forceinline__ float first(float lm, float c2) {
+        if (!UNIT && c2 <= 0.25f && lm > 1.f) return 1.f;
+        return lm < kTiny ? kTiny : lm;
     }
     // Whether a row's largest weight is one for far().
     static __device__ __forceinline__ bool tiny(float lm, float c2) { return lm < kTiny && c2 > 2.f; }
@@ -168,7 +184,7 @@ struct Stream {
                 if (lm == 0.f) return true;
                 if (!UNIT && tiny(lm, c2) && inv == __builtin_huge_valf()) return false;
                 if (UNIT || !(lm <= z0)) {
-                    const float z = lm < kTiny ? kTiny : lm;
+                    const float z = first(lm, c2);
                     move_by(z0 == 0.f ? 0.f : distance<TYPE>(z0, z, c2));
                     z0 = z;
                     inv = __fdiv_rn(1.f, z);
@@ -215,7 +231,7 @@ struct Stream {
                 z0 = lm;
             } else {
                 if (!(lm < kInf) || (!UNIT && tiny(lm, c2))) return false;
-                z0 = lm < kTiny ? kTiny : lm;
+                z0 = first(lm, c2);
                 inv = __fdiv_rn(1.f, z0);
             }
         }

@@ -781,6 +781,21 @@ def test_gradients_of_unlikely_amplitudes(scale, R, V):
     _check_amplitudes(torch.from_numpy(a.astype(np.complex64)), scale, rng, grad_floor=False)
 
 
+@pytest.mark.parametrize("R,V", [(9, 64), (9, 1500), (4, 40001), (1, 400001)], ids=lambda v: str(v))
+@pytest.mark.parametrize("lo,hi", [(-62, 0), (-62, 62), (0, 62), (-10, 60)])
+@pytest.mark.parametrize("scale", [2.0 ** -40, 0.001, 0.01, 0.05, 0.125, 0.25, 0.3])
+def test_amplitudes_at_high_temperature(scale, lo, hi, R, V):
+    """Weights up to 2^250 apart, whose powers are not far from each other;
+    ascending, descending and random."""
+    import torch
+    rng = np.random.default_rng(V)
+    size = 2.0 ** rng.uniform(lo, hi, size=(R, V))
+    size[0] = np.sort(size[0])
+    size[-1] = -np.sort(-size[-1])
+    a = size * np.exp(2j * np.pi * rng.random((R, V)))
+    _check_amplitudes(torch.from_numpy(a.astype(np.complex64)), scale, rng, grad_floor=False)
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
