@@ -46,9 +46,9 @@ __device__ __forceinline__ float amplitude_log_prob(const RowGrad &c, float w) {
 __device__ __forceinline__ float logit_grad(const RowGrad &c, float v, float add) {
     const float lp = max_nan(__fadd_rn(__fmul_rn(v, c.scale), -c.logz), -1e30f);
     const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
-    if (lp < -80.f) {       // p may underflow where p f does not
+    if (lp < -80.f) {       // p may underflow where its multiple does not
         const float q = ex2(lp * (0.5f * kLog2E));
-        return c.mult * fmaf(q, q * f, add);
+        return add == 0.f ? c.mult * q * (q * f) : c.mult * fmaf(q, q * f, add);
     }
     return c.mult * fmaf(ex2(lp * kLog2E), f, add);
 }

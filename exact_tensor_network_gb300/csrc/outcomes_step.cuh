@@ -55,13 +55,21 @@ __device__ __forceinline__ void cluster_store(const float2 *p, int rank, float2 
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(far), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// The dense part of a vector where the row's sums are at hand.
+// The dense part of a vector where the row's sums are at hand.  bf16 reaches
+// below the least p that ex2 gives (see dense_grad): it gets 2^64 p, and the
+// factor 2^-64.  That rounds the exponent to 2^-19, 2^-11 of a bf16's step; the
+// square that dense_grad takes cost the kernel of 256 threads, which has no
+// register to spare, 17 % (1024x131072 132 against 115 us).
 template <int TYPE>
 struct Dense {
     float2 z0, c2, ls, ma;
     __device__ __forceinline__ Dense(const RowGrad &c, float z, float s, float c2_)
         : z0(make_float2(-z, -z)), c2(make_float2(c2_, c2_)) {
-        const float l = -kLog2E * logf(s), m = c.mult * c.alpha;     // (as log Z has it)
+        float l = -kLog2E * logf(s), m = c.mult * c.alpha;     // (as log Z has it)
+        if constexpr (TYPE == TN_TYPE_BF16) {
+            l += 64.f;
+            m *= 0x1p-64f;
+        }
         ls = make_float2(l, l);
         ma = make_float2(m, m);
     }

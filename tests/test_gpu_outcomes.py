@@ -796,6 +796,31 @@ def test_amplitudes_at_high_temperature(scale, lo, hi, R, V):
     _check_amplitudes(torch.from_numpy(a.astype(np.complex64)), scale, rng, grad_floor=False)
 
 
+@pytest.mark.parametrize("R,V", [(600, 1000), (3, 3001), (2, 60000), (400, 40001), (1, 900001)],
+                         ids=lambda v: str(v))
+def test_step_keeps_small_bf16_gradients(R, V):
+    """bf16 reaches below the least probability of one exponential: logits 80
+    to 100 below the largest have a gradient with a loss scale of 2^20, whichever
+    way the step takes, the same as from the two calls."""
+    import torch
+    z = np.full((R, V), 100.0)
+    z[:, 1:] -= np.linspace(80, 100, V - 1)
+    rows = torch.from_numpy(z.astype(np.float32)).bfloat16()
+    ids = np.zeros((R, 1), np.int64)
+    w = np.full(R, 2.0 ** 20, np.float32)
+    d, d_ids, d_l = rows.cuda(), torch.from_numpy(ids).cuda(), torch.zeros((R, 1), device="cuda")
+    op = tn.Outcomes(V, torch.bfloat16, max_rows=R)
+    s = op.distill(d, d_ids, d_l)
+    step = to_np(op.distill_step(d, d_ids, d_l, torch.from_numpy(w).cuda()).grad)
+    both = to_np(op.distill_grad(d, d_ids, d_l, s.logz, torch.from_numpy(w).cuda()))
+    r = Row(to_np(rows)[0], None, 1.0)
+    want, mag = r.distill_grad(ids[0], np.zeros(1), w[0])
+    tol = (4 * tol_logz(r) + 16 * U) * mag + OUT_EPS["bf16"] * np.abs(want) + OUT_MIN["bf16"]
+    assert (np.abs(want[1:]) > 1e-38).sum() > V // 2
+    for what, got in (("step", step), ("distill", both)):
+        close(got, np.broadcast_to(want, (R, V)), np.broadcast_to(tol, (R, V)), what + " gradient")
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
