@@ -514,14 +514,13 @@ struct Teacher {
         if (in && r.m) t.keep = r.m[t.x * r.mcs];
     }
     template <int TYPE>
-    __device__ __forceinline__ void settle(int j, const Item<TYPE> &t, const OutTeacher &a, const OutRows &rows,
-                                           const Row<TYPE> &r, int64_t row) const {
+    __device__ __forceinline__ void settle(int j, const Item<TYPE> &t, const OutRows &rows, const Row<TYPE> &r,
+                                           int64_t row) const {
         const bool in = t.x >= 0 && t.x < r.cols, wrong = !in && t.x != -1;
-        const float l = t.l * a.scale;
-        const bool used_ = in && t.keep && l != -__builtin_huge_valf();
+        const bool used_ = in && t.keep && t.l != -__builtin_huge_valf();
         if (wrong) flag_bad_id(rows, row);
         id[j] = used_ ? t.x : wrong ? -2 : -1;       // -2: an id out of range
-        logq[j] = used_ ? l : -__builtin_huge_valf();
+        logq[j] = used_ ? t.l : -__builtin_huge_valf();   // (not scaled yet)
         value[j] = Entry<TYPE>::value(t.v);
     }
     template <int TYPE, int G>
@@ -534,11 +533,13 @@ struct Teacher {
             if (j >= a.count) break;
             Item<TYPE> t = item<TYPE>(a, row, j);
             look<TYPE>(t, r, values);
-            settle<TYPE>(j, t, a, rows, r, row);
+            settle<TYPE>(j, t, rows, r, row);
         }
     }
-    // one warp
-    __device__ __forceinline__ void normalise(int count) const {
+    // One warp.  Differences are scaled, which cannot overflow to where all
+    // outcomes are left out (or none is finite).
+    __device__ __forceinline__ void normalise(const OutTeacher &a) const {
+        const int count = a.count;
         const int lane = threadIdx.x % 32;
         float top = -__builtin_huge_valf(), total = 0.f;
 #pragma unroll 1
@@ -547,7 +548,7 @@ struct Teacher {
         for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll 1
         for (int j = lane; j < count; j += 32) {
-            const float l = logq[j] - top, e = id[j] >= 0 ? expf(l) : 0.f;
+            const float l = (logq[j] - top) * a.scale, e = id[j] >= 0 ? expf(l) : 0.f;
             logq[j] = l;
             q[j] = e;
             total += e;

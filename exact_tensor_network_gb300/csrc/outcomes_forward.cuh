@@ -577,7 +577,7 @@ __device__ __forceinline__ void finish_row(Group<G> &g, const OutForward &a, con
         }
     } else {
         if (g.warp == 0) {
-            te.normalise(a.teacher.count);
+            te.normalise(a.teacher);
             const float loss = teacher_loss<TYPE>(a.teacher.count, a.r, te, logz);
             if (g.t == 0) a.loss[row] = loss;
         }

@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
     if (a.teacher.count) {
         te.read(g, a.teacher, a.r, r, row, false);
         g.sync();
-        if (g.warp == 0) te.normalise(n);
+        if (g.warp == 0) te.normalise(a.teacher);
         g.sync();
         c.alpha = *te.used;
         c.mult = a.g_loss[row] * a.r.scale;

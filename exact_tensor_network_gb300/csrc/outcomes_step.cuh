@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
     Sums<TYPE> sum = sum_slice<TYPE, 32, MASK, UNIT>(s, hold, g.t, a.r);
     combine(g, sum, a.r.c2);
     g.sync();
-    te.normalise(n);
+    te.normalise(a.teacher);
     float logz, entropy;
     normaliser<TYPE>(a.r, sum, logz, entropy);
     const RowGrad c = step_grad<TYPE>(a, a.g_loss[row], logz, *te.used);
@@ -322,12 +322,12 @@ __global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ Ou
         if (t < n) {
             Teacher::Item<TYPE> it = Teacher::item<TYPE>(a.teacher, row, t);
             Teacher::look<TYPE>(it, s.r, rank == 0);
-            te.settle<TYPE>(t, it, a.teacher, a.r, s.r, row);
+            te.settle<TYPE>(t, it, a.r, s.r, row);
             if (te.id[t] >= 0) repeats(0).put(t, te.id[t]);
         }
         __syncthreads();
         if (t < n && te.id[t] >= 0) repeats(0).look(te.id, t, te.id[t]);
-        if (warp == kWarps - 2) te.normalise(n);
+        if (warp == kWarps - 2) te.normalise(a.teacher);
     }
     if (ranks > 1) cluster_wait();
     int turn = 0;
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ Ou
         }
         const Teacher then(te_base + (turn ^ 1) * teacher_bytes(n), n);
         const bool given = more && t < n && it.x >= 0;
-        if (more && t < n) then.settle<TYPE>(t, it, a.teacher, a.r, next.r, next_row);
+        if (more && t < n) then.settle<TYPE>(t, it, a.r, next.r, next_row);
         if (given) repeats(turn ^ 1).put(t, it.x);
         __syncthreads();
         if (given) repeats(turn ^ 1).look(then.id, t, it.x);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ Ou
                 a.logz[row] = logz;
             }
         }
-        if (warp == kWarps - 2 && more) then.normalise(n);
+        if (warp == kWarps - 2 && more) then.normalise(a.teacher);
         if (!more) break;
         row = next_row;
         s = next;

@@ -821,6 +821,20 @@ def test_step_keeps_small_bf16_gradients(R, V):
         close(got, np.broadcast_to(want, (R, V)), np.broadcast_to(tol, (R, V)), what + " gradient")
 
 
+@pytest.mark.parametrize("V", [100, 30000, 900001])
+@pytest.mark.parametrize("scale", [1.0, 1.25, 100.0])
+def test_large_teacher_logits(scale, V):
+    """A teacher whose logits leave fp32 when scaled: the lowest value alone
+    (uniform), beside ordinary ones (probability 0), and large positive ones
+    (the largest is certain)."""
+    rng = np.random.default_rng(V)
+    low = np.finfo(np.float32).min
+    ids = np.stack([rng.permutation(V)[:4] for _ in range(5)]).astype(np.int64)
+    t = np.array([[low] * 4, [low, 0.5, low, 0.25], [3e38, 2e38, 3e38, -3e38], [low, -INF, low, -INF],
+                  [1e38, 0.0, -1e38, 1e38]], np.float32)
+    run_all(make_rows(rng, 5, V, "f32"), "f32", None, 0, (ids, t), teacher_scale=scale, rng=rng)
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
