@@ -290,7 +290,7 @@ struct Stream {
         a.t = t.x + t.y;
         if (En::kReal && ref != -__builtin_huge_valf()) {
             const float left = fmaf(z0, c2, -ref), one = ex2(left);
-            if (a.s == one && a.t == one * left) {   // of one entry: exactly 1 and 0
+            if (a.s == one && (!ENT || a.t == one * left)) {   // of one entry: exactly 1 and 0
                 a.s = 1.f;
                 a.t = 0.f;
             } else {
@@ -526,15 +526,41 @@ __device__ __forceinline__ int rank_of(const uint64_t *c, int n, uint64_t x) {
 
 // ---- the end of a row -------------------------------------------------------
 
+// What a row's sums say: the reference's logit z0, ls = ln s (-inf: an empty
+// row), log Z and H; NaN where an entry was NaN or +inf.
+struct Norm {
+    float z0, ls, logz, entropy;
+};
+
 template <int TYPE>
-__device__ __forceinline__ float log_prob(const OutRows &r, float v, float logz) {
-    // not fused, as log Z is not: a row's only entry has log p = 0 exactly
-    return __fadd_rn(__fmul_rn(r.scale, Entry<TYPE>::kReal ? v : logf(v)), -logz);
+__device__ __forceinline__ Norm normaliser(const OutRows &r, const Sums<TYPE> &a) {
+    constexpr float kInf = __builtin_huge_valf();
+    Norm n;
+    n.z0 = Entry<TYPE>::kReal ? a.z0 : logf(a.z0);
+    if (a.s == 0.f) {
+        n.ls = n.logz = -kInf;
+        n.entropy = 0.f;
+    } else if (a.s < kInf) {
+        n.ls = logf(a.s);
+        n.logz = __fadd_rn(__fmul_rn(r.scale, n.z0), n.ls);
+        n.entropy = n.ls - kLn2 * (a.t / a.s);
+    } else {
+        n.ls = n.logz = n.entropy = __int_as_float(0x7fffffff);
+    }
+    return n;
+}
+
+// From the reference, not from log Z, whose rounding is ln V's size and more where
+// scale z is large (64 at 1e9: a row of nothing but a mask's fill).
+template <int TYPE>
+__device__ __forceinline__ float log_prob(const OutRows &r, float v, const Norm &n) {
+    // not fused: a row's only entry has log p = 0 exactly
+    return __fadd_rn(__fmul_rn(r.scale, (Entry<TYPE>::kReal ? v : logf(v)) - n.z0), -n.ls);
 }
 
 // The loss of a row by one warp.
 template <int TYPE>
-__device__ __forceinline__ float teacher_loss(int count, const OutRows &r, const Teacher &te, float logz) {
+__device__ __forceinline__ float teacher_loss(int count, const OutRows &r, const Teacher &te, const Norm &norm) {
     constexpr float kInf = __builtin_huge_valf();
     float loss = 0.f, bad = 0.f;
 #pragma unroll 1
@@ -542,11 +568,11 @@ __device__ __forceinline__ float teacher_loss(int count, const OutRows &r, const
         if (te.id[j] == -2) bad = __int_as_float(0x7fffffff);
         if (te.id[j] >= 0 && te.q[j] != 0.f) {
             const float v = te.value[j];
-            const float lp = v == absent<TYPE>() ? -kInf : log_prob<TYPE>(r, v, logz);
+            const float lp = v == absent<TYPE>() ? -kInf : log_prob<TYPE>(r, v, norm);
             loss += te.q[j] * (te.logq[j] - lp);
         }
     }
-    if (logz == -kInf) loss = 0.f;
+    if (norm.ls == -kInf) loss = 0.f;
     loss += bad;
 #pragma unroll
     for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
@@ -555,11 +581,11 @@ __device__ __forceinline__ float teacher_loss(int count, const OutRows &r, const
 
 template <int TYPE, bool ENT, int G>
 __device__ __forceinline__ void finish_row(Group<G> &g, const OutForward &a, const Row<TYPE> &r,
-                                           Teacher &te, int64_t row, float logz, float entropy) {
+                                           Teacher &te, int64_t row, const Norm &norm) {
     constexpr float kInf = __builtin_huge_valf();
-    if (g.t == 0) a.logz[row] = logz;
+    if (g.t == 0) a.logz[row] = norm.logz;
     if constexpr (ENT) {
-        if (g.t == 0) a.entropy[row] = entropy;
+        if (g.t == 0) a.entropy[row] = norm.entropy;
 #pragma unroll 1
         for (int j = g.t; j < a.n_given; j += G) {
             const int64_t id = a.given[row * a.n_given + j];
@@ -571,32 +597,16 @@ __device__ __forceinline__ void finish_row(Group<G> &g, const OutForward &a, con
                 flag_bad_id(a.r, row);
             } else {
                 const float v = row_value<TYPE>(r, id);
-                lp = v == absent<TYPE>() ? -kInf : log_prob<TYPE>(a.r, v, logz);
+                lp = v == absent<TYPE>() ? -kInf : log_prob<TYPE>(a.r, v, norm);
             }
             a.logp[row * a.n_given + j] = lp;
         }
     } else {
         if (g.warp == 0) {
             te.normalise(a.teacher);
-            const float loss = teacher_loss<TYPE>(a.teacher.count, a.r, te, logz);
+            const float loss = teacher_loss<TYPE>(a.teacher.count, a.r, te, norm);
             if (g.t == 0) a.loss[row] = loss;
         }
-    }
-}
-
-// log Z and H of the sums; NaN where an entry was NaN or +inf.
-template <int TYPE>
-__device__ __forceinline__ void normaliser(const OutRows &r, const Sums<TYPE> &a, float &logz, float &entropy) {
-    constexpr float kInf = __builtin_huge_valf();
-    if (a.s == 0.f) {
-        logz = -kInf;
-        entropy = 0.f;
-    } else if (a.s < kInf) {
-        const float ls = logf(a.s);
-        logz = __fadd_rn(__fmul_rn(r.scale, Entry<TYPE>::kReal ? a.z0 : logf(a.z0)), ls);
-        entropy = ls - kLn2 * (a.t / a.s);
-    } else {
-        logz = entropy = __int_as_float(0x7fffffff);
     }
 }
 
@@ -793,12 +803,12 @@ __device__ __forceinline__ int best_entries(Group<G> &g, const Scratch &sm, cons
 // Alternative i of the row, from sm.best.
 template <int TYPE>
 __device__ __forceinline__ void put_alternative(const OutForward &a, const Row<TYPE> &r, const Scratch &sm, int i,
-                                                int log, float logz, int64_t *ids, float *lps) {
+                                                int log, const Norm &norm, int64_t *ids, float *lps) {
     constexpr int E = Entry<TYPE>::E;
     const uint64_t c = sm.best[i];
     const uint32_t x = 0xffffffffu - (uint32_t)c, j = x / E;
     ids[i] = (((int64_t)sm.pos[j >> log] << log) + (j & ((1 << log) - 1))) * E + x % E - r.head;
-    lps[i] = log_prob<TYPE>(a.r, key_value((uint32_t)(c >> 32)), logz);
+    lps[i] = log_prob<TYPE>(a.r, key_value((uint32_t)(c >> 32)), norm);
 }
 
 // ---- the kernels ------------------------------------------------------------
@@ -987,9 +997,8 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         }
         return;
     }
-    float logz, entropy;
-    normaliser<TYPE>(a.r, sum, logz, entropy);
-    finish_row<TYPE, ENT>(g, a, r, te, row, logz, entropy);
+    const Norm norm = normaliser<TYPE>(a.r, sum);
+    finish_row<TYPE, ENT>(g, a, r, te, row, norm);
     if constexpr (ENT && G == 32) {
         if (k == 0) return;
         const bool valid = sum.s < kInf;
@@ -997,7 +1006,12 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         float *lps = a.top_logp + row * k;
         int found = 0;
         if constexpr (SHORT) {
-            // one vector a lane: take the largest k times
+            // one vector a lane: take the largest k times; lane i has the key of
+            // alternative i until their log p are due, 32 at once
+            uint32_t mine = 0;
+            const auto put_log_probs = [&](int first, int end) {
+                if (first + g.lane < end) lps[first + g.lane] = log_prob<TYPE>(a.r, key_value(mine), norm);
+            };
             const auto x = row_vector<TYPE>(r, g.lane);
             uint32_t key[E];
 #pragma unroll
@@ -1016,17 +1030,19 @@ outcomes_forward(const __grid_constant__ OutForward a) {
 #pragma unroll
                     for (int i = 0; i < E; ++i) key[i] = i == at ? 0u : key[i];
                     ids[found] = g.lane * E + at - r.head;
-                    lps[found] = log_prob<TYPE>(a.r, key_value(mx), logz);
                 }
+                if ((found & 31) == g.lane) mine = mx;
+                if ((found & 31) == 31) put_log_probs(found - 31, found + 1);
             }
+            put_log_probs(found & ~31, found);
         } else if (valid) {
             g.sync();
             found = best_entries<TYPE, MASK>(g, sm, r, (nv + (1 << log) - 1) >> log, k, log, a.cand_len);
-            for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, log, logz, ids, lps);
+            for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, log, norm, ids, lps);
         }
         for (int i = found + g.t; i < k; i += G) {
             ids[i] = -1;
-            lps[i] = valid ? -kInf : logz;
+            lps[i] = valid ? -kInf : norm.logz;
         }
     }
 }
@@ -1196,9 +1212,8 @@ __global__ void __launch_bounds__(finish_threads<G>(), CTAS) outcomes_finish(con
     combine(g, sum, a.r.c2);
     g.sync();
     const bool valid = sum.s < kInf;
-    float logz, entropy;
-    normaliser<TYPE>(a.r, sum, logz, entropy);
-    finish_row<TYPE, ENT>(g, a, r, te, row, logz, entropy);
+    const Norm norm = normaliser<TYPE>(a.r, sum);
+    finish_row<TYPE, ENT>(g, a, r, te, row, norm);
     if constexpr (ENT) {
         if (k == 0) return;
         int64_t *ids = a.top_ids + row * k;
@@ -1215,10 +1230,10 @@ __global__ void __launch_bounds__(finish_threads<G>(), CTAS) outcomes_finish(con
                 found = best_of_exact_chunks<TYPE>(g, sm, r, exact, k, log);
             }
         }
-        for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, log, logz, ids, lps);
+        for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, log, norm, ids, lps);
         for (int i = found + g.t; i < k; i += G) {
             ids[i] = -1;
-            lps[i] = valid ? -kInf : logz;
+            lps[i] = valid ? -kInf : norm.logz;
         }
     }
 }

@@ -227,10 +227,10 @@ __device__ __forceinline__ void grad_step(const Slice<TYPE, MASK, G> &s, const u
 }
 
 template <int TYPE>
-__device__ __forceinline__ RowGrad step_grad(const OutStep &a, float g_loss, float logz, float used) {
+__device__ __forceinline__ RowGrad step_grad(const OutStep &a, float g_loss, const Norm &norm, float used) {
     RowGrad c;
     c.scale = a.r.scale;
-    c.logz = logz;
+    c.logz = norm.logz;
     c.beta = c.entropy = 0.f;
     c.alpha = used;
     c.mult = g_loss * a.r.scale;
@@ -264,9 +264,8 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
     combine(g, sum, a.r.c2);
     g.sync();
     te.normalise(a.teacher);
-    float logz, entropy;
-    normaliser<TYPE>(a.r, sum, logz, entropy);
-    const RowGrad c = step_grad<TYPE>(a, a.g_loss[row], logz, *te.used);
+    const Norm norm = normaliser<TYPE>(a.r, sum);
+    const RowGrad c = step_grad<TYPE>(a, a.g_loss[row], norm, *te.used);
     const Dense<TYPE> dense(c, sum.z0, sum.s, a.r.c2);
     const Out<TYPE> out(a.grad, a.grad_row_stride, a.grad_col_stride, s.r, row);
 #pragma unroll 1
@@ -275,10 +274,10 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
     grad_ids<TYPE>(g, s.r, c, out, te.id, te.q, -1.f, n, s.first, s.first + (int64_t)s.nv * E,
                    lists + teacher_bytes(n), reinterpret_cast<const typename En::T *>(hold), s.first + (int64_t)s.lo * E,
                    s.first + (int64_t)s.hi * E);
-    const float loss = teacher_loss<TYPE>(n, a.r, te, logz);
+    const float loss = teacher_loss<TYPE>(n, a.r, te, norm);
     if (g.t == 0) {
         a.loss[row] = loss;
-        a.logz[row] = logz;
+        a.logz[row] = norm.logz;
     }
 }
 
@@ -378,11 +377,10 @@ __global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ Ou
         if (sum.z0 != m) sum.move_to(m, a.r.c2);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
-        float logz, entropy;
-        normaliser<TYPE>(a.r, sum, logz, entropy);
+        const Norm norm = normaliser<TYPE>(a.r, sum);
 
         Teacher te(te_base + turn * teacher_bytes(n), n);
-        const RowGrad c = step_grad<TYPE>(a, g_loss, logz, *te.used);
+        const RowGrad c = step_grad<TYPE>(a, g_loss, norm, *te.used);
         const Dense<TYPE> dense(c, sum.z0, sum.s, a.r.c2);
         const Out<TYPE> out(a.grad, a.grad_row_stride, a.grad_col_stride, s.r, row);
         const int64_t id = t < n ? te.id[t] : -1;
@@ -421,10 +419,10 @@ __global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ Ou
         // (small jobs, each on its own warp: the slowest warp of a cluster is
         // what its barrier waits for)
         if (warp == kWarps - 1 && rank == 0) {
-            const float loss = teacher_loss<TYPE>(n, a.r, te, logz);
+            const float loss = teacher_loss<TYPE>(n, a.r, te, norm);
             if (lane == 0) {
                 a.loss[row] = loss;
-                a.logz[row] = logz;
+                a.logz[row] = norm.logz;
             }
         }
         if (warp == kWarps - 2 && more) then.normalise(a.teacher);

@@ -835,6 +835,48 @@ def test_large_teacher_logits(scale, V):
     run_all(make_rows(rng, 5, V, "f32"), "f32", None, 0, (ids, t), teacher_scale=scale, rng=rng)
 
 
+@pytest.mark.parametrize("t,scale,offset", [
+    ("f32", 1.0, 0.0), ("f32", 1.0, 1e4), ("f32", 0.7, 1e7), ("f32", 1.25, -1e9), ("f32", 1.0, -3.4e38),
+    ("f32", 1.25, -3.4e38), ("f32", 1.25, 3.4e38), ("bf16", 1.0, -1e9), ("bf16", 1.25, -3.38e38),
+    ("f16", 1.0, -65504.0), ("f16", 2.0, -65504.0), ("c64", 2.0 ** 20, 0.0), ("c64", 2.0 ** 40, 0.0)])
+@pytest.mark.parametrize("R,V", [(5, 60), (4, 4001), (3, 50001), (1, 1500001), (2500, 33)], ids=lambda v: str(v))
+def test_log_probabilities_beside_large_logits(R, V, t, scale, offset):
+    """log p and the loss are differences, whatever log Z rounds to: of logits far
+    from 0, of rows that one value fills (also where scale z leaves fp32), of
+    equal amplitudes at large scales.
+
+    Bounds, without M: two roundings of scale (z - z0), the exponential's error
+    for every term of the sum, weighted by p (1 + H), and ln s: 16 u (1 + |log p|
+    + H).  The reference is of the logits less their largest, in 64 bits."""
+    import torch
+    rng = np.random.default_rng(V)
+    if t == "c64":
+        rows = torch.full((R, V), 0.3 + 0.1j, dtype=torch.complex64)
+    else:
+        z = 3.0 * rng.standard_normal((R, V)) if abs(offset) < 1e38 else np.zeros((R, V))
+        rows = torch.from_numpy((z + offset).astype(np.float32)).to(torch_type(t))
+        rows[0] = offset
+    h = np.zeros((min(R, 5), V)) if t == "c64" else to_np(rows)[:5].astype(np.float64)
+    ids, logits = rand_ids(rng, R, 4, V), rng.standard_normal((R, 4)).astype(np.float32)
+    d, d_ids, d_l = rows.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(logits).cuda()
+    op = tn.Outcomes(V, torch_type(t), max_rows=R, top=3, scale=scale)
+    s = op.score(d, d_ids)
+    loss = op.distill(d, d_ids, d_l).loss
+    step = op.distill_step(d, d_ids, d_l, torch.ones(R, device="cuda")).loss
+    for i in range(len(h)):
+        r = Row(h[i] - h[i].max(), None, scale)
+        unit = 16 * U * (1 + r.entropy)
+        lp = r.logp(ids[i])
+        close(to_np(s.logp)[i], lp, unit + 16 * U * np.abs(lp), "log p")
+        top = r.top(3)
+        assert (to_np(s.top_ids)[i] == top[0]).all()
+        close(to_np(s.top_logp)[i], top[1], unit + 16 * U * np.abs(top[1]), "alternatives")
+        want = np.array([r.distill(ids[i], logits[i].astype(np.float64))])
+        far = np.abs(np.where(ids[i] < 0, 0.0, lp)).max()
+        for what, got in (("loss", loss), ("step loss", step)):
+            close(to_np(got)[i:i + 1], want, np.array([2 * unit + 32 * U * (far + 8.0)]), what)
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
