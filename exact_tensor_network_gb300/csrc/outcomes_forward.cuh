@@ -527,25 +527,27 @@ __device__ __forceinline__ int rank_of(const uint64_t *c, int n, uint64_t x) {
 // ---- the end of a row -------------------------------------------------------
 
 // What a row's sums say: the reference's logit z0, ls = ln s (-inf: an empty
-// row), log Z and H; NaN where an entry was NaN or +inf.
+// row) and H; NaN where an entry was NaN or +inf.
 struct Norm {
-    float z0, ls, logz, entropy;
+    float z0, ls, entropy;
+    __device__ __forceinline__ float logz(const OutRows &r) const {
+        return __fadd_rn(__fmul_rn(r.scale, z0), ls);
+    }
 };
 
 template <int TYPE>
-__device__ __forceinline__ Norm normaliser(const OutRows &r, const Sums<TYPE> &a) {
+__device__ __forceinline__ Norm normaliser(const Sums<TYPE> &a) {
     constexpr float kInf = __builtin_huge_valf();
     Norm n;
     n.z0 = Entry<TYPE>::kReal ? a.z0 : logf(a.z0);
     if (a.s == 0.f) {
-        n.ls = n.logz = -kInf;
+        n.ls = -kInf;
         n.entropy = 0.f;
     } else if (a.s < kInf) {
         n.ls = logf(a.s);
-        n.logz = __fadd_rn(__fmul_rn(r.scale, n.z0), n.ls);
         n.entropy = n.ls - kLn2 * (a.t / a.s);
     } else {
-        n.ls = n.logz = n.entropy = __int_as_float(0x7fffffff);
+        n.ls = n.entropy = __int_as_float(0x7fffffff);
     }
     return n;
 }
@@ -583,7 +585,7 @@ template <int TYPE, bool ENT, int G>
 __device__ __forceinline__ void finish_row(Group<G> &g, const OutForward &a, const Row<TYPE> &r,
                                            Teacher &te, int64_t row, const Norm &norm) {
     constexpr float kInf = __builtin_huge_valf();
-    if (g.t == 0) a.logz[row] = norm.logz;
+    if (g.t == 0) a.logz[row] = norm.logz(a.r);
     if constexpr (ENT) {
         if (g.t == 0) a.entropy[row] = norm.entropy;
 #pragma unroll 1
@@ -997,7 +999,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         }
         return;
     }
-    const Norm norm = normaliser<TYPE>(a.r, sum);
+    const Norm norm = normaliser<TYPE>(sum);
     finish_row<TYPE, ENT>(g, a, r, te, row, norm);
     if constexpr (ENT && G == 32) {
         if (k == 0) return;
@@ -1042,7 +1044,7 @@ outcomes_forward(const __grid_constant__ OutForward a) {
         }
         for (int i = found + g.t; i < k; i += G) {
             ids[i] = -1;
-            lps[i] = valid ? -kInf : norm.logz;
+            lps[i] = valid ? -kInf : norm.ls;
         }
     }
 }
@@ -1212,7 +1214,7 @@ __global__ void __launch_bounds__(finish_threads<G>(), CTAS) outcomes_finish(con
     combine(g, sum, a.r.c2);
     g.sync();
     const bool valid = sum.s < kInf;
-    const Norm norm = normaliser<TYPE>(a.r, sum);
+    const Norm norm = normaliser<TYPE>(sum);
     finish_row<TYPE, ENT>(g, a, r, te, row, norm);
     if constexpr (ENT) {
         if (k == 0) return;
@@ -1233,7 +1235,7 @@ __global__ void __launch_bounds__(finish_threads<G>(), CTAS) outcomes_finish(con
         for (int i = g.t; i < found; i += G) put_alternative<TYPE>(a, r, sm, i, log, norm, ids, lps);
         for (int i = found + g.t; i < k; i += G) {
             ids[i] = -1;
-            lps[i] = valid ? -kInf : norm.logz;
+            lps[i] = valid ? -kInf : norm.ls;
         }
     }
 }

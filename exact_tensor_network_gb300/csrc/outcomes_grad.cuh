@@ -25,26 +25,29 @@ constexpr int kGradU = 4;           // vectors of a thread's step
 
 struct RowGrad {
     float mult, alpha, beta, logz, entropy;
+    float shift;      // log p = scale (z - shift) - log Z of the shifted row
     float inv_z;      // amplitudes at scale 1: p = w inv_z (0: not used)
     float scale;
     bool plain;       // log Z is a number: no entry needs a second look
 };
 
+// shift: 0, or the logit that c.logz is relative to; logz: as it is.
 template <int TYPE>
-__device__ __forceinline__ void finish_row_grad(RowGrad &c) {
+__device__ __forceinline__ void finish_row_grad(RowGrad &c, float shift, float logz) {
+    c.shift = shift;
     c.plain = fabsf(c.logz) < __builtin_huge_valf();
-    c.inv_z = !Entry<TYPE>::kReal && c.scale == 1.f && fabsf(c.logz) < 80.f ? expf(-c.logz) : 0.f;
+    c.inv_z = !Entry<TYPE>::kReal && c.scale == 1.f && fabsf(logz) < 80.f ? expf(-logz) : 0.f;
 }
 
 // log p of a weight; the roundings of scale ln w and log Z may leave it above 0,
 // and far above where scale is large
 __device__ __forceinline__ float amplitude_log_prob(const RowGrad &c, float w) {
-    return min_nan(__fadd_rn(__fmul_rn(c.scale, logf(w)), -c.logz), 0.f);
+    return min_nan(__fadd_rn(__fmul_rn(c.scale, logf(w) - c.shift), -c.logz), 0.f);
 }
 
 // Gradient of a real logit v that is present.
 __device__ __forceinline__ float logit_grad(const RowGrad &c, float v, float add) {
-    const float lp = max_nan(__fadd_rn(__fmul_rn(v, c.scale), -c.logz), -1e30f);
+    const float lp = max_nan(__fadd_rn(__fmul_rn(v - c.shift, c.scale), -c.logz), -1e30f);
     const float f = fmaf(c.beta, lp + c.entropy, c.alpha);
     if (lp < -80.f) {       // p may underflow where its multiple does not
         const float q = ex2(lp * (0.5f * kLog2E));
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(kOutThreads) outcomes_grad(const __grid_consta
         }
         c.mult = a.r.scale;
     }
-    finish_row_grad<TYPE>(c);
+    finish_row_grad<TYPE>(c, 0.f, c.logz);
     const Out<TYPE> out(a.grad, a.grad_row_stride, a.grad_col_stride, r, row);
     if (c.beta != 0.f) grad_dense<TYPE, G, MASK, true>(g, r, c, out, v0, nv);
     else grad_dense<TYPE, G, MASK, false>(g, r, c, out, v0, nv);

@@ -226,15 +226,17 @@ __device__ __forceinline__ void grad_step(const Slice<TYPE, MASK, G> &s, const u
     for (; odd; odd &= odd - 1) grad_vector<TYPE>(s.r, c, out, s.v0 + b + (__ffs(odd) - 1) * G + t);
 }
 
+// Relative to the reference, as Dense is: log Z may have lost ln s (a row that
+// one large value fills).
 template <int TYPE>
 __device__ __forceinline__ RowGrad step_grad(const OutStep &a, float g_loss, const Norm &norm, float used) {
     RowGrad c;
     c.scale = a.r.scale;
-    c.logz = norm.logz;
+    c.logz = norm.ls;
     c.beta = c.entropy = 0.f;
     c.alpha = used;
     c.mult = g_loss * a.r.scale;
-    finish_row_grad<TYPE>(c);
+    finish_row_grad<TYPE>(c, norm.z0, norm.logz(a.r));
     return c;
 }
 
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
     combine(g, sum, a.r.c2);
     g.sync();
     te.normalise(a.teacher);
-    const Norm norm = normaliser<TYPE>(a.r, sum);
+    const Norm norm = normaliser<TYPE>(sum);
     const RowGrad c = step_grad<TYPE>(a, a.g_loss[row], norm, *te.used);
     const Dense<TYPE> dense(c, sum.z0, sum.s, a.r.c2);
     const Out<TYPE> out(a.grad, a.grad_row_stride, a.grad_col_stride, s.r, row);
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kOutThreads, 6) outcomes_step_warps(const __gr
     const float loss = teacher_loss<TYPE>(n, a.r, te, norm);
     if (g.t == 0) {
         a.loss[row] = loss;
-        a.logz[row] = norm.logz;
+        a.logz[row] = norm.logz(a.r);
     }
 }
 
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ Ou
         if (sum.z0 != m) sum.move_to(m, a.r.c2);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
-        const Norm norm = normaliser<TYPE>(a.r, sum);
+        const Norm norm = normaliser<TYPE>(sum);
 
         Teacher te(te_base + turn * teacher_bytes(n), n);
         const RowGrad c = step_grad<TYPE>(a, g_loss, norm, *te.used);
@@ -422,7 +424,7 @@ __global__ void __launch_bounds__(G, 3) outcomes_step(const __grid_constant__ Ou
             const float loss = teacher_loss<TYPE>(n, a.r, te, norm);
             if (lane == 0) {
                 a.loss[row] = loss;
-                a.logz[row] = norm.logz;
+                a.logz[row] = norm.logz(a.r);
             }
         }
         if (warp == kWarps - 2 && more) then.normalise(a.teacher);

@@ -877,6 +877,41 @@ def test_log_probabilities_beside_large_logits(R, V, t, scale, offset):
             close(to_np(got)[i:i + 1], want, np.array([2 * unit + 32 * U * (far + 8.0)]), what)
 
 
+@pytest.mark.parametrize("layout", ["aligned", "misaligned", "strided"])
+@pytest.mark.parametrize("t,scale,value", [("f32", 1.0, -1e9), ("f32", 1.25, -3.4e38), ("f32", 0.7, 1e30),
+                                           ("bf16", 1.0, -1e9), ("bf16", 1.25, -3.38e38), ("f16", 1.0, -65504.0),
+                                           ("c64", 2.0 ** 20, 0.3), ("c64", 2.0 ** 40, 0.3)])
+@pytest.mark.parametrize("R,V", [(3, 60), (2, 4001), (2, 50001), (500, 700)], ids=lambda v: str(v))
+def test_step_of_filled_rows(R, V, t, scale, value, layout):
+    """Rows that one large value fills are uniform, for the entries that the
+    teacher names and those at the rows' ends as for all others.
+
+    Bounds: p = 1 / V to the rounding of ln V (8 u (1 + ln V)), the gradient's
+    type, and the factors' roundings."""
+    import torch
+    rng = np.random.default_rng(V)
+    buf = torch.zeros((R, 2 * V + 18), dtype=torch_type(t), device="cuda")
+    d = {"aligned": torch.zeros((R, V), dtype=torch_type(t), device="cuda"), "misaligned": buf[:, 1:V + 1],
+         "strided": buf[:, ::2][:, :V]}[layout]
+    d.fill_(value)
+    ids, logits = rand_ids(rng, R, 5, V), rng.standard_normal((R, 5)).astype(np.float32)
+    ids[0, :2] = [0, V - 1]
+    w = rng.standard_normal(R).astype(np.float32)
+    op = tn.Outcomes(V, torch_type(t), max_rows=R, scale=scale)
+    got = op.distill_step(d, torch.from_numpy(ids).cuda(), torch.from_numpy(logits).cuda(),
+                          torch.from_numpy(w).cuda())
+    grad = to_np(got.grad)
+    if t == "c64":      # 2 a / |a|^2 dL/dz, of a real amplitude
+        assert (grad.imag == 0).all()
+        grad = grad.real.astype(np.float64) * float(np.float32(value)) / 2.0
+    eps = 16 * U * (1 + np.log(V)) + OUT_EPS[t]
+    for i in range(min(R, 4)):
+        want, mag = Row(np.zeros(V, np.float32), None, scale).distill_grad(ids[i], logits[i].astype(np.float64), w[i])
+        close(grad[i].astype(np.float64), want, eps * mag + OUT_MIN[t], f"gradient of row {i}")
+    np.testing.assert_allclose(to_np(got.loss)[0], Row(np.zeros(V, np.float32), None, 1.0).distill(
+        ids[0], logits[0].astype(np.float64)), rtol=1e-5, atol=1e-5)
+
+
 def test_absent_teacher_outcomes():
     """A teacher's outcome with an unmasked -inf logit: infinite loss; the
     same outcome masked: left out of the teacher."""
