@@ -1114,6 +1114,97 @@ def test_own_stream_and_graph():
             assert (to_np(x) == y).all()
 
 
+CALLS = ["score", "score_grad", "distill", "distill_grad", "distill_step"]
+
+
+def _call(op, name, x, stream=None):
+    """One call on the inputs x, its outputs as a list."""
+    kw = {"mask": x["mask"], "stream": stream}
+    if name == "score":
+        r = op.score(x["rows"], x["ids"], **kw)
+    elif name == "score_grad":
+        r = (op.score_grad(x["rows"], x["ids"], x["logz"], x["entropy"], x["logits"], x["w"], **kw),)
+    elif name == "distill":
+        r = op.distill(x["rows"], x["ids"], x["logits"], **kw)[:2]
+    elif name == "distill_grad":
+        r = (op.distill_grad(x["rows"], x["ids"], x["logits"], x["logz"], x["w"], **kw),)
+    else:
+        r = op.distill_step(x["rows"], x["ids"], x["logits"], x["w"], **kw)
+    return list(r)
+
+
+def _inputs_of_calls(t, R, V, seed):
+    import torch
+    rng = np.random.default_rng(seed)
+    x = {"rows": make_rows(rng, R, V, t), "mask": torch.from_numpy(rng.random((R, V)) < 0.8),
+         "ids": torch.from_numpy(rand_ids(rng, R, 5, V)),
+         "logits": torch.from_numpy(rng.standard_normal((R, 5)).astype(np.float32)),
+         "w": torch.from_numpy(rng.standard_normal(R).astype(np.float32))}
+    x = {k: v.cuda() for k, v in x.items()}
+    op = tn.Outcomes(V, torch_type(t), max_rows=R, top=4, scale=0.7)
+    s = op.score(x["rows"], mask=x["mask"])
+    x["logz"], x["entropy"] = s.logz, s.entropy
+    return x
+
+
+@pytest.mark.parametrize("t,R,V", [("bf16", 5, 300), ("f32", 3, 20011), ("c64", 2, 400001), ("bf16", 700, 9001)])
+@pytest.mark.parametrize("name", CALLS)
+def test_every_call_in_a_graph(name, t, R, V):
+    """Captured on a fresh handle (its first call but for the workspace) and
+    replayed on new contents, bit by bit as the call itself."""
+    import torch
+    xs = [_inputs_of_calls(t, R, V, seed) for seed in (1, 2)]
+    plain = tn.Outcomes(V, torch_type(t), max_rows=R, top=4, scale=0.7)
+    want = [[to_np(o) for o in _call(plain, name, x)] for x in xs]
+    op = tn.Outcomes(V, torch_type(t), max_rows=R, top=4, scale=0.7)
+    op.bind_workspace()
+    buf = {k: v.clone() for k, v in xs[0].items()}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _call(op, name, buf)
+    for x, w in ((xs[1], want[1]), (xs[0], want[0]), (xs[1], want[1])):
+        for k, v in x.items():
+            buf[k].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, w):
+            assert to_np(a).tobytes() == b.tobytes()
+
+
+@pytest.mark.parametrize("t,R,V", [("bf16", 5, 300), ("f32", 64, 200003), ("c64", 700, 9001)])
+@pytest.mark.parametrize("name", CALLS)
+def test_every_call_on_a_side_stream(name, t, R, V):
+    """Given as a torch stream, as its handle, and as the current stream; inputs
+    are dropped while it still works, and what is allocated next is filled."""
+    import torch
+    base = _inputs_of_calls(t, R, V, 3)
+    plain = tn.Outcomes(V, torch_type(t), max_rows=R, top=4, scale=0.7)
+    want = [to_np(o) for o in _call(plain, name, base)]
+    side = torch.cuda.Stream()
+    for how in ("stream", "handle", "current"):
+        op = tn.Outcomes(V, torch_type(t), max_rows=R, top=4, scale=0.7)
+        op.bind_workspace()
+        for _ in range(4):
+            x = {k: v.clone() for k, v in base.items()}
+            side.wait_stream(torch.cuda.current_stream())
+            if how == "current":
+                with torch.cuda.stream(side):
+                    got = _call(op, name, x)
+                for v in x.values():
+                    v.record_stream(side)
+            else:
+                got = _call(op, name, x, stream=side if how == "stream" else side.cuda_stream)
+            sizes = [(v.shape, v.dtype) for v in x.values()]
+            del x
+            junk = [torch.ones(s, dtype=d, device="cuda") for s, d in sizes]
+            side.synchronize()
+            for a, b in zip(got, want):
+                assert to_np(a).tobytes() == b.tobytes()
+            torch.cuda.synchronize()
+            del junk, got
+
+
 def test_no_rows():
     import torch
     op = tn.Outcomes(100, torch.float32, max_rows=4, top=3)
