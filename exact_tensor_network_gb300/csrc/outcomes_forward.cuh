@@ -109,11 +109,13 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 // about -2^126 / c2, so that they add 0 to both sums instead of 0 times -inf.
 // Logits beyond 2^125 / c2 either way (masks written as the type's lowest
 // value) would overflow there, those below half of `floor` would not be told
-// from absent ones, and the rounding of a ref beyond 2^30 (2^6 and more: masks
+// from absent ones, and the rounding of a ref beyond 2^31 (2^7 and more: masks
 // written as -1e10) would itself be too large an exponent: ref = -inf then
 // sends every vector through far(), which works with differences of logits.
-// Different logits that far out differ by 2^6 powers of two at least, so the
-// sums of smaller ones are dropped on the way back.
+// Different logits that far out differ by 2^7 powers of two at least, so the
+// sums of smaller ones are dropped on the way back.  (A rounding of up to 80
+// leaves room for sums; far() costs, 2048x50001 bf16 with one half filled 71
+// against 46 us, and -1e9 stays out of it up to scale 4.)
 //
 // Amplitudes: the quotient w / z0 as q = w (1 / z0) with one Newton correction
 // q + (w - q z0) / z0 (Markstein 1990), which makes z0 / z0 exactly 1.  z0 is
@@ -148,7 +150,7 @@ struct Stream {
     // Whether a logit, of the rounded product r, can be the reference of the
     // straight way.  False for NaN and infinities.
     static __device__ __forceinline__ bool near(float lm, float r, float c2, float floor) {
-        return fabsf(r) <= kFar && lm >= 0.5f * floor && fabsf(fmaf(lm, c2, -r)) <= 32.f;
+        return fabsf(r) <= kFar && lm >= 0.5f * floor && fabsf(fmaf(lm, c2, -r)) <= 80.f;
     }
     // The reference for a largest weight.
     static __device__ __forceinline__ float first(float lm, float c2) {
@@ -216,7 +218,7 @@ struct Stream {
     __device__ __forceinline__ bool add_step(const uint4 (&raw)[kU], const OutRows &a) {
         const float c2 = a.c2;
         static_assert(!ENT, "the entropy's sum needs a near reference");
-        constexpr float kBig = 1.2379400392853803e27f;    // 2^90
+        constexpr float kBig = 0x1p100f;
         constexpr float kInf = __builtin_huge_valf();
         if (En::kReal ? ref == -kInf : inv == kInf) {
             if (s.x != 0.f || s.y != 0.f) return false;   // (far out, or tiny)
