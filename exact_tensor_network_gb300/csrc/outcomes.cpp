@@ -75,7 +75,7 @@ tn_status cuda_fail(Outcomes &o, cudaError_t e, const char *what) {
 // None of these is below the limit that the workspace is made for.
 int64_t warp_vecs(int64_t rows) { return rows > 2 * tn::kOutTarget ? 1024 : tn::kOutWarpVecs; }
 int64_t grad_warp_vecs(int64_t rows) { return rows > 4 * tn::kOutTarget ? 640 : tn::kOutWarpVecs; }
-int64_t step_warp_vecs(int64_t rows) { return rows > 3 * 152 ? 1024 : tn::kOutWarpVecs; }
+int64_t step_warp_vecs(int64_t rows) { return rows > 3 * tn::kOutSms ? 1024 : tn::kOutWarpVecs; }
 
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
 
@@ -289,7 +289,7 @@ tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, 
     const int64_t bytes = s.vecs * tn::kOutVecBytes, teachers = tn::step_lists(count);
     int64_t c = (bytes + tn::kStepSlice - teachers - 1) / (tn::kStepSlice - teachers);
     // few rows: more CTAs a row, of two vectors a thread at least
-    while (c < tn::kStepCluster && rows * c < 2 * 152 && s.vecs >= 2 * (c + 1) * tn::kStepThreads) ++c;
+    while (c < tn::kStepCluster && rows * c < 2 * tn::kOutSms && s.vecs >= 2 * (c + 1) * tn::kStepThreads) ++c;
     c = c <= 2 ? c : c <= 4 ? 4 : tn::kStepCluster;
     s.segs = c;
     s.seg_vecs = (s.vecs + c - 1) / c;
@@ -301,7 +301,7 @@ tn::OutSplit step_split(int32_t type, int64_t cols, int64_t rows, bool aligned, 
     // against 96, 2048x50001 bf16 by two 105 against 95, 2000x16384 amplitudes
     // by two 125 against 118).  And where the teacher's outcomes need them.
     a->wide = count > tn::kStepThreads || (slice > (32 << 10) && c >= (type == TN_TYPE_F32 ? 2 : 3));
-    const bool many = rows * c > 3 * 152;
+    const bool many = rows * c > 3 * tn::kOutSms;
     if (slice + teachers > tn::kStepSlice) s.segs = 0;
     if (many && (type == TN_TYPE_C64 ? c >= 4 : type != TN_TYPE_F32 && c == 8 && slice < (48 << 10))) s.segs = 0;
     return s;

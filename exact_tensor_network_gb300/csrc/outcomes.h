@@ -24,7 +24,8 @@ constexpr int kOutChunkLog = 7;
 constexpr int kOutTree = 2048;          // maxima of a row that one CTA looks at; more form a tree
 constexpr int64_t kOutSegVecs = (int64_t)kOutKeys << 5;   // longest segment (512 KiB)
 
-constexpr int64_t kOutTarget = kOutCtas * 152;   // CTAs that fill the GPU
+constexpr int kOutSms = 152;
+constexpr int64_t kOutTarget = kOutCtas * kOutSms;   // CTAs that fill the GPU
 
 // A first cut for k alternatives keeps up to this many chunks: a bisection
 // that may stop anywhere between k and here takes a few steps less.

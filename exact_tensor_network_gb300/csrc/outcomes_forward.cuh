@@ -1277,10 +1277,10 @@ cudaError_t launch_forward(const OutForward &a, bool warp_rows, cudaStream_t str
         if (a.r.rows >= kOutTarget && a.r.segs * a.seg_chunks <= kOutWarpVecs)
             return launch_rows(outcomes_finish<TYPE, 32, 6, MASK, ENT>, (a.r.rows + 3) / 4, 128, (size_t)4 * a.group_bytes,
                                a, stream);
-        if (a.r.rows > 152 && a.r.rows <= 2 * 152 && a.n_top >= 16)
+        if (a.r.rows > kOutSms && a.r.rows <= 2 * kOutSms && a.n_top >= 16)
             return launch_rows(outcomes_finish<TYPE, 512, 2, MASK, ENT>, a.r.rows, 512, a.group_bytes, a, stream);
     }
-    if (a.r.rows > 152)
+    if (a.r.rows > kOutSms)
         return launch_rows(outcomes_finish<TYPE, 128, 6, MASK, ENT>, a.r.rows, 128, a.group_bytes, a, stream);
     return launch_rows(outcomes_finish<TYPE, 512, 1, MASK, ENT>, a.r.rows, 512, a.group_bytes, a, stream);
 }

@@ -475,7 +475,7 @@ cudaError_t launch_clusters(const OutStep &a, cudaStream_t stream) {
     cfg.attrs = attr;
     // as many clusters as run at once: each goes through its share of the rows
     int64_t clusters = a.r.rows;
-    if (clusters * a.r.segs > 152) {
+    if (clusters * a.r.segs > kOutSms) {
         if (known.bytes != row_bytes || known.segs != a.r.segs) {
             cfg.numAttrs = 1;
             cfg.gridDim = dim3((unsigned)a.r.segs);
