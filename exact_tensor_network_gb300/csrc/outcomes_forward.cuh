@@ -1,11 +1,12 @@
 // Scores of outcome distributions, and the loss against a teacher: one pass
 // over the rows.  Included by the translation unit of each entry type.
 //
-// Per row: log Z = ln sum exp(scale z), H = log Z - scale sum p z, and the k
-// largest entries with their indices.  A thread keeps a reference entry z0
+// Per row: log Z = ln sum exp(scale z), H = log Z - scale sum p z, log p of
+// given entries, and the k largest entries with their indices.  A thread keeps a reference entry z0
 // and, with d = scale log2(e) (z - z0),
 //     s = sum 2^d,   t = sum 2^d d;
-// then log Z = scale z0 + ln s and H = ln s - ln2 t / s.  z0 follows the
+// then log Z = scale z0 + ln s, H = ln s - ln2 t / s and log p = scale (z - z0) -
+// ln s.  z0 follows the
 // largest entry seen only once that is more than 2^8 above it: any reference
 // near the maximum will do, and a rescale on every new maximum would be a
 // divergent branch in most steps.
@@ -28,14 +29,15 @@
 // the streaming loop they cost that loop its registers and its instruction
 // cache.
 //
-// What bounds it.  32-bit entries: memory (2^26 amplitudes 83 us, 6.4 TB/s;
-// 2048x50001 f32 67 us, 6.1 TB/s).  16-bit ones: twice the entries a byte, so
-// issue slots as well (2048x50001 bf16 42 us, 4.8 TB/s at 57 % of the issue
-// slots; without the entropy, for the loss, 39 us).  Alternatives: their
-// maxima, and the search, which is latency, about ten dependent steps (the
-// same with one alternative 56 us, with 20 67; 1x32768 with 5 8.9 us, without
-// 4.6).  Short rows: what a row costs besides its entries (20000 rows of 64
-// amplitudes 10 us, with 4 alternatives 16).
+// What bounds it.  32-bit entries: memory (2^26 amplitudes 83 us, 6.5 TB/s;
+// 2048x50001 f32 67 us, 6.1 TB/s).  16-bit ones: twice the entries a byte, and
+// neither memory nor issue slots are full (2048x50001 bf16 42 us, 4.8 TB/s; with
+// alternatives 54 and 55 % of them): warps wait for their loads, 44 % of the
+// most that an SM holds; without the entropy, for the loss, 39 us.
+// Alternatives: their maxima, and the search, which is latency, about ten
+// dependent steps (the same with one alternative 55 us, with 20 67; 1x32768 with
+// 5 8.8 us, without 4.4).  Short rows: what a row costs besides its entries
+// (20000 rows of 64 amplitudes 10 us, with 4 alternatives 15.6).
 #pragma once
 
 #include "outcomes.cuh"

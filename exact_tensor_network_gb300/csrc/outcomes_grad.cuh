@@ -10,9 +10,10 @@
 // segment and then, after a barrier, overwrites the few entries with ids: the
 // first of equal ids adds up all of them in order, so no atomics are needed.
 //
-// Bound by memory, one read and one write: 1024x50001 bf16 38 us (5.4 TB/s, at
-// 41 % of the issue slots), f32 75 us (5.4 TB/s), 2^20 amplitudes 6.8 us (of
-// which launch and one pass of the id's corrections after the last store).
+// Bound by memory, one read and one write: 1024x50001 bf16 38.8 us (5.3 TB/s, at
+// 45 % of the issue slots), f32 75 us (5.5 TB/s), 64x2^18 amplitudes 46 us (5.8
+// TB/s), 2^20 amplitudes 5.6 us (of which launch and one pass of the ids'
+// corrections after the last store).
 #pragma once
 
 #include "outcomes.cuh"

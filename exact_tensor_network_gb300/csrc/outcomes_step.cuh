@@ -14,11 +14,11 @@
 // What bounds it.  A row passes through a chain (its loads, sums, the cluster's
 // barrier, the join, the gradient) of some 5 us, which the CTAs of an SM run
 // side by side, and every warp pays some 800 instructions a row besides its
-// vectors: 1024x131072 bf16 110 us (4.9 TB/s read and written, memory and issue
-// slots both at 60 %), 1000x50000 f32 89 us (4.5 TB/s), 8192x16384 bf16 100 us
-// (5.3 TB/s), 2000x16384 amplitudes 120 us (4.4 TB/s); 10000x8000 bf16 by warps
-// 74 us (4.3 TB/s).  500x32003 f32 (36 us, 3.5 TB/s) takes three rounds of 220
-// clusters for 2.3 rounds' rows.
+// vectors: 1024x131072 bf16 104 to 109 us (5.0 TB/s read and written, memory and
+// issue slots at 65 and 62 %), 1000x50000 f32 91 to 97 us (4.2 TB/s), 8192x16384
+// bf16 101 us (5.3 TB/s), 2000x16384 amplitudes 121 us (4.3 TB/s); 10000x8000 bf16
+// by warps 75 us (4.2 TB/s).  500x32003 f32 (37 us, 3.5 TB/s) takes three rounds of
+// 220 clusters for 2.3 rounds' rows.
 #pragma once
 
 #include "outcomes_forward.cuh"

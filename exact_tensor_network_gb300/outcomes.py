@@ -171,7 +171,8 @@ class Outcomes:
     Calls are asynchronous on ``stream`` (default: torch's current stream).
     On another stream the caller orders it after the inputs' producers, as for
     any other launch; outputs made by the call belong to that stream, and the
-    inputs, ``out`` and the workspace are recorded on it.
+    inputs, ``out`` and the workspace are recorded on it.  ``out`` of a gradient
+    may not overlap the rows.
     """
 
     def __init__(self, cols: int, dtype=None, max_rows: int = 1, top: int = 0, scale: float = 1.0):

@@ -11,11 +11,17 @@
  *
  * Definitions.  A row has `cols` entries.  The logit z of an entry is the real
  * entry itself, or ln w with w = re^2 + im^2 for an amplitude (the two squares
- * and the sum each rounded to fp32: w must lie in fp32's range).
+ * and the sum each rounded to fp32: w must lie in fp32's range; one below 2^-126
+ * has fewer digits, and may count as 0 in a sum at other scales than 1).
  *   - An entry is absent if its mask byte is 0 or z = -inf (w = 0).  What lies
  *     in masked places is never used (NaN and infinities included).
  *   - log Z = ln sum exp(scale z) over the present entries, log p = scale z -
  *     log Z, entropy H = - sum p log p.  scale is the inverse temperature.
+ *     log p, losses and training steps are taken from differences of logits, so
+ *     they hold where log Z rounds by more than ln V (large logits, as where a
+ *     mask was written as one) or, scale z being beyond fp32, is infinite.  The
+ *     gradient calls that are given log Z have its rounding: p to about
+ *     2^-23 |log Z|.
  *   - Alternatives: the present entries of largest z (largest w for
  *     amplitudes), ties to the lowest index; id -1 and log p -inf past the
  *     number of present entries.
@@ -99,9 +105,10 @@ TN_API void tn_outcomes_destroy(tn_outcomes_t *h);
 /* Device workspace of the handle, in bytes. */
 TN_API tn_status tn_outcomes_workspace_bytes(const tn_outcomes_t *h, uint64_t *bytes);
 
-/* Bind device memory (256-byte aligned, at least that large, owned by the
- * caller and left alone by everyone else while bound).  Clears its status word
- * (synchronous).  Errors: TN_EINVAL, TN_ENOMEM (too small), TN_ECUDA. */
+/* Bind memory of the current device, on which all calls on the handle have to
+ * be made (256-byte aligned, at least that large, owned by the caller and left
+ * alone by everyone else while bound).  Clears its status word (synchronous,
+ * so not while a stream is captured).  Errors: TN_EINVAL, TN_ENOMEM (too small), TN_ECUDA. */
 TN_API tn_status tn_outcomes_set_workspace(tn_outcomes_t *h, void *dev_ptr, uint64_t bytes);
 
 /*
@@ -133,7 +140,8 @@ TN_API tn_status tn_outcomes_score(tn_outcomes_t *h, const tn_rows *rows, const 
  * grad_col_stride], in the rows' type; every entry is written, 0 where absent.
  * For amplitudes grad = dL/dRe + i dL/dIm = 2 a / |a|^2 dL/dz.
  * grad may not overlap the rows.  The alternatives' log probabilities are
- * differentiated by giving their ids.
+ * differentiated by giving their ids.  For TN_TYPE_F32 and TN_TYPE_F16 a p below
+ * 2^-126 may count as 0, here and in the other gradients.
  */
 TN_API tn_status tn_outcomes_score_grad(tn_outcomes_t *h, const tn_rows *rows, const int64_t *given,
                                         int32_t n_given, const float *logz, const float *entropy,
@@ -159,7 +167,9 @@ TN_API tn_status tn_outcomes_distill_grad(tn_outcomes_t *h, const tn_rows *rows,
                                           int64_t grad_col_stride, tn_stream_t stream);
 
 /* Loss and gradient together, where g_loss is known beforehand (a mean over
- * the batch: 1 / rows): the results of the two calls above. */
+ * the batch: 1 / rows): the results of the two calls above, but for a rounding,
+ * and without that of log Z (see the definitions) unless the rows are long and
+ * read twice. */
 TN_API tn_status tn_outcomes_distill_step(tn_outcomes_t *h, const tn_rows *rows,
                                           const tn_teacher *teacher, const float *g_loss,
                                           float *loss, float *logz, void *grad,
