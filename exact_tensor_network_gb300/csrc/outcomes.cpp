@@ -210,8 +210,7 @@ tn::OutRows rows_of(const Outcomes &o, const tn_rows *r, const tn::OutSplit &s) 
     int x;
     std::frexp(a.c2, &x);                       // c2 <= 2^x
     a.floor = -std::ldexp(1.f, x > 0 ? 126 - x : 126);   // a bf16 number as well
-    a.lag = a.c2 >= 4096.f ? 1.f : a.c2 <= 0.25f ? 0x1p127f : a.c2 <= 1.f ? 256.f : std::exp2(8.f / a.c2);
-    a.most = a.lag == 1.f ? 0.f : a.c2 <= 0.25f ? 64.f : 9.f;
+    a.lag = a.c2 <= 0.25f ? 0x1p127f : a.c2 <= 1.f ? 256.f : std::exp2(8.f / a.c2);
     a.seg_vecs = s.seg_vecs;
     a.segs = s.segs;
     a.status = reinterpret_cast<tn::DevStatus *>(o.ws);

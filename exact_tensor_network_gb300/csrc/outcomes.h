@@ -57,9 +57,7 @@ struct OutRows {
     // stands for absent logits in the sums, about -2^126 / max(c2, 1).  Present ones
     // may lie below it where c2 < 1 (the types end near -2^128).
     float floor;
-    // amplitudes: the quotient of a weight and the sums' reference at which the
-    // reference moves, and the most that the power of a quotient can be
-    float lag, most;
+    float lag;          // amplitudes: the quotient by the sums' reference that moves it
     int64_t seg_vecs;
     int64_t segs;
     DevStatus *status;

@@ -125,8 +125,8 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
 // Where all weights are smaller and the scale is above 2, powers of quotients by
 // that could vanish: inv = infinity then sends every vector through far(), which
 // divides.  z0 moves where a weight's power is 2^8 above its own, at a quotient
-// of 2^(8 / scale) (256 at most), and from scale 2^12 on at each larger weight:
-// the logarithm's error (2^-22) would be most of the distance.  Up to scale 1/4,
+// of 2^(8 / scale) (256 at most).  From scale 2^12 on, where the logarithm's error
+// (2^-22) counts, far() takes all and moves at each larger weight.  Up to scale 1/4,
 // where a weight far below another counts beside it, z0 is 1 at most, so that no
 // quotient is below its weight, and powers (2^32 at most) need no nearer one.
 template <int TYPE, bool ENT, bool UNIT>
@@ -160,7 +160,9 @@ struct Stream {
         return lm < kTiny ? kTiny : lm;
     }
     // Whether a row's largest weight is one for far().
-    static __device__ __forceinline__ bool tiny(float lm, float c2) { return lm < kTiny && c2 > 2.f; }
+    static __device__ __forceinline__ bool divided(float lm, float c2) {
+        return c2 > 2.f && (lm < kTiny || c2 >= 4096.f);
+    }
     // Add a vector: v its order values, for real logits not below `floor`, lm
     // their largest before that.  False if it is one for far().
     __device__ __forceinline__ bool add(const float (&v)[E], float lm, const OutRows &a) {
@@ -186,13 +188,11 @@ struct Stream {
         } else {
             if (UNIT ? !(lm * inv <= 256.f) : !(lm * inv < a.lag)) {
                 if (lm == 0.f) return true;
-                if (!UNIT && tiny(lm, c2) && inv == __builtin_huge_valf()) return false;
-                if (UNIT || !(lm <= z0)) {
-                    const float z = first(lm, c2);
-                    move_by(z0 == 0.f ? 0.f : distance<TYPE>(z0, z, c2));
-                    z0 = z;
-                    inv = __fdiv_rn(1.f, z);
-                }
+                if (!UNIT && divided(lm, c2) && inv == __builtin_huge_valf()) return false;
+                const float z = first(lm, c2);
+                move_by(z0 == 0.f ? 0.f : distance<TYPE>(z0, z, c2));
+                z0 = z;
+                inv = __fdiv_rn(1.f, z);
             }
 #pragma unroll
             for (int i = 0; i < E; ++i) {
@@ -201,7 +201,7 @@ struct Stream {
                 float d = 0.f, e = q;
                 // at scale 1 the weight may be below what lg2 takes, not 0
                 if (ENT || !UNIT) d = max_nan(UNIT ? lg2(q) : c2 * lg2(q), UNIT ? -200.f : -1e30f);
-                if (!UNIT) e = ex2(d = min_nan(d, a.most));
+                if (!UNIT) e = ex2(d);
                 if (i & 1) {
                     s.y += e;
                     if constexpr (ENT) t.y = fmaf(e, d, t.y);
@@ -223,7 +223,7 @@ struct Stream {
         constexpr float kBig = 0x1p100f;
         constexpr float kInf = __builtin_huge_valf();
         if (En::kReal ? ref == -kInf : inv == kInf) {
-            if (s.x != 0.f || s.y != 0.f) return false;   // (far out, or tiny)
+            if (s.x != 0.f || s.y != 0.f) return false;   // (far out, or divided)
             float lm = vector_max<TYPE>(raw[0]);
 #pragma unroll
             for (int u = 1; u < kU; ++u) lm = max_nan(lm, vector_max<TYPE>(raw[u]));
@@ -234,16 +234,10 @@ struct Stream {
                 ref = r;
                 z0 = lm;
             } else {
-                if (!(lm < kInf) || (!UNIT && tiny(lm, c2))) return false;
+                if (!(lm < kInf) || (!UNIT && divided(lm, c2))) return false;
                 z0 = first(lm, c2);
                 inv = __fdiv_rn(1.f, z0);
             }
-        }
-        if (!En::kReal && !UNIT && a.lag == 1.f) {      // every larger weight moves it
-            float lm = vector_max<TYPE>(raw[0]);
-#pragma unroll
-            for (int u = 1; u < kU; ++u) lm = max_nan(lm, vector_max<TYPE>(raw[u]));
-            if (!(lm <= z0)) return false;
         }
         const float2 before = s;
 #pragma unroll
@@ -272,7 +266,7 @@ struct Stream {
         s = before;
         return false;
     }
-    // the same for logits far out and tiny weights: v as they are
+    // the same for logits far out and weights to be divided: v as they are
     __device__ __forceinline__ void far(const float (&v)[E], float lm, float c2) {
         if (!(lm <= z0)) {
             move_by(z0 == absent<TYPE>() ? 0.f : distance<TYPE>(z0, lm, c2));
