@@ -78,9 +78,9 @@ __device__ __forceinline__ float2 amplitude_grad(const RowGrad &c, float w, floa
 // where p f = -add (p = 1)
 __device__ __forceinline__ float2 amplitude_grad(const RowGrad &c, float w, float2 a, float add) {
     if (add == 0.f) return amplitude_grad(c, w, a);
-    const float lp = amplitude_log_prob(c, w), q = ex2(lp * (0.5f * kLog2E)), t = 1.f / w;
+    const float lp = amplitude_log_prob(c, w), q = ex2(lp * (0.5f * kLog2E));
     const float n = 2.f * c.mult * fmaf(q, q * fmaf(c.beta, lp + c.entropy, c.alpha), add);
-    return make_float2(t * a.x * n, t * a.y * n);
+    return make_float2(a.x / w * n, a.y / w * n);
 }
 
 // The same for entry x of order value v, rounded to the rows' type.
