@@ -13,7 +13,9 @@ import ctypes
 import os
 from typing import Optional, Sequence, Tuple
 
-from . import outcomes
+from . import block8, outcomes
+from .block8 import (Blocks8, TN_BLOCK8, linear8, linear8_grad, product8, quantize8, tn_block8,  # noqa: F401
+                     tn_block8_check, tn_block8_last_error, tn_block8_product, tn_block8_quantize, tn_matrix)
 from .outcomes import (Distill, Outcomes, Scores, TN_OUTCOMES_MAX_IDS, TN_OUTCOMES_MAX_TOP,  # noqa: F401
                        TN_TYPE_BF16, TN_TYPE_C64, TN_TYPE_F16, TN_TYPE_F32, tn_outcomes_check,
                        tn_outcomes_create, tn_outcomes_destroy, tn_outcomes_distill,
@@ -117,6 +119,7 @@ SIGNATURES = {
     "tn_last_error": (ctypes.c_char_p, [_P]),
 }
 SIGNATURES.update(outcomes.SIGNATURES)
+SIGNATURES.update(block8.SIGNATURES)
 
 
 def lib() -> ctypes.CDLL:

@@ -1,0 +1,218 @@
+// Quantisation to 8 bits with a scale for each block of 128.
+//
+// A CTA reads one tile of 128 x 128 entries once, each of its eight warps 16 rows
+// with four neighbouring entries a lane, and holds it in registers: the largest
+// magnitudes along rows are one warp reduction a row, those along columns
+// go from warp to warp through shared memory, and codes of the transposed
+// matrix leave through a shared tile so that both layouts are written in whole
+// lines.  Magnitudes are compared as integers (the bits of |x| have its order, and
+// infinities and NaN are the largest of all).  Bound by memory.
+#include <cuda_fp16.h>
+
+#include "block8.h"
+#include "common.cuh"
+
+namespace tn {
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int WARP_ROWS = kB8Tile / (THREADS / 32);     // 16
+
+__device__ __forceinline__ float entry(const float *p) { return __ldcg(p); }
+__device__ __forceinline__ float entry(const __nv_bfloat16 *p) {
+    return __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short *>(p))) << 16);
+}
+__device__ __forceinline__ float entry(const __half *p) {
+    const unsigned short u = __ldcg(reinterpret_cast<const unsigned short *>(p));
+    return __half2float(*reinterpret_cast<const __half *>(&u));
+}
+__device__ __forceinline__ void entries(const float *p, float (&v)[4]) {
+    const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+}
+__device__ __forceinline__ void entries(const __nv_bfloat16 *p, float (&v)[4]) {
+    const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(p));
+    v[0] = __uint_as_float(u.x << 16);
+    v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16);
+    v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void entries(const __half *p, float (&v)[4]) {
+    const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(p));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
+}
+
+// The scale of a block whose largest magnitude has the bits `top`, and what
+// entries are multiplied by (0 with a NaN or an infinity among them).
+struct Scale {
+    float s, inverse;
+};
+__device__ __forceinline__ Scale scale_of(uint32_t top) {
+    if (top > 0x7f7fffffu) return {__uint_as_float(0x7fc00000u), 0.f};
+    if (top == 0) return {1.f, 1.f};
+    // top = m 2^e with 1 <= m < 2, and 448 = 1.75 2^8
+    int e = static_cast<int>(top >> 23) - 127 - ((top & 0x7fffffu) > 0x600000u ? 7 : 8);
+    if (e < -126) e = -126;
+    return {__uint_as_float(static_cast<uint32_t>(e + 127) << 23),
+            __uint_as_float(static_cast<uint32_t>(127 - e) << 23)};
+}
+
+// Four codes in a word, the first in its lowest byte.  A scaled entry is exact
+// (but where it underflows, far below the smallest code).
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+}
+// (0 * infinity and 0 * NaN are not 0)
+__device__ __forceinline__ float scaled(float x, float inverse) { return inverse == 0.f ? 0.f : x * inverse; }
+
+template <typename T, bool SQUARE>
+__global__ void __launch_bounds__(THREADS, 2) quantize_kernel(const QuantArgs a) {
+    __shared__ __align__(16) uint4 turned[kB8Tile * (kB8Tile / 16)];
+    __shared__ uint32_t tops[THREADS / 32][kB8Tile];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t rt = blockIdx.x / a.col_tiles, ct = blockIdx.x - rt * a.col_tiles;
+    const int64_t r0 = rt * kB8Tile + warp * WARP_ROWS, c0 = ct * kB8Tile + lane * 4;
+    const T *x = static_cast<const T *>(a.x) + r0 * a.row_stride + c0 * a.col_stride;
+
+    float v[WARP_ROWS][4];
+    if (a.vec && c0 + 4 <= a.cols) {
+#pragma unroll
+        for (int i = 0; i < WARP_ROWS; ++i) {
+            if (r0 + i < a.rows) entries(x + i * a.row_stride, v[i]);
+            else v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < WARP_ROWS; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[i][j] = r0 + i < a.rows && c0 + j < a.cols ? entry(x + i * a.row_stride + j * a.col_stride) : 0.f;
+    }
+
+    uint32_t ctop[4] = {0, 0, 0, 0};
+    if (SQUARE || a.c.codes) {
+#pragma unroll
+        for (int i = 0; i < WARP_ROWS; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ctop[j] = max(ctop[j], __float_as_uint(v[i][j]) & 0x7fffffffu);
+    }
+    Scale tile = {1.f, 1.f};
+    if (SQUARE) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, max(max(ctop[0], ctop[1]), max(ctop[2], ctop[3])));
+        if (lane == 0) tops[0][warp] = top;
+        __syncthreads();
+        tile = scale_of(__reduce_max_sync(0xffffffffu, lane < THREADS / 32 ? tops[0][lane] : 0u));
+        if (threadIdx.x == 0) {
+            if (a.r.codes) a.r.scales[rt * a.r.scale_stride + ct] = tile.s;
+            if (a.c.codes) a.c.scales[ct * a.c.scale_stride + rt] = tile.s;
+        }
+    }
+    if (a.r.codes) {
+        const bool whole = c0 + 4 <= a.cols;
+#pragma unroll
+        for (int i = 0; i < WARP_ROWS; ++i) {
+            Scale s = tile;
+            if (!SQUARE) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+                s = scale_of(__reduce_max_sync(0xffffffffu, top));
+            }
+            if (r0 + i >= a.rows) continue;
+            if (!SQUARE && lane == 0) a.r.scales[(r0 + i) * a.r.scale_stride + ct] = s.s;
+            const uint32_t w = codes4(scaled(v[i][0], s.inverse), scaled(v[i][1], s.inverse),
+                                      scaled(v[i][2], s.inverse), scaled(v[i][3], s.inverse));
+            uint8_t *to = a.r.codes + (r0 + i) * a.r.row_stride + c0;
+            if (whole) {
+                *reinterpret_cast<uint32_t *>(to) = w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (c0 + j < a.cols) to[j] = static_cast<uint8_t>(w >> (8 * j));
+            }
+        }
+    }
+    if (a.c.codes) {
+        Scale s[4] = {tile, tile, tile, tile};
+        if (!SQUARE) {
+            *reinterpret_cast<uint4 *>(&tops[warp][lane * 4]) = make_uint4(ctop[0], ctop[1], ctop[2], ctop[3]);
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) {
+                const uint4 t = *reinterpret_cast<const uint4 *>(&tops[w][lane * 4]);
+                ctop[0] = max(ctop[0], t.x);
+                ctop[1] = max(ctop[1], t.y);
+                ctop[2] = max(ctop[2], t.z);
+                ctop[3] = max(ctop[3], t.w);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[j] = scale_of(ctop[j]);
+                if (warp == 0 && c0 + j < a.cols) a.c.scales[(c0 + j) * a.c.scale_stride + rt] = s[j].s;
+            }
+        }
+        // Piece `warp` (16 codes) of column 4 lane + j lies at place warp ^ (lane % 8)
+        // of the column's eight: eight lanes write, and later read, all banks.
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = codes4(scaled(v[4 * i][j], s[j].inverse), scaled(v[4 * i + 1][j], s[j].inverse),
+                              scaled(v[4 * i + 2][j], s[j].inverse), scaled(v[4 * i + 3][j], s[j].inverse));
+            turned[(lane * 4 + j) * 8 + (warp ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncthreads();
+        const int piece = threadIdx.x % 8;
+        const int64_t row = rt * kB8Tile + piece * 16;
+#pragma unroll
+        for (int i = 0; i < kB8Tile * 8 / THREADS; ++i) {
+            const int c = i * (THREADS / 8) + threadIdx.x / 8;
+            const int64_t col = ct * kB8Tile + c;
+            if (col >= a.cols || row >= a.rows) continue;
+            const uint4 w = turned[c * 8 + (piece ^ ((c >> 2) & 7))];
+            uint8_t *to = a.c.codes + col * a.c.row_stride + row;
+            if (row + 16 <= a.rows) {
+                *reinterpret_cast<uint4 *>(to) = w;
+            } else {
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 15; ++k)
+                    if (row + k < a.rows) to[k] = static_cast<uint8_t>(u[k / 4] >> (8 * (k % 4)));
+            }
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch(const QuantArgs &a, bool square, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(a.row_tiles * a.col_tiles));
+    return square ? launch_pdl(quantize_kernel<T, true>, grid, dim3(THREADS), 0, stream, a)
+                  : launch_pdl(quantize_kernel<T, false>, grid, dim3(THREADS), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(const QuantArgs &a, int32_t type, bool square, cudaStream_t stream) {
+    switch (type) {
+        case TN_TYPE_F32: return launch<float>(a, square, stream);
+        case TN_TYPE_BF16: return launch<__nv_bfloat16>(a, square, stream);
+        default: return launch<__half>(a, square, stream);
+    }
+}
+
+}  // namespace tn
