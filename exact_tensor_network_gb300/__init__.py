@@ -13,7 +13,7 @@ import ctypes
 import os
 from typing import Optional, Sequence, Tuple
 
-from . import block8, outcomes
+from . import block8, outcomes, sampling
 from .block8 import (Blocks8, TN_BLOCK8, linear8, linear8_grad, product8, quantize8, tn_block8,  # noqa: F401
                      tn_block8_check, tn_block8_last_error, tn_block8_product, tn_block8_quantize, tn_matrix)
 from .outcomes import (Distill, Outcomes, Scores, TN_OUTCOMES_MAX_IDS, TN_OUTCOMES_MAX_TOP,  # noqa: F401
@@ -22,6 +22,9 @@ from .outcomes import (Distill, Outcomes, Scores, TN_OUTCOMES_MAX_IDS, TN_OUTCOM
                        tn_outcomes_distill_grad, tn_outcomes_distill_step, tn_outcomes_last_error,
                        tn_outcomes_score, tn_outcomes_score_grad, tn_outcomes_set_workspace,
                        tn_outcomes_workspace_bytes, tn_rows, tn_teacher)
+from .sampling import (Sampler, Samples, tn_filters, tn_sampler_check, tn_sampler_create,  # noqa: F401
+                       tn_sampler_destroy, tn_sampler_draw, tn_sampler_last_error,
+                       tn_sampler_set_workspace, tn_sampler_workspace_bytes)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtn_gb300.so")
@@ -120,6 +123,7 @@ SIGNATURES = {
 }
 SIGNATURES.update(outcomes.SIGNATURES)
 SIGNATURES.update(block8.SIGNATURES)
+SIGNATURES.update(sampling.SIGNATURES)
 
 
 def lib() -> ctypes.CDLL:

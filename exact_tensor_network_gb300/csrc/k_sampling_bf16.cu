@@ -1,0 +1,8 @@
+// Drawing outcomes from rows of bf16 logits.
+#include "sampling.cuh"
+
+namespace tn {
+
+template cudaError_t sample_of<TN_TYPE_BF16>(const SampleArgs &, cudaStream_t);
+
+}  // namespace tn

@@ -1,0 +1,75 @@
+"""Draws against the definitions with exact sums."""
+import itertools
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_tensor_network_gb300 as tn
+
+import sampling_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"c64": torch.complex64, "f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def _rows(type_, R, n, seed=0, spread=2.0):
+    g = torch.Generator().manual_seed(seed * 77 + n)
+    if type_ == "c64":
+        return torch.view_as_complex(torch.randn(R, n, 2, generator=g) * 0.1)
+    return (torch.randn(R, n, generator=g) * spread).to(TYPES[type_])
+
+
+def _numpy(rows):
+    return rows.cpu().numpy() if rows.is_complex() else rows.float().cpu().numpy()
+
+
+def _compare(got, rows, u, scale=1.0, mask=None, **filters):
+    x, u = _numpy(rows), u.cpu().numpy()
+    if u.ndim == 1:
+        u = u[:, None]
+    ids, logp, kept = got.ids.cpu().numpy().reshape(u.shape), got.logp.cpu().numpy().reshape(u.shape), got.kept.cpu().numpy()
+    if mask is not None:
+        mask = mask.expand(x.shape).cpu().numpy()
+    for r in range(x.shape[0]):
+        own = {k: (v[r].item() if torch.is_tensor(v) else v) for k, v in filters.items()}
+        entries = ref.left(x[r], None if mask is None else mask[r], scale, **own)
+        assert kept[r] == (0 if isinstance(entries, str) else len(entries)), r
+        for d in range(u.shape[1]):
+            e, lp = ref.draw(entries, u[r, d])
+            assert ids[r, d] == e, (r, d)
+            if math.isnan(lp):
+                assert math.isnan(logp[r, d])
+            elif math.isinf(lp):
+                assert logp[r, d] == lp
+            else:       # one rounding to fp32 of a number computed in 64 bits
+                assert abs(logp[r, d] - lp) <= 2.0 ** -24 * abs(lp) + 1e-12, (r, d)
+
+
+FILTERS = [{}, {"temperature": 0.7}, {"temperature": 0.0}, {"top_k": 1}, {"top_k": 5}, {"top_k": 50, "temperature": 1.3},
+           {"top_p": 0.9}, {"top_p": 0.3, "temperature": 0.5}, {"min_p": 0.1}, {"top_k": 20, "top_p": 0.8},
+           {"top_k": 40, "top_p": 0.95, "min_p": 0.05, "temperature": 0.8}, {"top_p": 0.0}, {"min_p": 1.0},
+           {"top_k": 10 ** 6, "top_p": 1.0}, {"top_p": 0.999}]
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("n", [1, 2, 7, 64, 100, 1000, 4099])
+@pytest.mark.parametrize("filters", FILTERS, ids=str)
+def test_sample(type_, n, filters):
+    R = 4
+    rows = _rows(type_, R, n)
+    u = torch.rand(R, 5, generator=torch.Generator().manual_seed(n), dtype=torch.float64)
+    u[0, 0] = 0.0
+    op = tn.Sampler(n, TYPES[type_], max_rows=R)
+    got = op.sample(rows.cuda(), u.cuda(), **filters)
+    torch.cuda.synchronize()
+    op.check()
+    _compare(got, rows, u, **filters)
