@@ -34,7 +34,18 @@ int64_t vectors(int32_t type, int64_t cols) {
     const int64_t E = tn::kOutVecBytes / tn::out_entry_bytes(type);
     return (cols + 2 * (E - 1)) / E;
 }
-int64_t pieces(int32_t type, int64_t cols) { return (vectors(type, cols) + tn::kPieceVecs - 1) / tn::kPieceVecs; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t pieces(int32_t type, int64_t cols) { return ceil_div(vectors(type, cols), tn::kPieceVecs); }
+
+// CTAs for every SM where rows alone are too few, segments of a piece a warp at least.
+int64_t segment(int64_t pieces, int64_t rows, int64_t *len) {
+    int64_t want = tn::kDrawTarget / rows;
+    const int64_t most = ceil_div(pieces, tn::kDrawWarps);
+    if (want > most) want = most;
+    if (want < 1) want = 1;
+    *len = ceil_div(ceil_div(pieces, want), tn::kDrawWarps) * tn::kDrawWarps;
+    return ceil_div(pieces, *len);
+}
 
 }  // namespace
 
@@ -49,7 +60,7 @@ tn_status tn_sampler_create(int32_t type, int64_t cols, int64_t max_rows, float 
         return fail(g_error, TN_EINVAL, "scale must lie in 2^-40 .. 2^40");
     if (cols > 0x7fffffff) return fail(g_error, TN_EOVERFLOW, "more than 2^31 - 1 entries a row");
     int64_t n;
-    if (__builtin_mul_overflow(max_rows, pieces(type, cols), &n) || n > (int64_t)1 << 56)
+    if (__builtin_mul_overflow(max_rows, pieces(type, cols), &n) || n > (int64_t)1 << 48)
         return fail(g_error, TN_EOVERFLOW, "the workspace's size overflows");
     tn_sampler_s *h = new (std::nothrow) tn_sampler_s;
     if (!h) return fail(g_error, TN_ENOMEM, "host allocation failed");
@@ -58,7 +69,19 @@ tn_status tn_sampler_create(int32_t type, int64_t cols, int64_t max_rows, float 
     s.cols = cols;
     s.max_rows = max_rows;
     s.scale = scale;
-    s.mass_off = 256;
+    uint64_t at = 256;
+    if (vectors(type, cols) > tn::kRowVecs) {
+        // rows of several segments are at most half of kDrawTarget, their segments kDrawTarget
+        const uint64_t cut = max_rows < tn::kDrawTarget / 2 ? max_rows : tn::kDrawTarget / 2;
+        s.state_off = at;
+        s.bins_off = align(s.state_off + static_cast<uint64_t>(max_rows) * tn::state_bytes());
+        s.clear_bytes = s.partial_off = align(s.bins_off + cut * tn::bins_bytes());
+        s.list_off = align(s.partial_off + tn::kDrawTarget * sizeof(ulonglong2));
+        at = align(s.list_off + cut * tn::kSorted * sizeof(uint64_t));
+    } else {
+        s.clear_bytes = at;
+    }
+    s.mass_off = at;
     s.ws_bytes = align(s.mass_off + static_cast<uint64_t>(n) * 8);
     g_error[0] = 0;
     *out = h;
@@ -82,7 +105,7 @@ tn_status tn_sampler_set_workspace(tn_sampler_t *h, void *dev_ptr, uint64_t byte
         return fail(s.error, TN_ENOMEM, "workspace of %llu bytes is smaller than the %llu bytes needed",
                     (unsigned long long)bytes, (unsigned long long)s.ws_bytes);
     s.ws = nullptr;
-    cudaError_t e = cudaMemset(dev_ptr, 0, s.mass_off);
+    cudaError_t e = cudaMemset(dev_ptr, 0, s.clear_bytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(s, e, "clearing the workspace");
     s.ws = static_cast<char *>(dev_ptr);
@@ -132,7 +155,18 @@ tn_status tn_sampler_draw(tn_sampler_t *h, const tn_rows *r, const tn_filters *f
     a.ids = ids;
     a.logp = logp;
     a.kept = kept;
+    const tn_filters &f = a.f;
+    a.filtered = f.top_ks || f.top_ps || f.top_k > 0 || f.top_p < 1.f;
     a.pieces = pieces(s.type, s.cols);
+    if (s.state_off) {
+        a.segs = segment(a.pieces, r->rows, &a.seg_pieces);
+        a.state = reinterpret_cast<tn::RowState *>(s.ws + s.state_off);
+        a.bins = reinterpret_cast<tn::RowBins *>(s.ws + s.bins_off);
+        a.partials = reinterpret_cast<ulonglong2 *>(s.ws + s.partial_off);
+        a.lists = reinterpret_cast<uint64_t *>(s.ws + s.list_off);
+    }
+    if (r->rows * (a.segs + ceil_div(draws, tn::kDrawWarps)) > 0x7fffffff)
+        return fail(s.error, TN_EOVERFLOW, "too many draws or rows for one call");
     a.masses = reinterpret_cast<uint64_t *>(s.ws + s.mass_off);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;

@@ -217,7 +217,7 @@ __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const 
 // and from an estimate of its weights' sum
 __device__ __forceinline__ int shift_of(float sum) {
     int x;
-    frexpf(sum * 1.001f, &x);
+    frexpf(fminf(fmaxf(sum, 0.25f), 0x1p33f) * 1.001f, &x);
     return 61 - x;
 }
 
@@ -362,10 +362,29 @@ struct RowCta {
     }
 };
 
-// One warp: a draw of row r from its pieces' sums.
+// The first of n sums at which their total exceeds `target`, which becomes what is
+// left of it there; one warp.  sums[i stride].
+__device__ __forceinline__ int64_t locate(const uint64_t *sums, int64_t n, int stride, uint64_t &target) {
+    const int lane = threadIdx.x % 32;
+    for (int64_t base = 0; base < n; base += 32) {
+        const uint64_t own = base + lane < n ? __ldcg(sums + (base + lane) * stride) : 0, upto = warp_scan(own, lane);
+        const uint32_t over = __ballot_sync(0xffffffffu, upto > target);
+        if (over) {
+            const int l = __ffs(over) - 1;
+            target -= shfl_from(upto - own, l);
+            return base + l;
+        }
+        target -= shfl_from(upto, 31);
+    }
+    return 0;
+}
+
+// One warp: a draw of row r.  Where the row has segments, `partials` are their
+// sums (the first of each pair) and `seg_pieces` their length.
 template <int TYPE>
 __device__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs, const RowPlan &p, const float2 *roots,
-                          const uint64_t *masses, int64_t pieces, uint64_t total, int64_t at, int64_t row) {
+                          const uint64_t *masses, int64_t pieces, const ulonglong2 *partials, uint64_t total,
+                          int64_t at, int64_t row) {
     constexpr int E = Entry<TYPE>::E;
     const int lane = threadIdx.x % 32;
     const double u = a.wide ? static_cast<const double *>(a.u)[at] : static_cast<const float *>(a.u)[at];
@@ -377,19 +396,13 @@ __device__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs,
         }
         return;
     }
-    uint64_t target = share(u, total, false);
-    int64_t piece = 0;
-    for (int64_t base = 0; base < pieces; base += 32) {
-        const uint64_t own = base + lane < pieces ? masses[base + lane] : 0, upto = warp_scan(own, lane);
-        const uint32_t over = __ballot_sync(0xffffffffu, upto > target);
-        if (over) {
-            const int l = __ffs(over) - 1;
-            target -= shfl_from(upto - own, l);
-            piece = base + l;
-            break;
-        }
-        target -= shfl_from(upto, 31);
+    uint64_t target = p.greedy ? 0 : share(u, total, false);
+    int64_t first = 0;
+    if (partials) {
+        first = locate(reinterpret_cast<const uint64_t *>(partials), a.segs, 2, target) * a.seg_pieces;
+        pieces = pieces - first < a.seg_pieces ? pieces - first : a.seg_pieces;
     }
+    const int64_t piece = first + locate(masses + first, pieces, 1, target);
     for (int i = 0; i < kPieceVecs / 32; ++i) {
         const int64_t j = piece * kPieceVecs + i * 32 + lane;
         float v[E];
@@ -428,6 +441,15 @@ __device__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs,
     }
 }
 
+// Outcomes of a row that has none.
+__device__ __forceinline__ void no_draws(const SampleArgs &a, int64_t row, int state) {
+    for (int64_t d = threadIdx.x; d < a.draws; d += kDrawThreads) {
+        a.ids[row * a.draws + d] = -1;
+        a.logp[row * a.draws + d] = state == kEmpty ? -__builtin_huge_valf() : __uint_as_float(0x7fc00000u);
+    }
+    if (threadIdx.x == 0) a.kept[row] = 0;
+}
+
 template <int TYPE, int NT>
 __global__ void __launch_bounds__(NT) sample_rows_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E;
@@ -456,11 +478,7 @@ __global__ void __launch_bounds__(NT) sample_rows_kernel(const __grid_constant__
         }
         __syncthreads();
         if (plan.state != kDraw) {
-            for (int64_t d = threadIdx.x; d < a.draws; d += NT) {
-                a.ids[row * a.draws + d] = -1;
-                a.logp[row * a.draws + d] = plan.state == kEmpty ? -__builtin_huge_valf() : __uint_as_float(0x7fc00000u);
-            }
-            if (threadIdx.x == 0) a.kept[row] = 0;
+            no_draws(a, row, plan.state);
             continue;
         }
         if (!plan.greedy) {
@@ -516,16 +534,532 @@ __global__ void __launch_bounds__(NT) sample_rows_kernel(const __grid_constant__
         if (threadIdx.x == 0) a.kept[row] = static_cast<int64_t>(kept);
         __syncthreads();
         for (int64_t d = warp; d < a.draws; d += NT / 32)
-            warp_draw<TYPE>(a, c.r, c.vecs, plan, roots, masses, pieces, total, row * a.draws + d, row);
+            warp_draw<TYPE>(a, c.r, c.vecs, plan, roots, masses, pieces, nullptr, total, row * a.draws + d,
+                            row);
         __syncthreads();
     }
 }
 
+// ---- rows in segments -------------------------------------------------------
+//
+// One CTA a segment, a kernel for each pass over the rows; the CTA that finishes a
+// row's last segment does what follows for the row:
+//   top_kernel      the largest entry and a rough sum of weights; then the row's plan
+//   bins_kernel     weights (and numbers) by bins of the order value, where a row has
+//                   a top_k or top_p; then the bin in which they cut
+//   cut_kernel      that bin's entries into a list; then sorted, the last rank left
+//   sums_kernel     sums of the weights left, by pieces and segments; then a few draws
+//   draws_kernel    many draws, a warp each
+// Passes are bound by memory or, those with weights, by arithmetic (some 60
+// operations an entry); launches hide behind each other's ends.
+
+struct RowState {
+    RowPlan plan;
+    float top_p, min_p;
+    int32_t top_k;
+    int32_t narrow;         // whether bins are wanted
+    float bin_scale;
+    int32_t slot_lo, slot_hi;   // slots (see slot_of) of the entries to sort
+    uint32_t expected;      // their number
+    uint64_t above, all;    // weights (or number, without top_p) before them, of all
+    uint64_t total;         // weights left
+    uint32_t arrived[4];
+    uint32_t listed;
+};
+
+struct RowBins {
+    unsigned long long mass[kBins];
+    uint32_t count[kBins];
+};
+
+// Place of an order value on a scale from the largest down, of kBins bins of kBins
+// slots: for logits linear, for amplitudes linear between powers of two.  A larger
+// value's is never greater (roundings are monotone).
+template <int TYPE>
+__device__ __forceinline__ int slot_of(const RowPlan &p, float bin_scale, float v) {
+    constexpr int kLast = kBins * kBins - 1;
+    if constexpr (Entry<TYPE>::kReal) {
+        const float t = (p.m - v) * bin_scale;
+        return t < static_cast<float>(kLast) ? static_cast<int>(t) : kLast;
+    } else {
+        const uint32_t d = (__float_as_uint(p.m) - __float_as_uint(v)) >> 7;
+        return d < kLast ? static_cast<int>(d) : kLast;
+    }
+}
+
+template <int TYPE>
+struct Segment {
+    Row<TYPE> r;
+    int64_t row, seg, vecs, lo, hi;     // vectors of the row and of the segment
+
+    __device__ __forceinline__ explicit Segment(const SampleArgs &a)
+        : r(a.r, static_cast<int64_t>(blockIdx.x / static_cast<uint32_t>(a.segs))) {
+        row = blockIdx.x / static_cast<uint32_t>(a.segs);
+        seg = blockIdx.x - row * a.segs;
+        vecs = (r.head + r.cols + Entry<TYPE>::E - 1) / Entry<TYPE>::E;
+        lo = seg * a.seg_pieces * kPieceVecs;
+        hi = lo + a.seg_pieces * kPieceVecs;
+        if (hi > vecs) hi = vecs;
+    }
+};
+
+// Whether this CTA is the last of its row's to come here.  What the others wrote
+// before is visible to it.
+__device__ __forceinline__ bool last_of_row(const SampleArgs &a, RowState &s, int which) {
+    __shared__ bool last;
+    if (a.segs == 1) {
+        __syncthreads();
+        return true;
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last = atomicAdd(&s.arrived[which], 1u) == a.segs - 1;
+        if (last) s.arrived[which] = 0;
+        __threadfence();
+    }
+    __syncthreads();
+    return last;
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E;
+    __shared__ uint32_t red[4 * kDrawWarps];
+    pdl_trigger();
+    pdl_wait();
+    Group<kDrawThreads> g(red);
+    const Segment<TYPE> c(a);
+    RowState &st = a.state[c.row];
+    Filters f;
+    const bool valid = filters_of(a, c.row, f);
+    // the sum relative to the largest entry so far
+    const float ch = fminf(f.beta * kLog2E, 3.402823466e38f);
+    float m = absent<TYPE>(), s = 0.f;
+    for (int64_t j = c.lo + threadIdx.x; j < c.hi; j += kDrawThreads) {
+        float v[E];
+        vector_values<TYPE>(c.r, j, v);
+        float top = v[0];
+#pragma unroll
+        for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
+        if (!(top <= m)) {
+            if constexpr (Entry<TYPE>::kReal) s *= ex2((m - top) * ch);
+            else if (f.beta != 1.f) s *= m > 0.f ? ex2(f.beta * (lg2(m) - lg2(top))) : 0.f;
+            m = max_nan(m, top);
+        }
+        if constexpr (Entry<TYPE>::kReal) {
+            if (top != absent<TYPE>()) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) s += ex2((v[i] - m) * ch);
+            }
+        } else if (f.beta == 1.f) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) s += v[i];
+        } else if (m > 0.f) {
+            const float l = lg2(m);
+#pragma unroll
+            for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(f.beta * (lg2(v[i]) - l)) : 0.f;
+        }
+    }
+    // threads', then segments'
+    const auto moved = [&](float from, float to) {
+        if (from == absent<TYPE>()) return 0.f;
+        if constexpr (Entry<TYPE>::kReal) return ex2((from - to) * ch);
+        else return f.beta == 1.f ? 1.f : ex2(f.beta * (lg2(from) - lg2(to)));
+    };
+    const float own = m;
+    m = g.max(m);
+    s = g.sum(own == absent<TYPE>() ? 0.f : s * moved(own, m));
+    if (a.segs > 1) {
+        ulonglong2 *parts = a.partials + c.row * a.segs;
+        if (threadIdx.x == 0)
+            __stcg(&parts[c.seg], make_ulonglong2(__float_as_uint(m), __float_as_uint(s)));
+        if (!last_of_row(a, st, 0)) return;
+        m = absent<TYPE>();
+        for (int64_t i = threadIdx.x; i < a.segs; i += kDrawThreads)
+            m = max_nan(m, __uint_as_float(static_cast<uint32_t>(__ldcg(&parts[i]).x)));
+        m = g.max(m);
+        s = 0.f;
+        for (int64_t i = threadIdx.x; i < a.segs; i += kDrawThreads) {
+            const ulonglong2 p = __ldcg(&parts[i]);
+            s += __uint_as_float(static_cast<uint32_t>(p.y)) * moved(__uint_as_float(static_cast<uint32_t>(p.x)), m);
+        }
+        s = g.sum(s);
+    }
+    __shared__ int state;
+    if (threadIdx.x == 0) {
+        RowPlan p;
+        plan_row<TYPE>(p, m, valid, f);
+        if (!valid) flag_bad_id(a.r, c.row);
+        state = p.state;
+        st.narrow = 0;
+        st.listed = 0;
+        if (p.state == kDraw) {
+            if (!Entry<TYPE>::kReal && f.beta == 1.f) s *= p.down;
+            p.shift = p.greedy ? 0 : shift_of(s);
+            if (p.greedy) {
+                p.bound = static_cast<uint64_t>(order_key<TYPE>(m)) << 32;
+            } else {
+                if (f.min_p > 0.f) p.bound = static_cast<uint64_t>(order_key<TYPE>(least_value<TYPE>(p, f.min_p))) << 32;
+                st.narrow = (f.top_k > 0 && f.top_k < a.r.cols) || f.top_p < 1.f;
+            }
+        }
+        st.plan = p;
+        st.top_p = fmaxf(f.top_p, 0.f);
+        st.top_k = f.top_k;
+        // 32 bins a power of two in weight; for top_k, whose place has nothing to do with weights, 128
+        // a unit of the logits at most
+        const float scale = 32.f * p.ch;
+        st.bin_scale = kBins * fminf(scale, f.top_k > 0 ? 128.f : 0x1p80f);
+    }
+    __syncthreads();
+    if (state != kDraw) no_draws(a, c.row, state);
+}
+
+__device__ __forceinline__ void add_mass(uint32_t *lo, uint32_t *hi, uint64_t w) {
+    const uint32_t l = static_cast<uint32_t>(w), old = atomicAdd(lo, l);
+    const uint32_t h = static_cast<uint32_t>(w >> 32) + (old + l < l);
+    if (h) atomicAdd(hi, h);
+}
+
+// exclusive prefix sums over the CTA's threads; `sums` has kDrawWarps + 1 places, the
+// last for the total
+__device__ __forceinline__ uint64_t cta_scan(uint64_t x, uint64_t *sums) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint64_t upto = warp_scan(x, lane);
+    __syncthreads();
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    uint64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kDrawWarps; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    if (threadIdx.x == 0) sums[kDrawWarps] = total;
+    __syncthreads();
+    return before + upto - x;
+}
+
+// FINE: the bins are the slots of the bin in which the first pass ended, where it
+// has more entries than are sorted.
+template <int TYPE, bool FINE>
+__global__ void __launch_bounds__(kDrawThreads) bins_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E, kOwn = kBins / kDrawThreads;
+    __shared__ uint32_t lo[kBins], hi[kBins], count[kBins];
+    __shared__ float2 roots[64];
+    __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
+    pdl_trigger();
+    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    for (int i = threadIdx.x; i < kBins; i += kDrawThreads) lo[i] = hi[i] = count[i] = 0;
+    pdl_wait();
+    const Segment<TYPE> c(a);
+    RowState &st = a.state[c.row];
+    if (!st.narrow || (FINE && (st.expected <= kSorted || st.slot_hi - st.slot_lo != kBins - 1))) return;
+    const RowPlan p = st.plan;
+    const float bin_scale = st.bin_scale;
+    const bool by_mass = st.top_p < 1.f;
+    const int64_t k = st.top_k > 0 && st.top_k < a.r.cols ? st.top_k : 0;
+    const int first = FINE ? st.slot_lo : 0;
+    const uint64_t above0 = FINE ? st.above : 0;
+    __syncthreads();
+    for (int64_t j = c.lo + threadIdx.x; j < c.hi; j += kDrawThreads) {
+        float v[E];
+        vector_values<TYPE>(c.r, j, v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (v[i] == absent<TYPE>()) continue;
+            int b = slot_of<TYPE>(p, bin_scale, v[i]) - first;
+            if (!FINE) b /= kBins;
+            if (FINE && (b < 0 || b >= kBins)) continue;
+            atomicAdd(&count[b], 1u);
+            if (by_mass) add_mass(&lo[b], &hi[b], weight<TYPE>(p, roots, v[i]));
+        }
+    }
+    __syncthreads();
+    RowBins *all = a.segs > 1 ? a.bins + c.row : nullptr;
+    if (all) {
+        for (int i = threadIdx.x; i < kBins; i += kDrawThreads)
+            if (count[i]) {
+                atomicAdd(&all->count[i], count[i]);
+                if (by_mass) atomicAdd(&all->mass[i], static_cast<unsigned long long>(hi[i]) << 32 | lo[i]);
+            }
+        if (!last_of_row(a, st, 1)) return;
+    }
+    uint64_t mass[kOwn], own_mass = 0, own_count = 0;
+    uint32_t num[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int b = threadIdx.x * kOwn + i;
+        num[i] = all ? __ldcg(&all->count[b]) : count[b];
+        mass[i] = all ? __ldcg(&all->mass[b]) : static_cast<uint64_t>(hi[b]) << 32 | lo[b];
+        if (all) {      // left clear
+            all->count[b] = 0;
+            all->mass[b] = 0;
+        }
+        own_mass += mass[i];
+        own_count += num[i];
+    }
+    uint64_t before_mass = cta_scan(own_mass, sums), before_count = cta_scan(own_count, nums);
+    const uint64_t total = sums[kDrawWarps], entries = nums[kDrawWarps];
+    const bool cut_k = FINE ? k > 0 : k > 0 && static_cast<uint64_t>(k) < entries;
+    if (!cut_k && !by_mass) {       // fewer entries than top_k
+        if (threadIdx.x == 0) st.narrow = 0;
+        return;
+    }
+    uint64_t target = cut_k ? k : share(st.top_p, FINE ? st.all : total, true);
+    if (target == 0) target = 1;
+    uint64_t before = above0 + (cut_k ? before_count : before_mass), through = before_count;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const uint64_t x = cut_k ? num[i] : mass[i];
+        through += num[i];
+        if (before < target && before + x >= target) {      // one thread, one bin
+            const int b = threadIdx.x * kOwn + i;
+            // with both filters the second needs all that the first leaves
+            const bool both = cut_k && by_mass;
+            st.slot_lo = both ? 0 : FINE ? first + b : b * kBins;
+            st.slot_hi = FINE ? first + b : b * kBins + kBins - 1;
+            st.expected = static_cast<uint32_t>(both ? through : num[i]);
+            st.above = both ? 0 : before;
+            st.all = FINE ? st.all : total;
+            if (!cut_k) st.top_k = 0;
+        }
+        before += x;
+    }
+}
+
+// Ranks in descending order; n a power of two.
+__device__ __forceinline__ void sort_ranks(uint64_t *x, int n) {
+    for (int size = 2; size <= n; size *= 2)
+        for (int step = size / 2; step; step /= 2) {
+            __syncthreads();
+            for (int t = threadIdx.x; t < n / 2; t += kDrawThreads) {
+                const int i = 2 * t - (t & (step - 1)), j = i + step;
+                const uint64_t y = x[i], z = x[j];
+                if ((y < z) == ((i & size) == 0)) {
+                    x[i] = z;
+                    x[j] = y;
+                }
+            }
+        }
+    __syncthreads();
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kDrawThreads) cut_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E;
+    __shared__ uint64_t list[kSorted];
+    __shared__ float2 roots[64];
+    __shared__ Select sel;
+    __shared__ uint64_t sums[kDrawWarps + 1];
+    __shared__ RowPlan plan;
+    __shared__ uint32_t listed;
+    pdl_trigger();
+    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    pdl_wait();
+    const Segment<TYPE> c(a);
+    RowState &st = a.state[c.row];
+    if (!st.narrow) return;
+    const bool by_mass = st.top_p < 1.f, sorted = st.expected <= kSorted;
+    const int lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        plan = st.plan;
+        listed = 0;
+    }
+    __syncthreads();
+    uint64_t *to = a.segs > 1 ? a.lists + c.row * kSorted : list;
+    uint32_t *counter = a.segs > 1 ? &st.listed : &listed;
+    if (sorted) {
+        const float bin_scale = st.bin_scale;
+        const int lo = st.slot_lo, hi = st.slot_hi;
+        for (int64_t j0 = c.lo; j0 < c.hi; j0 += kDrawThreads) {
+            const int64_t j = j0 + threadIdx.x;
+            float v[E];
+            uint32_t in = 0;
+            if (j < c.hi) {
+                vector_values<TYPE>(c.r, j, v);
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const int s = slot_of<TYPE>(plan, bin_scale, v[i]);
+                    if (v[i] != absent<TYPE>() && s >= lo && s <= hi) in |= 1u << i;
+                }
+            }
+            if (!__any_sync(0xffffffffu, in != 0)) continue;
+            const uint32_t n = __popc(in);
+            const uint32_t upto = static_cast<uint32_t>(warp_scan(n, lane));
+            uint32_t base = 0;
+            if (lane == 31) base = atomicAdd(counter, upto);
+            base = __shfl_sync(0xffffffffu, base, 31) + upto - n;
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (in >> i & 1) {
+                    if (base < kSorted) to[base] = rank_of<TYPE>(v[i], j * E - c.r.head + i);
+                    ++base;
+                }
+        }
+    }
+    if (!last_of_row(a, st, 2)) return;
+    uint64_t bound = kPresent;
+    if (sorted) {
+        const uint32_t found = a.segs > 1 ? __ldcg(&st.listed) : listed;
+        const int n = static_cast<int>(found < kSorted ? found : kSorted);
+        int room = 2;
+        while (room < n) room *= 2;
+        for (int i = threadIdx.x; i < room; i += kDrawThreads)
+            list[i] = i >= n ? 0 : a.segs > 1 ? __ldcg(&to[i]) : list[i];
+        sort_ranks(list, room);
+        int64_t left = n;
+        if (st.top_k > 0) {
+            left = st.top_k - static_cast<int64_t>(by_mass ? 0 : st.above);
+            if (left > n) left = n;
+            bound = list[left > 0 ? left - 1 : 0];
+        }
+        if (by_mass) {
+            // of consecutive ranks, a thread each
+            const int per = static_cast<int>((left + kDrawThreads - 1) / kDrawThreads);
+            const int lo = threadIdx.x * per < left ? threadIdx.x * per : static_cast<int>(left);
+            const int hi = lo + per < left ? lo + per : static_cast<int>(left);
+            uint64_t own = 0;
+            for (int i = lo; i < hi; ++i)
+                own += weight<TYPE>(plan, roots, key_value(static_cast<uint32_t>(list[i] >> 32)));
+            uint64_t upto = st.above + cta_scan(own, sums);
+            uint64_t target = share(st.top_p, st.top_k > 0 ? sums[kDrawWarps] : st.all, true);
+            if (target == 0) target = 1;
+            __shared__ uint64_t cut;
+            if (threadIdx.x == 0) cut = left > 0 ? list[left - 1] : kPresent;
+            __syncthreads();
+            for (int i = lo; i < hi; ++i) {
+                const uint64_t w = weight<TYPE>(plan, roots, key_value(static_cast<uint32_t>(list[i] >> 32)));
+                if (upto < target && upto + w >= target) cut = list[i];
+                upto += w;
+            }
+            __syncthreads();
+            bound = cut;
+        }
+    } else {
+        // more equal (or nearly equal) entries than are sorted: digit by digit
+        RowCta<TYPE, kDrawThreads> cta{c.r, c.vecs, &plan, roots, &sel, sums};
+        if (st.top_k > 0) bound = cta.template select<false>(st.top_k, bound);
+        if (by_mass) {
+            const uint64_t all = cta.template total<true>(bound), t = share(st.top_p, all, true);
+            bound = cta.template select<true>(t > 0 ? t : 1, bound);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        st.listed = 0;
+        if (bound > plan.bound) st.plan.bound = bound;
+    }
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kDrawThreads) sums_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E;
+    __shared__ float2 roots[64];
+    __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
+    pdl_trigger();
+    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    pdl_wait();
+    const Segment<TYPE> c(a);
+    RowState &st = a.state[c.row];
+    const RowPlan p = st.plan;
+    if (p.state != kDraw) return;
+    __syncthreads();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint64_t *masses = a.masses + c.row * a.pieces;
+    uint64_t total = 0, kept = 0;
+    for (int64_t q = c.lo / kPieceVecs + warp; q * kPieceVecs < c.hi; q += kDrawWarps) {
+        uint64_t own = 0;
+#pragma unroll
+        for (int i = 0; i < kPieceVecs / 32; ++i) {
+            const int64_t j = q * kPieceVecs + i * 32 + lane;
+            if (j >= c.hi) break;
+            float v[E];
+            vector_values<TYPE>(c.r, j, v);
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if (rank_of<TYPE>(v[k], j * E - c.r.head + k) >= p.bound) {
+                    own += weight<TYPE>(p, roots, v[k]);
+                    ++kept;
+                }
+        }
+        total += own;
+        own = warp_sum(own);
+        if (lane == 0) __stcg(&masses[q], own);
+    }
+    cta_scan(total, sums);
+    cta_scan(kept, nums);
+    total = sums[kDrawWarps];
+    kept = nums[kDrawWarps];
+    const ulonglong2 *parts = nullptr;
+    if (a.segs > 1) {
+        ulonglong2 *mine = a.partials + c.row * a.segs;
+        if (threadIdx.x == 0) __stcg(&mine[c.seg], make_ulonglong2(total, kept));
+        if (!last_of_row(a, st, 3)) return;
+        parts = mine;
+        total = kept = 0;
+        for (int64_t i = threadIdx.x; i < a.segs; i += kDrawThreads) {
+            const ulonglong2 x = __ldcg(&mine[i]);
+            total += x.x;
+            kept += x.y;
+        }
+        cta_scan(total, sums);
+        cta_scan(kept, nums);
+        total = sums[kDrawWarps];
+        kept = nums[kDrawWarps];
+    } else {
+        __syncthreads();        // the pieces' sums
+    }
+    if (threadIdx.x == 0) {
+        a.kept[c.row] = p.greedy ? 1 : static_cast<int64_t>(kept);
+        st.total = total;
+    }
+    if (a.draws > kFewDraws) return;
+    const int64_t pieces = (c.vecs + kPieceVecs - 1) / kPieceVecs;
+    for (int64_t d = warp; d < a.draws; d += kDrawWarps)
+        warp_draw<TYPE>(a, c.r, c.vecs, p, roots, masses, pieces, parts, total, c.row * a.draws + d, c.row);
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_constant__ SampleArgs a) {
+    __shared__ float2 roots[64];
+    pdl_trigger();
+    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    pdl_wait();
+    __syncthreads();
+    const int64_t ctas = (a.draws + kDrawWarps - 1) / kDrawWarps;
+    const int64_t row = blockIdx.x / ctas, d = (blockIdx.x - row * ctas) * kDrawWarps + threadIdx.x / 32;
+    const RowState &st = a.state[row];
+    const RowPlan p = st.plan;
+    if (p.state != kDraw || d >= a.draws) return;
+    const Row<TYPE> r(a.r, row);
+    const int64_t vecs = (r.head + r.cols + Entry<TYPE>::E - 1) / Entry<TYPE>::E;
+    warp_draw<TYPE>(a, r, vecs, p, roots, a.masses + row * a.pieces, (vecs + kPieceVecs - 1) / kPieceVecs,
+                    a.segs > 1 ? a.partials + row * a.segs : nullptr, st.total, row * a.draws + d, row);
+}
+
 template <int TYPE>
 cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
-    const int64_t ctas = a.r.rows < 8 * kOutSms ? a.r.rows : 8 * kOutSms;
-    return launch_pdl(sample_rows_kernel<TYPE, kRowThreads>, dim3(static_cast<unsigned>(ctas)), dim3(kRowThreads), 0,
-                      stream, a);
+    const dim3 block(kDrawThreads);
+    if (!a.state) {
+        const int64_t ctas = a.r.rows < kDrawTarget ? a.r.rows : kDrawTarget;
+        return launch_pdl(sample_rows_kernel<TYPE, kDrawThreads>, dim3(static_cast<unsigned>(ctas)), block, 0, stream, a);
+    }
+    const dim3 grid(static_cast<unsigned>(a.r.rows * a.segs));
+    cudaError_t e = launch_pdl(top_kernel<TYPE>, grid, block, 0, stream, a);
+    if (e == cudaSuccess && a.filtered) {
+        e = launch_pdl(bins_kernel<TYPE, false>, grid, block, 0, stream, a);
+        if (e == cudaSuccess && a.r.cols >= kLongRow)
+            e = launch_pdl(bins_kernel<TYPE, true>, grid, block, 0, stream, a);
+        if (e == cudaSuccess) e = launch_pdl(cut_kernel<TYPE>, grid, block, 0, stream, a);
+    }
+    if (e == cudaSuccess) e = launch_pdl(sums_kernel<TYPE>, grid, block, 0, stream, a);
+    if (e == cudaSuccess && a.draws > kFewDraws) {
+        const int64_t ctas = a.r.rows * ((a.draws + kDrawWarps - 1) / kDrawWarps);
+        e = launch_pdl(draws_kernel<TYPE>, dim3(static_cast<unsigned>(ctas)), block, 0, stream, a);
+    }
+    return e;
 }
 
 }  // namespace tn
