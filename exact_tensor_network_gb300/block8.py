@@ -4,7 +4,8 @@
 The functions with the C names only marshal arguments; the others work on torch
 tensors.  ``Blocks8`` is a quantised matrix: codes (float8_e4m3fn [rows, cols], rows
 starting at multiples of 16 bytes) and scales (float32, [rows, blocks] or, for
-blocks of 128 x 128 entries, [blocks of rows, blocks]).
+blocks of 128 x 128 entries, [blocks of rows, blocks], of any strides; ``quantize8``
+lays those of rows out with the rows next to each other, which products read fastest).
 
     w = quantize8(weight, square=True)              # a head's weights, kept in 8 bits
     y = linear8(x, w)                               # rows of logits
@@ -38,7 +39,7 @@ class tn_matrix(ctypes.Structure):
 
 class tn_block8(ctypes.Structure):
     _fields_ = [("codes", _P), ("scales", _P), ("rows", _I64), ("cols", _I64), ("row_stride", _I64),
-                ("scale_stride", _I64), ("block_rows", _I32)]
+                ("scale_stride", _I64), ("scale_block", _I64), ("block_rows", _I32), ("powers", _I32)]
 
 
 _MP, _BP = ctypes.POINTER(tn_matrix), ctypes.POINTER(tn_block8)
@@ -85,9 +86,12 @@ def tn_block8_last_error() -> str:
 # ---- over torch tensors ----------------------------------------------------
 
 class Blocks8(NamedTuple):
-    """A quantised matrix: ``codes`` and ``scales``."""
+    """A quantised matrix: ``codes`` and ``scales``.  ``powers``: the scales are
+    powers of two (or NaN), as ``quantize8`` makes them and products are faster with;
+    False for any float32 scales."""
     codes: object
     scales: object
+    powers: bool = True
 
     def values(self):
         """What the codes stand for, in float32 (by torch, for inspection)."""
@@ -123,16 +127,15 @@ def _matrix(t, name) -> tn_matrix:
 
 def _blocks(b, name, device) -> tn_block8:
     import torch
-    codes, scales = b
+    codes, scales, powers = b
     if codes.dtype is not torch.float8_e4m3fn or codes.dim() != 2 or codes.device != device:
         raise ValueError(f"codes of {name} must be a 2-dimensional float8_e4m3fn tensor on the other operands' device")
     R, C = codes.shape
     if C > 1 and codes.stride(1) != 1:
         raise ValueError(f"rows of the codes of {name} must be contiguous")
     blocks = -(-C // TN_BLOCK8)
-    if scales.dtype is not torch.float32 or scales.device != device or scales.dim() != 2 or (
-            blocks > 1 and scales.stride(1) != 1):
-        raise ValueError(f"scales of {name} must be a float32 matrix with contiguous rows on the codes' device")
+    if scales.dtype is not torch.float32 or scales.device != device or scales.dim() != 2 or scales.is_neg():
+        raise ValueError(f"scales of {name} must be a float32 matrix on the codes' device")
     if tuple(scales.shape) == (R, blocks):
         tall = 1
     elif tuple(scales.shape) == (-(-R // TN_BLOCK8), blocks):
@@ -142,8 +145,8 @@ def _blocks(b, name, device) -> tn_block8:
                          f"not {tuple(scales.shape)}")
     # one row, or empty ones, have no stride of their own
     stride = codes.stride(0) if R > 1 and C > 0 else -(-C // 16) * 16
-    return tn_block8(codes.data_ptr(), scales.data_ptr(), R, C, stride,
-                     scales.stride(0) if scales.shape[0] > 1 else blocks, tall)
+    return tn_block8(codes.data_ptr(), scales.data_ptr(), R, C, stride, scales.stride(0) if scales.shape[0] > 1 else 1,
+                     scales.stride(1) if blocks > 1 else 1, tall, 1 if powers else 0)
 
 
 def _stream(device, stream, tensors):
@@ -166,8 +169,10 @@ def _new(R, C, square, device) -> Blocks8:
     codes = torch.empty((R, -(-C // 16) * 16), dtype=torch.float8_e4m3fn, device=device)
     if codes.shape[1] != C:
         codes = codes[:, :C]
-    return Blocks8(codes, torch.empty((-(-R // TN_BLOCK8) if square else R, -(-C // TN_BLOCK8)),
-                                      dtype=torch.float32, device=device))
+    blocks = -(-C // TN_BLOCK8)
+    if square:
+        return Blocks8(codes, torch.empty((-(-R // TN_BLOCK8), blocks), dtype=torch.float32, device=device))
+    return Blocks8(codes, torch.empty((blocks, R), dtype=torch.float32, device=device).t())
 
 
 class _Scratch:
@@ -178,7 +183,7 @@ class _Scratch:
         stride, blocks = -(-C // 16) * 16, -(-C // TN_BLOCK8)
         self.memory = torch.empty(R * (stride + 4 * blocks), dtype=torch.uint8, device=device)
         p = self.memory.data_ptr()
-        self.blocks = tn_block8(p, p + R * stride, R, C, stride, blocks, 1)
+        self.blocks = tn_block8(p, p + R * stride, R, C, stride, 1, max(R, 1), 1, 1)
 
 
 def quantize8(x, square: bool = False, layout: str = "rows", out=None, stream=None):
@@ -192,7 +197,7 @@ def quantize8(x, square: bool = False, layout: str = "rows", out=None, stream=No
     m, dev = _matrix(x, "x"), x.device
     R, C = x.shape
     given = () if out is None else out if layout == "both" else (out,)
-    sp, on = _stream(dev, stream, (x, *(t for b in given for t in b)))
+    sp, on = _stream(dev, stream, (x, *(t for b in given for t in b[:2])))
     if out is None:
         with on:
             given = tuple(_new(*shape, square, dev) for want, shape in (("rows", (R, C)), ("columns", (C, R)))
@@ -204,6 +209,8 @@ def quantize8(x, square: bool = False, layout: str = "rows", out=None, stream=No
                                                                          else shape[0]):
             raise ValueError("out does not have the result's shapes")
         s.block_rows = TN_BLOCK8 if square else 1
+        if not b.powers:
+            raise ValueError("out is marked as having other scales than powers of two")
         made.append(s)
     st = _lib().tn_block8_quantize(m, made[0] if layout != "columns" else None,
                                    made[-1] if layout != "rows" else None, sp)
@@ -242,7 +249,7 @@ def product8(a: Blocks8, b: Blocks8, dtype=None, out=None, stream=None):
     if dev.type != "cuda" or dev.index != torch._C._cuda_getDevice():
         raise ValueError(f"a is on {dev}, which is not the current device")
     A, B = _blocks(a, "a", dev), _blocks(b, "b", dev)
-    sp, on = _stream(dev, stream, (*a, *b, out))
+    sp, on = _stream(dev, stream, (*a[:2], *b[:2], out))
     out = _out(out, (A.rows, B.rows), dtype, dev, on)
     _product(A, B, out, sp)
     return out
@@ -255,7 +262,7 @@ def linear8(x, w: Blocks8, dtype=None, out=None, stream=None):
     W = _blocks(w, "w", dev)
     if W.cols != m.cols:
         raise ValueError(f"x has {m.cols} columns, w {W.cols}")
-    sp, on = _stream(dev, stream, (x, *w, out))
+    sp, on = _stream(dev, stream, (x, *w[:2], out))
     out = _out(out, (m.rows, W.rows), dtype or (out.dtype if out is not None else x.dtype), dev, on)
     with on:
         q = _Scratch(m.rows, m.cols, dev)
@@ -279,7 +286,7 @@ def linear8_grad(x, dy, w: Blocks8, dtype=None, stream=None):
     if dy.device != dev or Y.rows != R or W.rows != k or W.cols != n:
         raise ValueError(f"x must be [R, k], dy [R, n] and w the transposed weight [k, n] on one device, not "
                          f"{tuple(x.shape)}, {tuple(dy.shape)} and {tuple(w.codes.shape)}")
-    sp, on = _stream(dev, stream, (x, dy, *w))
+    sp, on = _stream(dev, stream, (x, dy, *w[:2]))
     dx = _out(None, (R, k), x.dtype, dev, on)
     dw = _out(None, (n, k), dtype or torch.float32, dev, on)
     with on:

@@ -41,8 +41,7 @@ tn_status check(const tn_block8 *m, const char *name) {
         return fail(TN_EINVAL, "block_rows of %s must be 1 or %d", name, (int)TN_BLOCK8);
     if (m->row_stride < m->cols || m->row_stride % 16)
         return fail(TN_EINVAL, "the row stride of %s must be a multiple of 16 and at least its columns", name);
-    if (m->scale_stride < ceil_div(m->cols, TN_BLOCK8))
-        return fail(TN_EINVAL, "the scales' stride of %s is less than its blocks", name);
+    if (m->scale_stride < 1 || m->scale_block < 1) return fail(TN_EINVAL, "strides of the scales of %s must be > 0", name);
     if (m->rows > 0 && m->cols > 0) {
         if (!m->codes || !m->scales) return fail(TN_EINVAL, "codes and scales of %s are required", name);
         if (reinterpret_cast<uintptr_t>(m->codes) % 16)
@@ -82,13 +81,13 @@ struct Tiles {
     int bn, split;
 };
 
-Tiles choose(int64_t m, int64_t n, int64_t kbs) {
+Tiles choose(int64_t m, int64_t n, int64_t kbs, int most) {
     Tiles t;
     t.swapped = m <= 128;
     const int64_t p = t.swapped ? n : m, q = t.swapped ? m : n;
     t.split = 1;
-    if (q > 128 && ceil_div(p, tn::kB8Tile) * ceil_div(q, 256) >= tn::kB8Sms / 2) {
-        t.bn = 256;
+    if (q > 128 && ceil_div(p, tn::kB8Tile) * ceil_div(q, most) >= tn::kB8Sms / 2) {
+        t.bn = most;
         return t;
     }
     t.bn = q > 64 ? 128 : q > 32 ? 64 : q > 16 ? 32 : 16;
@@ -133,8 +132,9 @@ tn_status tn_block8_quantize(const tn_matrix *x, const tn_block8 *rows, const tn
     a.cols = x->cols;
     a.row_stride = x->row_stride;
     a.col_stride = x->col_stride;
-    if (rows) a.r = {rows->codes, rows->scales, rows->row_stride, rows->scale_stride};
-    if (columns) a.c = {columns->codes, columns->scales, columns->row_stride, columns->scale_stride};
+    if (rows) a.r = {rows->codes, rows->scales, rows->row_stride, rows->scale_stride, rows->scale_block};
+    if (columns) a.c = {columns->codes, columns->scales, columns->row_stride, columns->scale_stride,
+                        columns->scale_block};
     if (a.row_stride == 1 && a.col_stride != 1) {       // x transposed is read along its rows
         const tn::Block8Out r = a.r;
         a.r = a.c;
@@ -147,9 +147,11 @@ tn_status tn_block8_quantize(const tn_matrix *x, const tn_block8 *rows, const tn
     a.row_tiles = ceil_div(a.rows, tn::kB8Tile);
     a.col_tiles = ceil_div(a.cols, tn::kB8Tile);
     if (a.row_tiles > 0x7fffffff / a.col_tiles) return fail(TN_EOVERFLOW, "more than 2^31 - 1 blocks of 128 x 128");
-    a.vec = a.col_stride == 1 && reinterpret_cast<uintptr_t>(a.x) % (4 * size) == 0 &&
-            (a.row_stride % 4 == 0 || a.rows == 1);
     const bool square = (rows ? rows : columns)->block_rows == TN_BLOCK8;
+    // 16 bytes at once where the rows alone are written, else four entries
+    const int vec = !a.c.codes && !square ? 16 / size : 4;
+    a.vec = a.col_stride == 1 && reinterpret_cast<uintptr_t>(a.x) % (vec * size) == 0 &&
+            (a.row_stride % vec == 0 || a.rows == 1);
     const cudaError_t e = tn::launch_quantize(a, x->type, square, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TN_OK : cuda_fail(e, "launching the quantisation");
 }
@@ -169,7 +171,8 @@ tn_status tn_block8_product(const tn_block8 *a, const tn_block8 *b, void *out, i
         return fail(TN_EINVAL, "the output is missing or not aligned to its entry type");
     tn::ProductArgs g = {};
     g.kbs = static_cast<int32_t>(ceil_div(a->cols, TN_BLOCK8));
-    const Tiles t = choose(m, n, g.kbs);
+    const bool powers = a->powers && b->powers;
+    const Tiles t = choose(m, n, g.kbs, powers ? 240 : 256);
     const tn_block8 *p = t.swapped ? b : a, *q = t.swapped ? a : b;
     if (g.kbs > 0) {
         st = encode(&g.tmP, p, tn::kB8Tile);
@@ -180,6 +183,8 @@ tn_status tn_block8_product(const tn_block8 *a, const tn_block8 *b, void *out, i
     g.scaleQ = q->scales;
     g.strideP = p->scale_stride;
     g.strideQ = q->scale_stride;
+    g.blockP = p->scale_block;
+    g.blockQ = q->scale_block;
     g.shiftP = p->block_rows == TN_BLOCK8 ? 7 : 0;
     g.shiftQ = q->block_rows == TN_BLOCK8 ? 7 : 0;
     g.p = p->rows;
@@ -193,15 +198,23 @@ tn_status tn_block8_product(const tn_block8 *a, const tn_block8 *b, void *out, i
     g.qtiles = ceil_div(g.q, t.bn);
     if (g.ptiles > 0x7fffffff / 8 / g.qtiles) return fail(TN_EOVERFLOW, "too many tiles");
     const bool each = g.shiftQ == 0 || t.bn < 128;
-    const cudaError_t e = tn::launch_product(g, t.bn, each, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = tn::block8_status(&g.status);
+    if (e != cudaSuccess) return cuda_fail(e, "looking up the status word");
+    const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+    e = powers ? tn::launch_scaled(g, t.bn, on) : tn::launch_product(g, t.bn, each, on);
     return e == cudaSuccess ? TN_OK : cuda_fail(e, "launching the product");
 }
 
 tn_status tn_block8_check(void) {
-    tn::DevStatus d = {0, 0};
-    const cudaError_t e = tn::block8_status(&d);
+    tn::DevStatus d = {0, 0}, *at = nullptr;
+    cudaError_t e = tn::block8_status(&at);
+    if (e == cudaSuccess) e = cudaMemcpy(&d, at, sizeof(d), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
-    return d.code == tn::ERR_NONE ? TN_OK : fail(TN_ETIMEOUT, "a product gave up waiting: its outputs are not valid");
+    if (d.code == tn::ERR_NONE) return TN_OK;
+    e = cudaMemset(at, 0, sizeof(d));
+    if (e != cudaSuccess) return cuda_fail(e, "clearing the status word");
+    return d.code == tn::ERR_TIMEOUT ? fail(TN_ETIMEOUT, "a product gave up waiting: its outputs are not valid")
+                                     : fail(TN_EDEVICE, "a scale is no power of two: it counted as NaN");
 }
 
 const char *tn_block8_last_error(void) { return g_error; }

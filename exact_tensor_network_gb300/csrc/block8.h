@@ -19,7 +19,7 @@ constexpr int kB8Tile = 128;            // rows and columns of a quantised tile;
 struct Block8Out {
     uint8_t *codes;
     float *scales;
-    int64_t row_stride, scale_stride;
+    int64_t row_stride, scale_stride, scale_block;
 };
 
 struct QuantArgs {
@@ -27,7 +27,7 @@ struct QuantArgs {
     int64_t rows, cols, row_stride, col_stride;
     Block8Out r, c;
     int64_t row_tiles, col_tiles;
-    int32_t vec;        // four entries of a row may be read (and their codes written) at once
+    int32_t vec;        // neighbouring entries of a row may be read at once
 };
 
 // A product by tiles of 128 rows of operand P by BN rows of operand Q:
@@ -37,6 +37,7 @@ struct ProductArgs {
     CUtensorMap tmP, tmQ;
     const float *scaleP, *scaleQ;
     int64_t strideP, strideQ;       // of the scales' rows
+    int64_t blockP, blockQ;         // and blocks
     int32_t shiftP, shiftQ;         // log2 of the rows a scale stands for
     int64_t p, q;
     int64_t sp, sq;
@@ -45,12 +46,15 @@ struct ProductArgs {
     int32_t kbs;                    // blocks of k
     int32_t split;                  // CTAs of a cluster that share a tile's blocks
     int64_t ptiles, qtiles;
+    DevStatus *status;
 };
 
 cudaError_t launch_quantize(const QuantArgs &a, int32_t type, bool square, cudaStream_t stream);
 // bn: 256, 128, 64, 32 or 16; each: whether every row of Q has a scale of its own
 cudaError_t launch_product(const ProductArgs &a, int bn, bool each, cudaStream_t stream);
-// Read and clear the current device's status word.
-cudaError_t block8_status(DevStatus *s);
+// The same of scales that are powers of two; bn: 240, 128, 64, 32 or 16
+cudaError_t launch_scaled(const ProductArgs &a, int bn, cudaStream_t stream);
+// The current device's status word.
+cudaError_t block8_status(DevStatus **p);
 
 }  // namespace tn

@@ -1,5 +1,5 @@
-// Products of 8-bit matrices with a scale for each block of 128 (tcgen05, TMA,
-// TMEM).
+// Products of 8-bit matrices with any fp32 scale for each block of 128 (tcgen05, TMA,
+// TMEM).  Where scales are powers of two k_block8_scaled.cu has the faster way.
 //
 // out[p, q] = sum over blocks b of k of sP[p, b] sQ[q, b] (sum of the codes'
 // products in b).  The tensor core knows no scales that differ from block to
@@ -10,101 +10,92 @@
 // entries where Q's scale is the same for 128 rows (weights), a
 // multiplication more where every row has its own.
 //
-// A CTA computes a tile of 128 rows of P by BN rows of Q.  One thread loads blocks
+// A CTA computes tiles of 128 rows of P by BN rows of Q.  One thread loads blocks
 // of both operands by TMA into a ring of shared-memory stages (rows of 128
-// bytes, 128-byte swizzle), one issues the products, four or eight warps add
-// up: warp w owns TMEM lanes 32 (w % 4) .. and, of eight, half of the columns.
-//   BN 256: large products.  One persistent CTA an SM, 4 stages of 48 KB, two
-//   accumulators that fill TMEM.
-//   BN 16 .. 128: one tile a CTA, two CTAs an SM.  Where a has few rows its b is P:
-//   the weights' 128 rows are the tensor core's and a's rows its columns, so
-//   that nothing is padded to 128 rows and the weights stream at the memory's
-//   rate.  Where tiles are fewer than SMs, a cluster of 2, 4 or 8 CTAs shares a tile's k;
-//   their sums meet in shared memory, added in the order of k.
+// bytes, 128-byte swizzle), one issues the products, four or eight warps add up: warp w
+// owns TMEM lanes 32 (w % 4) .. and, of eight, half of the columns.  The loader and the
+// issuer run ahead of the adding warps from tile to tile.  A block costs one commit: it
+// tells the adding warps that its sums stand, and they tell the loader that its stage
+// is free (a commit costs the tensor core 130 cycles, a block's products 512; a
+// second one made 170 us of nothing but products 205).
+//   BN 256 and 128: large products.  One CTA an SM, a ring of 192 KB, accumulators
+//   that fill TMEM, and registers moved to the adding warps.
+//   BN 16 .. 64: two CTAs an SM.
+// Where a has few rows its b is P: the weights' 128 rows are the tensor core's and
+// a's rows its columns, so that nothing is padded to 128 rows and the weights
+// stream at the memory's rate.  Where tiles are fewer than SMs, a cluster of 2, 4 or 8
+// CTAs shares a tile's k; their sums meet in shared memory, added in the order of k.
 //
 // Every wait on a barrier is bounded: after its limit the CTA's flag goes up, its
 // roles leave, copies and products in flight are waited for (with a limit
 // too), TMEM is released and the status word says ERR_TIMEOUT.
-#include <cuda_fp16.h>
-
-#include "block8.h"
-#include "common.cuh"
-#include "tensor_core.cuh"
+#include "block8_product.cuh"
 
 namespace tn {
 
 namespace {
 
-__device__ DevStatus g_status;
-
-template <int BN>
+template <int BN, bool EACH>
 struct Shape {
-    static constexpr bool kBig = BN == 256;
+    static constexpr bool kBig = BN >= 128;
     static constexpr int kWarps = kBig ? 8 : 4;             // that add up
-    static constexpr int kThreads = (kWarps + 2) * 32;
-    static constexpr int kCols = kBig ? BN / 2 : BN;        // of one such warp
+    // Of large tiles the first warpgroup loads and issues, and gives registers to the
+    // two that add up (128 fp32 sums a thread); of small ones the last.
+    static constexpr int kFirst = kBig ? 4 : 0;             // of the adding warps
+    static constexpr int kLoader = kBig ? 0 : kWarps, kIssuer = kLoader + 1;
+    static constexpr int kThreads = kBig ? 384 : (kWarps + 2) * 32;
+    static constexpr int kRegsLow = 56, kRegsHigh = 224;    // of 168 at launch
+    static constexpr int kCols = kBig ? BN / 2 : BN;        // of an adding warp
+    static constexpr int kStep = kCols < 32 ? 16 : 32;      // columns read from TMEM at once
     static constexpr int kBytesP = kB8Tile * 128, kBytesQ = BN * 128;
     static constexpr int kStage = kBytesP + kBytesQ;
-    static constexpr int kStages = kBig ? 4 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
-    static constexpr int kBufs = BN >= 128 ? 2 : BN == 64 ? 4 : 8;
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 4 : 5;
+    static constexpr int kBufs = BN == 256 ? 2 : BN >= 64 ? 4 : 8;
     static constexpr int kTmem = BN * kBufs;
     static constexpr int kRing = kStage * kStages;
-    // each adding warp's: scales of Q of two blocks; in large tiles also a 32 x 32 block on
-    // its way to the output (others use the ring, which is free by then)
-    static constexpr int kStaging = 32 * 33 * 4;
-    static constexpr int kOwn = kBig ? kStaging : 2 * kCols * 4;
+    // each adding warp's: the scales of its columns of two blocks, and at the end of a tile a
+    // 32 x 16 block of outputs on its way
+    static constexpr int kOwn = 32 * 17;
     static constexpr int kBars = 2 * kStages + 2 * kBufs + 1;
-    static constexpr int kSmem = 1024 + kRing + kWarps * kOwn + kBars * 8 + 16;
+    static constexpr int kSmem = 1024 + kRing + kWarps * kOwn * 4 + kBars * 8 + 16;
     static constexpr int kCtas = kBig ? 1 : 2;              // on an SM
     static constexpr uint32_t kWhat = (1u << 4) | (static_cast<uint32_t>(BN) >> 3 << 17) | (128u >> 4 << 24);
-    static constexpr int kPitch = kB8Tile + 1;              // of a column of shared sums
     static_assert(kSmem <= (kBig ? 232448 : 115712) && kTmem * kCtas <= 512, "an SM's memory");
-    static_assert(kBig || (BN * kPitch * 4 <= kRing && kWarps * kStaging <= kRing), "the ring holds the sums");
+    static_assert(2 * kCols <= kOwn, "scales of two blocks");
+    static_assert(BN == 256 || BN * kPartPitch * 4 <= kRing, "the ring holds the sums");
+    static_assert(!kBig || 4 * kRegsLow + 8 * kRegsHigh <= 12 * 168, "registers of the launch");
 };
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(d)
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
-          "l"(reinterpret_cast<uint64_t &>(c)));
-    return reinterpret_cast<float2 &>(d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(d)
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return reinterpret_cast<float2 &>(d);
-}
-
-__device__ __forceinline__ void store(void *out, int32_t type, int64_t at, float v) {
-    if (type == TN_TYPE_F32) static_cast<float *>(out)[at] = v;
-    else if (type == TN_TYPE_BF16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
-    else static_cast<__half *>(out)[at] = __float2half_rn(v);
-}
-
-// Tile t: groups of eight row tiles, columns inside, so that the tiles that run
-// at once share operands in L2.
-__device__ __forceinline__ void tile_of(int64_t t, const ProductArgs &a, int64_t &pt, int64_t &qt) {
-    const int64_t group = 8 * a.qtiles, g = t / group, first = g * 8;
-    const int64_t n = a.ptiles - first < 8 ? a.ptiles - first : 8;
-    const int64_t r = t - g * group;
-    qt = r / n;
-    pt = first + (r - qt * n);
+// acc += (sums of a block) * scales, of N columns
+template <bool EACH, int N>
+__device__ __forceinline__ void add_scaled(float2 *acc, const uint32_t (&v)[N], float s, const float *qs) {
+    const float2 s2 = make_float2(s, s);
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 2) {
+        float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        float2 y = make_float2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3]));
+        if constexpr (EACH) {
+            const float4 q = *reinterpret_cast<const float4 *>(qs + 2 * i);
+            x = mul2(x, make_float2(q.x, q.y));
+            y = mul2(y, make_float2(q.z, q.w));
+        }
+        acc[i] = fma2(x, s2, acc[i]);
+        acc[i + 1] = fma2(y, s2, acc[i + 1]);
+    }
 }
 
 template <int BN, bool EACH>
-__global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
+__global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kCtas)
     product_kernel(const __grid_constant__ ProductArgs a) {
-    using S = Shape<BN>;
+    using S = Shape<BN, EACH>;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                             ~static_cast<uintptr_t>(1023));
-    unsigned char *own = smem + S::kRing;
+    float *own = reinterpret_cast<float *>(smem + S::kRing);
     uint64_t *bars = reinterpret_cast<uint64_t *>(own + S::kWarps * S::kOwn);
     const uint32_t full = tc::smem_address(bars), empty = full + 8 * S::kStages;
-    const uint32_t tfull = empty + 8 * S::kStages, tempty = tfull + 8 * S::kBufs, end = tempty + 8 * S::kBufs;
+    const uint32_t tfull = empty + 8 * S::kStages, tempty = tfull + 8 * S::kBufs;
+    const uint32_t end = tempty + 8 * S::kBufs;
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + S::kBars);
     volatile int *gave_up = reinterpret_cast<volatile int *>(slot + 1);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -112,7 +103,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             tc::bar_init(full + 8 * s, 1);
-            tc::bar_init(empty + 8 * s, 1);
+            tc::bar_init(empty + 8 * s, S::kWarps);
         }
         for (int b = 0; b < S::kBufs; ++b) {
             tc::bar_init(tfull + 8 * b, 1);
@@ -122,7 +113,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
         *gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == S::kWarps + 1) tc::tmem_alloc<S::kTmem>(tc::smem_address(slot));
+    if (warp == S::kIssuer) tc::tmem_alloc<S::kTmem>(tc::smem_address(slot));
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -141,8 +132,10 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
     const int kb0 = static_cast<int>(static_cast<int64_t>(a.kbs) * rank / split);
     const int kb1 = static_cast<int>(static_cast<int64_t>(a.kbs) * (rank + 1) / split);
 
-    if (warp == S::kWarps) {
-        if (lane == 0) {
+    const bool adds = S::kBig ? warp >= S::kFirst : warp < S::kWarps;
+    if (!adds) {
+        if constexpr (S::kBig) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsLow));
+        if (warp == S::kLoader && lane == 0) {
             uint32_t stage = 0, phase = 0, issued = 0, parity = 0;
             bool ok = true;
             for (int64_t t = first; t < tiles && ok; t += step) {
@@ -169,8 +162,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
                 for (int s = 0; s < S::kStages; ++s)
                     if (issued & (1u << s)) tc::bar_wait_end(full + 8 * s, (parity >> s) & 1);
         }
-    } else if (warp == S::kWarps + 1) {
-        if (lane == 0) {
+        if (warp == S::kIssuer && lane == 0) {
             uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
             bool ok = true;
             for (int64_t t = first; t < tiles && ok; t += step) {
@@ -186,7 +178,6 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
                     tc::mma8<false>(d, da, db, S::kWhat);
 #pragma unroll
                     for (int i = 1; i < 4; ++i) tc::mma8<true>(d, da + 2 * i, db + 2 * i, S::kWhat);
-                    tc::mma_commit(empty + 8 * stage);
                     tc::mma_commit(tfull + 8 * buf);
                     if (++stage == S::kStages) {
                         stage = 0;
@@ -204,77 +195,97 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
             }
         }
     } else {
-        const int quad = warp % 4, col0 = (warp / 4) * S::kCols;
+        if constexpr (S::kBig) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsHigh));
+        const int quad = warp % 4, col0 = (warp - S::kFirst) / 4 * S::kCols;
         const uint32_t tbase = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
-        float *mine = reinterpret_cast<float *>(own + warp * S::kOwn);
-        uint32_t buf = 0, bphase = 0;
+        float *mine = own + (warp - S::kFirst) * S::kOwn;
+        uint32_t buf = 0, bphase = 0, stage = 0;
         bool ok = true;
         for (int64_t t = first; t < tiles && ok; t += step) {
             int64_t pt, qt;
             tile_of(t, a, pt, qt);
-            const int64_t p = pt * kB8Tile + quad * 32 + lane, q0 = qt * BN + col0;
-            const float *sp = a.scaleP + ((p < a.p ? p : a.p - 1) >> a.shiftP) * a.strideP;
-            // scales of Q: of the warp's columns lane, lane + 32, .., or of all
-            constexpr int kScales = EACH ? (S::kCols + 31) / 32 : 1;
-            const float *sq[kScales];
+            const int64_t p0 = pt * kB8Tile + quad * 32, q0 = qt * BN + col0;
+            // scales, read two blocks ahead: of the lane's row of P, and of Q's columns lane,
+            // lane + 32, .. or of all of the warp's
+            constexpr int kQ = EACH ? (S::kCols + 31) / 32 : 1;
+            const float *sp = a.scaleP + ((p0 + lane < a.p ? p0 + lane : a.p - 1) >> a.shiftP) * a.strideP;
+            const float *sq[kQ];
 #pragma unroll
-            for (int i = 0; i < kScales; ++i) {
-                int64_t q = q0 + (EACH ? (lane + 32 * i) % S::kCols : 0);
-                q = q < a.q ? q : a.q - 1;
-                sq[i] = a.scaleQ + (q >> a.shiftQ) * a.strideQ;
+            for (int i = 0; i < kQ; ++i) {
+                const int64_t q = q0 + (EACH ? (lane + 32 * i) % S::kCols : 0);
+                sq[i] = a.scaleQ + ((q < a.q ? q : a.q - 1) >> a.shiftQ) * a.strideQ;
             }
+            float np[2] = {}, nq[2][kQ] = {};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+                if (kb0 + n < kb1) {
+                    np[n] = __ldcg(sp + (kb0 + n) * a.blockP);
+#pragma unroll
+                    for (int i = 0; i < kQ; ++i) nq[n][i] = __ldcg(sq[i] + (kb0 + n) * a.blockQ);
+                }
             float2 acc[S::kCols / 2];
 #pragma unroll
             for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            float next_p = 0.f, next_q[kScales] = {};
-            if (kb0 < kb1) {
-                next_p = __ldcg(sp + kb0);
-#pragma unroll
-                for (int i = 0; i < kScales; ++i) next_q[i] = __ldcg(sq[i] + kb0);
-            }
             for (int kb = kb0; kb < kb1; ++kb) {
-                float s = next_p;
-                float *qs = mine + (kb & 1) * S::kCols;
+                float s = np[0];
+                const float *qs = mine + (kb & 1) * S::kCols;
                 if constexpr (EACH) {
 #pragma unroll
-                    for (int i = 0; i < kScales; ++i)
-                        if (lane + 32 * i < S::kCols) qs[lane + 32 * i] = next_q[i];
+                    for (int i = 0; i < kQ; ++i)
+                        if (lane + 32 * i < S::kCols) mine[(kb & 1) * S::kCols + lane + 32 * i] = nq[0][i];
                     __syncwarp();
                 } else {
                     // 0 times a product beyond fp32's range is 0 all the same
-                    const float both = s * next_q[0];
-                    s = isinf(both) && !isinf(s) && !isinf(next_q[0]) ? copysignf(3.402823466e38f, both) : both;
+                    const float q = nq[0][0], both = s * q;
+                    s = isinf(both) && !isinf(s) && !isinf(q) ? copysignf(3.402823466e38f, both) : both;
                 }
-                if (kb + 1 < kb1) {
-                    next_p = __ldcg(sp + kb + 1);
+                np[0] = np[1];
 #pragma unroll
-                    for (int i = 0; i < kScales; ++i) next_q[i] = __ldcg(sq[i] + kb + 1);
+                for (int i = 0; i < kQ; ++i) nq[0][i] = nq[1][i];
+                if (kb + 2 < kb1) {
+                    np[1] = __ldcg(sp + (kb + 2) * a.blockP);
+#pragma unroll
+                    for (int i = 0; i < kQ; ++i) nq[1][i] = __ldcg(sq[i] + (kb + 2) * a.blockQ);
                 }
                 if (!tc::bar_wait(tfull + 8 * buf, bphase, gave_up)) {
                     ok = false;
                     break;
                 }
+                if (lane == 0) tc::bar_arrive(empty + 8 * stage);
+                if (++stage == S::kStages) stage = 0;
                 tc::fence_after();
                 const uint32_t from = tbase + buf * BN;
-                const float2 s2 = make_float2(s, s);
-                uint32_t r[2][16];
-                tc::tmem_load(from, r[0]);
+                const auto loaded = [&] {       // all of the accumulator is in registers
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive(tempty + 8 * buf);
+                };
+                if constexpr (!S::kBig) {
+                    uint32_t r[S::kStep];
 #pragma unroll
-                for (int c = 0; c < S::kCols / 16; ++c) {
-                    uint32_t(&v)[16] = r[c & 1];
-                    tc::tmem_wait(v);
-                    if (c + 1 < S::kCols / 16) {
-                        tc::tmem_load(from + 16 * (c + 1), r[(c + 1) & 1]);
-                    } else {
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) tc::bar_arrive(tempty + 8 * buf);
+                    for (int c = 0; c < S::kCols; c += S::kStep) {
+                        tc::tmem_load(from + c, r);
+                        tc::tmem_wait(r);
+                        if (c + S::kStep == S::kCols) loaded();
+                        add_scaled<EACH>(acc + c / 2, r, s, qs + c);
                     }
+                } else {
+                    // two loads in flight; the next pair starts as its registers come free
+                    uint32_t r0[32], r1[32];
+                    tc::tmem_load(from, r0);
+                    tc::tmem_load(from + 32, r1);
+                    tc::tmem_wait(r0, r1);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        if constexpr (EACH) x = mul2(x, *reinterpret_cast<const float2 *>(qs + 16 * c + 2 * i));
-                        acc[8 * c + i] = fma2(x, s2, acc[8 * c + i]);
+                    for (int c = 0; c < S::kCols; c += 64) {
+                        const bool more = c + 64 < S::kCols;
+                        if (!more) loaded();
+                        add_scaled<EACH>(acc + c / 2, r0, s, qs + c);
+                        if (more) tc::tmem_load(from + c + 64, r0);
+                        add_scaled<EACH>(acc + c / 2 + 16, r1, s, qs + c + 32);
+                        if (more) {
+                            tc::tmem_load(from + c + 96, r1);
+                            tc::tmem_wait(r0, r1);
+                        }
                     }
                 }
                 if (++buf == S::kBufs) {
@@ -283,101 +294,29 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
                 }
             }
             if (!ok) break;
-            if (!S::kBig && split > 1) {
-                // column q of the tile at q * kPitch; the ring is free, as the last
-                // products have been read
-                float *part = reinterpret_cast<float *>(smem);
-#pragma unroll
-                for (int i = 0; i < S::kCols / 2; ++i) {
-                    part[(2 * i) * S::kPitch + quad * 32 + lane] = acc[i].x;
-                    part[(2 * i + 1) * S::kPitch + quad * 32 + lane] = acc[i].y;
-                }
-            } else if (a.sp == 1) {
-#pragma unroll
-                for (int i = 0; i < S::kCols; ++i)
-                    if (p < a.p && q0 + i < a.q)
-                        store(a.out, a.type, p + (q0 + i) * a.sq, i & 1 ? acc[i / 2].y : acc[i / 2].x);
-            } else {
-                // 32 x 32 blocks turned in shared memory: a row's 32 columns are stored at once
-                float *block = S::kBig ? mine : reinterpret_cast<float *>(smem) + warp * 32 * 33;
-                const int64_t p0 = pt * kB8Tile + quad * 32;
-                const int rows = static_cast<int>(a.p - p0 < 32 ? a.p - p0 : 32);
-#pragma unroll
-                for (int c = 0; c < (S::kCols + 31) / 32; ++c) {
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < (S::kCols < 32 ? S::kCols : 32); ++i)
-                        block[lane * 33 + i] = i & 1 ? acc[16 * c + i / 2].y : acc[16 * c + i / 2].x;
-                    __syncwarp();
-                    const int64_t q = q0 + 32 * c + lane;
-                    if (q < a.q && lane < S::kCols)
-                        for (int r = 0; r < rows; ++r) store(a.out, a.type, (p0 + r) * a.sp + q, block[r * 33 + lane]);
-                }
-                __syncwarp();
-            }
+            // (shared: the ring is free, as the last products have been read)
+            if (BN < 256 && split > 1)
+                keep_part<S::kCols>(reinterpret_cast<float *>(smem), acc, quad * 32 + lane, col0);
+            else
+                store_sums<S::kCols, BN == 256>(a, acc, mine, p0, q0, (qt + 1) * BN);
         }
     }
     __syncwarp();
-    if (!S::kBig && split > 1) {
-        // CTA `rank` finishes its share of the tile: columns where p is the output's
-        // inner axis, rows where q is
-        tc::cluster_sync();
-        int64_t pt, qt;
-        tile_of(first, a, pt, qt);
-        const uint32_t part = tc::smem_address(smem);
-        const bool inner_p = a.sp == 1;
-        const int lo = (inner_p ? BN : kB8Tile) * rank / split, hi = (inner_p ? BN : kB8Tile) * (rank + 1) / split;
-        const int inner = inner_p ? kB8Tile : BN;
-        for (int i = threadIdx.x; i < (hi - lo) * inner; i += S::kThreads) {
-            const int o = lo + i / inner, n = i % inner;
-            const int pp = inner_p ? n : o, qq = inner_p ? o : n;
-            const int64_t p = pt * kB8Tile + pp, q = qt * BN + qq;
-            if (p >= a.p || q >= a.q) continue;
-            float sum = 0.f;
-            for (int r = 0; r < split; ++r) sum += tc::cluster_load(tc::in_cta(part + (qq * S::kPitch + pp) * 4, r));
-            store(a.out, a.type, p * a.sp + q * a.sq, sum);
-        }
-        tc::cluster_sync();     // others may still read this CTA's sums
-    }
+    if (BN < 256 && split > 1) join_parts<BN, S::kThreads>(a, reinterpret_cast<const float *>(smem), first, rank);
     tc::fence_before();
     __syncthreads();
-    if (warp == S::kWarps + 1) {
+    if (warp == S::kIssuer) {
         tc::fence_after();
         tc::tmem_free<S::kTmem>(tmem);
     }
-    if (threadIdx.x == 0 && *gave_up) atomicCAS(&g_status.code, ERR_NONE, ERR_TIMEOUT);
+    if (threadIdx.x == 0 && *gave_up) atomicCAS(&a.status->code, ERR_NONE, ERR_TIMEOUT);
 }
 
 template <int BN, bool EACH>
 cudaError_t launch(const ProductArgs &a, cudaStream_t stream) {
-    using S = Shape<BN>;
-    auto kernel = product_kernel<BN, EACH>;
-    static uint64_t ready = 0;      // devices whose limit is raised
-    int device;
-    cudaError_t e = cudaGetDevice(&device);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (device & 63);
-    if (!(__atomic_load_n(&ready, __ATOMIC_RELAXED) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e != cudaSuccess) return e;
-        __atomic_fetch_or(&ready, bit, __ATOMIC_RELAXED);
-    }
-    const int64_t tiles = a.ptiles * a.qtiles;
-    const int64_t ctas = S::kBig ? (tiles < kB8Sms ? tiles : kB8Sms) : tiles * a.split;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(a.split);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    using S = Shape<BN, EACH>;
+    static uint64_t ready = 0;
+    return launch_tiles(product_kernel<BN, EACH>, a, S::kThreads, S::kSmem, S::kCtas * kB8Sms, &ready, stream);
 }
 
 }  // namespace
@@ -390,13 +329,6 @@ cudaError_t launch_product(const ProductArgs &a, int bn, bool each, cudaStream_t
         case 32: return launch<32, true>(a, stream);
         default: return launch<16, true>(a, stream);
     }
-}
-
-cudaError_t block8_status(DevStatus *s) {
-    cudaError_t e = cudaMemcpyFromSymbol(s, g_status, sizeof(*s));
-    if (e != cudaSuccess || s->code == ERR_NONE) return e;
-    const DevStatus none = {ERR_NONE, 0};
-    return cudaMemcpyToSymbol(g_status, &none, sizeof(none));
 }
 
 }  // namespace tn

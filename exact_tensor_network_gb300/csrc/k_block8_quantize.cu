@@ -9,6 +9,8 @@
 // infinities and NaN are the largest of all).  Bound by memory.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "block8.h"
 #include "common.cuh"
 
@@ -19,37 +21,51 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int WARP_ROWS = kB8Tile / (THREADS / 32);     // 16
 
-__device__ __forceinline__ float entry(const float *p) { return __ldcg(p); }
-__device__ __forceinline__ float entry(const __nv_bfloat16 *p) {
-    return __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short *>(p))) << 16);
-}
-__device__ __forceinline__ float entry(const __half *p) {
-    const unsigned short u = __ldcg(reinterpret_cast<const unsigned short *>(p));
-    return __half2float(*reinterpret_cast<const __half *>(&u));
-}
-__device__ __forceinline__ void entries(const float *p, float (&v)[4]) {
-    const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
-    v[0] = f.x;
-    v[1] = f.y;
-    v[2] = f.z;
-    v[3] = f.w;
-}
-__device__ __forceinline__ void entries(const __nv_bfloat16 *p, float (&v)[4]) {
-    const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(p));
-    v[0] = __uint_as_float(u.x << 16);
-    v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16);
-    v[3] = __uint_as_float(u.y & 0xffff0000u);
-}
-__device__ __forceinline__ void entries(const __half *p, float (&v)[4]) {
-    const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(p));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = b.x;
-    v[3] = b.y;
-}
+// Neighbouring entries as they lie in memory, and their values.
+template <typename T, int N>
+struct Raw {
+    static constexpr int kWords = N * sizeof(T) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T *p) {      // all at once
+        if constexpr (kWords == 4) {
+            const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(p));
+            w[0] = u.x;
+            w[1] = u.y;
+            w[2] = u.z;
+            w[3] = u.w;
+        } else {
+            const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(p));
+            w[0] = u.x;
+            w[1] = u.y;
+        }
+    }
+    // `n` of them one by one, the others 0 (neighbours share lines: through the L1 cache)
+    __device__ __forceinline__ void load(const T *p, int64_t stride, int64_t n) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i >= n) continue;
+            if constexpr (sizeof(T) == 4) w[i] = *reinterpret_cast<const uint32_t *>(p + i * stride);
+            else w[i / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(p + i * stride)) << (16 * (i % 2));
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(w[i]);
+        } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i / 2]));
+            return i % 2 ? f.y : f.x;
+        }
+    }
+    __device__ __forceinline__ uint32_t size(int i) const { return __float_as_uint((*this)[i]) & 0x7fffffffu; }
+};
 
 // The scale of a block whose largest magnitude has the bits `top`, and what
 // entries are multiplied by (0 with a NaN or an infinity among them).
@@ -77,8 +93,62 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 // (0 * infinity and 0 * NaN are not 0)
 __device__ __forceinline__ float scaled(float x, float inverse) { return inverse == 0.f ? 0.f : x * inverse; }
 
+// Codes in the layout of x alone, with a scale for 128 entries of a row: 16 bytes of
+// a row a lane, four loads in flight, no shared memory.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const QuantArgs a) {
+    constexpr int N = 16 / sizeof(T), LANES = TN_BLOCK8 / N, LOADS = 4;
+    const int lane = threadIdx.x % 32;
+    pdl_trigger();
+    pdl_wait();
+    // items of 32 vectors: `per` of them a row
+    const int64_t per = (a.cols + 32 * N - 1) / (32 * N), items = a.rows * per;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32; it < items; it += step * LOADS) {
+        Raw<T, N> v[LOADS];
+        int64_t row[LOADS], col[LOADS];
+#pragma unroll
+        for (int l = 0; l < LOADS; ++l) {
+            const int64_t i = it + l * step;
+            row[l] = i < items ? i / per : a.rows;
+            col[l] = ((i < items ? i - row[l] * per : 0) * 32 + lane) * N;
+            v[l].clear();
+            if (row[l] >= a.rows || col[l] >= a.cols) continue;
+            const T *p = static_cast<const T *>(a.x) + row[l] * a.row_stride + col[l] * a.col_stride;
+            if (a.vec && col[l] + N <= a.cols) v[l].load(p);
+            else v[l].load(p, a.col_stride, a.cols - col[l]);
+        }
+#pragma unroll
+        for (int l = 0; l < LOADS; ++l) {
+            if (row[l] >= a.rows) break;            // the warp's
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) top = max(top, v[l].size(i));
+#pragma unroll
+            for (int o = LANES / 2; o; o /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (col[l] >= a.cols) continue;
+            const Scale s = scale_of(top);
+            if (lane % LANES == 0) a.r.scales[row[l] * a.r.scale_stride + col[l] / TN_BLOCK8 * a.r.scale_block] = s.s;
+            uint32_t w[N / 4];
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i)
+                w[i] = codes4(scaled(v[l][4 * i], s.inverse), scaled(v[l][4 * i + 1], s.inverse),
+                              scaled(v[l][4 * i + 2], s.inverse), scaled(v[l][4 * i + 3], s.inverse));
+            uint8_t *to = a.r.codes + row[l] * a.r.row_stride + col[l];
+            if (col[l] + N <= a.cols) {
+                if constexpr (N == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<uint32_t *>(to) = w[0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < N - 1; ++i)
+                    if (col[l] + i < a.cols) to[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
+            }
+        }
+    }
+}
+
 template <typename T, bool SQUARE>
-__global__ void __launch_bounds__(THREADS, 2) quantize_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : 3) quantize_kernel(const QuantArgs a) {
     __shared__ __align__(16) uint4 turned[kB8Tile * (kB8Tile / 16)];
     __shared__ uint32_t tops[THREADS / 32][kB8Tile];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -88,19 +158,17 @@ __global__ void __launch_bounds__(THREADS, 2) quantize_kernel(const QuantArgs a)
     const int64_t r0 = rt * kB8Tile + warp * WARP_ROWS, c0 = ct * kB8Tile + lane * 4;
     const T *x = static_cast<const T *>(a.x) + r0 * a.row_stride + c0 * a.col_stride;
 
-    float v[WARP_ROWS][4];
+    Raw<T, 4> v[WARP_ROWS];
     if (a.vec && c0 + 4 <= a.cols) {
 #pragma unroll
         for (int i = 0; i < WARP_ROWS; ++i) {
-            if (r0 + i < a.rows) entries(x + i * a.row_stride, v[i]);
-            else v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+            if (r0 + i < a.rows) v[i].load(x + i * a.row_stride);
+            else v[i].clear();
         }
     } else {
 #pragma unroll
         for (int i = 0; i < WARP_ROWS; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[i][j] = r0 + i < a.rows && c0 + j < a.cols ? entry(x + i * a.row_stride + j * a.col_stride) : 0.f;
+            v[i].load(x + i * a.row_stride, a.col_stride, r0 + i < a.rows ? a.cols - c0 : 0);
     }
 
     uint32_t ctop[4] = {0, 0, 0, 0};
@@ -108,7 +176,7 @@ __global__ void __launch_bounds__(THREADS, 2) quantize_kernel(const QuantArgs a)
 #pragma unroll
         for (int i = 0; i < WARP_ROWS; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) ctop[j] = max(ctop[j], __float_as_uint(v[i][j]) & 0x7fffffffu);
+            for (int j = 0; j < 4; ++j) ctop[j] = max(ctop[j], v[i].size(j));
     }
     Scale tile = {1.f, 1.f};
     if (SQUARE) {
@@ -117,8 +185,8 @@ __global__ void __launch_bounds__(THREADS, 2) quantize_kernel(const QuantArgs a)
         __syncthreads();
         tile = scale_of(__reduce_max_sync(0xffffffffu, lane < THREADS / 32 ? tops[0][lane] : 0u));
         if (threadIdx.x == 0) {
-            if (a.r.codes) a.r.scales[rt * a.r.scale_stride + ct] = tile.s;
-            if (a.c.codes) a.c.scales[ct * a.c.scale_stride + rt] = tile.s;
+            if (a.r.codes) a.r.scales[rt * a.r.scale_stride + ct * a.r.scale_block] = tile.s;
+            if (a.c.codes) a.c.scales[ct * a.c.scale_stride + rt * a.c.scale_block] = tile.s;
         }
     }
     if (a.r.codes) {
@@ -129,11 +197,11 @@ __global__ void __launch_bounds__(THREADS, 2) quantize_kernel(const QuantArgs a)
             if (!SQUARE) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+                for (int j = 0; j < 4; ++j) top = max(top, v[i].size(j));
                 s = scale_of(__reduce_max_sync(0xffffffffu, top));
             }
             if (r0 + i >= a.rows) continue;
-            if (!SQUARE && lane == 0) a.r.scales[(r0 + i) * a.r.scale_stride + ct] = s.s;
+            if (!SQUARE && lane == 0) a.r.scales[(r0 + i) * a.r.scale_stride + ct * a.r.scale_block] = s.s;
             const uint32_t w = codes4(scaled(v[i][0], s.inverse), scaled(v[i][1], s.inverse),
                                       scaled(v[i][2], s.inverse), scaled(v[i][3], s.inverse));
             uint8_t *to = a.r.codes + (r0 + i) * a.r.row_stride + c0;
@@ -162,7 +230,7 @@ __global__ void __launch_bounds__(THREADS, 2) quantize_kernel(const QuantArgs a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 s[j] = scale_of(ctop[j]);
-                if (warp == 0 && c0 + j < a.cols) a.c.scales[(c0 + j) * a.c.scale_stride + rt] = s[j].s;
+                if (warp == 0 && c0 + j < a.cols) a.c.scales[(c0 + j) * a.c.scale_stride + rt * a.c.scale_block] = s[j].s;
             }
         }
         // Piece `warp` (16 codes) of column 4 lane + j lies at place warp ^ (lane % 8)
@@ -200,6 +268,13 @@ __global__ void __launch_bounds__(THREADS, 2) quantize_kernel(const QuantArgs a)
 
 template <typename T>
 cudaError_t launch(const QuantArgs &a, bool square, cudaStream_t stream) {
+    if (!a.c.codes && !square) {
+        constexpr int64_t kItem = 32 * 16 / sizeof(T);
+        const int64_t warps = (a.rows * ((a.cols + kItem - 1) / kItem) + 3) / 4, most = 8 * kB8Sms;
+        const int64_t ctas = (warps + THREADS / 32 - 1) / (THREADS / 32);
+        return launch_pdl(quantize_rows_kernel<T>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(THREADS),
+                          0, stream, a);
+    }
     const dim3 grid(static_cast<unsigned>(a.row_tiles * a.col_tiles));
     return square ? launch_pdl(quantize_kernel<T, true>, grid, dim3(THREADS), 0, stream, a)
                   : launch_pdl(quantize_kernel<T, false>, grid, dim3(THREADS), 0, stream, a);

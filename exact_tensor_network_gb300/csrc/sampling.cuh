@@ -3,7 +3,7 @@
 // An outcome is a whole number, and near a border between two outcomes any
 // rounding decides it: a sum of 10^5 weights in fp32 is wrong by some 2^-22, and one
 // draw in ten of a broad row lies that near to a border.  So weights are computed as
-// pairs of fp32 numbers (44 bits and more) and summed as 64-bit integers, in
+// pairs of fp32 numbers (43 bits) and summed as 64-bit integers, in
 // units of 2^-shift of the largest, the shift chosen by an estimate of the row's
 // sum so that it uses 61 bits.  Integer sums need no order: histograms by
 // shared-memory atomics, partial sums of CTAs and of warps are all exact.
@@ -14,41 +14,44 @@
 
 namespace tn {
 
-// 2^(j/64) as the sum of two fp32 numbers
-static __device__ const float2 kRoots[64] = {
-    {0x1.000000p+0f, 0x0.0p+0f}, {0x1.02c9a4p+0f, -0x1.887fa0p-28f},
-    {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.087452p+0f, -0x1.e2990ep-26f},
-    {0x1.0b5586p+0f, 0x1.9f3122p-25f}, {0x1.0e3ec4p+0f, -0x1.a585ccp-25f},
-    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.1429aap+0f, 0x1.d525bcp-25f},
-    {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.1a35bep+0f, 0x1.6df96ep-25f},
-    {0x1.1d4874p+0f, -0x1.d2e8cap-25f}, {0x1.2063b8p+0f, 0x1.0c519ap-25f},
-    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.26b456p+0f, 0x1.789f38p-26f},
-    {0x1.29e9e0p+0f, -0x1.5c0424p-25f}, {0x1.2d285ap+0f, 0x1.b900c2p-26f},
-    {0x1.306fe0p+0f, 0x1.4636e2p-25f}, {0x1.33c08cp+0f, -0x1.b37d20p-25f},
-    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.3a7db4p+0f, -0x1.634c02p-25f},
-    {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.4160a2p+0f, 0x1.f72e2ap-28f},
-    {0x1.44e086p+0f, 0x1.8624b4p-30f}, {0x1.486a2cp+0f, -0x1.47d866p-25f},
-    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.4f9b28p+0f, -0x1.2c5a6cp-25f},
-    {0x1.5342b6p+0f, -0x1.2c5610p-25f}, {0x1.56f474p+0f, -0x1.295b04p-25f},
-    {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f}, {0x1.5e76f2p+0f, -0x1.4a5bd6p-25f},
-    {0x1.6247ecp+0f, -0x1.f8b550p-25f}, {0x1.662388p+0f, 0x1.2a9112p-27f},
-    {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.6dfb24p+0f, -0x1.cd72e8p-27f},
-    {0x1.71f75ep+0f, 0x1.1d8beep-25f}, {0x1.75feb6p+0f, -0x1.37b306p-25f},
-    {0x1.7a1148p+0f, -0x1.829fd0p-25f}, {0x1.7e2f34p+0f, -0x1.261634p-25f},
-    {0x1.82589ap+0f, -0x1.accc7cp-26f}, {0x1.868d9ap+0f, -0x1.2edb44p-26f},
-    {0x1.8ace54p+0f, 0x1.15506ep-27f}, {0x1.8f1aeap+0f, -0x1.baa232p-26f},
-    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.97d82ap+0f, -0x1.0d8d84p-31f},
-    {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.a0c668p+0f, -0x1.2886a6p-26f},
-    {0x1.a5503cp+0f, -0x1.b83b54p-25f}, {0x1.a9e6b6p+0f, -0x1.50c048p-25f},
-    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b33a2cp+0f, -0x1.ec3a82p-26f},
-    {0x1.b7f770p+0f, -0x1.a09438p-25f}, {0x1.bcc1eap+0f, -0x1.f687c6p-25f},
-    {0x1.c199bep+0f, -0x1.3d56b2p-27f}, {0x1.c67f12p+0f, 0x1.cafa2ap-25f},
-    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.d072d4p+0f, 0x1.40f130p-25f},
-    {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.da9e60p+0f, 0x1.ed9942p-27f},
-    {0x1.dfc974p+0f, -0x1.908c94p-25f}, {0x1.e502eep+0f, 0x1.e2cffep-26f},
-    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.efa1bep+0f, 0x1.cc2b44p-25f},
-    {0x1.f50766p+0f, -0x1.246eb0p-26f}, {0x1.fa7c18p+0f, 0x1.9e90d8p-28f},
+// 2^(i/32) and 2^(j/1024), each as the sum of two fp32 numbers
+static __device__ const float2 kCoarse[32] = {
+    {0x1.000000p+0f, 0x0.0p+0f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f},
+    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f},
+    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.29e9e0p+0f, -0x1.5c0424p-25f}, {0x1.306fe0p+0f, 0x1.4636e2p-25f},
+    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.5342b6p+0f, -0x1.2c5610p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f},
+    {0x1.6247ecp+0f, -0x1.f8b550p-25f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f},
+    {0x1.7a1148p+0f, -0x1.829fd0p-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f},
+    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b7f770p+0f, -0x1.a09438p-25f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f},
+    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f},
+    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.f50766p+0f, -0x1.246eb0p-26f},
 };
+static __device__ const float2 kFine[32] = {
+    {0x1.000000p+0f, 0x0.0p+0f}, {0x1.002c60p+0f, 0x1.78ba34p-26f}, {0x1.0058c8p+0f, 0x1.b68702p-26f},
+    {0x1.008538p+0f, 0x1.7d77c2p-27f}, {0x1.00b1b0p+0f, -0x1.6950d0p-26f}, {0x1.00de2ep+0f, 0x1.a1dc1ep-25f},
+    {0x1.010ab6p+0f, -0x1.34d0bcp-26f}, {0x1.013744p+0f, 0x1.326d6ep-26f}, {0x1.0163dap+0f, 0x1.3f6666p-25f},
+    {0x1.019078p+0f, 0x1.5ad434p-25f}, {0x1.01bd1ep+0f, 0x1.dc5c2ep-26f}, {0x1.01e9ccp+0f, -0x1.eec114p-32f},
+    {0x1.021682p+0f, -0x1.789fb0p-25f}, {0x1.02433ep+0f, 0x1.252dd6p-26f}, {0x1.027004p+0f, -0x1.df89dep-25f},
+    {0x1.029cd0p+0f, -0x1.98a37ep-26f}, {0x1.02c9a4p+0f, -0x1.887fa0p-28f}, {0x1.02f680p+0f, -0x1.626868p-30f},
+    {0x1.032364p+0f, -0x1.5ea7ecp-27f}, {0x1.035050p+0f, -0x1.1421f2p-25f}, {0x1.037d42p+0f, 0x1.c2377ap-25f},
+    {0x1.03aa3ep+0f, 0x1.70aafep-28f}, {0x1.03d742p+0f, -0x1.cdd4aep-25f}, {0x1.04044cp+0f, -0x1.76954ap-28f},
+    {0x1.04315ep+0f, 0x1.0dcff0p-25f}, {0x1.045e78p+0f, 0x1.eac818p-25f}, {0x1.048b9cp+0f, -0x1.9534c4p-25f},
+    {0x1.04b8c6p+0f, -0x1.6f70bcp-25f}, {0x1.04e5f8p+0f, -0x1.a1356ap-25f}, {0x1.051330p+0f, 0x1.d83408p-25f},
+    {0x1.054072p+0f, 0x1.ff05d8p-26f}, {0x1.056dbcp+0f, -0x1.448794p-28f},
+};
+
+// 2^(k/1024), k = 0 .. 1023, in shared memory: the products of the two.
+constexpr int kRoots = 1024;
+template <int NT>
+__device__ __forceinline__ void make_roots(float2 *roots) {
+    for (int k = threadIdx.x; k < kRoots; k += NT) {
+        const float2 c = kCoarse[k >> 5], f = kFine[k & 31];
+        const float h = c.x * f.x, l = fmaf(c.x, f.x, -h) + fmaf(c.x, f.y, c.y * f.x), x = h + l;
+        roots[k] = make_float2(x, (h - x) + l);
+    }
+}
 
 // What a row's weights are computed from.
 struct RowPlan {
@@ -82,30 +85,40 @@ __device__ __forceinline__ float2 exponent(const RowPlan &p, float v) {
 }
 
 // The weight of a present entry, 1 at least (so that a draw of u = 0 finds the
-// first entry left).  2^t of a pair t: 2^(k/64) from a table, the rest (at most
-// 2^-7) by the exponential series, whose first two terms are kept as pairs.
+// first entry left).  2^t of a pair t: 2^(k/1024) from a table, the rest (at most
+// 2^-11) by the exponential series, whose first term is kept as a pair.
 __device__ __forceinline__ uint64_t weight_real(const RowPlan &p, const float2 *roots, float v) {
     constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
     const float2 t = exponent(p, v);
     if (!(t.x > -64.f)) return 1;
-    const float kf = __fadd_rn(fmaf(t.x, 64.f, kMagic), -kMagic);
-    const float r = fmaf(kf, -0x1p-6f, t.x);                // exact
+    const float km = fmaf(t.x, 1024.f, kMagic), kf = __fadd_rn(km, -kMagic);
+    const int k = static_cast<int>(__float_as_uint(km) - __float_as_uint(kMagic));
+    const float r = fmaf(kf, -0x1p-10f, t.x);               // exact
     const float g = r * kLn2Hi;
     const float gl = fmaf(r, kLn2Hi, -g) + fmaf(r, kLn2Lo, t.y * kLn2Hi);
-    const float s = g * g, sl = fmaf(g, g, -s), half = 0.5f * s;
-    const float tail = g * s * fmaf(g, 1.f / 24, 1.f / 6);
-    const float q = g + half;                               // 2^r - 1 = q + ql
-    const float ql = ((g - q) + half) + fmaf(g, gl, 0.5f * sl) + (gl + tail);
-    const int k = static_cast<int>(kf);
-    const float2 root = roots[k & 63];
-    const float a = root.x * q, al = fmaf(root.x, q, -a);
-    const float w = root.x + a;
-    const float wl = ((root.x - w) + a) + (al + root.y + fmaf(root.x, ql, root.y * q));
-    const int x = (k >> 6) + p.shift;
-    if (x < -1) return 1;
-    const float unit = __uint_as_float(static_cast<uint32_t>(x + 127) << 23);
-    const long long n = __float2ll_rn(w * unit) + __float2ll_rn(wl * unit);
-    return n > 0 ? static_cast<uint64_t>(n) : 1;
+    const float lo = fmaf(g * g, fmaf(g, 1.f / 6, 0.5f), gl);   // 2^r - 1 = g + lo
+    const float2 root = roots[k & (kRoots - 1)];
+    const float a = root.x * g, al = fmaf(root.x, g, -a);
+    const float w0 = root.x + a;
+    const float wm = ((root.x - w0) + a) + (al + fmaf(root.x, lo, fmaf(root.y, g, root.y)));
+    const float w = w0 + wm, wl = (w0 - w) + wm;            // (t's low part makes wm up to 2^-19)
+    // w + wl in units of 2^-44 (conversions of fp32 to 64-bit integers would run on the fp64 pipe):
+    // w, below 2, to 2^-22 from the mantissa of w + 2, what is left of it with wl from
+    // that of a sum with kMagic (it is less than 2^-22)
+    const float up = __fadd_rn(w, 2.f), rest = (w - __fadd_rn(up, -2.f)) + wl;
+    const int low = static_cast<int>(__float_as_uint(fmaf(rest, 0x1p44f, kMagic)) - __float_as_uint(kMagic));
+    const int64_t n = static_cast<int64_t>(static_cast<int>(__float_as_uint(up) - 0x40000000u)) * (1 << 22) + low;
+    const int x = (k >> 10) + p.shift - 44;
+    const uint64_t whole = x >= 0 ? static_cast<uint64_t>(n) << x : x > -64 ? static_cast<uint64_t>(n) >> -x : 0;
+    return whole > 0 ? whole : 1;
+}
+
+// A number of 0 <= v < 4 in units of 2^-shift, the same way.
+__device__ __forceinline__ uint64_t in_units(float v, int shift) {
+    const uint32_t b = __float_as_uint(v);
+    const uint64_t n = (b & 0x7fffffu) | 0x800000u;
+    const int x = static_cast<int>(b >> 23) - 150 + shift;
+    return x >= 0 ? n << x : x > -64 ? n >> -x : 0;
 }
 
 template <int TYPE>
@@ -113,14 +126,14 @@ __device__ __forceinline__ uint64_t weight(const RowPlan &p, const float2 *roots
     if constexpr (Entry<TYPE>::kReal) {
         return weight_real(p, roots, v);
     } else {
-        long long n;
+        uint64_t n;
         if (p.beta == 1.0) {
-            n = __float2ll_rn(v * p.down * __uint_as_float(static_cast<uint32_t>(p.shift + 127) << 23));
+            n = in_units(v * p.down, p.shift);
         } else {
             const double x = p.beta * log(static_cast<double>(v) / p.m);
-            n = x < -60.0 ? 1 : __double2ll_rn(ldexp(exp(x), p.shift));
+            n = x < -60.0 ? 1 : static_cast<uint64_t>(__double2ll_rn(ldexp(exp(x), p.shift)));
         }
-        return n > 0 ? static_cast<uint64_t>(n) : 1;
+        return n > 0 ? n : 1;
     }
 }
 // The same in fp32, relative to the largest: for an estimate of the sum.
@@ -144,6 +157,52 @@ __device__ __forceinline__ void vector_values(const Row<TYPE> &r, int64_t j, flo
 #pragma unroll
         for (int i = 0; i < En::E; ++i) v[i] = o.v[i];
     }
+}
+
+// f(order values, vector) of vectors first, first + stride, .. below hi, N at a time with
+// their loads in flight together; `edge` is the first vector behind those that the
+// caller's threads read at a time (N stride further than the first of them), so that
+// they all take the same way.
+template <int TYPE, int N, class F>
+__device__ __forceinline__ void vectors_at(const Row<TYPE> &r, int64_t in_lo, int64_t in_hi, int64_t from, int64_t edge,
+                                           int64_t first, int stride, int64_t hi, F f) {
+    using En = Entry<TYPE>;
+    if (from >= in_lo && edge <= in_hi && edge <= hi) {
+        uint4 q[N];
+        const uint4 *p = r.vectors() + first;
+#pragma unroll
+        for (int n = 0; n < N; ++n) q[n] = __ldcg(p + n * stride);
+        if (r.m) {
+            typename Row<TYPE>::Keep keep[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) keep[n] = r.keep((first + n * stride) * En::E - r.head);
+#pragma unroll
+            for (int n = 0; n < N; ++n) En::blank(q[n], keep[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float v[En::E];
+            En::values(q[n], v);
+            f(v, first + n * stride);
+        }
+    } else {
+#pragma unroll 1
+        for (int n = 0; n < N; ++n) {
+            const int64_t j = first + n * stride;
+            if (j >= hi) break;
+            float v[En::E];
+            vector_values<TYPE>(r, j, v);
+            f(v, j);
+        }
+    }
+}
+// The same of all vectors lo .. hi - 1, by NT threads.
+template <int TYPE, int NT, int N, class F>
+__device__ __forceinline__ void each_vector(const Row<TYPE> &r, int64_t lo, int64_t hi, F f) {
+    int64_t in_lo, in_hi;
+    r.inside_range(in_lo, in_hi);
+    for (int64_t from = lo; from < hi; from += N * NT)
+        vectors_at<TYPE, N>(r, in_lo, in_hi, from, from + N * NT, from + threadIdx.x, NT, hi, f);
 }
 
 __device__ __forceinline__ uint64_t shfl_up(uint64_t x, int o) {
@@ -272,12 +331,10 @@ struct RowCta {
     // f(order value, index) of every entry of the row
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        for (int64_t j = threadIdx.x; j < vecs; j += NT) {
-            float v[E];
-            vector_values<TYPE>(r, j, v);
+        each_vector<TYPE, NT, 1>(r, 0, vecs, [&](const float (&v)[E], int64_t j) {
 #pragma unroll
             for (int i = 0; i < E; ++i) f(v[i], j * E - r.head + i);
-        }
+        });
     }
     __device__ __forceinline__ uint64_t sum(uint64_t x) const {
         x = warp_sum(x);
@@ -363,11 +420,11 @@ struct RowCta {
 };
 
 // The first of n sums at which their total exceeds `target`, which becomes what is
-// left of it there; one warp.  sums[i stride].
-__device__ __forceinline__ int64_t locate(const uint64_t *sums, int64_t n, int stride, uint64_t &target) {
+// left of it there; one warp.
+__device__ __forceinline__ int64_t locate(const uint64_t *sums, int64_t n, uint64_t &target) {
     const int lane = threadIdx.x % 32;
     for (int64_t base = 0; base < n; base += 32) {
-        const uint64_t own = base + lane < n ? __ldcg(sums + (base + lane) * stride) : 0, upto = warp_scan(own, lane);
+        const uint64_t own = base + lane < n ? __ldcg(sums + base + lane) : 0, upto = warp_scan(own, lane);
         const uint32_t over = __ballot_sync(0xffffffffu, upto > target);
         if (over) {
             const int l = __ffs(over) - 1;
@@ -379,8 +436,23 @@ __device__ __forceinline__ int64_t locate(const uint64_t *sums, int64_t n, int s
     return 0;
 }
 
-// One warp: a draw of row r.  Where the row has segments, `partials` are their
-// sums (the first of each pair) and `seg_pieces` their length.
+// The same of sums that are added up already: a search by 32.
+__device__ __forceinline__ int64_t locate_upto(const ulonglong2 *upto, int64_t n, uint64_t &target) {
+    const int lane = threadIdx.x % 32;
+    int64_t lo = 0, len = n;
+    while (len > 1) {
+        const int64_t step = (len + 31) / 32, at = lo + (lane + 1) * step - 1;
+        const bool over = lane * step < len && (at >= lo + len - 1 || __ldcg(&upto[at]).x > target);
+        const int l = __ffs(__ballot_sync(0xffffffffu, over)) - 1;
+        len = len - l * step < step ? len - l * step : step;
+        lo += l * step;
+    }
+    if (lo > 0) target -= __ldcg(&upto[lo - 1]).x;
+    return lo;
+}
+
+// One warp: a draw of row r.  Where the row has segments, `partials` holds their
+// sums up to each (the first of a pair).
 template <int TYPE>
 __device__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs, const RowPlan &p, const float2 *roots,
                           const uint64_t *masses, int64_t pieces, const ulonglong2 *partials, uint64_t total,
@@ -399,10 +471,10 @@ __device__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs,
     uint64_t target = p.greedy ? 0 : share(u, total, false);
     int64_t first = 0;
     if (partials) {
-        first = locate(reinterpret_cast<const uint64_t *>(partials), a.segs, 2, target) * a.seg_pieces;
+        first = locate_upto(partials, a.segs, target) * a.seg_pieces;
         pieces = pieces - first < a.seg_pieces ? pieces - first : a.seg_pieces;
     }
-    const int64_t piece = first + locate(masses + first, pieces, 1, target);
+    const int64_t piece = first + locate(masses + first, pieces, target);
     for (int i = 0; i < kPieceVecs / 32; ++i) {
         const int64_t j = piece * kPieceVecs + i * 32 + lane;
         float v[E];
@@ -453,13 +525,13 @@ __device__ __forceinline__ void no_draws(const SampleArgs &a, int64_t row, int s
 template <int TYPE, int NT>
 __global__ void __launch_bounds__(NT) sample_rows_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E;
-    __shared__ float2 roots[64];
+    __shared__ float2 roots[kRoots];
     __shared__ RowPlan plan;
     __shared__ Select sel;
     __shared__ uint64_t sums[NT / 32];
     __shared__ uint32_t red[4 * (NT / 32)];
     pdl_trigger();
-    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    make_roots<kDrawThreads>(roots);
     pdl_wait();
     Group<NT> g(red);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -636,9 +708,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
     // the sum relative to the largest entry so far
     const float ch = fminf(f.beta * kLog2E, 3.402823466e38f);
     float m = absent<TYPE>(), s = 0.f;
-    for (int64_t j = c.lo + threadIdx.x; j < c.hi; j += kDrawThreads) {
-        float v[E];
-        vector_values<TYPE>(c.r, j, v);
+    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, [&](const float (&v)[E], int64_t) {
         float top = v[0];
 #pragma unroll
         for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
@@ -660,7 +730,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(f.beta * (lg2(v[i]) - l)) : 0.f;
         }
-    }
+    });
     // threads', then segments'
     const auto moved = [&](float from, float to) {
         if (from == absent<TYPE>()) return 0.f;
@@ -747,10 +817,10 @@ template <int TYPE, bool FINE>
 __global__ void __launch_bounds__(kDrawThreads) bins_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E, kOwn = kBins / kDrawThreads;
     __shared__ uint32_t lo[kBins], hi[kBins], count[kBins];
-    __shared__ float2 roots[64];
+    __shared__ float2 roots[kRoots];
     __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
     pdl_trigger();
-    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    make_roots<kDrawThreads>(roots);
     for (int i = threadIdx.x; i < kBins; i += kDrawThreads) lo[i] = hi[i] = count[i] = 0;
     pdl_wait();
     const Segment<TYPE> c(a);
@@ -763,9 +833,7 @@ __global__ void __launch_bounds__(kDrawThreads) bins_kernel(const __grid_constan
     const int first = FINE ? st.slot_lo : 0;
     const uint64_t above0 = FINE ? st.above : 0;
     __syncthreads();
-    for (int64_t j = c.lo + threadIdx.x; j < c.hi; j += kDrawThreads) {
-        float v[E];
-        vector_values<TYPE>(c.r, j, v);
+    each_vector<TYPE, kDrawThreads, 2>(c.r, c.lo, c.hi, [&](const float (&v)[E], int64_t) {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             if (v[i] == absent<TYPE>()) continue;
@@ -775,7 +843,7 @@ __global__ void __launch_bounds__(kDrawThreads) bins_kernel(const __grid_constan
             atomicAdd(&count[b], 1u);
             if (by_mass) add_mass(&lo[b], &hi[b], weight<TYPE>(p, roots, v[i]));
         }
-    }
+    });
     __syncthreads();
     RowBins *all = a.segs > 1 ? a.bins + c.row : nullptr;
     if (all) {
@@ -850,19 +918,18 @@ template <int TYPE>
 __global__ void __launch_bounds__(kDrawThreads) cut_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E;
     __shared__ uint64_t list[kSorted];
-    __shared__ float2 roots[64];
+    __shared__ float2 roots[kRoots];
     __shared__ Select sel;
     __shared__ uint64_t sums[kDrawWarps + 1];
     __shared__ RowPlan plan;
     __shared__ uint32_t listed;
     pdl_trigger();
-    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    make_roots<kDrawThreads>(roots);
     pdl_wait();
     const Segment<TYPE> c(a);
     RowState &st = a.state[c.row];
     if (!st.narrow) return;
     const bool by_mass = st.top_p < 1.f, sorted = st.expected <= kSorted;
-    const int lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         plan = st.plan;
         listed = 0;
@@ -873,31 +940,23 @@ __global__ void __launch_bounds__(kDrawThreads) cut_kernel(const __grid_constant
     if (sorted) {
         const float bin_scale = st.bin_scale;
         const int lo = st.slot_lo, hi = st.slot_hi;
-        for (int64_t j0 = c.lo; j0 < c.hi; j0 += kDrawThreads) {
-            const int64_t j = j0 + threadIdx.x;
-            float v[E];
+        const RowPlan own = plan;       // (not read again behind every atomic)
+        each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, [&](const float (&v)[E], int64_t j) {
             uint32_t in = 0;
-            if (j < c.hi) {
-                vector_values<TYPE>(c.r, j, v);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int s = slot_of<TYPE>(plan, bin_scale, v[i]);
-                    if (v[i] != absent<TYPE>() && s >= lo && s <= hi) in |= 1u << i;
-                }
+            for (int i = 0; i < E; ++i) {
+                const int s = slot_of<TYPE>(own, bin_scale, v[i]);
+                if (v[i] != absent<TYPE>() && s >= lo && s <= hi) in |= 1u << i;
             }
-            if (!__any_sync(0xffffffffu, in != 0)) continue;
-            const uint32_t n = __popc(in);
-            const uint32_t upto = static_cast<uint32_t>(warp_scan(n, lane));
-            uint32_t base = 0;
-            if (lane == 31) base = atomicAdd(counter, upto);
-            base = __shfl_sync(0xffffffffu, base, 31) + upto - n;
+            if (!in) return;
+            uint32_t at = atomicAdd(counter, static_cast<uint32_t>(__popc(in)));
 #pragma unroll
             for (int i = 0; i < E; ++i)
                 if (in >> i & 1) {
-                    if (base < kSorted) to[base] = rank_of<TYPE>(v[i], j * E - c.r.head + i);
-                    ++base;
+                    if (at < kSorted) to[at] = rank_of<TYPE>(v[i], j * E - c.r.head + i);
+                    ++at;
                 }
-        }
+        });
     }
     if (!last_of_row(a, st, 2)) return;
     uint64_t bound = kPresent;
@@ -956,10 +1015,10 @@ __global__ void __launch_bounds__(kDrawThreads) cut_kernel(const __grid_constant
 template <int TYPE>
 __global__ void __launch_bounds__(kDrawThreads) sums_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E;
-    __shared__ float2 roots[64];
+    __shared__ float2 roots[kRoots];
     __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
     pdl_trigger();
-    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    make_roots<kDrawThreads>(roots);
     pdl_wait();
     const Segment<TYPE> c(a);
     RowState &st = a.state[c.row];
@@ -969,25 +1028,30 @@ __global__ void __launch_bounds__(kDrawThreads) sums_kernel(const __grid_constan
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     uint64_t *masses = a.masses + c.row * a.pieces;
     uint64_t total = 0, kept = 0;
+    uint32_t number = 0;
+    const uint32_t bound_key = static_cast<uint32_t>(p.bound >> 32), bound_index = 0xffffffffu - static_cast<uint32_t>(p.bound);
+    int64_t in_lo, in_hi;
+    c.r.inside_range(in_lo, in_hi);
     for (int64_t q = c.lo / kPieceVecs + warp; q * kPieceVecs < c.hi; q += kDrawWarps) {
         uint64_t own = 0;
+        vectors_at<TYPE, kPieceVecs / 32>(
+            c.r, in_lo, in_hi, q * kPieceVecs, (q + 1) * kPieceVecs, q * kPieceVecs + lane, 32, c.hi,
+            [&](const float (&v)[E], int64_t j) {
 #pragma unroll
-        for (int i = 0; i < kPieceVecs / 32; ++i) {
-            const int64_t j = q * kPieceVecs + i * 32 + lane;
-            if (j >= c.hi) break;
-            float v[E];
-            vector_values<TYPE>(c.r, j, v);
-#pragma unroll
-            for (int k = 0; k < E; ++k)
-                if (rank_of<TYPE>(v[k], j * E - c.r.head + k) >= p.bound) {
-                    own += weight<TYPE>(p, roots, v[k]);
-                    ++kept;
+                for (int k = 0; k < E; ++k) {
+                    const uint32_t key = order_key<TYPE>(v[k]);
+                    if (key > bound_key ||
+                        (key == bound_key && static_cast<uint32_t>(j * E - c.r.head + k) <= bound_index)) {
+                        own += weight<TYPE>(p, roots, v[k]);
+                        ++number;
+                    }
                 }
-        }
+            });
         total += own;
         own = warp_sum(own);
         if (lane == 0) __stcg(&masses[q], own);
     }
+    kept = number;
     cta_scan(total, sums);
     cta_scan(kept, nums);
     total = sums[kDrawWarps];
@@ -998,14 +1062,22 @@ __global__ void __launch_bounds__(kDrawThreads) sums_kernel(const __grid_constan
         if (threadIdx.x == 0) __stcg(&mine[c.seg], make_ulonglong2(total, kept));
         if (!last_of_row(a, st, 3)) return;
         parts = mine;
+        // sums up to each segment, of consecutive ones by a thread each
+        const int per = static_cast<int>((a.segs + kDrawThreads - 1) / kDrawThreads), s0 = threadIdx.x * per;
         total = kept = 0;
-        for (int64_t i = threadIdx.x; i < a.segs; i += kDrawThreads) {
+        for (int i = s0; i < s0 + per && i < a.segs; ++i) {
             const ulonglong2 x = __ldcg(&mine[i]);
             total += x.x;
             kept += x.y;
         }
-        cta_scan(total, sums);
         cta_scan(kept, nums);
+        uint64_t upto = cta_scan(total, sums);
+        for (int i = s0; i < s0 + per && i < a.segs; ++i) {
+            const ulonglong2 x = __ldcg(&mine[i]);
+            upto += x.x;
+            __stcg(&mine[i], make_ulonglong2(upto, x.y));
+        }
+        __syncthreads();
         total = sums[kDrawWarps];
         kept = nums[kDrawWarps];
     } else {
@@ -1023,9 +1095,9 @@ __global__ void __launch_bounds__(kDrawThreads) sums_kernel(const __grid_constan
 
 template <int TYPE>
 __global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_constant__ SampleArgs a) {
-    __shared__ float2 roots[64];
+    __shared__ float2 roots[kRoots];
     pdl_trigger();
-    if (threadIdx.x < 64) roots[threadIdx.x] = kRoots[threadIdx.x];
+    make_roots<kDrawThreads>(roots);
     pdl_wait();
     __syncthreads();
     const int64_t ctas = (a.draws + kDrawWarps - 1) / kDrawWarps;

@@ -42,7 +42,7 @@ constexpr uint64_t kWaitNs = 4000000000ull;
 
 // Wait for the phase of that parity; false if the CTA gave up (its flag is up)
 // or the wait ran past its limit, which raises the flag.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     const uint64_t t0 = nanoseconds();
     while (true) {
         for (int i = 0; i < 32; ++i)
@@ -58,7 +58,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     return bar_try(bar, parity) || bar_wait_long(bar, parity, gave_up);
 }
 // The same whatever the flag says: for copies in flight.
-__device__ __noinline__ void bar_wait_end(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ void bar_wait_end(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = nanoseconds();
     while (!bar_try(bar, parity))
         if (nanoseconds() - t0 > kWaitNs) return;
@@ -87,6 +87,28 @@ __device__ __forceinline__ void mma8(uint32_t d, uint32_t a, uint32_t b, uint32_
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
         "r"(a), "r"(b), "r"(what), "n"(ADD ? 1 : 0), "r"(kDesc128Hi));
 }
+// The same with a power of two for each 32 of k of each row of A and of B, which lie as
+// bytes (biased exponents) in TMEM: row r in lane r % 32 of column r / 32, one of the four
+// bytes there by what `what` says.
+template <bool ADD>
+__device__ __forceinline__ void mma8_scaled(uint32_t d, uint32_t a, uint32_t b, uint32_t what, uint32_t scale_a,
+                                            uint32_t scale_b) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%6], [%7], p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(what), "n"(ADD ? 1 : 0), "r"(kDesc128Hi), "r"(scale_a), "r"(scale_b));
+}
+// 32 rows of 16 bytes, one behind the other in shared memory, to four columns of TMEM and
+// all four quarters of its lanes; in order with this thread's products.
+__device__ __forceinline__ void copy_scales(uint32_t to, uint32_t address) {
+    // no swizzle, groups of eight rows 128 bytes apart
+    const uint64_t desc = static_cast<uint64_t>((address >> 4) & 0x3fffu) | static_cast<uint64_t>(128 >> 4) << 32 |
+                          static_cast<uint64_t>(1) << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
+}
+// What generic stores to shared memory wrote is seen by copies and products behind it.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Arrives on the barrier when this thread's products so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -103,7 +125,7 @@ template <int COLS>
 __device__ __forceinline__ void tmem_free(uint32_t tmem) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS) : "memory");
 }
-// 16 columns of the warp's 32 lanes; the registers hold them after tmem_wait.
+// 16 or 32 columns of the warp's 32 lanes; the registers hold them after tmem_wait.
 __device__ __forceinline__ void tmem_load(uint32_t from, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -112,12 +134,37 @@ __device__ __forceinline__ void tmem_load(uint32_t from, uint32_t (&r)[16]) {
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(from));
 }
+__device__ __forceinline__ void tmem_load(uint32_t from, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(from));
+}
 // (the registers go through it: nothing may use them before)
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15])::"memory");
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_keep(uint32_t (&r)[32]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    tmem_keep(r);
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32], uint32_t (&q)[32]) {
+    tmem_wait(r);
+    tmem_keep(q);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -18,9 +18,10 @@
  *     infinities; to nearest, ties to even) and stands for code * s.
  *   - The product of a [m, k] and b [n, k] is c[i, j] = sum over k of the values
  *     that the codes stand for.  The sums of the codes' products within a block
- *     of k are the tensor core's, in 32 bits; those over blocks are of (sum * both
- *     blocks' scales), in fp32, rounded once to the output's type.  Scales
- *     may be any fp32 numbers, not powers of two alone.
+ *     of k (of up to four, where scales are powers of two) are the tensor core's,
+ *     in 32 bits; those over blocks are in fp32, rounded once to the output's
+ *     type.  Scales from elsewhere may be any fp32 numbers (powers = 0); those that
+ *     tn_block8_quantize makes are powers of two, which products are faster with.
  *
  * Conventions are those of tn.h: no call throws, every failure is a
  * tn_status, no device memory is allocated, work is enqueued on the caller's
@@ -52,13 +53,15 @@ typedef struct tn_matrix {
 /* A matrix in 8 bits.  Row i of the codes starts at codes + i row_stride, which
  * is 16-byte aligned (row_stride a multiple of 16, at least cols); what lies
  * between a row's end and the next row is neither read nor written.  The scale of
- * block b of row i is scales[(i / block_rows) scale_stride + b]. */
+ * block b of row i is scales[(i / block_rows) scale_stride + b scale_block]; both
+ * strides are > 0.  scale_stride 1 is the fast layout of scales of single rows. */
 typedef struct tn_block8 {
     uint8_t *codes;
     float *scales;
     int64_t rows, cols;
-    int64_t row_stride, scale_stride;
+    int64_t row_stride, scale_stride, scale_block;
     int32_t block_rows;     /* 1 or 128 */
+    int32_t powers;         /* nonzero: scales are powers of two (from 2^-126 on) or NaN */
 } tn_block8;
 
 /*
@@ -80,8 +83,9 @@ TN_API tn_status tn_block8_product(const tn_block8 *a, const tn_block8 *b, void 
                                    int64_t out_stride, tn_stream_t stream);
 
 /* After the device has been synchronised: read and clear the current device's
- * status word of these calls.  TN_OK, or TN_ETIMEOUT (a product gave up
- * waiting; its outputs are not valid). */
+ * status word of these calls.  TN_OK, TN_ETIMEOUT (a product gave up
+ * waiting; its outputs are not valid), or TN_EDEVICE (a scale of a matrix with
+ * `powers` is neither a power of two nor NaN; it counted as NaN). */
 TN_API tn_status tn_block8_check(void);
 
 /* Text of this thread's last failed call. */

@@ -52,11 +52,12 @@ LINEAR = [(1, 128, 128), (1, 300, 4096), (2, 1, 1), (16, 129, 257), (17, 1000, 6
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("powers", [True, False])
 @pytest.mark.parametrize("R,N,K", LINEAR)
-def test_linear(R, N, K, dtype):
+def test_linear(R, N, K, powers, dtype):
     x, w = _x(R, K, torch.bfloat16, 1), _x(N, K, torch.float32, 2) * K ** -0.5
     q = tn.quantize8(w.cuda(), square=True)
-    y = tn.linear8(x.cuda(), q, dtype=dtype)
+    y = tn.linear8(x.cuda(), tn.Blocks8(q.codes, q.scales, powers), dtype=dtype)
     c, far = ref.product_bound(ref.values(*ref.quantize(x, False)), ref.values(*ref.quantize(w, True)), dtype)
     assert y.shape == (R, N) and y.dtype is dtype
     assert ((y.cpu().double() - c).abs() <= far).all()
@@ -72,3 +73,22 @@ def test_linear_grad(R, N, K):
     for got, (c, far) in ((dx, ref.product_bound(v[0], v[1], torch.bfloat16)),
                           (dw, ref.product_bound(v[2], v[3], torch.float32))):
         assert ((got.cpu().double() - c).abs() <= far).all()
+
+
+@pytest.mark.parametrize("R,N,K", [(3, 200, 300), (40, 700, 512), (200, 300, 1024), (2000, 1500, 640)])
+def test_any_scales(R, N, K):
+    """Scales that are no powers of two, of rows and of squares, in either layout."""
+    g = torch.Generator().manual_seed(R)
+    a, b = tn.quantize8(_x(R, K, seed=6).cuda()), tn.quantize8(_x(N, K, seed=7).cuda(), square=True)
+    fa, fb = torch.rand(a.scales.shape, generator=g) + 0.5, torch.rand(b.scales.shape, generator=g) + 0.5
+    a = tn.Blocks8(a.codes, (a.scales.cpu() * fa).cuda(), False)
+    b = tn.Blocks8(b.codes, (b.scales.cpu() * fb).cuda().t().contiguous().t(), False)
+    y = tn.product8(a, b, dtype=torch.float32)
+    c, far = ref.product_bound(ref.values(a.codes.cpu().float(), a.scales.cpu()),
+                               ref.values(b.codes.cpu().float(), b.scales.cpu()), torch.float32)
+    assert ((y.cpu().double() - c).abs() <= far).all()
+    # both operands with a scale a row
+    z = tn.product8(a, a, dtype=torch.float32)
+    v = ref.values(a.codes.cpu().float(), a.scales.cpu())
+    c, far = ref.product_bound(v, v, torch.float32)
+    assert ((z.cpu().double() - c).abs() <= far).all()
