@@ -53,7 +53,7 @@ __device__ __forceinline__ T rounded(float v) {
 
 // An adding warp's sums (32 rows of P, a lane each, by COLS of Q, those below `q_end`) to their
 // place.
-template <typename T, int COLS, bool ROWS>
+template <typename T, int COLS, bool ROWS, int TURN>
 __device__ __forceinline__ void store_tile(const ProductArgs &a, const float2 *acc, float *block, int64_t p0, int64_t q0,
                                            int64_t q_end) {
     const int lane = threadIdx.x % 32;
@@ -68,30 +68,53 @@ __device__ __forceinline__ void store_tile(const ProductArgs &a, const float2 *a
             if (lane < rows && i < cols) to[i * a.sq] = rounded<T>(i & 1 ? acc[i / 2].y : acc[i / 2].x);
         return;
     }
-    // 32 x 16 blocks turned in shared memory: 16 neighbours of two rows are stored at once
-    const int c = lane % 16;
+    // TURN bytes of 32 rows at a time, turned in shared memory so that neighbouring lanes store a
+    // row's (rows there are an odd number of 16 bytes apart: eight lanes meet all banks)
+    constexpr int E = 16 / sizeof(T), FULL = TURN / sizeof(T), STEP = FULL < COLS ? FULL : COLS;
+    constexpr int PITCH = (TURN + 16) / sizeof(T);
+    T *turned = reinterpret_cast<T *>(block);
+    const bool whole = reinterpret_cast<uintptr_t>(out + p0 * a.sp + q0) % 16 == 0 && (a.sp * sizeof(T)) % 16 == 0;
 #pragma unroll
-    for (int b = 0; b < COLS; b += 16) {
+    for (int b = 0; b < COLS; b += STEP) {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) block[lane * 17 + i] = i & 1 ? acc[(b + i) / 2].y : acc[(b + i) / 2].x;
+        for (int i = 0; i < STEP; i += E) {
+            union {
+                uint4 w;
+                T v[E];
+            } u;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int c = b + i + e;
+                u.v[e] = rounded<T>(c & 1 ? acc[c / 2].y : acc[c / 2].x);
+            }
+            *reinterpret_cast<uint4 *>(turned + lane * PITCH + i) = u.w;
+        }
         __syncwarp();
-        if (b + c >= cols) continue;
-        T *to = out + p0 * a.sp + q0 + b + c;
+        const int n = cols - b < STEP ? cols - b : STEP;
+        T *to = out + p0 * a.sp + q0 + b;
+        if (whole && n == STEP) {
+            constexpr int LANES = STEP / E;         // of a row
+            const int c = lane % LANES * E;
+#pragma unroll
+            for (int r = lane / LANES; r < 32; r += 32 / LANES)
+                if (r < rows) *reinterpret_cast<uint4 *>(to + r * a.sp + c) = *reinterpret_cast<const uint4 *>(turned + r * PITCH + c);
+        } else {
+            for (int c = lane; c < n; c += 32)
 #pragma unroll 4
-        for (int r = lane / 16; r < rows; r += 2) to[r * a.sp] = rounded<T>(block[r * 17 + c]);
+                for (int r = 0; r < rows; ++r) to[r * a.sp + c] = turned[r * PITCH + c];
+        }
     }
     __syncwarp();
 }
 
-
 // An adding warp's sums by the output's type.
-template <int COLS, bool ROWS>
+template <int COLS, bool ROWS, int TURN>
 __device__ __forceinline__ void store_sums(const ProductArgs &a, const float2 *acc, float *block, int64_t p0, int64_t q0,
                                            int64_t q_end) {
-    if (a.type == TN_TYPE_F32) store_tile<float, COLS, ROWS>(a, acc, block, p0, q0, q_end);
-    else if (a.type == TN_TYPE_BF16) store_tile<__nv_bfloat16, COLS, ROWS>(a, acc, block, p0, q0, q_end);
-    else store_tile<__half, COLS, ROWS>(a, acc, block, p0, q0, q_end);
+    if (a.type == TN_TYPE_F32) store_tile<float, COLS, ROWS, TURN>(a, acc, block, p0, q0, q_end);
+    else if (a.type == TN_TYPE_BF16) store_tile<__nv_bfloat16, COLS, ROWS, TURN>(a, acc, block, p0, q0, q_end);
+    else store_tile<__half, COLS, ROWS, TURN>(a, acc, block, p0, q0, q_end);
 }
 
 // Clusters that share a tile's k: column q of a CTA's sums lies at q * kPartPitch.

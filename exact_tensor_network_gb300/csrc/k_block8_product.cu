@@ -53,9 +53,10 @@ struct Shape {
     static constexpr int kBufs = BN == 256 ? 2 : BN >= 64 ? 4 : 8;
     static constexpr int kTmem = BN * kBufs;
     static constexpr int kRing = kStage * kStages;
-    // each adding warp's: the scales of its columns of two blocks, and at the end of a tile a
-    // 32 x 16 block of outputs on its way
-    static constexpr int kOwn = 32 * 17;
+    // words of each adding warp: the scales of its columns of two blocks, and at the end of a tile
+    // kTurn bytes of its 32 rows on their way out
+    static constexpr int kTurn = kBig ? 64 : 32;
+    static constexpr int kOwn = 32 * (kTurn + 16) / 4;
     static constexpr int kBars = 2 * kStages + 2 * kBufs + 1;
     static constexpr int kSmem = 1024 + kRing + kWarps * kOwn * 4 + kBars * 8 + 16;
     static constexpr int kCtas = kBig ? 1 : 2;              // on an SM
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kC
             if (BN < 256 && split > 1)
                 keep_part<S::kCols>(reinterpret_cast<float *>(smem), acc, quad * 32 + lane, col0);
             else
-                store_sums<S::kCols, BN == 256>(a, acc, mine, p0, q0, (qt + 1) * BN);
+                store_sums<S::kCols, BN == 256, S::kTurn>(a, acc, mine, p0, q0, (qt + 1) * BN);
         }
     }
     __syncwarp();

@@ -50,7 +50,8 @@ struct Shape {
     static constexpr int kScaleAt = kBufs * BN;
     static constexpr int kTmem = BN == 240 ? 512 : BN == 128 ? 512 : BN == 64 ? 256 : BN == 32 ? 128 : 64;
     static constexpr int kSlot = kScales * 128, kSlots = 2;         // bytes in shared memory
-    static constexpr int kOwn = 32 * 17;
+    static constexpr int kTurn = kBig ? 128 : 32;           // bytes of its 32 rows that an adding warp stores at once
+    static constexpr int kOwn = 32 * (kTurn + 16) / 4;
     static constexpr int kBars = 2 * kStages + 2 * kBufs + 2 * kSlots + 1;
     static constexpr int kSmem = 1024 + kRing + kSlots * kSlot + kWarps * kOwn * 4 + kBars * 8 + 16;
     static constexpr int kCtas = kBig ? 1 : 2;
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
             if (BN < 240 && split > 1) {
                 keep_part<S::kCols>(reinterpret_cast<float *>(smem), acc, quad * 32 + lane, col0);
             } else {
-                store_sums<S::kCols, BN == 240>(a, acc, mine, p0, q0, (qt + 1) * BN);
+                store_sums<S::kCols, BN == 240, S::kTurn>(a, acc, mine, p0, q0, (qt + 1) * BN);
             }
         }
     }
