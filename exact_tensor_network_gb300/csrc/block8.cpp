@@ -81,19 +81,31 @@ struct Tiles {
     int bn, split;
 };
 
+// By rounds of CTAs times what one takes: its blocks of k, and what a tile costs besides
+// (in blocks of 240 columns, some 0.4 us: launch, first loads and outputs 6, sums that meet in a
+// cluster 4 more).  1000 x 1112 x 5003: 72 tiles of 128 in two parts each 14 us, 40 of 240 43;
+// 500 x 500 x 8192: 16 tiles of 128 in eight parts 18 us, in one 40.
 Tiles choose(int64_t m, int64_t n, int64_t kbs, int most) {
-    Tiles t;
+    Tiles t = {};
     t.swapped = m <= 128;
     const int64_t p = t.swapped ? n : m, q = t.swapped ? m : n;
-    t.split = 1;
-    if (q > 128 && ceil_div(p, tn::kB8Tile) * ceil_div(q, most) >= tn::kB8Sms / 2) {
-        t.bn = most;
-        return t;
+    double best = 0;
+    for (const int bn : {most, 128, 64, 32, 16}) {
+        // the narrowest that holds q, or one of the two for many
+        if (q > 128 ? bn < 128 : bn > 128 || bn < q || (bn > 16 && bn / 2 >= q)) continue;
+        const int64_t tiles = ceil_div(p, tn::kB8Tile) * ceil_div(q, bn);
+        const int64_t room = bn >= 128 ? tn::kB8Sms : 2 * tn::kB8Sms;
+        const double block = bn >= 240 ? 1.0 : bn == 128 ? 0.6 : 0.5;
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (bn > 128 || kbs < 4 * split)) break;
+            const double cost = static_cast<double>(ceil_div(tiles * split, room)) *
+                                (static_cast<double>(ceil_div(kbs, split)) * block + (split > 1 ? 10 : 6));
+            if (best > 0 && cost >= best) continue;
+            best = cost;
+            t.bn = bn;
+            t.split = split;
+        }
     }
-    t.bn = q > 64 ? 128 : q > 32 ? 64 : q > 16 ? 32 : 16;
-    // Clusters until there are CTAs for every SM, of four blocks of k each at least.
-    const int64_t tiles = ceil_div(p, tn::kB8Tile) * ceil_div(q, t.bn);
-    while (t.split < 8 && tiles * t.split < tn::kB8Sms && kbs >= 8 * t.split) t.split *= 2;
     return t;
 }
 

@@ -117,18 +117,27 @@ __device__ __forceinline__ void store_sums(const ProductArgs &a, const float2 *a
     else store_tile<__half, COLS, ROWS, TURN>(a, acc, block, p0, q0, q_end);
 }
 
-// Clusters that share a tile's k: column q of a CTA's sums lies at q * kPartPitch.
-constexpr int kPartPitch = kB8Tile + 1;
-template <int COLS>
-__device__ __forceinline__ void keep_part(float *part, const float2 *acc, int row, int col) {
+// Clusters that share a tile's k.  A CTA's sums lie as the output does, its inner axis with four
+// words behind it: neighbouring lanes read 16 bytes each of another CTA's lines.
+constexpr int kPartPad = 4;
+constexpr int part_bytes(int bn) { return (bn > kB8Tile ? bn : kB8Tile) * (kB8Tile + kPartPad) * 4; }
+template <int BN, int COLS>
+__device__ __forceinline__ void keep_part(const ProductArgs &a, float *part, const float2 *acc, int row, int col) {
+    if (a.sp == 1) {
 #pragma unroll
-    for (int i = 0; i < COLS / 2; ++i) {
-        part[(col + 2 * i) * kPartPitch + row] = acc[i].x;
-        part[(col + 2 * i + 1) * kPartPitch + row] = acc[i].y;
+        for (int i = 0; i < COLS / 2; ++i) {
+            part[(col + 2 * i) * (kB8Tile + kPartPad) + row] = acc[i].x;
+            part[(col + 2 * i + 1) * (kB8Tile + kPartPad) + row] = acc[i].y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < COLS / 2; i += 2)
+            *reinterpret_cast<float4 *>(part + row * (BN + kPartPad) + col + 2 * i) =
+                make_float4(acc[i].x, acc[i].y, acc[i + 1].x, acc[i + 1].y);
     }
 }
-// All threads of all CTAs: CTA `rank` finishes its share of the tile, columns where p is the
-// output's inner axis, rows where q is.
+// All threads of all CTAs: CTA `rank` finishes its share of the tile, lines of the output's inner
+// axis.
 template <int BN, int THREADS>
 __device__ __forceinline__ void join_parts(const ProductArgs &a, const float *mine, int64_t tile, uint32_t rank) {
     tc::cluster_sync();
@@ -137,16 +146,31 @@ __device__ __forceinline__ void join_parts(const ProductArgs &a, const float *mi
     tile_of(tile, a, pt, qt);
     const uint32_t part = tc::smem_address(mine);
     const bool inner_p = a.sp == 1;
-    const int lo = (inner_p ? BN : kB8Tile) * rank / split, hi = (inner_p ? BN : kB8Tile) * (rank + 1) / split;
-    const int inner = inner_p ? kB8Tile : BN;
-    for (int i = threadIdx.x; i < (hi - lo) * inner; i += THREADS) {
-        const int o = lo + i / inner, n = i % inner;
-        const int pp = inner_p ? n : o, qq = inner_p ? o : n;
-        const int64_t p = pt * kB8Tile + pp, q = qt * BN + qq;
-        if (p >= a.p || q >= a.q) continue;
-        float sum = 0.f;
-        for (int r = 0; r < split; ++r) sum += tc::cluster_load(tc::in_cta(part + (qq * kPartPitch + pp) * 4, r));
-        store(a.out, a.type, p * a.sp + q * a.sq, sum);
+    const int lines = inner_p ? BN : kB8Tile, quads = (inner_p ? kB8Tile : BN) / 4;
+    const int shift = inner_p ? 5 : BN == 128 ? 5 : BN == 64 ? 4 : BN == 32 ? 3 : 2;    // quads = 2^shift
+    const int lo = lines * rank / split, hi = lines * (rank + 1) / split;
+    for (int i = threadIdx.x; i < (hi - lo) << shift; i += THREADS) {
+        const int o = lo + (i >> shift), n = (i & (quads - 1)) * 4;
+        const uint32_t at = part + (o * (quads * 4 + kPartPad) + n) * 4;
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < split) v[r] = tc::cluster_load4(tc::in_cta(at, r));
+        float4 sum = v[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+            if (r < split) {
+                sum.x += v[r].x;
+                sum.y += v[r].y;
+                sum.z += v[r].z;
+                sum.w += v[r].w;
+            }
+        const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t p = pt * kB8Tile + (inner_p ? n + e : o), q = qt * BN + (inner_p ? o : n + e);
+            if (p < a.p && q < a.q) store(a.out, a.type, p * a.sp + q * a.sq, out[e]);
+        }
     }
     tc::cluster_sync();     // others may still read this CTA's sums
 }

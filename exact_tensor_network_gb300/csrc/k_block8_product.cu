@@ -63,7 +63,7 @@ struct Shape {
     static constexpr uint32_t kWhat = (1u << 4) | (static_cast<uint32_t>(BN) >> 3 << 17) | (128u >> 4 << 24);
     static_assert(kSmem <= (kBig ? 232448 : 115712) && kTmem * kCtas <= 512, "an SM's memory");
     static_assert(2 * kCols <= kOwn, "scales of two blocks");
-    static_assert(BN == 256 || BN * kPartPitch * 4 <= kRing, "the ring holds the sums");
+    static_assert(BN == 256 || part_bytes(BN) <= kRing, "the ring holds the sums");
     static_assert(!kBig || 4 * kRegsLow + 8 * kRegsHigh <= 12 * 168, "registers of the launch");
 };
 
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kC
             if (!ok) break;
             // (shared: the ring is free, as the last products have been read)
             if (BN < 256 && split > 1)
-                keep_part<S::kCols>(reinterpret_cast<float *>(smem), acc, quad * 32 + lane, col0);
+                keep_part<BN, S::kCols>(a, reinterpret_cast<float *>(smem), acc, quad * 32 + lane, col0);
             else
                 store_sums<S::kCols, BN == 256, S::kTurn>(a, acc, mine, p0, q0, (qt + 1) * BN);
         }

@@ -59,7 +59,7 @@ struct Shape {
     static constexpr uint32_t kWhat = (static_cast<uint32_t>(BN) >> 3 << 17) | (1u << 23) | (128u >> 7 << 27);
     static_assert(kScaleAt + 16 * kBufs <= kTmem && kScaleAt % 16 == 0, "columns of TMEM");
     static_assert(kSmem <= (kBig ? 232448 : 115712) && kTmem * kCtas <= 512, "an SM's memory");
-    static_assert(BN == 240 || BN * kPartPitch * 4 <= kRing, "the ring holds the sums");
+    static_assert(BN == 240 || part_bytes(BN) <= kRing, "the ring holds the sums");
     static_assert(!kBig || 4 * kRegsLow + 8 * kRegsHigh <= 12 * 168, "registers of the launch");
 };
 
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
             const int64_t p0 = pt * kB8Tile + quad * 32, q0 = qt * BN + col0;
             // (shared: the ring is free, as the last products have been read)
             if (BN < 240 && split > 1) {
-                keep_part<S::kCols>(reinterpret_cast<float *>(smem), acc, quad * 32 + lane, col0);
+                keep_part<BN, S::kCols>(a, reinterpret_cast<float *>(smem), acc, quad * 32 + lane, col0);
             } else {
                 store_sums<S::kCols, BN == 240, S::kTurn>(a, acc, mine, p0, q0, (qt + 1) * BN);
             }
