@@ -76,7 +76,8 @@ tn_status tn_sampler_create(int32_t type, int64_t cols, int64_t max_rows, float 
         s.state_off = at;
         s.bins_off = align(s.state_off + static_cast<uint64_t>(max_rows) * tn::state_bytes());
         s.clear_bytes = s.partial_off = align(s.bins_off + cut * tn::bins_bytes());
-        s.list_off = align(s.partial_off + tn::kDrawTarget * sizeof(ulonglong2));
+        s.rest_off = align(s.partial_off + tn::kDrawTarget * sizeof(ulonglong2));
+        s.list_off = align(s.rest_off + tn::kDrawTarget * sizeof(uint64_t));
         at = align(s.list_off + cut * tn::kSorted * sizeof(uint64_t));
     } else {
         s.clear_bytes = at;
@@ -163,6 +164,7 @@ tn_status tn_sampler_draw(tn_sampler_t *h, const tn_rows *r, const tn_filters *f
         a.state = reinterpret_cast<tn::RowState *>(s.ws + s.state_off);
         a.bins = reinterpret_cast<tn::RowBins *>(s.ws + s.bins_off);
         a.partials = reinterpret_cast<ulonglong2 *>(s.ws + s.partial_off);
+        a.alls = reinterpret_cast<uint64_t *>(s.ws + s.rest_off);
         a.lists = reinterpret_cast<uint64_t *>(s.ws + s.list_off);
     }
     if (r->rows * (a.segs + ceil_div(draws, tn::kDrawWarps)) > 0x7fffffff)

@@ -121,21 +121,60 @@ __device__ __forceinline__ uint64_t in_units(float v, int shift) {
     return x >= 0 ? n << x : x > -64 ? n >> -x : 0;
 }
 
+// Out of line, as what follows is wherever a kernel's steady loop does not need it: a
+// kernel's first pass through its code costs more than what it computes there.
+static __device__ __noinline__ uint64_t weight_power(float v, float m, double beta, int shift) {
+    const double x = beta * log(static_cast<double>(v) / m);
+    return x < -60.0 ? 1 : static_cast<uint64_t>(__double2ll_rn(ldexp(exp(x), shift)));
+}
+
 template <int TYPE>
 __device__ __forceinline__ uint64_t weight(const RowPlan &p, const float2 *roots, float v) {
     if constexpr (Entry<TYPE>::kReal) {
         return weight_real(p, roots, v);
     } else {
-        uint64_t n;
-        if (p.beta == 1.0) {
-            n = in_units(v * p.down, p.shift);
-        } else {
-            const double x = p.beta * log(static_cast<double>(v) / p.m);
-            n = x < -60.0 ? 1 : static_cast<uint64_t>(__double2ll_rn(ldexp(exp(x), p.shift)));
-        }
+        const uint64_t n = p.beta == 1.0 ? in_units(v * p.down, p.shift) : weight_power(v, p.m, p.beta, p.shift);
         return n > 0 ? n : 1;
     }
 }
+template <int TYPE>
+__device__ __noinline__ uint64_t weight_once(const RowPlan &p, const float2 *roots, float v) {
+    return weight<TYPE>(p, roots, v);
+}
+// Sums of weights as pairs of fp32 numbers, the largest weight being 1: what several
+// entries next to each other cost less by than by integers one by one.
+struct PairSum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float h, float l) {
+        const float x = hi + h, b = x - hi;
+        lo += ((hi - (x - b)) + (h - b)) + l;
+        hi = x;
+    }
+    __device__ __forceinline__ uint64_t units(int shift) const {
+        const float h = hi + lo, l = (hi - h) + lo;
+        const uint64_t a = in_units(h, shift), b = in_units(fabsf(l), shift);
+        return h > 0.f ? (l < 0.f ? a - b : l > 0.f ? a + b : a) : 0;
+    }
+};
+// As weight_real, as a pair; times 0 where it does not count.
+__device__ __forceinline__ float2 weight_pair(const RowPlan &p, const float2 *roots, float v, bool counts) {
+    constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
+    const float2 t = exponent(p, counts ? v : p.m);
+    const float h = fmaxf(t.x, -100.f);
+    const float km = fmaf(h, 1024.f, kMagic), kf = __fadd_rn(km, -kMagic);
+    const uint32_t k = __float_as_uint(km) - __float_as_uint(kMagic);
+    const float r = fmaf(kf, -0x1p-10f, h);
+    const float g = r * kLn2Hi;
+    const float gl = fmaf(r, kLn2Hi, -g) + fmaf(r, kLn2Lo, t.y * kLn2Hi);
+    const float lo = fmaf(g * g, fmaf(g, 1.f / 6, 0.5f), gl);
+    const float2 root = roots[k & (kRoots - 1)];
+    const float a = root.x * g, al = fmaf(root.x, g, -a);
+    const float w = root.x + a;
+    const float wl = ((root.x - w) + a) + (al + fmaf(root.x, lo, fmaf(root.y, g, root.y)));
+    const float unit = counts ? __uint_as_float((k & ~(kRoots - 1u)) * (1u << 13) + 0x3f800000u) : 0.f;
+    return make_float2(w * unit, wl * unit);
+}
+
 // The same in fp32, relative to the largest: for an estimate of the sum.
 template <int TYPE>
 __device__ __forceinline__ float rough_weight(const RowPlan &p, float v) {
@@ -179,10 +218,15 @@ __device__ __forceinline__ void vectors_at(const Row<TYPE> &r, int64_t in_lo, in
 #pragma unroll
             for (int n = 0; n < N; ++n) En::blank(q[n], keep[n]);
         }
-#pragma unroll
+        // (one copy of f's code)
+#pragma unroll 1
         for (int n = 0; n < N; ++n) {
+            uint4 x = q[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i)
+                if (n == i) x = q[i];
             float v[En::E];
-            En::values(q[n], v);
+            En::values(x, v);
             f(v, first + n * stride);
         }
     } else {
@@ -196,13 +240,13 @@ __device__ __forceinline__ void vectors_at(const Row<TYPE> &r, int64_t in_lo, in
         }
     }
 }
-// The same of all vectors lo .. hi - 1, by NT threads.
+// The same of all vectors lo .. hi - 1, by NT threads of which this is t.
 template <int TYPE, int NT, int N, class F>
-__device__ __forceinline__ void each_vector(const Row<TYPE> &r, int64_t lo, int64_t hi, F f) {
+__device__ __forceinline__ void each_vector(const Row<TYPE> &r, int64_t lo, int64_t hi, int t, F f) {
     int64_t in_lo, in_hi;
     r.inside_range(in_lo, in_hi);
     for (int64_t from = lo; from < hi; from += N * NT)
-        vectors_at<TYPE, N>(r, in_lo, in_hi, from, from + N * NT, from + threadIdx.x, NT, hi, f);
+        vectors_at<TYPE, N>(r, in_lo, in_hi, from, from + N * NT, from + t, NT, hi, f);
 }
 
 __device__ __forceinline__ uint64_t shfl_up(uint64_t x, int o) {
@@ -227,7 +271,7 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {
 }
 
 // floor(u z) and ceil(u z) of a number 0 <= u <= 1, exact.
-__device__ __forceinline__ uint64_t share(double u, uint64_t z, bool up) {
+static __device__ __noinline__ uint64_t share(double u, uint64_t z, bool up) {
     const uint64_t b = static_cast<uint64_t>(__double_as_longlong(u));
     const int e = static_cast<int>(b >> 52 & 0x7ff);
     const uint64_t m = (b & ((1ull << 52) - 1)) | (e ? 1ull << 52 : 0);
@@ -282,7 +326,7 @@ __device__ __forceinline__ int shift_of(float sum) {
 
 // Entries of weight >= min_p of the largest: those of order value >= this.
 template <int TYPE>
-__device__ __forceinline__ float least_value(const RowPlan &p, float min_p) {
+__device__ __noinline__ float least_value(const RowPlan &p, float min_p) {
     double x;
     if constexpr (Entry<TYPE>::kReal) x = p.m + log(static_cast<double>(min_p)) / p.beta;
     else if (p.beta == 1.0) x = static_cast<double>(p.m) * min_p;
@@ -292,23 +336,26 @@ __device__ __forceinline__ float least_value(const RowPlan &p, float min_p) {
     return fminf(v, p.m);
 }
 
-// log p of an entry left, from the weights' sum.
+// The logarithm of the sum of the weights left, in the logits' units (less beta times the largest
+// for logits and powers), and log p of an entry left.
 template <int TYPE>
-__device__ __noinline__ float log_p(const RowPlan &p, float v, uint64_t total) {
+__device__ __noinline__ double log_z(const RowPlan &p, uint64_t total) {
     constexpr double kLn2d = 0.693147180559945309;
-    double z = log(static_cast<double>(total)) - p.shift * kLn2d, x;
-    if constexpr (Entry<TYPE>::kReal) {
-        x = p.beta * (static_cast<double>(v) - p.m);
-    } else if (p.beta == 1.0) {
-        x = log(static_cast<double>(v));
-        z += p.down_log * kLn2d;
-    } else {
-        x = p.beta * log(static_cast<double>(v) / p.m);
-    }
+    int units = p.shift;
+    if (!Entry<TYPE>::kReal && p.beta == 1.0) units -= p.down_log;
+    return log(static_cast<double>(total)) - units * kLn2d;
+}
+template <int TYPE>
+__device__ __noinline__ float log_p(const RowPlan &p, float v, double z) {
+    if (p.greedy) return 0.f;
+    double x;
+    if constexpr (Entry<TYPE>::kReal) x = p.beta * (static_cast<double>(v) - p.m);
+    else if (p.beta == 1.0) x = log(static_cast<double>(v));
+    else x = p.beta * log(static_cast<double>(v) / p.m);
     return static_cast<float>(x - z);
 }
 
-// ---- a row of one CTA -------------------------------------------------------
+// ---- a row of one group of threads ------------------------------------------
 
 struct Select {
     uint32_t lo[256], hi[256], count[256];
@@ -318,6 +365,46 @@ struct Select {
     bool whole;
 };
 
+__device__ __forceinline__ void add_digit(Select *sel, int d, uint64_t w, bool mass) {
+    atomicAdd(&sel->count[d], 1u);
+    if (!mass) return;
+    const uint32_t l = static_cast<uint32_t>(w), old = atomicAdd(&sel->lo[d], l);
+    const uint32_t h = static_cast<uint32_t>(w >> 32) + (old + l < l);
+    if (h) atomicAdd(&sel->hi[d], h);
+}
+// One warp: the digit, from the top, at which sums (or numbers) that begin with `above` reach the
+// target; -1 if they do not.
+template <bool MASS>
+__device__ __noinline__ void find_digit(Select *sel, uint64_t above, uint64_t target) {
+    const int lane = threadIdx.x % 32;
+    const auto at = [&](int i) -> uint64_t {        // eight digits a lane
+        const int d = 255 - lane * 8 - i;
+        return MASS ? static_cast<uint64_t>(sel->hi[d]) << 32 | sel->lo[d] : sel->count[d];
+    };
+    uint64_t own = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own += at(i);
+    uint64_t upto = above + warp_scan(own, lane);
+    const uint32_t reached = __ballot_sync(0xffffffffu, upto >= target);
+    if (lane == 0) sel->digit = -1;
+    __syncwarp();
+    if (!reached || lane != __ffs(reached) - 1) return;
+    upto -= own;
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t x = at(i);
+        if (upto + x >= target) {
+            const int d = 255 - lane * 8 - i;
+            sel->digit = d;
+            sel->in_digit = sel->count[d];
+            sel->above = upto;
+            sel->whole = upto + x == target;
+            return;
+        }
+        upto += x;
+    }
+}
+
+// NT threads, a warp or the CTA, that share a row.
 template <int TYPE, int NT>
 struct RowCta {
     static constexpr int E = Entry<TYPE>::E;
@@ -327,22 +414,30 @@ struct RowCta {
     const float2 *roots;
     Select *sel;
     uint64_t *sums;     // NT / 32
+    int t;              // thread of the group
+
+    __device__ __forceinline__ void sync() const {
+        if constexpr (NT == 32) __syncwarp();
+        else __syncthreads();
+    }
 
     // f(order value, index) of every entry of the row
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        each_vector<TYPE, NT, 1>(r, 0, vecs, [&](const float (&v)[E], int64_t j) {
+        each_vector<TYPE, NT, 1>(r, 0, vecs, t, [&](const float (&v)[E], int64_t j) {
 #pragma unroll
             for (int i = 0; i < E; ++i) f(v[i], j * E - r.head + i);
         });
     }
     __device__ __forceinline__ uint64_t sum(uint64_t x) const {
         x = warp_sum(x);
-        __syncthreads();
-        if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = x;
-        __syncthreads();
-        x = 0;
-        for (int w = 0; w < NT / 32; ++w) x += sums[w];
+        if constexpr (NT > 32) {
+            __syncthreads();
+            if (t % 32 == 0) sums[t / 32] = x;
+            __syncthreads();
+            x = 0;
+            for (int w = 0; w < NT / 32; ++w) x += sums[w];
+        }
         return x;
     }
     // Weights' sum (or the number) of the entries of at least that rank.
@@ -350,7 +445,7 @@ struct RowCta {
     __device__ __noinline__ uint64_t total(uint64_t bound) const {
         uint64_t s = 0;
         each([&](float v, int64_t e) {
-            if (rank_of<TYPE>(v, e) >= bound) s += MASS ? weight<TYPE>(*p, roots, v) : 1;
+            if (rank_of<TYPE>(v, e) >= bound) s += MASS ? weight_once<TYPE>(*p, roots, v) : 1;
         });
         return sum(s);
     }
@@ -366,50 +461,18 @@ struct RowCta {
                 prefix |= 0xffull << 24;
                 continue;
             }
-            __syncthreads();
-            for (int i = threadIdx.x; i < 256; i += NT) sel->lo[i] = sel->hi[i] = sel->count[i] = 0;
-            __syncthreads();
+            sync();
+            for (int i = t; i < 256; i += NT) sel->lo[i] = sel->hi[i] = sel->count[i] = 0;
+            sync();
             each([&](float v, int64_t e) {
                 const uint64_t k = rank_of<TYPE>(v, e);
                 if (k < bound || k == 0 || (shift < 56 && (k ^ prefix) >> (shift + 8))) return;
                 const int d = static_cast<int>(k >> shift & 255);
-                atomicAdd(&sel->count[d], 1u);
-                if constexpr (MASS) {
-                    const uint64_t w = weight<TYPE>(*p, roots, v);
-                    const uint32_t l = static_cast<uint32_t>(w), old = atomicAdd(&sel->lo[d], l);
-                    const uint32_t h = static_cast<uint32_t>(w >> 32) + (old + l < l);
-                    if (h) atomicAdd(&sel->hi[d], h);
-                }
+                add_digit(sel, d, MASS ? weight_once<TYPE>(*p, roots, v) : 0, MASS);
             });
-            __syncthreads();
-            if (threadIdx.x < 32) {     // eight digits a lane, from the top
-                const int lane = threadIdx.x;
-                uint64_t own = 0;
-                for (int i = 0; i < 8; ++i) {
-                    const int d = 255 - lane * 8 - i;
-                    own += MASS ? static_cast<uint64_t>(sel->hi[d]) << 32 | sel->lo[d] : sel->count[d];
-                }
-                uint64_t upto = above + warp_scan(own, lane);
-                const uint32_t reached = __ballot_sync(0xffffffffu, upto >= target);
-                if (lane == 0) sel->digit = -1;
-                __syncwarp();
-                if (reached && lane == __ffs(reached) - 1) {
-                    upto -= own;
-                    for (int i = 0; i < 8; ++i) {
-                        const int d = 255 - lane * 8 - i;
-                        const uint64_t x = MASS ? static_cast<uint64_t>(sel->hi[d]) << 32 | sel->lo[d] : sel->count[d];
-                        if (upto + x >= target) {
-                            sel->digit = d;
-                            sel->in_digit = sel->count[d];
-                            sel->above = upto;
-                            sel->whole = upto + x == target;
-                            break;
-                        }
-                        upto += x;
-                    }
-                }
-            }
-            __syncthreads();
+            sync();
+            if (t < 32) find_digit<MASS>(sel, above, target);
+            sync();
             if (sel->digit < 0) return bound;
             above = sel->above;
             prefix |= static_cast<uint64_t>(sel->digit) << shift;
@@ -418,6 +481,54 @@ struct RowCta {
         return prefix > bound ? prefix : bound;
     }
 };
+
+// Which entries of a row are left: those of order value >= gate, and of those below it but
+// >= list the ones of rank >= bound.
+struct Cut {
+    float gate, list;
+    uint64_t bound;
+};
+template <int TYPE>
+__device__ __forceinline__ bool is_left(const Cut &c, float v, int64_t e) {
+    return v >= c.gate || (v >= c.list && rank_of<TYPE>(v, e) >= c.bound);
+}
+// The lowest order value of a present entry.
+template <int TYPE>
+__device__ __forceinline__ constexpr float least_present() {
+    return Entry<TYPE>::kReal ? -3.402823466e38f : 1.4e-45f;
+}
+
+// Weights' sum of a vector's entries that are left, 1 at least for each: of those
+// above the gate together, of the others one by one.
+template <int TYPE>
+__device__ __noinline__ uint64_t vector_weight(const RowPlan &p, const Cut &c, const float2 *roots,
+                                               const float (&v)[Entry<TYPE>::E], int64_t e0) {
+    constexpr int E = Entry<TYPE>::E;
+    uint64_t own = 0;
+    if constexpr (Entry<TYPE>::kReal) {
+        PairSum sum;
+        uint32_t n = 0, some = 0;
+#pragma unroll 1
+        for (int k = 0; k < E; ++k) {
+            const bool above = v[k] >= c.gate;
+            const float2 w = weight_pair(p, roots, v[k], above);
+            sum.add(w.x, w.y);
+            n += above;
+            some |= !above && v[k] >= c.list;
+        }
+        own = sum.units(p.shift) + n;
+        if (some) {
+#pragma unroll 1
+            for (int k = 0; k < E; ++k)
+                if (!(v[k] >= c.gate) && is_left<TYPE>(c, v[k], e0 + k)) own += weight_once<TYPE>(p, roots, v[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (is_left<TYPE>(c, v[k], e0 + k)) own += weight_once<TYPE>(p, roots, v[k]);
+    }
+    return own;
+}
 
 // The first of n sums at which their total exceeds `target`, which becomes what is
 // left of it there; one warp.
@@ -435,60 +546,71 @@ __device__ __forceinline__ int64_t locate(const uint64_t *sums, int64_t n, uint6
     }
     return 0;
 }
-
-// The same of sums that are added up already: a search by 32.
-__device__ __forceinline__ int64_t locate_upto(const ulonglong2 *upto, int64_t n, uint64_t &target) {
+// The same of sums that are added up already, upto(i): a search by 32.
+template <class F>
+__device__ __forceinline__ int64_t locate_upto(F upto, int64_t n, uint64_t &target) {
     const int lane = threadIdx.x % 32;
     int64_t lo = 0, len = n;
     while (len > 1) {
         const int64_t step = (len + 31) / 32, at = lo + (lane + 1) * step - 1;
-        const bool over = lane * step < len && (at >= lo + len - 1 || __ldcg(&upto[at]).x > target);
+        const bool over = lane * step < len && (at >= lo + len - 1 || upto(at) > target);
         const int l = __ffs(__ballot_sync(0xffffffffu, over)) - 1;
         len = len - l * step < step ? len - l * step : step;
         lo += l * step;
     }
-    if (lo > 0) target -= __ldcg(&upto[lo - 1]).x;
+    if (lo > 0) target -= upto(lo - 1);
     return lo;
 }
 
-// One warp: a draw of row r.  Where the row has segments, `partials` holds their
-// sums up to each (the first of a pair).
+__device__ __forceinline__ double random_number(const SampleArgs &a, int64_t at) {
+    return a.wide ? static_cast<const double *>(a.u)[at] : static_cast<const float *>(a.u)[at];
+}
+// A draw with an invalid number.
+__device__ __forceinline__ void bad_draw(const SampleArgs &a, int64_t at, int64_t row) {
+    a.ids[at] = -1;
+    a.logp[at] = __uint_as_float(0x7fc00000u);
+    flag_bad_id(a.r, row);
+}
+// One thread: the draw falls into this vector, `left` behind its first entry's begin.
 template <int TYPE>
-__device__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs, const RowPlan &p, const float2 *roots,
-                          const uint64_t *masses, int64_t pieces, const ulonglong2 *partials, uint64_t total,
-                          int64_t at, int64_t row) {
+__device__ __noinline__ void finish_draw(const SampleArgs &a, const RowPlan &p, const Cut &c, const float2 *roots,
+                                            const float (&v)[Entry<TYPE>::E], int64_t e0, uint64_t left, double z,
+                                            int64_t at) {
+    constexpr int E = Entry<TYPE>::E;
+    // (the vector's sum may be some units more than its entries': the last one's then)
+    float value = 0.f;
+    int64_t id = -1;
+    bool found = false;
+#pragma unroll 1
+    for (int k = 0; k < E; ++k) {
+        if (found || !is_left<TYPE>(c, v[k], e0 + k)) continue;
+        const uint64_t w = weight_once<TYPE>(p, roots, v[k]) + (Entry<TYPE>::kReal && v[k] >= c.gate ? 1 : 0);
+        value = v[k];
+        id = e0 + k;
+        found = w > left;
+        left -= w;
+    }
+    a.ids[at] = id;
+    a.logp[at] = log_p<TYPE>(p, value, z);
+}
+
+// One warp: a draw of row r that lies `target` behind the begin of piece `first`, within the next
+// `pieces`; z as log_z makes it.
+template <int TYPE>
+__device__ __noinline__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs, const RowPlan &p, const Cut &c,
+                                       const float2 *roots, const uint64_t *masses, int64_t first, int64_t pieces,
+                                       uint64_t target, double z, int64_t at) {
     constexpr int E = Entry<TYPE>::E;
     const int lane = threadIdx.x % 32;
-    const double u = a.wide ? static_cast<const double *>(a.u)[at] : static_cast<const float *>(a.u)[at];
-    if (!(u >= 0.0 && u < 1.0)) {
-        if (lane == 0) {
-            a.ids[at] = -1;
-            a.logp[at] = __uint_as_float(0x7fc00000u);
-            flag_bad_id(a.r, row);
-        }
-        return;
-    }
-    uint64_t target = p.greedy ? 0 : share(u, total, false);
-    int64_t first = 0;
-    if (partials) {
-        first = locate_upto(partials, a.segs, target) * a.seg_pieces;
-        pieces = pieces - first < a.seg_pieces ? pieces - first : a.seg_pieces;
-    }
     const int64_t piece = first + locate(masses + first, pieces, target);
+#pragma unroll 1
     for (int i = 0; i < kPieceVecs / 32; ++i) {
         const int64_t j = piece * kPieceVecs + i * 32 + lane;
         float v[E];
-        uint64_t w[E], own = 0;
-#pragma unroll
-        for (int k = 0; k < E; ++k) w[k] = 0;
+        uint64_t own = 0;
         if (j < vecs) {
             vector_values<TYPE>(r, j, v);
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const uint64_t rank = rank_of<TYPE>(v[k], j * E - r.head + k);
-                if (rank >= p.bound) w[k] = weight<TYPE>(p, roots, v[k]);
-                own += w[k];
-            }
+            own = vector_weight<TYPE>(p, c, roots, v, j * E - r.head);
         }
         const uint64_t upto = warp_scan(own, lane);
         const uint32_t over = __ballot_sync(0xffffffffu, upto > target);
@@ -496,90 +618,86 @@ __device__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs,
             target -= shfl_from(upto, 31);
             continue;
         }
-        if (lane == __ffs(over) - 1) {
-            uint64_t left = target - (upto - own);
-            bool found = false;
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                if (!found && w[k] > left) {
-                    found = true;
-                    a.ids[at] = j * E - r.head + k;
-                    a.logp[at] = p.greedy ? 0.f : log_p<TYPE>(p, v[k], total);
-                }
-                left -= w[k];
-            }
-        }
+        if (lane == __ffs(over) - 1) finish_draw<TYPE>(a, p, c, roots, v, j * E - r.head, target - (upto - own), z, at);
         return;
     }
 }
+// Whether a random number is valid; what it aims at.
+__device__ __forceinline__ bool aim(const SampleArgs &a, double u, bool greedy, uint64_t total, int64_t at, int64_t row,
+                                    uint64_t &target) {
+    if (!(u >= 0.0 && u < 1.0)) {
+        if (threadIdx.x % 32 == 0) bad_draw(a, at, row);
+        return false;
+    }
+    target = greedy ? 0 : share(u, total, false);
+    return true;
+}
 
-// Outcomes of a row that has none.
-__device__ __forceinline__ void no_draws(const SampleArgs &a, int64_t row, int state) {
-    for (int64_t d = threadIdx.x; d < a.draws; d += kDrawThreads) {
+// Outcomes of a row that has none, by thread t of n.
+__device__ __forceinline__ void no_draws(const SampleArgs &a, int64_t row, int state, int t, int n) {
+    for (int64_t d = t; d < a.draws; d += n) {
         a.ids[row * a.draws + d] = -1;
         a.logp[row * a.draws + d] = state == kEmpty ? -__builtin_huge_valf() : __uint_as_float(0x7fc00000u);
     }
-    if (threadIdx.x == 0) a.kept[row] = 0;
+    if (t == 0) a.kept[row] = 0;
 }
 
+// The filters of a row, by a group, from its plan; its pieces' sums, their total and the draws.
 template <int TYPE, int NT>
-__global__ void __launch_bounds__(NT) sample_rows_kernel(const __grid_constant__ SampleArgs a) {
-    constexpr int E = Entry<TYPE>::E;
+__device__ __noinline__ uint64_t bound_of(const RowCta<TYPE, NT> &c, const RowPlan &p, int64_t top_k, float top_p) {
+    uint64_t bound = kPresent;
+    if (top_k > 0 && top_k < c.r.cols) bound = c.template select<false>(top_k, bound);
+    if (top_p < 1.f) {
+        const uint64_t all = c.template total<true>(bound), t = share(fmaxf(top_p, 0.f), all, true);
+        bound = c.template select<true>(t > 0 ? t : 1, bound);
+    }
+    return bound > p.bound ? bound : p.bound;
+}
+
+// Rows of a group of NT threads each (a warp, or the whole CTA), from end to end.
+template <int TYPE, int NT>
+__global__ void __launch_bounds__(kDrawThreads) rows_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E, GROUPS = kDrawThreads / NT;
     __shared__ float2 roots[kRoots];
-    __shared__ RowPlan plan;
-    __shared__ Select sel;
-    __shared__ uint64_t sums[NT / 32];
-    __shared__ uint32_t red[4 * (NT / 32)];
+    __shared__ Select sel[GROUPS];
+    __shared__ uint64_t sums[GROUPS][NT / 32];
+    __shared__ uint32_t red[GROUPS][4 * (NT / 32)];
     pdl_trigger();
-    make_roots<kDrawThreads>(roots);
+    if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
     pdl_wait();
-    Group<NT> g(red);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int64_t row = blockIdx.x; row < a.r.rows; row += gridDim.x) {
-        RowCta<TYPE, NT> c{Row<TYPE>(a.r, row), 0, &plan, roots, &sel, sums};
+    __syncthreads();
+    const int group = threadIdx.x / NT, t = threadIdx.x % NT, warp = t / 32, lane = t % 32;
+    Group<NT> g(red[group]);
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group; row < a.r.rows;
+         row += static_cast<int64_t>(gridDim.x) * GROUPS) {
+        RowPlan plan;
+        RowCta<TYPE, NT> c{Row<TYPE>(a.r, row), 0, &plan, roots, &sel[group], sums[group], t};
         c.vecs = (c.r.head + c.r.cols + E - 1) / E;
         float m = absent<TYPE>();
         c.each([&](float v, int64_t) { m = max_nan(m, v); });
         m = g.max(m);
         Filters f;
         const bool valid = filters_of(a, row, f);
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            plan_row<TYPE>(plan, m, valid, f);
-            if (!valid) flag_bad_id(a.r, row);
-        }
-        __syncthreads();
+        plan_row<TYPE>(plan, m, valid, f);
+        if (!valid && t == 0) flag_bad_id(a.r, row);
         if (plan.state != kDraw) {
-            no_draws(a, row, plan.state);
+            no_draws(a, row, plan.state, t, NT);
             continue;
         }
+        Cut cut = {plan.greedy ? m : least_present<TYPE>(), m, kPresent};
         if (!plan.greedy) {
             float s = 0.f;
             c.each([&](float v, int64_t) {
                 if (v != absent<TYPE>()) s += rough_weight<TYPE>(plan, v);
             });
-            s = g.sum(s);
-            if (threadIdx.x == 0) plan.shift = shift_of(s);
-            __syncthreads();
-        }
-        uint64_t bound = kPresent;
-        if (plan.greedy) {
-            bound = c.template select<false>(1, kPresent);
-        } else {
-            if (f.top_k > 0 && f.top_k < a.r.cols) bound = c.template select<false>(f.top_k, bound);
-            if (f.top_p < 1.f) {
-                const uint64_t all = c.template total<true>(bound), t = share(fmaxf(f.top_p, 0.f), all, true);
-                bound = c.template select<true>(t > 0 ? t : 1, bound);
-            }
+            plan.shift = shift_of(g.sum(s));
             if (f.min_p > 0.f) {
-                const uint64_t least = static_cast<uint64_t>(order_key<TYPE>(least_value<TYPE>(plan, f.min_p))) << 32;
-                if (least > bound) bound = least;
+                cut.gate = least_value<TYPE>(plan, f.min_p);
+                plan.bound = static_cast<uint64_t>(order_key<TYPE>(cut.gate)) << 32;
             }
+            if ((f.top_k > 0 && f.top_k < a.r.cols) || f.top_p < 1.f)
+                cut = {__builtin_huge_valf(), least_present<TYPE>(), bound_of<TYPE, NT>(c, plan, f.top_k, f.top_p)};
         }
-        __syncthreads();
-        if (threadIdx.x == 0) plan.bound = bound;
-        __syncthreads();
-        // sums of pieces
         uint64_t *masses = a.masses + row * a.pieces;
         const int64_t pieces = (c.vecs + kPieceVecs - 1) / kPieceVecs;
         uint64_t total = 0, kept = 0;
@@ -590,25 +708,224 @@ __global__ void __launch_bounds__(NT) sample_rows_kernel(const __grid_constant__
                 if (j >= c.vecs) break;
                 float v[E];
                 vector_values<TYPE>(c.r, j, v);
+                own += vector_weight<TYPE>(plan, cut, roots, v, j * E - c.r.head);
 #pragma unroll
-                for (int k = 0; k < E; ++k)
-                    if (rank_of<TYPE>(v[k], j * E - c.r.head + k) >= bound) {
-                        own += weight<TYPE>(plan, roots, v[k]);
-                        ++kept;
-                    }
+                for (int k = 0; k < E; ++k) kept += is_left<TYPE>(cut, v[k], j * E - c.r.head + k);
             }
             total += own;
             own = warp_sum(own);
-            if (lane == 0) masses[q] = own;
+            if (lane == 0) __stcg(&masses[q], own);
         }
         total = c.sum(total);
         kept = c.sum(kept);
-        if (threadIdx.x == 0) a.kept[row] = static_cast<int64_t>(kept);
-        __syncthreads();
-        for (int64_t d = warp; d < a.draws; d += NT / 32)
-            warp_draw<TYPE>(a, c.r, c.vecs, plan, roots, masses, pieces, nullptr, total, row * a.draws + d,
-                            row);
-        __syncthreads();
+        if (t == 0) a.kept[row] = plan.greedy ? 1 : static_cast<int64_t>(kept);
+        c.sync();
+        const double z = a.draws > 0 && !plan.greedy ? log_z<TYPE>(plan, total) : 0.0;
+        for (int64_t d = warp; d < a.draws; d += NT / 32) {
+            const int64_t at = row * a.draws + d;
+            uint64_t target;
+            if (aim(a, random_number(a, at), plan.greedy, total, at, row, target))
+                warp_draw<TYPE>(a, c.r, c.vecs, plan, cut, roots, masses, 0, pieces, target, z, at);
+        }
+        c.sync();
+    }
+}
+
+// ---- rows that a warp has in its registers ------------------------------------
+//
+// kWarpEntries entries a lane, whose weights are kept too.  Filters find the rank where they cut
+// bit by bit (how many, or how much, lies at or above it).  Bound by its chain of warp
+// reductions where rows are filtered.
+
+constexpr int kWarpEntries = 16;
+
+template <int TYPE>
+__global__ void __launch_bounds__(kDrawThreads, 2) warp_rows_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E, V = kWarpEntries / E;
+    __shared__ float2 roots[kRoots];
+    pdl_trigger();
+    if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
+    pdl_wait();
+    __syncthreads();
+    const int lane = threadIdx.x % 32;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kDrawWarps + threadIdx.x / 32; row < a.r.rows;
+         row += static_cast<int64_t>(gridDim.x) * kDrawWarps) {
+        const Row<TYPE> r(a.r, row);
+        const int vecs = static_cast<int>((r.head + r.cols + E - 1) / E);
+        Filters f;
+        const bool valid = filters_of(a, row, f);
+        float v[V][E];
+        float m = absent<TYPE>();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (32 * i + lane < vecs) {
+                vector_values<TYPE>(r, 32 * i + lane, v[i]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) v[i][k] = absent<TYPE>();
+            }
+#pragma unroll
+            for (int k = 0; k < E; ++k) m = max_nan(m, v[i][k]);
+        }
+        m = warp_max_nan(m);
+        RowPlan p;
+        plan_row<TYPE>(p, m, valid, f);
+        if (!valid && lane == 0) flag_bad_id(a.r, row);
+        if (p.state != kDraw) {
+            no_draws(a, row, p.state, lane, 32);
+            continue;
+        }
+        if (!p.greedy) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (v[i][k] != absent<TYPE>()) s += rough_weight<TYPE>(p, v[i][k]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            p.shift = shift_of(s);
+        }
+        uint64_t w[V][E];
+        uint32_t left = 0;      // bit i E + k: entry k of vector i
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const bool here = p.greedy ? v[i][k] == m : v[i][k] != absent<TYPE>();
+                w[i][k] = here ? weight<TYPE>(p, roots, v[i][k]) : 0;
+                left |= static_cast<uint32_t>(here) << (i * E + k);
+            }
+        const auto index = [&](int i, int k) { return (32 * i + lane) * E + k - r.head; };
+        // keep the entries, largest first, until `target` is reached
+        const auto cut = [&](uint64_t target, bool by_mass) {
+            uint32_t key = 0;
+            for (int b = 31; b >= 0; --b) {
+                const uint32_t x = key | 1u << b;
+                uint64_t s = 0;
+                uint32_t n = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int k = 0; k < E; ++k)
+                        if ((left >> (i * E + k) & 1) && order_key<TYPE>(v[i][k]) >= x) {
+                            s += w[i][k];
+                            ++n;
+                        }
+                s = by_mass ? warp_sum(s) : __reduce_add_sync(0xffffffffu, n);
+                if (s >= target) key = x;
+            }
+            // of the entries of that key the first ones: `above` is what lies over them
+            uint64_t above = 0;
+            uint32_t tied = 0, next = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    const uint32_t bit = 1u << (i * E + k);
+                    if (!(left & bit)) continue;
+                    const uint32_t o = order_key<TYPE>(v[i][k]);
+                    if (o > key) {
+                        above += by_mass ? w[i][k] : 1;
+                        next |= bit;
+                    } else if (o == key) {
+                        tied |= bit;
+                    }
+                }
+            above = warp_sum(above);
+            // equal entries have equal weights: as many as it takes
+            uint64_t one = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (tied >> (i * E + k) & 1) one = by_mass ? w[i][k] : 1;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                const uint64_t x = __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(one), o);
+                one = x > one ? x : one;
+            }
+            uint32_t need = one > 0 && target > above ? static_cast<uint32_t>((target - above + one - 1) / one) : 0;
+            for (int i = 0; i < V && need > 0; ++i) {       // in the order of indices
+                const uint32_t mine = __popc(tied >> (i * E) & ((1u << E) - 1u));
+                const uint32_t upto = static_cast<uint32_t>(warp_scan(mine, lane));
+                uint32_t before = upto - mine;
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (tied >> (i * E + k) & 1) {
+                        if (before < need) next |= 1u << (i * E + k);
+                        ++before;
+                    }
+                const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+                need = need > all ? need - all : 0;
+            }
+            left = next;
+        };
+        const auto sum_left = [&] {
+            uint64_t s = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (left >> (i * E + k) & 1) s += w[i][k];
+            return warp_sum(s);
+        };
+        if (!p.greedy) {
+            if (f.top_k > 0 && f.top_k < a.r.cols && __reduce_add_sync(0xffffffffu, __popc(left)) > static_cast<uint32_t>(f.top_k))
+                cut(f.top_k, false);
+            if (f.top_p < 1.f) {
+                const uint64_t t = share(fmaxf(f.top_p, 0.f), sum_left(), true);
+                cut(t > 0 ? t : 1, true);
+            }
+            if (f.min_p > 0.f) {
+                const float least = least_value<TYPE>(p, f.min_p);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int k = 0; k < E; ++k)
+                        if (v[i][k] < least) left &= ~(1u << (i * E + k));
+            }
+        }
+        const uint32_t kept = __reduce_add_sync(0xffffffffu, __popc(left));
+        if (lane == 0) a.kept[row] = p.greedy ? 1 : kept;
+        // sums up to each of the lane's vectors
+        uint64_t upto[V], total = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            uint64_t own = 0;
+#pragma unroll
+            for (int k = 0; k < E; ++k) own += left >> (i * E + k) & 1 ? w[i][k] : 0;
+            upto[i] = total + warp_scan(own, lane);
+            total = shfl_from(upto[i], 31);
+        }
+        const double z = a.draws > 0 && !p.greedy ? log_z<TYPE>(p, total) : 0.0;
+        for (int64_t d = 0; d < a.draws; ++d) {
+            const int64_t at = row * a.draws + d;
+            uint64_t target;
+            if (!aim(a, random_number(a, at), p.greedy, total, at, row, target)) continue;
+            bool done = false;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t over = __ballot_sync(0xffffffffu, upto[i] > target);
+                if (done || !over) continue;
+                done = true;
+                if (lane == __ffs(over) - 1) {
+                    uint64_t before = upto[i];
+#pragma unroll
+                    for (int k = 0; k < E; ++k) before -= left >> (i * E + k) & 1 ? w[i][k] : 0;
+                    bool found = false;
+#pragma unroll
+                    for (int k = 0; k < E; ++k) {
+                        if (found || !(left >> (i * E + k) & 1)) continue;
+                        before += w[i][k];
+                        if (before <= target) continue;
+                        found = true;
+                        a.ids[at] = index(i, k);
+                        a.logp[at] = log_p<TYPE>(p, v[i][k], z);
+                    }
+                }
+            }
+        }
     }
 }
 
@@ -616,47 +933,71 @@ __global__ void __launch_bounds__(NT) sample_rows_kernel(const __grid_constant__
 //
 // One CTA a segment, a kernel for each pass over the rows; the CTA that finishes a
 // row's last segment does what follows for the row:
-//   top_kernel      the largest entry and a rough sum of weights; then the row's plan
-//   bins_kernel     weights (and numbers) by bins of the order value, where a row has
-//                   a top_k or top_p; then the bin in which they cut
-//   cut_kernel      that bin's entries into a list; then sorted, the last rank left
-//   sums_kernel     sums of the weights left, by pieces and segments; then a few draws
-//   draws_kernel    many draws, a warp each
-// Passes are bound by memory or, those with weights, by arithmetic (some 60
-// operations an entry); launches hide behind each other's ends.
+//   top_kernel    the largest entry and a rough sum of weights; then the row's plan
+//   bins_kernel   where a row has a top_k or top_p: how many entries lie in bins of the
+//                 order value; then a range of bins in which the filters cut (a bin's
+//                 weight is about its number times that of its middle)
+//   sums_kernel   sums of the weights above the range, by pieces and segments, and the
+//                 range's entries in a list; then the list is sorted, the cut found among it
+//                 by exact sums, what is left of it added to the pieces, and a few draws made
+//   draws_kernel  many draws, a warp each
+// The first two are bound by memory, the third by arithmetic (some 50 operations for a
+// weight); launches hide behind each other's ends.
 
 struct RowState {
     RowPlan plan;
-    float top_p, min_p;
+    Cut cut;
+    float top_p;
     int32_t top_k;
-    int32_t narrow;         // whether bins are wanted
-    float bin_scale;
-    int32_t slot_lo, slot_hi;   // slots (see slot_of) of the entries to sort
-    uint32_t expected;      // their number
-    uint64_t above, all;    // weights (or number, without top_p) before them, of all
+    int32_t narrow;         // bins are wanted (kBinned), the list decides (kListed), or neither
+    float bin_scale, min_value;
+    int32_t slot_lo, slot_hi;   // slots (see slot_of) of the range
+    uint32_t expected;      // its entries
+    uint32_t above;         // and those above it
     uint64_t total;         // weights left
-    uint32_t arrived[4];
+    double z;               // log_z of them
+    uint32_t arrived[3];
     uint32_t listed;
 };
+enum { kBinned = 1, kListed = 2 };
 
 struct RowBins {
-    unsigned long long mass[kBins];
     uint32_t count[kBins];
 };
 
-// Place of an order value on a scale from the largest down, of kBins bins of kBins
+// Place of an order value on a scale from the largest down, of kBins bins of kSlots
 // slots: for logits linear, for amplitudes linear between powers of two.  A larger
 // value's is never greater (roundings are monotone).
+constexpr int kSlots = 1024, kLastSlot = kBins * kSlots - 1;
 template <int TYPE>
 __device__ __forceinline__ int slot_of(const RowPlan &p, float bin_scale, float v) {
-    constexpr int kLast = kBins * kBins - 1;
     if constexpr (Entry<TYPE>::kReal) {
         const float t = (p.m - v) * bin_scale;
-        return t < static_cast<float>(kLast) ? static_cast<int>(t) : kLast;
+        return static_cast<int>(fminf(t, static_cast<float>(kLastSlot)));
     } else {
         const uint32_t d = (__float_as_uint(p.m) - __float_as_uint(v)) >> 7;
-        return d < kLast ? static_cast<int>(d) : kLast;
+        return d < kLastSlot ? static_cast<int>(d) : kLastSlot;
     }
+}
+// The lowest order value whose slot is below `slot`.
+template <int TYPE>
+__device__ __noinline__ float slot_begin(const RowPlan &p, float bin_scale, int slot) {
+    if (slot <= 0) return __builtin_huge_valf();
+    uint32_t lo = order_key<TYPE>(least_present<TYPE>()), hi = order_key<TYPE>(p.m);    // hi's slot is 0
+    if (Entry<TYPE>::kReal) {       // near where it should be, if it is there
+        const uint32_t guess = order_key<TYPE>(p.m - slot / bin_scale);
+        if (guess > lo + 64 && guess + 64 < hi && slot_of<TYPE>(p, bin_scale, key_value(guess - 64)) >= slot &&
+            slot_of<TYPE>(p, bin_scale, key_value(guess + 64)) < slot) {
+            lo = guess - 64;
+            hi = guess + 64;
+        }
+    }
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (slot_of<TYPE>(p, bin_scale, key_value(mid)) < slot) hi = mid;
+        else lo = mid + 1;
+    }
+    return key_value(hi);
 }
 
 template <int TYPE>
@@ -708,7 +1049,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
     // the sum relative to the largest entry so far
     const float ch = fminf(f.beta * kLog2E, 3.402823466e38f);
     float m = absent<TYPE>(), s = 0.f;
-    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, [&](const float (&v)[E], int64_t) {
+    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t) {
         float top = v[0];
 #pragma unroll
         for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
@@ -764,37 +1105,36 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
         state = p.state;
         st.narrow = 0;
         st.listed = 0;
+        st.min_value = least_present<TYPE>();
         if (p.state == kDraw) {
             if (!Entry<TYPE>::kReal && f.beta == 1.f) s *= p.down;
             p.shift = p.greedy ? 0 : shift_of(s);
             if (p.greedy) {
-                p.bound = static_cast<uint64_t>(order_key<TYPE>(m)) << 32;
+                st.min_value = m;
             } else {
-                if (f.min_p > 0.f) p.bound = static_cast<uint64_t>(order_key<TYPE>(least_value<TYPE>(p, f.min_p))) << 32;
-                st.narrow = (f.top_k > 0 && f.top_k < a.r.cols) || f.top_p < 1.f;
+                if (f.min_p > 0.f) {
+                    st.min_value = least_value<TYPE>(p, f.min_p);
+                    p.bound = static_cast<uint64_t>(order_key<TYPE>(st.min_value)) << 32;
+                }
+                if ((f.top_k > 0 && f.top_k < a.r.cols) || f.top_p < 1.f) st.narrow = kBinned;
             }
         }
         st.plan = p;
+        st.cut = {st.min_value, st.min_value, p.bound};
         st.top_p = fmaxf(f.top_p, 0.f);
         st.top_k = f.top_k;
-        // 32 bins a power of two in weight; for top_k, whose place has nothing to do with weights, 128
+        // 64 bins a power of two in weight; for top_k, whose place has nothing to do with weights, 128
         // a unit of the logits at most
-        const float scale = 32.f * p.ch;
-        st.bin_scale = kBins * fminf(scale, f.top_k > 0 ? 128.f : 0x1p80f);
+        const float scale = 64.f * p.ch;
+        st.bin_scale = kSlots * fminf(scale, f.top_k > 0 ? 128.f : 0x1p80f);
     }
     __syncthreads();
-    if (state != kDraw) no_draws(a, c.row, state);
-}
-
-__device__ __forceinline__ void add_mass(uint32_t *lo, uint32_t *hi, uint64_t w) {
-    const uint32_t l = static_cast<uint32_t>(w), old = atomicAdd(lo, l);
-    const uint32_t h = static_cast<uint32_t>(w >> 32) + (old + l < l);
-    if (h) atomicAdd(hi, h);
+    if (state != kDraw) no_draws(a, c.row, state, threadIdx.x, kDrawThreads);
 }
 
 // exclusive prefix sums over the CTA's threads; `sums` has kDrawWarps + 1 places, the
 // last for the total
-__device__ __forceinline__ uint64_t cta_scan(uint64_t x, uint64_t *sums) {
+static __device__ __noinline__ uint64_t cta_scan(uint64_t x, uint64_t *sums) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint64_t upto = warp_scan(x, lane);
     __syncthreads();
@@ -811,214 +1151,357 @@ __device__ __forceinline__ uint64_t cta_scan(uint64_t x, uint64_t *sums) {
     return before + upto - x;
 }
 
-// FINE: the bins are the slots of the bin in which the first pass ended, where it
-// has more entries than are sorted.
+// FINE: the bins are the slots of the range that the first pass found, where it has more
+// entries than are sorted.
 template <int TYPE, bool FINE>
-__global__ void __launch_bounds__(kDrawThreads) bins_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E, kOwn = kBins / kDrawThreads;
-    __shared__ uint32_t lo[kBins], hi[kBins], count[kBins];
-    __shared__ float2 roots[kRoots];
+    // (absent entries count behind the last; at the end a thread's bins lie together, its neighbours' one
+    // place further, so that they meet no bank twice)
+    __shared__ uint32_t count[kBins + kDrawThreads];
     __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
+    __shared__ int range[2];
     pdl_trigger();
-    make_roots<kDrawThreads>(roots);
-    for (int i = threadIdx.x; i < kBins; i += kDrawThreads) lo[i] = hi[i] = count[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += kDrawThreads) count[i] = 0;
     pdl_wait();
     const Segment<TYPE> c(a);
     RowState &st = a.state[c.row];
-    if (!st.narrow || (FINE && (st.expected <= kSorted || st.slot_hi - st.slot_lo != kBins - 1))) return;
+    if (st.narrow == 0 || (FINE && st.expected <= kSorted)) return;
     const RowPlan p = st.plan;
     const float bin_scale = st.bin_scale;
-    const bool by_mass = st.top_p < 1.f;
     const int64_t k = st.top_k > 0 && st.top_k < a.r.cols ? st.top_k : 0;
-    const int first = FINE ? st.slot_lo : 0;
-    const uint64_t above0 = FINE ? st.above : 0;
+    const float top_p = st.top_p;
+    const bool by_mass = top_p < 1.f && (!FINE || k == 0);
+    // FINE: up to four bins, each slot a bin
+    const int first = FINE ? st.slot_lo : 0, last = FINE ? st.slot_hi : kLastSlot;
+    const uint32_t above0 = FINE ? st.above : 0;
+    if (FINE && last - first >= kBins) return;
     __syncthreads();
-    each_vector<TYPE, kDrawThreads, 2>(c.r, c.lo, c.hi, [&](const float (&v)[E], int64_t) {
+    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t) {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            if (v[i] == absent<TYPE>()) continue;
-            int b = slot_of<TYPE>(p, bin_scale, v[i]) - first;
-            if (!FINE) b /= kBins;
-            if (FINE && (b < 0 || b >= kBins)) continue;
-            atomicAdd(&count[b], 1u);
-            if (by_mass) add_mass(&lo[b], &hi[b], weight<TYPE>(p, roots, v[i]));
+            const int s = slot_of<TYPE>(p, bin_scale, v[i]);
+            if (FINE) {
+                if (v[i] != absent<TYPE>() && s >= first && s <= last) atomicAdd(&count[s - first], 1u);
+            } else {
+                atomicAdd(&count[v[i] == absent<TYPE>() ? kBins + threadIdx.x % 32 : s / kSlots], 1u);
+            }
         }
     });
     __syncthreads();
     RowBins *all = a.segs > 1 ? a.bins + c.row : nullptr;
     if (all) {
         for (int i = threadIdx.x; i < kBins; i += kDrawThreads)
-            if (count[i]) {
-                atomicAdd(&all->count[i], count[i]);
-                if (by_mass) atomicAdd(&all->mass[i], static_cast<unsigned long long>(hi[i]) << 32 | lo[i]);
-            }
+            if (count[i]) atomicAdd(&all->count[i], count[i]);
         if (!last_of_row(a, st, 1)) return;
     }
-    uint64_t mass[kOwn], own_mass = 0, own_count = 0;
-    uint32_t num[kOwn];
+    // numbers, and weights about: in units of which the row's largest possible sum takes 62 bits
+    int log_cols;
+    frexpf(static_cast<float>(a.r.cols) * 1.01f, &log_cols);
+    const auto middle = [&](int b) {
+        if constexpr (Entry<TYPE>::kReal) {
+            if (TYPE == TN_TYPE_BF16 && !FINE) {
+                // a bin may hold one or two of the type's values only: those
+                const float around = __bfloat162float(__float2bfloat16_rn(p.m - (b + 0.5f) * kSlots / bin_scale));
+                float s = 0.f;
+                int n = 0;
+                for (int i = -2; i <= 2; ++i) {
+                    const float v = key_value(order_key<TYPE>(around) + (i << 16));
+                    if (slot_of<TYPE>(p, bin_scale, v) / kSlots != b) continue;
+                    s += ex2((v - p.m) * p.ch);
+                    ++n;
+                }
+                if (n > 0 && n < 5) return s / n;
+            }
+            return ex2(-(FINE ? first + b + 0.5f : (b + 0.5f) * kSlots) * p.ch / bin_scale);
+        } else {
+            const float d = (FINE ? first + b + 0.5f : (b + 0.5f) * kSlots) * 128.f;
+            const uint32_t top = __float_as_uint(p.m), down = static_cast<uint32_t>(d);
+            const float q = down < top ? __uint_as_float(top - down) / p.m : 0.f;
+            return p.beta == 1.0 ? q : q > 0.f ? ex2(static_cast<float>(p.beta) * lg2(q)) : 0.f;
+        }
+    };
+    // (rolled, and weights computed again, here and below: the streaming loop wants its registers)
+    const auto number = [&](int b) { return count[b + b / kOwn]; };
+    const auto mass_of = [&](int b) -> uint64_t {
+        return by_mass && number(b) ? number(b) * in_units(middle(b), 61 - log_cols) : 0;
+    };
+    {
+        uint32_t n[kOwn];
 #pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int b = threadIdx.x + i * kDrawThreads;
+            n[i] = all ? __ldcg(&all->count[b]) : count[b];
+            if (all) all->count[b] = 0;     // left clear
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int b = threadIdx.x + i * kDrawThreads;
+            count[b + b / kOwn] = n[i];
+        }
+        __syncthreads();
+    }
+    uint64_t own_mass = 0, own_count = 0;
+#pragma unroll 1
     for (int i = 0; i < kOwn; ++i) {
         const int b = threadIdx.x * kOwn + i;
-        num[i] = all ? __ldcg(&all->count[b]) : count[b];
-        mass[i] = all ? __ldcg(&all->mass[b]) : static_cast<uint64_t>(hi[b]) << 32 | lo[b];
-        if (all) {      // left clear
-            all->count[b] = 0;
-            all->mass[b] = 0;
-        }
-        own_mass += mass[i];
-        own_count += num[i];
+        own_mass += mass_of(b);
+        own_count += number(b);
     }
-    uint64_t before_mass = cta_scan(own_mass, sums), before_count = cta_scan(own_count, nums);
-    const uint64_t total = sums[kDrawWarps], entries = nums[kDrawWarps];
+    const uint64_t before_mass = cta_scan(own_mass, sums), before_count = cta_scan(own_count, nums);
+    const uint64_t entries = nums[kDrawWarps];
     const bool cut_k = FINE ? k > 0 : k > 0 && static_cast<uint64_t>(k) < entries;
+    // both filters: the second needs all that the first leaves, so all from the top is listed
+    const bool both = cut_k && top_p < 1.f;
     if (!cut_k && !by_mass) {       // fewer entries than top_k
         if (threadIdx.x == 0) st.narrow = 0;
         return;
     }
-    uint64_t target = cut_k ? k : share(st.top_p, FINE ? st.all : total, true);
-    if (target == 0) target = 1;
-    uint64_t before = above0 + (cut_k ? before_count : before_mass), through = before_count;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-        const uint64_t x = cut_k ? num[i] : mass[i];
-        through += num[i];
-        if (before < target && before + x >= target) {      // one thread, one bin
-            const int b = threadIdx.x * kOwn + i;
-            // with both filters the second needs all that the first leaves
-            const bool both = cut_k && by_mass;
-            st.slot_lo = both ? 0 : FINE ? first + b : b * kBins;
-            st.slot_hi = FINE ? first + b : b * kBins + kBins - 1;
-            st.expected = static_cast<uint32_t>(both ? through : num[i]);
-            st.above = both ? 0 : before;
-            st.all = FINE ? st.all : total;
-            if (!cut_k) st.top_k = 0;
+    // FINE: the weight above the range is not known but by the row's: what the first pass had
+    const uint64_t total = FINE ? st.total : sums[kDrawWarps];
+    uint64_t target = cut_k ? k : share(top_p, total, false);
+    const uint64_t base = cut_k ? above0 : FINE ? st.cut.bound : 0;
+    // the bins that meet the target give or take the error of their middles, less of it
+    // where those hold too many
+    uint32_t expected = 0, above = 0;
+    uint64_t base_mass = 0;
+    for (int round = 0; round < 4; ++round) {
+        const uint64_t off = cut_k ? 0 : round == 0 ? total >> 10 : round == 1 ? total >> 12 : round == 2 ? total >> 14 : 0;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            range[0] = kBins;
+            range[1] = -1;
         }
-        before += x;
+        __syncthreads();
+        uint64_t x = base + (cut_k ? before_count : before_mass);
+        int lo = kBins, hi = -1;
+        if (x <= target + off && x + (cut_k ? own_count : own_mass) + off >= target) {
+#pragma unroll 1
+            for (int i = 0; i < kOwn; ++i) {
+                const int b = threadIdx.x * kOwn + i;
+                const uint64_t next = x + (cut_k ? number(b) : mass_of(b));
+                if (number(b) && next + off >= target && x <= target + off && (cut_k ? x < target : true)) {
+                    if (lo == kBins) lo = b;
+                    hi = b;
+                }
+                x = next;
+            }
+        }
+        if (lo < kBins) {
+            atomicMin(&range[0], lo);
+            atomicMax(&range[1], hi);
+        }
+        __syncthreads();
+        if (range[1] < 0) range[1] = -1;        // (none: past all of them)
+        const int r0 = both ? 0 : range[0], r1 = range[1];
+        // what lies above the range and in it: the thread with its first and the one with its last bin know
+        __shared__ uint64_t at_range[3];
+        if (threadIdx.x == 0) at_range[0] = at_range[1] = at_range[2] = 0;
+        __syncthreads();
+        if (r1 >= 0 && (threadIdx.x == r0 / kOwn || threadIdx.x == r1 / kOwn)) {
+            uint64_t n = before_count, w = before_mass;
+            for (int b = threadIdx.x * kOwn; b < (static_cast<int>(threadIdx.x) + 1) * kOwn; ++b) {
+                if (b == r0) {
+                    at_range[0] = n;
+                    at_range[1] = w;
+                }
+                n += number(b);
+                w += mass_of(b);
+                if (b == r1) at_range[2] = n;
+            }
+        }
+        __syncthreads();
+        above = static_cast<uint32_t>(at_range[0]);
+        base_mass = at_range[1];
+        expected = static_cast<uint32_t>(at_range[2] - at_range[0]);
+        if (cut_k || (range[1] >= 0 && expected <= kSorted)) break;
+    }
+    __shared__ int slots[2];
+    if (threadIdx.x == 0) {
+        const int r0 = both ? 0 : range[0], r1 = range[1];
+        const bool none = r1 < 0 || r0 > r1;
+        if (none) expected = 0xffffffffu;       // digit by digit
+        st.slot_lo = slots[0] = none ? 0 : FINE ? (both ? 0 : first + r0) : r0 * kSlots;
+        st.slot_hi = slots[1] = none ? kLastSlot : FINE ? first + r1 : r1 * kSlots + kSlots - 1;
+        st.expected = both && FINE ? expected + above0 : expected;
+        st.above = both ? 0 : above0 + above;
+        st.total = total;
+        if (!cut_k) st.top_k = 0;
+        st.narrow = kListed;
+    }
+    __syncthreads();
+    // order values instead of slots; and where min_p cuts above the range, nothing else does
+    __shared__ float values[2];
+    const int lo = slots[0], hi = slots[1];
+    if (threadIdx.x == 0) values[0] = slot_begin<TYPE>(p, bin_scale, lo);
+    if (threadIdx.x == 32) values[1] = hi >= kLastSlot ? least_present<TYPE>() : slot_begin<TYPE>(p, bin_scale, hi + 1);
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    // (the bound is not known yet: until then the weight above the range, for the fine bins)
+    st.cut = {values[0], values[1], base + base_mass};
+    if (p.bound > kPresent && slot_of<TYPE>(p, bin_scale, st.min_value) < lo) {
+        st.narrow = 0;
+        st.cut = {st.min_value, st.min_value, p.bound};
     }
 }
 
-// Ranks in descending order; n a power of two.
+// Ranks in descending order, n (a power of two) of them; every warp has a part of its own, so that
+// only the few steps that are longer need the CTA's barrier.
 __device__ __forceinline__ void sort_ranks(uint64_t *x, int n) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int own = n / 2 / kDrawWarps;         // pairs of a warp
+    bool far = true;
+    __syncthreads();
     for (int size = 2; size <= n; size *= 2)
         for (int step = size / 2; step; step /= 2) {
-            __syncthreads();
-            for (int t = threadIdx.x; t < n / 2; t += kDrawThreads) {
+            const bool now = own < 32 || step > own;
+            if (now || far) __syncthreads();
+            else __syncwarp();
+            far = now;
+            const auto pair = [&](int t) {
                 const int i = 2 * t - (t & (step - 1)), j = i + step;
                 const uint64_t y = x[i], z = x[j];
                 if ((y < z) == ((i & size) == 0)) {
                     x[i] = z;
                     x[j] = y;
                 }
+            };
+            if (own < 32) {
+                if (threadIdx.x < n / 2) pair(threadIdx.x);
+            } else {
+                for (int t = lane; t < own; t += 32) pair(warp * own + t);
             }
         }
     __syncthreads();
 }
 
+// A row's list (in shared memory, room for a power of two): the rank where the filters cut, and what is
+// left of the list joins its pieces (and segments).  Returns the bound, 0 where the cut
+// does not lie in the list after all; `more` and `joined`: weight and number of what joined.
 template <int TYPE>
-__global__ void __launch_bounds__(kDrawThreads) cut_kernel(const __grid_constant__ SampleArgs a) {
+__device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, int n, const float2 *roots, uint64_t above,
+                                          uint64_t all, int head, int64_t pieces, int64_t seg_pieces, uint64_t *masses,
+                                          ulonglong2 *parts, uint64_t *sums, uint64_t &more, uint64_t &joined) {
+    constexpr int E = Entry<TYPE>::E, kOwn = kSorted / kDrawThreads;
+    const RowPlan p = st.plan;
+    int room = 2;
+    while (room < n) room *= 2;
+    for (int i = n + threadIdx.x; i < room; i += kDrawThreads) list[i] = 0;
+    sort_ranks(list, room);
+    int64_t left = n;
+    if (st.top_k > 0) {
+        left = st.top_k - static_cast<int64_t>(st.above);
+        if (left > n || left < 1) return 0;
+    }
+    // of consecutive ranks, a thread each; equal keys have equal weights
+    const int per = (n + kDrawThreads - 1) / kDrawThreads, lo = threadIdx.x * per;
+    uint64_t w[kOwn], own = 0;
+    uint32_t key = 0;
+    uint64_t same = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        w[i] = 0;
+        if (i >= per || lo + i >= n) continue;
+        const uint32_t k = static_cast<uint32_t>(list[lo + i] >> 32);
+        if (k != key) same = weight_once<TYPE>(p, roots, key_value(k));
+        key = k;
+        w[i] = same;
+        if (lo + i < left) own += same;
+    }
+    uint64_t bound = left > 0 ? list[left - 1] : kPresent;
+    if (st.top_p < 1.f) {
+        __shared__ uint64_t found;
+        if (threadIdx.x == 0) found = 0;
+        uint64_t upto = above + cta_scan(own, sums);
+        const uint64_t in = sums[kDrawWarps];
+        // of all that top_k leaves, or of all
+        uint64_t target = share(st.top_p, st.top_k > 0 ? above + in : all, true);
+        if (target == 0) target = 1;
+        if (target <= above || target > above + in) return 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            if (i >= per || lo + i >= left) continue;
+            if (upto < target && upto + w[i] >= target) found = list[lo + i];
+            upto += w[i];
+        }
+        __syncthreads();
+        bound = found;
+        if (bound == 0) return 0;
+    }
+    if (p.bound > bound) bound = p.bound;
+    uint64_t mass = 0, num = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        if (i >= per || lo + i >= n || list[lo + i] < bound) continue;
+        const int64_t e = 0xffffffffu - static_cast<uint32_t>(list[lo + i]);
+        const int64_t q = (e + head) / E / kPieceVecs;
+        if (q >= pieces) continue;      // (a workspace that others wrote to)
+        atomicAdd(reinterpret_cast<unsigned long long *>(&masses[q]), static_cast<unsigned long long>(w[i]));
+        if (parts) atomicAdd(reinterpret_cast<unsigned long long *>(&parts[q / seg_pieces].x), static_cast<unsigned long long>(w[i]));
+        mass += w[i];
+        ++num;
+    }
+    cta_scan(mass, sums);
+    more = sums[kDrawWarps];
+    cta_scan(num, sums);
+    joined = sums[kDrawWarps];
+    return bound;
+}
+
+// More equal (or nearly equal) entries than are sorted, or a cut elsewhere: digit by digit, and the
+// row's sums by this CTA, whose totals are left in the scans' last places.
+template <int TYPE>
+__device__ __noinline__ Cut by_digits(const SampleArgs &a, const Segment<TYPE> &c, const RowState &st, const RowPlan &p,
+                                      const float2 *roots, Select *sel, uint64_t *masses, ulonglong2 *parts,
+                                      int64_t pieces, uint64_t *sums, uint64_t *nums) {
     constexpr int E = Entry<TYPE>::E;
-    __shared__ uint64_t list[kSorted];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const RowCta<TYPE, kDrawThreads> cta{c.r, c.vecs, &p, roots, sel, sums, static_cast<int>(threadIdx.x)};
+    const Cut cut = {__builtin_huge_valf(), least_present<TYPE>(),
+                     bound_of<TYPE, kDrawThreads>(cta, p, st.top_k, st.top_p)};
+    uint64_t total = 0, kept = 0;
+    for (int64_t q = warp; q < pieces; q += kDrawWarps) {
+        uint64_t own = 0;
+        for (int i = 0; i < kPieceVecs / 32; ++i) {
+            const int64_t j = q * kPieceVecs + i * 32 + lane;
+            if (j >= c.vecs) break;
+            float v[E];
+            vector_values<TYPE>(c.r, j, v);
+            own += vector_weight<TYPE>(p, cut, roots, v, j * E - c.r.head);
+#pragma unroll
+            for (int k = 0; k < E; ++k) kept += is_left<TYPE>(cut, v[k], j * E - c.r.head + k);
+        }
+        total += own;
+        own = warp_sum(own);
+        if (lane == 0) __stcg(&masses[q], own);
+    }
+    if (parts) {
+        __threadfence();
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.segs; i += kDrawThreads) {
+            uint64_t own = 0;
+            for (int64_t q = i * a.seg_pieces; q < (i + 1) * a.seg_pieces && q < pieces; ++q) own += __ldcg(&masses[q]);
+            __stcg(&parts[i], make_ulonglong2(own, 0));
+        }
+    }
+    cta_scan(total, sums);
+    cta_scan(kept, nums);
+    return cut;
+}
+
+// FILTERED: rows may have lists.
+template <int TYPE, bool FILTERED>
+__global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E;
     __shared__ float2 roots[kRoots];
+    __shared__ uint64_t list[FILTERED ? kSorted : 1];
     __shared__ Select sel;
-    __shared__ uint64_t sums[kDrawWarps + 1];
-    __shared__ RowPlan plan;
+    __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
     __shared__ uint32_t listed;
     pdl_trigger();
-    make_roots<kDrawThreads>(roots);
-    pdl_wait();
-    const Segment<TYPE> c(a);
-    RowState &st = a.state[c.row];
-    if (!st.narrow) return;
-    const bool by_mass = st.top_p < 1.f, sorted = st.expected <= kSorted;
-    if (threadIdx.x == 0) {
-        plan = st.plan;
-        listed = 0;
-    }
-    __syncthreads();
-    uint64_t *to = a.segs > 1 ? a.lists + c.row * kSorted : list;
-    uint32_t *counter = a.segs > 1 ? &st.listed : &listed;
-    if (sorted) {
-        const float bin_scale = st.bin_scale;
-        const int lo = st.slot_lo, hi = st.slot_hi;
-        const RowPlan own = plan;       // (not read again behind every atomic)
-        each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, [&](const float (&v)[E], int64_t j) {
-            uint32_t in = 0;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int s = slot_of<TYPE>(own, bin_scale, v[i]);
-                if (v[i] != absent<TYPE>() && s >= lo && s <= hi) in |= 1u << i;
-            }
-            if (!in) return;
-            uint32_t at = atomicAdd(counter, static_cast<uint32_t>(__popc(in)));
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if (in >> i & 1) {
-                    if (at < kSorted) to[at] = rank_of<TYPE>(v[i], j * E - c.r.head + i);
-                    ++at;
-                }
-        });
-    }
-    if (!last_of_row(a, st, 2)) return;
-    uint64_t bound = kPresent;
-    if (sorted) {
-        const uint32_t found = a.segs > 1 ? __ldcg(&st.listed) : listed;
-        const int n = static_cast<int>(found < kSorted ? found : kSorted);
-        int room = 2;
-        while (room < n) room *= 2;
-        for (int i = threadIdx.x; i < room; i += kDrawThreads)
-            list[i] = i >= n ? 0 : a.segs > 1 ? __ldcg(&to[i]) : list[i];
-        sort_ranks(list, room);
-        int64_t left = n;
-        if (st.top_k > 0) {
-            left = st.top_k - static_cast<int64_t>(by_mass ? 0 : st.above);
-            if (left > n) left = n;
-            bound = list[left > 0 ? left - 1 : 0];
-        }
-        if (by_mass) {
-            // of consecutive ranks, a thread each
-            const int per = static_cast<int>((left + kDrawThreads - 1) / kDrawThreads);
-            const int lo = threadIdx.x * per < left ? threadIdx.x * per : static_cast<int>(left);
-            const int hi = lo + per < left ? lo + per : static_cast<int>(left);
-            uint64_t own = 0;
-            for (int i = lo; i < hi; ++i)
-                own += weight<TYPE>(plan, roots, key_value(static_cast<uint32_t>(list[i] >> 32)));
-            uint64_t upto = st.above + cta_scan(own, sums);
-            uint64_t target = share(st.top_p, st.top_k > 0 ? sums[kDrawWarps] : st.all, true);
-            if (target == 0) target = 1;
-            __shared__ uint64_t cut;
-            if (threadIdx.x == 0) cut = left > 0 ? list[left - 1] : kPresent;
-            __syncthreads();
-            for (int i = lo; i < hi; ++i) {
-                const uint64_t w = weight<TYPE>(plan, roots, key_value(static_cast<uint32_t>(list[i] >> 32)));
-                if (upto < target && upto + w >= target) cut = list[i];
-                upto += w;
-            }
-            __syncthreads();
-            bound = cut;
-        }
-    } else {
-        // more equal (or nearly equal) entries than are sorted: digit by digit
-        RowCta<TYPE, kDrawThreads> cta{c.r, c.vecs, &plan, roots, &sel, sums};
-        if (st.top_k > 0) bound = cta.template select<false>(st.top_k, bound);
-        if (by_mass) {
-            const uint64_t all = cta.template total<true>(bound), t = share(st.top_p, all, true);
-            bound = cta.template select<true>(t > 0 ? t : 1, bound);
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        st.listed = 0;
-        if (bound > plan.bound) st.plan.bound = bound;
-    }
-}
-
-template <int TYPE>
-__global__ void __launch_bounds__(kDrawThreads) sums_kernel(const __grid_constant__ SampleArgs a) {
-    constexpr int E = Entry<TYPE>::E;
-    __shared__ float2 roots[kRoots];
-    __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
-    pdl_trigger();
-    make_roots<kDrawThreads>(roots);
+    if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
+    if (threadIdx.x == 0) listed = 0;
     pdl_wait();
     const Segment<TYPE> c(a);
     RowState &st = a.state[c.row];
@@ -1026,78 +1509,185 @@ __global__ void __launch_bounds__(kDrawThreads) sums_kernel(const __grid_constan
     if (p.state != kDraw) return;
     __syncthreads();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // (on its way early: whichever CTA ends the row makes the draws)
+    const double u = a.draws <= kFewDraws && warp < a.draws ? random_number(a, c.row * a.draws + warp) : 0.0;
     uint64_t *masses = a.masses + c.row * a.pieces;
-    uint64_t total = 0, kept = 0;
+    const bool lists = FILTERED && st.narrow == kListed, sorted = !lists || st.expected <= kSorted;
+    const bool by_mass = lists && st.top_p < 1.f && st.top_k <= 0;      // the weight of all entries is wanted
+    Cut cut = st.cut;
+    uint64_t *to = a.segs > 1 ? a.lists + c.row * kSorted : list;
+    uint32_t *counter = a.segs > 1 ? &st.listed : &listed;
+    uint64_t total = 0, all = 0;
     uint32_t number = 0;
-    const uint32_t bound_key = static_cast<uint32_t>(p.bound >> 32), bound_index = 0xffffffffu - static_cast<uint32_t>(p.bound);
-    int64_t in_lo, in_hi;
-    c.r.inside_range(in_lo, in_hi);
-    for (int64_t q = c.lo / kPieceVecs + warp; q * kPieceVecs < c.hi; q += kDrawWarps) {
-        uint64_t own = 0;
-        vectors_at<TYPE, kPieceVecs / 32>(
-            c.r, in_lo, in_hi, q * kPieceVecs, (q + 1) * kPieceVecs, q * kPieceVecs + lane, 32, c.hi,
-            [&](const float (&v)[E], int64_t j) {
+    if (sorted) {
+        int64_t in_lo, in_hi;
+        c.r.inside_range(in_lo, in_hi);
+#pragma unroll 1
+        for (int64_t q = c.lo / kPieceVecs + warp; q * kPieceVecs < c.hi; q += kDrawWarps) {
+            uint64_t own = 0;
+            vectors_at<TYPE, kPieceVecs / 32>(
+                c.r, in_lo, in_hi, q * kPieceVecs, (q + 1) * kPieceVecs, q * kPieceVecs + lane, 32, c.hi,
+                [&](const float (&v)[E], int64_t j) {
+                    uint32_t in = 0;
+                    if constexpr (Entry<TYPE>::kReal) {
+                        PairSum sum, whole;
+                        uint32_t n = 0;
 #pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    const uint32_t key = order_key<TYPE>(v[k]);
-                    if (key > bound_key ||
-                        (key == bound_key && static_cast<uint32_t>(j * E - c.r.head + k) <= bound_index)) {
-                        own += weight<TYPE>(p, roots, v[k]);
-                        ++number;
+                        for (int k = 0; k < E; ++k) {
+                            const bool above = v[k] >= cut.gate, below = !(v[k] >= cut.list);
+                            n += above;
+                            if constexpr (FILTERED) in |= static_cast<uint32_t>(!above && !below) << k;
+                        }
+                        if (n || (FILTERED && by_mass)) {
+#pragma unroll (FILTERED ? 2 : 4)
+                            for (int k = 0; k < E; ++k) {
+                                if constexpr (FILTERED) {
+                                    const bool above = v[k] >= cut.gate;
+                                    const float2 w = weight_pair(p, roots, v[k], v[k] != absent<TYPE>());
+                                    sum.add(above ? w.x : 0.f, above ? w.y : 0.f);
+                                    if (by_mass) whole.add(w.x, w.y);
+                                } else {
+                                    const float2 w = weight_pair(p, roots, v[k], v[k] >= cut.gate);
+                                    sum.add(w.x, w.y);
+                                }
+                            }
+                            if (FILTERED && by_mass) all += whole.units(p.shift);
+                        }
+                        own += sum.units(p.shift) + n;
+                        number += n;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < E; ++k) {
+                            if (v[k] == absent<TYPE>()) continue;
+                            const uint64_t w = weight<TYPE>(p, roots, v[k]);
+                            all += w;
+                            if (v[k] >= cut.gate) {
+                                own += w;
+                                ++number;
+                            } else if (v[k] >= cut.list) {
+                                in |= 1u << k;
+                            }
+                        }
                     }
-                }
-            });
-        total += own;
-        own = warp_sum(own);
-        if (lane == 0) __stcg(&masses[q], own);
+                    if (!FILTERED || !lists || !in) return;
+                    uint32_t at = atomicAdd(counter, static_cast<uint32_t>(__popc(in)));
+#pragma unroll
+                    for (int k = 0; k < E; ++k)
+                        if (in >> k & 1) {
+                            if (at < kSorted) to[at] = rank_of<TYPE>(v[k], j * E - c.r.head + k);
+                            ++at;
+                        }
+                });
+            total += own;
+            own = warp_sum(own);
+            if (lane == 0) __stcg(&masses[q], own);
+        }
     }
-    kept = number;
     cta_scan(total, sums);
-    cta_scan(kept, nums);
+    cta_scan(number, nums);
     total = sums[kDrawWarps];
-    kept = nums[kDrawWarps];
-    const ulonglong2 *parts = nullptr;
+    uint64_t kept = nums[kDrawWarps];
+    if (by_mass) {
+        cta_scan(all, sums);
+        all = sums[kDrawWarps];
+    }
+    ulonglong2 *parts = nullptr;
+    const int per = static_cast<int>((a.segs + kDrawThreads - 1) / kDrawThreads), s0 = threadIdx.x * per;
     if (a.segs > 1) {
-        ulonglong2 *mine = a.partials + c.row * a.segs;
-        if (threadIdx.x == 0) __stcg(&mine[c.seg], make_ulonglong2(total, kept));
-        if (!last_of_row(a, st, 3)) return;
-        parts = mine;
-        // sums up to each segment, of consecutive ones by a thread each
-        const int per = static_cast<int>((a.segs + kDrawThreads - 1) / kDrawThreads), s0 = threadIdx.x * per;
-        total = kept = 0;
+        parts = a.partials + c.row * a.segs;
+        uint64_t *alls = a.alls + c.row * a.segs;
+        if (threadIdx.x == 0) {
+            __stcg(&parts[c.seg], make_ulonglong2(total, kept));
+            if (by_mass) __stcg(&alls[c.seg], all);
+        }
+        if (!last_of_row(a, st, 2)) return;
+        total = kept = all = 0;
         for (int i = s0; i < s0 + per && i < a.segs; ++i) {
-            const ulonglong2 x = __ldcg(&mine[i]);
+            const ulonglong2 x = __ldcg(&parts[i]);
             total += x.x;
             kept += x.y;
+            if (by_mass) all += __ldcg(&alls[i]);
         }
         cta_scan(kept, nums);
-        uint64_t upto = cta_scan(total, sums);
-        for (int i = s0; i < s0 + per && i < a.segs; ++i) {
-            const ulonglong2 x = __ldcg(&mine[i]);
-            upto += x.x;
-            __stcg(&mine[i], make_ulonglong2(upto, x.y));
-        }
-        __syncthreads();
+        cta_scan(total, sums);
         total = sums[kDrawWarps];
         kept = nums[kDrawWarps];
+        if (by_mass) {
+            cta_scan(all, sums);
+            all = sums[kDrawWarps];
+        }
     } else {
-        __syncthreads();        // the pieces' sums
+        __syncthreads();        // the pieces' sums and the list
+    }
+    const int64_t pieces = (c.vecs + kPieceVecs - 1) / kPieceVecs;
+    if constexpr (FILTERED) if (lists) {
+        uint64_t bound = 0;
+        const uint32_t found = sorted ? (a.segs > 1 ? __ldcg(&st.listed) : listed) : 0;
+        if (sorted && found <= kSorted) {
+            if (a.segs > 1) {
+                for (int i = threadIdx.x; i < found; i += kDrawThreads) list[i] = __ldcg(&to[i]);
+                __syncthreads();
+            }
+            uint64_t more = 0, joined = 0;
+            bound = cut_list<TYPE>(st, list, found, roots, total, all, c.r.head, pieces, a.seg_pieces, masses, parts, sums,
+                                   more, joined);
+            total += more;
+            kept += joined;
+            cut.bound = bound;
+        }
+        if (bound == 0) {
+            cut = by_digits<TYPE>(a, c, st, p, roots, &sel, masses, parts, pieces, sums, nums);
+            total = sums[kDrawWarps];
+            kept = nums[kDrawWarps];
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    // sums up to each segment, of consecutive ones by a thread each; log Z by another warp meanwhile
+    __shared__ uint64_t upto_segment[kDrawThreads];
+    __shared__ double z;
+    const bool few = a.segs <= kDrawThreads;
+    if (threadIdx.x == kDrawThreads - 1) z = p.greedy ? 0.0 : log_z<TYPE>(p, total);
+    if (parts) {
+        uint64_t own = 0;
+        for (int i = s0; i < s0 + per && i < a.segs; ++i) own += __ldcg(&parts[i]).x;
+        uint64_t upto = cta_scan(own, sums);
+        for (int i = s0; i < s0 + per && i < a.segs; ++i) {
+            upto += few ? own : __ldcg(&parts[i]).x;
+            if (few) upto_segment[i] = upto;
+            if (!few || a.draws > kFewDraws) __stcg(&parts[i], make_ulonglong2(upto, 0));
+        }
     }
     if (threadIdx.x == 0) {
         a.kept[c.row] = p.greedy ? 1 : static_cast<int64_t>(kept);
         st.total = total;
+        st.cut = cut;
+        st.listed = 0;
     }
+    if (!few) __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) st.z = z;
     if (a.draws > kFewDraws) return;
-    const int64_t pieces = (c.vecs + kPieceVecs - 1) / kPieceVecs;
-    for (int64_t d = warp; d < a.draws; d += kDrawWarps)
-        warp_draw<TYPE>(a, c.r, c.vecs, p, roots, masses, pieces, parts, total, c.row * a.draws + d, c.row);
+    for (int64_t d = warp; d < a.draws; d += kDrawWarps) {
+        const int64_t at = c.row * a.draws + d;
+        uint64_t target;
+        if (!aim(a, d < kDrawWarps ? u : random_number(a, at), p.greedy, total, at, c.row, target)) continue;
+        int64_t first = 0, n = pieces;
+        if (parts) {
+            first = few ? locate_upto([&](int64_t i) { return upto_segment[i]; }, a.segs, target)
+                        : locate_upto([&](int64_t i) -> uint64_t { return __ldcg(&parts[i]).x; }, a.segs, target);
+            first *= a.seg_pieces;
+            n = pieces - first < a.seg_pieces ? pieces - first : a.seg_pieces;
+        }
+        warp_draw<TYPE>(a, c.r, c.vecs, p, cut, roots, masses, first, n, target, z, at);
+    }
 }
 
 template <int TYPE>
 __global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_constant__ SampleArgs a) {
     __shared__ float2 roots[kRoots];
     pdl_trigger();
-    make_roots<kDrawThreads>(roots);
+    if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
     pdl_wait();
     __syncthreads();
     const int64_t ctas = (a.draws + kDrawWarps - 1) / kDrawWarps;
@@ -1107,16 +1697,31 @@ __global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_consta
     if (p.state != kDraw || d >= a.draws) return;
     const Row<TYPE> r(a.r, row);
     const int64_t vecs = (r.head + r.cols + Entry<TYPE>::E - 1) / Entry<TYPE>::E;
-    warp_draw<TYPE>(a, r, vecs, p, roots, a.masses + row * a.pieces, (vecs + kPieceVecs - 1) / kPieceVecs,
-                    a.segs > 1 ? a.partials + row * a.segs : nullptr, st.total, row * a.draws + d, row);
+    const int64_t at = row * a.draws + d;
+    uint64_t target;
+    if (!aim(a, random_number(a, at), p.greedy, st.total, at, row, target)) return;
+    int64_t first = 0, n = (vecs + kPieceVecs - 1) / kPieceVecs;
+    if (a.segs > 1) {
+        const ulonglong2 *parts = a.partials + row * a.segs;
+        first = locate_upto([&](int64_t i) -> uint64_t { return __ldcg(&parts[i]).x; }, a.segs, target) * a.seg_pieces;
+        n = n - first < a.seg_pieces ? n - first : a.seg_pieces;
+    }
+    warp_draw<TYPE>(a, r, vecs, p, st.cut, roots, a.masses + row * a.pieces, first, n, target, st.z, at);
 }
 
 template <int TYPE>
 cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
+    constexpr int E = Entry<TYPE>::E;
     const dim3 block(kDrawThreads);
     if (!a.state) {
-        const int64_t ctas = a.r.rows < kDrawTarget ? a.r.rows : kDrawTarget;
-        return launch_pdl(sample_rows_kernel<TYPE, kDrawThreads>, dim3(static_cast<unsigned>(ctas)), block, 0, stream, a);
+        // A warp a row where its registers hold it, or where there are rows enough for all warps
+        const bool held = (a.r.cols + E - 2 + E) / E * E <= 32 * kWarpEntries;
+        const bool warps = held || a.r.rows >= 16 * kOutSms;
+        const int64_t groups = warps ? (a.r.rows + kDrawWarps - 1) / kDrawWarps : a.r.rows;
+        const dim3 grid(static_cast<unsigned>(groups < kDrawTarget ? groups : kDrawTarget));
+        if (held) return launch_pdl(warp_rows_kernel<TYPE>, grid, block, 0, stream, a);
+        return warps ? launch_pdl(rows_kernel<TYPE, 32>, grid, block, 0, stream, a)
+                     : launch_pdl(rows_kernel<TYPE, kDrawThreads>, grid, block, 0, stream, a);
     }
     const dim3 grid(static_cast<unsigned>(a.r.rows * a.segs));
     cudaError_t e = launch_pdl(top_kernel<TYPE>, grid, block, 0, stream, a);
@@ -1124,9 +1729,10 @@ cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
         e = launch_pdl(bins_kernel<TYPE, false>, grid, block, 0, stream, a);
         if (e == cudaSuccess && a.r.cols >= kLongRow)
             e = launch_pdl(bins_kernel<TYPE, true>, grid, block, 0, stream, a);
-        if (e == cudaSuccess) e = launch_pdl(cut_kernel<TYPE>, grid, block, 0, stream, a);
     }
-    if (e == cudaSuccess) e = launch_pdl(sums_kernel<TYPE>, grid, block, 0, stream, a);
+    if (e == cudaSuccess)
+        e = a.filtered ? launch_pdl(sums_kernel<TYPE, true>, grid, block, 0, stream, a)
+                       : launch_pdl(sums_kernel<TYPE, false>, grid, block, 0, stream, a);
     if (e == cudaSuccess && a.draws > kFewDraws) {
         const int64_t ctas = a.r.rows * ((a.draws + kDrawWarps - 1) / kDrawWarps);
         e = launch_pdl(draws_kernel<TYPE>, dim3(static_cast<unsigned>(ctas)), block, 0, stream, a);

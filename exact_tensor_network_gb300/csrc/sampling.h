@@ -16,14 +16,14 @@ constexpr int kPieceVecs = 64;
 constexpr int kDrawThreads = 256;       // CTA of the kernels
 constexpr int kDrawWarps = kDrawThreads / 32;
 // Rows are cut into segments of a multiple of kDrawWarps pieces, one CTA each,
-// until that many CTAs run.
-constexpr int64_t kDrawTarget = 8 * kOutSms;
+// until that many CTAs run (as many as fit the SMs at once).
+constexpr int64_t kDrawTarget = 4 * kOutSms;
 // Rows of at most this many vectors (8 KiB) are one CTA's from end to end.
 constexpr int kRowVecs = 512;
 // Bins by which filters narrow down to the entry where they cut, the entries of
-// a bin that are sorted, and the rows from which there is a second level of bins.
-constexpr int kBins = 2048;
-constexpr int kSorted = 4096;
+// their range that are looked at one by one, and the rows from which there is a second level of bins.
+constexpr int kBins = 4096;
+constexpr int kSorted = 2048;
 constexpr int64_t kLongRow = 1 << 18;
 // Draws of a row that the CTA makes which finishes the row's sums.
 constexpr int64_t kFewDraws = 2 * kDrawWarps;
@@ -45,10 +45,11 @@ struct SampleArgs {
     int64_t segs, seg_pieces;
     uint64_t *masses;       // [rows][pieces]
     // of rows in segments: state [rows]; partial results [rows][segs] of
-    // segments, first maxima with rough sums, then sums and counts; and, of several
-    // segments, bins [rows] and lists [rows][kSorted]
+    // segments, first maxima with rough sums, then sums and counts, and sums of all
+    // entries; and, of several segments, bins [rows] and lists [rows][kSorted]
     RowState *state;
     ulonglong2 *partials;
+    uint64_t *alls;
     RowBins *bins;
     uint64_t *lists;
 };
@@ -58,7 +59,7 @@ struct Sampler {
     int64_t cols = 0, max_rows = 0;
     float scale = 1.f;
     uint64_t ws_bytes = 0, clear_bytes = 0;
-    uint64_t state_off = 0, bins_off = 0, partial_off = 0, list_off = 0, mass_off = 0;
+    uint64_t state_off = 0, bins_off = 0, partial_off = 0, rest_off = 0, list_off = 0, mass_off = 0;
     char *ws = nullptr;
     char error[256] = {0};
 };
