@@ -60,9 +60,10 @@ struct RowPlan {
     float down;         // amplitudes at beta = 1: 2^-x with weights up to 2^x
     int shift;          // a weight of 1 is 2^shift
     int down_log;       // x
-    double beta;
+    float beta;
     int state;          // kDraw, or how the row ends
     bool greedy;
+    bool unit;          // beta is 1
     uint64_t bound;     // entries of at least this rank are left
 };
 enum { kDraw = 0, kEmpty = 1, kUndefined = 2 };
@@ -123,8 +124,8 @@ __device__ __forceinline__ uint64_t in_units(float v, int shift) {
 
 // Out of line, as what follows is wherever a kernel's steady loop does not need it: a
 // kernel's first pass through its code costs more than what it computes there.
-static __device__ __noinline__ uint64_t weight_power(float v, float m, double beta, int shift) {
-    const double x = beta * log(static_cast<double>(v) / m);
+static __device__ __noinline__ uint64_t weight_power(float v, float m, float beta, int shift) {
+    const double x = static_cast<double>(beta) * log(static_cast<double>(v) / m);
     return x < -60.0 ? 1 : static_cast<uint64_t>(__double2ll_rn(ldexp(exp(x), shift)));
 }
 
@@ -133,7 +134,7 @@ __device__ __forceinline__ uint64_t weight(const RowPlan &p, const float2 *roots
     if constexpr (Entry<TYPE>::kReal) {
         return weight_real(p, roots, v);
     } else {
-        const uint64_t n = p.beta == 1.0 ? in_units(v * p.down, p.shift) : weight_power(v, p.m, p.beta, p.shift);
+        const uint64_t n = p.unit ? in_units(v * p.down, p.shift) : weight_power(v, p.m, p.beta, p.shift);
         return n > 0 ? n : 1;
     }
 }
@@ -179,8 +180,8 @@ __device__ __forceinline__ float2 weight_pair(const RowPlan &p, const float2 *ro
 template <int TYPE>
 __device__ __forceinline__ float rough_weight(const RowPlan &p, float v) {
     if constexpr (Entry<TYPE>::kReal) return ex2((v - p.m) * p.ch);
-    else if (p.beta == 1.0) return v * p.down;
-    else return ex2(static_cast<float>(p.beta) * lg2(v / p.m));
+    else if (p.unit) return v * p.down;
+    else return ex2(p.beta * lg2(v / p.m));
 }
 
 template <int TYPE>
@@ -304,6 +305,7 @@ template <int TYPE>
 __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const Filters &f) {
     p.m = m;
     p.beta = f.beta;
+    p.unit = f.beta == 1.f;
     const double c = static_cast<double>(f.beta) * 1.4426950408889634;
     p.ch = c < 3.4e38 ? static_cast<float>(c) : 3.402823466e38f;
     p.cl = c < 3.4e38 ? static_cast<float>(c - p.ch) : 0.f;
@@ -312,7 +314,7 @@ __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const 
     int x = 0;
     if (!Entry<TYPE>::kReal) frexpf(m, &x);                 // m < 2^x
     x = x < -126 ? -126 : x > 126 ? 126 : x;                // (2^-x is a number; weights may be up to 4)
-    p.down_log = x;
+    p.down_log = p.unit && !Entry<TYPE>::kReal ? x : 0;
     p.down = ldexpf(1.f, -x);
     p.shift = 0;
     p.state = !valid || m != m || m == __builtin_huge_valf() ? kUndefined : m == absent<TYPE>() ? kEmpty : kDraw;
@@ -329,30 +331,41 @@ template <int TYPE>
 __device__ __noinline__ float least_value(const RowPlan &p, float min_p) {
     double x;
     if constexpr (Entry<TYPE>::kReal) x = p.m + log(static_cast<double>(min_p)) / p.beta;
-    else if (p.beta == 1.0) x = static_cast<double>(p.m) * min_p;
+    else if (p.unit) x = static_cast<double>(p.m) * min_p;
     else x = p.m * exp(log(static_cast<double>(min_p)) / p.beta);
     float v = static_cast<float>(x);
     if (v < x) v = nextafterf(v, __builtin_huge_valf());
     return fminf(v, p.m);
 }
 
-// The logarithm of the sum of the weights left, in the logits' units (less beta times the largest
-// for logits and powers), and log p of an entry left.
+// What log p of a draw is computed from: its order value, and the row's sum of weights left.  In 64
+// bits, which a row's warp is slow at: the warps that take row after row collect a draw a lane
+// and do 32 at a time.
+struct LogP {
+    uint64_t total;
+    float v, m, beta;
+    int shift;          // weights' unit: 2^-shift of m's (of 1 for amplitudes at beta = 1)
+    bool greedy, unit;
+
+    __device__ __forceinline__ void of(const RowPlan &p, uint64_t t) {
+        total = t;
+        m = p.m;
+        beta = p.beta;
+        greedy = p.greedy;
+        unit = p.unit;
+        shift = p.shift - p.down_log;
+    }
+};
 template <int TYPE>
-__device__ __noinline__ double log_z(const RowPlan &p, uint64_t total) {
+__device__ __noinline__ float log_p(const LogP &l) {
     constexpr double kLn2d = 0.693147180559945309;
-    int units = p.shift;
-    if (!Entry<TYPE>::kReal && p.beta == 1.0) units -= p.down_log;
-    return log(static_cast<double>(total)) - units * kLn2d;
-}
-template <int TYPE>
-__device__ __noinline__ float log_p(const RowPlan &p, float v, double z) {
-    if (p.greedy) return 0.f;
+    if (l.greedy) return 0.f;
+    const double z = log(static_cast<double>(l.total));
     double x;
-    if constexpr (Entry<TYPE>::kReal) x = p.beta * (static_cast<double>(v) - p.m);
-    else if (p.beta == 1.0) x = log(static_cast<double>(v));
-    else x = p.beta * log(static_cast<double>(v) / p.m);
-    return static_cast<float>(x - z);
+    if constexpr (Entry<TYPE>::kReal) x = l.beta * (static_cast<double>(l.v) - l.m);
+    else if (l.unit) x = log(static_cast<double>(l.v));
+    else x = l.beta * log(static_cast<double>(l.v) / l.m);
+    return static_cast<float>(x - (z - l.shift * kLn2d));
 }
 
 // ---- a row of one group of threads ------------------------------------------
@@ -487,6 +500,8 @@ struct RowCta {
 struct Cut {
     float gate, list;
     uint64_t bound;
+    // (a second range for top_k, where top_p cuts far above it)
+    float gate2, list2;
 };
 template <int TYPE>
 __device__ __forceinline__ bool is_left(const Cut &c, float v, int64_t e) {
@@ -571,11 +586,10 @@ __device__ __forceinline__ void bad_draw(const SampleArgs &a, int64_t at, int64_
     a.logp[at] = __uint_as_float(0x7fc00000u);
     flag_bad_id(a.r, row);
 }
-// One thread: the draw falls into this vector, `left` behind its first entry's begin.
+// One thread: the draw falls into this vector, `left` behind its first entry's begin.  Its order value.
 template <int TYPE>
-__device__ __noinline__ void finish_draw(const SampleArgs &a, const RowPlan &p, const Cut &c, const float2 *roots,
-                                            const float (&v)[Entry<TYPE>::E], int64_t e0, uint64_t left, double z,
-                                            int64_t at) {
+__device__ __noinline__ float finish_draw(const SampleArgs &a, const RowPlan &p, const Cut &c, const float2 *roots,
+                                          const float (&v)[Entry<TYPE>::E], int64_t e0, uint64_t left, int64_t at) {
     constexpr int E = Entry<TYPE>::E;
     // (the vector's sum may be some units more than its entries': the last one's then)
     float value = 0.f;
@@ -591,15 +605,15 @@ __device__ __noinline__ void finish_draw(const SampleArgs &a, const RowPlan &p, 
         left -= w;
     }
     a.ids[at] = id;
-    a.logp[at] = log_p<TYPE>(p, value, z);
+    return value;
 }
 
 // One warp: a draw of row r that lies `target` behind the begin of piece `first`, within the next
-// `pieces`; z as log_z makes it.
+// `pieces`.  Its order value, to all lanes.
 template <int TYPE>
-__device__ __noinline__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs, const RowPlan &p, const Cut &c,
-                                       const float2 *roots, const uint64_t *masses, int64_t first, int64_t pieces,
-                                       uint64_t target, double z, int64_t at) {
+__device__ __noinline__ float warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs, const RowPlan &p, const Cut &c,
+                                        const float2 *roots, const uint64_t *masses, int64_t first, int64_t pieces,
+                                        uint64_t target, int64_t at) {
     constexpr int E = Entry<TYPE>::E;
     const int lane = threadIdx.x % 32;
     const int64_t piece = first + locate(masses + first, pieces, target);
@@ -618,9 +632,12 @@ __device__ __noinline__ void warp_draw(const SampleArgs &a, const Row<TYPE> &r, 
             target -= shfl_from(upto, 31);
             continue;
         }
-        if (lane == __ffs(over) - 1) finish_draw<TYPE>(a, p, c, roots, v, j * E - r.head, target - (upto - own), z, at);
-        return;
+        const int l = __ffs(over) - 1;
+        float value = 0.f;
+        if (lane == l) value = finish_draw<TYPE>(a, p, c, roots, v, j * E - r.head, target - (upto - own), at);
+        return __shfl_sync(0xffffffffu, value, l);
     }
+    return 0.f;
 }
 // Whether a random number is valid; what it aims at.
 __device__ __forceinline__ bool aim(const SampleArgs &a, double u, bool greedy, uint64_t total, int64_t at, int64_t row,
@@ -632,6 +649,27 @@ __device__ __forceinline__ bool aim(const SampleArgs &a, double u, bool greedy, 
     target = greedy ? 0 : share(u, total, false);
     return true;
 }
+
+// Draws of a warp whose log p is still to come, a lane each.
+template <int TYPE>
+struct Pending {
+    LogP l;
+    int64_t at;
+    int n = 0;
+
+    __device__ __forceinline__ void flush(const SampleArgs &a) {
+        if (static_cast<int>(threadIdx.x % 32) < n) a.logp[at] = log_p<TYPE>(l);
+        n = 0;
+    }
+    __device__ __forceinline__ void add(const SampleArgs &a, const RowPlan &p, uint64_t total, float v, int64_t where) {
+        if (static_cast<int>(threadIdx.x % 32) == n) {
+            l.of(p, total);
+            l.v = v;
+            at = where;
+        }
+        if (++n == 32) flush(a);
+    }
+};
 
 // Outcomes of a row that has none, by thread t of n.
 __device__ __forceinline__ void no_draws(const SampleArgs &a, int64_t row, int state, int t, int n) {
@@ -668,6 +706,7 @@ __global__ void __launch_bounds__(kDrawThreads) rows_kernel(const __grid_constan
     __syncthreads();
     const int group = threadIdx.x / NT, t = threadIdx.x % NT, warp = t / 32, lane = t % 32;
     Group<NT> g(red[group]);
+    Pending<TYPE> pending;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group; row < a.r.rows;
          row += static_cast<int64_t>(gridDim.x) * GROUPS) {
         RowPlan plan;
@@ -684,7 +723,7 @@ __global__ void __launch_bounds__(kDrawThreads) rows_kernel(const __grid_constan
             no_draws(a, row, plan.state, t, NT);
             continue;
         }
-        Cut cut = {plan.greedy ? m : least_present<TYPE>(), m, kPresent};
+        Cut cut = {plan.greedy ? m : least_present<TYPE>(), m, kPresent, 0.f, 0.f};
         if (!plan.greedy) {
             float s = 0.f;
             c.each([&](float v, int64_t) {
@@ -696,7 +735,7 @@ __global__ void __launch_bounds__(kDrawThreads) rows_kernel(const __grid_constan
                 plan.bound = static_cast<uint64_t>(order_key<TYPE>(cut.gate)) << 32;
             }
             if ((f.top_k > 0 && f.top_k < a.r.cols) || f.top_p < 1.f)
-                cut = {__builtin_huge_valf(), least_present<TYPE>(), bound_of<TYPE, NT>(c, plan, f.top_k, f.top_p)};
+                cut = {__builtin_huge_valf(), least_present<TYPE>(), bound_of<TYPE, NT>(c, plan, f.top_k, f.top_p), 0.f, 0.f};
         }
         uint64_t *masses = a.masses + row * a.pieces;
         const int64_t pieces = (c.vecs + kPieceVecs - 1) / kPieceVecs;
@@ -720,34 +759,36 @@ __global__ void __launch_bounds__(kDrawThreads) rows_kernel(const __grid_constan
         kept = c.sum(kept);
         if (t == 0) a.kept[row] = plan.greedy ? 1 : static_cast<int64_t>(kept);
         c.sync();
-        const double z = a.draws > 0 && !plan.greedy ? log_z<TYPE>(plan, total) : 0.0;
         for (int64_t d = warp; d < a.draws; d += NT / 32) {
             const int64_t at = row * a.draws + d;
             uint64_t target;
             if (aim(a, random_number(a, at), plan.greedy, total, at, row, target))
-                warp_draw<TYPE>(a, c.r, c.vecs, plan, cut, roots, masses, 0, pieces, target, z, at);
+                pending.add(a, plan, total,
+                            warp_draw<TYPE>(a, c.r, c.vecs, plan, cut, roots, masses, 0, pieces, target, at), at);
         }
         c.sync();
     }
+    pending.flush(a);
 }
 
 // ---- rows that a warp has in its registers ------------------------------------
 //
-// kWarpEntries entries a lane, whose weights are kept too.  Filters find the rank where they cut
+// N entries a lane (4 or 8 for the shortest rows, or kWarpEntries), whose weights are kept too.  Filters find the rank where they cut
 // bit by bit (how many, or how much, lies at or above it).  Bound by its chain of warp
 // reductions where rows are filtered.
 
 constexpr int kWarpEntries = 16;
 
-template <int TYPE>
-__global__ void __launch_bounds__(kDrawThreads, 2) warp_rows_kernel(const __grid_constant__ SampleArgs a) {
-    constexpr int E = Entry<TYPE>::E, V = kWarpEntries / E;
+template <int TYPE, int N>
+__global__ void __launch_bounds__(kDrawThreads, N <= 8 ? 4 : 2) warp_rows_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E, V = N / E;
     __shared__ float2 roots[kRoots];
     pdl_trigger();
     if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
     pdl_wait();
     __syncthreads();
     const int lane = threadIdx.x % 32;
+    Pending<TYPE> pending;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * kDrawWarps + threadIdx.x / 32; row < a.r.rows;
          row += static_cast<int64_t>(gridDim.x) * kDrawWarps) {
         const Row<TYPE> r(a.r, row);
@@ -898,35 +939,38 @@ __global__ void __launch_bounds__(kDrawThreads, 2) warp_rows_kernel(const __grid
             upto[i] = total + warp_scan(own, lane);
             total = shfl_from(upto[i], 31);
         }
-        const double z = a.draws > 0 && !p.greedy ? log_z<TYPE>(p, total) : 0.0;
         for (int64_t d = 0; d < a.draws; ++d) {
             const int64_t at = row * a.draws + d;
             uint64_t target;
             if (!aim(a, random_number(a, at), p.greedy, total, at, row, target)) continue;
             bool done = false;
+            float value = 0.f;
+            int from = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const uint32_t over = __ballot_sync(0xffffffffu, upto[i] > target);
                 if (done || !over) continue;
                 done = true;
-                if (lane == __ffs(over) - 1) {
-                    uint64_t before = upto[i];
+                from = __ffs(over) - 1;
+                if (lane != from) continue;
+                uint64_t before = upto[i];
 #pragma unroll
-                    for (int k = 0; k < E; ++k) before -= left >> (i * E + k) & 1 ? w[i][k] : 0;
-                    bool found = false;
+                for (int k = 0; k < E; ++k) before -= left >> (i * E + k) & 1 ? w[i][k] : 0;
+                bool found = false;
 #pragma unroll
-                    for (int k = 0; k < E; ++k) {
-                        if (found || !(left >> (i * E + k) & 1)) continue;
-                        before += w[i][k];
-                        if (before <= target) continue;
-                        found = true;
-                        a.ids[at] = index(i, k);
-                        a.logp[at] = log_p<TYPE>(p, v[i][k], z);
-                    }
+                for (int k = 0; k < E; ++k) {
+                    if (found || !(left >> (i * E + k) & 1)) continue;
+                    before += w[i][k];
+                    if (before <= target) continue;
+                    found = true;
+                    a.ids[at] = index(i, k);
+                    value = v[i][k];
                 }
             }
+            pending.add(a, p, total, __shfl_sync(0xffffffffu, value, from), at);
         }
     }
+    pending.flush(a);
 }
 
 // ---- rows in segments -------------------------------------------------------
@@ -954,8 +998,9 @@ struct RowState {
     int32_t slot_lo, slot_hi;   // slots (see slot_of) of the range
     uint32_t expected;      // its entries
     uint32_t above;         // and those above it
+    int32_t two;            // a second range, for top_k
+    uint32_t above2;        // entries above that
     uint64_t total;         // weights left
-    double z;               // log_z of them
     uint32_t arrived[3];
     uint32_t listed;
 };
@@ -1120,7 +1165,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
             }
         }
         st.plan = p;
-        st.cut = {st.min_value, st.min_value, p.bound};
+        st.cut = {st.min_value, st.min_value, p.bound, 0.f, 0.f};
         st.top_p = fmaxf(f.top_p, 0.f);
         st.top_k = f.top_k;
         // 64 bins a power of two in weight; for top_k, whose place has nothing to do with weights, 128
@@ -1218,7 +1263,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
             const float d = (FINE ? first + b + 0.5f : (b + 0.5f) * kSlots) * 128.f;
             const uint32_t top = __float_as_uint(p.m), down = static_cast<uint32_t>(d);
             const float q = down < top ? __uint_as_float(top - down) / p.m : 0.f;
-            return p.beta == 1.0 ? q : q > 0.f ? ex2(static_cast<float>(p.beta) * lg2(q)) : 0.f;
+            return p.unit ? q : q > 0.f ? ex2(p.beta * lg2(q)) : 0.f;
         }
     };
     // (rolled, and weights computed again, here and below: the streaming loop wants its registers)
@@ -1317,32 +1362,103 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
         expected = static_cast<uint32_t>(at_range[2] - at_range[0]);
         if (cut_k || (range[1] >= 0 && expected <= kSorted)) break;
     }
+    // Too many from the top to top_k's bin: a range of its own for top_p, whose whole is the weight of
+    // top_k entries, and top_k's bin as a second one where that does not reach it.
+    bool two = false;
+    int k_bin = 0;
+    uint32_t above2 = 0;
+    if (both && !FINE && expected > kSorted) {
+        k_bin = range[1];
+        __shared__ uint64_t at_bin[2];
+        if (threadIdx.x == k_bin / kOwn) {
+            uint64_t n = before_count, w = before_mass;
+            for (int b = threadIdx.x * kOwn; b < k_bin; ++b) {
+                n += number(b);
+                w += mass_of(b);
+            }
+            at_bin[0] = n;
+            at_bin[1] = w + mass_of(k_bin) / number(k_bin) * (k - n);
+        }
+        __syncthreads();
+        above2 = static_cast<uint32_t>(at_bin[0]);
+        target = share(top_p, at_bin[1], false);
+        for (int round = 0; round < 4; ++round) {
+            const uint64_t off = round == 3 ? 0 : at_bin[1] >> (10 + 2 * round);
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                range[0] = kBins;
+                range[1] = -1;
+            }
+            __syncthreads();
+            uint64_t x = before_mass, n = before_count;
+#pragma unroll 1
+            for (int i = 0; i < kOwn; ++i) {
+                const int b = threadIdx.x * kOwn + i;
+                if (b > k_bin) break;
+                const uint64_t next = x + mass_of(b);
+                if (number(b) && ((next + off >= target && x <= target + off) || b == k_bin)) {
+                    // (the range's ends with the entries before and through them)
+                    if (b < k_bin || x <= target + off) {
+                        atomicMin(&range[0], b);
+                        atomicMax(&range[1], b);
+                    }
+                }
+                x = next;
+                n += number(b);
+            }
+            __syncthreads();
+            const int r0 = range[0], r1 = range[1];
+            if (r1 < 0) continue;
+            __shared__ uint64_t ends[3];
+            if (threadIdx.x == r0 / kOwn || threadIdx.x == r1 / kOwn || threadIdx.x == k_bin / kOwn) {
+                n = before_count;
+                for (int b = threadIdx.x * kOwn; b < (static_cast<int>(threadIdx.x) + 1) * kOwn; ++b) {
+                    if (b == r0) ends[0] = n;
+                    n += number(b);
+                    if (b == r1) ends[1] = n;
+                    if (b == k_bin) ends[2] = number(b);
+                }
+            }
+            __syncthreads();
+            above = static_cast<uint32_t>(ends[0]);
+            two = r1 < k_bin;
+            expected = static_cast<uint32_t>(ends[1] - ends[0] + (two ? ends[2] : 0));
+            if (expected <= kSorted) break;
+        }
+        if (expected > kSorted) two = false;
+    }
+    const bool from_top = both && (FINE || expected > kSorted || above2 == 0);
     __shared__ int slots[2];
     if (threadIdx.x == 0) {
-        const int r0 = both ? 0 : range[0], r1 = range[1];
+        const int r0 = from_top ? 0 : range[0], r1 = range[1];
         const bool none = r1 < 0 || r0 > r1;
         if (none) expected = 0xffffffffu;       // digit by digit
-        st.slot_lo = slots[0] = none ? 0 : FINE ? (both ? 0 : first + r0) : r0 * kSlots;
+        st.slot_lo = slots[0] = none ? 0 : FINE ? (from_top ? 0 : first + r0) : r0 * kSlots;
         st.slot_hi = slots[1] = none ? kLastSlot : FINE ? first + r1 : r1 * kSlots + kSlots - 1;
         st.expected = both && FINE ? expected + above0 : expected;
-        st.above = both ? 0 : above0 + above;
+        st.above = from_top ? 0 : above0 + above;
+        st.two = two;
+        st.above2 = above2;
         st.total = total;
         if (!cut_k) st.top_k = 0;
         st.narrow = kListed;
     }
     __syncthreads();
     // order values instead of slots; and where min_p cuts above the range, nothing else does
-    __shared__ float values[2];
+    __shared__ float values[4];
     const int lo = slots[0], hi = slots[1];
-    if (threadIdx.x == 0) values[0] = slot_begin<TYPE>(p, bin_scale, lo);
-    if (threadIdx.x == 32) values[1] = hi >= kLastSlot ? least_present<TYPE>() : slot_begin<TYPE>(p, bin_scale, hi + 1);
+    if (threadIdx.x % 32 == 0 && threadIdx.x < 128) {
+        const int which = threadIdx.x / 32;
+        const int slot = which == 0 ? lo : which == 1 ? hi + 1 : (k_bin + which - 2) * kSlots;
+        values[which] = which > 1 && !two ? 0.f : slot > kLastSlot ? least_present<TYPE>() : slot_begin<TYPE>(p, bin_scale, slot);
+    }
     __syncthreads();
     if (threadIdx.x != 0) return;
     // (the bound is not known yet: until then the weight above the range, for the fine bins)
-    st.cut = {values[0], values[1], base + base_mass};
+    st.cut = {values[0], values[1], base + base_mass, values[2], values[3]};
     if (p.bound > kPresent && slot_of<TYPE>(p, bin_scale, st.min_value) < lo) {
         st.narrow = 0;
-        st.cut = {st.min_value, st.min_value, p.bound};
+        st.cut = {st.min_value, st.min_value, p.bound, 0.f, 0.f};
     }
 }
 
@@ -1389,9 +1505,22 @@ __device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, in
     while (room < n) room *= 2;
     for (int i = n + threadIdx.x; i < room; i += kDrawThreads) list[i] = 0;
     sort_ranks(list, room);
-    int64_t left = n;
-    if (st.top_k > 0) {
-        left = st.top_k - static_cast<int64_t>(st.above);
+    int64_t left = n, last = n;         // entries that top_k leaves, and among which top_p cuts
+    if (st.two) {
+        // the first range's, then as many of the second as top_k takes
+        const uint64_t end = static_cast<uint64_t>(order_key<TYPE>(st.cut.list)) << 32;
+        __shared__ int in_first;
+        if (threadIdx.x == 0) in_first = 0;
+        __syncthreads();
+        int mine = 0;
+        for (int i = threadIdx.x; i < n; i += kDrawThreads) mine += list[i] >= end;
+        atomicAdd(&in_first, mine);
+        __syncthreads();
+        last = in_first;
+        left = last + st.top_k - static_cast<int64_t>(st.above2);
+        if (left > n || left <= last) return 0;
+    } else if (st.top_k > 0) {
+        last = left = st.top_k - static_cast<int64_t>(st.above);
         if (left > n || left < 1) return 0;
     }
     // of consecutive ranks, a thread each; equal keys have equal weights
@@ -1416,12 +1545,12 @@ __device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, in
         uint64_t upto = above + cta_scan(own, sums);
         const uint64_t in = sums[kDrawWarps];
         // of all that top_k leaves, or of all
-        uint64_t target = share(st.top_p, st.top_k > 0 ? above + in : all, true);
+        uint64_t target = share(st.top_p, st.two ? above + in + all : st.top_k > 0 ? above + in : all, true);
         if (target == 0) target = 1;
         if (target <= above || target > above + in) return 0;
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
-            if (i >= per || lo + i >= left) continue;
+            if (i >= per || lo + i >= last) continue;
             if (upto < target && upto + w[i] >= target) found = list[lo + i];
             upto += w[i];
         }
@@ -1459,7 +1588,7 @@ __device__ __noinline__ Cut by_digits(const SampleArgs &a, const Segment<TYPE> &
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const RowCta<TYPE, kDrawThreads> cta{c.r, c.vecs, &p, roots, sel, sums, static_cast<int>(threadIdx.x)};
     const Cut cut = {__builtin_huge_valf(), least_present<TYPE>(),
-                     bound_of<TYPE, kDrawThreads>(cta, p, st.top_k, st.top_p)};
+                     bound_of<TYPE, kDrawThreads>(cta, p, st.top_k, st.top_p), 0.f, 0.f};
     uint64_t total = 0, kept = 0;
     for (int64_t q = warp; q < pieces; q += kDrawWarps) {
         uint64_t own = 0;
@@ -1513,7 +1642,8 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
     const double u = a.draws <= kFewDraws && warp < a.draws ? random_number(a, c.row * a.draws + warp) : 0.0;
     uint64_t *masses = a.masses + c.row * a.pieces;
     const bool lists = FILTERED && st.narrow == kListed, sorted = !lists || st.expected <= kSorted;
-    const bool by_mass = lists && st.top_p < 1.f && st.top_k <= 0;      // the weight of all entries is wanted
+    // the weight of all entries is wanted, or of those between two ranges
+    const bool two = lists && st.two, by_mass = lists && st.top_p < 1.f && (st.top_k <= 0 || two);
     Cut cut = st.cut;
     uint64_t *to = a.segs > 1 ? a.lists + c.row * kSorted : list;
     uint32_t *counter = a.segs > 1 ? &st.listed : &listed;
@@ -1523,11 +1653,13 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
         int64_t in_lo, in_hi;
         c.r.inside_range(in_lo, in_hi);
 #pragma unroll 1
-        for (int64_t q = c.lo / kPieceVecs + warp; q * kPieceVecs < c.hi; q += kDrawWarps) {
-            uint64_t own = 0;
-            vectors_at<TYPE, kPieceVecs / 32>(
-                c.r, in_lo, in_hi, q * kPieceVecs, (q + 1) * kPieceVecs, q * kPieceVecs + lane, 32, c.hi,
+        for (int64_t q = c.lo / kPieceVecs + 2 * warp; q * kPieceVecs < c.hi; q += 2 * kDrawWarps) {
+            // two pieces, their loads in flight together
+            uint64_t both[2] = {0, 0};
+            vectors_at<TYPE, 2 * kPieceVecs / 32>(
+                c.r, in_lo, in_hi, q * kPieceVecs, (q + 2) * kPieceVecs, q * kPieceVecs + lane, 32, c.hi,
                 [&](const float (&v)[E], int64_t j) {
+                    uint64_t own = 0;
                     uint32_t in = 0;
                     if constexpr (Entry<TYPE>::kReal) {
                         PairSum sum, whole;
@@ -1536,7 +1668,8 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                         for (int k = 0; k < E; ++k) {
                             const bool above = v[k] >= cut.gate, below = !(v[k] >= cut.list);
                             n += above;
-                            if constexpr (FILTERED) in |= static_cast<uint32_t>(!above && !below) << k;
+                            if constexpr (FILTERED)
+                                in |= static_cast<uint32_t>(!above && (!below || (two && v[k] < cut.gate2 && v[k] >= cut.list2))) << k;
                         }
                         if (n || (FILTERED && by_mass)) {
 #pragma unroll (FILTERED ? 2 : 4)
@@ -1545,7 +1678,8 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                                     const bool above = v[k] >= cut.gate;
                                     const float2 w = weight_pair(p, roots, v[k], v[k] != absent<TYPE>());
                                     sum.add(above ? w.x : 0.f, above ? w.y : 0.f);
-                                    if (by_mass) whole.add(w.x, w.y);
+                                    const bool counts = by_mass && (!two || (v[k] < cut.list && v[k] >= cut.gate2));
+                                    if (by_mass) whole.add(counts ? w.x : 0.f, counts ? w.y : 0.f);
                                 } else {
                                     const float2 w = weight_pair(p, roots, v[k], v[k] >= cut.gate);
                                     sum.add(w.x, w.y);
@@ -1558,17 +1692,19 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                     } else {
 #pragma unroll
                         for (int k = 0; k < E; ++k) {
-                            if (v[k] == absent<TYPE>()) continue;
+                            const bool above = v[k] >= cut.gate, below = !(v[k] >= cut.list);
+                            const bool second = FILTERED && two && v[k] < cut.gate2 && v[k] >= cut.list2;
+                            if (FILTERED && !above && (!below || second)) in |= 1u << k;
+                            const bool counts = FILTERED && by_mass && v[k] != absent<TYPE>() && (!two || (below && v[k] >= cut.gate2));
+                            if (!above && !counts) continue;
                             const uint64_t w = weight<TYPE>(p, roots, v[k]);
-                            all += w;
-                            if (v[k] >= cut.gate) {
-                                own += w;
-                                ++number;
-                            } else if (v[k] >= cut.list) {
-                                in |= 1u << k;
-                            }
+                            own += above ? w : 0;
+                            number += above;
+                            all += counts ? w : 0;
                         }
                     }
+                    both[0] += j < (q + 1) * kPieceVecs ? own : 0;
+                    both[1] += j < (q + 1) * kPieceVecs ? 0 : own;
                     if (!FILTERED || !lists || !in) return;
                     uint32_t at = atomicAdd(counter, static_cast<uint32_t>(__popc(in)));
 #pragma unroll
@@ -1578,9 +1714,13 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                             ++at;
                         }
                 });
-            total += own;
-            own = warp_sum(own);
-            if (lane == 0) __stcg(&masses[q], own);
+            total += both[0] + both[1];
+            both[0] = warp_sum(both[0]);
+            both[1] = warp_sum(both[1]);
+            if (lane == 0) {
+                __stcg(&masses[q], both[0]);
+                if ((q + 1) * kPieceVecs < c.hi) __stcg(&masses[q + 1], both[1]);
+            }
         }
     }
     cta_scan(total, sums);
@@ -1643,11 +1783,9 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
     }
     __threadfence();
     __syncthreads();
-    // sums up to each segment, of consecutive ones by a thread each; log Z by another warp meanwhile
+    // sums up to each segment, of consecutive ones by a thread each
     __shared__ uint64_t upto_segment[kDrawThreads];
-    __shared__ double z;
     const bool few = a.segs <= kDrawThreads;
-    if (threadIdx.x == kDrawThreads - 1) z = p.greedy ? 0.0 : log_z<TYPE>(p, total);
     if (parts) {
         uint64_t own = 0;
         for (int i = s0; i < s0 + per && i < a.segs; ++i) own += __ldcg(&parts[i]).x;
@@ -1666,7 +1804,6 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
     }
     if (!few) __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) st.z = z;
     if (a.draws > kFewDraws) return;
     for (int64_t d = warp; d < a.draws; d += kDrawWarps) {
         const int64_t at = c.row * a.draws + d;
@@ -1679,7 +1816,10 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
             first *= a.seg_pieces;
             n = pieces - first < a.seg_pieces ? pieces - first : a.seg_pieces;
         }
-        warp_draw<TYPE>(a, c.r, c.vecs, p, cut, roots, masses, first, n, target, z, at);
+        LogP l;
+        l.of(p, total);
+        l.v = warp_draw<TYPE>(a, c.r, c.vecs, p, cut, roots, masses, first, n, target, at);
+        if (lane == 0) a.logp[at] = log_p<TYPE>(l);
     }
 }
 
@@ -1706,7 +1846,10 @@ __global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_consta
         first = locate_upto([&](int64_t i) -> uint64_t { return __ldcg(&parts[i]).x; }, a.segs, target) * a.seg_pieces;
         n = n - first < a.seg_pieces ? n - first : a.seg_pieces;
     }
-    warp_draw<TYPE>(a, r, vecs, p, st.cut, roots, a.masses + row * a.pieces, first, n, target, st.z, at);
+    LogP l;
+    l.of(p, st.total);
+    l.v = warp_draw<TYPE>(a, r, vecs, p, st.cut, roots, a.masses + row * a.pieces, first, n, target, at);
+    if (threadIdx.x % 32 == 0) a.logp[at] = log_p<TYPE>(l);
 }
 
 template <int TYPE>
@@ -1715,11 +1858,14 @@ cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
     const dim3 block(kDrawThreads);
     if (!a.state) {
         // A warp a row where its registers hold it, or where there are rows enough for all warps
-        const bool held = (a.r.cols + E - 2 + E) / E * E <= 32 * kWarpEntries;
+        const int64_t entries = (a.r.cols + E - 2 + E) / E * E;
+        const bool held = entries <= 32 * kWarpEntries;
         const bool warps = held || a.r.rows >= 16 * kOutSms;
         const int64_t groups = warps ? (a.r.rows + kDrawWarps - 1) / kDrawWarps : a.r.rows;
         const dim3 grid(static_cast<unsigned>(groups < kDrawTarget ? groups : kDrawTarget));
-        if (held) return launch_pdl(warp_rows_kernel<TYPE>, grid, block, 0, stream, a);
+        constexpr int kFew = E == 8 ? 8 : 4;
+        if (entries <= 32 * kFew) return launch_pdl(warp_rows_kernel<TYPE, kFew>, grid, block, 0, stream, a);
+        if (held) return launch_pdl(warp_rows_kernel<TYPE, kWarpEntries>, grid, block, 0, stream, a);
         return warps ? launch_pdl(rows_kernel<TYPE, 32>, grid, block, 0, stream, a)
                      : launch_pdl(rows_kernel<TYPE, kDrawThreads>, grid, block, 0, stream, a);
     }

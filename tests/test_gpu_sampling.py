@@ -76,7 +76,8 @@ def test_sample(type_, n, filters):
 
 
 LONG = [{}, {"temperature": 0.8, "top_k": 40, "top_p": 0.95}, {"top_p": 0.9}, {"top_k": 300}, {"top_p": 0.5, "min_p": 1e-3},
-        {"temperature": 0.0}, {"top_k": 6000, "top_p": 0.9}, {"top_k": 5000}]
+        {"temperature": 0.0}, {"top_k": 6000, "top_p": 0.9}, {"top_k": 5000}, {"top_k": 9000, "top_p": 0.5, "temperature": 0.6},
+        {"top_k": 20000, "top_p": 0.997}, {"top_k": 3000, "top_p": 0.1, "min_p": 0.01}]
 
 
 @pytest.mark.parametrize("filters", LONG, ids=str)
