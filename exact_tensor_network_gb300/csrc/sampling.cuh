@@ -42,14 +42,16 @@ static __device__ const float2 kFine[32] = {
     {0x1.054072p+0f, 0x1.ff05d8p-26f}, {0x1.056dbcp+0f, -0x1.448794p-28f},
 };
 
-// 2^(k/1024), k = 0 .. 1023, in shared memory: the products of the two.
+// 2^(k/1024), k = 0 .. 1023, in shared memory: the products of the two, what a pair adds to its
+// larger number kRoots places behind that.
 constexpr int kRoots = 1024;
 template <int NT>
-__device__ __forceinline__ void make_roots(float2 *roots) {
+__device__ __forceinline__ void make_roots(float *roots) {
     for (int k = threadIdx.x; k < kRoots; k += NT) {
         const float2 c = kCoarse[k >> 5], f = kFine[k & 31];
         const float h = c.x * f.x, l = fmaf(c.x, f.x, -h) + fmaf(c.x, f.y, c.y * f.x), x = h + l;
-        roots[k] = make_float2(x, (h - x) + l);
+        roots[k] = x;
+        roots[kRoots + k] = (h - x) + l;
     }
 }
 
@@ -88,7 +90,7 @@ __device__ __forceinline__ float2 exponent(const RowPlan &p, float v) {
 // The weight of a present entry, 1 at least (so that a draw of u = 0 finds the
 // first entry left).  2^t of a pair t: 2^(k/1024) from a table, the rest (at most
 // 2^-11) by the exponential series, whose first term is kept as a pair.
-__device__ __forceinline__ uint64_t weight_real(const RowPlan &p, const float2 *roots, float v) {
+__device__ __forceinline__ uint64_t weight_real(const RowPlan &p, const float *roots, float v) {
     constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
     const float2 t = exponent(p, v);
     if (!(t.x > -64.f)) return 1;
@@ -98,7 +100,7 @@ __device__ __forceinline__ uint64_t weight_real(const RowPlan &p, const float2 *
     const float g = r * kLn2Hi;
     const float gl = fmaf(r, kLn2Hi, -g) + fmaf(r, kLn2Lo, t.y * kLn2Hi);
     const float lo = fmaf(g * g, fmaf(g, 1.f / 6, 0.5f), gl);   // 2^r - 1 = g + lo
-    const float2 root = roots[k & (kRoots - 1)];
+    const float2 root = make_float2(roots[k & (kRoots - 1)], roots[(k & (kRoots - 1)) + kRoots]);
     const float a = root.x * g, al = fmaf(root.x, g, -a);
     const float w0 = root.x + a;
     const float wm = ((root.x - w0) + a) + (al + fmaf(root.x, lo, fmaf(root.y, g, root.y)));
@@ -130,7 +132,7 @@ static __device__ __noinline__ uint64_t weight_power(float v, float m, float bet
 }
 
 template <int TYPE>
-__device__ __forceinline__ uint64_t weight(const RowPlan &p, const float2 *roots, float v) {
+__device__ __forceinline__ uint64_t weight(const RowPlan &p, const float *roots, float v) {
     if constexpr (Entry<TYPE>::kReal) {
         return weight_real(p, roots, v);
     } else {
@@ -139,41 +141,55 @@ __device__ __forceinline__ uint64_t weight(const RowPlan &p, const float2 *roots
     }
 }
 template <int TYPE>
-__device__ __noinline__ uint64_t weight_once(const RowPlan &p, const float2 *roots, float v) {
+__device__ __noinline__ uint64_t weight_once(const RowPlan &p, const float *roots, float v) {
     return weight<TYPE>(p, roots, v);
 }
 // Sums of weights as pairs of fp32 numbers, the largest weight being 1: what several
-// entries next to each other cost less by than by integers one by one.
+// entries next to each other cost less by than by integers one by one.  Two entries at a time,
+// in packed arithmetic, into two sums.
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 struct PairSum {
-    float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float h, float l) {
-        const float x = hi + h, b = x - hi;
-        lo += ((hi - (x - b)) + (h - b)) + l;
+    float2 hi = {0.f, 0.f}, lo = {0.f, 0.f};
+    __device__ __forceinline__ void add(float2 h, float2 l) {
+        const float2 x = add2(hi, h), b = sub2(x, hi);
+        lo = add2(lo, add2(add2(sub2(hi, sub2(x, b)), sub2(h, b)), l));
         hi = x;
     }
     __device__ __forceinline__ uint64_t units(int shift) const {
-        const float h = hi + lo, l = (hi - h) + lo;
-        const uint64_t a = in_units(h, shift), b = in_units(fabsf(l), shift);
-        return h > 0.f ? (l < 0.f ? a - b : l > 0.f ? a + b : a) : 0;
+        const float x = hi.x + hi.y, b = x - hi.x;
+        const float y = ((hi.x - (x - b)) + (hi.y - b)) + (lo.x + lo.y);
+        const float h = x + y, l = (x - h) + y;
+        const uint64_t u = in_units(h, shift), v = in_units(fabsf(l), shift);
+        return h > 0.f ? (l < 0.f ? u - v : l > 0.f ? u + v : u) : 0;
     }
 };
-// As weight_real, as a pair; times 0 where it does not count.
-__device__ __forceinline__ float2 weight_pair(const RowPlan &p, const float2 *roots, float v, bool counts) {
+// As weight_real, of two entries, as pairs; 0 where they do not count.
+struct Weights {
+    float2 hi, lo;
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Weights weight_pairs(const RowPlan &p, const float *roots, float v0, float v1, bool counts0,
+                                                bool counts1) {
     constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
-    const float2 t = exponent(p, counts ? v : p.m);
-    const float h = fmaxf(t.x, -100.f);
-    const float km = fmaf(h, 1024.f, kMagic), kf = __fadd_rn(km, -kMagic);
-    const uint32_t k = __float_as_uint(km) - __float_as_uint(kMagic);
-    const float r = fmaf(kf, -0x1p-10f, h);
-    const float g = r * kLn2Hi;
-    const float gl = fmaf(r, kLn2Hi, -g) + fmaf(r, kLn2Lo, t.y * kLn2Hi);
-    const float lo = fmaf(g * g, fmaf(g, 1.f / 6, 0.5f), gl);
-    const float2 root = roots[k & (kRoots - 1)];
-    const float a = root.x * g, al = fmaf(root.x, g, -a);
-    const float w = root.x + a;
-    const float wl = ((root.x - w) + a) + (al + fmaf(root.x, lo, fmaf(root.y, g, root.y)));
-    const float unit = counts ? __uint_as_float((k & ~(kRoots - 1u)) * (1u << 13) + 0x3f800000u) : 0.f;
-    return make_float2(w * unit, wl * unit);
+    const float2 v = make_float2(counts0 ? v0 : p.m, counts1 ? v1 : p.m);
+    const float2 d = add2(v, both(-p.m)), b = sub2(d, v);   // as in exponent()
+    const float2 e = add2(sub2(v, sub2(d, b)), sub2(both(-p.m), b));
+    float2 h = mul2(d, both(p.ch));
+    const float2 t = fma2(d, both(p.cl), fma2(e, both(p.ch), fma2(d, both(p.ch), mul2(d, both(-p.ch)))));
+    h = make_float2(fmaxf(h.x, -100.f), fmaxf(h.y, -100.f));
+    const float2 km = fma2(h, both(1024.f), both(kMagic)), kf = add2(km, both(-kMagic));
+    const uint32_t k0 = __float_as_uint(km.x) - __float_as_uint(kMagic), k1 = __float_as_uint(km.y) - __float_as_uint(kMagic);
+    const float2 r = fma2(kf, both(-0x1p-10f), h);
+    const float2 g = mul2(r, both(kLn2Hi)), ng = mul2(r, both(-kLn2Hi));
+    const float2 gl = add2(fma2(r, both(kLn2Hi), ng), fma2(r, both(kLn2Lo), mul2(t, both(kLn2Hi))));
+    const float2 lo = fma2(mul2(g, g), fma2(g, both(1.f / 6), both(0.5f)), gl);
+    const uint32_t i0 = k0 & (kRoots - 1), i1 = k1 & (kRoots - 1);
+    const float2 x = make_float2(roots[i0], roots[i1]), y = make_float2(roots[i0 + kRoots], roots[i1 + kRoots]);
+    const float2 a = mul2(x, g), al = fma2(x, g, mul2(x, ng)), w = add2(x, a);
+    const float2 wl = add2(add2(sub2(x, w), a), add2(al, fma2(x, lo, fma2(y, g, y))));
+    const float2 unit = make_float2(counts0 ? __uint_as_float((k0 & ~(kRoots - 1u)) * (1u << 13) + 0x3f800000u) : 0.f,
+                                    counts1 ? __uint_as_float((k1 & ~(kRoots - 1u)) * (1u << 13) + 0x3f800000u) : 0.f);
+    return {mul2(w, unit), mul2(wl, unit)};
 }
 
 // The same in fp32, relative to the largest: for an estimate of the sum.
@@ -199,7 +215,7 @@ __device__ __forceinline__ void vector_values(const Row<TYPE> &r, int64_t j, flo
     }
 }
 
-// f(order values, vector) of vectors first, first + stride, .. below hi, N at a time with
+// f(order values, vector, n) of vectors first, first + stride, .. below hi, N at a time with
 // their loads in flight together; `edge` is the first vector behind those that the
 // caller's threads read at a time (N stride further than the first of them), so that
 // they all take the same way.
@@ -219,16 +235,25 @@ __device__ __forceinline__ void vectors_at(const Row<TYPE> &r, int64_t in_lo, in
 #pragma unroll
             for (int n = 0; n < N; ++n) En::blank(q[n], keep[n]);
         }
-        // (one copy of f's code)
-#pragma unroll 1
-        for (int n = 0; n < N; ++n) {
-            uint4 x = q[0];
+        if constexpr (En::E == 2) {
 #pragma unroll
-            for (int i = 1; i < N; ++i)
-                if (n == i) x = q[i];
-            float v[En::E];
-            En::values(x, v);
-            f(v, first + n * stride);
+            for (int n = 0; n < N; ++n) {
+                float v[En::E];
+                En::values(q[n], v);
+                f(v, first + n * stride, n);
+            }
+        } else {
+            // one copy of f's code
+#pragma unroll 1
+            for (int n = 0; n < N; ++n) {
+                uint4 x = q[0];
+#pragma unroll
+                for (int i = 1; i < N; ++i)
+                    if (n == i) x = q[i];
+                float v[En::E];
+                En::values(x, v);
+                f(v, first + n * stride, n);
+            }
         }
     } else {
 #pragma unroll 1
@@ -237,7 +262,7 @@ __device__ __forceinline__ void vectors_at(const Row<TYPE> &r, int64_t in_lo, in
             if (j >= hi) break;
             float v[En::E];
             vector_values<TYPE>(r, j, v);
-            f(v, j);
+            f(v, j, n);
         }
     }
 }
@@ -424,7 +449,7 @@ struct RowCta {
     Row<TYPE> r;
     int64_t vecs;
     const RowPlan *p;
-    const float2 *roots;
+    const float *roots;
     Select *sel;
     uint64_t *sums;     // NT / 32
     int t;              // thread of the group
@@ -437,7 +462,7 @@ struct RowCta {
     // f(order value, index) of every entry of the row
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        each_vector<TYPE, NT, 1>(r, 0, vecs, t, [&](const float (&v)[E], int64_t j) {
+        each_vector<TYPE, NT, 1>(r, 0, vecs, t, [&](const float (&v)[E], int64_t j, int) {
 #pragma unroll
             for (int i = 0; i < E; ++i) f(v[i], j * E - r.head + i);
         });
@@ -516,7 +541,7 @@ __device__ __forceinline__ constexpr float least_present() {
 // Weights' sum of a vector's entries that are left, 1 at least for each: of those
 // above the gate together, of the others one by one.
 template <int TYPE>
-__device__ __noinline__ uint64_t vector_weight(const RowPlan &p, const Cut &c, const float2 *roots,
+__device__ __noinline__ uint64_t vector_weight(const RowPlan &p, const Cut &c, const float *roots,
                                                const float (&v)[Entry<TYPE>::E], int64_t e0) {
     constexpr int E = Entry<TYPE>::E;
     uint64_t own = 0;
@@ -524,12 +549,12 @@ __device__ __noinline__ uint64_t vector_weight(const RowPlan &p, const Cut &c, c
         PairSum sum;
         uint32_t n = 0, some = 0;
 #pragma unroll 1
-        for (int k = 0; k < E; ++k) {
-            const bool above = v[k] >= c.gate;
-            const float2 w = weight_pair(p, roots, v[k], above);
-            sum.add(w.x, w.y);
-            n += above;
-            some |= !above && v[k] >= c.list;
+        for (int k = 0; k < E; k += 2) {
+            const bool above = v[k] >= c.gate, above1 = v[k + 1] >= c.gate;
+            const Weights w = weight_pairs(p, roots, v[k], v[k + 1], above, above1);
+            sum.add(w.hi, w.lo);
+            n += above + above1;
+            some |= (!above && v[k] >= c.list) || (!above1 && v[k + 1] >= c.list);
         }
         own = sum.units(p.shift) + n;
         if (some) {
@@ -588,7 +613,7 @@ __device__ __forceinline__ void bad_draw(const SampleArgs &a, int64_t at, int64_
 }
 // One thread: the draw falls into this vector, `left` behind its first entry's begin.  Its order value.
 template <int TYPE>
-__device__ __noinline__ float finish_draw(const SampleArgs &a, const RowPlan &p, const Cut &c, const float2 *roots,
+__device__ __noinline__ float finish_draw(const SampleArgs &a, const RowPlan &p, const Cut &c, const float *roots,
                                           const float (&v)[Entry<TYPE>::E], int64_t e0, uint64_t left, int64_t at) {
     constexpr int E = Entry<TYPE>::E;
     // (the vector's sum may be some units more than its entries': the last one's then)
@@ -612,7 +637,7 @@ __device__ __noinline__ float finish_draw(const SampleArgs &a, const RowPlan &p,
 // `pieces`.  Its order value, to all lanes.
 template <int TYPE>
 __device__ __noinline__ float warp_draw(const SampleArgs &a, const Row<TYPE> &r, int64_t vecs, const RowPlan &p, const Cut &c,
-                                        const float2 *roots, const uint64_t *masses, int64_t first, int64_t pieces,
+                                        const float *roots, const uint64_t *masses, int64_t first, int64_t pieces,
                                         uint64_t target, int64_t at) {
     constexpr int E = Entry<TYPE>::E;
     const int lane = threadIdx.x % 32;
@@ -696,7 +721,7 @@ __device__ __noinline__ uint64_t bound_of(const RowCta<TYPE, NT> &c, const RowPl
 template <int TYPE, int NT>
 __global__ void __launch_bounds__(kDrawThreads) rows_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E, GROUPS = kDrawThreads / NT;
-    __shared__ float2 roots[kRoots];
+    __shared__ float roots[2 * kRoots];
     __shared__ Select sel[GROUPS];
     __shared__ uint64_t sums[GROUPS][NT / 32];
     __shared__ uint32_t red[GROUPS][4 * (NT / 32)];
@@ -782,7 +807,7 @@ constexpr int kWarpEntries = 16;
 template <int TYPE, int N>
 __global__ void __launch_bounds__(kDrawThreads, N <= 8 ? 4 : 2) warp_rows_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E, V = N / E;
-    __shared__ float2 roots[kRoots];
+    __shared__ float roots[2 * kRoots];
     pdl_trigger();
     if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
     pdl_wait();
@@ -1094,7 +1119,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
     // the sum relative to the largest entry so far
     const float ch = fminf(f.beta * kLog2E, 3.402823466e38f);
     float m = absent<TYPE>(), s = 0.f;
-    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t) {
+    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t, int) {
         float top = v[0];
 #pragma unroll
         for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
@@ -1222,7 +1247,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
     const uint32_t above0 = FINE ? st.above : 0;
     if (FINE && last - first >= kBins) return;
     __syncthreads();
-    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t) {
+    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t, int) {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const int s = slot_of<TYPE>(p, bin_scale, v[i]);
@@ -1496,7 +1521,7 @@ __device__ __forceinline__ void sort_ranks(uint64_t *x, int n) {
 // left of the list joins its pieces (and segments).  Returns the bound, 0 where the cut
 // does not lie in the list after all; `more` and `joined`: weight and number of what joined.
 template <int TYPE>
-__device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, int n, const float2 *roots, uint64_t above,
+__device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, int n, const float *roots, uint64_t above,
                                           uint64_t all, int head, int64_t pieces, int64_t seg_pieces, uint64_t *masses,
                                           ulonglong2 *parts, uint64_t *sums, uint64_t &more, uint64_t &joined) {
     constexpr int E = Entry<TYPE>::E, kOwn = kSorted / kDrawThreads;
@@ -1582,7 +1607,7 @@ __device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, in
 // row's sums by this CTA, whose totals are left in the scans' last places.
 template <int TYPE>
 __device__ __noinline__ Cut by_digits(const SampleArgs &a, const Segment<TYPE> &c, const RowState &st, const RowPlan &p,
-                                      const float2 *roots, Select *sel, uint64_t *masses, ulonglong2 *parts,
+                                      const float *roots, Select *sel, uint64_t *masses, ulonglong2 *parts,
                                       int64_t pieces, uint64_t *sums, uint64_t *nums) {
     constexpr int E = Entry<TYPE>::E;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -1623,7 +1648,7 @@ __device__ __noinline__ Cut by_digits(const SampleArgs &a, const Segment<TYPE> &
 template <int TYPE, bool FILTERED>
 __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E;
-    __shared__ float2 roots[kRoots];
+    __shared__ float roots[2 * kRoots];
     __shared__ uint64_t list[FILTERED ? kSorted : 1];
     __shared__ Select sel;
     __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
@@ -1658,7 +1683,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
             uint64_t both[2] = {0, 0};
             vectors_at<TYPE, 2 * kPieceVecs / 32>(
                 c.r, in_lo, in_hi, q * kPieceVecs, (q + 2) * kPieceVecs, q * kPieceVecs + lane, 32, c.hi,
-                [&](const float (&v)[E], int64_t j) {
+                [&](const float (&v)[E], int64_t j, int which) {
                     uint64_t own = 0;
                     uint32_t in = 0;
                     if constexpr (Entry<TYPE>::kReal) {
@@ -1672,17 +1697,24 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                                 in |= static_cast<uint32_t>(!above && (!below || (two && v[k] < cut.gate2 && v[k] >= cut.list2))) << k;
                         }
                         if (n || (FILTERED && by_mass)) {
-#pragma unroll (FILTERED ? 2 : 4)
-                            for (int k = 0; k < E; ++k) {
+#pragma unroll (FILTERED ? 4 : 8)
+                            for (int k = 0; k < E; k += 2) {
+                                const bool above0 = v[k] >= cut.gate, above1 = v[k + 1] >= cut.gate;
                                 if constexpr (FILTERED) {
-                                    const bool above = v[k] >= cut.gate;
-                                    const float2 w = weight_pair(p, roots, v[k], v[k] != absent<TYPE>());
-                                    sum.add(above ? w.x : 0.f, above ? w.y : 0.f);
-                                    const bool counts = by_mass && (!two || (v[k] < cut.list && v[k] >= cut.gate2));
-                                    if (by_mass) whole.add(counts ? w.x : 0.f, counts ? w.y : 0.f);
+                                    const Weights w = weight_pairs(p, roots, v[k], v[k + 1], v[k] != absent<TYPE>(),
+                                                                   v[k + 1] != absent<TYPE>());
+                                    const float2 f = make_float2(above0 ? 1.f : 0.f, above1 ? 1.f : 0.f);
+                                    sum.add(mul2(w.hi, f), mul2(w.lo, f));
+                                    if (two) {
+                                        const float2 c = make_float2(v[k] < cut.list && v[k] >= cut.gate2 ? 1.f : 0.f,
+                                                                     v[k + 1] < cut.list && v[k + 1] >= cut.gate2 ? 1.f : 0.f);
+                                        whole.add(mul2(w.hi, c), mul2(w.lo, c));
+                                    } else if (by_mass) {
+                                        whole.add(w.hi, w.lo);
+                                    }
                                 } else {
-                                    const float2 w = weight_pair(p, roots, v[k], v[k] >= cut.gate);
-                                    sum.add(w.x, w.y);
+                                    const Weights w = weight_pairs(p, roots, v[k], v[k + 1], above0, above1);
+                                    sum.add(w.hi, w.lo);
                                 }
                             }
                             if (FILTERED && by_mass) all += whole.units(p.shift);
@@ -1703,8 +1735,8 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                             all += counts ? w : 0;
                         }
                     }
-                    both[0] += j < (q + 1) * kPieceVecs ? own : 0;
-                    both[1] += j < (q + 1) * kPieceVecs ? 0 : own;
+                    both[0] += which < kPieceVecs / 32 ? own : 0;
+                    both[1] += which < kPieceVecs / 32 ? 0 : own;
                     if (!FILTERED || !lists || !in) return;
                     uint32_t at = atomicAdd(counter, static_cast<uint32_t>(__popc(in)));
 #pragma unroll
@@ -1825,31 +1857,42 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
 
 template <int TYPE>
 __global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_constant__ SampleArgs a) {
-    __shared__ float2 roots[kRoots];
+    __shared__ float roots[2 * kRoots];
     pdl_trigger();
     if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
     pdl_wait();
     __syncthreads();
     const int64_t ctas = (a.draws + kDrawWarps - 1) / kDrawWarps;
-    const int64_t row = blockIdx.x / ctas, d = (blockIdx.x - row * ctas) * kDrawWarps + threadIdx.x / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t row = blockIdx.x / ctas, d0 = (blockIdx.x - row * ctas) * kDrawWarps, d = d0 + warp;
     const RowState &st = a.state[row];
     const RowPlan p = st.plan;
-    if (p.state != kDraw || d >= a.draws) return;
-    const Row<TYPE> r(a.r, row);
-    const int64_t vecs = (r.head + r.cols + Entry<TYPE>::E - 1) / Entry<TYPE>::E;
+    if (p.state != kDraw) return;
+    __shared__ float values[kDrawWarps];
+    __shared__ bool drawn[kDrawWarps];
+    uint64_t target = 0;
     const int64_t at = row * a.draws + d;
-    uint64_t target;
-    if (!aim(a, random_number(a, at), p.greedy, st.total, at, row, target)) return;
-    int64_t first = 0, n = (vecs + kPieceVecs - 1) / kPieceVecs;
-    if (a.segs > 1) {
-        const ulonglong2 *parts = a.partials + row * a.segs;
-        first = locate_upto([&](int64_t i) -> uint64_t { return __ldcg(&parts[i]).x; }, a.segs, target) * a.seg_pieces;
-        n = n - first < a.seg_pieces ? n - first : a.seg_pieces;
+    const bool valid = d < a.draws && aim(a, random_number(a, at), p.greedy, st.total, at, row, target);
+    if (lane == 0) drawn[warp] = valid;
+    if (valid) {
+        const Row<TYPE> r(a.r, row);
+        const int64_t vecs = (r.head + r.cols + Entry<TYPE>::E - 1) / Entry<TYPE>::E;
+        int64_t first = 0, n = (vecs + kPieceVecs - 1) / kPieceVecs;
+        if (a.segs > 1) {
+            const ulonglong2 *parts = a.partials + row * a.segs;
+            first = locate_upto([&](int64_t i) -> uint64_t { return __ldcg(&parts[i]).x; }, a.segs, target) * a.seg_pieces;
+            n = n - first < a.seg_pieces ? n - first : a.seg_pieces;
+        }
+        const float v = warp_draw<TYPE>(a, r, vecs, p, st.cut, roots, a.masses + row * a.pieces, first, n, target, at);
+        if (lane == 0) values[warp] = v;
     }
-    LogP l;
-    l.of(p, st.total);
-    l.v = warp_draw<TYPE>(a, r, vecs, p, st.cut, roots, a.masses + row * a.pieces, first, n, target, at);
-    if (threadIdx.x % 32 == 0) a.logp[at] = log_p<TYPE>(l);
+    __syncthreads();
+    if (threadIdx.x < kDrawWarps && drawn[threadIdx.x]) {       // all logarithms in one warp
+        LogP l;
+        l.of(p, st.total);
+        l.v = values[threadIdx.x];
+        a.logp[row * a.draws + d0 + threadIdx.x] = log_p<TYPE>(l);
+    }
 }
 
 template <int TYPE>
