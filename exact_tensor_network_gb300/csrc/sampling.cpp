@@ -69,7 +69,7 @@ tn_status tn_sampler_create(int32_t type, int64_t cols, int64_t max_rows, float 
     s.cols = cols;
     s.max_rows = max_rows;
     s.scale = scale;
-    uint64_t at = 256;
+    const uint64_t at = 256;
     if (vectors(type, cols) > tn::kRowVecs) {
         // rows of several segments are at most half of kDrawTarget, their segments kDrawTarget
         const uint64_t cut = max_rows < tn::kDrawTarget / 2 ? max_rows : tn::kDrawTarget / 2;
@@ -78,12 +78,11 @@ tn_status tn_sampler_create(int32_t type, int64_t cols, int64_t max_rows, float 
         s.clear_bytes = s.partial_off = align(s.bins_off + cut * tn::bins_bytes());
         s.rest_off = align(s.partial_off + tn::kDrawTarget * sizeof(ulonglong2));
         s.list_off = align(s.rest_off + tn::kDrawTarget * sizeof(uint64_t));
-        at = align(s.list_off + cut * tn::kSorted * sizeof(uint64_t));
+        s.mass_off = align(s.list_off + cut * tn::kSorted * sizeof(uint64_t));
+        s.ws_bytes = align(s.mass_off + static_cast<uint64_t>(n) * 8);
     } else {
-        s.clear_bytes = at;
+        s.clear_bytes = s.ws_bytes = at;
     }
-    s.mass_off = at;
-    s.ws_bytes = align(s.mass_off + static_cast<uint64_t>(n) * 8);
     g_error[0] = 0;
     *out = h;
     return TN_OK;
@@ -166,10 +165,10 @@ tn_status tn_sampler_draw(tn_sampler_t *h, const tn_rows *r, const tn_filters *f
         a.partials = reinterpret_cast<ulonglong2 *>(s.ws + s.partial_off);
         a.alls = reinterpret_cast<uint64_t *>(s.ws + s.rest_off);
         a.lists = reinterpret_cast<uint64_t *>(s.ws + s.list_off);
+        a.masses = reinterpret_cast<uint64_t *>(s.ws + s.mass_off);
     }
     if (r->rows * (a.segs + ceil_div(draws, tn::kDrawWarps)) > 0x7fffffff)
         return fail(s.error, TN_EOVERFLOW, "too many draws or rows for one call");
-    a.masses = reinterpret_cast<uint64_t *>(s.ws + s.mass_off);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (s.type) {

@@ -87,6 +87,19 @@ __device__ __forceinline__ float2 exponent(const RowPlan &p, float v) {
     return make_float2(h, fmaf(d, p.cl, fmaf(e, p.ch, fmaf(d, p.ch, -h))));
 }
 
+// w + wl in units of 2^-44 (conversions of fp32 to 64-bit integers would run on the fp64 pipe): w,
+// below 2, to 2^-22 from the mantissa of w + 2, what is left of it with wl from that of a sum
+// with 1.5 2^23 (it is less than 2^-22); then times 2^(k / 1024 + shift).
+__device__ __forceinline__ uint64_t whole_weight(float w, float wl, int k, int shift) {
+    constexpr float kMagic = 12582912.f;
+    const float up = __fadd_rn(w, 2.f), rest = (w - __fadd_rn(up, -2.f)) + wl;
+    const int low = static_cast<int>(__float_as_uint(fmaf(rest, 0x1p44f, kMagic)) - __float_as_uint(kMagic));
+    const int64_t n = static_cast<int64_t>(static_cast<int>(__float_as_uint(up) - 0x40000000u)) * (1 << 22) + low;
+    const int x = (k >> 10) + shift - 44;
+    const uint64_t whole = x >= 0 ? static_cast<uint64_t>(n) << x : x > -64 ? static_cast<uint64_t>(n) >> -x : 0;
+    return whole > 0 ? whole : 1;
+}
+
 // The weight of a present entry, 1 at least (so that a draw of u = 0 finds the
 // first entry left).  2^t of a pair t: 2^(k/1024) from a table, the rest (at most
 // 2^-11) by the exponential series, whose first term is kept as a pair.
@@ -105,15 +118,7 @@ __device__ __forceinline__ uint64_t weight_real(const RowPlan &p, const float *r
     const float w0 = root.x + a;
     const float wm = ((root.x - w0) + a) + (al + fmaf(root.x, lo, fmaf(root.y, g, root.y)));
     const float w = w0 + wm, wl = (w0 - w) + wm;            // (t's low part makes wm up to 2^-19)
-    // w + wl in units of 2^-44 (conversions of fp32 to 64-bit integers would run on the fp64 pipe):
-    // w, below 2, to 2^-22 from the mantissa of w + 2, what is left of it with wl from
-    // that of a sum with kMagic (it is less than 2^-22)
-    const float up = __fadd_rn(w, 2.f), rest = (w - __fadd_rn(up, -2.f)) + wl;
-    const int low = static_cast<int>(__float_as_uint(fmaf(rest, 0x1p44f, kMagic)) - __float_as_uint(kMagic));
-    const int64_t n = static_cast<int64_t>(static_cast<int>(__float_as_uint(up) - 0x40000000u)) * (1 << 22) + low;
-    const int x = (k >> 10) + p.shift - 44;
-    const uint64_t whole = x >= 0 ? static_cast<uint64_t>(n) << x : x > -64 ? static_cast<uint64_t>(n) >> -x : 0;
-    return whole > 0 ? whole : 1;
+    return whole_weight(w, wl, k, p.shift);
 }
 
 // A number of 0 <= v < 4 in units of 2^-shift, the same way.
@@ -163,15 +168,14 @@ struct PairSum {
         return h > 0.f ? (l < 0.f ? u - v : l > 0.f ? u + v : u) : 0;
     }
 };
-// As weight_real, of two entries, as pairs; 0 where they do not count.
-struct Weights {
-    float2 hi, lo;
+// As weight_real, of two entries: 2^(k mod 1024 / 1024 + r) as unnormalised pairs w + wl, and k.
+struct Powers {
+    float2 w, wl;
+    uint32_t k0, k1;
 };
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ Weights weight_pairs(const RowPlan &p, const float *roots, float v0, float v1, bool counts0,
-                                                bool counts1) {
+__device__ __forceinline__ Powers powers_of(const RowPlan &p, const float *roots, float2 v) {
     constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
-    const float2 v = make_float2(counts0 ? v0 : p.m, counts1 ? v1 : p.m);
     const float2 d = add2(v, both(-p.m)), b = sub2(d, v);   // as in exponent()
     const float2 e = add2(sub2(v, sub2(d, b)), sub2(both(-p.m), b));
     float2 h = mul2(d, both(p.ch));
@@ -186,10 +190,32 @@ __device__ __forceinline__ Weights weight_pairs(const RowPlan &p, const float *r
     const uint32_t i0 = k0 & (kRoots - 1), i1 = k1 & (kRoots - 1);
     const float2 x = make_float2(roots[i0], roots[i1]), y = make_float2(roots[i0 + kRoots], roots[i1 + kRoots]);
     const float2 a = mul2(x, g), al = fma2(x, g, mul2(x, ng)), w = add2(x, a);
-    const float2 wl = add2(add2(sub2(x, w), a), add2(al, fma2(x, lo, fma2(y, g, y))));
-    const float2 unit = make_float2(counts0 ? __uint_as_float((k0 & ~(kRoots - 1u)) * (1u << 13) + 0x3f800000u) : 0.f,
-                                    counts1 ? __uint_as_float((k1 & ~(kRoots - 1u)) * (1u << 13) + 0x3f800000u) : 0.f);
-    return {mul2(w, unit), mul2(wl, unit)};
+    return {w, add2(add2(sub2(x, w), a), add2(al, fma2(x, lo, fma2(y, g, y)))), k0, k1};
+}
+// Of two entries, as pairs; 0 where they do not count.
+struct Weights {
+    float2 hi, lo;
+};
+__device__ __forceinline__ Weights weight_pairs(const RowPlan &p, const float *roots, float v0, float v1, bool counts0,
+                                                bool counts1) {
+    const Powers o = powers_of(p, roots, make_float2(counts0 ? v0 : p.m, counts1 ? v1 : p.m));
+    const float2 unit = make_float2(counts0 ? __uint_as_float((o.k0 & ~(kRoots - 1u)) * (1u << 13) + 0x3f800000u) : 0.f,
+                                    counts1 ? __uint_as_float((o.k1 & ~(kRoots - 1u)) * (1u << 13) + 0x3f800000u) : 0.f);
+    return {mul2(o.w, unit), mul2(o.wl, unit)};
+}
+// The weights of two present entries, 1 at least (so that a draw of u = 0 finds the first entry left).
+template <int TYPE>
+__device__ __forceinline__ void two_weights(const RowPlan &p, const float *roots, float v0, float v1, uint64_t &w0,
+                                            uint64_t &w1) {
+    if constexpr (Entry<TYPE>::kReal) {
+        const Powers o = powers_of(p, roots, make_float2(v0, v1));
+        const float2 w = add2(o.w, o.wl), wl = add2(sub2(o.w, w), o.wl);    // (t's low part makes o.wl up to 2^-19)
+        w0 = whole_weight(w.x, wl.x, static_cast<int>(o.k0), p.shift);
+        w1 = whole_weight(w.y, wl.y, static_cast<int>(o.k1), p.shift);
+    } else {
+        w0 = weight<TYPE>(p, roots, v0);
+        w1 = weight<TYPE>(p, roots, v1);
+    }
 }
 
 // The same in fp32, relative to the largest: for an estimate of the sum.
@@ -281,10 +307,13 @@ __device__ __forceinline__ uint64_t shfl_up(uint64_t x, int o) {
 __device__ __forceinline__ uint64_t shfl_from(uint64_t x, int lane) {
     return __shfl_sync(0xffffffffu, static_cast<unsigned long long>(x), lane);
 }
+// (parts of 27 bits, whose sums over 32 lanes fit into 32)
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(x), o);
-    return x;
+    constexpr uint32_t kPart = (1u << 27) - 1u;
+    const uint32_t a = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x) & kPart);
+    const uint32_t b = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x >> 27) & kPart);
+    const uint32_t c = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x >> 54));
+    return a + (static_cast<uint64_t>(b) << 27) + (static_cast<uint64_t>(c) << 54);
 }
 // inclusive
 __device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {
@@ -393,7 +422,7 @@ __device__ __noinline__ float log_p(const LogP &l) {
     return static_cast<float>(x - (z - l.shift * kLn2d));
 }
 
-// ---- a row of one group of threads ------------------------------------------
+// ---- a row, digit by digit ------------------------------------------
 
 struct Select {
     uint32_t lo[256], hi[256], count[256];
@@ -442,8 +471,8 @@ __device__ __noinline__ void find_digit(Select *sel, uint64_t above, uint64_t ta
     }
 }
 
-// NT threads, a warp or the CTA, that share a row.
-template <int TYPE, int NT>
+// A row that the CTA's threads share.
+template <int TYPE>
 struct RowCta {
     static constexpr int E = Entry<TYPE>::E;
     Row<TYPE> r;
@@ -451,31 +480,23 @@ struct RowCta {
     const RowPlan *p;
     const float *roots;
     Select *sel;
-    uint64_t *sums;     // NT / 32
-    int t;              // thread of the group
-
-    __device__ __forceinline__ void sync() const {
-        if constexpr (NT == 32) __syncwarp();
-        else __syncthreads();
-    }
+    uint64_t *sums;     // kDrawWarps
 
     // f(order value, index) of every entry of the row
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        each_vector<TYPE, NT, 1>(r, 0, vecs, t, [&](const float (&v)[E], int64_t j, int) {
+        each_vector<TYPE, kDrawThreads, 1>(r, 0, vecs, threadIdx.x, [&](const float (&v)[E], int64_t j, int) {
 #pragma unroll
             for (int i = 0; i < E; ++i) f(v[i], j * E - r.head + i);
         });
     }
     __device__ __forceinline__ uint64_t sum(uint64_t x) const {
         x = warp_sum(x);
-        if constexpr (NT > 32) {
-            __syncthreads();
-            if (t % 32 == 0) sums[t / 32] = x;
-            __syncthreads();
-            x = 0;
-            for (int w = 0; w < NT / 32; ++w) x += sums[w];
-        }
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = x;
+        __syncthreads();
+        x = 0;
+        for (int w = 0; w < kDrawWarps; ++w) x += sums[w];
         return x;
     }
     // Weights' sum (or the number) of the entries of at least that rank.
@@ -499,18 +520,18 @@ struct RowCta {
                 prefix |= 0xffull << 24;
                 continue;
             }
-            sync();
-            for (int i = t; i < 256; i += NT) sel->lo[i] = sel->hi[i] = sel->count[i] = 0;
-            sync();
+            __syncthreads();
+            for (int i = threadIdx.x; i < 256; i += kDrawThreads) sel->lo[i] = sel->hi[i] = sel->count[i] = 0;
+            __syncthreads();
             each([&](float v, int64_t e) {
                 const uint64_t k = rank_of<TYPE>(v, e);
                 if (k < bound || k == 0 || (shift < 56 && (k ^ prefix) >> (shift + 8))) return;
                 const int d = static_cast<int>(k >> shift & 255);
                 add_digit(sel, d, MASS ? weight_once<TYPE>(*p, roots, v) : 0, MASS);
             });
-            sync();
-            if (t < 32) find_digit<MASS>(sel, above, target);
-            sync();
+            __syncthreads();
+            if (threadIdx.x < 32) find_digit<MASS>(sel, above, target);
+            __syncthreads();
             if (sel->digit < 0) return bound;
             above = sel->above;
             prefix |= static_cast<uint64_t>(sel->digit) << shift;
@@ -705,9 +726,9 @@ __device__ __forceinline__ void no_draws(const SampleArgs &a, int64_t row, int s
     if (t == 0) a.kept[row] = 0;
 }
 
-// The filters of a row, by a group, from its plan; its pieces' sums, their total and the draws.
-template <int TYPE, int NT>
-__device__ __noinline__ uint64_t bound_of(const RowCta<TYPE, NT> &c, const RowPlan &p, int64_t top_k, float top_p) {
+// The rank where the filters of a row cut.
+template <int TYPE>
+__device__ __noinline__ uint64_t bound_of(const RowCta<TYPE> &c, const RowPlan &p, int64_t top_k, float top_p) {
     uint64_t bound = kPresent;
     if (top_k > 0 && top_k < c.r.cols) bound = c.template select<false>(top_k, bound);
     if (top_p < 1.f) {
@@ -717,105 +738,119 @@ __device__ __noinline__ uint64_t bound_of(const RowCta<TYPE, NT> &c, const RowPl
     return bound > p.bound ? bound : p.bound;
 }
 
-// Rows of a group of NT threads each (a warp, or the whole CTA), from end to end.
-template <int TYPE, int NT>
-__global__ void __launch_bounds__(kDrawThreads) rows_kernel(const __grid_constant__ SampleArgs a) {
-    constexpr int E = Entry<TYPE>::E, GROUPS = kDrawThreads / NT;
-    __shared__ float roots[2 * kRoots];
-    __shared__ Select sel[GROUPS];
-    __shared__ uint64_t sums[GROUPS][NT / 32];
-    __shared__ uint32_t red[GROUPS][4 * (NT / 32)];
-    pdl_trigger();
-    if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
-    pdl_wait();
-    __syncthreads();
-    const int group = threadIdx.x / NT, t = threadIdx.x % NT, warp = t / 32, lane = t % 32;
-    Group<NT> g(red[group]);
-    Pending<TYPE> pending;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group; row < a.r.rows;
-         row += static_cast<int64_t>(gridDim.x) * GROUPS) {
-        RowPlan plan;
-        RowCta<TYPE, NT> c{Row<TYPE>(a.r, row), 0, &plan, roots, &sel[group], sums[group], t};
-        c.vecs = (c.r.head + c.r.cols + E - 1) / E;
-        float m = absent<TYPE>();
-        c.each([&](float v, int64_t) { m = max_nan(m, v); });
-        m = g.max(m);
-        Filters f;
-        const bool valid = filters_of(a, row, f);
-        plan_row<TYPE>(plan, m, valid, f);
-        if (!valid && t == 0) flag_bad_id(a.r, row);
-        if (plan.state != kDraw) {
-            no_draws(a, row, plan.state, t, NT);
-            continue;
-        }
-        Cut cut = {plan.greedy ? m : least_present<TYPE>(), m, kPresent, 0.f, 0.f};
-        if (!plan.greedy) {
-            float s = 0.f;
-            c.each([&](float v, int64_t) {
-                if (v != absent<TYPE>()) s += rough_weight<TYPE>(plan, v);
-            });
-            plan.shift = shift_of(g.sum(s));
-            if (f.min_p > 0.f) {
-                cut.gate = least_value<TYPE>(plan, f.min_p);
-                plan.bound = static_cast<uint64_t>(order_key<TYPE>(cut.gate)) << 32;
-            }
-            if ((f.top_k > 0 && f.top_k < a.r.cols) || f.top_p < 1.f)
-                cut = {__builtin_huge_valf(), least_present<TYPE>(), bound_of<TYPE, NT>(c, plan, f.top_k, f.top_p), 0.f, 0.f};
-        }
-        uint64_t *masses = a.masses + row * a.pieces;
-        const int64_t pieces = (c.vecs + kPieceVecs - 1) / kPieceVecs;
-        uint64_t total = 0, kept = 0;
-        for (int64_t q = warp; q < pieces; q += NT / 32) {
-            uint64_t own = 0;
-            for (int i = 0; i < kPieceVecs / 32; ++i) {
-                const int64_t j = q * kPieceVecs + i * 32 + lane;
-                if (j >= c.vecs) break;
-                float v[E];
-                vector_values<TYPE>(c.r, j, v);
-                own += vector_weight<TYPE>(plan, cut, roots, v, j * E - c.r.head);
-#pragma unroll
-                for (int k = 0; k < E; ++k) kept += is_left<TYPE>(cut, v[k], j * E - c.r.head + k);
-            }
-            total += own;
-            own = warp_sum(own);
-            if (lane == 0) __stcg(&masses[q], own);
-        }
-        total = c.sum(total);
-        kept = c.sum(kept);
-        if (t == 0) a.kept[row] = plan.greedy ? 1 : static_cast<int64_t>(kept);
-        c.sync();
-        for (int64_t d = warp; d < a.draws; d += NT / 32) {
-            const int64_t at = row * a.draws + d;
-            uint64_t target;
-            if (aim(a, random_number(a, at), plan.greedy, total, at, row, target))
-                pending.add(a, plan, total,
-                            warp_draw<TYPE>(a, c.r, c.vecs, plan, cut, roots, masses, 0, pieces, target, at), at);
-        }
-        c.sync();
-    }
-    pending.flush(a);
-}
-
-// ---- rows that a warp has in its registers ------------------------------------
+// ---- rows in registers ---------------------------------------------------------
 //
-// N entries a lane (4 or 8 for the shortest rows, or kWarpEntries), whose weights are kept too.  Filters find the rank where they cut
-// bit by bit (how many, or how much, lies at or above it).  Bound by its chain of warp
-// reductions where rows are filtered.
+// N entries a thread (4 or 8 for the shortest rows, or kHeldEntries), whose weights are kept too;
+// a warp a row, or a CTA of NT threads.  Filters find where they cut by halves of the order
+// values (how many, or how much, lies at or above the middle) until one entry, or one value, is
+// left in question.  Bound by its chain of reductions where rows are filtered, by the weights'
+// arithmetic where not.
 
-constexpr int kWarpEntries = 16;
+constexpr int kHeldEntries = 16;
 
-template <int TYPE, int N>
-__global__ void __launch_bounds__(kDrawThreads, N <= 8 ? 4 : 2) warp_rows_kernel(const __grid_constant__ SampleArgs a) {
-    constexpr int E = Entry<TYPE>::E, V = N / E;
+// Sums over a warp or a CTA; of a CTA, one barrier each, with two sets of places in turn.
+template <int NT>
+struct RowGroup {
+    static constexpr int kWarps = NT / 32;
+    uint64_t *places;       // 2 * 2 * kWarps (unused by a warp)
+    int lane, warp, half = 0;
+
+    __device__ __forceinline__ uint64_t *next() {
+        half ^= 1;
+        return places + half * 2 * kWarps;
+    }
+    __device__ __forceinline__ float max(float x) {
+        x = warp_max_nan(x);
+        if constexpr (NT > 32) {
+            float *s = reinterpret_cast<float *>(next());
+            if (lane == 0) s[warp] = x;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) x = max_nan(x, s[w]);
+        }
+        return x;
+    }
+    __device__ __forceinline__ float sum(float x) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if constexpr (NT > 32) {
+            float *s = reinterpret_cast<float *>(next());
+            if (lane == 0) s[warp] = x;
+            __syncthreads();
+            x = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) x += s[w];
+        }
+        return x;
+    }
+    __device__ __forceinline__ void sum(uint64_t &x, uint32_t &n) {
+        x = warp_sum(x);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if constexpr (NT > 32) {
+            ulonglong2 *s = reinterpret_cast<ulonglong2 *>(next());
+            if (lane == 0) s[warp] = make_ulonglong2(x, n);
+            __syncthreads();
+            x = n = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const ulonglong2 y = s[w];
+                x += y.x;
+                n += static_cast<uint32_t>(y.y);
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t sum(uint32_t n) {
+        n = __reduce_add_sync(0xffffffffu, n);
+        if constexpr (NT > 32) {
+            uint32_t *s = reinterpret_cast<uint32_t *>(next());
+            if (lane == 0) s[warp] = n;
+            __syncthreads();
+            n = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) n += s[w];
+        }
+        return n;
+    }
+    // inclusive; all: the sum of all
+    __device__ __forceinline__ uint64_t scan(uint64_t x, uint64_t &all) {
+        x = warp_scan(x, lane);
+        if constexpr (NT == 32) {
+            all = shfl_from(x, 31);
+        } else {
+            uint64_t *s = next();
+            if (lane == 31) s[warp] = x;
+            __syncthreads();
+            all = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) x += s[w];
+                all += s[w];
+            }
+        }
+        return x;
+    }
+};
+
+template <int TYPE, int N, int NT>
+__global__ void __launch_bounds__(NT == 32 ? kDrawThreads : NT, (N <= 8 ? 1024 : 512) / (NT == 32 ? kDrawThreads : NT))
+held_rows_kernel(const __grid_constant__ SampleArgs a) {
+    constexpr int E = Entry<TYPE>::E, V = N / E, THREADS = NT == 32 ? kDrawThreads : NT, ROWS = THREADS / NT;
+    constexpr int WARPS = NT / 32;
+    // bits below these are the same in all order values
+    constexpr int LOWEST = TYPE == TN_TYPE_BF16 ? 16 : TYPE == TN_TYPE_F16 ? 13 : 0;
     __shared__ float roots[2 * kRoots];
+    __shared__ __align__(16) uint64_t places[4 * WARPS];
+    __shared__ float values[2][WARPS];
     pdl_trigger();
-    if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
+    if (Entry<TYPE>::kReal) make_roots<THREADS>(roots);
     pdl_wait();
     __syncthreads();
-    const int lane = threadIdx.x % 32;
+    const int t = threadIdx.x % NT, lane = t % 32, warp = t / 32;
+    RowGroup<NT> g{places, lane, warp};
+    int turn = 0;
     Pending<TYPE> pending;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kDrawWarps + threadIdx.x / 32; row < a.r.rows;
-         row += static_cast<int64_t>(gridDim.x) * kDrawWarps) {
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / NT; row < a.r.rows;
+         row += static_cast<int64_t>(gridDim.x) * ROWS) {
         const Row<TYPE> r(a.r, row);
         const int vecs = static_cast<int>((r.head + r.cols + E - 1) / E);
         Filters f;
@@ -824,8 +859,8 @@ __global__ void __launch_bounds__(kDrawThreads, N <= 8 ? 4 : 2) warp_rows_kernel
         float m = absent<TYPE>();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (32 * i + lane < vecs) {
-                vector_values<TYPE>(r, 32 * i + lane, v[i]);
+            if (NT * i + t < vecs) {
+                vector_values<TYPE>(r, NT * i + t, v[i]);
             } else {
 #pragma unroll
                 for (int k = 0; k < E; ++k) v[i][k] = absent<TYPE>();
@@ -833,12 +868,12 @@ __global__ void __launch_bounds__(kDrawThreads, N <= 8 ? 4 : 2) warp_rows_kernel
 #pragma unroll
             for (int k = 0; k < E; ++k) m = max_nan(m, v[i][k]);
         }
-        m = warp_max_nan(m);
+        m = g.max(m);
         RowPlan p;
         plan_row<TYPE>(p, m, valid, f);
-        if (!valid && lane == 0) flag_bad_id(a.r, row);
+        if (!valid && t == 0) flag_bad_id(a.r, row);
         if (p.state != kDraw) {
-            no_draws(a, row, p.state, lane, 32);
+            no_draws(a, row, p.state, t, NT);
             continue;
         }
         if (!p.greedy) {
@@ -848,151 +883,218 @@ __global__ void __launch_bounds__(kDrawThreads, N <= 8 ? 4 : 2) warp_rows_kernel
 #pragma unroll
                 for (int k = 0; k < E; ++k)
                     if (v[i][k] != absent<TYPE>()) s += rough_weight<TYPE>(p, v[i][k]);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            p.shift = shift_of(s);
+            p.shift = shift_of(g.sum(s));
         }
-        uint64_t w[V][E];
-        uint32_t left = 0;      // bit i E + k: entry k of vector i
+        uint64_t w[V][E];       // 0 of what is not left, 1 at least otherwise
+        uint64_t total = 0;     // of the row's
+        uint32_t left = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const bool here = p.greedy ? v[i][k] == m : v[i][k] != absent<TYPE>();
-                w[i][k] = here ? weight<TYPE>(p, roots, v[i][k]) : 0;
-                left |= static_cast<uint32_t>(here) << (i * E + k);
+            for (int k = 0; k < E; k += 2) {
+                two_weights<TYPE>(p, roots, v[i][k], v[i][k + 1], w[i][k], w[i][k + 1]);
+#pragma unroll
+                for (int h = k; h < k + 2; ++h) {
+                    const bool here = p.greedy ? v[i][h] == m : v[i][h] != absent<TYPE>();
+                    if (!here) {
+                        v[i][h] = absent<TYPE>();
+                        w[i][h] = 0;
+                    }
+                    total += w[i][h];
+                    left += here;
+                }
             }
-        const auto index = [&](int i, int k) { return (32 * i + lane) * E + k - r.head; };
         // keep the entries, largest first, until `target` is reached
         const auto cut = [&](uint64_t target, bool by_mass) {
-            uint32_t key = 0;
-            for (int b = 31; b >= 0; --b) {
-                const uint32_t x = key | 1u << b;
+            // the entry where it is has a key of lo <= key < hi: halves of the values between them, from a
+            // first step below the largest on; halves of the keys where those would take too long
+            constexpr uint32_t kUnit = 1u << LOWEST;
+            uint32_t lo = order_key<TYPE>(least_present<TYPE>()) & ~(kUnit - 1u);
+            uint32_t hi = (order_key<TYPE>(m) & ~(kUnit - 1u)) + kUnit;
+            uint32_t least = left, most = 0;    // entries of lo and above, of hi and above
+            uint64_t above = 0;                 // what of hi and above amounts to
+            float step = __fdiv_rn(16.f, p.beta);
+            bool under = !Entry<TYPE>::kReal;
+            for (int probes = 0; hi - lo > kUnit && least - most > 1; ++probes) {
+                float mid = 0.5f * key_value(lo) + 0.5f * key_value(hi);
+                if (!under) {
+                    mid = m - step;
+                    step *= 8.f;
+                }
+                uint32_t x = order_key<TYPE>(mid) & ~(kUnit - 1u);
+                if (x <= lo || x >= hi || probes >= 20) x = lo + ((hi - lo) / 2 & ~(kUnit - 1u));
+                const float from = key_value(x);
                 uint64_t s = 0;
                 uint32_t n = 0;
+                if (by_mass) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
+                    for (int i = 0; i < V; ++i)
 #pragma unroll
-                    for (int k = 0; k < E; ++k)
-                        if ((left >> (i * E + k) & 1) && order_key<TYPE>(v[i][k]) >= x) {
-                            s += w[i][k];
-                            ++n;
-                        }
-                s = by_mass ? warp_sum(s) : __reduce_add_sync(0xffffffffu, n);
-                if (s >= target) key = x;
+                        for (int k = 0; k < E; ++k)
+                            if (v[i][k] >= from) {
+                                s += w[i][k];
+                                ++n;
+                            }
+                    g.sum(s, n);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+#pragma unroll
+                        for (int k = 0; k < E; ++k) n += v[i][k] >= from;
+                    s = n = g.sum(n);
+                }
+                if (s >= target) {
+                    lo = x;
+                    least = n;
+                    under = true;
+                } else {
+                    hi = x;
+                    above = s;
+                    most = n;
+                }
             }
-            // of the entries of that key the first ones: `above` is what lies over them
-            uint64_t above = 0;
-            uint32_t tied = 0, next = 0;
+            // of equal entries (which have equal weights) as many as it takes, the first ones
+            uint64_t one = 0;
+            uint32_t tied = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
                 for (int k = 0; k < E; ++k) {
-                    const uint32_t bit = 1u << (i * E + k);
-                    if (!(left & bit)) continue;
                     const uint32_t o = order_key<TYPE>(v[i][k]);
-                    if (o > key) {
-                        above += by_mass ? w[i][k] : 1;
-                        next |= bit;
-                    } else if (o == key) {
-                        tied |= bit;
+                    if (o >= lo && o < hi && w[i][k] > 0) {
+                        one = by_mass ? w[i][k] : 1;
+                        tied |= 1u << (i * E + k);
+                    } else if (o < lo) {
+                        v[i][k] = absent<TYPE>();
+                        w[i][k] = 0;
                     }
                 }
-            above = warp_sum(above);
-            // equal entries have equal weights: as many as it takes
-            uint64_t one = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int k = 0; k < E; ++k)
-                    if (tied >> (i * E + k) & 1) one = by_mass ? w[i][k] : 1;
+            if (least - most <= 1) return;
+            // (one weight only: its parts are those of the largest)
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
                 const uint64_t x = __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(one), o);
                 one = x > one ? x : one;
             }
+            if constexpr (NT > 32) {
+                uint64_t *s = g.next();
+                if (lane == 0) s[warp] = one;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < WARPS; ++i) one = s[i] > one ? s[i] : one;
+            }
             uint32_t need = one > 0 && target > above ? static_cast<uint32_t>((target - above + one - 1) / one) : 0;
-            for (int i = 0; i < V && need > 0; ++i) {       // in the order of indices
+#pragma unroll
+            for (int i = 0; i < V; ++i) {       // in the order of indices
                 const uint32_t mine = __popc(tied >> (i * E) & ((1u << E) - 1u));
-                const uint32_t upto = static_cast<uint32_t>(warp_scan(mine, lane));
-                uint32_t before = upto - mine;
+                uint64_t all;
+                uint32_t before = static_cast<uint32_t>(g.scan(mine, all)) - mine;
 #pragma unroll
                 for (int k = 0; k < E; ++k)
                     if (tied >> (i * E + k) & 1) {
-                        if (before < need) next |= 1u << (i * E + k);
+                        if (before >= need) {
+                            v[i][k] = absent<TYPE>();
+                            w[i][k] = 0;
+                        }
                         ++before;
                     }
-                const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
-                need = need > all ? need - all : 0;
+                need = need > all ? need - static_cast<uint32_t>(all) : 0;
             }
-            left = next;
         };
-        const auto sum_left = [&] {
-            uint64_t s = 0;
+        // what is left after a filter
+        const auto count = [&] {
+            total = 0;
+            left = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    total += w[i][k];
+                    left += w[i][k] > 0;
+                }
+            g.sum(total, left);
+        };
+        if (!p.greedy && a.filtered) {
+            g.sum(total, left);
+            if (f.top_k > 0 && static_cast<uint32_t>(f.top_k) < left) {
+                cut(f.top_k, false);
+                count();
+            }
+            if (f.top_p < 1.f) {
+                const uint64_t x = share(fmaxf(f.top_p, 0.f), total, true);
+                cut(x > 0 ? x : 1, true);
+            }
+        }
+        if (!p.greedy && f.min_p > 0.f) {
+            const float least = least_value<TYPE>(p, f.min_p);
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
                 for (int k = 0; k < E; ++k)
-                    if (left >> (i * E + k) & 1) s += w[i][k];
-            return warp_sum(s);
-        };
-        if (!p.greedy) {
-            if (f.top_k > 0 && f.top_k < a.r.cols && __reduce_add_sync(0xffffffffu, __popc(left)) > static_cast<uint32_t>(f.top_k))
-                cut(f.top_k, false);
-            if (f.top_p < 1.f) {
-                const uint64_t t = share(fmaxf(f.top_p, 0.f), sum_left(), true);
-                cut(t > 0 ? t : 1, true);
-            }
-            if (f.min_p > 0.f) {
-                const float least = least_value<TYPE>(p, f.min_p);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int k = 0; k < E; ++k)
-                        if (v[i][k] < least) left &= ~(1u << (i * E + k));
-            }
+                    if (v[i][k] < least) w[i][k] = 0;
         }
-        const uint32_t kept = __reduce_add_sync(0xffffffffu, __popc(left));
-        if (lane == 0) a.kept[row] = p.greedy ? 1 : kept;
-        // sums up to each of the lane's vectors
-        uint64_t upto[V], total = 0;
+        left = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < E; ++k) left += w[i][k] > 0;
+        left = g.sum(left);
+        if (t == 0) a.kept[row] = p.greedy ? 1 : left;
+        // sums up to each of the thread's vectors
+        uint64_t upto[V];
+        total = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            uint64_t own = 0;
+            uint64_t own = 0, all;
 #pragma unroll
-            for (int k = 0; k < E; ++k) own += left >> (i * E + k) & 1 ? w[i][k] : 0;
-            upto[i] = total + warp_scan(own, lane);
-            total = shfl_from(upto[i], 31);
+            for (int k = 0; k < E; ++k) own += w[i][k];
+            upto[i] = total + g.scan(own, all);
+            total += all;
         }
-        for (int64_t d = 0; d < a.draws; ++d) {
-            const int64_t at = row * a.draws + d;
-            uint64_t target;
-            if (!aim(a, random_number(a, at), p.greedy, total, at, row, target)) continue;
-            bool done = false;
+        // draws, in a CTA one for each warp between two barriers: the thread that has the outcome finds it
+        for (int64_t d0 = 0; d0 < a.draws; d0 += WARPS) {
+            bool drawn = false;         // this warp's
             float value = 0.f;
-            int from = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const uint32_t over = __ballot_sync(0xffffffffu, upto[i] > target);
-                if (done || !over) continue;
-                done = true;
-                from = __ffs(over) - 1;
-                if (lane != from) continue;
-                uint64_t before = upto[i];
+            for (int j = 0; j < WARPS; ++j) {
+                if (d0 + j >= a.draws) break;
+                const int64_t at = row * a.draws + d0 + j;
+                uint64_t target;
+                const bool good = aim(a, random_number(a, at), p.greedy, total, at, row, target);
+                if (j == warp) drawn = good;
+                if (!good) continue;
+                bool owner = false;
 #pragma unroll
-                for (int k = 0; k < E; ++k) before -= left >> (i * E + k) & 1 ? w[i][k] : 0;
-                bool found = false;
+                for (int i = 0; i < V; ++i) {
+                    uint64_t own = 0;
 #pragma unroll
-                for (int k = 0; k < E; ++k) {
-                    if (found || !(left >> (i * E + k) & 1)) continue;
-                    before += w[i][k];
-                    if (before <= target) continue;
-                    found = true;
-                    a.ids[at] = index(i, k);
-                    value = v[i][k];
+                    for (int k = 0; k < E; ++k) own += w[i][k];
+                    uint64_t before = upto[i] - own;
+                    if (upto[i] <= target || before > target) continue;
+                    owner = true;
+                    bool found = false;
+#pragma unroll
+                    for (int k = 0; k < E; ++k) {
+                        before += w[i][k];
+                        if (found || before <= target) continue;
+                        found = true;
+                        a.ids[at] = (NT * i + t) * E + k - r.head;
+                        value = v[i][k];
+                    }
+                }
+                if constexpr (NT == 32) {
+                    const uint32_t who = __ballot_sync(0xffffffffu, owner);
+                    value = __shfl_sync(0xffffffffu, value, __ffs(who) - 1);
+                } else if (owner) {
+                    values[turn][j] = value;
                 }
             }
-            pending.add(a, p, total, __shfl_sync(0xffffffffu, value, from), at);
+            if constexpr (NT > 32) {
+                __syncthreads();
+                value = values[turn][warp];
+                turn ^= 1;
+            }
+            if (drawn) pending.add(a, p, total, value, row * a.draws + d0 + warp);
         }
     }
     pending.flush(a);
@@ -1611,9 +1713,9 @@ __device__ __noinline__ Cut by_digits(const SampleArgs &a, const Segment<TYPE> &
                                       int64_t pieces, uint64_t *sums, uint64_t *nums) {
     constexpr int E = Entry<TYPE>::E;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const RowCta<TYPE, kDrawThreads> cta{c.r, c.vecs, &p, roots, sel, sums, static_cast<int>(threadIdx.x)};
+    const RowCta<TYPE> cta{c.r, c.vecs, &p, roots, sel, sums};
     const Cut cut = {__builtin_huge_valf(), least_present<TYPE>(),
-                     bound_of<TYPE, kDrawThreads>(cta, p, st.top_k, st.top_p), 0.f, 0.f};
+                     bound_of<TYPE>(cta, p, st.top_k, st.top_p), 0.f, 0.f};
     uint64_t total = 0, kept = 0;
     for (int64_t q = warp; q < pieces; q += kDrawWarps) {
         uint64_t own = 0;
@@ -1895,24 +1997,33 @@ __global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_consta
     }
 }
 
+template <int TYPE, int N, int NT>
+cudaError_t launch_held(const SampleArgs &a, cudaStream_t stream) {
+    constexpr int THREADS = NT == 32 ? kDrawThreads : NT, ROWS = THREADS / NT;
+    const int64_t groups = (a.r.rows + ROWS - 1) / ROWS, most = kDrawTarget * (kDrawThreads / THREADS);
+    return launch_pdl(held_rows_kernel<TYPE, N, NT>, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(THREADS),
+                      0, stream, a);
+}
+
 template <int TYPE>
 cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
     constexpr int E = Entry<TYPE>::E;
-    const dim3 block(kDrawThreads);
     if (!a.state) {
-        // A warp a row where its registers hold it, or where there are rows enough for all warps
-        const int64_t entries = (a.r.cols + E - 2 + E) / E * E;
-        const bool held = entries <= 32 * kWarpEntries;
-        const bool warps = held || a.r.rows >= 16 * kOutSms;
-        const int64_t groups = warps ? (a.r.rows + kDrawWarps - 1) / kDrawWarps : a.r.rows;
-        const dim3 grid(static_cast<unsigned>(groups < kDrawTarget ? groups : kDrawTarget));
-        constexpr int kFew = E == 8 ? 8 : 4;
-        if (entries <= 32 * kFew) return launch_pdl(warp_rows_kernel<TYPE, kFew>, grid, block, 0, stream, a);
-        if (held) return launch_pdl(warp_rows_kernel<TYPE, kWarpEntries>, grid, block, 0, stream, a);
-        return warps ? launch_pdl(rows_kernel<TYPE, 32>, grid, block, 0, stream, a)
-                     : launch_pdl(rows_kernel<TYPE, kDrawThreads>, grid, block, 0, stream, a);
+        // a warp a row where its registers hold it, otherwise the least CTA that does
+        const bool aligned = a.r.col_stride != 1 || (reinterpret_cast<uintptr_t>(a.r.data) % 16 == 0 &&
+                                                     a.r.row_stride % E == 0);
+        const int64_t entries = (a.r.cols + (aligned ? 0 : E - 1) + E - 1) / E * E;
+        constexpr int kFew = E == 8 ? 8 : 4, N = kHeldEntries;
+        if (entries <= 32 * kFew) return launch_held<TYPE, kFew, 32>(a, stream);
+        if (entries <= 32 * N) return launch_held<TYPE, N, 32>(a, stream);
+        if (entries <= 64 * N) return launch_held<TYPE, N, 64>(a, stream);
+        if constexpr (E > 2)
+            if (entries <= 128 * N) return launch_held<TYPE, N, 128>(a, stream);
+        if constexpr (E > 4)
+            if (entries <= 256 * N) return launch_held<TYPE, N, 256>(a, stream);
+        return cudaErrorInvalidValue;       // (rows of more than kRowVecs vectors have a state)
     }
-    const dim3 grid(static_cast<unsigned>(a.r.rows * a.segs));
+    const dim3 block(kDrawThreads), grid(static_cast<unsigned>(a.r.rows * a.segs));
     cudaError_t e = launch_pdl(top_kernel<TYPE>, grid, block, 0, stream, a);
     if (e == cudaSuccess && a.filtered) {
         e = launch_pdl(bins_kernel<TYPE, false>, grid, block, 0, stream, a);
