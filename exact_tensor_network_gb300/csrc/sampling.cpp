@@ -127,15 +127,15 @@ tn_status tn_sampler_draw(tn_sampler_t *h, const tn_rows *r, const tn_filters *f
     if (r->mask && (r->mask_row_stride < 0 || r->mask_col_stride < 0))
         return fail(s.error, TN_EINVAL, "mask strides must be >= 0");
     if (draws < 0) return fail(s.error, TN_EINVAL, "draws must be >= 0");
-    if (!s.ws) return fail(s.error, TN_ENOMEM, "no workspace bound (tn_sampler_set_workspace)");
-    if (r->rows == 0) return TN_OK;
     int64_t n;
     if (__builtin_mul_overflow(r->rows, draws, &n) || n > (int64_t)1 << 40)
         return fail(s.error, TN_EOVERFLOW, "more than 2^40 draws");
-    if (!kept || (draws > 0 && (!u || !ids || !logp)))
+    if (r->rows > 0 && (!kept || (draws > 0 && (!u || !ids || !logp))))
         return fail(s.error, TN_EINVAL, "the random numbers or an output are missing");
-    if (draws > 0 && reinterpret_cast<uintptr_t>(u) % (wide ? 8 : 4))
+    if (n > 0 && reinterpret_cast<uintptr_t>(u) % (wide ? 8 : 4))
         return fail(s.error, TN_EINVAL, "the random numbers are not aligned to their type");
+    if (!s.ws) return fail(s.error, TN_ENOMEM, "no workspace bound (tn_sampler_set_workspace)");
+    if (r->rows == 0) return TN_OK;
     tn::SampleArgs a = {};
     a.r.data = static_cast<const char *>(r->data);
     a.r.rows = r->rows;

@@ -59,6 +59,7 @@ __device__ __forceinline__ void make_roots(float *roots) {
 struct RowPlan {
     float m;            // largest order value
     float ch, cl;       // beta log2(e) as a pair
+    float low;          // lower order values weigh as much (next to nothing)
     float down;         // amplitudes at beta = 1: 2^-x with weights up to 2^x
     int shift;          // a weight of 1 is 2^shift
     int down_log;       // x
@@ -105,8 +106,7 @@ __device__ __forceinline__ uint64_t whole_weight(float w, float wl, int k, int s
 // 2^-11) by the exponential series, whose first term is kept as a pair.
 __device__ __forceinline__ uint64_t weight_real(const RowPlan &p, const float *roots, float v) {
     constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
-    const float2 t = exponent(p, v);
-    if (!(t.x > -64.f)) return 1;
+    const float2 t = exponent(p, fmaxf(v, p.low));
     const float km = fmaf(t.x, 1024.f, kMagic), kf = __fadd_rn(km, -kMagic);
     const int k = static_cast<int>(__float_as_uint(km) - __float_as_uint(kMagic));
     const float r = fmaf(kf, -0x1p-10f, t.x);               // exact
@@ -176,11 +176,11 @@ struct Powers {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ Powers powers_of(const RowPlan &p, const float *roots, float2 v) {
     constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
+    v = make_float2(fmaxf(v.x, p.low), fmaxf(v.y, p.low));
     const float2 d = add2(v, both(-p.m)), b = sub2(d, v);   // as in exponent()
     const float2 e = add2(sub2(v, sub2(d, b)), sub2(both(-p.m), b));
-    float2 h = mul2(d, both(p.ch));
+    const float2 h = mul2(d, both(p.ch));
     const float2 t = fma2(d, both(p.cl), fma2(e, both(p.ch), fma2(d, both(p.ch), mul2(d, both(-p.ch)))));
-    h = make_float2(fmaxf(h.x, -100.f), fmaxf(h.y, -100.f));
     const float2 km = fma2(h, both(1024.f), both(kMagic)), kf = add2(km, both(-kMagic));
     const uint32_t k0 = __float_as_uint(km.x) - __float_as_uint(kMagic), k1 = __float_as_uint(km.y) - __float_as_uint(kMagic);
     const float2 r = fma2(kf, both(-0x1p-10f), h);
@@ -363,6 +363,16 @@ __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const 
     const double c = static_cast<double>(f.beta) * 1.4426950408889634;
     p.ch = c < 3.4e38 ? static_cast<float>(c) : 3.402823466e38f;
     p.cl = c < 3.4e38 ? static_cast<float>(c - p.ch) : 0.f;
+    // With this the number next to m weighs 2^-124 .. 2^-62: less than a unit already, and what the
+    // tables and fp32's exponents reach
+    const float most = __fdiv_rn(62.f * 0x1p24f, fabsf(m));
+    if (p.ch > most) {
+        p.ch = most;
+        p.cl = 0.f;
+    }
+    // (2^-60 .. 2^-120, where m's neighbours are few; differences beyond fp32 count as the largest number)
+    p.low = fmaxf(fminf(m - __fdiv_rn(90.f, p.ch), nextafterf(m, -__builtin_huge_valf())),
+                  fmaxf(m, 0.f) - 3.402823466e38f);
     p.greedy = f.greedy;
     p.bound = kPresent;
     int x = 0;

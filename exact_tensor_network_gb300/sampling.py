@@ -218,6 +218,8 @@ class Sampler:
             raise ValueError(f"u must be a contiguous tensor [{R}] or [{R}, draws] on the rows' device")
         draws = ushape[1] if len(ushape) == 2 else 1
         f.temperature, f.temperatures = self._parameter(temperature, 1.0, "temperature", self._f32, R, device)
+        if isinstance(top_k, int):
+            top_k = max(0, min(top_k, self.cols))       # (a larger number would wrap around)
         f.top_k, f.top_ks = self._parameter(top_k, 0, "top_k", torch.int32, R, device)
         f.top_p, f.top_ps = self._parameter(top_p, 1.0, "top_p", self._f32, R, device)
         f.min_p, f.min_ps = self._parameter(min_p, 0.0, "min_p", self._f32, R, device)

@@ -7,7 +7,9 @@
  * Definitions.  Logits z, absent entries and rows without a distribution are
  * those of tn_outcomes.h.
  *   - With beta = scale / temperature (one fp32 division; a quotient beyond fp32
- *     counts as the largest number) a present entry's weight is exp(beta z).
+ *     counts as the largest number) a present entry's weight is exp(beta z), relative to
+ *     the largest (of which logits that are further from it than fp32 reaches count as
+ *     that far).
  *   - Three filters follow each other.  top_k: the entries of largest z (largest
  *     w for amplitudes), ties to the lowest index.  top_p: of those, in that
  *     order, the fewest whose weight is at least top_p times that of all of
