@@ -53,9 +53,15 @@ SIGNATURES = {
 }
 
 
+_L = None           # the library, looked up once: small calls cost what their host side costs
+
+
 def _lib():
-    from . import lib
-    return lib()
+    global _L
+    if _L is None:
+        from . import lib
+        _L = lib()
+    return _L
 
 
 def _check(st: int) -> None:
@@ -102,58 +108,62 @@ class Blocks8(NamedTuple):
         return c * s.repeat_interleave(TN_BLOCK8, 1)[:, :c.shape[1]]
 
 
-_TYPES = None       # torch dtype -> TN_TYPE_*
+_TORCH = _TYPES = _F8 = _F32 = None     # torch, torch dtype -> TN_TYPE_*, two of its types
 
 
 def _types():
-    global _TYPES
+    global _TORCH, _TYPES, _F8, _F32
     if _TYPES is None:
         import torch
+        _TORCH, _F8, _F32 = torch, torch.float8_e4m3fn, torch.float32
         _TYPES = {torch.float32: TN_TYPE_F32, torch.bfloat16: TN_TYPE_BF16, torch.float16: TN_TYPE_F16}
     return _TYPES
 
 
 def _matrix(t, name) -> tn_matrix:
-    import torch
     type_ = _types().get(t.dtype)
-    if type_ is None or not t.is_cuda or t.dim() != 2:
+    shape = t.shape
+    if type_ is None or not t.is_cuda or len(shape) != 2:
         raise ValueError(f"{name} must be a 2-dimensional float32, bfloat16 or float16 CUDA tensor")
     if t.is_neg():
         raise ValueError(f"{name} is a lazily negated view: resolve it first")
-    if t.device.index != torch._C._cuda_getDevice():
+    if t.device.index != _TORCH._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return tn_matrix(t.data_ptr(), type_, t.shape[0], t.shape[1], t.stride(0), t.stride(1))
+    return tn_matrix(t.data_ptr(), type_, *shape, *t.stride())
 
 
 def _blocks(b, name, device) -> tn_block8:
-    import torch
+    _types()
     codes, scales, powers = b
-    if codes.dtype is not torch.float8_e4m3fn or codes.dim() != 2 or codes.device != device:
+    shape, sshape = codes.shape, scales.shape
+    if codes.dtype is not _F8 or len(shape) != 2 or codes.device != device:
         raise ValueError(f"codes of {name} must be a 2-dimensional float8_e4m3fn tensor on the other operands' device")
-    R, C = codes.shape
-    if C > 1 and codes.stride(1) != 1:
+    R, C = shape
+    stride, step = codes.stride()
+    if C > 1 and step != 1:
         raise ValueError(f"rows of the codes of {name} must be contiguous")
     blocks = -(-C // TN_BLOCK8)
-    if scales.dtype is not torch.float32 or scales.device != device or scales.dim() != 2 or scales.is_neg():
+    if scales.dtype is not _F32 or scales.device != device or len(sshape) != 2 or scales.is_neg():
         raise ValueError(f"scales of {name} must be a float32 matrix on the codes' device")
-    if tuple(scales.shape) == (R, blocks):
-        tall = 1
-    elif tuple(scales.shape) == (-(-R // TN_BLOCK8), blocks):
-        tall = TN_BLOCK8
-    else:
-        raise ValueError(f"scales of {name} must be [{R}, {blocks}] or [{-(-R // TN_BLOCK8)}, {blocks}], "
-                         f"not {tuple(scales.shape)}")
+    tall = -(-R // TN_BLOCK8)
+    if sshape[1] != blocks or (sshape[0] != R and sshape[0] != tall):
+        raise ValueError(f"scales of {name} must be [{R}, {blocks}] or [{tall}, {blocks}], not {tuple(sshape)}")
     # one row, or empty ones, have no stride of their own
-    stride = codes.stride(0) if R > 1 and C > 0 else -(-C // 16) * 16
-    return tn_block8(codes.data_ptr(), scales.data_ptr(), R, C, stride, scales.stride(0) if scales.shape[0] > 1 else 1,
-                     scales.stride(1) if blocks > 1 else 1, tall, 1 if powers else 0)
+    if R <= 1 or C == 0:
+        stride = -(-C // 16) * 16
+    row, block = scales.stride()
+    return tn_block8(codes.data_ptr(), scales.data_ptr(), R, C, stride, row if sshape[0] > 1 else 1,
+                     block if blocks > 1 else 1, 1 if sshape[0] == R else TN_BLOCK8, 1 if powers else 0)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _stream(device, stream, tensors):
     """(stream handle, what makes tensors on it)."""
-    import torch
+    torch = _TORCH
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index), contextlib.nullcontext()
+        return torch._C._cuda_getCurrentRawStream(device.index), _HERE
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     elif getattr(stream, "device", device) != device:
@@ -164,24 +174,27 @@ def _stream(device, stream, tensors):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _new(R, C, square, device) -> Blocks8:
-    import torch
-    codes = torch.empty((R, -(-C // 16) * 16), dtype=torch.float8_e4m3fn, device=device)
-    if codes.shape[1] != C:
-        codes = codes[:, :C]
-    blocks = -(-C // TN_BLOCK8)
+def _new(R, C, square, device):
+    """(a new matrix, its tn_block8)."""
+    stride, blocks = -(-C // 16) * 16, -(-C // TN_BLOCK8)
+    codes = _TORCH.empty((R, stride), dtype=_F8, device=device)
     if square:
-        return Blocks8(codes, torch.empty((-(-R // TN_BLOCK8), blocks), dtype=torch.float32, device=device))
-    return Blocks8(codes, torch.empty((blocks, R), dtype=torch.float32, device=device).t())
+        tall = -(-R // TN_BLOCK8)
+        scales = _TORCH.empty((tall, blocks), dtype=_F32, device=device)
+        row, block = max(blocks, 1), 1
+    else:
+        scales = _TORCH.empty_strided((R, blocks), (1, max(R, 1)), dtype=_F32, device=device)
+        row, block = 1, max(R, 1)
+    b = tn_block8(codes.data_ptr(), scales.data_ptr(), R, C, stride, row, block, TN_BLOCK8 if square else 1, 1)
+    return Blocks8(codes if stride == C else codes[:, :C], scales), b
 
 
 class _Scratch:
     """Codes and scales of a call's own, in one allocation."""
 
     def __init__(self, R, C, device):
-        import torch
         stride, blocks = -(-C // 16) * 16, -(-C // TN_BLOCK8)
-        self.memory = torch.empty(R * (stride + 4 * blocks), dtype=torch.uint8, device=device)
+        self.memory = _TORCH.empty(R * (stride + 4 * blocks), dtype=_TORCH.uint8, device=device)
         p = self.memory.data_ptr()
         self.blocks = tn_block8(p, p + R * stride, R, C, stride, 1, max(R, 1), 1, 1)
 
@@ -196,37 +209,34 @@ def quantize8(x, square: bool = False, layout: str = "rows", out=None, stream=No
         raise ValueError("layout must be rows, columns or both")
     m, dev = _matrix(x, "x"), x.device
     R, C = x.shape
-    given = () if out is None else out if layout == "both" else (out,)
-    sp, on = _stream(dev, stream, (x, *(t for b in given for t in b[:2])))
+    shapes = ((R, C),) if layout == "rows" else ((C, R),) if layout == "columns" else ((R, C), (C, R))
+    given = () if out is None else tuple(out) if layout == "both" else (out,)
+    sp, on = _stream(dev, stream, (x, *(t for b in given for t in b[:2])) if stream is not None else ())
     if out is None:
         with on:
-            given = tuple(_new(*shape, square, dev) for want, shape in (("rows", (R, C)), ("columns", (C, R)))
-                          if layout in (want, "both"))
-    made = []
-    for b, shape in zip(given, [(R, C), (C, R)] if layout != "columns" else [(C, R)]):
-        s = _blocks(b, "out", dev)
-        if tuple(b.codes.shape) != shape or tuple(b.scales.shape)[0] != (-(-shape[0] // TN_BLOCK8) if square
-                                                                         else shape[0]):
-            raise ValueError("out does not have the result's shapes")
-        s.block_rows = TN_BLOCK8 if square else 1
-        if not b.powers:
-            raise ValueError("out is marked as having other scales than powers of two")
-        made.append(s)
+            given, made = zip(*(_new(*shape, square, dev) for shape in shapes))
+    else:
+        made = [_blocks(b, "out", dev) for b in given]
+        for b, o, shape in zip(given, made, shapes):
+            if (o.rows, o.cols) != shape or b.scales.shape[0] != (-(-shape[0] // TN_BLOCK8) if square else shape[0]):
+                raise ValueError("out does not have the result's shapes")
+            if not b.powers:
+                raise ValueError("out is marked as having other scales than powers of two")
+            o.block_rows = TN_BLOCK8 if square else 1
     st = _lib().tn_block8_quantize(m, made[0] if layout != "columns" else None,
                                    made[-1] if layout != "rows" else None, sp)
     if st:
         _check(st)
-    return tuple(given) if layout == "both" else given[0]
+    return given if layout == "both" else given[0]
 
 
 def _out(out, shape, dtype, device, on):
-    import torch
-    dtype = dtype or (out.dtype if out is not None else torch.bfloat16)
+    dtype = dtype or (out.dtype if out is not None else _TORCH.bfloat16)
     if dtype not in _types():
         raise ValueError("dtype must be float32, bfloat16 or float16")
     if out is None:
         with on:
-            return torch.empty(shape, dtype=dtype, device=device)
+            return _TORCH.empty(shape, dtype=dtype, device=device)
     if tuple(out.shape) != shape or out.dtype is not dtype or out.device != device:
         raise ValueError(f"out must be a {dtype} tensor of shape {shape} on the operands' device")
     if out.is_neg() or (shape[1] > 1 and out.stride(1) != 1) or (shape[0] > 1 and out.stride(0) < shape[1]):
@@ -244,12 +254,12 @@ def _product(a: tn_block8, b: tn_block8, out, sp):
 def product8(a: Blocks8, b: Blocks8, dtype=None, out=None, stream=None):
     """``a b^T`` ([m, n], ``dtype`` float32, bfloat16 (default) or float16) of quantised
     [m, k] and [n, k]."""
-    import torch
+    _types()
     dev = a.codes.device
-    if dev.type != "cuda" or dev.index != torch._C._cuda_getDevice():
+    if dev.type != "cuda" or dev.index != _TORCH._C._cuda_getDevice():
         raise ValueError(f"a is on {dev}, which is not the current device")
     A, B = _blocks(a, "a", dev), _blocks(b, "b", dev)
-    sp, on = _stream(dev, stream, (*a[:2], *b[:2], out))
+    sp, on = _stream(dev, stream, (*a[:2], *b[:2], out) if stream is not None else ())
     out = _out(out, (A.rows, B.rows), dtype, dev, on)
     _product(A, B, out, sp)
     return out
@@ -262,7 +272,7 @@ def linear8(x, w: Blocks8, dtype=None, out=None, stream=None):
     W = _blocks(w, "w", dev)
     if W.cols != m.cols:
         raise ValueError(f"x has {m.cols} columns, w {W.cols}")
-    sp, on = _stream(dev, stream, (x, *w[:2], out))
+    sp, on = _stream(dev, stream, (x, *w[:2], out) if stream is not None else ())
     out = _out(out, (m.rows, W.rows), dtype or (out.dtype if out is not None else x.dtype), dev, on)
     with on:
         q = _Scratch(m.rows, m.cols, dev)
@@ -279,7 +289,6 @@ def linear8_grad(x, dy, w: Blocks8, dtype=None, stream=None):
     ``quantize8(weight, square=True, layout="columns")`` makes it.  dx = Q(dy) W;
     dW = Q'(dy)^T Q'(x) with x and dy quantised along their rows' number (which is
     taken as having no gradient of its own)."""
-    import torch
     X, Y, dev = _matrix(x, "x"), _matrix(dy, "dy"), x.device
     W = _blocks(w, "w", dev)
     R, k, n = X.rows, X.cols, Y.cols
@@ -288,7 +297,7 @@ def linear8_grad(x, dy, w: Blocks8, dtype=None, stream=None):
                          f"{tuple(x.shape)}, {tuple(dy.shape)} and {tuple(w.codes.shape)}")
     sp, on = _stream(dev, stream, (x, dy, *w[:2]))
     dx = _out(None, (R, k), x.dtype, dev, on)
-    dw = _out(None, (n, k), dtype or torch.float32, dev, on)
+    dw = _out(None, (n, k), dtype or _F32, dev, on)
     with on:
         qy, qyt, qxt = _Scratch(R, n, dev), _Scratch(n, R, dev), _Scratch(k, R, dev)
     L = _lib()
