@@ -58,8 +58,12 @@ __device__ __forceinline__ void make_roots(float *roots) {
 // What a row's weights are computed from.
 struct RowPlan {
     float m;            // largest order value
-    float ch, cl;       // beta log2(e) as a pair
+    float b;            // beta, as large as weights need it
+    float ch;           // b log2(e), for estimates
     float low;          // lower order values weigh as much (next to nothing)
+    float origin;       // weights are relative to m (far) or to e^(origin ln 2 / 1024), which is near m's
+    uint32_t first;     // what a rounded exponent's bits less this are the power of
+    bool far;
     float down;         // amplitudes at beta = 1: 2^-x with weights up to 2^x
     int shift;          // a weight of 1 is 2^shift
     int down_log;       // x
@@ -80,19 +84,13 @@ __device__ __forceinline__ uint64_t rank_of(float v, int64_t e) {
     return k ? static_cast<uint64_t>(k) << 32 | (0xffffffffu - static_cast<uint32_t>(e)) : 0;
 }
 
-// beta log2(e) (v - m) as a pair of fp32 numbers.
-__device__ __forceinline__ float2 exponent(const RowPlan &p, float v) {
-    const float d = v - p.m, b = d - v;                     // d + e is the exact difference
-    const float e = (v - (d - b)) + (-p.m - b);
-    const float h = d * p.ch;
-    return make_float2(h, fmaf(d, p.cl, fmaf(e, p.ch, fmaf(d, p.ch, -h))));
-}
+// ln 2 / 1024 as a pair, and 1.5 2^23, which rounds what it is added to.
+constexpr float kStepHi = 0x1.62e43p-11f, kStepLo = -0x1.05c61p-39f, kMagic = 12582912.f;
 
 // w + wl in units of 2^-44 (conversions of fp32 to 64-bit integers would run on the fp64 pipe): w,
 // below 2, to 2^-22 from the mantissa of w + 2, what is left of it with wl from that of a sum
 // with 1.5 2^23 (it is less than 2^-22); then times 2^(k / 1024 + shift).
 __device__ __forceinline__ uint64_t whole_weight(float w, float wl, int k, int shift) {
-    constexpr float kMagic = 12582912.f;
     const float up = __fadd_rn(w, 2.f), rest = (w - __fadd_rn(up, -2.f)) + wl;
     const int low = static_cast<int>(__float_as_uint(fmaf(rest, 0x1p44f, kMagic)) - __float_as_uint(kMagic));
     const int64_t n = static_cast<int64_t>(static_cast<int>(__float_as_uint(up) - 0x40000000u)) * (1 << 22) + low;
@@ -101,24 +99,38 @@ __device__ __forceinline__ uint64_t whole_weight(float w, float wl, int k, int s
     return whole > 0 ? whole : 1;
 }
 
-// The weight of a present entry, 1 at least (so that a draw of u = 0 finds the
-// first entry left).  2^t of a pair t: 2^(k/1024) from a table, the rest (at most
-// 2^-11) by the exponential series, whose first term is kept as a pair.
-__device__ __forceinline__ uint64_t weight_real(const RowPlan &p, const float *roots, float v) {
-    constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
-    const float2 t = exponent(p, fmaxf(v, p.low));
-    const float km = fmaf(t.x, 1024.f, kMagic), kf = __fadd_rn(km, -kMagic);
-    const int k = static_cast<int>(__float_as_uint(km) - __float_as_uint(kMagic));
-    const float r = fmaf(kf, -0x1p-10f, t.x);               // exact
-    const float g = r * kLn2Hi;
-    const float gl = fmaf(r, kLn2Hi, -g) + fmaf(r, kLn2Lo, t.y * kLn2Hi);
-    const float lo = fmaf(g * g, fmaf(g, 1.f / 6, 0.5f), gl);   // 2^r - 1 = g + lo
-    const float2 root = make_float2(roots[k & (kRoots - 1)], roots[(k & (kRoots - 1)) + kRoots]);
-    const float a = root.x * g, al = fmaf(root.x, g, -a);
-    const float w0 = root.x + a;
-    const float wm = ((root.x - w0) + a) + (al + fmaf(root.x, lo, fmaf(root.y, g, root.y)));
-    const float w = w0 + wm, wl = (w0 - w) + wm;            // (t's low part makes wm up to 2^-19)
-    return whole_weight(w, wl, k, p.shift);
+// The weights of two present entries, e^(b v) relative to the row's origin, to some 2^-44: 2^(k / 1024)
+// e^r from a table and the exponential series, |r| <= ln 2 / 2048.  As unnormalised pairs w + wl without
+// the whole part of k / 1024, and k.  Packed fp32 (a pair's operations cost what two single ones do);
+// the origin on the grid of the table leaves no difference v - m to be taken, which rows whose |b m| is
+// large need (`far`: b v would be known to fewer bits).
+struct Powers {
+    float2 w, wl;
+    uint32_t k0, k1;
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, both(-1.f), a); }
+__device__ __forceinline__ Powers powers_of(const RowPlan &p, const float *roots, float2 v) {
+    v = make_float2(fmaxf(v.x, p.low), fmaxf(v.y, p.low));
+    float2 h, l;                                            // b v (or b (v - m)) as a pair
+    if (p.far) {
+        const float2 d = add2(v, both(-p.m)), b = sub2(d, v);
+        const float2 e = add2(sub2(v, sub2(d, b)), sub2(both(-p.m), b));    // d + e is the exact difference
+        h = mul2(d, both(p.b));
+        l = fma2(e, both(p.b), fma2(d, both(p.b), mul2(d, both(-p.b))));
+    } else {
+        h = mul2(v, both(p.b));
+        l = fma2(v, both(p.b), mul2(v, both(-p.b)));
+    }
+    const float2 km = fma2(h, both(0x1.71547652b82fep+10f), both(kMagic)), kf = add2(km, both(-kMagic));
+    const uint32_t k0 = __float_as_uint(km.x) - p.first, k1 = __float_as_uint(km.y) - p.first;
+    const float2 q = fma2(kf, both(-kStepHi), h), ql = fma2(kf, both(-kStepLo), l);     // (the first exact)
+    const float2 r = add2(q, ql), rl = add2(sub2(q, r), ql);
+    const float2 lo = fma2(mul2(r, r), fma2(r, both(1.f / 6), both(0.5f)), rl);     // e^r - 1 = r + lo
+    const uint32_t i0 = k0 & (kRoots - 1), i1 = k1 & (kRoots - 1);
+    const float2 x = make_float2(roots[i0], roots[i1]), y = make_float2(roots[i0 + kRoots], roots[i1 + kRoots]);
+    const float2 a = mul2(x, r), al = fma2(x, r, mul2(x, mul2(r, both(-1.f)))), w = add2(x, a);
+    return {w, add2(add2(sub2(x, w), a), add2(al, fma2(x, lo, fma2(y, r, y)))), k0, k1};
 }
 
 // A number of 0 <= v < 4 in units of 2^-shift, the same way.
@@ -139,7 +151,9 @@ static __device__ __noinline__ uint64_t weight_power(float v, float m, float bet
 template <int TYPE>
 __device__ __forceinline__ uint64_t weight(const RowPlan &p, const float *roots, float v) {
     if constexpr (Entry<TYPE>::kReal) {
-        return weight_real(p, roots, v);
+        const Powers o = powers_of(p, roots, both(v));
+        const float w = o.w.x + o.wl.x;
+        return whole_weight(w, (o.w.x - w) + o.wl.x, static_cast<int>(o.k0), p.shift);
     } else {
         const uint64_t n = p.unit ? in_units(v * p.down, p.shift) : weight_power(v, p.m, p.beta, p.shift);
         return n > 0 ? n : 1;
@@ -152,46 +166,23 @@ __device__ __noinline__ uint64_t weight_once(const RowPlan &p, const float *root
 // Sums of weights as pairs of fp32 numbers, the largest weight being 1: what several
 // entries next to each other cost less by than by integers one by one.  Two entries at a time,
 // in packed arithmetic, into two sums.
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 struct PairSum {
-    float2 hi = {0.f, 0.f}, lo = {0.f, 0.f};
+    // (from the first on larger than what is added, so that a difference's error is one itself)
+    static constexpr float kFrom = 4.f;
+    float2 hi = {kFrom, kFrom}, lo = {0.f, 0.f};
     __device__ __forceinline__ void add(float2 h, float2 l) {
-        const float2 x = add2(hi, h), b = sub2(x, hi);
-        lo = add2(lo, add2(add2(sub2(hi, sub2(x, b)), sub2(h, b)), l));
+        const float2 x = add2(hi, h);
+        lo = add2(lo, add2(sub2(h, sub2(x, hi)), l));
         hi = x;
     }
     __device__ __forceinline__ uint64_t units(int shift) const {
-        const float x = hi.x + hi.y, b = x - hi.x;
-        const float y = ((hi.x - (x - b)) + (hi.y - b)) + (lo.x + lo.y);
+        const float u0 = hi.x - kFrom, u1 = hi.y - kFrom, x = u0 + u1, b = x - u0;
+        const float y = ((u0 - (x - b)) + (u1 - b)) + (lo.x + lo.y);
         const float h = x + y, l = (x - h) + y;
         const uint64_t u = in_units(h, shift), v = in_units(fabsf(l), shift);
         return h > 0.f ? (l < 0.f ? u - v : l > 0.f ? u + v : u) : 0;
     }
 };
-// As weight_real, of two entries: 2^(k mod 1024 / 1024 + r) as unnormalised pairs w + wl, and k.
-struct Powers {
-    float2 w, wl;
-    uint32_t k0, k1;
-};
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ Powers powers_of(const RowPlan &p, const float *roots, float2 v) {
-    constexpr float kLn2Hi = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f, kMagic = 12582912.f;
-    v = make_float2(fmaxf(v.x, p.low), fmaxf(v.y, p.low));
-    const float2 d = add2(v, both(-p.m)), b = sub2(d, v);   // as in exponent()
-    const float2 e = add2(sub2(v, sub2(d, b)), sub2(both(-p.m), b));
-    const float2 h = mul2(d, both(p.ch));
-    const float2 t = fma2(d, both(p.cl), fma2(e, both(p.ch), fma2(d, both(p.ch), mul2(d, both(-p.ch)))));
-    const float2 km = fma2(h, both(1024.f), both(kMagic)), kf = add2(km, both(-kMagic));
-    const uint32_t k0 = __float_as_uint(km.x) - __float_as_uint(kMagic), k1 = __float_as_uint(km.y) - __float_as_uint(kMagic);
-    const float2 r = fma2(kf, both(-0x1p-10f), h);
-    const float2 g = mul2(r, both(kLn2Hi)), ng = mul2(r, both(-kLn2Hi));
-    const float2 gl = add2(fma2(r, both(kLn2Hi), ng), fma2(r, both(kLn2Lo), mul2(t, both(kLn2Hi))));
-    const float2 lo = fma2(mul2(g, g), fma2(g, both(1.f / 6), both(0.5f)), gl);
-    const uint32_t i0 = k0 & (kRoots - 1), i1 = k1 & (kRoots - 1);
-    const float2 x = make_float2(roots[i0], roots[i1]), y = make_float2(roots[i0 + kRoots], roots[i1 + kRoots]);
-    const float2 a = mul2(x, g), al = fma2(x, g, mul2(x, ng)), w = add2(x, a);
-    return {w, add2(add2(sub2(x, w), a), add2(al, fma2(x, lo, fma2(y, g, y)))), k0, k1};
-}
 // Of two entries, as pairs; 0 where they do not count.
 struct Weights {
     float2 hi, lo;
@@ -360,19 +351,18 @@ __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const 
     p.m = m;
     p.beta = f.beta;
     p.unit = f.beta == 1.f;
-    const double c = static_cast<double>(f.beta) * 1.4426950408889634;
-    p.ch = c < 3.4e38 ? static_cast<float>(c) : 3.402823466e38f;
-    p.cl = c < 3.4e38 ? static_cast<float>(c - p.ch) : 0.f;
     // With this the number next to m weighs 2^-124 .. 2^-62: less than a unit already, and what the
-    // tables and fp32's exponents reach
-    const float most = __fdiv_rn(62.f * 0x1p24f, fabsf(m));
-    if (p.ch > most) {
-        p.ch = most;
-        p.cl = 0.f;
-    }
+    // table and fp32's exponents reach
+    p.b = fminf(f.beta, __fdiv_rn(43.f * 0x1p24f, fabsf(m)));
+    p.ch = fminf(p.b * 1.44269504f, 3.402823466e38f);
     // (2^-60 .. 2^-120, where m's neighbours are few; differences beyond fp32 count as the largest number)
-    p.low = fmaxf(fminf(m - __fdiv_rn(90.f, p.ch), nextafterf(m, -__builtin_huge_valf())),
+    p.low = fmaxf(fminf(m - __fdiv_rn(62.4f, p.b), nextafterf(m, -__builtin_huge_valf())),
                   fmaxf(m, 0.f) - 3.402823466e38f);
+    const float at = m * p.b;
+    p.far = !(fabsf(at) <= 64.f);
+    const float grid = __fadd_rn(__fadd_rn(p.far ? 0.f : at * 0x1.71547652b82fep+10f, kMagic), -kMagic);
+    p.origin = Entry<TYPE>::kReal && !p.far ? grid : m;
+    p.first = __float_as_uint(kMagic) + static_cast<uint32_t>(static_cast<int>(grid));
     p.greedy = f.greedy;
     p.bound = kPresent;
     int x = 0;
@@ -407,13 +397,14 @@ __device__ __noinline__ float least_value(const RowPlan &p, float min_p) {
 // and do 32 at a time.
 struct LogP {
     uint64_t total;
-    float v, m, beta;
-    int shift;          // weights' unit: 2^-shift of m's (of 1 for amplitudes at beta = 1)
-    bool greedy, unit;
+    float v, origin, beta;
+    int shift;          // weights' unit: 2^-shift of the origin's (of 1 for amplitudes at beta = 1)
+    bool greedy, unit, far;
 
     __device__ __forceinline__ void of(const RowPlan &p, uint64_t t) {
         total = t;
-        m = p.m;
+        origin = p.origin;
+        far = p.far;
         beta = p.beta;
         greedy = p.greedy;
         unit = p.unit;
@@ -426,9 +417,10 @@ __device__ __noinline__ float log_p(const LogP &l) {
     if (l.greedy) return 0.f;
     const double z = log(static_cast<double>(l.total));
     double x;
-    if constexpr (Entry<TYPE>::kReal) x = l.beta * (static_cast<double>(l.v) - l.m);
+    if constexpr (Entry<TYPE>::kReal)
+        x = l.far ? l.beta * (static_cast<double>(l.v) - l.origin) : static_cast<double>(l.beta) * l.v - l.origin * (kLn2d / 1024);
     else if (l.unit) x = log(static_cast<double>(l.v));
-    else x = l.beta * log(static_cast<double>(l.v) / l.m);
+    else x = l.beta * log(static_cast<double>(l.v) / l.origin);
     return static_cast<float>(x - (z - l.shift * kLn2d));
 }
 
