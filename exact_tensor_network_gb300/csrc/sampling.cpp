@@ -157,6 +157,7 @@ tn_status tn_sampler_draw(tn_sampler_t *h, const tn_rows *r, const tn_filters *f
     a.kept = kept;
     const tn_filters &f = a.f;
     a.filtered = f.top_ks || f.top_ps || f.top_k > 0 || f.top_p < 1.f;
+    a.powers = f.temperatures || s.scale != f.temperature;      // (their quotient is 1 only where they are equal)
     a.pieces = pieces(s.type, s.cols);
     if (s.state_off) {
         a.segs = segment(a.pieces, r->rows, &a.seg_pieces);

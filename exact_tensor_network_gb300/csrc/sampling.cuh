@@ -55,13 +55,85 @@ __device__ __forceinline__ void make_roots(float *roots) {
     }
 }
 
+// For c = 1 + (i + 1/2) / 128: a number of eight bits that is near 1 / c, and the logarithm of its inverse, to
+// 16 bits and what is left.
+static __device__ const float4 kLogs[128] = {
+    {0x1.fep-1f, 0x1.01p-8f, -0x1.fea9aap-18f, 0.f}, {0x1.fap-1f, 0x1.828p-7f, -0x1.dbae3cp-18f, 0.f},
+    {0x1.f6p-1f, 0x1.434p-6f, -0x1.56da68p-18f, 0.f}, {0x1.f2p-1f, 0x1.c64p-6f, -0x1.689f5ap-21f, 0.f},
+    {0x1.eep-1f, 0x1.252p-5f, 0x1.e65f1ap-18f, 0.f}, {0x1.eap-1f, 0x1.67cp-5f, 0x1.29e5aap-18f, 0.f},
+    {0x1.e8p-1f, 0x1.894p-5f, 0x1.54294p-18f, 0.f}, {0x1.e4p-1f, 0x1.cccp-5f, -0x1.186444p-18f, 0.f},
+    {0x1.ep-1f, 0x1.086p-4f, -0x1.9d2988p-18f, 0.f}, {0x1.dcp-1f, 0x1.2aap-4f, 0x1.2911c6p-22f, 0.f},
+    {0x1.dap-1f, 0x1.3bep-4f, -0x1.4b05c2p-21f, 0.f}, {0x1.d6p-1f, 0x1.5e9p-4f, 0x1.69365ep-18f, 0.f},
+    {0x1.d2p-1f, 0x1.819p-4f, 0x1.f8bd04p-18f, 0.f}, {0x1.dp-1f, 0x1.933p-4f, 0x1.797566p-18f, 0.f},
+    {0x1.ccp-1f, 0x1.b6bp-4f, -0x1.bb9296p-19f, 0.f}, {0x1.c8p-1f, 0x1.da7p-4f, 0x1.3b1c22p-19f, 0.f},
+    {0x1.c6p-1f, 0x1.ec7p-4f, 0x1.cc185p-19f, 0.f}, {0x1.c2p-1f, 0x1.0858p-3f, 0x1.8b59e4p-19f, 0.f},
+    {0x1.cp-1f, 0x1.1178p-3f, 0x1.d044fcp-20f, 0.f}, {0x1.bcp-1f, 0x1.23d8p-3f, -0x1.dab6c8p-20f, 0.f},
+    {0x1.bap-1f, 0x1.2d18p-3f, -0x1.ef3798p-19f, 0.f}, {0x1.b6p-1f, 0x1.3fb8p-3f, -0x1.d2d336p-18f, 0.f},
+    {0x1.b4p-1f, 0x1.491p-3f, 0x1.ec199ep-18f, 0.f}, {0x1.bp-1f, 0x1.5bf8p-3f, -0x1.fca55ep-18f, 0.f},
+    {0x1.aep-1f, 0x1.6578p-3f, -0x1.8a0bap-18f, 0.f}, {0x1.aap-1f, 0x1.7898p-3f, 0x1.b0a88ap-20f, 0.f},
+    {0x1.a8p-1f, 0x1.824p-3f, -0x1.f4d572p-18f, 0.f}, {0x1.a6p-1f, 0x1.8be8p-3f, 0x1.7f59c8p-18f, 0.f},
+    {0x1.a2p-1f, 0x1.9f7p-3f, -0x1.dfc7bcp-18f, 0.f}, {0x1.ap-1f, 0x1.a94p-3f, -0x1.2c3752p-19f, 0.f},
+    {0x1.9ep-1f, 0x1.b32p-3f, -0x1.3d4522p-18f, 0.f}, {0x1.9ap-1f, 0x1.c7p-3f, -0x1.0e43fcp-21f, 0.f},
+    {0x1.98p-1f, 0x1.d1p-3f, 0x1.bf932ap-18f, 0.f}, {0x1.96p-1f, 0x1.db1p-3f, 0x1.ed86a4p-18f, 0.f},
+    {0x1.94p-1f, 0x1.e53p-3f, 0x1.dffce2p-20f, 0.f}, {0x1.9p-1f, 0x1.f99p-3f, 0x1.c6cb3cp-19f, 0.f},
+    {0x1.8ep-1f, 0x1.01ecp-2f, -0x1.1a9d94p-18f, 0.f}, {0x1.8cp-1f, 0x1.0714p-2f, -0x1.e7ecaap-20f, 0.f},
+    {0x1.8ap-1f, 0x1.0c44p-2f, -0x1.2989eap-18f, 0.f}, {0x1.88p-1f, 0x1.1178p-2f, 0x1.d044fcp-19f, 0.f},
+    {0x1.84p-1f, 0x1.1bf8p-2f, 0x1.9635a6p-18f, 0.f}, {0x1.82p-1f, 0x1.2144p-2f, 0x1.5b43aep-20f, 0.f},
+    {0x1.8p-1f, 0x1.2698p-2f, -0x1.deecb2p-18f, 0.f}, {0x1.7ep-1f, 0x1.2bfp-2f, -0x1.f0646ep-19f, 0.f},
+    {0x1.7cp-1f, 0x1.315p-2f, -0x1.c3c594p-19f, 0.f}, {0x1.7ap-1f, 0x1.36b8p-2f, -0x1.88941ep-18f, 0.f},
+    {0x1.78p-1f, 0x1.3c24p-2f, 0x1.277334p-18f, 0.f}, {0x1.76p-1f, 0x1.419cp-2f, -0x1.7b8542p-19f, 0.f},
+    {0x1.74p-1f, 0x1.4718p-2f, 0x1.b84e38p-19f, 0.f}, {0x1.72p-1f, 0x1.4cap-2f, -0x1.f61e8ep-18f, 0.f},
+    {0x1.7p-1f, 0x1.522cp-2f, -0x1.1f8c76p-18f, 0.f}, {0x1.6ep-1f, 0x1.57cp-2f, -0x1.1586e6p-19f, 0.f},
+    {0x1.6cp-1f, 0x1.5d5cp-2f, -0x1.10535p-21f, 0.f}, {0x1.6ap-1f, 0x1.63p-2f, 0x1.859d56p-21f, 0.f},
+    {0x1.68p-1f, 0x1.68acp-2f, 0x1.07d38ep-19f, 0.f}, {0x1.66p-1f, 0x1.6e6p-2f, 0x1.dcd5e4p-19f, 0.f},
+    {0x1.64p-1f, 0x1.741cp-2f, 0x1.876c68p-18f, 0.f}, {0x1.62p-1f, 0x1.79e4p-2f, -0x1.99783p-18f, 0.f},
+    {0x1.6p-1f, 0x1.7fbp-2f, -0x1.7109fap-20f, 0.f}, {0x1.5ep-1f, 0x1.8584p-2f, 0x1.5776dcp-18f, 0.f},
+    {0x1.5cp-1f, 0x1.8b64p-2f, -0x1.95dd34p-20f, 0.f}, {0x1.5ap-1f, 0x1.914cp-2f, -0x1.79ca4p-18f, 0.f},
+    {0x1.58p-1f, 0x1.973cp-2f, -0x1.cbcecap-18f, 0.f}, {0x1.56p-1f, 0x1.9d34p-2f, -0x1.415ea2p-18f, 0.f},
+    {0x1.54p-1f, 0x1.a334p-2f, 0x1.00893ep-20f, 0.f}, {0x1.52p-1f, 0x1.a94p-2f, -0x1.2c3752p-18f, 0.f},
+    {0x1.5p-1f, 0x1.af54p-2f, -0x1.6adb74p-18f, 0.f}, {0x1.5p-1f, 0x1.af54p-2f, -0x1.6adb74p-18f, 0.f},
+    {0x1.4ep-1f, 0x1.b57p-2f, -0x1.7eee76p-20f, 0.f}, {0x1.4cp-1f, 0x1.bb98p-2f, -0x1.ee47f2p-18f, 0.f},
+    {0x1.4ap-1f, 0x1.c1c8p-2f, -0x1.f96c06p-18f, 0.f}, {0x1.48p-1f, 0x1.c8p-2f, -0x1.8e2eaap-20f, 0.f},
+    {0x1.46p-1f, 0x1.ce44p-2f, -0x1.0e7f9cp-18f, 0.f}, {0x1.46p-1f, 0x1.ce44p-2f, -0x1.0e7f9cp-18f, 0.f},
+    {0x1.44p-1f, 0x1.d49p-2f, 0x1.236f7ep-21f, 0.f}, {0x1.42p-1f, 0x1.dae8p-2f, -0x1.56f66ep-19f, 0.f},
+    {0x1.4p-1f, 0x1.e148p-2f, 0x1.4344e4p-19f, 0.f}, {0x1.3ep-1f, 0x1.e7b4p-2f, 0x1.61eed6p-21f, 0.f},
+    {0x1.3ep-1f, 0x1.e7b4p-2f, 0x1.61eed6p-21f, 0.f}, {0x1.3cp-1f, 0x1.ee2cp-2f, -0x1.ea94bep-18f, 0.f},
+    {0x1.3ap-1f, 0x1.f4acp-2f, -0x1.811fcep-18f, 0.f}, {0x1.38p-1f, 0x1.fb34p-2f, 0x1.8af7a4p-18f, 0.f},
+    {0x1.38p-1f, 0x1.fb34p-2f, 0x1.8af7a4p-18f, 0.f}, {0x1.36p-1f, 0x1.00e6p-1f, -0x1.46937ep-19f, 0.f},
+    {0x1.34p-1f, 0x1.0436p-1f, 0x1.7cec08p-22f, 0.f}, {0x1.32p-1f, 0x1.078cp-1f, -0x1.f59876p-22f, 0.f},
+    {0x1.32p-1f, 0x1.078cp-1f, -0x1.f59876p-22f, 0.f}, {0x1.3p-1f, 0x1.0ae8p-1f, -0x1.23a5f6p-18f, 0.f},
+    {0x1.2ep-1f, 0x1.0e48p-1f, 0x1.30c23ap-18f, 0.f}, {0x1.2ep-1f, 0x1.0e48p-1f, 0x1.30c23ap-18f, 0.f},
+    {0x1.2cp-1f, 0x1.11bp-1f, -0x1.f70e2ap-19f, 0.f}, {0x1.2ap-1f, 0x1.151cp-1f, 0x1.fb794cp-20f, 0.f},
+    {0x1.2ap-1f, 0x1.151cp-1f, 0x1.fb794cp-20f, 0.f}, {0x1.28p-1f, 0x1.188ep-1f, 0x1.c81e48p-18f, 0.f},
+    {0x1.26p-1f, 0x1.1c08p-1f, -0x1.ed9468p-19f, 0.f}, {0x1.26p-1f, 0x1.1c08p-1f, -0x1.ed9468p-19f, 0.f},
+    {0x1.24p-1f, 0x1.1f86p-1f, 0x1.afe30cp-20f, 0.f}, {0x1.22p-1f, 0x1.230cp-1f, -0x1.e4e828p-18f, 0.f},
+    {0x1.22p-1f, 0x1.230cp-1f, -0x1.e4e828p-18f, 0.f}, {0x1.2p-1f, 0x1.2696p-1f, 0x1.089a6ep-20f, 0.f},
+    {0x1.1ep-1f, 0x1.2a28p-1f, -0x1.e4bc5p-19f, 0.f}, {0x1.1ep-1f, 0x1.2a28p-1f, -0x1.e4bc5p-19f, 0.f},
+    {0x1.1cp-1f, 0x1.2dcp-1f, -0x1.5509e4p-18f, 0.f}, {0x1.1cp-1f, 0x1.2dcp-1f, -0x1.5509e4p-18f, 0.f},
+    {0x1.1ap-1f, 0x1.315ep-1f, -0x1.6ef2fep-19f, 0.f}, {0x1.18p-1f, 0x1.3502p-1f, 0x1.15b3b2p-18f, 0.f},
+    {0x1.18p-1f, 0x1.3502p-1f, 0x1.15b3b2p-18f, 0.f}, {0x1.16p-1f, 0x1.38aep-1f, 0x1.0b8cbcp-20f, 0.f},
+    {0x1.16p-1f, 0x1.38aep-1f, 0x1.0b8cbcp-20f, 0.f}, {0x1.14p-1f, 0x1.3c6p-1f, 0x1.0186d8p-18f, 0.f},
+    {0x1.12p-1f, 0x1.401ap-1f, -0x1.ef6d1ap-20f, 0.f}, {0x1.12p-1f, 0x1.401ap-1f, -0x1.ef6d1ap-20f, 0.f},
+    {0x1.1p-1f, 0x1.43dap-1f, -0x1.a0db88p-26f, 0.f}, {0x1.1p-1f, 0x1.43dap-1f, -0x1.a0db88p-26f, 0.f},
+    {0x1.0ep-1f, 0x1.47a2p-1f, -0x1.5b02ecp-18f, 0.f}, {0x1.0ep-1f, 0x1.47a2p-1f, -0x1.5b02ecp-18f, 0.f},
+    {0x1.0cp-1f, 0x1.4b7p-1f, -0x1.48347ap-20f, 0.f}, {0x1.0ap-1f, 0x1.4f46p-1f, -0x1.5f296cp-19f, 0.f},
+    {0x1.0ap-1f, 0x1.4f46p-1f, -0x1.5f296cp-19f, 0.f}, {0x1.08p-1f, 0x1.5322p-1f, 0x1.c4d0dp-18f, 0.f},
+    {0x1.08p-1f, 0x1.5322p-1f, 0x1.c4d0dp-18f, 0.f}, {0x1.06p-1f, 0x1.5708p-1f, -0x1.76511cp-19f, 0.f},
+    {0x1.06p-1f, 0x1.5708p-1f, -0x1.76511cp-19f, 0.f}, {0x1.04p-1f, 0x1.5af4p-1f, 0x1.70d928p-23f, 0.f},
+    {0x1.04p-1f, 0x1.5af4p-1f, 0x1.70d928p-23f, 0.f}, {0x1.02p-1f, 0x1.5ee8p-1f, 0x1.55120cp-20f, 0.f},
+    {0x1.02p-1f, 0x1.5ee8p-1f, 0x1.55120cp-20f, 0.f}, {0x1p-1f, 0x1.62e4p-1f, 0x1.7f7d1cp-20f, 0.f},
+};
+constexpr float kLn2Hi = 0x1.62e4p-1f, kLn2Lo = 0x1.7f7d1cp-20f;    // ln 2 likewise
+
 // What a row's weights are computed from.
 struct RowPlan {
     float m;            // largest order value
     float b;            // beta, as large as weights need it
     float ch;           // b log2(e), for estimates
     float low;          // lower order values weigh as much (next to nothing)
-    float origin;       // weights are relative to m (far) or to e^(origin ln 2 / 1024), which is near m's
+    // Weights are relative to m's (far), or to a number near it: e^(origin ln 2 / 1024), or of
+    // amplitudes (2^n e^g)^beta with n + g = origin, n whole
+    float origin;
     uint32_t first;     // what a rounded exponent's bits less this are the power of
     bool far;
     float down;         // amplitudes at beta = 1: 2^-x with weights up to 2^x
@@ -143,7 +215,35 @@ __device__ __forceinline__ uint64_t in_units(float v, int shift) {
 
 // Out of line, as what follows is wherever a kernel's steady loop does not need it: a
 // kernel's first pass through its code costs more than what it computes there.
-static __device__ __noinline__ uint64_t weight_power(float v, float m, float beta, int shift) {
+//
+// An amplitude's weight at beta != 1, to some 2^-40 (2^-46 on average): ln v = e ln 2 - ln t + ln(1 + r) with
+// r = t c - 1 exact, t from the table; the parts of 16 bits add up exactly, the series' first two
+// terms are kept as a pair.  148 x 226333 amplitudes, with logarithms and exponentials in 64 bits 4.1 ms.
+static __device__ __noinline__ uint64_t weight_power(float v, float b, float origin, int shift, const float *roots) {
+    const float up = v < 0x1p-126f ? 0x1p24f : 1.f;
+    const uint32_t u = __float_as_uint(v * up);
+    const float e = static_cast<float>(static_cast<int>(u >> 23) - (up > 1.f ? 151 : 127));
+    const float c = __uint_as_float((u & 0x7fffffu) | 0x3f800000u), n = floorf(origin);
+    const float4 t = kLogs[u >> 16 & 127];
+    const float r = fmaf(c, t.x, -1.f), s = r * r;
+    const float d = fmaf(e - n, kLn2Hi, t.y - (origin - n));
+    const float ph = fmaf(-0.5f, s, r);
+    const float cube = r * s * fmaf(r, fmaf(r, fmaf(r, fmaf(r, 1.f / 7, -1.f / 6), 0.2f), -0.25f), 1.f / 3);
+    const float pl = fmaf(-0.5f, s, r - ph) + (fmaf(e - n, kLn2Lo, t.z) + fmaf(-0.5f, fmaf(r, r, -s), cube));
+    const float x = d + ph, y = x - d, xl = ((d - (x - y)) + (ph - y)) + pl;
+    const float h = x * b, l = fmaf(xl, b, fmaf(x, b, -h));
+    if (!(h > -62.f)) return 1;
+    const float km = fmaf(h, 0x1.71547652b82fep+10f, kMagic), kf = __fadd_rn(km, -kMagic);
+    const int k = static_cast<int>(__float_as_uint(km) - __float_as_uint(kMagic));
+    const float q = fmaf(kf, -kStepHi, h), ql = fmaf(kf, -kStepLo, l), a = q + ql;
+    const float lo = fmaf(a * a, fmaf(a, 1.f / 6, 0.5f), (q - a) + ql);
+    const float g = roots[k & (kRoots - 1)], gl = roots[(k & (kRoots - 1)) + kRoots];
+    const float w = g * a, wl = fmaf(g, a, -w), w0 = g + w;
+    const float wm = ((g - w0) + w) + (wl + fmaf(g, lo, fmaf(gl, a, gl))), whole = w0 + wm;
+    return whole_weight(whole, (w0 - whole) + wm, k, shift);
+}
+// In 64 bits, at a beta that makes more of the logarithm's error.
+static __device__ __noinline__ uint64_t weight_far_power(float v, float m, float beta, int shift) {
     const double x = static_cast<double>(beta) * log(static_cast<double>(v) / m);
     return x < -60.0 ? 1 : static_cast<uint64_t>(__double2ll_rn(ldexp(exp(x), shift)));
 }
@@ -155,7 +255,9 @@ __device__ __forceinline__ uint64_t weight(const RowPlan &p, const float *roots,
         const float w = o.w.x + o.wl.x;
         return whole_weight(w, (o.w.x - w) + o.wl.x, static_cast<int>(o.k0), p.shift);
     } else {
-        const uint64_t n = p.unit ? in_units(v * p.down, p.shift) : weight_power(v, p.m, p.beta, p.shift);
+        const uint64_t n = p.unit  ? in_units(v * p.down, p.shift)
+                           : p.far ? weight_far_power(v, p.m, p.beta, p.shift)
+                                   : weight_power(v, p.b, p.origin, p.shift, roots);
         return n > 0 ? n : 1;
     }
 }
@@ -351,18 +453,26 @@ __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const 
     p.m = m;
     p.beta = f.beta;
     p.unit = f.beta == 1.f;
-    // With this the number next to m weighs 2^-124 .. 2^-62: less than a unit already, and what the
-    // table and fp32's exponents reach
-    p.b = fminf(f.beta, __fdiv_rn(43.f * 0x1p24f, fabsf(m)));
-    p.ch = fminf(p.b * 1.44269504f, 3.402823466e38f);
-    // (2^-60 .. 2^-120, where m's neighbours are few; differences beyond fp32 count as the largest number)
-    p.low = fmaxf(fminf(m - __fdiv_rn(62.4f, p.b), nextafterf(m, -__builtin_huge_valf())),
-                  fmaxf(m, 0.f) - 3.402823466e38f);
-    const float at = m * p.b;
-    p.far = !(fabsf(at) <= 64.f);
-    const float grid = __fadd_rn(__fadd_rn(p.far ? 0.f : at * 0x1.71547652b82fep+10f, kMagic), -kMagic);
-    p.origin = Entry<TYPE>::kReal && !p.far ? grid : m;
-    p.first = __float_as_uint(kMagic) + static_cast<uint32_t>(static_cast<int>(grid));
+    if constexpr (Entry<TYPE>::kReal) {
+        // With this the number next to m weighs 2^-124 .. 2^-62: less than a unit already, and what the
+        // table and fp32's exponents reach
+        p.b = fminf(f.beta, __fdiv_rn(43.f * 0x1p24f, fabsf(m)));
+        p.ch = fminf(p.b * 1.44269504f, 3.402823466e38f);
+        // (2^-60 .. 2^-120, where m's neighbours are few; differences beyond fp32 count as the largest number)
+        p.low = fmaxf(fminf(m - __fdiv_rn(62.4f, p.b), nextafterf(m, -__builtin_huge_valf())),
+                      fmaxf(m, 0.f) - 3.402823466e38f);
+        const float at = m * p.b;
+        p.far = !(fabsf(at) <= 64.f);
+        const float grid = __fadd_rn(__fadd_rn(p.far ? 0.f : at * 0x1.71547652b82fep+10f, kMagic), -kMagic);
+        p.origin = p.far ? m : grid;
+        p.first = __float_as_uint(kMagic) + static_cast<uint32_t>(static_cast<int>(grid));
+    } else {
+        p.b = f.beta;
+        p.far = f.beta > 2.f;           // (the errors of logarithms count beta times)
+        int n;
+        const float g = lg2(2.f * frexpf(m, &n)) * 0.693147181f;       // (an estimate will do)
+        p.origin = p.far ? m : (n - 1) + rintf(fmaxf(g, 0.f) * 65536.f) * 0x1p-16f;
+    }
     p.greedy = f.greedy;
     p.bound = kPresent;
     int x = 0;
@@ -420,7 +530,8 @@ __device__ __noinline__ float log_p(const LogP &l) {
     if constexpr (Entry<TYPE>::kReal)
         x = l.far ? l.beta * (static_cast<double>(l.v) - l.origin) : static_cast<double>(l.beta) * l.v - l.origin * (kLn2d / 1024);
     else if (l.unit) x = log(static_cast<double>(l.v));
-    else x = l.beta * log(static_cast<double>(l.v) / l.origin);
+    else if (l.far) x = l.beta * log(static_cast<double>(l.v) / l.origin);
+    else x = l.beta * (log(static_cast<double>(l.v)) - floorf(l.origin) * kLn2d - (l.origin - floorf(l.origin)));
     return static_cast<float>(x - (z - l.shift * kLn2d));
 }
 
@@ -844,7 +955,7 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
     __shared__ __align__(16) uint64_t places[4 * WARPS];
     __shared__ float values[2][WARPS];
     pdl_trigger();
-    if (Entry<TYPE>::kReal) make_roots<THREADS>(roots);
+    if (Entry<TYPE>::kReal || a.powers) make_roots<THREADS>(roots);
     pdl_wait();
     __syncthreads();
     const int t = threadIdx.x % NT, lane = t % 32, warp = t / 32;
@@ -1758,7 +1869,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
     __shared__ uint64_t sums[kDrawWarps + 1], nums[kDrawWarps + 1];
     __shared__ uint32_t listed;
     pdl_trigger();
-    if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
+    if (Entry<TYPE>::kReal || a.powers) make_roots<kDrawThreads>(roots);
     if (threadIdx.x == 0) listed = 0;
     pdl_wait();
     const Segment<TYPE> c(a);
@@ -1963,7 +2074,7 @@ template <int TYPE>
 __global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_constant__ SampleArgs a) {
     __shared__ float roots[2 * kRoots];
     pdl_trigger();
-    if (Entry<TYPE>::kReal) make_roots<kDrawThreads>(roots);
+    if (Entry<TYPE>::kReal || a.powers) make_roots<kDrawThreads>(roots);
     pdl_wait();
     __syncthreads();
     const int64_t ctas = (a.draws + kDrawWarps - 1) / kDrawWarps;

@@ -41,6 +41,7 @@ struct SampleArgs {
     int64_t draws;
     int32_t wide;
     bool filtered;          // top_k or top_p of a row may leave less than all
+    bool powers;            // beta of a row may be other than 1
     int64_t pieces;         // of a row
     int64_t segs, seg_pieces;
     uint64_t *masses;       // [rows][pieces]
