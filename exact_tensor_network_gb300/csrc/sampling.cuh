@@ -861,38 +861,85 @@ __device__ __noinline__ uint64_t bound_of(const RowCta<TYPE> &c, const RowPlan &
 
 constexpr int kHeldEntries = 16;
 
-// Sums over a warp or a CTA; of a CTA, one barrier each, with two sets of places in turn.
-template <int NT>
-struct RowGroup {
-    static constexpr int kWarps = NT / 32;
-    uint64_t *places;       // 2 * 2 * kWarps (unused by a warp)
-    int lane, warp, half = 0;
+// Sums over a warp, a CTA or a cluster of up to kMostRanks CTAs; of more than a warp, one barrier each, with two sets
+// of places in turn.  In a cluster every warp's part goes to a place in every CTA.
+constexpr int kMostRanks = 8;
+__device__ __forceinline__ uint32_t rank_address(const void *p, int rank) {
+    uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(rank));
+    return at;
+}
+__device__ __forceinline__ void ranks_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
-    __device__ __forceinline__ uint64_t *next() {
+template <int NT, bool RANKS>
+struct RowGroup {
+    static constexpr int kWarps = NT / 32, kMost = RANKS ? kMostRanks * kWarps : kWarps;
+    ulonglong2 *places;     // 2 * kMost (unused by a warp)
+    int lane, warp, rank = 0, ranks = 1, half = 0;
+
+    // Each warp's (x, y), given by its lanes alike: those of warp `i` at the place returned + i, all to be read
+    // from then on by every warp.
+    __device__ __forceinline__ const ulonglong2 *meet(uint64_t x, uint64_t y) {
         half ^= 1;
-        return places + half * 2 * kWarps;
+        ulonglong2 *s = places + half * kMost;
+        if constexpr (RANKS) {
+            if (lane < ranks)
+                asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(rank_address(s + rank * kWarps + warp, lane)),
+                             "l"(x), "l"(y) : "memory");
+            ranks_sync();
+        } else {
+            if (lane == 0) s[warp] = make_ulonglong2(x, y);
+            __syncthreads();
+        }
+        return s;
+    }
+    // f(x, y) of every warp's part; in a cluster of 32nds of the parts by lane
+    template <class F>
+    __device__ __forceinline__ void each(const ulonglong2 *s, F f) const {
+        if constexpr (RANKS) {
+            for (int i = lane; i < ranks * kWarps; i += 32) f(s[i]);
+        } else {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) f(s[w]);
+        }
     }
     __device__ __forceinline__ float max(float x) {
         x = warp_max_nan(x);
         if constexpr (NT > 32) {
-            float *s = reinterpret_cast<float *>(next());
-            if (lane == 0) s[warp] = x;
-            __syncthreads();
+            each(meet(__float_as_uint(x), 0), [&](ulonglong2 y) { x = max_nan(x, __uint_as_float(static_cast<uint32_t>(y.x))); });
+            if constexpr (RANKS) x = warp_max_nan(x);
+        }
+        return x;
+    }
+    __device__ __forceinline__ uint64_t max(uint64_t x) {
+        const auto over_warp = [&] {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) x = max_nan(x, s[w]);
+            for (int o = 16; o; o >>= 1) {
+                const uint64_t y = __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(x), o);
+                x = y > x ? y : x;
+            }
+        };
+        over_warp();
+        if constexpr (NT > 32) {
+            each(meet(x, 0), [&](ulonglong2 y) { x = y.x > x ? y.x : x; });
+            if constexpr (RANKS) over_warp();
         }
         return x;
     }
     __device__ __forceinline__ float sum(float x) {
+        const auto over_warp = [&] {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        };
+        over_warp();
         if constexpr (NT > 32) {
-            float *s = reinterpret_cast<float *>(next());
-            if (lane == 0) s[warp] = x;
-            __syncthreads();
+            const ulonglong2 *s = meet(__float_as_uint(x), 0);
             x = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) x += s[w];
+            each(s, [&](ulonglong2 y) { x += __uint_as_float(static_cast<uint32_t>(y.x)); });
+            if constexpr (RANKS) over_warp();
         }
         return x;
     }
@@ -900,51 +947,57 @@ struct RowGroup {
         x = warp_sum(x);
         n = __reduce_add_sync(0xffffffffu, n);
         if constexpr (NT > 32) {
-            ulonglong2 *s = reinterpret_cast<ulonglong2 *>(next());
-            if (lane == 0) s[warp] = make_ulonglong2(x, n);
-            __syncthreads();
+            const ulonglong2 *s = meet(x, n);
             x = n = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const ulonglong2 y = s[w];
+            each(s, [&](ulonglong2 y) {
                 x += y.x;
                 n += static_cast<uint32_t>(y.y);
+            });
+            if constexpr (RANKS) {
+                x = warp_sum(x);
+                n = __reduce_add_sync(0xffffffffu, n);
             }
         }
     }
     __device__ __forceinline__ uint32_t sum(uint32_t n) {
         n = __reduce_add_sync(0xffffffffu, n);
         if constexpr (NT > 32) {
-            uint32_t *s = reinterpret_cast<uint32_t *>(next());
-            if (lane == 0) s[warp] = n;
-            __syncthreads();
+            const ulonglong2 *s = meet(n, 0);
             n = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) n += s[w];
+            each(s, [&](ulonglong2 y) { n += static_cast<uint32_t>(y.x); });
+            if constexpr (RANKS) n = __reduce_add_sync(0xffffffffu, n);
         }
         return n;
     }
     // inclusive; all: the sum of all
     __device__ __forceinline__ uint64_t scan(uint64_t x, uint64_t &all) {
         x = warp_scan(x, lane);
-        if constexpr (NT == 32) {
-            all = shfl_from(x, 31);
-        } else {
-            uint64_t *s = next();
-            if (lane == 31) s[warp] = x;
-            __syncthreads();
+        all = shfl_from(x, 31);
+        if constexpr (NT > 32) {
+            const ulonglong2 *s = meet(all, 0);
+            uint64_t before = 0;
             all = 0;
+            if constexpr (RANKS) {
+                for (int i = lane; i < ranks * kWarps; i += 32) {
+                    all += s[i].x;
+                    before += i < rank * kWarps + warp ? s[i].x : 0;
+                }
+                all = warp_sum(all);
+                before = warp_sum(before);
+            } else {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) x += s[w];
-                all += s[w];
+                for (int w = 0; w < kWarps; ++w) {
+                    all += s[w].x;
+                    before += w < warp ? s[w].x : 0;
+                }
             }
+            x += before;
         }
         return x;
     }
 };
 
-template <int TYPE, int N, int NT>
+template <int TYPE, int N, int NT, bool RANKS>
 __global__ void __launch_bounds__(NT == 32 ? kDrawThreads : NT, (N <= 8 ? 1024 : 512) / (NT == 32 ? kDrawThreads : NT))
 held_rows_kernel(const __grid_constant__ SampleArgs a) {
     constexpr int E = Entry<TYPE>::E, V = N / E, THREADS = NT == 32 ? kDrawThreads : NT, ROWS = THREADS / NT;
@@ -952,18 +1005,26 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
     // bits below these are the same in all order values
     constexpr int LOWEST = TYPE == TN_TYPE_BF16 ? 16 : TYPE == TN_TYPE_F16 ? 13 : 0;
     __shared__ float roots[2 * kRoots];
-    __shared__ __align__(16) uint64_t places[4 * WARPS];
+    __shared__ ulonglong2 places[2 * RowGroup<NT, RANKS>::kMost];
     __shared__ float values[2][WARPS];
     pdl_trigger();
     if (Entry<TYPE>::kReal || a.powers) make_roots<THREADS>(roots);
     pdl_wait();
     __syncthreads();
     const int t = threadIdx.x % NT, lane = t % 32, warp = t / 32;
-    RowGroup<NT> g{places, lane, warp};
+    RowGroup<NT, RANKS> g{places, lane, warp};
+    if constexpr (RANKS) {
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(g.rank));
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(g.ranks));
+        ranks_sync();       // (all have started before any writes to another's memory)
+    }
+    const int rank = g.rank, ranks = g.ranks;
+    // vector i of this thread
+    const auto vector_at = [&](int i) { return (i * ranks + rank) * NT + t; };
     int turn = 0;
     Pending<TYPE> pending;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / NT; row < a.r.rows;
-         row += static_cast<int64_t>(gridDim.x) * ROWS) {
+    for (int64_t row = static_cast<int64_t>(blockIdx.x / ranks) * ROWS + threadIdx.x / NT; row < a.r.rows;
+         row += static_cast<int64_t>(gridDim.x / ranks) * ROWS) {
         const Row<TYPE> r(a.r, row);
         const int vecs = static_cast<int>((r.head + r.cols + E - 1) / E);
         Filters f;
@@ -972,8 +1033,8 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
         float m = absent<TYPE>();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (NT * i + t < vecs) {
-                vector_values<TYPE>(r, NT * i + t, v[i]);
+            if (vector_at(i) < vecs) {
+                vector_values<TYPE>(r, vector_at(i), v[i]);
             } else {
 #pragma unroll
                 for (int k = 0; k < E; ++k) v[i][k] = absent<TYPE>();
@@ -986,7 +1047,7 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
         plan_row<TYPE>(p, m, valid, f);
         if (!valid && t == 0) flag_bad_id(a.r, row);
         if (p.state != kDraw) {
-            no_draws(a, row, p.state, t, NT);
+            if (rank == 0) no_draws(a, row, p.state, t, NT);
             continue;
         }
         if (!p.greedy) {
@@ -1083,19 +1144,7 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
                     }
                 }
             if (least - most <= 1) return;
-            // (one weight only: its parts are those of the largest)
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                const uint64_t x = __shfl_xor_sync(0xffffffffu, static_cast<unsigned long long>(one), o);
-                one = x > one ? x : one;
-            }
-            if constexpr (NT > 32) {
-                uint64_t *s = g.next();
-                if (lane == 0) s[warp] = one;
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < WARPS; ++i) one = s[i] > one ? s[i] : one;
-            }
+            one = g.max(one);       // (one weight only)
             uint32_t need = one > 0 && target > above ? static_cast<uint32_t>((target - above + one - 1) / one) : 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) {       // in the order of indices
@@ -1152,7 +1201,7 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
 #pragma unroll
             for (int k = 0; k < E; ++k) left += w[i][k] > 0;
         left = g.sum(left);
-        if (t == 0) a.kept[row] = p.greedy ? 1 : left;
+        if (t == 0 && rank == 0) a.kept[row] = p.greedy ? 1 : left;
         // sums up to each of the thread's vectors
         uint64_t upto[V];
         total = 0;
@@ -1191,7 +1240,7 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
                         before += w[i][k];
                         if (found || before <= target) continue;
                         found = true;
-                        a.ids[at] = (NT * i + t) * E + k - r.head;
+                        a.ids[at] = vector_at(i) * E + k - r.head;
                         value = v[i][k];
                     }
                 }
@@ -1199,15 +1248,20 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
                     const uint32_t who = __ballot_sync(0xffffffffu, owner);
                     value = __shfl_sync(0xffffffffu, value, __ffs(who) - 1);
                 } else if (owner) {
-                    values[turn][j] = value;
+                    if constexpr (RANKS)
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(rank_address(&values[turn][j], 0)), "f"(value)
+                                     : "memory");
+                    else
+                        values[turn][j] = value;
                 }
             }
             if constexpr (NT > 32) {
-                __syncthreads();
+                if constexpr (RANKS) ranks_sync();
+                else __syncthreads();
                 value = values[turn][warp];
                 turn ^= 1;
             }
-            if (drawn) pending.add(a, p, total, value, row * a.draws + d0 + warp);
+            if (drawn && rank == 0) pending.add(a, p, total, value, row * a.draws + d0 + warp);
         }
     }
     pending.flush(a);
@@ -2114,18 +2168,34 @@ template <int TYPE, int N, int NT>
 cudaError_t launch_held(const SampleArgs &a, cudaStream_t stream) {
     constexpr int THREADS = NT == 32 ? kDrawThreads : NT, ROWS = THREADS / NT;
     const int64_t groups = (a.r.rows + ROWS - 1) / ROWS, most = kDrawTarget * (kDrawThreads / THREADS);
-    return launch_pdl(held_rows_kernel<TYPE, N, NT>, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(THREADS),
-                      0, stream, a);
+    return launch_pdl(held_rows_kernel<TYPE, N, NT, false>, dim3(static_cast<unsigned>(groups < most ? groups : most)),
+                      dim3(THREADS), 0, stream, a);
+}
+template <int TYPE>
+cudaError_t launch_ranks(const SampleArgs &a, int ranks, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.r.rows * ranks));
+    cfg.blockDim = dim3(kDrawThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, held_rows_kernel<TYPE, kHeldEntries, kDrawThreads, true>, a);
 }
 
 template <int TYPE>
 cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
     constexpr int E = Entry<TYPE>::E;
+    const bool aligned = a.r.col_stride != 1 || (reinterpret_cast<uintptr_t>(a.r.data) % 16 == 0 &&
+                                                 a.r.row_stride % E == 0);
+    const int64_t entries = (a.r.cols + (aligned ? 0 : E - 1) + E - 1) / E * E;
     if (!a.state) {
         // a warp a row where its registers hold it, otherwise the least CTA that does
-        const bool aligned = a.r.col_stride != 1 || (reinterpret_cast<uintptr_t>(a.r.data) % 16 == 0 &&
-                                                     a.r.row_stride % E == 0);
-        const int64_t entries = (a.r.cols + (aligned ? 0 : E - 1) + E - 1) / E * E;
         constexpr int kFew = E == 8 ? 8 : 4, N = kHeldEntries;
         if (entries <= 32 * kFew) return launch_held<TYPE, kFew, 32>(a, stream);
         if (entries <= 32 * N) return launch_held<TYPE, N, 32>(a, stream);
@@ -2136,6 +2206,12 @@ cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
             if (entries <= 256 * N) return launch_held<TYPE, N, 256>(a, stream);
         return cudaErrorInvalidValue;       // (rows of more than kRowVecs vectors have a state)
     }
+    // Few rows that a cluster holds: one kernel instead of three, at the price of a barrier of the
+    // cluster for every sum
+    int ranks = 2;
+    while (ranks <= kMostRanks && entries > ranks * kDrawThreads * kHeldEntries) ranks *= 2;
+    if (ranks <= kMostRanks && a.r.rows * ranks <= 2 * kOutSms && a.draws <= kFewDraws)
+        return launch_ranks<TYPE>(a, ranks, stream);
     const dim3 block(kDrawThreads), grid(static_cast<unsigned>(a.r.rows * a.segs));
     cudaError_t e = launch_pdl(top_kernel<TYPE>, grid, block, 0, stream, a);
     if (e == cudaSuccess && a.filtered) {
