@@ -1078,29 +1078,30 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
                     left += here;
                 }
             }
-        // keep the entries, largest first, until `target` is reached
+        // Keep the entries, largest first, until `target` is reached.  What is left has keys of `bottom` on;
+        // under: that is a bound found already.
+        uint32_t bottom = order_key<TYPE>(least_present<TYPE>()) & ~((1u << LOWEST) - 1u);
+        bool under = !Entry<TYPE>::kReal;
         const auto cut = [&](uint64_t target, bool by_mass) {
-            // the entry where it is has a key of lo <= key < hi: halves of the values between them, from a
-            // first step below the largest on; halves of the keys where those would take too long
+            // the entry where it is has a key of lo <= key < hi: halves (numbers: quarters) of the values between
+            // them, from first steps below the largest on; of the keys where those would take too long
             constexpr uint32_t kUnit = 1u << LOWEST;
-            uint32_t lo = order_key<TYPE>(least_present<TYPE>()) & ~(kUnit - 1u);
-            uint32_t hi = (order_key<TYPE>(m) & ~(kUnit - 1u)) + kUnit;
+            uint32_t lo = bottom, hi = (order_key<TYPE>(m) & ~(kUnit - 1u)) + kUnit;
             uint32_t least = left, most = 0;    // entries of lo and above, of hi and above
             uint64_t above = 0;                 // what of hi and above amounts to
-            float step = __fdiv_rn(16.f, p.beta);
-            bool under = !Entry<TYPE>::kReal;
+            float step = __fdiv_rn(8.f, p.beta);
             for (int probes = 0; hi - lo > kUnit && least - most > 1; ++probes) {
-                float mid = 0.5f * key_value(lo) + 0.5f * key_value(hi);
-                if (!under) {
-                    mid = m - step;
-                    step *= 8.f;
-                }
-                uint32_t x = order_key<TYPE>(mid) & ~(kUnit - 1u);
-                if (x <= lo || x >= hi || probes >= 20) x = lo + ((hi - lo) / 2 & ~(kUnit - 1u));
-                const float from = key_value(x);
-                uint64_t s = 0;
-                uint32_t n = 0;
+                const float lowest = key_value(lo), highest = key_value(hi), middle = 0.5f * lowest + 0.5f * highest;
+                // the key of a value between lo and hi, or if there is none of `part` quarters of the way
+                const auto between = [&](float value, uint32_t part) {
+                    const uint32_t x = order_key<TYPE>(value) & ~(kUnit - 1u);
+                    return x > lo && x < hi && probes < 20 ? x : lo + ((hi - lo) / 4 * part + (hi - lo) % 4 * part / 4 & ~(kUnit - 1u));
+                };
                 if (by_mass) {
+                    const uint32_t x = between(under ? middle : m - step, 2);
+                    const float from = key_value(x);
+                    uint64_t s = 0;
+                    uint32_t n = 0;
 #pragma unroll
                     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -1110,23 +1111,60 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
                                 ++n;
                             }
                     g.sum(s, n);
+                    if (s >= target) {
+                        lo = x;
+                        least = n;
+                        under = true;
+                    } else {
+                        hi = x;
+                        above = s;
+                        most = n;
+                    }
                 } else {
+                    const uint32_t x2 = between(under ? middle : m - step, 2);
+                    const uint32_t y1 = between(under ? 0.5f * lowest + 0.5f * middle : m - 8.f * step, 1);
+                    const uint32_t y3 = between(under ? 0.5f * middle + 0.5f * highest : m - 0.125f * step, 3);
+                    const uint32_t x1 = y1 < x2 ? y1 : x2, x3 = y3 > x2 ? y3 : x2;
+                    const float from1 = key_value(x1), from2 = key_value(x2), from3 = key_value(x3);
+                    uint64_t s = 0;             // three numbers of 21 bits
+                    uint32_t n1 = 0, n2 = 0, n3 = 0;
 #pragma unroll
                     for (int i = 0; i < V; ++i)
 #pragma unroll
-                        for (int k = 0; k < E; ++k) n += v[i][k] >= from;
-                    s = n = g.sum(n);
-                }
-                if (s >= target) {
-                    lo = x;
-                    least = n;
-                    under = true;
-                } else {
-                    hi = x;
-                    above = s;
-                    most = n;
+                        for (int k = 0; k < E; ++k) {
+                            n1 += v[i][k] >= from1;
+                            n2 += v[i][k] >= from2;
+                            n3 += v[i][k] >= from3;
+                        }
+                    s = n1 | static_cast<uint64_t>(n2) << 21 | static_cast<uint64_t>(n3) << 42;
+                    uint32_t none = 0;
+                    g.sum(s, none);
+                    constexpr uint32_t kNumber = (1u << 21) - 1u;
+                    n1 = static_cast<uint32_t>(s) & kNumber;
+                    n2 = static_cast<uint32_t>(s >> 21) & kNumber;
+                    n3 = static_cast<uint32_t>(s >> 42);
+                    const auto reached = [&](uint32_t x, uint32_t n) {
+                        if (n >= target && x > lo) {
+                            lo = x;
+                            least = n;
+                            under = true;
+                        }
+                    };
+                    const auto missed = [&](uint32_t x, uint32_t n) {
+                        if (n < target && x < hi) {
+                            hi = x;
+                            above = most = n;
+                        }
+                    };
+                    reached(x1, n1);
+                    reached(x2, n2);
+                    reached(x3, n3);
+                    missed(x3, n3);
+                    missed(x2, n2);
+                    missed(x1, n1);
                 }
             }
+            bottom = lo;
             // of equal entries (which have equal weights) as many as it takes, the first ones
             uint64_t one = 0;
             uint32_t tied = 0;
@@ -2210,7 +2248,8 @@ cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
     // cluster for every sum
     int ranks = 2;
     while (ranks <= kMostRanks && entries > ranks * kDrawThreads * kHeldEntries) ranks *= 2;
-    if (ranks <= kMostRanks && a.r.rows * ranks <= 2 * kOutSms && a.draws <= kFewDraws)
+    const bool both = (a.f.top_ks || a.f.top_k > 0) && (a.f.top_ps || a.f.top_p < 1.f);
+    if (ranks <= kMostRanks && a.r.rows * ranks <= (both ? 2 : 3) * kOutSms && a.draws <= kFewDraws)
         return launch_ranks<TYPE>(a, ranks, stream);
     const dim3 block(kDrawThreads), grid(static_cast<unsigned>(a.r.rows * a.segs));
     cudaError_t e = launch_pdl(top_kernel<TYPE>, grid, block, 0, stream, a);
