@@ -65,6 +65,21 @@ struct Raw {
         }
     }
     __device__ __forceinline__ uint32_t size(int i) const { return __float_as_uint((*this)[i]) & 0x7fffffffu; }
+    // the largest of all sizes (of 16-bit types two at a time, as they lie)
+    __device__ __forceinline__ uint32_t largest() const {
+        uint32_t m = w[0] & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 1; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        } else {
+#pragma unroll
+            for (int i = 1; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            Raw<T, 2> one;
+            one.w[0] = max(m & 0xffffu, m >> 16);
+            return one.size(0);
+        }
+    }
 };
 
 // The scale of a block whose largest magnitude has the bits `top`, and what
@@ -93,6 +108,14 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 // (0 * infinity and 0 * NaN are not 0)
 __device__ __forceinline__ float scaled(float x, float inverse) { return inverse == 0.f ? 0.f : x * inverse; }
 
+// a b, packed
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
 // Codes in the layout of x alone, with a scale for 128 entries of a row: 16 bytes of
 // a row a lane, four loads in flight, no shared memory.
 template <typename T>
@@ -101,47 +124,58 @@ __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const QuantArgs 
     const int lane = threadIdx.x % 32;
     pdl_trigger();
     pdl_wait();
-    // items of 32 vectors: `per` of them a row
-    const int64_t per = (a.cols + 32 * N - 1) / (32 * N), items = a.rows * per;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (THREADS / 32);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + threadIdx.x / 32; it < items; it += step * LOADS) {
+    // items of 32 vectors: `per` of them a row (sides are below 2^31 - 1024)
+    const uint32_t rows = static_cast<uint32_t>(a.rows);
+    const int cols = static_cast<int>(a.cols), per = (cols + 32 * N - 1) / (32 * N);
+    const int step = gridDim.x * (THREADS / 32), first = blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
+    // (one division each; from item to item by sums, which stay below 2^32)
+    const int step_rows = step / per, step_rest = step - step_rows * per;
+    uint32_t at_row = first / per;
+    int at = first - first / per * per;
+    while (at_row < rows) {
         Raw<T, N> v[LOADS];
-        int64_t row[LOADS], col[LOADS];
+        uint32_t row[LOADS];
+        int col[LOADS];
 #pragma unroll
         for (int l = 0; l < LOADS; ++l) {
-            const int64_t i = it + l * step;
-            row[l] = i < items ? i / per : a.rows;
-            col[l] = ((i < items ? i - row[l] * per : 0) * 32 + lane) * N;
+            row[l] = at_row;
+            col[l] = (at * 32 + lane) * N;
+            at_row = min(at_row, rows) + step_rows;
+            at += step_rest;
+            if (at >= per) {
+                at -= per;
+                ++at_row;
+            }
             v[l].clear();
-            if (row[l] >= a.rows || col[l] >= a.cols) continue;
-            const T *p = static_cast<const T *>(a.x) + row[l] * a.row_stride + col[l] * a.col_stride;
-            if (a.vec && col[l] + N <= a.cols) v[l].load(p);
-            else v[l].load(p, a.col_stride, a.cols - col[l]);
+            if (row[l] >= rows || col[l] >= cols) continue;
+            const T *p = static_cast<const T *>(a.x) + row[l] * a.row_stride;
+            if (a.vec && col[l] + N <= cols) v[l].load(p + col[l]);
+            else v[l].load(p + col[l] * a.col_stride, a.col_stride, cols - col[l]);
         }
 #pragma unroll
         for (int l = 0; l < LOADS; ++l) {
-            if (row[l] >= a.rows) break;            // the warp's
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < N; ++i) top = max(top, v[l].size(i));
+            if (row[l] >= rows) break;              // the warp's
+            uint32_t top = v[l].largest();
 #pragma unroll
             for (int o = LANES / 2; o; o /= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (col[l] >= a.cols) continue;
+            if (col[l] >= cols) continue;
             const Scale s = scale_of(top);
             if (lane % LANES == 0) a.r.scales[row[l] * a.r.scale_stride + col[l] / TN_BLOCK8 * a.r.scale_block] = s.s;
             uint32_t w[N / 4];
 #pragma unroll
-            for (int i = 0; i < N / 4; ++i)
-                w[i] = codes4(scaled(v[l][4 * i], s.inverse), scaled(v[l][4 * i + 1], s.inverse),
-                              scaled(v[l][4 * i + 2], s.inverse), scaled(v[l][4 * i + 3], s.inverse));
+            for (int i = 0; i < N / 4; ++i) {
+                const float2 x = mul2(make_float2(v[l][4 * i], v[l][4 * i + 1]), make_float2(s.inverse, s.inverse));
+                const float2 y = mul2(make_float2(v[l][4 * i + 2], v[l][4 * i + 3]), make_float2(s.inverse, s.inverse));
+                w[i] = s.inverse == 0.f ? 0 : codes4(x.x, x.y, y.x, y.y);
+            }
             uint8_t *to = a.r.codes + row[l] * a.r.row_stride + col[l];
-            if (col[l] + N <= a.cols) {
+            if (col[l] + N <= cols) {
                 if constexpr (N == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
                 else *reinterpret_cast<uint32_t *>(to) = w[0];
             } else {
 #pragma unroll
                 for (int i = 0; i < N - 1; ++i)
-                    if (col[l] + i < a.cols) to[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
+                    if (col[l] + i < cols) to[i] = static_cast<uint8_t>(w[i / 4] >> (8 * (i % 4)));
             }
         }
     }
