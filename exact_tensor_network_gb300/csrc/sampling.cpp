@@ -79,7 +79,8 @@ tn_status tn_sampler_create(int32_t type, int64_t cols, int64_t max_rows, float 
         s.rest_off = align(s.partial_off + tn::kDrawTarget * sizeof(ulonglong2));
         s.list_off = align(s.rest_off + tn::kDrawTarget * sizeof(uint64_t));
         s.mass_off = align(s.list_off + cut * tn::kSorted * sizeof(uint64_t));
-        s.ws_bytes = align(s.mass_off + static_cast<uint64_t>(n) * 8);
+        s.tie_off = align(s.mass_off + static_cast<uint64_t>(n) * 8);
+        s.ws_bytes = align(s.tie_off + static_cast<uint64_t>(n) * 4);
     } else {
         s.clear_bytes = s.ws_bytes = at;
     }
@@ -167,6 +168,7 @@ tn_status tn_sampler_draw(tn_sampler_t *h, const tn_rows *r, const tn_filters *f
         a.alls = reinterpret_cast<uint64_t *>(s.ws + s.rest_off);
         a.lists = reinterpret_cast<uint64_t *>(s.ws + s.list_off);
         a.masses = reinterpret_cast<uint64_t *>(s.ws + s.mass_off);
+        a.ties = reinterpret_cast<uint32_t *>(s.ws + s.tie_off);
     }
     if (r->rows * (a.segs + ceil_div(draws, tn::kDrawWarps)) > 0x7fffffff)
         return fail(s.error, TN_EOVERFLOW, "too many draws or rows for one call");

@@ -3,10 +3,14 @@
 // An outcome is a whole number, and near a border between two outcomes any
 // rounding decides it: a sum of 10^5 weights in fp32 is wrong by some 2^-22, and one
 // draw in ten of a broad row lies that near to a border.  So weights are computed as
-// pairs of fp32 numbers (43 bits) and summed as 64-bit integers, in
+// pairs of fp32 numbers (2^-44) and summed as 64-bit integers, in
 // units of 2^-shift of the largest, the shift chosen by an estimate of the row's
 // sum so that it uses 61 bits.  Integer sums need no order: histograms by
 // shared-memory atomics, partial sums of CTAs and of warps are all exact.
+//
+// Rows of up to 8 KiB stay in the registers of a warp or a CTA, a few longer ones (up to
+// 32768 entries) in those of a cluster; all others are cut into segments and read twice, or three
+// times where they are filtered.
 #pragma once
 
 #include "outcomes.cuh"
@@ -1335,6 +1339,9 @@ struct RowState {
     uint64_t total;         // weights left
     uint32_t arrived[3];
     uint32_t listed;
+    uint32_t key_hi, key_not;       // of a range too full to be listed: largest key, largest complement of one
+    // sums of estimates of all weights and of those above the bins looked into, in the bins' units
+    unsigned long long rough, rough_above;
 };
 enum { kBinned = 1, kListed = 2 };
 
@@ -1554,17 +1561,31 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
     const uint32_t above0 = FINE ? st.above : 0;
     if (FINE && last - first >= kBins) return;
     __syncthreads();
+    const float unit = !Entry<TYPE>::kReal && p.unit ? __fdiv_rn(1.f, p.m * p.down) : 1.f;
+    float rough = 0.f, rough_above = 0.f;
     each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t, int) {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const int s = slot_of<TYPE>(p, bin_scale, v[i]);
             if (FINE) {
                 if (v[i] != absent<TYPE>() && s >= first && s <= last) atomicAdd(&count[s - first], 1u);
+                if (by_mass && v[i] != absent<TYPE>()) {
+                    const float w = rough_weight<TYPE>(p, v[i]) * unit;
+                    rough += w;
+                    rough_above += s < first ? w : 0.f;
+                }
             } else {
                 atomicAdd(&count[v[i] == absent<TYPE>() ? kBins + threadIdx.x % 32 : s / kSlots], 1u);
             }
         }
     });
+    // numbers, and weights about: in units of which the row's largest possible sum takes 62 bits
+    int log_cols;
+    frexpf(static_cast<float>(a.r.cols) * 1.01f, &log_cols);
+    if (FINE && by_mass) {
+        atomicAdd(&st.rough, static_cast<unsigned long long>(in_units(rough, 61 - log_cols)));
+        atomicAdd(&st.rough_above, static_cast<unsigned long long>(in_units(rough_above, 61 - log_cols)));
+    }
     __syncthreads();
     RowBins *all = a.segs > 1 ? a.bins + c.row : nullptr;
     if (all) {
@@ -1572,9 +1593,6 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
             if (count[i]) atomicAdd(&all->count[i], count[i]);
         if (!last_of_row(a, st, 1)) return;
     }
-    // numbers, and weights about: in units of which the row's largest possible sum takes 62 bits
-    int log_cols;
-    frexpf(static_cast<float>(a.r.cols) * 1.01f, &log_cols);
     const auto middle = [&](int b) {
         if constexpr (Entry<TYPE>::kReal) {
             if (TYPE == TN_TYPE_BF16 && !FINE) {
@@ -1635,16 +1653,17 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
         if (threadIdx.x == 0) st.narrow = 0;
         return;
     }
-    // FINE: the weight above the range is not known but by the row's: what the first pass had
-    const uint64_t total = FINE ? st.total : sums[kDrawWarps];
+    // FINE: the weights above the bins and of all, better known by now than from bins' middles
+    const uint64_t total = FINE ? __ldcg(&st.rough) : sums[kDrawWarps];
     uint64_t target = cut_k ? k : share(top_p, total, false);
-    const uint64_t base = cut_k ? above0 : FINE ? st.cut.bound : 0;
-    // the bins that meet the target give or take the error of their middles, less of it
-    // where those hold too many
+    const uint64_t base = cut_k ? above0 : FINE ? __ldcg(&st.rough_above) : 0;
+    // the bins that meet the target give or take the error of their middles (that of exponentials
+    // in fp32, where those do not count), less of it where those hold too many
+    constexpr int kOff = FINE ? 17 : 10;
+    const bool again = !FINE && a.r.cols >= kLongRow;       // (four bins are looked into once more)
     uint32_t expected = 0, above = 0;
-    uint64_t base_mass = 0;
     for (int round = 0; round < 4; ++round) {
-        const uint64_t off = cut_k ? 0 : round == 0 ? total >> 10 : round == 1 ? total >> 12 : round == 2 ? total >> 14 : 0;
+        const uint64_t off = cut_k || round == 3 ? 0 : total >> (kOff + 2 * round);
         __syncthreads();
         if (threadIdx.x == 0) {
             range[0] = kBins;
@@ -1673,26 +1692,21 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
         if (range[1] < 0) range[1] = -1;        // (none: past all of them)
         const int r0 = both ? 0 : range[0], r1 = range[1];
         // what lies above the range and in it: the thread with its first and the one with its last bin know
-        __shared__ uint64_t at_range[3];
-        if (threadIdx.x == 0) at_range[0] = at_range[1] = at_range[2] = 0;
+        __shared__ uint64_t at_range[2];
+        if (threadIdx.x == 0) at_range[0] = at_range[1] = 0;
         __syncthreads();
         if (r1 >= 0 && (threadIdx.x == r0 / kOwn || threadIdx.x == r1 / kOwn)) {
-            uint64_t n = before_count, w = before_mass;
+            uint64_t n = before_count;
             for (int b = threadIdx.x * kOwn; b < (static_cast<int>(threadIdx.x) + 1) * kOwn; ++b) {
-                if (b == r0) {
-                    at_range[0] = n;
-                    at_range[1] = w;
-                }
+                if (b == r0) at_range[0] = n;
                 n += number(b);
-                w += mass_of(b);
-                if (b == r1) at_range[2] = n;
+                if (b == r1) at_range[1] = n;
             }
         }
         __syncthreads();
         above = static_cast<uint32_t>(at_range[0]);
-        base_mass = at_range[1];
-        expected = static_cast<uint32_t>(at_range[2] - at_range[0]);
-        if (cut_k || (range[1] >= 0 && expected <= kSorted)) break;
+        expected = static_cast<uint32_t>(at_range[1] - at_range[0]);
+        if (cut_k || (range[1] >= 0 && (expected <= kSorted || (again && range[1] - range[0] < kBins / kSlots)))) break;
     }
     // Too many from the top to top_k's bin: a range of its own for top_p, whose whole is the weight of
     // top_k entries, and top_k's bin as a second one where that does not reach it.
@@ -1771,7 +1785,6 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
         st.above = from_top ? 0 : above0 + above;
         st.two = two;
         st.above2 = above2;
-        st.total = total;
         if (!cut_k) st.top_k = 0;
         st.narrow = kListed;
     }
@@ -1786,8 +1799,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
     }
     __syncthreads();
     if (threadIdx.x != 0) return;
-    // (the bound is not known yet: until then the weight above the range, for the fine bins)
-    st.cut = {values[0], values[1], base + base_mass, values[2], values[3]};
+    st.cut = {values[0], values[1], 0, values[2], values[3]};
     if (p.bound > kPresent && slot_of<TYPE>(p, bin_scale, st.min_value) < lo) {
         st.narrow = 0;
         st.cut = {st.min_value, st.min_value, p.bound, 0.f, 0.f};
@@ -1829,7 +1841,7 @@ __device__ __forceinline__ void sort_ranks(uint64_t *x, int n) {
 // does not lie in the list after all; `more` and `joined`: weight and number of what joined.
 template <int TYPE>
 __device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, int n, const float *roots, uint64_t above,
-                                          uint64_t all, int head, int64_t pieces, int64_t seg_pieces, uint64_t *masses,
+                                          uint64_t below, int head, int64_t pieces, int64_t seg_pieces, uint64_t *masses,
                                           ulonglong2 *parts, uint64_t *sums, uint64_t &more, uint64_t &joined) {
     constexpr int E = Entry<TYPE>::E, kOwn = kSorted / kDrawThreads;
     const RowPlan p = st.plan;
@@ -1876,8 +1888,8 @@ __device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, in
         if (threadIdx.x == 0) found = 0;
         uint64_t upto = above + cta_scan(own, sums);
         const uint64_t in = sums[kDrawWarps];
-        // of all that top_k leaves, or of all
-        uint64_t target = share(st.top_p, st.two ? above + in + all : st.top_k > 0 ? above + in : all, true);
+        // of all that top_k leaves, or of all (equal entries' weights as they are added up here)
+        uint64_t target = share(st.top_p, above + in + below, true);
         if (target == 0) target = 1;
         if (target <= above || target > above + in) return 0;
 #pragma unroll
@@ -1908,6 +1920,75 @@ __device__ __noinline__ uint64_t cut_list(const RowState &st, uint64_t *list, in
     cta_scan(num, sums);
     joined = sums[kDrawWarps];
     return bound;
+}
+
+// The same of a range whose entries all have the key `key`, by their numbers in the pieces (`ties`): of equal
+// entries the first ones are left.  kept: how many lie above the range.
+template <int TYPE>
+__device__ __noinline__ uint64_t cut_ties(const RowState &st, const Segment<TYPE> &c, uint32_t key, const float *roots,
+                                          uint64_t above, uint64_t below, uint64_t kept, int64_t pieces, int64_t seg_pieces,
+                                          uint64_t *masses, const uint32_t *ties, ulonglong2 *parts, uint64_t *sums,
+                                          uint64_t &more, uint64_t &joined) {
+    constexpr int E = Entry<TYPE>::E;
+    __shared__ uint64_t cut_need, cut_bound;
+    __shared__ int64_t cut_piece;
+    if (st.two) return 0;
+    const RowPlan p = st.plan;
+    const int64_t per = (pieces + kDrawThreads - 1) / kDrawThreads, lo = threadIdx.x * per;
+    const int64_t hi = lo + per < pieces ? lo + per : pieces;
+    uint64_t own = 0;
+    for (int64_t q = lo; q < hi; ++q) own += __ldcg(&ties[q]);
+    uint64_t before = cta_scan(own, sums);
+    uint64_t need = sums[kDrawWarps];
+    const uint64_t w = weight_once<TYPE>(p, roots, key_value(key));
+    if (st.top_k > 0) {
+        if (static_cast<uint64_t>(st.top_k) <= kept || st.top_k - kept > need) return 0;
+        need = st.top_k - kept;
+    }
+    if (st.top_p < 1.f) {
+        uint64_t target = share(st.top_p, above + need * w + below, true);
+        if (target == 0) target = 1;
+        if (target <= above || target > above + need * w) return 0;
+        need = (target - above + w - 1) / w;
+    }
+    if (p.bound > kPresent && p.bound >> 32 > key) return p.bound;      // (min_p leaves none of them)
+    for (int64_t q = lo; q < hi && before < need; ++q) {
+        const uint64_t n = __ldcg(&ties[q]), take = n < need - before ? n : need - before;
+        if (take > 0) {
+            masses[q] += take * w;
+            if (parts) atomicAdd(reinterpret_cast<unsigned long long *>(&parts[q / seg_pieces].x), static_cast<unsigned long long>(take * w));
+        }
+        before += n;
+        if (before >= need) {
+            cut_piece = q;
+            cut_need = take;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        uint64_t upto = 0;
+        for (int i = 0; i < kPieceVecs / 32; ++i) {
+            const int64_t j = cut_piece * kPieceVecs + i * 32 + threadIdx.x;
+            float v[E];
+            uint64_t n = 0;
+            if (j < c.vecs) {
+                vector_values<TYPE>(c.r, j, v);
+#pragma unroll
+                for (int k = 0; k < E; ++k) n += order_key<TYPE>(v[k]) == key;
+            }
+            uint64_t at = upto + warp_scan(n, threadIdx.x) - n;
+            upto = shfl_from(at + n, 31);
+            if (j < c.vecs) {
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (order_key<TYPE>(v[k]) == key && ++at == cut_need) cut_bound = rank_of<TYPE>(v[k], j * E - c.r.head + k);
+            }
+        }
+    }
+    __syncthreads();
+    more = need * w;
+    joined = need;
+    return cut_bound;
 }
 
 // More equal (or nearly equal) entries than are sorted, or a cut elsewhere: digit by digit, and the
@@ -1973,21 +2054,27 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
     // (on its way early: whichever CTA ends the row makes the draws)
     const double u = a.draws <= kFewDraws && warp < a.draws ? random_number(a, c.row * a.draws + warp) : 0.0;
     uint64_t *masses = a.masses + c.row * a.pieces;
-    const bool lists = FILTERED && st.narrow == kListed, sorted = !lists || st.expected <= kSorted;
-    // the weight of all entries is wanted, or of those between two ranges
+    const bool lists = FILTERED && st.narrow == kListed, passes = !lists || st.expected != 0xffffffffu;
+    // too many for a list: if all of the range are equal, pieces' numbers of them will do
+    const bool tied = lists && st.expected > kSorted, sorted = passes && !tied;
+    uint32_t *ties = FILTERED ? a.ties + c.row * a.pieces : nullptr;
+    uint32_t key_hi = 0, key_not = 0;
+    // the weight of what lies below the range is wanted, all of it or as far as the second range
     const bool two = lists && st.two, by_mass = lists && st.top_p < 1.f && (st.top_k <= 0 || two);
     Cut cut = st.cut;
+    const float lowest = two ? cut.gate2 : least_present<TYPE>();
     uint64_t *to = a.segs > 1 ? a.lists + c.row * kSorted : list;
     uint32_t *counter = a.segs > 1 ? &st.listed : &listed;
     uint64_t total = 0, all = 0;
     uint32_t number = 0;
-    if (sorted) {
+    if (passes) {
         int64_t in_lo, in_hi;
         c.r.inside_range(in_lo, in_hi);
 #pragma unroll 1
         for (int64_t q = c.lo / kPieceVecs + 2 * warp; q * kPieceVecs < c.hi; q += 2 * kDrawWarps) {
             // two pieces, their loads in flight together
             uint64_t both[2] = {0, 0};
+            uint32_t in_piece[2] = {0, 0};
             vectors_at<TYPE, 2 * kPieceVecs / 32>(
                 c.r, in_lo, in_hi, q * kPieceVecs, (q + 2) * kPieceVecs, q * kPieceVecs + lane, 32, c.hi,
                 [&](const float (&v)[E], int64_t j, int which) {
@@ -2012,12 +2099,10 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                                                                    v[k + 1] != absent<TYPE>());
                                     const float2 f = make_float2(above0 ? 1.f : 0.f, above1 ? 1.f : 0.f);
                                     sum.add(mul2(w.hi, f), mul2(w.lo, f));
-                                    if (two) {
-                                        const float2 c = make_float2(v[k] < cut.list && v[k] >= cut.gate2 ? 1.f : 0.f,
-                                                                     v[k + 1] < cut.list && v[k + 1] >= cut.gate2 ? 1.f : 0.f);
+                                    if (by_mass) {
+                                        const float2 c = make_float2(v[k] < cut.list && v[k] >= lowest ? 1.f : 0.f,
+                                                                     v[k + 1] < cut.list && v[k + 1] >= lowest ? 1.f : 0.f);
                                         whole.add(mul2(w.hi, c), mul2(w.lo, c));
-                                    } else if (by_mass) {
-                                        whole.add(w.hi, w.lo);
                                     }
                                 } else {
                                     const Weights w = weight_pairs(p, roots, v[k], v[k + 1], above0, above1);
@@ -2034,7 +2119,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                             const bool above = v[k] >= cut.gate, below = !(v[k] >= cut.list);
                             const bool second = FILTERED && two && v[k] < cut.gate2 && v[k] >= cut.list2;
                             if (FILTERED && !above && (!below || second)) in |= 1u << k;
-                            const bool counts = FILTERED && by_mass && v[k] != absent<TYPE>() && (!two || (below && v[k] >= cut.gate2));
+                            const bool counts = FILTERED && by_mass && below && v[k] >= lowest;
                             if (!above && !counts) continue;
                             const uint64_t w = weight<TYPE>(p, roots, v[k]);
                             own += above ? w : 0;
@@ -2045,6 +2130,21 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                     both[0] += which < kPieceVecs / 32 ? own : 0;
                     both[1] += which < kPieceVecs / 32 ? 0 : own;
                     if (!FILTERED || !lists || !in) return;
+                    if (tied) {
+                        in_piece[0] += which < kPieceVecs / 32 ? __popc(in) : 0;
+                        in_piece[1] += which < kPieceVecs / 32 ? 0 : __popc(in);
+#pragma unroll 1
+                        for (uint32_t rest = in; rest; rest &= rest - 1) {
+                            const int at = __ffs(rest) - 1;
+                            float x = v[0];
+#pragma unroll
+                            for (int k = 1; k < E; ++k) x = k == at ? v[k] : x;
+                            const uint32_t key = order_key<TYPE>(x);
+                            key_hi = max(key_hi, key);
+                            key_not = max(key_not, ~key);
+                        }
+                        return;
+                    }
                     uint32_t at = atomicAdd(counter, static_cast<uint32_t>(__popc(in)));
 #pragma unroll
                     for (int k = 0; k < E; ++k)
@@ -2060,6 +2160,22 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
                 __stcg(&masses[q], both[0]);
                 if ((q + 1) * kPieceVecs < c.hi) __stcg(&masses[q + 1], both[1]);
             }
+            if (FILTERED && tied) {
+                in_piece[0] = __reduce_add_sync(0xffffffffu, in_piece[0]);
+                in_piece[1] = __reduce_add_sync(0xffffffffu, in_piece[1]);
+                if (lane == 0) {
+                    __stcg(&ties[q], in_piece[0]);
+                    if ((q + 1) * kPieceVecs < c.hi) __stcg(&ties[q + 1], in_piece[1]);
+                }
+            }
+        }
+    }
+    if (FILTERED && tied && passes) {
+        key_hi = __reduce_max_sync(0xffffffffu, key_hi);
+        key_not = __reduce_max_sync(0xffffffffu, key_not);
+        if (lane == 0) {
+            atomicMax(&st.key_hi, key_hi);
+            atomicMax(&st.key_not, key_not);
         }
     }
     cta_scan(total, sums);
@@ -2096,6 +2212,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
             all = sums[kDrawWarps];
         }
     } else {
+        if (FILTERED && tied) __threadfence();
         __syncthreads();        // the pieces' sums and the list
     }
     const int64_t pieces = (c.vecs + kPieceVecs - 1) / kPieceVecs;
@@ -2114,6 +2231,15 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
             kept += joined;
             cut.bound = bound;
         }
+        const uint32_t key = tied && passes ? __ldcg(&st.key_hi) : 0;
+        if (key != 0 && key == ~__ldcg(&st.key_not)) {
+            uint64_t more = 0, joined = 0;
+            bound = cut_ties<TYPE>(st, c, key, roots, total, all, kept, pieces, a.seg_pieces, masses, ties, parts, sums, more,
+                                   joined);
+            total += more;
+            kept += joined;
+            cut.bound = bound;
+        }
         if (bound == 0) {
             cut = by_digits<TYPE>(a, c, st, p, roots, &sel, masses, parts, pieces, sums, nums);
             total = sums[kDrawWarps];
@@ -2122,6 +2248,10 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
     }
     __threadfence();
     __syncthreads();
+    if (FILTERED && threadIdx.x == 0) {
+        st.key_hi = st.key_not = 0;
+        st.rough = st.rough_above = 0;
+    }
     // sums up to each segment, of consecutive ones by a thread each
     __shared__ uint64_t upto_segment[kDrawThreads];
     const bool few = a.segs <= kDrawThreads;

@@ -45,6 +45,7 @@ struct SampleArgs {
     int64_t pieces;         // of a row
     int64_t segs, seg_pieces;
     uint64_t *masses;       // [rows][pieces]
+    uint32_t *ties;         // [rows][pieces] equal entries where a filter cuts through many
     // of rows in segments: state [rows]; partial results [rows][segs] of
     // segments, first maxima with rough sums, then sums and counts, and sums of all
     // entries; and, of several segments, bins [rows] and lists [rows][kSorted]
@@ -60,7 +61,7 @@ struct Sampler {
     int64_t cols = 0, max_rows = 0;
     float scale = 1.f;
     uint64_t ws_bytes = 0, clear_bytes = 0;
-    uint64_t state_off = 0, bins_off = 0, partial_off = 0, rest_off = 0, list_off = 0, mass_off = 0;
+    uint64_t state_off = 0, bins_off = 0, partial_off = 0, rest_off = 0, list_off = 0, mass_off = 0, tie_off = 0;
     char *ws = nullptr;
     char error[256] = {0};
 };

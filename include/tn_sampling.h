@@ -25,9 +25,10 @@
  *   - A row without present entries has outcome -1, log p -inf and kept 0; a row
  *     without a distribution, or one with an invalid parameter, outcome -1, log p NaN and
  *     kept 0.  A draw with an invalid u has outcome -1 and log p NaN.
- * Weights are computed to some 43 bits and summed as 64-bit integers, so that
- * an outcome is that of the definition but where u (or top_p) lies within some
- * 2^-43 of a border between two.  Results do not depend on timing.
+ * Weights are computed to some 2^-43 of the largest (those of amplitudes at a beta other than
+ * 1 and up to 2 to 2^-40) and summed as 64-bit integers, so that an outcome is that of the
+ * definition but where u (or top_p) lies that near to a border between two.  Results do not
+ * depend on timing.
  *
  * Invalid parameters: a temperature that is negative or no finite number, a NaN top_p or
  * min_p, a min_p above 1, a u outside [0, 1).  tn_sampler_check reports them.

@@ -233,3 +233,37 @@ def test_refusals():
     with pytest.raises(tn.TNError):
         op.sample(torch.zeros(4, 1, device="cuda").expand(4, 100), u)                       # one entry for all columns
     op.check()
+
+
+@pytest.mark.parametrize("type_,n", [("bf16", 2000003), ("f16", 1 << 21), ("f32", 5000011)])
+@pytest.mark.parametrize("filters", [{"top_p": 0.9}, {"top_p": 0.4}, {"top_k": 5000, "top_p": 0.5}, {"top_k": 3000}], ids=str)
+def test_very_long_rows(type_, n, filters):
+    """16-bit logits of rows this long have thousands of equal entries wherever a filter cuts."""
+    rows, u = _rows(type_, 2, n, 12), _u(2, 3, 4, torch.float64)
+    op = tn.Sampler(n, TYPES[type_], max_rows=2)
+    _many(op.sample(rows.cuda(), u.cuda(), **filters), rows, u.numpy(), **filters)
+    op.check()
+
+
+@pytest.mark.parametrize("n", [9001, 60000, 400001])
+@pytest.mark.parametrize("filters", [{"top_p": 0.1}, {"top_p": 0.7}, {"top_p": 0.95}, {"top_k": 7}, {"top_k": 4000},
+                                     {"top_k": 5000, "top_p": 0.6}, {"top_k": 8000, "top_p": 0.9}], ids=str)
+@pytest.mark.parametrize("draws", [2, 20])
+def test_few_different_values(n, filters, draws):
+    """Rows of four values, among whose equal entries every filter cuts."""
+    g = torch.Generator().manual_seed(n)
+    rows = torch.tensor([-1.0, 0.25, 1.5, 3.0])[torch.multinomial(torch.tensor([0.5, 0.3, 0.15, 0.05]), 3 * n, True,
+                                                                  generator=g)].view(3, n)
+    rows[2, : n // 3] = -math.inf
+    u = _u(3, draws, 7, torch.float64)
+    for dtype in (torch.float32, torch.bfloat16):
+        op = tn.Sampler(n, dtype, max_rows=3)
+        got = op.sample(rows.to(dtype).cuda(), u.cuda(), **filters)
+        _many(got, rows, u.numpy(), **filters)
+        # min_p that cuts above what is equal
+        got = op.sample(rows.to(dtype).cuda(), u.cuda(), min_p=0.5, **filters)
+        most = (rows == 3.0).sum(1)
+        assert (got.kept.cpu() <= most).all() and (got.kept > 0).all()
+        for r in range(3):
+            assert (rows[r, got.ids[r].cpu()] == 3.0).all()
+        op.check()
