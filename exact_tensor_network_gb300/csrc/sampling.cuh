@@ -861,7 +861,9 @@ __device__ __noinline__ uint64_t bound_of(const RowCta<TYPE> &c, const RowPlan &
 // a warp a row, or a CTA of NT threads.  Filters find where they cut by halves of the order
 // values (how many, or how much, lies at or above the middle) until one entry, or one value, is
 // left in question.  Bound by its chain of reductions where rows are filtered, by the weights'
-// arithmetic where not.
+// arithmetic where not: 20000 x 64 amplitudes 32 us (with top_p 48), 16384 x 2048 bf16 147 (372),
+// 1 x 32768 bf16 in a cluster of eight 10 (24, with top_k and top_p 29).  With 16 entries a thread
+// 20000 x 256 bf16 take as long as 20000 x 512 (52 us), with 8 32.
 
 constexpr int kHeldEntries = 16;
 
@@ -1322,7 +1324,14 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
 //                 by exact sums, what is left of it added to the pieces, and a few draws made
 //   draws_kernel  many draws, a warp each
 // The first two are bound by memory, the third by arithmetic (some 50 operations for a
-// weight); launches hide behind each other's ends.
+// weight); launches hide behind each other's ends.  64 x 131072 bf16 44 us (with top_p 121), 1024 x 50001 f16
+// with a mask 170, 4096 shots of 2^24 amplitudes 88.
+//
+// A range with more entries than are listed: rows of kLongRow entries on look once more into up to
+// four bins, each slot a bin; where all of the range are equal (16-bit logits of long rows, uniform
+// states), their numbers in the pieces say how far they are left; else the row's CTA goes digit by
+// digit through the ranks, which takes 100 ms for 2^24 entries (top_k above 2048 together with top_p
+// whose last entry has thousands of equals).
 
 struct RowState {
     RowPlan plan;
@@ -1955,7 +1964,8 @@ __device__ __noinline__ uint64_t cut_ties(const RowState &st, const Segment<TYPE
     for (int64_t q = lo; q < hi && before < need; ++q) {
         const uint64_t n = __ldcg(&ties[q]), take = n < need - before ? n : need - before;
         if (take > 0) {
-            masses[q] += take * w;
+            // (past the L1 cache, which may hold the line as another row's CTA found it)
+            atomicAdd(reinterpret_cast<unsigned long long *>(&masses[q]), static_cast<unsigned long long>(take * w));
             if (parts) atomicAdd(reinterpret_cast<unsigned long long *>(&parts[q / seg_pieces].x), static_cast<unsigned long long>(take * w));
         }
         before += n;
@@ -2375,11 +2385,13 @@ cudaError_t sample_of(const SampleArgs &a, cudaStream_t stream) {
         return cudaErrorInvalidValue;       // (rows of more than kRowVecs vectors have a state)
     }
     // Few rows that a cluster holds: one kernel instead of three, at the price of a barrier of the
-    // cluster for every sum
+    // cluster for every sum.  bf16, by clusters and in segments, us without filters, with top_k, top_p and
+    // both: 40 x 32768 22, 44, 56, 62 and 28, 51, 76, 62; 154 x 8192 19, 37, 43, 60 and 28, 58, 80, 69;
+    // 76 x 32768 33, 74, 89, 119 and 32, 57, 87, 68.
     int ranks = 2;
     while (ranks <= kMostRanks && entries > ranks * kDrawThreads * kHeldEntries) ranks *= 2;
     const bool both = (a.f.top_ks || a.f.top_k > 0) && (a.f.top_ps || a.f.top_p < 1.f);
-    if (ranks <= kMostRanks && a.r.rows * ranks <= (both ? 2 : 3) * kOutSms && a.draws <= kFewDraws)
+    if (ranks <= kMostRanks && a.r.rows * ranks <= (both ? 2 : 3) * kOutSms && a.draws <= 2 * kFewDraws)
         return launch_ranks<TYPE>(a, ranks, stream);
     const dim3 block(kDrawThreads), grid(static_cast<unsigned>(a.r.rows * a.segs));
     cudaError_t e = launch_pdl(top_kernel<TYPE>, grid, block, 0, stream, a);
