@@ -15,8 +15,9 @@ lays those of rows out with the rows next to each other, which products read fas
 All tensors of a call and its stream are on the current device.  Calls are
 asynchronous on ``stream`` (default: torch's current stream); on another stream
 the caller orders it after the inputs' producers, the inputs and outputs are recorded
-on it, and what the call makes belongs to it.  Every call runs in the library's
-CUDA kernels; there is no fallback.
+on it, and what the call makes belongs to it.  Nothing is recorded for automatic
+differentiation: ``linear8_grad`` is the backward pass.  Every call runs in the
+library's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations
 

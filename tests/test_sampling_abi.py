@@ -97,6 +97,52 @@ def test_sampler_refuses_host_tensors():
         tn.Sampler(16, torch.float64)
 
 
+class _Tensor:
+    """What a call looks at before it launches anything, on any device."""
+
+    def __init__(self, device, shape=(2, 16)):
+        import torch
+        self.device, self.shape, self.dtype, self.is_cuda = torch.device(device), shape, torch.float32, True
+
+    def stride(self):
+        return (self.shape[1], 1)
+
+    def dim(self):
+        return len(self.shape)
+
+    def data_ptr(self):
+        return 4096
+
+    def is_conj(self):
+        return False
+
+    is_neg = is_conj
+
+
+@pytest.mark.parametrize("bound, current, rows", [(0, 0, 1), (0, 1, 1), (0, 1, 0), (None, 0, 1)])
+def test_rows_of_another_device_are_refused(bound, current, rows, monkeypatch):
+    """On the host, before anything is bound or launched: a kernel would run on the current device with
+    another one's addresses."""
+    import torch
+    op = tn.Sampler(16, torch.float32, max_rows=2)
+    monkeypatch.setattr(op, "_L", None)
+    monkeypatch.setattr(op, "_current_device", lambda: current)
+    monkeypatch.setattr(op, "bind_workspace", lambda device=None: pytest.fail("workspace bound"))
+    if bound is not None:
+        op._ws, op._index = object(), bound
+    with pytest.raises(ValueError, match="cuda"):
+        op.sample(_Tensor(f"cuda:{rows}"), _Tensor(f"cuda:{rows}", (2,)))
+    op._ws = None
+
+
+def test_matrices_of_another_device_are_refused(monkeypatch):
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    for call in (lambda x: tn.quantize8(x), lambda x: tn.linear8(x, None), lambda x: tn.linear8_grad(x, x, None)):
+        with pytest.raises(ValueError, match="not the current device"):
+            call(_Tensor("cuda:1"))
+
+
 def test_sampler_reference_closed_forms():
     z = np.log(np.array([1, 2, 4, 1], np.float64)).astype(np.float32)
     assert list(ref.left(z, None, 1.0)) == [0, 1, 2, 3]
