@@ -21,6 +21,14 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int WARP_ROWS = kB8Tile / (THREADS / 32);     // 16
 
+// The bits of a magnitude as fp32's.
+template <typename T>
+__device__ __forceinline__ uint32_t as_float(uint32_t raw) {
+    if constexpr (sizeof(T) == 4) return raw;
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value) return raw << 16;
+    else return __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(raw))));
+}
+
 // Neighbouring entries as they lie in memory, and their values.
 template <typename T, int N>
 struct Raw {
@@ -65,21 +73,17 @@ struct Raw {
         }
     }
     __device__ __forceinline__ uint32_t size(int i) const { return __float_as_uint((*this)[i]) & 0x7fffffffu; }
-    // the largest of all sizes (of 16-bit types two at a time, as they lie)
-    __device__ __forceinline__ uint32_t largest() const {
+    // The largest of all sizes, of 16-bit types as they lie (two at a time; their bits have the same order).
+    __device__ __forceinline__ uint32_t largest_raw() const {
         uint32_t m = w[0] & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
-        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 1; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
-            return m;
-        } else {
-#pragma unroll
-            for (int i = 1; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-            Raw<T, 2> one;
-            one.w[0] = max(m & 0xffffu, m >> 16);
-            return one.size(0);
+        for (int i = 1; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) m = max(m, w[i] & 0x7fffffffu);
+            else m = __vmaxu2(m, w[i] & 0x7fff7fffu);
         }
+        return sizeof(T) == 4 ? m : max(m & 0xffffu, m >> 16);
     }
+    __device__ __forceinline__ uint32_t largest() const { return as_float<T>(largest_raw()); }
 };
 
 // The scale of a block whose largest magnitude has the bits `top`, and what
@@ -105,15 +109,18 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
 }
-// (0 * infinity and 0 * NaN are not 0)
-__device__ __forceinline__ float scaled(float x, float inverse) { return inverse == 0.f ? 0.f : x * inverse; }
-
 // a b, packed
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;
     asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
+}
+
+// Codes of four entries (0 where there is a NaN or an infinity in the block: 0 times those is not 0).
+__device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d, float inverse) {
+    const float2 by = make_float2(inverse, inverse), x = mul2(make_float2(a, b), by), y = mul2(make_float2(c, d), by);
+    return inverse == 0.f ? 0 : codes4(x.x, x.y, y.x, y.y);
 }
 
 // Codes in the layout of x alone, with a scale for 128 entries of a row: 16 bytes of
@@ -163,11 +170,8 @@ __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const QuantArgs 
             if (lane % LANES == 0) a.r.scales[row[l] * a.r.scale_stride + col[l] / TN_BLOCK8 * a.r.scale_block] = s.s;
             uint32_t w[N / 4];
 #pragma unroll
-            for (int i = 0; i < N / 4; ++i) {
-                const float2 x = mul2(make_float2(v[l][4 * i], v[l][4 * i + 1]), make_float2(s.inverse, s.inverse));
-                const float2 y = mul2(make_float2(v[l][4 * i + 2], v[l][4 * i + 3]), make_float2(s.inverse, s.inverse));
-                w[i] = s.inverse == 0.f ? 0 : codes4(x.x, x.y, y.x, y.y);
-            }
+            for (int i = 0; i < N / 4; ++i)
+                w[i] = codes_of(v[l][4 * i], v[l][4 * i + 1], v[l][4 * i + 2], v[l][4 * i + 3], s.inverse);
             uint8_t *to = a.r.codes + row[l] * a.r.row_stride + col[l];
             if (col[l] + N <= cols) {
                 if constexpr (N == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
@@ -192,25 +196,37 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : 3) quantize_kern
     const int64_t r0 = rt * kB8Tile + warp * WARP_ROWS, c0 = ct * kB8Tile + lane * 4;
     const T *x = static_cast<const T *>(a.x) + r0 * a.row_stride + c0 * a.col_stride;
 
+    const int here = static_cast<int>(a.rows - r0 < WARP_ROWS ? a.rows - r0 : WARP_ROWS);    // rows (none if below 0)
+    const int left = static_cast<int>(a.cols - c0 < 4 ? a.cols - c0 : 4);                    // entries of a row
+
     Raw<T, 4> v[WARP_ROWS];
-    if (a.vec && c0 + 4 <= a.cols) {
+    if (a.vec && left == 4) {
 #pragma unroll
-        for (int i = 0; i < WARP_ROWS; ++i) {
-            if (r0 + i < a.rows) v[i].load(x + i * a.row_stride);
+        for (int i = 0; i < WARP_ROWS; ++i, x += a.row_stride) {
+            if (i < here) v[i].load(x);
             else v[i].clear();
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < WARP_ROWS; ++i)
-            v[i].load(x + i * a.row_stride, a.col_stride, r0 + i < a.rows ? a.cols - c0 : 0);
+        for (int i = 0; i < WARP_ROWS; ++i, x += a.row_stride) v[i].load(x, a.col_stride, i < here ? left : 0);
     }
 
     uint32_t ctop[4] = {0, 0, 0, 0};
     if (SQUARE || a.c.codes) {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < WARP_ROWS; ++i)
+            for (int i = 0; i < WARP_ROWS; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) ctop[j] = max(ctop[j], v[i].size(j));
+                for (int j = 0; j < 4; ++j) ctop[j] = max(ctop[j], v[i].size(j));
+        } else {
+            uint32_t pair[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < WARP_ROWS; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) pair[j] = __vmaxu2(pair[j], v[i].w[j] & 0x7fff7fffu);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ctop[j] = as_float<T>(pair[j / 2] >> (16 * (j % 2)) & 0xffffu);
+        }
     }
     Scale tile = {1.f, 1.f};
     if (SQUARE) {
@@ -224,27 +240,30 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : 3) quantize_kern
         }
     }
     if (a.r.codes) {
-        const bool whole = c0 + 4 <= a.cols;
+        // (a row's scale is made by the lane of its number, and handed to the others)
+        Scale own = tile;
+        if (!SQUARE) {
+            uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < WARP_ROWS; ++i) {
-            Scale s = tile;
-            if (!SQUARE) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, v[i].size(j));
-                s = scale_of(__reduce_max_sync(0xffffffffu, top));
+            for (int i = 0; i < WARP_ROWS; ++i) {
+                const uint32_t row_top = __reduce_max_sync(0xffffffffu, v[i].largest_raw());
+                top = lane == i ? row_top : top;
             }
-            if (r0 + i >= a.rows) continue;
-            if (!SQUARE && lane == 0) a.r.scales[(r0 + i) * a.r.scale_stride + ct * a.r.scale_block] = s.s;
-            const uint32_t w = codes4(scaled(v[i][0], s.inverse), scaled(v[i][1], s.inverse),
-                                      scaled(v[i][2], s.inverse), scaled(v[i][3], s.inverse));
-            uint8_t *to = a.r.codes + (r0 + i) * a.r.row_stride + c0;
-            if (whole) {
+            own = scale_of(as_float<T>(top));
+            if (lane < here) a.r.scales[(r0 + lane) * a.r.scale_stride + ct * a.r.scale_block] = own.s;
+        }
+        uint8_t *to = a.r.codes + r0 * a.r.row_stride + c0;
+#pragma unroll
+        for (int i = 0; i < WARP_ROWS; ++i, to += a.r.row_stride) {
+            const float inverse = SQUARE ? tile.inverse : __shfl_sync(0xffffffffu, own.inverse, i);
+            const uint32_t w = codes_of(v[i][0], v[i][1], v[i][2], v[i][3], inverse);
+            if (i >= here) continue;
+            if (left == 4) {
                 *reinterpret_cast<uint32_t *>(to) = w;
             } else {
 #pragma unroll
                 for (int j = 0; j < 3; ++j)
-                    if (c0 + j < a.cols) to[j] = static_cast<uint8_t>(w >> (8 * j));
+                    if (j < left) to[j] = static_cast<uint8_t>(w >> (8 * j));
             }
         }
     }
@@ -274,8 +293,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : 3) quantize_kern
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                w[i] = codes4(scaled(v[4 * i][j], s[j].inverse), scaled(v[4 * i + 1][j], s[j].inverse),
-                              scaled(v[4 * i + 2][j], s[j].inverse), scaled(v[4 * i + 3][j], s[j].inverse));
+                w[i] = codes_of(v[4 * i][j], v[4 * i + 1][j], v[4 * i + 2][j], v[4 * i + 3][j], s[j].inverse);
             turned[(lane * 4 + j) * 8 + (warp ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncthreads();
