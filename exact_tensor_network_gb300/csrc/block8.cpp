@@ -160,8 +160,8 @@ tn_status tn_block8_quantize(const tn_matrix *x, const tn_block8 *rows, const tn
     a.col_tiles = ceil_div(a.cols, tn::kB8Tile);
     if (a.row_tiles > 0x7fffffff / a.col_tiles) return fail(TN_EOVERFLOW, "more than 2^31 - 1 blocks of 128 x 128");
     const bool square = (rows ? rows : columns)->block_rows == TN_BLOCK8;
-    // 16 bytes at once where the rows alone are written, else four entries
-    const int vec = !a.c.codes && !square ? 16 / size : 4;
+    a.few = !a.c.codes && !square && a.rows < 256;
+    const int vec = a.few ? 16 / size : 4;      // entries at once: 16 bytes, or a lane's of a tile
     a.vec = a.col_stride == 1 && reinterpret_cast<uintptr_t>(a.x) % (vec * size) == 0 &&
             (a.row_stride % vec == 0 || a.rows == 1);
     const cudaError_t e = tn::launch_quantize(a, x->type, square, reinterpret_cast<cudaStream_t>(stream));

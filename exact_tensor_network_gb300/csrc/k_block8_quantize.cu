@@ -123,7 +123,7 @@ __device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d,
     return inverse == 0.f ? 0 : codes4(x.x, x.y, y.x, y.y);
 }
 
-// Codes in the layout of x alone, with a scale for 128 entries of a row: 16 bytes of
+// Few rows in the layout of x alone, with a scale for 128 entries of a row: 16 bytes of
 // a row a lane, four loads in flight, no shared memory.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) quantize_rows_kernel(const QuantArgs a) {
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 4 ? 2 : 3) quantize_kern
 
 template <typename T>
 cudaError_t launch(const QuantArgs &a, bool square, cudaStream_t stream) {
-    if (!a.c.codes && !square) {
+    if (a.few) {
         constexpr int64_t kItem = 32 * 16 / sizeof(T);
         const int64_t warps = (a.rows * ((a.cols + kItem - 1) / kItem) + 3) / 4, most = 8 * kB8Sms;
         const int64_t ctas = (warps + THREADS / 32 - 1) / (THREADS / 32);
