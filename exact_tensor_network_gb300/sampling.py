@@ -97,8 +97,8 @@ class Sampler:
     """Owns a handle and (optionally) a torch workspace tensor.
 
     ``cols`` entries a row of ``dtype`` (complex64 amplitudes, or float32,
-    bfloat16 or float16 logits), at most ``max_rows`` rows a call, inverse
-    temperature ``scale`` before any other.
+    bfloat16 or float16 logits), at most ``max_rows`` rows a call and ``draws`` draws
+    of each (None: any number), inverse temperature ``scale`` before any other.
 
     Rows and masks are those of ``Outcomes``.  All tensors of a call, its
     stream and the workspace are on the current device; the first call binds a
@@ -111,12 +111,15 @@ class Sampler:
     workspace are recorded on it.
     """
 
-    def __init__(self, cols: int, dtype=None, max_rows: int = 1, scale: float = 1.0):
+    def __init__(self, cols: int, dtype=None, max_rows: int = 1, scale: float = 1.0, draws: Optional[int] = None):
         import torch
         self.handle = None
         dtype = torch.complex64 if dtype is None else dtype
         if dtype not in _types():
             raise ValueError("dtype must be complex64, float32, bfloat16 or float16")
+        if draws is not None and (draws != int(draws) or draws < 0):
+            raise ValueError("draws must be None or a whole number >= 0")
+        self.draws = None if draws is None else int(draws)
         self.handle = tn_sampler_create(_types()[dtype], int(cols), int(max_rows), float(scale))
         self.cols, self.dtype, self.max_rows, self.scale = int(cols), dtype, int(max_rows), float(scale)
         self._ws, self._ws_streams = None, set()
@@ -217,6 +220,8 @@ class Sampler:
         if not 1 <= len(ushape) <= 2 or ushape[0] != R or u.device != device or not u.is_contiguous():
             raise ValueError(f"u must be a contiguous tensor [{R}] or [{R}, draws] on the rows' device")
         draws = ushape[1] if len(ushape) == 2 else 1
+        if self.draws is not None and draws > self.draws:
+            raise ValueError(f"{draws} draws of a row: the sampler was made for at most {self.draws}")
         f.temperature, f.temperatures = self._parameter(temperature, 1.0, "temperature", self._f32, R, device)
         if isinstance(top_k, int):
             top_k = max(0, min(top_k, self.cols))       # (a larger number would wrap around)
