@@ -220,7 +220,8 @@ def prepare(case, seed):
     f["case"] = dict(case)
     if case["op"] == "sample" and own:
         import exact_tensor_network_gb300 as tn
-        f["op"] = tn.Sampler(case["cols"], _TYPES[case["type"]], max_rows=case["rows"], scale=case["scale"])
+        f["op"] = tn.Sampler(case["cols"], _TYPES[case["type"]], max_rows=case["rows"],
+                             draws=case["draws"], scale=case["scale"])
         f["op"].bind_workspace()
     if case["op"].startswith("linear"):
         # the weights as a program keeps them: 8 bits, for a backward pass transposed
