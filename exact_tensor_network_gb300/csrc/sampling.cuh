@@ -494,7 +494,14 @@ __device__ __forceinline__ int shift_of(float sum) {
     return 61 - x;
 }
 
-// Entries of weight >= min_p of the largest: those of order value >= this.
+// The lowest order value of a present entry.
+template <int TYPE>
+__device__ __forceinline__ constexpr float least_present() {
+    return Entry<TYPE>::kReal ? -3.402823466e38f : 1.4e-45f;
+}
+
+// Entries of weight >= min_p of the largest: those of order value >= this.  (At a high temperature all: the
+// value may lie below any, where the absent entries are.)
 template <int TYPE>
 __device__ __noinline__ float least_value(const RowPlan &p, float min_p) {
     double x;
@@ -503,7 +510,7 @@ __device__ __noinline__ float least_value(const RowPlan &p, float min_p) {
     else x = p.m * exp(log(static_cast<double>(min_p)) / p.beta);
     float v = static_cast<float>(x);
     if (v < x) v = nextafterf(v, __builtin_huge_valf());
-    return fminf(v, p.m);
+    return fminf(fmaxf(v, least_present<TYPE>()), p.m);
 }
 
 // What log p of a draw is computed from: its order value, and the row's sum of weights left.  In 64
@@ -669,11 +676,6 @@ struct Cut {
 template <int TYPE>
 __device__ __forceinline__ bool is_left(const Cut &c, float v, int64_t e) {
     return v >= c.gate || (v >= c.list && rank_of<TYPE>(v, e) >= c.bound);
-}
-// The lowest order value of a present entry.
-template <int TYPE>
-__device__ __forceinline__ constexpr float least_present() {
-    return Entry<TYPE>::kReal ? -3.402823466e38f : 1.4e-45f;
 }
 
 // Weights' sum of a vector's entries that are left, 1 at least for each: of those
