@@ -129,6 +129,8 @@ static __device__ const float4 kLogs[128] = {
 };
 constexpr float kLn2Hi = 0x1.62e4p-1f, kLn2Lo = 0x1.7f7d1cp-20f;    // ln 2 likewise
 
+constexpr float kFarthest = -3.402823466e38f;      // a difference beyond fp32 counts as this one
+
 // What a row's weights are computed from.
 struct RowPlan {
     float m;            // largest order value
@@ -315,10 +317,11 @@ __device__ __forceinline__ void two_weights(const RowPlan &p, const float *roots
     }
 }
 
-// The same in fp32, relative to the largest: for an estimate of the sum.
+// The same in fp32, relative to the largest: for an estimate of the sum.  It must not be far too small, or
+// the sums would overflow.
 template <int TYPE>
 __device__ __forceinline__ float rough_weight(const RowPlan &p, float v) {
-    if constexpr (Entry<TYPE>::kReal) return ex2((v - p.m) * p.ch);
+    if constexpr (Entry<TYPE>::kReal) return ex2(fmaxf(v - p.m, kFarthest) * p.ch);
     else if (p.unit) return v * p.down;
     else return ex2(p.beta * lg2(v / p.m));
 }
@@ -500,6 +503,9 @@ __device__ __forceinline__ constexpr float least_present() {
     return Entry<TYPE>::kReal ? -3.402823466e38f : 1.4e-45f;
 }
 
+// Lower order values count as this one.
+__device__ __forceinline__ float farthest(const RowPlan &p) { return fmaxf(p.m, 0.f) + kFarthest; }
+
 // Entries of weight >= min_p of the largest: those of order value >= this.  (At a high temperature all: the
 // value may lie below any, where the absent entries are.)
 template <int TYPE>
@@ -510,6 +516,7 @@ __device__ __noinline__ float least_value(const RowPlan &p, float min_p) {
     else x = p.m * exp(log(static_cast<double>(min_p)) / p.beta);
     float v = static_cast<float>(x);
     if (v < x) v = nextafterf(v, __builtin_huge_valf());
+    if (Entry<TYPE>::kReal && v <= farthest(p)) v = least_present<TYPE>();      // (lower ones weigh as much as that)
     return fminf(fmaxf(v, least_present<TYPE>()), p.m);
 }
 
@@ -522,8 +529,9 @@ struct LogP {
     int shift;          // weights' unit: 2^-shift of the origin's (of 1 for amplitudes at beta = 1)
     bool greedy, unit, far;
 
-    __device__ __forceinline__ void of(const RowPlan &p, uint64_t t) {
+    __device__ __forceinline__ void of(const RowPlan &p, uint64_t t, float value) {
         total = t;
+        v = fmaxf(value, farthest(p));
         origin = p.origin;
         far = p.far;
         beta = p.beta;
@@ -828,8 +836,7 @@ struct Pending {
     }
     __device__ __forceinline__ void add(const SampleArgs &a, const RowPlan &p, uint64_t total, float v, int64_t where) {
         if (static_cast<int>(threadIdx.x % 32) == n) {
-            l.of(p, total);
-            l.v = v;
+            l.of(p, total, v);
             at = where;
         }
         if (++n == 32) flush(a);
@@ -1449,14 +1456,18 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
 #pragma unroll
         for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
         if (!(top <= m)) {
-            if constexpr (Entry<TYPE>::kReal) s *= ex2((m - top) * ch);
+            if constexpr (Entry<TYPE>::kReal) s *= ex2(fmaxf(m - top, kFarthest) * ch);
             else if (f.beta != 1.f) s *= m > 0.f ? ex2(f.beta * (lg2(m) - lg2(top))) : 0.f;
             m = max_nan(m, top);
         }
         if constexpr (Entry<TYPE>::kReal) {
-            if (top != absent<TYPE>()) {
+            if (top != absent<TYPE>() && ch >= 0x1p-118f) {     // (what is farthest, or absent, adds nothing)
 #pragma unroll
                 for (int i = 0; i < E; ++i) s += ex2((v[i] - m) * ch);
+            } else if (top != absent<TYPE>()) {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (v[i] != absent<TYPE>()) s += ex2(fmaxf(v[i] - m, kFarthest) * ch);
             }
         } else if (f.beta == 1.f) {
 #pragma unroll
@@ -1470,7 +1481,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
     // threads', then segments'
     const auto moved = [&](float from, float to) {
         if (from == absent<TYPE>()) return 0.f;
-        if constexpr (Entry<TYPE>::kReal) return ex2((from - to) * ch);
+        if constexpr (Entry<TYPE>::kReal) return ex2(fmaxf(from - to, kFarthest) * ch);
         else return f.beta == 1.f ? 1.f : ex2(f.beta * (lg2(from) - lg2(to)));
     };
     const float own = m;
@@ -2298,8 +2309,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) sums_kernel(const __grid_cons
             n = pieces - first < a.seg_pieces ? pieces - first : a.seg_pieces;
         }
         LogP l;
-        l.of(p, total);
-        l.v = warp_draw<TYPE>(a, c.r, c.vecs, p, cut, roots, masses, first, n, target, at);
+        l.of(p, total, warp_draw<TYPE>(a, c.r, c.vecs, p, cut, roots, masses, first, n, target, at));
         if (lane == 0) a.logp[at] = log_p<TYPE>(l);
     }
 }
@@ -2338,8 +2348,7 @@ __global__ void __launch_bounds__(kDrawThreads) draws_kernel(const __grid_consta
     __syncthreads();
     if (threadIdx.x < kDrawWarps && drawn[threadIdx.x]) {       // all logarithms in one warp
         LogP l;
-        l.of(p, st.total);
-        l.v = values[threadIdx.x];
+        l.of(p, st.total, values[threadIdx.x]);
         a.logp[row * a.draws + d0 + threadIdx.x] = log_p<TYPE>(l);
     }
 }

@@ -2,12 +2,13 @@
 amplitudes near the type's smallest numbers; against the definitions."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import exact_tensor_network_gb300 as tn
 
-from test_gpu_sampling import _compare, _rows
+from test_gpu_sampling import TYPES, _compare, _rows
 from test_gpu_sampling_use import _u
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +43,39 @@ def test_min_p_below_every_amplitude(n, filters):
     got = op.sample(rows, u.cuda(), mask=mask, **filters)
     op.check()
     _compare(got, rows, u, mask=mask, **filters)
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("n", [50, 2000, 9001, 40003, 300007])
+@pytest.mark.parametrize("filters", [{}, {"min_p": 0.05}, {"min_p": 1.0}, {"top_k": 9}, {"top_p": 0.5, "min_p": 1.0},
+                                     {"top_k": 5000, "top_p": 0.5}], ids=str)
+def test_temperature_that_leaves_no_difference(type_, n, filters):
+    """scale / temperature is 0 in fp32: all present entries weigh the same."""
+    rows, mask = _holes(type_, n, 31)
+    u = _u(3, 5, n, torch.float64)
+    op = tn.Sampler(n, TYPES[type_], max_rows=3, scale=2.0 ** -40)
+    got = op.sample(rows, u.cuda(), mask=mask, temperature=1e38, **filters)
+    op.check()
+    _compare(got, rows, u, scale=2.0 ** -40, mask=mask, temperature=1e38, **filters)
+
+
+@pytest.mark.parametrize("n", [50, 2000, 9001, 40003, 300007])
+def test_logits_further_apart_than_numbers_reach(n):
+    """A difference beyond fp32 counts as the largest number, which at such a temperature is next to nothing."""
+    rows = torch.full((2, n), -3e38)
+    rows[:, n // 3] = 3e38
+    u = _u(2, 50, n, torch.float64)
+    op = tn.Sampler(n, torch.float32, max_rows=2)
+    got = op.sample(rows.cuda(), u.cuda(), temperature=3e38)
+    beta = float(np.float32(1) / np.float32(3e38))
+    w = np.full(n, math.exp(-beta * float(np.finfo(np.float32).max)))
+    w[n // 3] = 1.0
+    c = np.cumsum(w)
+    want = np.searchsorted(c, u.numpy() * c[-1], side="right")
+    assert (got.ids.cpu().numpy() == want).all() and (got.kept == n).all()
+    logp = np.log(w[want] / c[-1])
+    assert (np.abs(got.logp.cpu().numpy() - logp) <= 2.0 ** -24 * np.abs(logp) + 1e-12).all()
+    # (they weigh e^-1.134 of the largest; order values would say e^-2)
+    assert (op.sample(rows.cuda(), u.cuda(), temperature=3e38, min_p=0.2).kept == n).all()
+    assert (op.sample(rows.cuda(), u.cuda(), temperature=3e38, min_p=0.33).kept == 1).all()
+    op.check()
