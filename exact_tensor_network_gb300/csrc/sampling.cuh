@@ -317,13 +317,21 @@ __device__ __forceinline__ void two_weights(const RowPlan &p, const float *roots
     }
 }
 
+// log2 of an amplitude's order value, which may be subnormal (lg2 takes those for 0; at a high temperature
+// they are not).
+__device__ __forceinline__ float log2_of(float v) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(v));
+    return y;
+}
+
 // The same in fp32, relative to the largest: for an estimate of the sum.  It must not be far too small, or
 // the sums would overflow.
 template <int TYPE>
 __device__ __forceinline__ float rough_weight(const RowPlan &p, float v) {
     if constexpr (Entry<TYPE>::kReal) return ex2(fmaxf(v - p.m, kFarthest) * p.ch);
     else if (p.unit) return v * p.down;
-    else return ex2(p.beta * lg2(v / p.m));
+    else return ex2(p.beta * (log2_of(v) - log2_of(p.m)));
 }
 
 template <int TYPE>
@@ -1457,7 +1465,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
         for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
         if (!(top <= m)) {
             if constexpr (Entry<TYPE>::kReal) s *= ex2(fmaxf(m - top, kFarthest) * ch);
-            else if (f.beta != 1.f) s *= m > 0.f ? ex2(f.beta * (lg2(m) - lg2(top))) : 0.f;
+            else if (f.beta != 1.f) s *= m > 0.f ? ex2(f.beta * (log2_of(m) - log2_of(top))) : 0.f;
             m = max_nan(m, top);
         }
         if constexpr (Entry<TYPE>::kReal) {
@@ -1473,16 +1481,16 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < E; ++i) s += v[i];
         } else if (m > 0.f) {
-            const float l = lg2(m);
+            const float l = log2_of(m);
 #pragma unroll
-            for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(f.beta * (lg2(v[i]) - l)) : 0.f;
+            for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(f.beta * (log2_of(v[i]) - l)) : 0.f;
         }
     });
     // threads', then segments'
     const auto moved = [&](float from, float to) {
         if (from == absent<TYPE>()) return 0.f;
         if constexpr (Entry<TYPE>::kReal) return ex2(fmaxf(from - to, kFarthest) * ch);
-        else return f.beta == 1.f ? 1.f : ex2(f.beta * (lg2(from) - lg2(to)));
+        else return f.beta == 1.f ? 1.f : ex2(f.beta * (log2_of(from) - log2_of(to)));
     };
     const float own = m;
     m = g.max(m);
@@ -1635,7 +1643,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) bins_kernel(const __grid_cons
             const float d = (FINE ? first + b + 0.5f : (b + 0.5f) * kSlots) * 128.f;
             const uint32_t top = __float_as_uint(p.m), down = static_cast<uint32_t>(d);
             const float q = down < top ? __uint_as_float(top - down) / p.m : 0.f;
-            return p.unit ? q : q > 0.f ? ex2(p.beta * lg2(q)) : 0.f;
+            return p.unit ? q : q > 0.f ? ex2(p.beta * log2_of(q)) : 0.f;
         }
     };
     // (rolled, and weights computed again, here and below: the streaming loop wants its registers)

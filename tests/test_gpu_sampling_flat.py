@@ -79,3 +79,21 @@ def test_logits_further_apart_than_numbers_reach(n):
     assert (op.sample(rows.cuda(), u.cuda(), temperature=3e38, min_p=0.2).kept == n).all()
     assert (op.sample(rows.cuda(), u.cuda(), temperature=3e38, min_p=0.33).kept == 1).all()
     op.check()
+
+
+@pytest.mark.parametrize("n", [50, 2000, 9001, 40003, 300007])
+@pytest.mark.parametrize("largest", [0.0, 1.0])
+@pytest.mark.parametrize("filters", [{"temperature": 0.5}, {"temperature": 1.5}, {"temperature": 100.0},
+                                     {"temperature": 100.0, "min_p": 0.3}, {"temperature": 1.5, "top_p": 0.8},
+                                     {"temperature": 100.0, "top_k": 3000, "top_p": 0.5}], ids=str)
+def test_amplitudes_of_subnormal_probability(n, largest, filters):
+    """|a|^2 below 2^-126, in all of a row or next to an amplitude of 1 (which at a high temperature is not
+    much more)."""
+    rows = _rows("c64", 2, n, 32) * 1e-19
+    if largest:
+        rows[:, n // 2] = largest
+    u = _u(2, 5, n, torch.float64)
+    op = tn.Sampler(n, torch.complex64, max_rows=2)
+    got = op.sample(rows.cuda(), u.cuda(), **filters)
+    op.check()
+    _compare(got, rows, u, **filters)
