@@ -324,6 +324,12 @@ __device__ __forceinline__ float log2_of(float v) {
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(v));
     return y;
 }
+// The estimate of an amplitude's weight relative to the larger m's, as a power of two.  Logarithms in fp32 are known to
+// 2^-18 only; where beta makes much of that, by ln(v / m) <= (v - m) / m, which is exact for what is close to m (what
+// is not weighs next to nothing there).  ch is beta log2(e).
+__device__ __forceinline__ float rough_power(float beta, float ch, float v, float m) {
+    return beta > 64.f ? ch * ((v - m) / m) : beta * (log2_of(v) - log2_of(m));
+}
 
 // The same in fp32, relative to the largest: for an estimate of the sum.  It must not be far too small, or
 // the sums would overflow.
@@ -331,7 +337,7 @@ template <int TYPE>
 __device__ __forceinline__ float rough_weight(const RowPlan &p, float v) {
     if constexpr (Entry<TYPE>::kReal) return ex2(fmaxf(v - p.m, kFarthest) * p.ch);
     else if (p.unit) return v * p.down;
-    else return ex2(p.beta * (log2_of(v) - log2_of(p.m)));
+    else return ex2(rough_power(p.beta, p.ch, v, p.m));
 }
 
 template <int TYPE>
@@ -472,7 +478,7 @@ __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const 
         // With this the number next to m weighs 2^-124 .. 2^-62: less than a unit already, and what the
         // table and fp32's exponents reach
         p.b = fminf(f.beta, __fdiv_rn(43.f * 0x1p24f, fabsf(m)));
-        p.ch = fminf(p.b * 1.44269504f, 3.402823466e38f);
+        p.ch = fminf(p.b * kLog2E, 3.402823466e38f);
         // (2^-60 .. 2^-120, where m's neighbours are few; differences beyond fp32 count as the largest number)
         p.low = fmaxf(fminf(m - __fdiv_rn(62.4f, p.b), nextafterf(m, -__builtin_huge_valf())),
                       fmaxf(m, 0.f) - 3.402823466e38f);
@@ -483,6 +489,7 @@ __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const 
         p.first = __float_as_uint(kMagic) + static_cast<uint32_t>(static_cast<int>(grid));
     } else {
         p.b = f.beta;
+        p.ch = fminf(p.b * kLog2E, 3.402823466e38f);
         p.far = f.beta > 2.f;           // (the errors of logarithms count beta times)
         int n;
         const float g = lg2(2.f * frexpf(m, &n)) * 0.693147181f;       // (an estimate will do)
@@ -1465,7 +1472,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
         for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
         if (!(top <= m)) {
             if constexpr (Entry<TYPE>::kReal) s *= ex2(fmaxf(m - top, kFarthest) * ch);
-            else if (f.beta != 1.f) s *= m > 0.f ? ex2(f.beta * (log2_of(m) - log2_of(top))) : 0.f;
+            else if (f.beta != 1.f) s *= m > 0.f ? ex2(rough_power(f.beta, ch, m, top)) : 0.f;
             m = max_nan(m, top);
         }
         if constexpr (Entry<TYPE>::kReal) {
@@ -1481,16 +1488,15 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < E; ++i) s += v[i];
         } else if (m > 0.f) {
-            const float l = log2_of(m);
 #pragma unroll
-            for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(f.beta * (log2_of(v[i]) - l)) : 0.f;
+            for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(rough_power(f.beta, ch, v[i], m)) : 0.f;
         }
     });
     // threads', then segments'
     const auto moved = [&](float from, float to) {
         if (from == absent<TYPE>()) return 0.f;
         if constexpr (Entry<TYPE>::kReal) return ex2(fmaxf(from - to, kFarthest) * ch);
-        else return f.beta == 1.f ? 1.f : ex2(f.beta * (log2_of(from) - log2_of(to)));
+        else return f.beta == 1.f ? 1.f : ex2(rough_power(f.beta, ch, from, to));
     };
     const float own = m;
     m = g.max(m);

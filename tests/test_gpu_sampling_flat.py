@@ -97,3 +97,29 @@ def test_amplitudes_of_subnormal_probability(n, largest, filters):
     got = op.sample(rows.cuda(), u.cuda(), **filters)
     op.check()
     _compare(got, rows, u, **filters)
+
+
+@pytest.mark.parametrize("n", [60, 900, 9001, 40003])
+@pytest.mark.parametrize("temperature", [1e-2, 1e-5, 1e-6, 2e-7, 1e-7])
+def test_amplitudes_next_to_each_other_at_a_low_temperature(n, temperature):
+    """Nearly uniform states whose small differences a low temperature makes large: |a|^2 within 8 temperatures of
+    the largest, at many sizes of it."""
+    R, g = 4000 if n < 1000 else 200, torch.Generator().manual_seed(n)
+    size = torch.exp2(torch.linspace(-120, -66, R, dtype=torch.float64))[:, None]
+    w = size * (1 - min(8 * temperature, 0.5) * torch.rand(R, n, generator=g, dtype=torch.float64))
+    rows = torch.complex(w.sqrt().float(), torch.zeros(R, n))
+    u = _u(R, 4, n, torch.float64)
+    op = tn.Sampler(n, torch.complex64, max_rows=R)
+    got = op.sample(rows.cuda(), u.cuda(), temperature=temperature)
+    v = (rows.real * rows.real).double().numpy()
+    beta = float(np.float32(1) / np.float32(temperature))
+    top = v.max(1, keepdims=True)
+    x = beta * np.log1p((v - top) / top)
+    c = np.cumsum(np.exp(x), 1)
+    ids = np.stack([np.searchsorted(c[r], u[r].numpy() * c[r, -1], side="right") for r in range(R)])
+    assert (got.ids.cpu().numpy() == ids).all() and (got.kept == n).all()
+    logp = np.take_along_axis(x, ids, 1) - np.log(c[:, -1:])
+    # beta times the rounding of a 64-bit logarithm of up to 63, on either side
+    far = 2.0 ** -24 * np.abs(logp) + 1e-12 + beta * 64 * 2.0 ** -52
+    assert (np.abs(got.logp.cpu().numpy() - logp) <= far).all()
+    op.check()
