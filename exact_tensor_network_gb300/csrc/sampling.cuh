@@ -468,6 +468,13 @@ __device__ __forceinline__ bool filters_of(const SampleArgs &a, int64_t row, Fil
     return t >= 0.f && t <= 3.402823466e38f && f.top_p == f.top_p && f.min_p <= 1.f;
 }
 
+// m < 2^x of amplitudes' largest order value, where both 2^x and 2^-x are numbers (m 2^-x may be up to 4); 2^-x.
+__device__ __forceinline__ int exponent_of(float m) {
+    const int x = static_cast<int>(__float_as_uint(m) >> 23) - 126;
+    return x > 126 ? 126 : x;
+}
+__device__ __forceinline__ float down_of(float m) { return __uint_as_float(static_cast<uint32_t>(127 - exponent_of(m)) << 23); }
+
 // What follows from a row's largest order value.
 template <int TYPE>
 __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const Filters &f) {
@@ -497,11 +504,8 @@ __device__ __forceinline__ void plan_row(RowPlan &p, float m, bool valid, const 
     }
     p.greedy = f.greedy;
     p.bound = kPresent;
-    int x = 0;
-    if (!Entry<TYPE>::kReal) frexpf(m, &x);                 // m < 2^x
-    x = x < -126 ? -126 : x > 126 ? 126 : x;                // (2^-x is a number; weights may be up to 4)
-    p.down_log = p.unit && !Entry<TYPE>::kReal ? x : 0;
-    p.down = ldexpf(1.f, -x);
+    p.down_log = p.unit && !Entry<TYPE>::kReal ? exponent_of(m) : 0;
+    p.down = Entry<TYPE>::kReal ? 1.f : down_of(m);
     p.shift = 0;
     p.state = !valid || m != m || m == __builtin_huge_valf() ? kUndefined : m == absent<TYPE>() ? kEmpty : kDraw;
 }
@@ -1463,9 +1467,9 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
     RowState &st = a.state[c.row];
     Filters f;
     const bool valid = filters_of(a, c.row, f);
-    // the sum relative to the largest entry so far
+    // the sum relative to the largest entry so far (of amplitudes at beta = 1 times down_of it)
     const float ch = fminf(f.beta * kLog2E, 3.402823466e38f);
-    float m = absent<TYPE>(), s = 0.f;
+    float m = absent<TYPE>(), s = 0.f, down = 1.f;
     each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t, int) {
         float top = v[0];
 #pragma unroll
@@ -1473,6 +1477,10 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
         if (!(top <= m)) {
             if constexpr (Entry<TYPE>::kReal) s *= ex2(fmaxf(m - top, kFarthest) * ch);
             else if (f.beta != 1.f) s *= m > 0.f ? ex2(rough_power(f.beta, ch, m, top)) : 0.f;
+            else {
+                s *= down_of(top) / down;
+                down = down_of(top);
+            }
             m = max_nan(m, top);
         }
         if constexpr (Entry<TYPE>::kReal) {
@@ -1486,7 +1494,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
             }
         } else if (f.beta == 1.f) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) s += v[i];
+            for (int i = 0; i < E; ++i) s = fmaf(v[i], down, s);
         } else if (m > 0.f) {
 #pragma unroll
             for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(rough_power(f.beta, ch, v[i], m)) : 0.f;
@@ -1496,7 +1504,7 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
     const auto moved = [&](float from, float to) {
         if (from == absent<TYPE>()) return 0.f;
         if constexpr (Entry<TYPE>::kReal) return ex2(fmaxf(from - to, kFarthest) * ch);
-        else return f.beta == 1.f ? 1.f : ex2(rough_power(f.beta, ch, from, to));
+        else return f.beta == 1.f ? down_of(to) / down_of(from) : ex2(rough_power(f.beta, ch, from, to));
     };
     const float own = m;
     m = g.max(m);
@@ -1527,7 +1535,6 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
         st.listed = 0;
         st.min_value = least_present<TYPE>();
         if (p.state == kDraw) {
-            if (!Entry<TYPE>::kReal && f.beta == 1.f) s *= p.down;
             p.shift = p.greedy ? 0 : shift_of(s);
             if (p.greedy) {
                 st.min_value = m;

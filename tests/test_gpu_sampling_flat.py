@@ -123,3 +123,19 @@ def test_amplitudes_next_to_each_other_at_a_low_temperature(n, temperature):
     far = 2.0 ** -24 * np.abs(logp) + 1e-12 + beta * 64 * 2.0 ** -52
     assert (np.abs(got.logp.cpu().numpy() - logp) <= far).all()
     op.check()
+
+
+@pytest.mark.parametrize("n", [900, 9001, 40003, 300007])
+@pytest.mark.parametrize("each", [1.4e19, 1e-12])
+def test_amplitudes_whose_sum_is_beyond_numbers(n, each):
+    """Two amplitudes whose |a|^2 add up to more than fp32 holds, and n - 2 others of 2^-30 of that: a draw that aims
+    into the middle of one of those finds it.  And the same far below."""
+    rows = torch.full((2, n), each * 2.0 ** -15, dtype=torch.complex64)
+    rows[:, :2] = each
+    v = (rows.real * rows.real).double()
+    at = torch.randint(2, n, (2, 40), generator=torch.Generator().manual_seed(n))
+    c = v.cumsum(1)
+    u = (c.gather(1, at) - 0.5 * v.gather(1, at)) / c[:, -1:]
+    got = tn.Sampler(n, torch.complex64, max_rows=2).sample(rows.cuda(), u.cuda())
+    assert torch.equal(got.ids.cpu(), at) and (got.kept == n).all()
+    assert (got.logp.cpu() - (v.gather(1, at) / c[:, -1:]).log()).abs().max() <= 2.0 ** -24 * 32 + 1e-12
