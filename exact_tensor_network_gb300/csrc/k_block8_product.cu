@@ -62,7 +62,7 @@ struct Shape {
     static constexpr int kCtas = kBig ? 1 : 2;              // on an SM
     static constexpr uint32_t kWhat = (1u << 4) | (static_cast<uint32_t>(BN) >> 3 << 17) | (128u >> 4 << 24);
     static_assert(kSmem <= (kBig ? 232448 : 115712) && kTmem * kCtas <= 512, "an SM's memory");
-    static_assert(2 * kCols <= kOwn, "scales of two blocks");
+    static_assert(3 * kCols <= kOwn, "scales of two blocks, and ones");
     static_assert(BN == 256 || part_bytes(BN) <= kRing, "the ring holds the sums");
     static_assert(!kBig || 4 * kRegsLow + 8 * kRegsHigh <= 12 * 168, "registers of the launch");
 };
@@ -83,6 +83,40 @@ __device__ __forceinline__ void add_scaled(float2 *acc, const uint32_t (&v)[N], 
         acc[i] = fma2(x, s2, acc[i]);
         acc[i + 1] = fma2(y, s2, acc[i + 1]);
     }
+}
+
+// Where the product of two scales, or a block's sum (0, or 2^-18 .. 2^25) times Q's scale, is no normal number although
+// the value may be one, sums are scaled before they are added: a scale is split into a number with half of its
+// exponent and a power of two, and the sum times both of the first and then times both powers leaves fp32 only
+// where the value does.
+struct Halves {
+    float part, power;
+};
+__device__ __forceinline__ Halves halves_of(float x) {
+    if (x == 0.f || !(fabsf(x) <= 3.402823466e38f)) return {x, 1.f};
+    int e;
+    const float m = frexpf(x, &e);
+    return {ldexpf(m, e - (e >> 1)), ldexpf(1.f, e >> 1)};
+}
+// N columns: row times col, or (EACH) times each column's.
+template <bool EACH, int N>
+__device__ __forceinline__ void scale_far(uint32_t (&v)[N], float row, float col, const float *each) {
+    const Halves p = halves_of(row);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const Halves q = halves_of(EACH ? each[i] : col);
+        v[i] = __float_as_uint(__uint_as_float(v[i]) * (p.part * q.part) * fminf(p.power * q.power, 0x1p127f));
+    }
+}
+// Whether two scales have to go that way; whether Q's of a column of its own has to.
+__device__ __forceinline__ bool far_product(float s, float q) {
+    const float x = fabsf(s * q);
+    return !(x >= 0x1p-126f && x <= 3.402823466e38f) && s != 0.f && q != 0.f && fabsf(s) <= 3.402823466e38f &&
+           fabsf(q) <= 3.402823466e38f;
+}
+__device__ __forceinline__ bool far_scale(float q) {
+    const float x = fabsf(q);
+    return (x < 0x1p-100f && x > 0.f) || (x > 0x1p100f && x <= 3.402823466e38f);
 }
 
 template <int BN, bool EACH>
@@ -230,16 +264,34 @@ __global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kC
             for (int kb = kb0; kb < kb1; ++kb) {
                 float s = np[0];
                 const float *qs = mine + (kb & 1) * S::kCols;
+                bool far = false;
                 if constexpr (EACH) {
 #pragma unroll
-                    for (int i = 0; i < kQ; ++i)
+                    for (int i = 0; i < kQ; ++i) {
                         if (lane + 32 * i < S::kCols) mine[(kb & 1) * S::kCols + lane + 32 * i] = nq[0][i];
+                        far |= far_scale(nq[0][i]);
+                    }
                     __syncwarp();
                 } else {
-                    // 0 times a product beyond fp32's range is 0 all the same
-                    const float q = nq[0][0], both = s * q;
-                    s = isinf(both) && !isinf(s) && !isinf(q) ? copysignf(3.402823466e38f, both) : both;
+                    far = far_product(s, nq[0][0]);
+                    s *= nq[0][0];
                 }
+                far = __any_sync(0xffffffffu, far);
+                if (far) {      // scaled before they are added: with 1 from then on
+                    s = 1.f;
+                    if constexpr (EACH) {
+#pragma unroll
+                        for (int i = 0; i < kQ; ++i)
+                            if (lane + 32 * i < S::kCols) mine[2 * S::kCols + lane + 32 * i] = 1.f;
+                        __syncwarp();
+                        qs = mine + 2 * S::kCols;
+                    }
+                }
+                // (the scales are read again: kept until here they would cost every product registers)
+                const auto if_far = [&](auto &r, int c) {
+                    if (far) scale_far<EACH>(r, __ldcg(sp + kb * a.blockP), EACH ? 0.f : __ldcg(sq[0] + kb * a.blockQ),
+                                             mine + (kb & 1) * S::kCols + c);
+                };
                 np[0] = np[1];
 #pragma unroll
                 for (int i = 0; i < kQ; ++i) nq[0][i] = nq[1][i];
@@ -268,6 +320,7 @@ __global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kC
                         tc::tmem_load(from + c, r);
                         tc::tmem_wait(r);
                         if (c + S::kStep == S::kCols) loaded();
+                        if_far(r, c);
                         add_scaled<EACH>(acc + c / 2, r, s, qs + c);
                     }
                 } else {
@@ -280,6 +333,8 @@ __global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kC
                     for (int c = 0; c < S::kCols; c += 64) {
                         const bool more = c + 64 < S::kCols;
                         if (!more) loaded();
+                        if_far(r0, c);
+                        if_far(r1, c + 32);
                         add_scaled<EACH>(acc + c / 2, r0, s, qs + c);
                         if (more) tc::tmem_load(from + c + 64, r0);
                         add_scaled<EACH>(acc + c / 2 + 16, r1, s, qs + c + 32);
