@@ -300,12 +300,13 @@ __global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kC
 #pragma unroll
                     for (int i = 0; i < kQ; ++i) nq[1][i] = __ldcg(sq[i] + (kb + 2) * a.blockQ);
                 }
-                if (!tc::bar_wait(tfull + 8 * buf, bphase, gave_up)) {
+                if (!tc::warp_wait(tfull + 8 * buf, bphase, gave_up)) {
                     ok = false;
                     break;
                 }
                 if (lane == 0) tc::bar_arrive(empty + 8 * stage);
                 if (++stage == S::kStages) stage = 0;
+                __syncwarp();
                 tc::fence_after();
                 const uint32_t from = tbase + buf * BN;
                 const auto loaded = [&] {       // all of the accumulator is in registers

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
                         }
                     }
                     if (g + kGroup < kb1) load(g + kGroup);
-                    if (!tc::bar_wait(sempty + 8 * place, phase ^ 1, gave_up)) {
+                    if (!tc::warp_wait(sempty + 8 * place, phase ^ 1, gave_up)) {
                         ok = false;
                         break;
                     }
@@ -289,12 +289,13 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
 #pragma unroll
             for (int i = 0; i < S::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
             for (int g = kb0; g < kb1; g += kGroup) {
-                if (!tc::bar_wait(tfull + 8 * buf, bphase, gave_up)) {
+                if (!tc::warp_wait(tfull + 8 * buf, bphase, gave_up)) {
                     ok = false;
                     break;
                 }
                 if (lane == 0) tc::bar_arrive(sempty + 8 * place);
                 if (++place == S::kSlots) place = 0;
+                __syncwarp();
                 tc::fence_after();
                 const uint32_t from = tbase + buf * BN;
                 uint32_t r[S::kStep];

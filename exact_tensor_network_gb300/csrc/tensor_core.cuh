@@ -57,6 +57,10 @@ __device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, vol
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     return bar_try(bar, parity) || bar_wait_long(bar, parity, gave_up);
 }
+// The same by a whole warp, whose lanes go on together and all with the same answer (TMEM loads want that).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
+}
 // The same whatever the flag says: for copies in flight.
 __device__ __forceinline__ void bar_wait_end(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = nanoseconds();
@@ -173,6 +177,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();       // (every lane has to be there at once)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The same place of CTA `rank`'s shared memory, and four words there.

@@ -74,3 +74,23 @@ def test_whole_numbers(R, N, K, powers):
         m.append(tn.Blocks8(codes.cuda()[:, :K], torch.ones(x.shape[0], -(-K // 128), device="cuda"), powers))
     y = tn.product8(*m, dtype=torch.float32)
     assert torch.equal(y.cpu().double(), a.double() @ b.double().t())
+
+
+@pytest.mark.parametrize("powers", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("R,N,K", [(1, 130, 4096), (5, 131, 4100), (33, 77, 6000), (100, 333, 5000), (130, 130, 8192),
+                                   (257, 1, 8192), (1, 1, 16384), (61, 257, 2048)])
+def test_ragged_tiles_of_clusters(R, N, K, dtype, powers):
+    """Tiles that a cluster shares and that the output ends in: only some lanes of a warp store at the end.  Whole numbers
+    below 2^16, so that a rounding to the output's type is all."""
+    g = torch.Generator().manual_seed(K + N)
+    a, b = torch.randint(-1, 2, (R, K), generator=g).float(), torch.randint(-1, 2, (N, K), generator=g).float()
+    q = [tn.quantize8(x.cuda()) for x in (a, b)]
+    q = [tn.Blocks8(x.codes, x.scales, powers) for x in q]
+    want = (a.double() @ b.double().t()).float().to(dtype)
+    for _ in range(5):
+        whole = torch.full((R + 2, N + 5), 3.25, dtype=dtype, device="cuda")
+        y = tn.product8(*q, out=whole[1:-1, 2:N + 2])
+        assert torch.equal(y.cpu(), want)
+        whole[1:-1, 2:N + 2] = 3.25
+        assert (whole == 3.25).all()
