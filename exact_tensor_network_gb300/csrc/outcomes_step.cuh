@@ -42,10 +42,13 @@ __device__ __forceinline__ void copy_wait_all_but(int n) {
     }
 }
 
+// (.aligned: every lane has to be there at once)
 __device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // v to where p is in the shared memory of CTA `rank` of the cluster
