@@ -211,22 +211,31 @@ tn_status tn_block8_product(const tn_block8 *a, const tn_block8 *b, void *out, i
     if (g.ptiles > 0x7fffffff / 8 / g.qtiles) return fail(TN_EOVERFLOW, "too many tiles");
     const bool each = g.shiftQ == 0 || t.bn < 128;
     cudaError_t e = tn::block8_status(&g.status);
-    if (e != cudaSuccess) return cuda_fail(e, "looking up the status word");
+    if (e != cudaSuccess) return cuda_fail(e, "looking up the status");
     const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
     e = powers ? tn::launch_scaled(g, t.bn, on) : tn::launch_product(g, t.bn, each, on);
     return e == cudaSuccess ? TN_OK : cuda_fail(e, "launching the product");
 }
 
 tn_status tn_block8_check(void) {
-    tn::DevStatus d = {0, 0}, *at = nullptr;
-    cudaError_t e = tn::block8_status(&at);
+    // what this thread has been told of each device's counts
+    thread_local tn::Block8Status told[64] = {};
+    tn::Block8Status d = {}, *at = nullptr;
+    int device;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = tn::block8_status(&at);
     if (e == cudaSuccess) e = cudaMemcpy(&d, at, sizeof(d), cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return cuda_fail(e, "reading the status word");
-    if (d.code == tn::ERR_NONE) return TN_OK;
-    e = cudaMemset(at, 0, sizeof(d));
-    if (e != cudaSuccess) return cuda_fail(e, "clearing the status word");
-    return d.code == tn::ERR_TIMEOUT ? fail(TN_ETIMEOUT, "a product gave up waiting: its outputs are not valid")
-                                     : fail(TN_EDEVICE, "a scale is no power of two: it counted as NaN");
+    if (e != cudaSuccess) return cuda_fail(e, "reading the status");
+    tn::Block8Status &seen = told[device & 63];
+    if (d.timeouts != seen.timeouts) {
+        seen.timeouts = d.timeouts;
+        return fail(TN_ETIMEOUT, "a product gave up waiting: its outputs are not valid");
+    }
+    if (d.scales != seen.scales) {
+        seen.scales = d.scales;
+        return fail(TN_EDEVICE, "a scale is no power of two: it counted as NaN");
+    }
+    return TN_OK;
 }
 
 const char *tn_block8_last_error(void) { return g_error; }

@@ -33,6 +33,13 @@ struct QuantArgs {
     int32_t few;
 };
 
+// What the products of a device have reported so far: counts that only grow, so that no report is lost to
+// another, or to a thread that asks at the same time.
+struct Block8Status {
+    unsigned long long timeouts;    // CTAs that gave up waiting
+    unsigned long long scales;      // threads that met a scale that should be a power of two
+};
+
 // A product by tiles of 128 rows of operand P by BN rows of operand Q:
 // out[p sp + q sq].  P is the call's a (sp the output's stride, sq 1) or, where a
 // has few rows, its b (sp 1).
@@ -49,7 +56,7 @@ struct ProductArgs {
     int32_t kbs;                    // blocks of k
     int32_t split;                  // CTAs of a cluster that share a tile's blocks
     int64_t ptiles, qtiles;
-    DevStatus *status;
+    Block8Status *status;
 };
 
 cudaError_t launch_quantize(const QuantArgs &a, int32_t type, bool square, cudaStream_t stream);
@@ -57,7 +64,7 @@ cudaError_t launch_quantize(const QuantArgs &a, int32_t type, bool square, cudaS
 cudaError_t launch_product(const ProductArgs &a, int bn, bool each, cudaStream_t stream);
 // The same of scales that are powers of two; bn: 240, 128, 64, 32 or 16
 cudaError_t launch_scaled(const ProductArgs &a, int bn, cudaStream_t stream);
-// The current device's status word.
-cudaError_t block8_status(DevStatus **p);
+// The current device's counts.
+cudaError_t block8_status(Block8Status **p);
 
 }  // namespace tn

@@ -28,7 +28,7 @@
 //
 // Every wait on a barrier is bounded: after its limit the CTA's flag goes up, its
 // roles leave, copies and products in flight are waited for (with a limit
-// too), TMEM is released and the status word says ERR_TIMEOUT.
+// too), TMEM is released and the device's count of timeouts goes up.
 #include "block8_product.cuh"
 
 namespace tn {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kC
         tc::fence_after();
         tc::tmem_free<S::kTmem>(tmem);
     }
-    if (threadIdx.x == 0 && *gave_up) atomicCAS(&a.status->code, ERR_NONE, ERR_TIMEOUT);
+    if (threadIdx.x == 0 && *gave_up) atomicAdd(&a.status->timeouts, 1ull);
 }
 
 template <int BN, bool EACH>

@@ -26,8 +26,9 @@
  * Conventions are those of tn.h: no call throws, every failure is a
  * tn_status, no device memory is allocated, work is enqueued on the caller's
  * stream on the current device and the calls return at once.  Results do not
- * depend on timing.  The calls keep nothing, can be captured into CUDA graphs,
- * and may be made by several host threads and on several streams at once.
+ * depend on timing.  The calls keep nothing (but counts of what went wrong, for
+ * tn_block8_check), can be captured into CUDA graphs, and may be made by several host threads
+ * and on several streams at once.
  */
 #ifndef TN_GB300_BLOCK8_H
 #define TN_GB300_BLOCK8_H
@@ -82,10 +83,11 @@ TN_API tn_status tn_block8_quantize(const tn_matrix *x, const tn_block8 *rows, c
 TN_API tn_status tn_block8_product(const tn_block8 *a, const tn_block8 *b, void *out, int32_t type,
                                    int64_t out_stride, tn_stream_t stream);
 
-/* After the device has been synchronised: read and clear the current device's
- * status word of these calls.  TN_OK, TN_ETIMEOUT (a product gave up
- * waiting; its outputs are not valid), or TN_EDEVICE (a scale of a matrix with
- * `powers` is neither a power of two nor NaN; it counted as NaN). */
+/* After the device has been synchronised: what the calls on the current device, by any thread,
+ * have reported since this host thread's last call of this (or since the process began).
+ * TN_OK, TN_ETIMEOUT (a product gave up waiting; its outputs are not valid), or TN_EDEVICE
+ * (a scale of a matrix with `powers` is neither a power of two nor NaN; it counted as NaN).
+ * One report a call, timeouts first: call until TN_OK.  Other threads are told for themselves. */
 TN_API tn_status tn_block8_check(void);
 
 /* Text of this thread's last failed call. */

@@ -1,5 +1,7 @@
 """Products with scales far from 1 against the definitions in 64 bits; sums that are exact; and what is
 reported."""
+import threading
+
 import pytest
 import torch
 
@@ -94,3 +96,34 @@ def test_ragged_tiles_of_clusters(R, N, K, dtype, powers):
         assert torch.equal(y.cpu(), want)
         whole[1:-1, 2:N + 2] = 3.25
         assert (whole == 3.25).all()
+
+
+def test_reports_reach_every_thread():
+    """A thread's question takes no report away from another, and is answered once."""
+    q = tn.quantize8(_codes(40, 256, 95, False).float().cuda())
+    bad = q.scales.clone()
+    bad[3, 1] = 1.5
+    seen = []
+
+    def ask():
+        try:
+            tn.tn_block8_check()
+            seen.append(tn.TN_OK)
+        except tn.TNError as e:
+            seen.append(e.status)
+
+    def other(n):
+        t = threading.Thread(target=lambda: [ask() for _ in range(n)])
+        t.start()
+        t.join()
+
+    torch.cuda.synchronize()
+    ask()
+    assert seen == [tn.TN_OK]
+    tn.product8(q._replace(scales=bad), q)
+    torch.cuda.synchronize()
+    other(2)
+    assert seen[1:] == [tn.TN_EDEVICE, tn.TN_OK]
+    ask()
+    ask()
+    assert seen[3:] == [tn.TN_EDEVICE, tn.TN_OK]
