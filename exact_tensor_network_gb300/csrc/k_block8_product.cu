@@ -304,15 +304,14 @@ __global__ void __launch_bounds__(Shape<BN, EACH>::kThreads, Shape<BN, EACH>::kC
                     ok = false;
                     break;
                 }
-                if (lane == 0) tc::bar_arrive(empty + 8 * stage);
+                tc::bar_arrive_once(empty + 8 * stage);
                 if (++stage == S::kStages) stage = 0;
-                __syncwarp();
                 tc::fence_after();
                 const uint32_t from = tbase + buf * BN;
                 const auto loaded = [&] {       // all of the accumulator is in registers
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::bar_arrive(tempty + 8 * buf);
+                    tc::bar_arrive_once(tempty + 8 * buf);
                 };
                 if constexpr (!S::kBig) {
                     uint32_t r[S::kStep];

@@ -293,9 +293,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
                     ok = false;
                     break;
                 }
-                if (lane == 0) tc::bar_arrive(sempty + 8 * place);
+                tc::bar_arrive_once(sempty + 8 * place);
                 if (++place == S::kSlots) place = 0;
-                __syncwarp();
                 tc::fence_after();
                 const uint32_t from = tbase + buf * BN;
                 uint32_t r[S::kStep];
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, Shape<BN>::kCtas)
                     if (c + S::kStep == S::kCols) {
                         tc::fence_before();
                         __syncwarp();
-                        if (lane == 0) tc::bar_arrive(tempty + 8 * buf);
+                        tc::bar_arrive_once(tempty + 8 * buf);
                     }
                     add_sums(acc + c / 2, r);
                 }
