@@ -129,7 +129,9 @@ static __device__ const float4 kLogs[128] = {
 };
 constexpr float kLn2Hi = 0x1.62e4p-1f, kLn2Lo = 0x1.7f7d1cp-20f;    // ln 2 likewise
 
-constexpr float kFarthest = -3.402823466e38f;      // a difference beyond fp32 counts as this one
+// A difference beyond fp32 counts as this one; from this ch on it weighs nothing (2^-1024), as absent logits
+// at -inf do then.
+constexpr float kFarthest = -3.402823466e38f, kRareScale = 0x1p-118f;
 
 // What a row's weights are computed from.
 struct RowPlan {
@@ -468,11 +470,12 @@ __device__ __forceinline__ bool filters_of(const SampleArgs &a, int64_t row, Fil
     return t >= 0.f && t <= 3.402823466e38f && f.top_p == f.top_p && f.min_p <= 1.f;
 }
 
-// m < 2^x of amplitudes' largest order value, where both 2^x and 2^-x are numbers (m 2^-x may be up to 4); 2^-x.
+// m < 2^x of amplitudes' largest order value, where both 2^x and 2^-x are numbers (m 2^-x may be up to 4); those.
 __device__ __forceinline__ int exponent_of(float m) {
     const int x = static_cast<int>(__float_as_uint(m) >> 23) - 126;
     return x > 126 ? 126 : x;
 }
+__device__ __forceinline__ float up_of(float m) { return __uint_as_float(static_cast<uint32_t>(127 + exponent_of(m)) << 23); }
 __device__ __forceinline__ float down_of(float m) { return __uint_as_float(static_cast<uint32_t>(127 - exponent_of(m)) << 23); }
 
 // What follows from a row's largest order value.
@@ -1086,11 +1089,18 @@ held_rows_kernel(const __grid_constant__ SampleArgs a) {
         }
         if (!p.greedy) {
             float s = 0.f;
+            if (Entry<TYPE>::kReal && p.ch >= kRareScale) {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+                for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int k = 0; k < E; ++k)
-                    if (v[i][k] != absent<TYPE>()) s += rough_weight<TYPE>(p, v[i][k]);
+                    for (int k = 0; k < E; ++k) s += ex2((v[i][k] - m) * p.ch);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int k = 0; k < E; ++k)
+                        if (v[i][k] != absent<TYPE>()) s += rough_weight<TYPE>(p, v[i][k]);
+            }
             p.shift = shift_of(g.sum(s));
         }
         uint64_t w[V][E];       // 0 of what is not left, 1 at least otherwise
@@ -1469,42 +1479,63 @@ __global__ void __launch_bounds__(kDrawThreads) top_kernel(const __grid_constant
     const bool valid = filters_of(a, c.row, f);
     // the sum relative to the largest entry so far (of amplitudes at beta = 1 times down_of it)
     const float ch = fminf(f.beta * kLog2E, 3.402823466e38f);
-    float m = absent<TYPE>(), s = 0.f, down = 1.f;
-    each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, [&](const float (&v)[E], int64_t, int) {
-        float top = v[0];
+    float m = absent<TYPE>(), s = 0.f;
+    const auto over = [&](auto f) { each_vector<TYPE, kDrawThreads, 4>(c.r, c.lo, c.hi, threadIdx.x, f); };
+    if (!Entry<TYPE>::kReal && f.beta == 1.f) {
+        float down = 1.f, limit = 0.f;      // which down_of(m) holds below
+        over([&](const float (&v)[E], int64_t, int) {
+            float top = v[0];
 #pragma unroll
-        for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
-        if (!(top <= m)) {
-            if constexpr (Entry<TYPE>::kReal) s *= ex2(fmaxf(m - top, kFarthest) * ch);
-            else if (f.beta != 1.f) s *= m > 0.f ? ex2(rough_power(f.beta, ch, m, top)) : 0.f;
-            else {
-                s *= down_of(top) / down;
+            for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
+            if (!(top < limit)) {
                 down = down_of(top);
+                limit = up_of(top);
+                s *= down * up_of(m);
             }
             m = max_nan(m, top);
-        }
-        if constexpr (Entry<TYPE>::kReal) {
-            if (top != absent<TYPE>() && ch >= 0x1p-118f) {     // (what is farthest, or absent, adds nothing)
-#pragma unroll
-                for (int i = 0; i < E; ++i) s += ex2((v[i] - m) * ch);
-            } else if (top != absent<TYPE>()) {
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (v[i] != absent<TYPE>()) s += ex2(fmaxf(v[i] - m, kFarthest) * ch);
-            }
-        } else if (f.beta == 1.f) {
 #pragma unroll
             for (int i = 0; i < E; ++i) s = fmaf(v[i], down, s);
-        } else if (m > 0.f) {
+        });
+    } else {
+        // RARE: see kRareScale; amplitudes' logarithms: see rough_power
+        const auto pass = [&](auto rare) {
+            constexpr bool RARE = decltype(rare)::value;
+            over([&](const float (&v)[E], int64_t, int) {
+                float top = v[0];
 #pragma unroll
-            for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(rough_power(f.beta, ch, v[i], m)) : 0.f;
-        }
-    });
+                for (int i = 1; i < E; ++i) top = max_nan(top, v[i]);
+                if (!(top <= m)) {
+                    if constexpr (Entry<TYPE>::kReal) s *= ex2(fmaxf(m - top, kFarthest) * ch);
+                    else s *= m > 0.f ? ex2(rough_power(f.beta, ch, m, top)) : 0.f;
+                    m = max_nan(m, top);
+                }
+                if constexpr (Entry<TYPE>::kReal) {
+                    if (top != absent<TYPE>()) {
+#pragma unroll
+                        for (int i = 0; i < E; ++i) {
+                            if (!RARE) s += ex2((v[i] - m) * ch);
+                            else if (v[i] != absent<TYPE>()) s += ex2(fmaxf(v[i] - m, kFarthest) * ch);
+                        }
+                    }
+                } else if (!RARE && m >= 0x1p-60f) {    // (below 2^-126 less than 2^-33 of m's)
+                    const float l = lg2(m);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) s += ex2(f.beta * (lg2(v[i]) - l));
+                } else if (m > 0.f) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) s += v[i] > 0.f ? ex2(rough_power(f.beta, ch, v[i], m)) : 0.f;
+                }
+            });
+        };
+        const bool rare = Entry<TYPE>::kReal ? ch < kRareScale : f.beta < 0.5f || f.beta > 64.f;
+        if (rare) pass(std::true_type{});
+        else pass(std::false_type{});
+    }
     // threads', then segments'
     const auto moved = [&](float from, float to) {
         if (from == absent<TYPE>()) return 0.f;
         if constexpr (Entry<TYPE>::kReal) return ex2(fmaxf(from - to, kFarthest) * ch);
-        else return f.beta == 1.f ? down_of(to) / down_of(from) : ex2(rough_power(f.beta, ch, from, to));
+        else return f.beta == 1.f ? down_of(to) * up_of(from) : ex2(rough_power(f.beta, ch, from, to));
     };
     const float own = m;
     m = g.max(m);

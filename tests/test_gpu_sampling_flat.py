@@ -9,7 +9,7 @@ import torch
 import exact_tensor_network_gb300 as tn
 
 from test_gpu_sampling import TYPES, _compare, _rows
-from test_gpu_sampling_use import _u
+from test_gpu_sampling_use import _many, _u
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,15 @@ def test_amplitudes_whose_sum_is_beyond_numbers(n, each):
     got = tn.Sampler(n, torch.complex64, max_rows=2).sample(rows.cuda(), u.cuda())
     assert torch.equal(got.ids.cpu(), at) and (got.kept == n).all()
     assert (got.logp.cpu() - (v.gather(1, at) / c[:, -1:]).log()).abs().max() <= 2.0 ** -24 * 32 + 1e-12
+
+
+@pytest.mark.parametrize("type_,n", [("f32", 40003), ("bf16", 40003), ("f16", 131072), ("f32", 131072), ("f32", 300007),
+                                     ("bf16", 1 << 20)])
+@pytest.mark.parametrize("spread", [1e-4, 0.01, 0.1])
+@pytest.mark.parametrize("filters", [{"top_p": 0.9}, {"top_k": 1000}, {"top_k": 5000, "top_p": 0.6}], ids=str)
+def test_logits_of_little_spread(type_, n, spread, filters):
+    """A head at its start: more entries in the bin where a filter cuts than are sorted."""
+    rows, u = _rows(type_, 3, n, 33, spread), _u(3, 12, n, torch.float64)
+    op = tn.Sampler(n, TYPES[type_], max_rows=3)
+    _many(op.sample(rows.cuda(), u.cuda(), **filters), rows, u.numpy(), **filters)
+    op.check()
