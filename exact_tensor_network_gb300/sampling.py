@@ -103,7 +103,8 @@ class Sampler:
     Rows and masks are those of ``Outcomes``.  All tensors of a call, its
     stream and the workspace are on the current device; the first call binds a
     workspace there unless ``bind_workspace`` did, and waits for the device once
-    (so bind it before a call is captured into a graph).
+    (so bind it before a call is captured into a graph, which works in it: keep the
+    sampler, and bind no other, as long as the graph).
 
     Calls are asynchronous on ``stream`` (default: torch's current stream).
     On another stream the caller orders it after the inputs' producers; outputs
